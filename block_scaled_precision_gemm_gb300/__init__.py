@@ -19,6 +19,11 @@ Entry points (see ``include/bsmm.h`` for the full contract):
 * :func:`gemm_grouped`    FP8 GEMM with 1x128 / 128x128 FP32 scales
 * :func:`int8_channel`    INT8 per-channel matmul with exact INT32 sums
 * :func:`linear_backward` MXFP8 dX / dW of a linear layer
+* :func:`gated_act`, :func:`gated_act_backward`  act(gate) * up, its inputs
+                          kept for the backward pass in 8 bits
+* :func:`linear_backward_checkpoint`  :func:`linear_backward` from an 8-bit X
+* :func:`adapters`, :func:`adapters_backward`  low-rank adapters of many
+                          requests beside a shared projection
 """
 
 from __future__ import annotations
@@ -33,6 +38,8 @@ __all__ = [
     "linear_backward", "gemm_workspace_size", "int8_channel_workspace_size",
     "linear_backward_workspace_size", "check_device_status", "selftest_wait_timeout", "selftest_quotient", "trace",
     "scale_atoms_size", "quantize_atoms", "gemm_atoms", "linear_backward_quantized",
+    "gated_act", "gated_act_backward", "linear_backward_checkpoint", "adapters", "adapters_backward",
+    "adapters_backward_workspace_size",
     "set_wait_timeout_ns", "version",
     "F32", "BF16", "E4M3", "E5M2", "E2M1", "INT8", "SCALE_F32", "SCALE_UE8M0", "SCALE_UE4M3",
 ]
@@ -45,6 +52,10 @@ F32, BF16, E4M3, E5M2, E2M1, INT8 = range(6)
 # bsmm_scale_type
 SCALE_F32, SCALE_UE8M0, SCALE_UE4M3 = range(3)
 
+# bsmm_act
+SILU, GELU = range(2)
+
+_ACT_NAMES = {"silu": SILU, "gelu": GELU}
 _CODE_NAMES = {"e4m3": E4M3, "e5m2": E5M2, "e2m1": E2M1, "int8": INT8}
 _SCALE_NAMES = {"f32": SCALE_F32, "ue8m0": SCALE_UE8M0, "ue4m3": SCALE_UE4M3}
 
@@ -102,6 +113,14 @@ _SIGS = {
     "bsmm_linear_backward_quantized_workspace_size": ([_I64, _I64, _I64, _INT], _SZ),
     "bsmm_linear_backward_quantized": ([_I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _P, _P,
                                         _SZ, _P], _INT),
+    "bsmm_gated_act": ([_P, _INT, _I64, _I64, _I64, _INT, _INT, _P, _P, _INT, _INT, _INT, _P, _P, _P], _INT),
+    "bsmm_gated_act_backward": ([_P, _INT, _I64, _I64, _INT, _P, _INT, _P, _INT, _P, _P, _P], _INT),
+    "bsmm_linear_backward_checkpoint": ([_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P, _SZ, _P],
+                                        _INT),
+    "bsmm_adapters": ([_I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _I64, _INT, _P, _P], _INT),
+    "bsmm_adapters_backward_workspace_size": ([_I64, _I64], _SZ),
+    "bsmm_adapters_backward": ([_I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _P, _P, _P, _P, _P,
+                                _I64, _P, _P, _P, _INT, _P, _SZ, _P], _INT),
 }
 
 
@@ -597,3 +616,262 @@ def linear_backward_quantized(dy_n, dy_n_scales, w_t, w_t_scales, dy_t, dy_t_sca
                                                 _ptr(workspace), _nbytes(workspace),
                                                 _stream(stream)), "bsmm_linear_backward_quantized")
     return dX, dW
+
+
+# --------------------------------------------------------------------------- #
+# Activation checkpoints in 8 bits                                            #
+# --------------------------------------------------------------------------- #
+
+def _empty(shape, dtype, dev, stream):
+    """An output or scratch tensor for a call on `stream`: where that is not
+    the current stream, the allocator is told that the memory is in use there."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None and t.numel():
+        t.record_stream(stream)
+    return t
+
+
+def _act(a) -> int:
+    return _ACT_NAMES[a] if isinstance(a, str) else int(a)
+
+
+def _checkpoint_scales(s: int):
+    """Block along the rows and scale dtype of a checkpoint's scale type."""
+    return (128, torch.float32) if s == SCALE_F32 else (32, torch.uint8)
+
+
+def gated_act(gate_up, act="silu", h_type="e4m3", code="int8", scale="f32", h_scales_are_atoms=False, h=None,
+              h_scales=None, codes=None, scales=None, stream=None):
+    """``h = act(gate) * up`` of ``gate_up`` [M, 2 I] (gate first), quantized
+    as the next GEMM's MXFP8 operand (``h_type`` "e4m3" / "e5m2") or bfloat16
+    ("bf16"), with ``gate_up`` kept for the backward pass as 8-bit codes
+    (``code``, ``scale`` as :func:`quantize` names them; ``code=None`` keeps
+    nothing).
+
+    Returns ``(h, h_scales, codes, scales)``; ``h_scales`` is None for
+    bfloat16, ``codes`` and ``scales`` are None when nothing is kept."""
+    _want(gate_up, "gate_up", dtypes=_FLOATS)
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2:
+        raise ValueError("gate_up must be a 2-D float32 or bfloat16 tensor [M, 2 I]")
+    M, I = gate_up.shape[0], gate_up.shape[1] // 2
+    ht = BF16 if h_type == "bf16" else _code(h_type)
+    quantized = ht != BF16
+    c, s = (-1 if code is None else _code(code)), _scale(scale)
+    block, scale_dtype = _checkpoint_scales(s)
+    if h is not None:
+        _want(h, "h", (M, I), dtypes=(torch.bfloat16,) if not quantized else None, itemsize=1 if quantized else None)
+    if h_scales is not None:
+        if h_scales_are_atoms:
+            _want(h_scales, "h_scales", min_bytes=scale_atoms_size(1, M, I, ht, SCALE_UE8M0))
+        else:
+            _want(h_scales, "h_scales", (M, I // 32), itemsize=1)
+    if code is None:
+        codes = scales = None
+    if codes is not None:
+        _want(codes, "codes", (M, 2 * I), itemsize=1)
+    if scales is not None:
+        _want(scales, "scales", (M, 2 * I // block), itemsize=scale_dtype.itemsize)
+    dev = _on_device(gate_up=gate_up, h=h, h_scales=h_scales, codes=codes, scales=scales)
+    if h is None:
+        h = _empty((M, I), torch.uint8 if quantized else torch.bfloat16, dev, stream)
+    if quantized and h_scales is None:
+        n = max(scale_atoms_size(1, M, I, ht, SCALE_UE8M0), 1) if h_scales_are_atoms else 0
+        h_scales = _empty((n,) if h_scales_are_atoms else (M, I // 32), torch.uint8, dev, stream)
+    if code is not None:
+        if codes is None:
+            codes = _empty((M, 2 * I), torch.int8 if c == INT8 else torch.uint8, dev, stream)
+        if scales is None:
+            scales = _empty((M, 2 * I // block), scale_dtype, dev, stream)
+    _check(lib().bsmm_gated_act(gate_up.data_ptr(), BF16 if gate_up.dtype == torch.bfloat16 else F32, M, I, 2 * I,
+                                _act(act), ht, h.data_ptr(), _ptr(h_scales) if quantized else None,
+                                1 if h_scales_are_atoms else 0, c, s, _ptr(codes), _ptr(scales), _stream(stream)),
+           "bsmm_gated_act")
+    return h, (h_scales if quantized else None), codes, scales
+
+
+def gated_act_backward(dh, codes, scales, act="silu", code="int8", scale="f32", return_h=False, d_gate_up=None, h=None,
+                       stream=None):
+    """Backward of :func:`gated_act` from its checkpoint: returns
+    ``(d_gate_up, h)``, ``d_gate_up`` [M, 2 I] of ``dh``'s type and ``h`` the
+    recomputed bfloat16 activation (None without ``return_h``)."""
+    _want(dh, "dh", dtypes=_FLOATS)
+    if dh.dim() != 2:
+        raise ValueError("dh must be a 2-D float32 or bfloat16 tensor [M, I]")
+    M, I = dh.shape
+    c, s = _code(code), _scale(scale)
+    block, scale_dtype = _checkpoint_scales(s)
+    _want(codes, "codes", (M, 2 * I), itemsize=1)
+    _want(scales, "scales", (M, 2 * I // block), itemsize=scale_dtype.itemsize)
+    if d_gate_up is not None:
+        _want(d_gate_up, "d_gate_up", (M, 2 * I), dtypes=(dh.dtype,))
+    if h is not None:
+        _want(h, "h", (M, I), dtypes=(torch.bfloat16,))
+    dev = _on_device(dh=dh, codes=codes, scales=scales, d_gate_up=d_gate_up, h=h)
+    if d_gate_up is None:
+        d_gate_up = _empty((M, 2 * I), dh.dtype, dev, stream)
+    if return_h and h is None:
+        h = _empty((M, I), torch.bfloat16, dev, stream)
+    _check(lib().bsmm_gated_act_backward(dh.data_ptr(), BF16 if dh.dtype == torch.bfloat16 else F32, M, I, _act(act),
+                                         codes.data_ptr(), c, scales.data_ptr(), s, d_gate_up.data_ptr(), _ptr(h),
+                                         _stream(stream)), "bsmm_gated_act_backward")
+    return d_gate_up, h
+
+
+def linear_backward_checkpoint(dY, W, x_codes, x_scales, x_code="e4m3", x_scale="ue8m0", fp8="e5m2", dX=None, dW=None,
+                               workspace=None, stream=None):
+    """:func:`linear_backward` with X kept in 8 bits (:func:`quantize` with
+    blocks of 1 x 32 UE8M0 or 1 x 128 F32): returns ``(dX, dW)`` in bfloat16."""
+    bf16 = (torch.bfloat16,)
+    for t, n in ((dY, "dY"), (W, "W")):
+        _want(t, n, dtypes=bf16)
+        if t.dim() != 2:
+            raise ValueError(f"{n} must be a 2-D bfloat16 tensor")
+    M, N = dY.shape
+    K = W.shape[1]
+    c, s = _code(x_code), _scale(x_scale)
+    block, scale_dtype = _checkpoint_scales(s)
+    _want(W, "W", (N, K))
+    _want(x_codes, "x_codes", (M, K), itemsize=1)
+    if K % block == 0:  # else the library says why
+        _want(x_scales, "x_scales", (M, K // block), itemsize=scale_dtype.itemsize)
+    if dX is not None:
+        _want(dX, "dX", (M, K), dtypes=bf16)
+    if dW is not None:
+        _want(dW, "dW", (N, K), dtypes=bf16)
+    if workspace is not None:
+        _want(workspace, "workspace")
+    dev = _on_device(dY=dY, W=W, x_codes=x_codes, x_scales=x_scales, dX=dX, dW=dW, workspace=workspace)
+    if dX is None:
+        dX = _empty((M, K), torch.bfloat16, dev, stream)
+    if dW is None:
+        dW = _empty((N, K), torch.bfloat16, dev, stream)
+    if workspace is None:
+        workspace = _empty(max(linear_backward_workspace_size(M, N, K), 1), torch.uint8, dev, stream)
+    _check(lib().bsmm_linear_backward_checkpoint(_ptr(dY), _ptr(W), _ptr(x_codes), c, _ptr(x_scales), s, M, N, K,
+                                                 _code(fp8), _ptr(dX), _ptr(dW), _ptr(workspace), _nbytes(workspace),
+                                                 _stream(stream)), "bsmm_linear_backward_checkpoint")
+    return dX, dW
+
+
+# --------------------------------------------------------------------------- #
+# Low-rank adapters of many requests                                          #
+# --------------------------------------------------------------------------- #
+
+def _rows(t, name, shape, dtypes):
+    """A 2-D argument whose rows are contiguous at any pitch; returns the pitch."""
+    _want(t, name, shape, dtypes=dtypes)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    pitch, step = t.stride()
+    if (step != 1 and t.shape[1] > 1) or (pitch < t.shape[1] and t.shape[0] > 1):
+        raise ValueError(f"{name} must have contiguous rows")
+    return max(pitch, t.shape[1])
+
+
+def _adapter_weights(a, b, ids, scaling, T):
+    bf16 = (torch.bfloat16,)
+    _want(a, "a", dtypes=bf16)
+    _want(b, "b", dtypes=bf16)
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a and b must be (L, R, K) and (L, N, R) bfloat16 tensors")
+    L, R, K = a.shape
+    N = b.shape[1]
+    _want(b, "b", (L, N, R))
+    _want(ids, "ids", (T,), dtypes=(torch.int32,))
+    if scaling is not None:
+        _want(scaling, "scaling", (L,), dtypes=(torch.float32,))
+    return L, R, K, N
+
+
+def adapters(x, a, b, ids, y=None, scaling=None, out=None, u=None, out_dtype=torch.bfloat16, stream=None):
+    """``out = y + scaling[id] * (x @ a[id].T) @ b[id].T`` for every token's
+    adapter ``id = ids[t]`` (outside ``[0, L)``: none).
+
+    ``x`` [T, K] bfloat16, ``a`` [L, R, K], ``b`` [L, N, R] bfloat16, ``ids``
+    [T] int32, ``y`` [T, N] float32 or bfloat16, the shared projection's
+    product (None: 0).  Rows of ``x``, ``y`` and ``out`` may lie at any pitch;
+    ``out`` may be ``y``.  Returns ``(out, u)``: ``u`` [T, R] float32 is
+    ``x @ a[id].T``, which :func:`adapters_backward` takes."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16 tensor [T, K]")
+    T = x.shape[0]
+    L, R, K, N = _adapter_weights(a, b, ids, scaling, T)
+    dtype = y.dtype if y is not None else out.dtype if out is not None else out_dtype
+    ld_x = _rows(x, "x", (T, K), (torch.bfloat16,))
+    ld_y = _rows(y, "y", (T, N), _FLOATS) if y is not None else N
+    ld_out = _rows(out, "out", (T, N), (dtype,)) if out is not None else N
+    if dtype not in _FLOATS:
+        raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {dtype}")
+    if u is not None:
+        _want(u, "u", (T, R), dtypes=(torch.float32,))
+    dev = _on_device(a=a, b=b, ids=ids, scaling=scaling, u=u)
+    for n, t in (("x", x), ("y", y), ("out", out)):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
+    if out is None:
+        out = _empty((T, N), dtype, dev, stream)
+    if u is None:
+        u = _empty((T, R), torch.float32, dev, stream)
+    _check(lib().bsmm_adapters(T, K, N, R, L, x.data_ptr(), ld_x, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
+                               _ptr(scaling), _ptr(y), ld_y, out.data_ptr(), ld_out,
+                               BF16 if dtype == torch.bfloat16 else F32, u.data_ptr(), _stream(stream)),
+           "bsmm_adapters")
+    return out, u
+
+
+def adapters_backward_workspace_size(T, R) -> int:
+    return lib().bsmm_adapters_backward_workspace_size(T, R)
+
+
+def adapters_backward(dy, x, a, b, ids, u, scaling=None, dx_base=None, x_scales=None, x_code="e4m3",
+                      grad_dtype=torch.float32, dx=None, da=None, db=None, workspace=None, stream=None):
+    """Backward of :func:`adapters` from ``dy`` [T, N] bfloat16 and the
+    forward's ``u``: returns ``(dx, da, db)``.
+
+    ``x`` is the forward's bfloat16 input, or with ``x_scales`` its MXFP8
+    checkpoint (codes [T, K] of type ``x_code``, scales [T, K / 32]).  ``dx``
+    [T, K] bfloat16 adds to ``dx_base`` (the shared projection's own dX; may
+    be the same tensor); ``da`` and ``db`` are of ``grad_dtype``."""
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        raise ValueError("dy must be a 2-D bfloat16 tensor [T, N]")
+    T = dy.shape[0]
+    L, R, K, N = _adapter_weights(a, b, ids, scaling, T)
+    bf16 = (torch.bfloat16,)
+    ld_dy = _rows(dy, "dy", (T, N), bf16)
+    if x_scales is not None:
+        _want(x, "x", (T, K), itemsize=1)
+        if K % 32 == 0:  # else the library says why
+            _want(x_scales, "x_scales", (T, K // 32), itemsize=1)
+        ld_x, xt = K, _code(x_code)
+    else:
+        ld_x, xt = _rows(x, "x", (T, K), bf16), BF16
+    _want(u, "u", (T, R), dtypes=(torch.float32,))
+    if grad_dtype not in _FLOATS:
+        raise ValueError("grad_dtype must be float32 or bfloat16")
+    for t, n, shape in ((dx_base, "dx_base", (T, K)), (dx, "dx", (T, K))):
+        if t is not None:
+            _want(t, n, shape, dtypes=bf16)
+    for t, n, shape in ((da, "da", (L, R, K)), (db, "db", (L, N, R))):
+        if t is not None:
+            _want(t, n, shape, dtypes=(grad_dtype,))
+    if workspace is not None:
+        _want(workspace, "workspace")
+    dev = _on_device(a=a, b=b, ids=ids, scaling=scaling, u=u, x_scales=x_scales, dx_base=dx_base, dx=dx, da=da, db=db,
+                     workspace=workspace, **({"x": x} if x_scales is not None else {}))
+    for n, t in (("dy", dy), ("x", x)):
+        if t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
+    if dx is None:
+        dx = _empty((T, K), torch.bfloat16, dev, stream)
+    if da is None:
+        da = _empty((L, R, K), grad_dtype, dev, stream)
+    if db is None:
+        db = _empty((L, N, R), grad_dtype, dev, stream)
+    if workspace is None:
+        workspace = _empty(max(adapters_backward_workspace_size(T, R), 1), torch.uint8, dev, stream)
+    _check(lib().bsmm_adapters_backward(T, K, N, R, L, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, xt, _ptr(x_scales),
+                                        a.data_ptr(), b.data_ptr(), ids.data_ptr(), _ptr(scaling), u.data_ptr(),
+                                        _ptr(dx_base), K, dx.data_ptr(), da.data_ptr(), db.data_ptr(),
+                                        BF16 if grad_dtype == torch.bfloat16 else F32, _ptr(workspace),
+                                        _nbytes(workspace), _stream(stream)), "bsmm_adapters_backward")
+    return dx, da, db

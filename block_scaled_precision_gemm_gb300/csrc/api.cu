@@ -636,24 +636,23 @@ bsmm_status backward_gemms(int64_t M, int64_t N, int64_t K, int ft, const void* 
 }
 }  // namespace
 
-bsmm_status bsmm_linear_backward(const void* dY, const void* W, const void* X, int64_t M, int64_t N, int64_t K,
-                                 bsmm_dtype fp8_type, void* dX, void* dW, void* workspace, size_t workspace_bytes,
-                                 bsmm_stream_t stream) {
-  if (M < 0 || N < 0 || K < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
-  if (fp8_type != BSMM_E5M2 && fp8_type != BSMM_E4M3) return fail(BSMM_ERR_INVALID_ARG, "fp8_type must be E5M2 or E4M3");
-  if (M == 0 || N == 0 || K == 0) {
-    set_error("");
-    return BSMM_OK;
-  }
-  if (!dY || !W || !X || !dX || !dW) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+namespace {
+// X of the backward: bf16, or a checkpoint's codes and scales.
+struct BackwardX {
+  const void* x;
+  const void* scales;  // null: bf16
+  int code, scale;
+};
+
+bsmm_status linear_backward(const void* dY, const void* W, const BackwardX& X, int64_t M, int64_t N, int64_t K, int ft,
+                            void* dX, void* dW, void* workspace, size_t workspace_bytes, cudaStream_t s) {
   if (M % 32 || N % 32 || K % 32) return fail(BSMM_ERR_SHAPE, "M, N and K must be multiples of 32");
-  if (!aligned16(dY) || !aligned16(W) || !aligned16(X) || !aligned16(dX) || !aligned16(dW))
+  if (!aligned16(dY) || !aligned16(W) || !aligned16(X.x) || !aligned16(dX) || !aligned16(dW))
     return fail(BSMM_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
   const size_t need = bsmm_linear_backward_workspace_size(M, N, K);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) +
                                         " bytes");
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* p = static_cast<uint8_t*>(workspace);
   auto take = [&](size_t bytes) {
     uint8_t* r = p;
@@ -672,19 +671,199 @@ bsmm_status bsmm_linear_backward(const void* dY, const void* W, const void* X, i
   // Each operand quantized along its GEMM's contraction axis, scales straight
   // into the tensor-core atom layout (no relayout before the GEMMs); dY's two
   // quantizations in one pass over it.
-  const int ft = fp8_type;
   QuantRequest q_dyn, q_dyt;
   cudaError_t e = atoms_request(dY, true, 1, M, N, false, ft, BSMM_SCALE_UE8M0, dy_n, dy_n_s, s, &q_dyn);  // [M, N]
   if (e == cudaSuccess)
     e = atoms_request(dY, true, 1, N, M, true, ft, BSMM_SCALE_UE8M0, dyt, dyt_s, s, &q_dyt);  // dY^T [N, M]
   if (e == cudaSuccess) e = launch_quantize_dual(q_dyt, q_dyn, s);
-  // W [N,K] along N -> W^T [K, N] and X [M,K] along M -> X^T [K, M], one launch
+  // W [N,K] along N -> W^T [K, N] and X [M,K] along M -> X^T [K, M]: one launch
+  // for a bf16 X, a launch of its own for a checkpoint
   QuantRequest q_wt, q_xt;
   if (e == cudaSuccess) e = atoms_request(W, true, 1, K, N, true, ft, BSMM_SCALE_UE8M0, wt, wt_s, s, &q_wt);
-  if (e == cudaSuccess) e = atoms_request(X, true, 1, K, M, true, ft, BSMM_SCALE_UE8M0, xt, xt_s, s, &q_xt);
-  if (e == cudaSuccess) e = launch_quantize_pair(q_wt, q_xt, s);
+  if (!X.scales) {
+    if (e == cudaSuccess) e = atoms_request(X.x, true, 1, K, M, true, ft, BSMM_SCALE_UE8M0, xt, xt_s, s, &q_xt);
+    if (e == cudaSuccess) e = launch_quantize_pair(q_wt, q_xt, s);
+  } else {
+    if (e == cudaSuccess) e = launch_quantize(q_wt, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(xt_s, 127, sf_atoms_plain_bytes(1, K, M, kFmtMXF8), s);
+    if (e == cudaSuccess)
+      e = launch_requantize_cols(RequantRequest{X.x, X.scales, X.code, X.scale, M, K, ft, xt, xt_s}, s);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "backward quantize launch");
   return backward_gemms(M, N, K, ft, dy_n, dy_n_s, wt, wt_s, dyt, dyt_s, xt, xt_s, true, dX, dW, nullptr, s);
+}
+
+// A checkpoint format: the block along the rows, or 0 for none.
+int checkpoint_block(int code, int scale) {
+  const bool fp8 = code == BSMM_E4M3 || code == BSMM_E5M2;
+  if (scale == BSMM_SCALE_F32 && (fp8 || code == BSMM_INT8)) return 128;
+  if (scale == BSMM_SCALE_UE8M0 && fp8) return 32;
+  return 0;
+}
+constexpr const char* kCheckpointFormats = "a checkpoint is E4M3, E5M2 or INT8 with F32 scales, or E4M3 or E5M2 with UE8M0";
+}  // namespace
+
+bsmm_status bsmm_linear_backward(const void* dY, const void* W, const void* X, int64_t M, int64_t N, int64_t K,
+                                 bsmm_dtype fp8_type, void* dX, void* dW, void* workspace, size_t workspace_bytes,
+                                 bsmm_stream_t stream) {
+  if (M < 0 || N < 0 || K < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  if (fp8_type != BSMM_E5M2 && fp8_type != BSMM_E4M3) return fail(BSMM_ERR_INVALID_ARG, "fp8_type must be E5M2 or E4M3");
+  if (M == 0 || N == 0 || K == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if (!dY || !W || !X || !dX || !dW) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  return linear_backward(dY, W, BackwardX{X, nullptr, 0, 0}, M, N, K, fp8_type, dX, dW, workspace, workspace_bytes,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmm_status bsmm_linear_backward_checkpoint(const void* dY, const void* W, const void* x_codes, bsmm_dtype x_type,
+                                            const void* x_scales, bsmm_scale_type x_scale_type, int64_t M, int64_t N,
+                                            int64_t K, bsmm_dtype fp8_type, void* dX, void* dW, void* workspace,
+                                            size_t workspace_bytes, bsmm_stream_t stream) {
+  if (M < 0 || N < 0 || K < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  if (fp8_type != BSMM_E5M2 && fp8_type != BSMM_E4M3) return fail(BSMM_ERR_INVALID_ARG, "fp8_type must be E5M2 or E4M3");
+  const int block = checkpoint_block(x_type, x_scale_type);
+  if (!block) return fail(BSMM_ERR_UNSUPPORTED, kCheckpointFormats);
+  if (M == 0 || N == 0 || K == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if (!dY || !W || !x_codes || !x_scales || !dX || !dW) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (K % block) return fail(BSMM_ERR_SHAPE, "K must be a multiple of the checkpoint's block");
+  if (M > 65535LL * 128) return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  if (x_scale_type == BSMM_SCALE_F32 && (reinterpret_cast<uintptr_t>(x_scales) & 3u))
+    return fail(BSMM_ERR_ALIGNMENT, "F32 scales must be 4-byte aligned");
+  return linear_backward(dY, W, BackwardX{x_codes, x_scales, x_type, x_scale_type}, M, N, K, fp8_type, dX, dW, workspace,
+                         workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmm_status bsmm_gated_act(const void* gate_up, bsmm_dtype x_type, int64_t M, int64_t I, int64_t ld_x, bsmm_act act,
+                           bsmm_dtype h_type, void* h, void* h_scales, int h_scales_are_atoms, bsmm_dtype code_type,
+                           bsmm_scale_type scale_type, void* codes, void* scales, bsmm_stream_t stream) {
+  if (x_type != BSMM_F32 && x_type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "x_type must be F32 or BF16");
+  if (act != BSMM_SILU && act != BSMM_GELU) return fail(BSMM_ERR_INVALID_ARG, "act must be SILU or GELU");
+  if (h_type != BSMM_BF16 && h_type != BSMM_E4M3 && h_type != BSMM_E5M2)
+    return fail(BSMM_ERR_INVALID_ARG, "h_type must be BF16, E4M3 or E5M2");
+  if (M < 0 || I < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  const int block = codes ? checkpoint_block(code_type, scale_type) : 32;
+  if (!block) return fail(BSMM_ERR_UNSUPPORTED, kCheckpointFormats);
+  if (M == 0 || I == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  const bool hq = h_type != BSMM_BF16;
+  if (!gate_up || !h || (hq && !h_scales) || (codes && !scales)) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (I % 32 || I % block) return fail(BSMM_ERR_SHAPE, "I must be a multiple of 32 and of the checkpoint's block");
+  if (ld_x < 2 * I) return fail(BSMM_ERR_SHAPE, "ld_x < 2 I");
+  if (I > INT32_MAX / 4) return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  if (!aligned16(gate_up) || !aligned16(h) || !aligned16(codes) || ld_x % (x_type == BSMM_BF16 ? 8 : 4))
+    return fail(BSMM_ERR_ALIGNMENT, "gate_up, its row pitch, h and codes must be 16-byte aligned");
+  if (codes && scale_type == BSMM_SCALE_F32 && (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return fail(BSMM_ERR_ALIGNMENT, "F32 scales must be 4-byte aligned");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool atoms = hq && h_scales_are_atoms;
+  if (atoms) {  // the padding's neutral scale
+    const cudaError_t e = cudaMemsetAsync(h_scales, 127, sf_atoms_plain_bytes(1, M, I, kFmtMXF8), s);
+    if (e != cudaSuccess) return cuda_fail(e, "gated activation launch");
+  }
+  const GatedRequest r{gate_up, x_type == BSMM_BF16, M,     I,         ld_x,       act,   h_type, h,
+                       h_scales, atoms, ceil_div(I, 128), code_type, scale_type, codes, scales};
+  return launched(launch_gated_act(r, s), "gated activation launch");
+}
+
+bsmm_status bsmm_gated_act_backward(const void* dh, bsmm_dtype d_type, int64_t M, int64_t I, bsmm_act act,
+                                    const void* codes, bsmm_dtype code_type, const void* scales,
+                                    bsmm_scale_type scale_type, void* d_gate_up, void* h, bsmm_stream_t stream) {
+  if (d_type != BSMM_F32 && d_type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "d_type must be F32 or BF16");
+  if (act != BSMM_SILU && act != BSMM_GELU) return fail(BSMM_ERR_INVALID_ARG, "act must be SILU or GELU");
+  if (M < 0 || I < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  const int block = checkpoint_block(code_type, scale_type);
+  if (!block) return fail(BSMM_ERR_UNSUPPORTED, kCheckpointFormats);
+  if (M == 0 || I == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if (!dh || !codes || !scales || !d_gate_up) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (I % block) return fail(BSMM_ERR_SHAPE, "I must be a multiple of the checkpoint's block");
+  if (I > INT32_MAX / 4) return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  if (!aligned16(dh) || !aligned16(codes) || !aligned16(d_gate_up) || !aligned16(h))
+    return fail(BSMM_ERR_ALIGNMENT, "dh, codes, d_gate_up and h must be 16-byte aligned");
+  if (scale_type == BSMM_SCALE_F32 && (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return fail(BSMM_ERR_ALIGNMENT, "F32 scales must be 4-byte aligned");
+  const GatedBackwardRequest r{dh, d_type == BSMM_BF16, M, I, act, codes, scales, code_type, scale_type, d_gate_up, h};
+  return launched(launch_gated_act_backward(r, reinterpret_cast<cudaStream_t>(stream)), "gated activation backward launch");
+}
+
+namespace {
+// The sizes both adapter calls check alike.
+bsmm_status adapter_sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L) {
+  if (T < 0 || K < 0 || N < 0 || R < 0 || L < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  if (K == 0 || N == 0 || R == 0 || L == 0) return fail(BSMM_ERR_SHAPE, "K, N, R and L must be at least 1");
+  if (R > 128) return fail(BSMM_ERR_UNSUPPORTED, "ranks up to 128");
+  if (T > INT32_MAX || K > (1 << 22) || N > (1 << 22) || L > 65535)
+    return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  return BSMM_OK;
+}
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+}  // namespace
+
+bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* x, int64_t ld_x,
+                          const void* A, const void* B, const int32_t* ids, const float* scaling, const void* y,
+                          int64_t ld_y, void* out, int64_t ld_out, bsmm_dtype y_type, float* u, bsmm_stream_t stream) {
+  const bsmm_status st = adapter_sizes(T, K, N, R, L);
+  if (st != BSMM_OK) return st;
+  if (y_type != BSMM_F32 && y_type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "y_type must be F32 or BF16");
+  if (T == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if (!x || !A || !B || !ids || !out || !u) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (ld_x < K || ld_out < N || (y && ld_y < N)) return fail(BSMM_ERR_SHAPE, "a row pitch is shorter than its row");
+  if (y == out && ld_y != ld_out) return fail(BSMM_ERR_SHAPE, "in place, ld_out must be ld_y");
+  const size_t ye = y_type == BSMM_BF16 ? 2 : 4;
+  if (!aligned_to(x, 2) || !aligned_to(A, 2) || !aligned_to(B, 2) || !aligned_to(ids, 4) || !aligned_to(scaling, 4) ||
+      !aligned_to(y, ye) || !aligned_to(out, ye) || !aligned_to(u, 4))
+    return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements");
+  const AdaptersRequest r{T, K, N, R, L, x, ld_x, A, B, ids, scaling, y, ld_y, out, ld_out, y_type == BSMM_BF16, u};
+  return launched(launch_adapters(r, reinterpret_cast<cudaStream_t>(stream)), "adapters launch");
+}
+
+size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R) {
+  if (T <= 0 || R <= 0) return 0;
+  return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256);
+}
+
+bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* dy,
+                                   int64_t ld_dy, const void* x, int64_t ld_x, bsmm_dtype x_type,
+                                   const void* x_scales, const void* A, const void* B, const int32_t* ids,
+                                   const float* scaling, const float* u, const void* dx_base, int64_t ld_dx, void* dx,
+                                   void* dA, void* dB, bsmm_dtype grad_type, void* workspace, size_t workspace_bytes,
+                                   bsmm_stream_t stream) {
+  const bsmm_status st = adapter_sizes(T, K, N, R, L);
+  if (st != BSMM_OK) return st;
+  if (grad_type != BSMM_F32 && grad_type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "grad_type must be F32 or BF16");
+  if (x_type != BSMM_BF16 && x_type != BSMM_E4M3 && x_type != BSMM_E5M2)
+    return fail(BSMM_ERR_INVALID_ARG, "x_type must be BF16, E4M3 or E5M2");
+  const bool kept = x_type != BSMM_BF16;
+  if (!dA || !dB || !A || !B) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (T > 0 && (!dy || !x || !ids || !u || !dx || kept != (x_scales != nullptr)))
+    return fail(BSMM_ERR_INVALID_ARG, "null pointer, or x_scales without codes");
+  if (T > 0 && (ld_dy < N || ld_x < K || ld_dx < K)) return fail(BSMM_ERR_SHAPE, "a row pitch is shorter than its row");
+  if (kept && (K % 32 || ld_x != K)) return fail(BSMM_ERR_SHAPE, "a checkpoint needs K % 32 == 0 and ld_x = K");
+  const size_t ge = grad_type == BSMM_BF16 ? 2 : 4;
+  if (!aligned_to(dy, 2) || !aligned_to(x, kept ? 16 : 2) || !aligned_to(A, 2) || !aligned_to(B, 2) ||
+      !aligned_to(ids, 4) || !aligned_to(scaling, 4) || !aligned_to(u, 4) || !aligned_to(dx_base, 2) ||
+      !aligned_to(dx, 2) || !aligned_to(dA, ge) || !aligned_to(dB, ge))
+    return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements (codes: 16 bytes)");
+  const size_t need = bsmm_adapters_backward_workspace_size(T, R);
+  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+    return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) +
+                                        " bytes");
+  const AdaptersBackwardRequest r{T, K, N, R, L, dy, ld_dy, x, ld_x, static_cast<const uint8_t*>(x_scales), x_type, A, B,
+                                  ids, scaling, u, dx_base, ld_dx, dx, dA, dB, grad_type == BSMM_BF16,
+                                  static_cast<float*>(workspace)};
+  return launched(launch_adapters_backward(r, reinterpret_cast<cudaStream_t>(stream)), "adapters backward launch");
 }
 
 size_t bsmm_linear_backward_quantized_workspace_size(int64_t M, int64_t N, int64_t K, int scales_are_atoms) {

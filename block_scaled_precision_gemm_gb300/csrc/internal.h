@@ -87,6 +87,91 @@ cudaError_t launch_quantize_dual(const QuantRequest& qc, const QuantRequest& qr,
 // column kernel, else the two launches.
 cudaError_t launch_quantize_pair(const QuantRequest& qa, const QuantRequest& qb, cudaStream_t s);
 
+// ---- activation checkpoints in 8 bits (checkpoint.cu) ---------------------
+struct GatedRequest {
+  const void* x;  // [M][2 I], gate then up
+  bool x_bf16;
+  int64_t M, I, ld;
+  int act;     // bsmm_act
+  int h_type;  // BF16, or the codes' type
+  void* h;
+  void* h_scales;
+  bool h_atoms;
+  int64_t h_ks4;  // atoms per row tile, when h_atoms
+  int code, scale;
+  void* codes;  // null: nothing is kept
+  void* scales;
+};
+cudaError_t launch_gated_act(const GatedRequest& r, cudaStream_t s);
+
+struct GatedBackwardRequest {
+  const void* dh;
+  bool d_bf16;
+  int64_t M, I;
+  int act;
+  const void* codes;
+  const void* scales;
+  int code, scale;
+  void* d;
+  void* h;  // null: not wanted
+};
+cudaError_t launch_gated_act_backward(const GatedBackwardRequest& r, cudaStream_t s);
+
+// A checkpoint [M, K] (codes and scales along K) into MXFP8 codes of its
+// transpose [K, M] with UE8M0 scales per 32 along M in the atom layout (whose
+// padding is not written).
+struct RequantRequest {
+  const void* x;
+  const void* scales;
+  int code, scale;
+  int64_t M, K;
+  int out_code;  // E4M3 or E5M2
+  void* codes;
+  void* atoms;
+};
+cudaError_t launch_requantize_cols(const RequantRequest& r, cudaStream_t s);
+
+// ---- low-rank adapters (adapters.cu) ---------------------------------------
+struct AdaptersRequest {
+  int64_t T, K, N, R, L;
+  const void* x;  // [T][ld_x] bf16
+  int64_t ld_x;
+  const void* a;  // [L][R][K] bf16
+  const void* b;  // [L][N][R] bf16
+  const int* ids;
+  const float* scaling;  // null: 1
+  const void* y;         // null: 0
+  int64_t ld_y;
+  void* out;
+  int64_t ld_out;
+  bool y_bf16;
+  float* u;  // [T][R]
+};
+cudaError_t launch_adapters(const AdaptersRequest& r, cudaStream_t s);
+
+struct AdaptersBackwardRequest {
+  int64_t T, K, N, R, L;
+  const void* dy;  // [T][ld_dy] bf16
+  int64_t ld_dy;
+  const void* x;  // [T][ld_x] bf16, or codes
+  int64_t ld_x;
+  const uint8_t* x_scales;  // null: x is bf16; else UE8M0 [T][K / 32]
+  int x_code;
+  const void* a;
+  const void* b;
+  const int* ids;
+  const float* scaling;
+  const float* u;
+  const void* dx_base;  // null: 0
+  int64_t ld_dx;        // of dx_base and dx
+  void* dx;
+  void* da;
+  void* db;
+  bool grad_bf16;
+  float* d;  // [T][R] scratch
+};
+cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s);
+
 // Block-scaled formats of bsmm_gemm.
 enum MxFormat { kFmtMXF8 = 0, kFmtNVF4 = 1, kFmtMXF4 = 2 };
 // Scale relayout into the tensor-core scale-factor atoms (see gemm_tc.cu).

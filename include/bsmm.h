@@ -459,6 +459,128 @@ bsmm_status bsmm_linear_backward_quantized(int64_t M, int64_t N, int64_t K, bsmm
                                            void* dX, void* dW, void* workspace, size_t workspace_bytes,
                                            bsmm_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Activation checkpoints in 8 bits                                          */
+/* ------------------------------------------------------------------------ */
+
+/* These have no counterpart on the pages: what a training step keeps between
+ * its forward and its backward pass, held as bsmm_quantize holds it.
+ *
+ * A checkpoint of an array [rows, cols] is its codes [rows, cols] and its
+ * scales [rows, cols / block], row-major and contiguous, as bsmm_quantize
+ * writes them for blocks along the rows, in one of the formats
+ *   E4M3, E5M2 or INT8 codes with an F32 scale per 1 x 128 block,
+ *   E4M3 or E5M2 codes with a UE8M0 scale per 1 x 32 block (MXFP8),
+ * and each code stands for the binary32 product code * scale.  An MXFP8
+ * operand of the forward GEMM is such a checkpoint already. */
+typedef enum bsmm_act {
+  BSMM_SILU = 0, /* g / (1 + exp(-g))            */
+  BSMM_GELU = 1  /* g Phi(g), Phi the normal CDF */
+} bsmm_act;
+
+/* Gated activation h = act(gate) * up in binary32, from gate_up [M, 2 I] (the
+ * first I columns of a row are gate, the rest up), which is read once:
+ *
+ *   x_type   F32 or BF16, of gate_up; rows at a pitch of ld_x elements.
+ *   h_type   E4M3 or E5M2: h as the next GEMM's MXFP8 operand, codes [M, I]
+ *            and UE8M0 scales per 1 x 32 (rule of bsmm_quantize).  The scales
+ *            are row-major [M, I / 32] (h_scales_are_atoms = 0), or in the
+ *            atom layout, bsmm_scale_atoms_size(1, M, I, h_type, UE8M0) bytes
+ *            with the padding (h_scales_are_atoms = 1).
+ *            BF16: h [M, I] rounded to nearest even; h_scales is not used.
+ *   codes, scales  the checkpoint of gate_up, format code_type / scale_type;
+ *            codes NULL keeps nothing (serving) and the rest is not used.
+ *            The codes are those of bsmm_quantize for the scale stored, and
+ *            so are UE8M0 scales; an F32 scale is binary32(absmax * r), r =
+ *            binary32(1 / qmax) (E4M3, E5M2: at least 1e-10; INT8: an
+ *            all-zero block 1), at most an ulp from bsmm_quantize's quotient.
+ *   I a multiple of 32, of 128 for a checkpoint with F32 scales.
+ *   Pointers (but for h_scales and scales) and row pitches 16-byte aligned.
+ *   Inputs are taken to be finite, as bsmm_quantize takes them. */
+bsmm_status bsmm_gated_act(const void* gate_up, bsmm_dtype x_type, int64_t M, int64_t I, int64_t ld_x, bsmm_act act,
+                           bsmm_dtype h_type, void* h, void* h_scales, int h_scales_are_atoms, bsmm_dtype code_type,
+                           bsmm_scale_type scale_type, void* codes, void* scales, bsmm_stream_t stream);
+
+/* Its backward pass from the checkpoint (g, u the values of its codes):
+ *   d_gate = dh * u * act'(g),  d_up = dh * act(g),  h = act(g) * u,
+ * each computed in binary32 and rounded once.
+ *
+ *   dh [M, I] and d_gate_up [M, 2 I] of type d_type (F32 or BF16), contiguous.
+ *   h        BF16 [M, I]: the down projection's input again, for its weight
+ *            gradient; NULL to skip.
+ *   I as in bsmm_gated_act; pointers (but for scales) 16-byte aligned. */
+bsmm_status bsmm_gated_act_backward(const void* dh, bsmm_dtype d_type, int64_t M, int64_t I, bsmm_act act,
+                                    const void* codes, bsmm_dtype code_type, const void* scales,
+                                    bsmm_scale_type scale_type, void* d_gate_up, void* h, bsmm_stream_t stream);
+
+/* bsmm_linear_backward with X kept as a checkpoint [M, K]: its values are
+ * quantized along M for dW, straight from the codes; X itself is never
+ * written.  x_scales row-major [M, K / 32] (UE8M0) or [M, K / 128] (F32, K a
+ * multiple of 128).  Everything else, the workspace and what is left in it
+ * included, as in bsmm_linear_backward. */
+bsmm_status bsmm_linear_backward_checkpoint(const void* dY, const void* W, const void* x_codes, bsmm_dtype x_type,
+                                            const void* x_scales, bsmm_scale_type x_scale_type, int64_t M, int64_t N,
+                                            int64_t K, bsmm_dtype fp8_type, void* dX, void* dW, void* workspace,
+                                            size_t workspace_bytes, bsmm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Low-rank adapters of many requests                                        */
+/* ------------------------------------------------------------------------ */
+
+/* No counterpart on the pages.  Beside a projection y = x W^T that all tokens
+ * share (any GEMM above), each token t adds the low-rank product of its own
+ * request's adapter, l = ids[t]:
+ *
+ *   u[t]   = A[l] x[t]                    binary32 sums
+ *   out[t] = y[t] + scaling[l] * B[l] u[t]  binary32, rounded once
+ *
+ *   T tokens, in any order of adapters (neighbours that share one are fastest).
+ *   ids [T] int32; an id outside [0, L) means no adapter: u[t] = 0, out[t] =
+ *            y[t].  Rows never mix: an infinity or NaN in a token or in an
+ *            adapter reaches only the tokens that use it.
+ *   x [T, K] bfloat16 at a row pitch of ld_x, A [L, R, K] and B [L, N, R]
+ *            bfloat16, contiguous.  1 <= R <= 128; any K, N >= 1.
+ *   scaling  binary32 [L], or NULL for 1.
+ *   y [T, N] of type y_type (F32 or BF16) at a pitch of ld_y, or NULL for 0;
+ *            out of the same type at a pitch of ld_out.  out may be y itself
+ *            (then ld_out = ld_y); no other overlap.
+ *   u        binary32 [T, R], contiguous: an output, which the backward takes.
+ * Rows whose start is 16-byte aligned (K, N and pitches multiples of 8, R of
+ * 4) are read and written in 16-byte pieces; others element by element.
+ * Every sum has a fixed order. */
+bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* x, int64_t ld_x,
+                          const void* A, const void* B, const int32_t* ids, const float* scaling, const void* y,
+                          int64_t ld_y, void* out, int64_t ld_out, bsmm_dtype y_type, float* u, bsmm_stream_t stream);
+
+/* The backward pass of bsmm_adapters, from dy = d(out) and the forward's u:
+ *
+ *   d[t]  = B[l]^T dy[t]
+ *   dx[t] = dx_base[t] + scaling[l] * A[l]^T d[t]
+ *   dA[l] = scaling[l] * sum of d[t] x[t]^T,  dB[l] = scaling[l] * sum of dy[t] u[t]^T
+ *                                             over the tokens t of adapter l
+ *
+ *   dy [T, N] bfloat16 at a pitch of ld_dy.
+ *   x        bfloat16 [T, K] at a pitch of ld_x (x_type BF16, x_scales NULL),
+ *            or an MXFP8 checkpoint: codes [T, K] (x_type E4M3 or E5M2,
+ *            ld_x = K) with UE8M0 scales x_scales [T, K / 32]; K a multiple of
+ *            32.  The codes' values are taken as bfloat16, which holds them
+ *            exactly (below 2^-126 in magnitude they round).
+ *   dx_base  bfloat16 [T, K], the shared projection's dX, or NULL for 0; dx
+ *            bfloat16 [T, K], may be dx_base itself.  Both at a pitch of ld_dx.
+ *   dA [L, R, K], dB [L, N, R] of type grad_type (F32 or BF16), contiguous:
+ *            overwritten; zero for an adapter without tokens.
+ *   workspace  bsmm_adapters_backward_workspace_size() bytes, 256-byte
+ *            aligned (holds d).
+ * dA and dB need the tokens' sums only: T == 0 writes zeros. */
+size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R);
+
+bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* dy,
+                                   int64_t ld_dy, const void* x, int64_t ld_x, bsmm_dtype x_type,
+                                   const void* x_scales, const void* A, const void* B, const int32_t* ids,
+                                   const float* scaling, const float* u, const void* dx_base, int64_t ld_dx, void* dx,
+                                   void* dA, void* dB, bsmm_dtype grad_type, void* workspace, size_t workspace_bytes,
+                                   bsmm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
