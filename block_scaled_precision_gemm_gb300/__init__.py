@@ -39,7 +39,7 @@ __all__ = [
     "linear_backward_workspace_size", "check_device_status", "selftest_wait_timeout", "selftest_quotient", "trace",
     "scale_atoms_size", "quantize_atoms", "gemm_atoms", "linear_backward_quantized",
     "gated_act", "gated_act_backward", "linear_backward_checkpoint", "adapters", "adapters_backward",
-    "adapters_backward_workspace_size",
+    "adapters_workspace_size", "adapters_backward_workspace_size",
     "set_wait_timeout_ns", "version",
     "F32", "BF16", "E4M3", "E5M2", "E2M1", "INT8", "SCALE_F32", "SCALE_UE8M0", "SCALE_UE4M3",
 ]
@@ -117,8 +117,10 @@ _SIGS = {
     "bsmm_gated_act_backward": ([_P, _INT, _I64, _I64, _INT, _P, _INT, _P, _INT, _P, _P, _P], _INT),
     "bsmm_linear_backward_checkpoint": ([_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P, _SZ, _P],
                                         _INT),
-    "bsmm_adapters": ([_I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _I64, _INT, _P, _P], _INT),
-    "bsmm_adapters_backward_workspace_size": ([_I64, _I64], _SZ),
+    "bsmm_adapters_workspace_size": ([_I64, _I64], _SZ),
+    "bsmm_adapters": ([_I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _I64, _INT, _P, _P, _SZ,
+                       _P], _INT),
+    "bsmm_adapters_backward_workspace_size": ([_I64, _I64, _I64], _SZ),
     "bsmm_adapters_backward": ([_I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _P, _P, _P, _P, _P,
                                 _I64, _P, _P, _P, _INT, _P, _SZ, _P], _INT),
 }
@@ -622,6 +624,24 @@ def linear_backward_quantized(dy_n, dy_n_scales, w_t, w_t_scales, dy_t, dy_t_sca
 # Activation checkpoints in 8 bits                                            #
 # --------------------------------------------------------------------------- #
 
+def _raw_stream(stream, dev) -> int:
+    """The stream's handle; the current stream's through torch's raw query,
+    which builds no Stream object (a tenth of its time)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _fits(t, dtype, shape, dev) -> bool:
+    """Whether a tensor is all that its checks ask for.  A call whose tensors
+    all fit skips the checks that say what is wrong; one that does not goes
+    through them (small calls spend most of their time on the host)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous())
+
+
+def _current(t) -> bool:
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.device.index == torch.cuda.current_device()
+
+
 def _empty(shape, dtype, dev, stream):
     """An output or scratch tensor for a call on `stream`: where that is not
     the current stream, the allocator is told that the memory is in use there."""
@@ -629,6 +649,10 @@ def _empty(shape, dtype, dev, stream):
     if stream is not None and t.numel():
         t.record_stream(stream)
     return t
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _act(a) -> int:
@@ -653,7 +677,8 @@ def gated_act(gate_up, act="silu", h_type="e4m3", code="int8", scale="f32", h_sc
     _want(gate_up, "gate_up", dtypes=_FLOATS)
     if gate_up.dim() != 2 or gate_up.shape[1] % 2:
         raise ValueError("gate_up must be a 2-D float32 or bfloat16 tensor [M, 2 I]")
-    M, I = gate_up.shape[0], gate_up.shape[1] // 2
+    M, I = gate_up.shape
+    I //= 2
     ht = BF16 if h_type == "bf16" else _code(h_type)
     quantized = ht != BF16
     c, s = (-1 if code is None else _code(code)), _scale(scale)
@@ -683,8 +708,8 @@ def gated_act(gate_up, act="silu", h_type="e4m3", code="int8", scale="f32", h_sc
         if scales is None:
             scales = _empty((M, 2 * I // block), scale_dtype, dev, stream)
     _check(lib().bsmm_gated_act(gate_up.data_ptr(), BF16 if gate_up.dtype == torch.bfloat16 else F32, M, I, 2 * I,
-                                _act(act), ht, h.data_ptr(), _ptr(h_scales) if quantized else None,
-                                1 if h_scales_are_atoms else 0, c, s, _ptr(codes), _ptr(scales), _stream(stream)),
+                                _act(act), ht, h.data_ptr(), h_scales.data_ptr() if quantized else None,
+                                1 if h_scales_are_atoms else 0, c, s, _at(codes), _at(scales), _raw_stream(stream, dev)),
            "bsmm_gated_act")
     return h, (h_scales if quantized else None), codes, scales
 
@@ -712,8 +737,8 @@ def gated_act_backward(dh, codes, scales, act="silu", code="int8", scale="f32", 
     if return_h and h is None:
         h = _empty((M, I), torch.bfloat16, dev, stream)
     _check(lib().bsmm_gated_act_backward(dh.data_ptr(), BF16 if dh.dtype == torch.bfloat16 else F32, M, I, _act(act),
-                                         codes.data_ptr(), c, scales.data_ptr(), s, d_gate_up.data_ptr(), _ptr(h),
-                                         _stream(stream)), "bsmm_gated_act_backward")
+                                         codes.data_ptr(), c, scales.data_ptr(), s, d_gate_up.data_ptr(), _at(h),
+                                         _raw_stream(stream, dev)), "bsmm_gated_act_backward")
     return d_gate_up, h
 
 
@@ -783,7 +808,12 @@ def _adapter_weights(a, b, ids, scaling, T):
     return L, R, K, N
 
 
-def adapters(x, a, b, ids, y=None, scaling=None, out=None, u=None, out_dtype=torch.bfloat16, stream=None):
+def adapters_workspace_size(T, L) -> int:
+    return lib().bsmm_adapters_workspace_size(T, L)
+
+
+def adapters(x, a, b, ids, y=None, scaling=None, out=None, u=None, out_dtype=torch.bfloat16, workspace=None,
+             stream=None):
     """``out = y + scaling[id] * (x @ a[id].T) @ b[id].T`` for every token's
     adapter ``id = ids[t]`` (outside ``[0, L)``: none).
 
@@ -795,32 +825,52 @@ def adapters(x, a, b, ids, y=None, scaling=None, out=None, u=None, out_dtype=tor
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D bfloat16 tensor [T, K]")
     T = x.shape[0]
-    L, R, K, N = _adapter_weights(a, b, ids, scaling, T)
     dtype = y.dtype if y is not None else out.dtype if out is not None else out_dtype
-    ld_x = _rows(x, "x", (T, K), (torch.bfloat16,))
-    ld_y = _rows(y, "y", (T, N), _FLOATS) if y is not None else N
-    ld_out = _rows(out, "out", (T, N), (dtype,)) if out is not None else N
-    if dtype not in _FLOATS:
-        raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {dtype}")
-    if u is not None:
-        _want(u, "u", (T, R), dtypes=(torch.float32,))
-    dev = _on_device(a=a, b=b, ids=ids, scaling=scaling, u=u)
-    for n, t in (("x", x), ("y", y), ("out", out)):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
+    bf16, dev = torch.bfloat16, x.device
+    if (_current(x) and isinstance(a, torch.Tensor) and a.dim() == 3 and isinstance(b, torch.Tensor) and b.dim() == 3
+            and dtype in _FLOATS):
+        (L, R, K), N = a.shape, b.shape[1]
+        fit = (_fits(x, bf16, (T, K), dev) and _fits(a, bf16, (L, R, K), dev) and _fits(b, bf16, (L, N, R), dev)
+               and _fits(ids, torch.int32, (T,), dev)
+               and (scaling is None or _fits(scaling, torch.float32, (L,), dev))
+               and (y is None or _fits(y, dtype, (T, N), dev)) and (out is None or _fits(out, dtype, (T, N), dev))
+               and (u is None or _fits(u, torch.float32, (T, R), dev)) and workspace is None)
+    else:
+        fit = False
+    if fit:
+        ld_x, ld_y, ld_out = K, N, N
+    else:
+        L, R, K, N = _adapter_weights(a, b, ids, scaling, T)
+        ld_x = _rows(x, "x", (T, K), (bf16,))
+        ld_y = _rows(y, "y", (T, N), _FLOATS) if y is not None else N
+        ld_out = _rows(out, "out", (T, N), (dtype,)) if out is not None else N
+        if dtype not in _FLOATS:
+            raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {dtype}")
+        if u is not None:
+            _want(u, "u", (T, R), dtypes=(torch.float32,))
+        if workspace is not None:
+            _want(workspace, "workspace")
+        dev = _on_device(a=a, b=b, ids=ids, scaling=scaling, u=u, workspace=workspace)
+        for n, t in (("x", x), ("y", y), ("out", out)):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
     if out is None:
         out = _empty((T, N), dtype, dev, stream)
     if u is None:
         u = _empty((T, R), torch.float32, dev, stream)
+    if workspace is None:
+        need = adapters_workspace_size(T, L)
+        if need:
+            workspace = _empty((need,), torch.uint8, dev, stream)
     _check(lib().bsmm_adapters(T, K, N, R, L, x.data_ptr(), ld_x, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
-                               _ptr(scaling), _ptr(y), ld_y, out.data_ptr(), ld_out,
-                               BF16 if dtype == torch.bfloat16 else F32, u.data_ptr(), _stream(stream)),
+                               _at(scaling), _at(y), ld_y, out.data_ptr(), ld_out, BF16 if dtype is bf16 else F32,
+                               u.data_ptr(), _at(workspace), _nbytes(workspace), _raw_stream(stream, dev)),
            "bsmm_adapters")
     return out, u
 
 
-def adapters_backward_workspace_size(T, R) -> int:
-    return lib().bsmm_adapters_backward_workspace_size(T, R)
+def adapters_backward_workspace_size(T, R, L) -> int:
+    return lib().bsmm_adapters_backward_workspace_size(T, R, L)
 
 
 def adapters_backward(dy, x, a, b, ids, u, scaling=None, dx_base=None, x_scales=None, x_code="e4m3",
@@ -835,32 +885,49 @@ def adapters_backward(dy, x, a, b, ids, u, scaling=None, dx_base=None, x_scales=
     if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
         raise ValueError("dy must be a 2-D bfloat16 tensor [T, N]")
     T = dy.shape[0]
-    L, R, K, N = _adapter_weights(a, b, ids, scaling, T)
-    bf16 = (torch.bfloat16,)
-    ld_dy = _rows(dy, "dy", (T, N), bf16)
-    if x_scales is not None:
-        _want(x, "x", (T, K), itemsize=1)
-        if K % 32 == 0:  # else the library says why
-            _want(x_scales, "x_scales", (T, K // 32), itemsize=1)
-        ld_x, xt = K, _code(x_code)
+    if (_current(dy) and isinstance(a, torch.Tensor) and a.dim() == 3 and isinstance(b, torch.Tensor) and b.dim() == 3
+            and grad_dtype in _FLOATS and isinstance(x, torch.Tensor)):
+        one, dev = torch.bfloat16, dy.device
+        (L, R, K), N = a.shape, b.shape[1]
+        fit = (_fits(dy, one, (T, N), dev) and _fits(a, one, (L, R, K), dev) and _fits(b, one, (L, N, R), dev)
+               and _fits(ids, torch.int32, (T,), dev) and _fits(u, torch.float32, (T, R), dev)
+               and (scaling is None or _fits(scaling, torch.float32, (L,), dev))
+               and (_fits(x, one, (T, K), dev) if x_scales is None else
+                    K % 32 == 0 and x.element_size() == 1 and _fits(x, x.dtype, (T, K), dev)
+                    and _fits(x_scales, torch.uint8, (T, K // 32), dev))
+               and (dx_base is None or _fits(dx_base, one, (T, K), dev)) and (dx is None or _fits(dx, one, (T, K), dev))
+               and da is None and db is None and workspace is None)
     else:
-        ld_x, xt = _rows(x, "x", (T, K), bf16), BF16
-    _want(u, "u", (T, R), dtypes=(torch.float32,))
-    if grad_dtype not in _FLOATS:
-        raise ValueError("grad_dtype must be float32 or bfloat16")
-    for t, n, shape in ((dx_base, "dx_base", (T, K)), (dx, "dx", (T, K))):
-        if t is not None:
-            _want(t, n, shape, dtypes=bf16)
-    for t, n, shape in ((da, "da", (L, R, K)), (db, "db", (L, N, R))):
-        if t is not None:
-            _want(t, n, shape, dtypes=(grad_dtype,))
-    if workspace is not None:
-        _want(workspace, "workspace")
-    dev = _on_device(a=a, b=b, ids=ids, scaling=scaling, u=u, x_scales=x_scales, dx_base=dx_base, dx=dx, da=da, db=db,
-                     workspace=workspace, **({"x": x} if x_scales is not None else {}))
-    for n, t in (("dy", dy), ("x", x)):
-        if t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
+        fit = False
+    if fit:
+        ld_dy, ld_x, xt = N, K, (BF16 if x_scales is None else _code(x_code))
+    else:
+        L, R, K, N = _adapter_weights(a, b, ids, scaling, T)
+        bf16 = (torch.bfloat16,)
+        ld_dy = _rows(dy, "dy", (T, N), bf16)
+        if x_scales is not None:
+            _want(x, "x", (T, K), itemsize=1)
+            if K % 32 == 0:  # else the library says why
+                _want(x_scales, "x_scales", (T, K // 32), itemsize=1)
+            ld_x, xt = K, _code(x_code)
+        else:
+            ld_x, xt = _rows(x, "x", (T, K), bf16), BF16
+        _want(u, "u", (T, R), dtypes=(torch.float32,))
+        if grad_dtype not in _FLOATS:
+            raise ValueError("grad_dtype must be float32 or bfloat16")
+        for t, n, shape in ((dx_base, "dx_base", (T, K)), (dx, "dx", (T, K))):
+            if t is not None:
+                _want(t, n, shape, dtypes=bf16)
+        for t, n, shape in ((da, "da", (L, R, K)), (db, "db", (L, N, R))):
+            if t is not None:
+                _want(t, n, shape, dtypes=(grad_dtype,))
+        if workspace is not None:
+            _want(workspace, "workspace")
+        dev = _on_device(a=a, b=b, ids=ids, scaling=scaling, u=u, x_scales=x_scales, dx_base=dx_base, dx=dx, da=da, db=db,
+                         workspace=workspace, **({"x": x} if x_scales is not None else {}))
+        for n, t in (("dy", dy), ("x", x)):
+            if t.device != dev:
+                raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
     if dx is None:
         dx = _empty((T, K), torch.bfloat16, dev, stream)
     if da is None:
@@ -868,10 +935,11 @@ def adapters_backward(dy, x, a, b, ids, u, scaling=None, dx_base=None, x_scales=
     if db is None:
         db = _empty((L, N, R), grad_dtype, dev, stream)
     if workspace is None:
-        workspace = _empty(max(adapters_backward_workspace_size(T, R), 1), torch.uint8, dev, stream)
-    _check(lib().bsmm_adapters_backward(T, K, N, R, L, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, xt, _ptr(x_scales),
-                                        a.data_ptr(), b.data_ptr(), ids.data_ptr(), _ptr(scaling), u.data_ptr(),
-                                        _ptr(dx_base), K, dx.data_ptr(), da.data_ptr(), db.data_ptr(),
-                                        BF16 if grad_dtype == torch.bfloat16 else F32, _ptr(workspace),
-                                        _nbytes(workspace), _stream(stream)), "bsmm_adapters_backward")
+        workspace = _empty(max(adapters_backward_workspace_size(T, R, L), 1), torch.uint8, dev, stream)
+    _check(lib().bsmm_adapters_backward(T, K, N, R, L, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, xt, _at(x_scales),
+                                        a.data_ptr(), b.data_ptr(), ids.data_ptr(), _at(scaling), u.data_ptr(),
+                                        _at(dx_base), K, dx.data_ptr(), da.data_ptr(), db.data_ptr(),
+                                        BF16 if grad_dtype == torch.bfloat16 else F32, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
+           "bsmm_adapters_backward")
     return dx, da, db

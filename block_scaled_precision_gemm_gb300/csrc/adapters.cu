@@ -15,11 +15,12 @@
 // until each lane's share of an operand row is 16 consecutive bytes and the
 // fragments need no shared memory and no shuffles.
 //
-// Tokens of different adapters share MMA tiles.  A warp loops over the
-// distinct adapters among its rows; each adapter's product goes to
-// accumulators of its own, of which only the rows that belong to it are taken,
-// so that an infinity or NaN in one adapter's weights or in one token stays in
-// the rows it belongs to.
+// Few tokens are taken as they come, and those of different adapters share MMA
+// tiles: a warp loops over the distinct adapters among its rows; each
+// adapter's product goes to accumulators of its own, of which only the rows
+// that belong to it are taken, so that an infinity or NaN in one adapter's
+// weights or in one token stays in the rows it belongs to.  Many tokens are
+// sorted first, and a tile has one adapter.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -132,26 +133,26 @@ __device__ __forceinline__ int down_col(int j, int n, int nt) {
   return (j / 2) * 16 + (n / 2) * 4 + 2 * (j % 2) + (n % 2);
 }
 
-// A CTA has WR x WK warps: WR row tiles of 16 MT rows, the contraction split
-// over WK warps and over the CTAs of the cluster.  The partial sums are added
-// in a fixed order: over the warps through shared memory, over the cluster
-// through distributed shared memory, each CTA summing a share of the tile.
-template <int NT, int MT, int WR, int WK, bool TRANS, bool VEC, int UNROLL>
-__global__ void __launch_bounds__(WR* WK * 32) adapter_down(const Down p) {
-  constexpr int kRows = WR * MT * 16, kCols = NT * 8;
+// For few tokens, taken as they come.  A CTA takes up to 16 rows; the
+// contraction is split over its WK warps and over the CTAs of the cluster.  The
+// partial sums are added in a fixed order: over the warps through shared
+// memory, over the cluster through distributed shared memory, each CTA summing
+// a share of the tile.
+template <int NT, int WK, bool TRANS, bool VEC, int UNROLL>
+__global__ void __launch_bounds__(WK * 32) adapter_down(const Down p) {
+  constexpr int MT = 1, kRows = 16, kCols = NT * 8;
   extern __shared__ float part[];  // [WK][kRows][kCols]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int wr = warp / WK, wk = warp % WK;
+  const int wk = warp;
   const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);  // a cluster spans y
-  const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * (WR == 1 ? p.rows_per_tile : kRows);
-  const int64_t row0 = tile0 + wr * MT * 16;
-  const int tile_rows = WR == 1 ? p.rows_per_tile : MT * 16;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_tile;
+  const int tile_rows = p.rows_per_tile;
 
   int id = -1;  // lane i: the adapter of the warp's row i
   if (lane < tile_rows) id = adapter_of(p.ids, row0 + lane, p.T, p.L);
 
-  float* mine = part + (wk * kRows + wr * MT * 16) * kCols;
+  float* mine = part + wk * kRows * kCols;
 #pragma unroll
   for (int i = lane; i < MT * 16 * kCols; i += 32) mine[i] = 0.f;
   __syncwarp();
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(WR* WK * 32) adapter_down(const Down p) {
       }
   }
   __syncthreads();
-  constexpr int kThreads = WR * WK * 32, kElems = kRows * kCols;
+  constexpr int kThreads = WK * 32, kElems = kRows * kCols;
   if constexpr (WK > 1) {  // over the warps
     for (int i = tid; i < kElems; i += kThreads) {
       float v = part[i];
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(WR* WK * 32) adapter_down(const Down p) {
     __syncthreads();
   }
   grid_launch_dependents();
-  const int rows_here = static_cast<int>(min(static_cast<int64_t>(WR == 1 ? p.rows_per_tile : kRows), p.T - tile0));
+  const int rows_here = static_cast<int>(min(static_cast<int64_t>(tile_rows), p.T - row0));
   const int n = rows_here * p.R, share = (n + cs - 1) / cs;
   const int e_end = min(n, (rank + 1) * share);
   for (int e = rank * share + tid; e < e_end; e += kThreads) {
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(WR* WK * 32) adapter_down(const Down p) {
     } else {
       v = part[r * kCols + c];
     }
-    p.u[(tile0 + r) * p.R + c] = v;
+    p.u[(row0 + r) * p.R + c] = v;
   }
   __syncwarp();
   if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
@@ -361,15 +362,15 @@ __device__ __forceinline__ void store_out(Y* row, int64_t c, int64_t limit, cons
 // u keeps its binary32 precision (three terms for binary32 outputs, 16 bits of
 // it for bf16 ones), and runs along its columns, 32 at a time: lane q of each
 // row ends up with 8 consecutive outputs.
-template <int KT, int MT, int WR, int WN, typename Y, bool TRANS, bool VEC>
-__global__ void __launch_bounds__(WR* WN * 32) adapter_up(const Up p) {
+template <int KT, int WN, typename Y, bool TRANS, bool VEC>
+__global__ void __launch_bounds__(WN * 32) adapter_up(const Up p) {
+  constexpr int MT = 1;
   constexpr int TERMS = sizeof(Y) == 4 ? 3 : 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int wr = warp % WR, wn = warp / WR;
-  const int tile_rows = WR == 1 ? p.rows_per_tile : MT * 16;
-  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * WR + wr) * tile_rows;
-  const int64_t n_begin = (static_cast<int64_t>(blockIdx.y) * WN + wn) * p.cols_per_warp;
+  const int tile_rows = p.rows_per_tile;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tile_rows;
+  const int64_t n_begin = (static_cast<int64_t>(blockIdx.y) * WN + warp) * p.cols_per_warp;
   const int64_t n_end = min(n_begin + p.cols_per_warp, p.C);
 
   int id = -1;
@@ -483,10 +484,636 @@ __global__ void __launch_bounds__(WR* WN * 32) adapter_up(const Up p) {
 }
 
 // ---------------------------------------------------------------------------
+// Tokens in order of their adapter
+// ---------------------------------------------------------------------------
+// For many tokens the rows are worked on in tiles of one adapter each.  Every
+// segment of kSegment tokens is sorted by adapter on its own (a stable
+// counting sort in one CTA), which keeps the cost linear in T; a segment's
+// tokens without an adapter come last, under adapter -1.
+constexpr int kSegment = 8192, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortRounds = kSegment / kSortThreads;
+constexpr int kTileRows = 128;
+constexpr int kSortMaxL = 1024;
+
+struct Tile {
+  int adapter, start, count, unused;  // rows perm[start .. start + count)
+};
+
+// The sort's output in the caller's workspace.
+struct Order {
+  int* perm;      // [T]
+  int* starts;    // [segments][L + 2]: the first position of each adapter, of -1, and the segment's end
+  Tile* tiles;    // [segments][tiles_per_segment], unused ones with count 0
+  int tiles_per_segment, segments;
+};
+
+__host__ __device__ inline int tiles_per_segment(int64_t T, int L) {
+  const int64_t rows = T < kSegment ? T : kSegment;
+  const int64_t groups = L + 1 < rows ? L + 1 : rows;
+  return static_cast<int>((rows + kTileRows - 1) / kTileRows + groups);
+}
+
+__global__ void __launch_bounds__(kSortThreads) adapter_sort(const int* ids, int64_t T, int L, Order o) {
+  extern __shared__ uint16_t hist[];  // [kSortWarps][L + 1]: tokens of each adapter, then those before the warp's
+  __shared__ int first[kSortMaxL + 2], tile0[kSortMaxL + 2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = L + 1;
+  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kSegment;
+  for (int i = tid; i < kSortWarps * G; i += kSortThreads) hist[i] = 0;
+  int key[kSortRounds], rank[kSortRounds];
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    const int64_t t = s0 + (warp * kSortRounds + i) * 32 + lane;
+    key[i] = -1;
+    if (t < T) {
+      const int a = __ldg(ids + t);
+      key[i] = a >= 0 && a < L ? a : L;
+    }
+  }
+  __syncthreads();
+  grid_launch_dependents();
+  uint16_t* mine = hist + warp * G;
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i) {
+    const unsigned peers = __match_any_sync(0xFFFFFFFFu, key[i]);
+    const unsigned before = peers & ((1u << lane) - 1u);
+    if (key[i] >= 0) rank[i] = mine[key[i]] + __popc(before);
+    __syncwarp();
+    if (key[i] >= 0 && before == 0) mine[key[i]] = static_cast<uint16_t>(mine[key[i]] + __popc(peers));
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int k = tid; k < G; k += kSortThreads) {
+    int run = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int n = hist[w * G + k];
+      hist[w * G + k] = static_cast<uint16_t>(run);
+      run += n;
+    }
+    first[k] = run;
+    tile0[k] = (run + kTileRows - 1) / kTileRows;
+  }
+  __syncthreads();
+  if (warp == 0) {  // exclusive sums over the adapters
+    const int per = (G + 31) / 32, k0 = lane * per, k1 = min(G, k0 + per);
+    int n = 0, m = 0;
+    for (int k = k0; k < k1; ++k) {
+      n += first[k];
+      m += tile0[k];
+    }
+    int pn = n, pm = m;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int un = __shfl_up_sync(0xFFFFFFFFu, pn, d), um = __shfl_up_sync(0xFFFFFFFFu, pm, d);
+      if (lane >= d) {
+        pn += un;
+        pm += um;
+      }
+    }
+    pn -= n;
+    pm -= m;
+    for (int k = k0; k < k1; ++k) {
+      const int cn = first[k], cm = tile0[k];
+      first[k] = pn;
+      tile0[k] = pm;
+      pn += cn;
+      pm += cm;
+    }
+    if (k0 < G && k1 == G) {
+      first[G] = pn;
+      tile0[G] = pm;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortRounds; ++i)
+    if (key[i] >= 0)
+      o.perm[s0 + first[key[i]] + mine[key[i]] + rank[i]] =
+          static_cast<int>(s0) + (warp * kSortRounds + i) * 32 + lane;
+  int* starts = o.starts + static_cast<int64_t>(blockIdx.x) * (L + 2);
+  for (int k = tid; k <= G; k += kSortThreads) starts[k] = static_cast<int>(s0) + first[k];
+  Tile* tiles = o.tiles + static_cast<int64_t>(blockIdx.x) * o.tiles_per_segment;
+  for (int i = tid; i < o.tiles_per_segment; i += kSortThreads) {
+    Tile t{-1, 0, 0, 0};
+    if (i < tile0[G]) {
+      int lo = 0, hi = G - 1;  // the last group whose first tile is at or before i
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (tile0[mid] <= i)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int at = (i - tile0[lo]) * kTileRows;
+      t.adapter = lo == L ? -1 : lo;
+      t.start = static_cast<int>(s0) + first[lo] + at;
+      t.count = min(kTileRows, first[lo + 1] - first[lo] - at);
+    }
+    tiles[i] = t;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Staged copies
+// ---------------------------------------------------------------------------
+// BYTES (16 or 8) of a row into shared memory, asynchronously; `bytes` of them
+// are read, the rest are zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  else if constexpr (BYTES == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed; lane 8 i + r gives the
+// address of row r of matrix i.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Eight bf16 of a row from column c, zeros from `limit` on, into shared memory:
+// asynchronously when rows are 16-byte aligned (VEC), else element by element.
+template <bool VEC>
+__device__ __forceinline__ void stage8(uint32_t dst, const bf16* row, int64_t c, int64_t limit) {
+  if constexpr (VEC) {
+    const bool in = c < limit;
+    copy_async<16>(dst, in ? row + c : row, in ? 16 : 0);
+  } else {
+    uint32_t w[4];
+    load_row<8, false>(row, c, limit, w);
+    st_shared16(dst, w);
+  }
+}
+
+// Four of them (rows of R elements need R % 4 == 0 for VEC).
+template <bool VEC>
+__device__ __forceinline__ void stage4(uint32_t dst, const bf16* row, int64_t c, int64_t limit) {
+  if constexpr (VEC) {
+    const bool in = c < limit;
+    copy_async<8>(dst, in ? row + c : row, in ? 8 : 0);
+  } else {
+    uint32_t w[2];
+    load_row<4, false>(row, c, limit, w);
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[0]), "r"(w[1]) : "memory");
+  }
+}
+
+constexpr int kChunk = 64;  // columns of a stage
+
+// ---------------------------------------------------------------------------
+// u = W x for a tile of 128 tokens of one adapter
+// ---------------------------------------------------------------------------
+// As adapter_down, but the operands come through a ring of kStages stages of
+// 64 contraction columns, so that the bytes in flight do not depend on
+// registers: a lane's own pieces of x are copied to and read from places of its
+// own; the adapter's weights, which all row tiles of the CTA share, are read
+// once per CTA.
+//
+// Weights of a stage in shared memory: TRANS = false, row r's eight 16-byte
+// pieces, the halves swapped in odd rows; TRANS = true, the 64 rows of R
+// elements at a pitch of 2 RP + 16 bytes, in the order in which the MMA takes
+// them (see the load), so that each ldmatrix reads eight consecutive rows:
+// both without bank conflicts.
+template <int NT, bool TRANS>
+struct DownTile {
+  static constexpr int kMT = NT <= 8 ? 2 : 1;
+  static constexpr int kWR = 8 / kMT, kWK = kMT;  // warps along rows and along the contraction
+  static constexpr int kStages = 4;
+  static constexpr int kXBytes = kTileRows * kChunk * 2;
+  static constexpr int kPitch = TRANS ? NT * 16 + 16 : kChunk * 2;  // of the weights' rows
+  static constexpr int kWBytes = (TRANS ? kChunk : NT * 8) * kPitch;
+  static constexpr int kStageBytes = kXBytes + kWBytes;
+  static constexpr int kRing = kStages * kStageBytes, kSums = kWK * kTileRows * NT * 8 * 4;
+  static constexpr int kSmem = kRing > kSums ? kRing : kSums;
+};
+
+struct DownSorted {
+  Down d;
+  Order o;
+};
+
+template <int NT, bool TRANS, bool VEC>
+__global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__ DownSorted ps) {
+  using Cfg = DownTile<NT, TRANS>;
+  constexpr int MT = Cfg::kMT, WK = Cfg::kWK, kCols = NT * 8, kHalves = 2 / WK;
+  constexpr int kPitch = Cfg::kPitch;
+  extern __shared__ __align__(128) uint8_t ring[];
+  const Down& p = ps.d;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int wr = warp / WK, wk = warp % WK;
+  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
+  const uint32_t ring_at = smem_u32(ring);
+
+  // the padding of the weights' stages: ranks R .. 8 NT are never copied
+  if (p.R < kCols) {
+    for (int st = 0; st < Cfg::kStages; ++st) {
+      uint8_t* w = ring + st * Cfg::kStageBytes + Cfg::kXBytes;
+      for (int i = tid * 16; i < Cfg::kWBytes; i += 256 * 16)
+        *reinterpret_cast<uint4*>(w + i) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncthreads();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Tile tile = ps.o.tiles[blockIdx.x];
+  if (tile.count == 0) return;  // the whole cluster
+  if (tile.adapter < 0) {
+    for (int i = rank * 256 + tid; i < tile.count * p.R; i += cs * 256)
+      p.u[static_cast<int64_t>(ps.o.perm[tile.start + i / p.R]) * p.R + i % p.R] = 0.f;
+    return;
+  }
+  const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
+  const bf16* xr[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = wr * MT * 16 + m * 16 + h * 8 + g;  // rows past the tile repeat its last one and are not stored
+      xr[m][h] = p.x + ps.o.perm[tile.start + min(i, tile.count - 1)] * p.ld;
+    }
+  const int64_t chunks = (p.C + kChunk - 1) / kChunk;
+  const int64_t c_begin = chunks * rank / cs, c_end = chunks * (rank + 1) / cs;
+  const int n = static_cast<int>(c_end - c_begin);
+
+  auto issue = [&](int c) {  // chunk c of this CTA's range into stage c % kStages
+    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
+    const int64_t k = (c_begin + c) * kChunk;
+#pragma unroll
+    for (int hh = 0; hh < kHalves; ++hh)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          stage8<VEC>(at + (((hh * MT + m) * 2 + h) * 256 + tid) * 16, xr[m][h],
+                      k + (kHalves == 2 ? hh : wk) * 32 + 8 * q, p.C);
+    const uint32_t wt = at + Cfg::kXBytes;
+    if constexpr (!TRANS) {
+      for (int i = tid; i < p.R * 8; i += 256) {
+        const int r = i >> 3, piece = i & 7;
+        stage8<VEC>(wt + r * kPitch + ((piece ^ ((r & 1) * 4)) * 16), w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C);
+      }
+    } else {
+      // row c = 32 half + 8 a + 4 s + 2 b + e goes to place 32 half + (2 s + b) 8 + 2 a + e
+      const int pieces = (p.R + 3) / 4;
+      for (int i = tid; i < kChunk * pieces; i += 256) {
+        const int cc = i / pieces, piece = i - cc * pieces;
+        const int place = (cc & 32) + ((cc >> 1) & 3) * 8 + ((cc >> 3) & 3) * 2 + (cc & 1);
+        stage4<VEC>(wt + place * kPitch + piece * 8, w + (k + cc) * p.R, piece * 4, k + cc < p.C ? p.R : 0);
+      }
+    }
+  };
+
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+#pragma unroll
+  for (int c = 0; c < Cfg::kStages - 1; ++c) {
+    if (c < n) issue(c);
+    copy_commit();
+  }
+  for (int c = 0; c < n; ++c) {
+    copy_wait<Cfg::kStages - 2>();
+    __syncthreads();  // stage c is there for all; stage c - 1 has been read by all
+    if (c + Cfg::kStages - 1 < n) issue(c + Cfg::kStages - 1);
+    copy_commit();
+    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
+    const uint32_t wt = at + Cfg::kXBytes;
+#pragma unroll
+    for (int hh = 0; hh < kHalves; ++hh) {
+      const int half = kHalves == 2 ? hh : wk;
+      uint4 xa[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) xa[m][h] = ld_shared16(at + (((hh * MT + m) * 2 + h) * 256 + tid) * 16);
+      if constexpr (!TRANS) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int r = j * 8 + g;
+          const uint4 b = ld_shared16(wt + r * kPitch + (((half * 4 + q) ^ ((r & 1) * 4)) * 16));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, b.x, b.y);
+            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, b.z, b.w);
+          }
+        }
+      } else {
+        // one ldmatrix: both halves of steps 0 and 1 of n-tile j (matrix i = 2 s + b)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t b[4];
+          ldmatrix_x4_trans(wt + (half * 32 + lane) * kPitch + j * 16, b);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, b[0], b[1]);
+            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, b[2], b[3]);
+          }
+        }
+      }
+    }
+  }
+  copy_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);  // [WK][kTileRows][kCols]
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        *reinterpret_cast<float2*>(sums + (wk * kTileRows + wr * MT * 16 + m * 16 + h * 8 + g) * kCols + j * 8 + 2 * q) =
+            make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+  __syncthreads();
+  if constexpr (WK == 2) {
+    for (int i = tid; i < kTileRows * kCols; i += 256) sums[i] += sums[kTileRows * kCols + i];
+  }
+  if (cs > 1) {
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  const int total = tile.count * p.R, share = (total + cs - 1) / cs;
+  const int e_end = min(total, (rank + 1) * share);
+  for (int e = rank * share + tid; e < e_end; e += 256) {
+    const int r = e / p.R, c = e - r * p.R;
+    float v = 0.f;
+    if (cs > 1) {
+      const uint32_t addr = smem_u32(sums + r * kCols + c);
+      for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
+    } else {
+      v = sums[r * kCols + c];
+    }
+    p.u[static_cast<int64_t>(ps.o.perm[tile.start + r]) * p.R + c] = v;
+  }
+  __syncwarp();
+  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// ---------------------------------------------------------------------------
+// out = base + s W u for a tile of 128 tokens of one adapter
+// ---------------------------------------------------------------------------
+// As adapter_up, with base and the weights through a ring of stages of 64
+// columns.  Weights of a stage: TRANS = false, the 64 rows of R elements in the
+// order in which the MMA takes them, at a pitch of 2 RP bytes (+ 32 from RP =
+// 32 on); TRANS = true, R rows of 64 columns at a pitch of 192 bytes.  Either
+// way the fragment loads meet no bank conflicts.
+template <int KT, typename Y, bool TRANS>
+struct UpTile {
+  static constexpr int kMT = KT <= 4 && !(KT == 4 && sizeof(Y) == 4) ? 2 : 1;
+  static constexpr int kWR = 8 / kMT, kWN = kMT;
+  static constexpr int kStages = sizeof(Y) == 4 ? 3 : 4;
+  static constexpr int kYBytes = kTileRows * kChunk * static_cast<int>(sizeof(Y));
+  static constexpr int kPitch = TRANS ? 192 : KT * 32 + (KT >= 2 ? 32 : 0);  // of the weights' rows
+  static constexpr int kWBytes = (TRANS ? KT * 16 : kChunk) * kPitch;
+  static constexpr int kStageBytes = kYBytes + kWBytes;
+  static constexpr int kSmem = kStages * kStageBytes;
+};
+
+struct UpSorted {
+  Up d;
+  Order o;
+  int chunks_per_cta;
+};
+
+template <int KT, typename Y, bool TRANS, bool VEC>
+__global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ UpSorted ps) {
+  using Cfg = UpTile<KT, Y, TRANS>;
+  constexpr int MT = Cfg::kMT, WN = Cfg::kWN, kGroups = 2 / WN, RP = KT * 16;
+  constexpr int TERMS = sizeof(Y) == 4 ? 3 : 2;
+  constexpr int kPieces = sizeof(Y) / 2;  // 16-byte pieces of a lane's 8 columns
+  constexpr int kPitch = Cfg::kPitch;
+  extern __shared__ __align__(128) uint8_t ring[];
+  const Up& p = ps.d;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int wr = warp / WN, wn = warp % WN;
+  const uint32_t ring_at = smem_u32(ring);
+
+  const Tile tile = ps.o.tiles[blockIdx.x];  // of two launches before, done before the last one released this one
+  if (tile.count == 0) return;
+  const int64_t chunks = (p.C + kChunk - 1) / kChunk;
+  const int64_t c_begin = static_cast<int64_t>(blockIdx.y) * ps.chunks_per_cta;
+  const int n = static_cast<int>(min(static_cast<int64_t>(ps.chunks_per_cta), chunks - c_begin));
+  const bool plain = tile.adapter < 0;  // no product: out = base
+  const bf16* w = p.w + static_cast<int64_t>(plain ? 0 : tile.adapter) * p.R * p.C;
+
+  int64_t row[MT][2];
+  bool live[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = wr * MT * 16 + m * 16 + h * 8 + g;
+      live[m][h] = i < tile.count;
+      row[m][h] = ps.o.perm[tile.start + min(i, tile.count - 1)];
+    }
+  if (p.R < RP) {  // the padding of the weights' stages
+    for (int st = 0; st < Cfg::kStages; ++st) {
+      uint8_t* s = ring + st * Cfg::kStageBytes + Cfg::kYBytes;
+      for (int i = tid * 16; i < Cfg::kWBytes; i += 256 * 16)
+        *reinterpret_cast<uint4*>(s + i) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncthreads();
+  }
+  auto issue = [&](int c) {
+    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
+    const int64_t k = (c_begin + c) * kChunk;
+    if (p.base) {
+#pragma unroll
+      for (int cg = 0; cg < kGroups; ++cg)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t col = k + (kGroups == 2 ? cg : wn) * 32 + 8 * q;
+            const Y* src = static_cast<const Y*>(p.base) + row[m][h] * p.ld_base;
+            const uint32_t dst = at + ((((cg * MT + m) * 2 + h) * kPieces) * 256 + tid) * 16;
+            if constexpr (VEC) {
+              const bool in = col < p.C;
+#pragma unroll
+              for (int e = 0; e < kPieces; ++e)
+                copy_async<16>(dst + e * 256 * 16, in ? src + col + e * (16 / sizeof(Y)) : src, in ? 16 : 0);
+            } else {
+              float v[8];
+              load_out<Y, false>(src, col, p.C, v);
+              uint32_t bits[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) bits[e] = __float_as_uint(v[e]);
+              if constexpr (sizeof(Y) == 2) {
+                const uint32_t b[4] = {pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+                st_shared16(dst, b);
+              } else {
+                const uint32_t b0[4] = {bits[0], bits[1], bits[2], bits[3]}, b1[4] = {bits[4], bits[5], bits[6], bits[7]};
+                st_shared16(dst, b0);
+                st_shared16(dst + 256 * 16, b1);
+              }
+            }
+          }
+    }
+    if (plain) return;
+    const uint32_t wt = at + Cfg::kYBytes;
+    if constexpr (!TRANS) {
+      // column c = 32 group + 8 a + 2 j + e goes to place 32 group + 8 j + 2 a + e
+      const int pieces = (p.R + 3) / 4;
+      for (int i = tid; i < kChunk * pieces; i += 256) {
+        const int cc = i / pieces, piece = i - cc * pieces;
+        const int place = (cc & 32) + ((cc >> 1) & 3) * 8 + ((cc >> 3) & 3) * 2 + (cc & 1);
+        stage4<VEC>(wt + place * kPitch + piece * 8, w + (k + cc) * p.R, piece * 4, k + cc < p.C ? p.R : 0);
+      }
+    } else {
+      for (int i = tid; i < p.R * 8; i += 256) {
+        const int r = i >> 3, piece = i & 7;
+        stage8<VEC>(wt + r * kPitch + piece * 16, w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C);
+      }
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < Cfg::kStages - 1; ++c) {
+    if (c < n) issue(c);
+    copy_commit();
+  }
+  const float sc = plain ? 0.f : (p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f);
+  grid_dependency_wait();  // u is the launch before this one's
+  uint32_t ua[MT][KT][2][2][TERMS];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int ks = 0; ks < KT; ++ks)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = ks * 16 + 4 * q + e;
+          v[e] = !plain && r < p.R ? p.u[row[m][h] * p.R + r] : 0.f;
+        }
+        split_pair<TERMS>(v[0], v[1], ua[m][ks][h][0]);
+        split_pair<TERMS>(v[2], v[3], ua[m][ks][h][1]);
+      }
+  for (int c = 0; c < n; ++c) {
+    copy_wait<Cfg::kStages - 2>();
+    __syncthreads();
+    if (c + Cfg::kStages - 1 < n) issue(c + Cfg::kStages - 1);
+    copy_commit();
+    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
+    const uint32_t wt = at + Cfg::kYBytes;
+#pragma unroll
+    for (int cg = 0; cg < kGroups; ++cg) {
+      const int group = kGroups == 2 ? cg : wn;
+      float acc[MT][4][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+      if (!plain) {
+#pragma unroll
+        for (int ks = 0; ks < KT; ++ks) {
+          uint32_t wb[4][2];
+          if constexpr (!TRANS) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint2 v = ld_shared8(wt + (group * 32 + j * 8 + g) * kPitch + ks * 32 + q * 8);
+              wb[j][0] = v.x;
+              wb[j][1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = ks * 16 + (g / 2) * 4 + 2 * h + (g % 2);
+              const uint4 v = ld_shared16(wt + r * kPitch + (group * 4 + q) * 16);
+              wb[0][h] = transpose8x8(v.x);
+              wb[1][h] = transpose8x8(v.y);
+              wb[2][h] = transpose8x8(v.z);
+              wb[3][h] = transpose8x8(v.w);
+            }
+          }
+#pragma unroll
+          for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_bf16(acc[m][j], ua[m][ks][0][0][k], ua[m][ks][1][0][k], ua[m][ks][0][1][k], ua[m][ks][1][1][k],
+                         wb[j][0], wb[j][1]);
+        }
+      }
+      const int64_t col = (c_begin + c) * kChunk + group * 32 + 8 * q;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float y[8];
+          const uint32_t src = at + ((((cg * MT + m) * 2 + h) * kPieces) * 256 + tid) * 16;
+          if (p.base) {
+            const uint4 b = ld_shared16(src);
+            if constexpr (sizeof(Y) == 2) {
+              const uint32_t b4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[2 * e] = __uint_as_float(b4[e] << 16);
+                y[2 * e + 1] = __uint_as_float(b4[e] & 0xFFFF0000u);
+              }
+            } else {
+              const uint4 b2 = ld_shared16(src + 256 * 16);
+              const uint32_t b8[8] = {b.x, b.y, b.z, b.w, b2.x, b2.y, b2.z, b2.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(b8[e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = 0.f;
+          }
+          if (!plain) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) y[2 * j + e] = fmaf(sc, acc[m][j][2 * h + e], y[2 * j + e]);
+          }
+          if (live[m][h]) store_out<Y, VEC>(static_cast<Y*>(p.out) + row[m][h] * p.ld_out, col, p.C, y);
+        }
+    }
+  }
+  copy_wait<0>();
+}
+
+// ---------------------------------------------------------------------------
 // Weight gradients: sums over an adapter's tokens
 // ---------------------------------------------------------------------------
 // grad[l][r][c] = s[l] sum over the tokens t of l of coef[t][r] x[t][c],
-// written as [L][R][C] (dA) or [L][C][R] (dB).
+// written as [L][R][C] (dA) or [L][C][R] (dB); x is bf16 or an MXFP8
+// checkpoint.
 struct GradJob {
   const float* coef;  // [T][R]
   const void* x;      // [T][ld] bf16, or 8-bit codes
@@ -494,20 +1121,19 @@ struct GradJob {
   int64_t ld;
   void* out;
   int64_t C;
-  int tiles;          // column tiles of kGradCols
-  int out_cr;         // 1: [L][C][R]
+  int tiles;   // column tiles of kGradCols
+  int out_cr;  // 1: [L][C][R]
 };
 struct Grads {
   GradJob job[2];
-  const int* ids;
   const float* scaling;
-  int64_t T;
+  Order o;
   int R, L;
-  int e5m2;     // the codes' type
+  int e5m2;    // the codes' type
+  int coef16;  // the coefficients' rows are 16-byte aligned
 };
-constexpr int kGradCols = 128;   // columns of a CTA: 4 warps of 32
-constexpr int kGradRows = 64;    // tokens of a block
-constexpr int kGradWindow = 512; // blocks whose use a CTA lists at a time
+constexpr int kGradCols = 128;  // columns of a CTA: 4 warps of 32
+constexpr int kGradRows = 64;   // tokens of a stage
 
 // Eight 8-bit codes times 2^e as bf16 pairs (exact).
 __device__ __forceinline__ void codes_to_bf16(uint2 c, uint32_t scale_byte, bool e5m2, uint32_t (&w)[4]) {
@@ -528,28 +1154,46 @@ __device__ __forceinline__ void codes_to_bf16(uint2 c, uint32_t scale_byte, bool
   }
 }
 
-// 8 warps: 4 across the tile's columns x 2 across a block's tokens.  The
-// blocks that hold tokens of the adapter are dealt out over the CTAs of the
-// cluster (y); partial sums meet in a fixed order, over the two warps in
-// shared memory and over the cluster in distributed shared memory.
+template <int MR, int TERMS>
+struct GradTile {
+  static constexpr int kStages = MR <= 2 ? 4 : (MR <= 4 ? 3 : 2);
+  static constexpr int kXBytes = kGradRows * kGradCols * 2;
+  static constexpr int kCoefBytes = kGradRows * MR * 16 * 4;
+  static constexpr int kStageBytes = kXBytes + kCoefBytes + 256;  // + scale bytes of a checkpoint's rows
+  static constexpr int kFragBytes = (kGradRows / 16) * MR * TERMS * 512;
+  // ring, coefficient fragments, and the decoded tile of a checkpoint
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kFragBytes + kXBytes;
+  static_assert(static_cast<size_t>(MR) * 16 * kGradCols * 4 <= kSmem, "the sums reuse the ring");
+};
+
+// One CTA: an adapter's tokens, taken 64 at a time from the sorted order, by
+// 128 columns; the blocks are dealt out over the CTAs of the cluster (y).  The
+// 8 warps are 4 across the columns x 2 across a block's tokens.  Tokens are the
+// contraction axis of both operands, so both reach the MMA transposed: x by
+// ldmatrix.trans from its staged tile, the coefficients as fragments that the
+// CTA splits into TERMS bf16 terms once for all its columns.  A block's sum is
+// added to the running one in binary32 outside the MMA (whose accumulation
+// truncates; adding every product there lost 1e-6 of the result over 8192
+// tokens).  Partial sums meet in a fixed order.
 template <int MR, int TERMS, typename G, bool VEC>
 __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Grads p) {
-  constexpr int kSteps = kGradRows / 16;
-  extern __shared__ __align__(16) uint8_t gsm[];
-  // coefficient fragments [step][MR][TERMS][lane][4 words]; the sums reuse the space
-  uint32_t* frag = reinterpret_cast<uint32_t*>(gsm);
-  float* sums = reinterpret_cast<float*>(gsm);  // [16 MR][kGradCols]
-  __shared__ int bid[kGradRows];
-  __shared__ uint8_t flags[kGradWindow];
+  using Cfg = GradTile<MR, TERMS>;
+  constexpr int kSteps = kGradRows / 16, RP = MR * 16;
+  constexpr bool kFlush = MR <= 4;
+  extern __shared__ __align__(128) uint8_t ring[];
+  uint32_t* frag = reinterpret_cast<uint32_t*>(ring + Cfg::kStages * Cfg::kStageBytes);
+  uint8_t* decoded = ring + Cfg::kStages * Cfg::kStageBytes + Cfg::kFragBytes;
+  float* sums = reinterpret_cast<float*>(ring);  // [RP][kGradCols], at the end
+  const uint32_t ring_at = smem_u32(ring);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int wc = warp & 3, wt = warp >> 2;
   const bool second = blockIdx.x >= static_cast<unsigned>(p.job[0].tiles);
   const GradJob& j = p.job[second ? 1 : 0];
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? p.job[0].tiles : 0)) * kGradCols + wc * 32;
+  const bool kept = j.x_scales != nullptr;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? p.job[0].tiles : 0)) * kGradCols;
   const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
   const int a = static_cast<int>(blockIdx.z);
-  const int64_t blocks = (p.T + kGradRows - 1) / kGradRows;
 
   float acc[MR][4][4];
 #pragma unroll
@@ -560,80 +1204,173 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
 
   grid_dependency_wait();
-  int turn = 0;  // blocks with the adapter so far: dealt to the ranks in turn
-  for (int64_t w0 = 0; w0 < blocks; w0 += kGradWindow) {
-    const int wn = static_cast<int>(min(static_cast<int64_t>(kGradWindow), blocks - w0));
-    __syncthreads();
-    for (int b = warp; b < wn; b += 8) {
-      const int64_t t = (w0 + b) * kGradRows + lane;
-      const bool f0 = t < p.T && __ldg(p.ids + t) == a, f1 = t + 32 < p.T && __ldg(p.ids + t + 32) == a;
-      const unsigned any = __ballot_sync(0xFFFFFFFFu, f0 || f1);
-      const unsigned all = __ballot_sync(0xFFFFFFFFu, f0 && f1);
-      if (lane == 0) flags[b] = all == 0xFFFFFFFFu ? 2 : (any ? 1 : 0);
-    }
-    __syncthreads();
-    for (int b = 0; b < wn; ++b) {
-      const int flag = flags[b];
-      if (!flag) continue;
-      if (turn++ % cs != rank) continue;
-      const int64_t t0 = (w0 + b) * kGradRows;
-      __syncthreads();  // the last block's fragments have been read
-      if (tid < kGradRows) bid[tid] = t0 + tid < p.T ? __ldg(p.ids + t0 + tid) : -1;
-      // fragments: logical (= actual) tokens 16 step + 2 q .., rank 16 m + g
-      for (int i = tid; i < kSteps * MR * 32; i += 256) {
-        const int fl = i & 31, fm = (i >> 5) % MR, fs = (i >> 5) / MR;
-        const int fg = fl >> 2, fq = fl & 3;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // a0..a3: rank half e % 2, token half e / 2
-          const int r = fm * 16 + (e & 1) * 8 + fg;
-          const int64_t t = t0 + fs * 16 + (e >> 1) * 8 + 2 * fq;
-          float v[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const bool on = r < p.R && t + k < p.T && (flag == 2 || __ldg(p.ids + t + k) == a);
-            v[k] = on ? j.coef[(t + k) * p.R + r] : 0.f;
-          }
-          uint32_t w[TERMS];
-          split_pair<TERMS>(v[0], v[1], w);
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) frag[(((fs * MR + fm) * TERMS + k) * 32 + fl) * 4 + e] = w[k];
-        }
+  // this CTA's blocks: number i of the adapter's blocks over all segments goes to rank i % cs
+  struct Walk {
+    int seg, pos, end, turn;
+  };
+  auto enter = [&](Walk& k) {  // the segment's range of this adapter
+    const int* s = p.o.starts + static_cast<int64_t>(k.seg) * (p.L + 2) + a;
+    k.pos = s[0];
+    k.end = s[1];
+  };
+  auto settle = [&](Walk& k) -> bool {  // to the next block of this rank; false: none is left
+    while (true) {
+      while (k.pos >= k.end) {
+        if (++k.seg >= p.o.segments) return false;
+        enter(k);
       }
-      __syncthreads();
-#pragma unroll
-      for (int s2 = 0; s2 < kSteps / 2; ++s2) {
-        const int s = 2 * s2 + wt;
-        uint32_t xb[4][2];  // [n-tile][half]: tokens 16 s + 8 half + .., columns by 8 q
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int tr = s * 16 + h * 8 + g;
-          const int64_t t = t0 + tr;
-          uint32_t v[4] = {0u, 0u, 0u, 0u};
-          if (t < p.T && (flag == 2 || bid[tr] == a)) {
-            if (j.x_scales) {
-              if (c0 + 8 * q < j.C) {
-                const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(j.x) + t * j.ld + c0 + 8 * q));
-                codes_to_bf16(c, __ldg(j.x_scales + t * (j.C / 32) + c0 / 32), p.e5m2 != 0, v);
-              }
-            } else {
-              load_row<8, VEC>(static_cast<const bf16*>(j.x) + t * j.ld, c0 + 8 * q, j.C, v);
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) xb[n][h] = transpose8x8(v[n]);
-        }
-#pragma unroll
-        for (int m = 0; m < MR; ++m)
-#pragma unroll
-          for (int k = TERMS - 1; k >= 0; --k) {
-            const uint4 f = *reinterpret_cast<const uint4*>(frag + (((s * MR + m) * TERMS + k) * 32 + lane) * 4);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) mma_bf16(acc[m][n], f.x, f.y, f.z, f.w, xb[n][0], xb[n][1]);
-          }
-      }
+      if (k.turn % cs == rank) return true;
+      ++k.turn;
+      k.pos += kGradRows;
     }
+  };
+  Walk ahead{0, 0, 0, 0};
+  bool more = p.o.segments > 0;
+  if (more) {
+    enter(ahead);
+    more = settle(ahead);
   }
-  // accumulator column g' = 2 q + e of n-tile n is column 8 q + 2 n + e
+
+  // copies rows perm[pos .. end) (at most 64) into a stage; rows past them are zeros
+  auto issue = [&](int st, int pos, int end) {
+    const uint32_t at = ring_at + st * Cfg::kStageBytes;
+    const int rows = min(kGradRows, end - pos);
+    if (!kept) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (tid >> 4) + 16 * i, piece = tid & 15;
+        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
+        stage8<VEC>(at + r * 256 + ((piece ^ (r & 7)) * 16), static_cast<const bf16*>(j.x) + t * j.ld, c0 + piece * 8,
+                    r < rows ? j.C : 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = (tid >> 3) + 32 * i, piece = tid & 7;
+        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
+        const int64_t c = c0 + piece * 16;
+        const bool in = r < rows && c < j.C;
+        const uint8_t* row = static_cast<const uint8_t*>(j.x) + t * j.ld;
+        copy_async<16>(at + r * 128 + piece * 16, in ? row + c : row, in ? 16 : 0);
+      }
+      if (tid < kGradRows) {  // the row's scale bytes of the tile's (up to) four blocks
+        const int64_t t = tid < rows ? p.o.perm[pos + tid] : 0;
+        uint32_t four = 0u;
+        const int64_t nb = j.C / 32;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (tid < rows && c0 / 32 + b < nb) four |= static_cast<uint32_t>(__ldg(j.x_scales + t * nb + c0 / 32 + b)) << (8 * b);
+        *reinterpret_cast<uint32_t*>(ring + st * Cfg::kStageBytes + Cfg::kXBytes + Cfg::kCoefBytes + tid * 4) = four;
+      }
+    }
+    // coefficients, 4 ranks at a time where rows are aligned, else one by one; ranks past R are zeros
+    const uint32_t ct = at + Cfg::kXBytes;
+    if (p.coef16) {
+      for (int i = tid; i < kGradRows * (RP / 4); i += 256) {
+        const int r = i / (RP / 4), piece = i % (RP / 4);
+        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
+        const bool in = r < rows && piece * 4 < p.R;
+        const float* row = j.coef + t * p.R;
+        copy_async<16>(ct + (r * RP + piece * 4) * 4, in ? row + piece * 4 : row, in ? 16 : 0);
+      }
+    } else {
+      for (int i = tid; i < kGradRows * RP; i += 256) {
+        const int r = i / RP, c = i % RP;
+        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
+        const bool in = r < rows && c < p.R;
+        const float* row = j.coef + t * p.R;
+        copy_async<4>(ct + i * 4, in ? row + c : row, in ? 4 : 0);
+      }
+    }
+  };
+
+  int issued = 0, done = 0;  // blocks
+  auto next = [&]() {
+    if (more) {
+      issue(issued % Cfg::kStages, ahead.pos, ahead.end);
+      ++issued;
+      ++ahead.turn;
+      ahead.pos += kGradRows;
+      more = settle(ahead);
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int c = 0; c < Cfg::kStages - 1; ++c) next();
+  while (done < issued) {
+    copy_wait<Cfg::kStages - 2>();
+    __syncthreads();  // block `done` is there for all; the one before has been read by all
+    const int st = done % Cfg::kStages;
+    const uint8_t* stage = ring + st * Cfg::kStageBytes;
+    const float* coef = reinterpret_cast<const float*>(stage + Cfg::kXBytes);
+    // fragments: tokens 16 step + 8 (e / 2) + 2 q .., rank 16 m + 8 (e % 2) + g
+    for (int i = tid; i < kSteps * MR * 32; i += 256) {
+      const int fl = i & 31, fm = (i >> 5) % MR, fs = (i >> 5) / MR;
+      const int fg = fl >> 2, fq = fl & 3;
+      uint32_t w[4][TERMS];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* v = coef + (fs * 16 + (e >> 1) * 8 + 2 * fq) * RP + fm * 16 + (e & 1) * 8 + fg;
+        split_pair<TERMS>(v[0], v[RP], w[e]);
+      }
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k)
+        *reinterpret_cast<uint4*>(frag + (((fs * MR + fm) * TERMS + k) * 32 + fl) * 4) =
+            make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+    }
+    if (kept) {  // decode into the bf16 tile: thread, row tid / 4, block tid % 4
+      const int r = tid >> 2, b = tid & 3;
+      const uint32_t sb = stage[Cfg::kXBytes + Cfg::kCoefBytes + r * 4 + b];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2 c = *reinterpret_cast<const uint2*>(stage + r * 128 + b * 32 + i * 8);
+        uint32_t v[4];
+        codes_to_bf16(c, sb, p.e5m2 != 0, v);
+        *reinterpret_cast<uint4*>(decoded + r * 256 + (((b * 4 + i) ^ (r & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    __syncthreads();
+    next();  // into the stage of the block before
+    const uint32_t xt = kept ? smem_u32(decoded) : ring_at + st * Cfg::kStageBytes;
+    float part[MR][4][4];
+    if constexpr (kFlush) {
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[m][n][e] = 0.f;
+    }
+#pragma unroll
+    for (int s2 = 0; s2 < kSteps / 2; ++s2) {
+      const int s = 2 * s2 + wt;
+      uint32_t xb[2][4];  // [pair of n-tiles][tile 0 half 0, half 1, tile 1 half 0, half 1]
+#pragma unroll
+      for (int n2 = 0; n2 < 2; ++n2) {
+        const int r = s * 16 + (lane & 15), piece = wc * 4 + n2 * 2 + (lane >> 4);
+        ldmatrix_x4_trans(xt + r * 256 + ((piece ^ (r & 7)) * 16), xb[n2]);
+      }
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int k = TERMS - 1; k >= 0; --k) {
+          const uint4 f = *reinterpret_cast<const uint4*>(frag + (((s * MR + m) * TERMS + k) * 32 + lane) * 4);
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            mma_bf16(kFlush ? part[m][n] : acc[m][n], f.x, f.y, f.z, f.w, xb[n / 2][(n % 2) * 2], xb[n / 2][(n % 2) * 2 + 1]);
+        }
+    }
+    if constexpr (kFlush) {
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[m][n][e] += part[m][n][e];
+    }
+    ++done;
+  }
+  copy_wait<0>();
   __syncthreads();
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
@@ -646,16 +1383,18 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
           for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float* d = sums + (m * 16 + h * 8 + g) * kGradCols + wc * 32 + 8 * q + 2 * n + e;
+              float* d = sums + (m * 16 + h * 8 + g) * kGradCols + wc * 32 + 8 * n + 2 * q + e;
               *d = pass ? *d + acc[m][n][2 * h + e] : acc[m][n][2 * h + e];
             }
     }
     __syncthreads();
   }
-  if (cs > 1) cluster_sync();
+  if (cs > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
   const float s = p.scaling ? __ldg(p.scaling + a) : 1.f;
-  const int64_t cta_c0 = c0 - wc * 32;
-  const int cols = static_cast<int>(min(static_cast<int64_t>(kGradCols), j.C - cta_c0));
+  const int cols = static_cast<int>(min(static_cast<int64_t>(kGradCols), j.C - c0));
   const int n = p.R * cols, share = (n + cs - 1) / cs;
   const int e_end = min(n, (rank + 1) * share);
   G* out = static_cast<G*>(j.out) + static_cast<int64_t>(a) * p.R * j.C;
@@ -676,7 +1415,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       v = sums[r * kGradCols + c];
     }
     v *= s;
-    const int64_t at = j.out_cr ? (cta_c0 + c) * p.R + r : static_cast<int64_t>(r) * j.C + cta_c0 + c;
+    const int64_t at = j.out_cr ? (c0 + c) * p.R + r : static_cast<int64_t>(r) * j.C + c0 + c;
     if constexpr (sizeof(G) == 2)
       out[at] = __float2bfloat16_rn(v);
     else
@@ -723,46 +1462,53 @@ cudaError_t launch(const char* name, void (*kernel)(P), const P& p, dim3 grid, i
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// From this many tokens on they are sorted and worked on in tiles of one
+// adapter; below, taken as they come, several adapters to a tile.
+constexpr int64_t kSortFrom = 2048;
+
 template <int NT, bool TRANS, bool VEC>
-cudaError_t down_rank(Down p, const DeviceCtx* ctx, cudaStream_t s) {
-  const int64_t chunks = ceil_div(p.C, 32);
-  if (p.T >= 2048) {
-    constexpr int MT = NT <= 8 ? 2 : 1, WR = 4, WK = 2, kRows = WR * MT * 16;
-    constexpr int U = NT <= 2 ? 4 : (NT <= 4 ? 2 : 1);
-    const int64_t tiles = ceil_div(p.T, kRows);
+cudaError_t down_rank(Down p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
+  if (o) {
+    using Cfg = DownTile<NT, TRANS>;
+    const int64_t slots = static_cast<int64_t>(o->segments) * o->tiles_per_segment;
+    const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));  // likely in use
     unsigned cs = 1;
-    while (cs < 8 && tiles * cs < 4 * ctx->num_sms && chunks >= 4 * WK * cs) cs *= 2;
-    const size_t smem = static_cast<size_t>(WK) * kRows * NT * 8 * 4;
-    return launch("adapter_down", adapter_down<NT, MT, WR, WK, TRANS, VEC, U>, p,
-                  dim3(static_cast<unsigned>(tiles), cs), WR * WK * 32, smem, cs, false, s);
+    while (cs < 8 && tiles * cs * 2 <= 2 * ctx->num_sms && p.C >= 4 * kChunk * static_cast<int64_t>(cs)) cs *= 2;
+    return launch("adapter_down_tile", adapter_down_tile<NT, TRANS, VEC>, DownSorted{p, *o},
+                  dim3(static_cast<unsigned>(slots), cs), 256, Cfg::kSmem, cs, true, s);
   }
+  const int64_t chunks = ceil_div(p.C, 32);
   constexpr int WK = 8, U = NT <= 4 ? 4 : 2;
   unsigned cs = 8;
   while (cs > 1 && chunks < static_cast<int64_t>(WK) * cs) cs /= 2;
   p.rows_per_tile = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, ceil_div(p.T * cs, ctx->num_sms))));
   const int64_t tiles = ceil_div(p.T, p.rows_per_tile);
   const size_t smem = static_cast<size_t>(WK) * 16 * NT * 8 * 4;
-  return launch("adapter_down", adapter_down<NT, 1, 1, WK, TRANS, VEC, U>, p, dim3(static_cast<unsigned>(tiles), cs),
-                WK * 32, smem, cs, false, s);
+  return launch("adapter_down", adapter_down<NT, WK, TRANS, VEC, U>, p, dim3(static_cast<unsigned>(tiles), cs), WK * 32,
+                smem, cs, false, s);
 }
 
 template <bool TRANS, bool VEC>
-cudaError_t down(const Down& p, const DeviceCtx* ctx, cudaStream_t s) {
-  if (p.R <= 8) return down_rank<1, TRANS, VEC>(p, ctx, s);
-  if (p.R <= 16) return down_rank<2, TRANS, VEC>(p, ctx, s);
-  if (p.R <= 32) return down_rank<4, TRANS, VEC>(p, ctx, s);
-  if (p.R <= 64) return down_rank<8, TRANS, VEC>(p, ctx, s);
-  return down_rank<16, TRANS, VEC>(p, ctx, s);
+cudaError_t down(const Down& p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
+  if (p.R <= 8) return down_rank<1, TRANS, VEC>(p, o, ctx, s);
+  if (p.R <= 16) return down_rank<2, TRANS, VEC>(p, o, ctx, s);
+  if (p.R <= 32) return down_rank<4, TRANS, VEC>(p, o, ctx, s);
+  if (p.R <= 64) return down_rank<8, TRANS, VEC>(p, o, ctx, s);
+  return down_rank<16, TRANS, VEC>(p, o, ctx, s);
 }
 
 template <int KT, typename Y, bool TRANS, bool VEC>
-cudaError_t up_rank(Up p, const DeviceCtx* ctx, cudaStream_t s) {
-  if (p.T >= 2048) {
-    constexpr int MT = KT <= 4 ? 2 : 1, WR = 4, WN = 2;
-    p.cols_per_warp = 256;
-    const dim3 grid(static_cast<unsigned>(ceil_div(p.T, WR * MT * 16)),
-                    static_cast<unsigned>(ceil_div(p.C, static_cast<int64_t>(p.cols_per_warp) * WN)));
-    return launch("adapter_up", adapter_up<KT, MT, WR, WN, Y, TRANS, VEC>, p, grid, WR * WN * 32, 0, 1, true, s);
+cudaError_t up_rank(Up p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
+  if (o) {
+    using Cfg = UpTile<KT, Y, TRANS>;
+    const int64_t slots = static_cast<int64_t>(o->segments) * o->tiles_per_segment;
+    const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));
+    const int64_t chunks = ceil_div(p.C, kChunk);
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 2 * ctx->num_sms / tiles));
+    UpSorted u{p, *o, static_cast<int>(ceil_div(chunks, splits))};
+    return launch("adapter_up_tile", adapter_up_tile<KT, Y, TRANS, VEC>, u,
+                  dim3(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, u.chunks_per_cta))), 256,
+                  Cfg::kSmem, 1, true, s);
   }
   constexpr int WN = 4;
   p.cols_per_warp = 32;
@@ -770,56 +1516,99 @@ cudaError_t up_rank(Up p, const DeviceCtx* ctx, cudaStream_t s) {
   p.rows_per_tile =
       static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, ceil_div(p.T * col_tiles, 4 * ctx->num_sms))));
   const dim3 grid(static_cast<unsigned>(ceil_div(p.T, p.rows_per_tile)), static_cast<unsigned>(col_tiles));
-  return launch("adapter_up", adapter_up<KT, 1, 1, WN, Y, TRANS, VEC>, p, grid, WN * 32, 0, 1, true, s);
+  return launch("adapter_up", adapter_up<KT, WN, Y, TRANS, VEC>, p, grid, WN * 32, 0, 1, true, s);
 }
 
 template <typename Y, bool TRANS, bool VEC>
-cudaError_t up(const Up& p, const DeviceCtx* ctx, cudaStream_t s) {
-  if (p.R <= 16) return up_rank<1, Y, TRANS, VEC>(p, ctx, s);
-  if (p.R <= 32) return up_rank<2, Y, TRANS, VEC>(p, ctx, s);
-  if (p.R <= 64) return up_rank<4, Y, TRANS, VEC>(p, ctx, s);
-  return up_rank<8, Y, TRANS, VEC>(p, ctx, s);
+cudaError_t up(const Up& p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
+  if (p.R <= 16) return up_rank<1, Y, TRANS, VEC>(p, o, ctx, s);
+  if (p.R <= 32) return up_rank<2, Y, TRANS, VEC>(p, o, ctx, s);
+  if (p.R <= 64) return up_rank<4, Y, TRANS, VEC>(p, o, ctx, s);
+  return up_rank<8, Y, TRANS, VEC>(p, o, ctx, s);
 }
 
 template <int MR, typename G, bool VEC>
-cudaError_t grads_rank(const Grads& p, const DeviceCtx* ctx, cudaStream_t s) {
+cudaError_t grads_rank(const Grads& p, int64_t T, const DeviceCtx* ctx, cudaStream_t s) {
   constexpr int TERMS = sizeof(G) == 4 ? 3 : 2;
-  const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(p.T, kGradRows);
+  const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
   unsigned cs = 1;
   while (cs < 8 && tiles * p.L * cs < 4 * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
-  const size_t smem = std::max<size_t>(static_cast<size_t>(kGradRows / 16) * MR * TERMS * 512,
-                                       static_cast<size_t>(MR) * 16 * kGradCols * 4);
   return launch("adapter_grads", adapter_grads<MR, TERMS, G, VEC>, p,
-                dim3(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L)), 256, smem, cs, true, s);
+                dim3(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L)), 256, GradTile<MR, TERMS>::kSmem, cs,
+                true, s);
 }
 
 template <typename G, bool VEC>
-cudaError_t grads(const Grads& p, const DeviceCtx* ctx, cudaStream_t s) {
-  if (p.R <= 16) return grads_rank<1, G, VEC>(p, ctx, s);
-  if (p.R <= 32) return grads_rank<2, G, VEC>(p, ctx, s);
-  if (p.R <= 64) return grads_rank<4, G, VEC>(p, ctx, s);
-  return grads_rank<8, G, VEC>(p, ctx, s);
+cudaError_t grads(const Grads& p, int64_t T, const DeviceCtx* ctx, cudaStream_t s) {
+  if (p.R <= 16) return grads_rank<1, G, VEC>(p, T, ctx, s);
+  if (p.R <= 32) return grads_rank<2, G, VEC>(p, T, ctx, s);
+  if (p.R <= 64) return grads_rank<4, G, VEC>(p, T, ctx, s);
+  return grads_rank<8, G, VEC>(p, T, ctx, s);
+}
+
+// The order's arrays in the workspace.
+Order order_at(void* workspace, int64_t T, int L) {
+  Order o{};
+  o.segments = static_cast<int>(ceil_div(T, kSegment));
+  o.tiles_per_segment = tiles_per_segment(T, L);
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  o.perm = reinterpret_cast<int*>(p);
+  p += align_up(static_cast<size_t>(T) * 4, 256);
+  o.starts = reinterpret_cast<int*>(p);
+  p += align_up(static_cast<size_t>(o.segments) * (L + 2) * 4, 256);
+  o.tiles = reinterpret_cast<Tile*>(p);
+  return o;
+}
+
+cudaError_t sort(const int* ids, int64_t T, int L, const Order& o, cudaStream_t s) {
+  const size_t smem = static_cast<size_t>(kSortWarps) * (L + 1) * 2;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(adapter_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  {
+    TraceScope tr("adapter_sort", s);
+    adapter_sort<<<o.segments, kSortThreads, smem, s>>>(ids, T, L, o);
+  }
+  return cudaGetLastError();
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
 
+size_t adapter_order_bytes(int64_t T, int64_t L) {
+  const int64_t segments = ceil_div(T, kSegment);
+  return align_up(static_cast<size_t>(T) * 4, 256) + align_up(static_cast<size_t>(segments) * (L + 2) * 4, 256) +
+         align_up(static_cast<size_t>(segments) * tiles_per_segment(T, static_cast<int>(L)) * sizeof(Tile), 256);
+}
+
+bool adapters_sorted(int64_t T, int64_t L) { return T >= kSortFrom && L <= kSortMaxL; }
+int64_t adapters_sort_max() { return kSortMaxL; }
+
 cudaError_t launch_adapters(const AdaptersRequest& r, cudaStream_t s) {
   const DeviceCtx* ctx = device_ctx();
   if (!ctx) return cudaErrorInitializationError;
   const bf16 *a = static_cast<const bf16*>(r.a), *b = static_cast<const bf16*>(r.b);
   const int R = static_cast<int>(r.R), L = static_cast<int>(r.L);
+  Order order{};
+  const Order* o = nullptr;
+  cudaError_t e;
+  if (adapters_sorted(r.T, r.L)) {
+    order = order_at(r.workspace, r.T, L);
+    o = &order;
+    e = sort(r.ids, r.T, L, order, s);
+    if (e != cudaSuccess) return e;
+  }
   const Down d{static_cast<const bf16*>(r.x), r.ld_x, a, r.ids, r.u, r.T, r.K, R, L, 16};
   const bool dv = r.K % 8 == 0 && r.ld_x % 8 == 0 && aligned(r.x, 16) && aligned(a, 16);
-  cudaError_t e = dv ? down<false, true>(d, ctx, s) : down<false, false>(d, ctx, s);
+  e = dv ? down<false, true>(d, o, ctx, s) : down<false, false>(d, o, ctx, s);
   if (e != cudaSuccess) return e;
   const Up u{r.u, b, r.ids, r.scaling, r.y, r.ld_y, r.out, r.ld_out, r.T, r.N, R, L, 16, 32};
-  const int n = 8;
-  const bool uv = r.N % n == 0 && r.ld_out % n == 0 && aligned(r.out, 16) && (!r.y || (r.ld_y % n == 0 && aligned(r.y, 16))) &&
-                  R % 4 == 0 && aligned(b, 8);
-  if (r.y_bf16) return uv ? up<bf16, false, true>(u, ctx, s) : up<bf16, false, false>(u, ctx, s);
-  return uv ? up<float, false, true>(u, ctx, s) : up<float, false, false>(u, ctx, s);
+  const bool uv = r.N % 8 == 0 && r.ld_out % 8 == 0 && aligned(r.out, 16) &&
+                  (!r.y || (r.ld_y % 8 == 0 && aligned(r.y, 16))) && R % 4 == 0 && aligned(b, 8);
+  if (r.y_bf16) return uv ? up<bf16, false, true>(u, o, ctx, s) : up<bf16, false, false>(u, o, ctx, s);
+  return uv ? up<float, false, true>(u, o, ctx, s) : up<float, false, false>(u, o, ctx, s);
 }
 
 cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s) {
@@ -827,30 +1616,37 @@ cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStrea
   if (!ctx) return cudaErrorInitializationError;
   const bf16 *a = static_cast<const bf16*>(r.a), *b = static_cast<const bf16*>(r.b);
   const int R = static_cast<int>(r.R), L = static_cast<int>(r.L);
-  cudaError_t e = cudaSuccess;
-  if (r.T > 0) {
-    const Down d{static_cast<const bf16*>(r.dy), r.ld_dy, b, r.ids, r.d, r.T, r.N, R, L, 16};
-    const bool dv = r.N % 8 == 0 && r.ld_dy % 8 == 0 && aligned(r.dy, 16) && R % 4 == 0 && aligned(b, 8);
-    e = dv ? down<true, true>(d, ctx, s) : down<true, false>(d, ctx, s);
-    if (e != cudaSuccess) return e;
-    const Up u{r.d, a, r.ids, r.scaling, r.dx_base, r.ld_dx, r.dx, r.ld_dx, r.T, r.K, R, L, 16, 32};
-    const bool uv = r.K % 8 == 0 && r.ld_dx % 8 == 0 && aligned(r.dx, 16) && aligned(r.dx_base, 16) && aligned(a, 16);
-    e = uv ? up<bf16, true, true>(u, ctx, s) : up<bf16, true, false>(u, ctx, s);
-    if (e != cudaSuccess) return e;
+  if (r.T == 0) {
+    const size_t g = r.grad_bf16 ? 2 : 4;
+    cudaError_t e = cudaMemsetAsync(r.da, 0, static_cast<size_t>(r.L) * R * r.K * g, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(r.db, 0, static_cast<size_t>(r.L) * R * r.N * g, s);
+    return e;
   }
+  const Order order = order_at(r.order, r.T, L);  // the gradients always go by it
+  cudaError_t e = sort(r.ids, r.T, L, order, s);
+  if (e != cudaSuccess) return e;
+  const Order* o = adapters_sorted(r.T, r.L) ? &order : nullptr;
+  const Down d{static_cast<const bf16*>(r.dy), r.ld_dy, b, r.ids, r.d, r.T, r.N, R, L, 16};
+  const bool dv = r.N % 8 == 0 && r.ld_dy % 8 == 0 && aligned(r.dy, 16) && R % 4 == 0 && aligned(b, 8);
+  e = dv ? down<true, true>(d, o, ctx, s) : down<true, false>(d, o, ctx, s);
+  if (e != cudaSuccess) return e;
+  const Up u{r.d, a, r.ids, r.scaling, r.dx_base, r.ld_dx, r.dx, r.ld_dx, r.T, r.K, R, L, 16, 32};
+  const bool uv = r.K % 8 == 0 && r.ld_dx % 8 == 0 && aligned(r.dx, 16) && aligned(r.dx_base, 16) && aligned(a, 16);
+  e = uv ? up<bf16, true, true>(u, o, ctx, s) : up<bf16, true, false>(u, o, ctx, s);
+  if (e != cudaSuccess) return e;
   Grads p{};
   p.job[0] = GradJob{r.d, r.x, r.x_scales, r.ld_x, r.da, r.K, static_cast<int>(ceil_div(r.K, kGradCols)), 0};
   p.job[1] = GradJob{r.u, r.dy, nullptr, r.ld_dy, r.db, r.N, static_cast<int>(ceil_div(r.N, kGradCols)), 1};
-  p.ids = r.ids;
   p.scaling = r.scaling;
-  p.T = r.T;
+  p.o = order;
   p.R = R;
   p.L = L;
   p.e5m2 = r.x_code == BSMM_E5M2;
+  p.coef16 = R % 4 == 0 && aligned(r.u, 16) && aligned(r.d, 16);
   const bool xv = r.x_scales || (r.K % 8 == 0 && r.ld_x % 8 == 0 && aligned(r.x, 16));
   const bool gv = xv && r.N % 8 == 0 && r.ld_dy % 8 == 0 && aligned(r.dy, 16);
-  if (r.grad_bf16) return gv ? grads<bf16, true>(p, ctx, s) : grads<bf16, false>(p, ctx, s);
-  return gv ? grads<float, true>(p, ctx, s) : grads<float, false>(p, ctx, s);
+  if (r.grad_bf16) return gv ? grads<bf16, true>(p, r.T, ctx, s) : grads<bf16, false>(p, r.T, ctx, s);
+  return gv ? grads<float, true>(p, r.T, ctx, s) : grads<float, false>(p, r.T, ctx, s);
 }
 
 }  // namespace bsmm

@@ -808,9 +808,15 @@ bsmm_status adapter_sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 }  // namespace
 
+size_t bsmm_adapters_workspace_size(int64_t T, int64_t L) {
+  if (T <= 0 || L <= 0 || !adapters_sorted(T, L)) return 0;
+  return adapter_order_bytes(T, L);
+}
+
 bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* x, int64_t ld_x,
                           const void* A, const void* B, const int32_t* ids, const float* scaling, const void* y,
-                          int64_t ld_y, void* out, int64_t ld_out, bsmm_dtype y_type, float* u, bsmm_stream_t stream) {
+                          int64_t ld_y, void* out, int64_t ld_out, bsmm_dtype y_type, float* u, void* workspace,
+                          size_t workspace_bytes, bsmm_stream_t stream) {
   const bsmm_status st = adapter_sizes(T, K, N, R, L);
   if (st != BSMM_OK) return st;
   if (y_type != BSMM_F32 && y_type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "y_type must be F32 or BF16");
@@ -825,13 +831,18 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
   if (!aligned_to(x, 2) || !aligned_to(A, 2) || !aligned_to(B, 2) || !aligned_to(ids, 4) || !aligned_to(scaling, 4) ||
       !aligned_to(y, ye) || !aligned_to(out, ye) || !aligned_to(u, 4))
     return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements");
-  const AdaptersRequest r{T, K, N, R, L, x, ld_x, A, B, ids, scaling, y, ld_y, out, ld_out, y_type == BSMM_BF16, u};
+  const size_t need = bsmm_adapters_workspace_size(T, L);
+  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+    return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) +
+                                        " bytes");
+  const AdaptersRequest r{T,   K,    N,  R,    L,    x,   ld_x,   A, B, ids,
+                          scaling, y, ld_y, out, ld_out, y_type == BSMM_BF16, u, workspace};
   return launched(launch_adapters(r, reinterpret_cast<cudaStream_t>(stream)), "adapters launch");
 }
 
-size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R) {
-  if (T <= 0 || R <= 0) return 0;
-  return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256);
+size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R, int64_t L) {
+  if (T <= 0 || R <= 0 || L <= 0) return 0;
+  return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256) + adapter_order_bytes(T, L);
 }
 
 bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* dy,
@@ -845,6 +856,8 @@ bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, i
   if (grad_type != BSMM_F32 && grad_type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "grad_type must be F32 or BF16");
   if (x_type != BSMM_BF16 && x_type != BSMM_E4M3 && x_type != BSMM_E5M2)
     return fail(BSMM_ERR_INVALID_ARG, "x_type must be BF16, E4M3 or E5M2");
+  if (L > adapters_sort_max())
+    return fail(BSMM_ERR_UNSUPPORTED, "gradients of up to " + std::to_string(adapters_sort_max()) + " adapters");
   const bool kept = x_type != BSMM_BF16;
   if (!dA || !dB || !A || !B) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
   if (T > 0 && (!dy || !x || !ids || !u || !dx || kept != (x_scales != nullptr)))
@@ -856,13 +869,14 @@ bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, i
       !aligned_to(ids, 4) || !aligned_to(scaling, 4) || !aligned_to(u, 4) || !aligned_to(dx_base, 2) ||
       !aligned_to(dx, 2) || !aligned_to(dA, ge) || !aligned_to(dB, ge))
     return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements (codes: 16 bytes)");
-  const size_t need = bsmm_adapters_backward_workspace_size(T, R);
+  const size_t need = bsmm_adapters_backward_workspace_size(T, R, L);
   if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) +
                                         " bytes");
   const AdaptersBackwardRequest r{T, K, N, R, L, dy, ld_dy, x, ld_x, static_cast<const uint8_t*>(x_scales), x_type, A, B,
                                   ids, scaling, u, dx_base, ld_dx, dx, dA, dB, grad_type == BSMM_BF16,
-                                  static_cast<float*>(workspace)};
+                                  static_cast<float*>(workspace),
+                                  static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T) * R * 4, 256)};
   return launched(launch_adapters_backward(r, reinterpret_cast<cudaStream_t>(stream)), "adapters backward launch");
 }
 

@@ -145,7 +145,8 @@ struct AdaptersRequest {
   void* out;
   int64_t ld_out;
   bool y_bf16;
-  float* u;  // [T][R]
+  float* u;         // [T][R]
+  void* workspace;  // adapter_order_bytes, where adapters_sorted
 };
 cudaError_t launch_adapters(const AdaptersRequest& r, cudaStream_t s);
 
@@ -168,8 +169,14 @@ struct AdaptersBackwardRequest {
   void* da;
   void* db;
   bool grad_bf16;
-  float* d;  // [T][R] scratch
+  float* d;     // [T][R] scratch
+  void* order;  // adapter_order_bytes of scratch
 };
+// Whether bsmm_adapters sorts its tokens (and needs the order's bytes), the
+// bytes, and the most adapters that can be sorted by.
+bool adapters_sorted(int64_t T, int64_t L);
+size_t adapter_order_bytes(int64_t T, int64_t L);
+int64_t adapters_sort_max();
 cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s);
 
 // Block-scaled formats of bsmm_gemm.

@@ -534,7 +534,8 @@ bsmm_status bsmm_linear_backward_checkpoint(const void* dY, const void* W, const
  *   u[t]   = A[l] x[t]                    binary32 sums
  *   out[t] = y[t] + scaling[l] * B[l] u[t]  binary32, rounded once
  *
- *   T tokens, in any order of adapters (neighbours that share one are fastest).
+ *   T tokens, in any order of adapters; up to 65535 adapters, of which any
+ *            number may be in use.
  *   ids [T] int32; an id outside [0, L) means no adapter: u[t] = 0, out[t] =
  *            y[t].  Rows never mix: an infinity or NaN in a token or in an
  *            adapter reaches only the tokens that use it.
@@ -545,12 +546,17 @@ bsmm_status bsmm_linear_backward_checkpoint(const void* dY, const void* W, const
  *            out of the same type at a pitch of ld_out.  out may be y itself
  *            (then ld_out = ld_y); no other overlap.
  *   u        binary32 [T, R], contiguous: an output, which the backward takes.
+ *   workspace  bsmm_adapters_workspace_size() bytes, 256-byte aligned: the
+ *            order of many tokens by their adapter; few tokens need none (0).
  * Rows whose start is 16-byte aligned (K, N and pitches multiples of 8, R of
  * 4) are read and written in 16-byte pieces; others element by element.
  * Every sum has a fixed order. */
+size_t bsmm_adapters_workspace_size(int64_t T, int64_t L);
+
 bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* x, int64_t ld_x,
                           const void* A, const void* B, const int32_t* ids, const float* scaling, const void* y,
-                          int64_t ld_y, void* out, int64_t ld_out, bsmm_dtype y_type, float* u, bsmm_stream_t stream);
+                          int64_t ld_y, void* out, int64_t ld_out, bsmm_dtype y_type, float* u, void* workspace,
+                          size_t workspace_bytes, bsmm_stream_t stream);
 
 /* The backward pass of bsmm_adapters, from dy = d(out) and the forward's u:
  *
@@ -570,9 +576,10 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
  *   dA [L, R, K], dB [L, N, R] of type grad_type (F32 or BF16), contiguous:
  *            overwritten; zero for an adapter without tokens.
  *   workspace  bsmm_adapters_backward_workspace_size() bytes, 256-byte
- *            aligned (holds d).
+ *            aligned (holds d and the order of the tokens by their adapter).
+ *   L up to 1024 (BSMM_ERR_UNSUPPORTED beyond).
  * dA and dB need the tokens' sums only: T == 0 writes zeros. */
-size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R);
+size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R, int64_t L);
 
 bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* dy,
                                    int64_t ld_dy, const void* x, int64_t ld_x, bsmm_dtype x_type,

@@ -87,7 +87,7 @@ def test_linear_binding():
 
 def adapters_args(**kw):
     d = dict(T=4, K=64, N=32, R=8, L=2, x=fake, ld_x=64, A=fake, B=fake, ids=fake, s=None, y=fake, ld_y=32, out=fake,
-             ld_out=32, yt=bsmm.BF16, u=fake, stream=None)
+             ld_out=32, yt=bsmm.BF16, u=fake, ws=None, wb=0, stream=None)
     d.update(kw)
     return list(d.values())
 
@@ -97,7 +97,8 @@ def adapters_args(**kw):
     (dict(L=0), bsmm.ERR_SHAPE), (dict(R=129), bsmm.ERR_UNSUPPORTED), (dict(yt=bsmm.E4M3), bsmm.ERR_INVALID_ARG),
     (dict(x=None), bsmm.ERR_INVALID_ARG), (dict(u=None), bsmm.ERR_INVALID_ARG), (dict(ld_x=63), bsmm.ERR_SHAPE),
     (dict(ld_y=31), bsmm.ERR_SHAPE), (dict(ld_y=40), bsmm.ERR_SHAPE), (dict(x=odd), bsmm.ERR_ALIGNMENT),
-    (dict(ids=ctypes.c_void_p(4098)), bsmm.ERR_ALIGNMENT), (dict(T=0, x=None, out=None), bsmm.OK)])
+    (dict(ids=ctypes.c_void_p(4098)), bsmm.ERR_ALIGNMENT), (dict(T=8192), bsmm.ERR_WORKSPACE),
+    (dict(T=8192, ws=fake, wb=100), bsmm.ERR_WORKSPACE), (dict(T=0, x=None, out=None), bsmm.OK)])
 def test_adapters_library(lib, change, status):
     assert lib.bsmm_adapters(*adapters_args(**change)) == status
 
@@ -115,7 +116,7 @@ def backward_args(**kw):
     (dict(xt=bsmm.INT8), bsmm.ERR_INVALID_ARG), (dict(xt=bsmm.E4M3), bsmm.ERR_INVALID_ARG),
     (dict(xs=fake), bsmm.ERR_INVALID_ARG), (dict(K=40, ld_x=40, ld_dx=40, xt=bsmm.E4M3, xs=fake), bsmm.ERR_SHAPE),
     (dict(ld_x=96, xt=bsmm.E4M3, xs=fake), bsmm.ERR_SHAPE), (dict(ld_dy=31), bsmm.ERR_SHAPE),
-    (dict(dA=None), bsmm.ERR_INVALID_ARG), (dict(ws=None), bsmm.ERR_WORKSPACE), (dict(wb=127), bsmm.ERR_WORKSPACE),
+    (dict(dA=None), bsmm.ERR_INVALID_ARG), (dict(ws=None), bsmm.ERR_WORKSPACE), (dict(wb=127), bsmm.ERR_WORKSPACE), (dict(L=1025), bsmm.ERR_UNSUPPORTED),
     (dict(ws=ctypes.c_void_p(4100)), bsmm.ERR_WORKSPACE), (dict(dy=odd), bsmm.ERR_ALIGNMENT)])
 def test_adapters_backward_library(lib, change, status):
     assert lib.bsmm_adapters_backward(*backward_args(**change)) == status
@@ -163,8 +164,10 @@ def test_linear_library(lib, change, status):
 
 
 def test_workspace_query(lib):
-    assert bsmm.adapters_backward_workspace_size(0, 8) == 0
-    assert bsmm.adapters_backward_workspace_size(100, 8) >= 100 * 8 * 4
+    assert bsmm.adapters_workspace_size(64, 64) == 0  # few tokens are not sorted
+    assert bsmm.adapters_workspace_size(8192, 4) >= 8192 * 4
+    assert bsmm.adapters_backward_workspace_size(0, 8, 4) == 0
+    assert bsmm.adapters_backward_workspace_size(100, 8, 4) >= 100 * 8 * 4 + 100 * 4
 
 
 def test_oracle_adapters_are_a_dense_product_per_token():
