@@ -238,9 +238,12 @@ cudaError_t atoms_request(const void* x, bool bf16, int64_t B, int64_t rows, int
   const int fmt = atom_format(code, scale);
   const int bs = fmt == kFmtNVF4 ? 16 : 32;
   const int per_tile = fmt == kFmtNVF4 ? 4 : (fmt == kFmtMXF4 ? 2 : 1);
-  const int64_t k_tiles = ceil_div(K, fmt == kFmtMXF8 ? 128 : 256);
-  cudaError_t e = cudaMemsetAsync(atoms, scale == BSMM_SCALE_UE4M3 ? 0 : 127, sf_atoms_plain_bytes(B, rows, K, fmt), s);
-  if (e != cudaSuccess) return e;
+  const int64_t kt = fmt == kFmtMXF8 ? 128 : 256, k_tiles = ceil_div(K, kt);
+  if (rows % 256 || K % kt) {  // else there is no padding
+    const cudaError_t e =
+        cudaMemsetAsync(atoms, scale == BSMM_SCALE_UE4M3 ? 0 : 127, sf_atoms_plain_bytes(B, rows, K, fmt), s);
+    if (e != cudaSuccess) return e;
+  }
   *q = transpose_in ? QuantRequest{x, bf16, K, rows, rows, bs, 1, code, scale, true, codes, K, atoms, 1}
                     : QuantRequest{x, bf16, B * rows, K, K, 1, bs, code, scale, false, codes, K, atoms, 1};
   q->sf_atoms = true;
@@ -685,7 +688,8 @@ bsmm_status linear_backward(const void* dY, const void* W, const BackwardX& X, i
     if (e == cudaSuccess) e = launch_quantize_pair(q_wt, q_xt, s);
   } else {
     if (e == cudaSuccess) e = launch_quantize(q_wt, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(xt_s, 127, sf_atoms_plain_bytes(1, K, M, kFmtMXF8), s);
+    if (e == cudaSuccess && (K % 256 || M % 128))  // the padding's neutral scale
+      e = cudaMemsetAsync(xt_s, 127, sf_atoms_plain_bytes(1, K, M, kFmtMXF8), s);
     if (e == cudaSuccess)
       e = launch_requantize_cols(RequantRequest{X.x, X.scales, X.code, X.scale, M, K, ft, xt, xt_s}, s);
   }
@@ -763,7 +767,7 @@ bsmm_status bsmm_gated_act(const void* gate_up, bsmm_dtype x_type, int64_t M, in
     return fail(BSMM_ERR_ALIGNMENT, "F32 scales must be 4-byte aligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool atoms = hq && h_scales_are_atoms;
-  if (atoms) {  // the padding's neutral scale
+  if (atoms && (M % 256 || I % 128)) {  // the padding's neutral scale
     const cudaError_t e = cudaMemsetAsync(h_scales, 127, sf_atoms_plain_bytes(1, M, I, kFmtMXF8), s);
     if (e != cudaSuccess) return cuda_fail(e, "gated activation launch");
   }

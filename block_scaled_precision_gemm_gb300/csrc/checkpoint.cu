@@ -13,10 +13,15 @@
 //   requant_cols  a checkpoint [M, K] into MXFP8 codes of its transpose
 //                 (blocks of 32 along M), the linear layer's backward operand.
 //
-// The gated kernels are elementwise but for the blocks' maxima: a thread takes
-// 8 consecutive columns of gate and the 8 of up beside them, so a 1 x 32 block
-// is 4 neighbouring lanes and a 1 x 128 block 16, reduced by xor-shuffles; no
-// shared memory, one read of each input and one write of each output.
+// The gated kernels are elementwise but for the blocks' maxima: in the forward
+// a thread takes 16 consecutive columns of gate and the 16 of up beside them,
+// so a 1 x 32 block is 2 neighbouring lanes and a 1 x 128 block 8, reduced by
+// xor-shuffles; no shared memory, one read of each input and one write of each
+// output.  A thread keeps its columns and steps down the rows, so that every
+// address advances by a constant.  The forward is close to the instruction
+// issue limit before HBM's: the arithmetic runs on pairs (packed binary32,
+// bf16x2) where it can.  The backward, which has no maxima to find, takes 8
+// columns a thread: every access of a warp is then one contiguous run.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -30,95 +35,158 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float silu_sigmoid(float g) {
-  // exp and the division by their approximate forms (2 ulp): h and the
-  // gradients are rounded to bf16 or 8 bits right after
-  return __fdividef(1.f, 1.f + __expf(-g));
+constexpr int kFwdPer = 16, kBwdPer = 8;  // columns of a thread
+
+// exp and the reciprocal by their approximate forms (2 ulp, subnormals flushed):
+// h and the gradients are rounded to bf16 or 8 bits right after, or are within
+// 2^-20 of their magnitude as binary32.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 1 / (1 + exp(-g)) of a pair
+__device__ __forceinline__ float2 sigmoid2(float2 g) {
+  const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
+  const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
-// act(g).  GELU is the exact form g Phi(g), Phi through erfc so that its
-// lower tail keeps its relative precision.
-template <int ACT>
-__device__ __forceinline__ float act_value(float g) {
-  if constexpr (ACT == BSMM_SILU) return g * silu_sigmoid(g);
-  return 0.5f * g * erfcf(g * -0.70710678118654752f);
-}
+// g Phi(g), Phi through erfc so that its lower tail keeps its relative
+// precision.
+__device__ __forceinline__ float gelu(float g) { return 0.5f * g * erfcf(g * -0.70710678118654752f); }
 
-// act(g) and its derivative.  In GELU's lower tail erfc(x) turns a relative
+// g Phi(g) and its derivative.  In the lower tail erfc(x) turns a relative
 // error of x into 2 x^2 times as much; x = -g / sqrt(2) is therefore corrected
 // for its rounding to first order, by the density that the derivative needs
 // anyway.
+__device__ __forceinline__ void gelu_slope(float g, float& f, float& df) {
+  constexpr float c = 0.70710678118654752f;
+  constexpr float c_lo = static_cast<float>(0.70710678118654752440 - static_cast<double>(c));
+  const float density = 0.39894228040143268f * __expf(-0.5f * g * g);
+  const float x = -g * c;
+  const float dx = fmaf(-g, c_lo, fmaf(-g, c, -x));
+  const float cdf = 0.5f * erfcf(x) - 1.41421356237309505f * dx * density;
+  f = g * cdf;
+  df = cdf + g * density;
+}
+
+// act(g) of a pair.
 template <int ACT>
-__device__ __forceinline__ void act_slope(float g, float& f, float& df) {
+__device__ __forceinline__ float2 act2(float2 g) {
+  if constexpr (ACT == BSMM_SILU) return __fmul2_rn(g, sigmoid2(g));
+  return make_float2(gelu(g.x), gelu(g.y));
+}
+
+// act(g) and its derivative of a pair.
+template <int ACT>
+__device__ __forceinline__ void act_slope2(float2 g, float2& f, float2& df) {
   if constexpr (ACT == BSMM_SILU) {
-    const float p = silu_sigmoid(g);
-    f = g * p;
-    df = p + f * (1.f - p);
+    const float2 p = sigmoid2(g);
+    f = __fmul2_rn(g, p);
+    df = __ffma2_rn(f, __ffma2_rn(p, both(-1.f), both(1.f)), p);  // p + g p (1 - p)
   } else {
-    constexpr float c = 0.70710678118654752f;
-    constexpr float c_lo = static_cast<float>(0.70710678118654752440 - static_cast<double>(c));
-    const float density = 0.39894228040143268f * __expf(-0.5f * g * g);
-    const float x = -g * c;
-    const float dx = fmaf(-g, c_lo, fmaf(-g, c, -x));
-    const float cdf = 0.5f * erfcf(x) - 1.41421356237309505f * dx * density;
-    f = g * cdf;
-    df = cdf + g * density;
+    gelu_slope(g.x, f.x, df.x);
+    gelu_slope(g.y, f.y, df.y);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Values
 // ---------------------------------------------------------------------------
-// Eight consecutive elements, raw: one 16-byte vector of bf16, two of binary32.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const void* p) { a = __ldcs(static_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// kPer consecutive elements, raw.
+template <typename T, int kPer>
+struct Raw {
+  static constexpr int kWords = kPer * static_cast<int>(sizeof(T)) / 16;
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const void* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcs(static_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void values(float2 (&v)[kPer / 2]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[4 * i + k] = make_float2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xFFFF0000u));
+      } else {
+        v[2 * i] = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+        v[2 * i + 1] = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+      }
     }
   }
-  __device__ __forceinline__ float absmax() const {
-    const uint32_t m = bf16x2_max_abs(bf16x2_max_abs(a.x, a.y), bf16x2_max_abs(a.z, a.w));
-    return fmaxf(bf16_lo_abs(m), bf16_hi_abs(m));
-  }
-};
-template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p) {
-    a = __ldcs(static_cast<const float4*>(p));
-    b = __ldcs(static_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-  __device__ __forceinline__ float absmax() const {
-    return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
-                 fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
-  }
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
+// The largest magnitudes of gate's and up's elements over W lanes.
+template <int W>
+__device__ __forceinline__ unsigned lanes_mask() {
+  return ((1u << W) - 1u) << ((threadIdx.x & 31u) & ~static_cast<unsigned>(W - 1));
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float m) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes_mask<W>(), m, o));
+  return m;
+}
+using RawBf16 = Raw<__nv_bfloat16, kFwdPer>;
+using RawF32 = Raw<float, kFwdPer>;
+template <int W>
+__device__ __forceinline__ void absmax2(const RawBf16& g, const RawBf16& u, float& mg, float& mu) {
+  // maxima of bf16 numbers are bf16 numbers: both travel in one word
+  auto fold = [](const RawBf16& r) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < RawBf16::kWords; ++i)
+      m = bf16x2_max_abs(m, bf16x2_max_abs(bf16x2_max_abs(r.w[i].x, r.w[i].y), bf16x2_max_abs(r.w[i].z, r.w[i].w)));
+    return bf16x2_max_abs(m, m >> 16);
+  };
+  uint32_t m = __byte_perm(fold(g), fold(u), 0x5410);
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) m = bf16x2_max_abs(m, __shfl_xor_sync(lanes_mask<W>(), m, o));
+  mg = bf16_lo_abs(m);
+  mu = bf16_hi_abs(m);
+}
+template <int W>
+__device__ __forceinline__ void absmax2(const RawF32& g, const RawF32& u, float& mg, float& mu) {
+  auto fold = [](const RawF32& r) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < RawF32::kWords; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(r.w[i].x)), fabsf(__uint_as_float(r.w[i].y))),
+                         fmaxf(fabsf(__uint_as_float(r.w[i].z)), fabsf(__uint_as_float(r.w[i].w)))));
+    return m;
+  };
+  mg = lanes_max<W>(fold(g));
+  mu = lanes_max<W>(fold(u));
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(void* p, const float (&v)[8]) {
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, int kPairs>
+__device__ __forceinline__ void store(void* p, const float2 (&v)[kPairs]) {
+  constexpr int kPer = 2 * kPairs;
+  uint4* dst = static_cast<uint4*>(p);
   if constexpr (sizeof(T) == 2) {
-    *static_cast<uint4*>(p) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+#pragma unroll
+    for (int i = 0; i < kPer / 8; ++i)
+      dst[i] = make_uint4(pack_bf16(v[4 * i]), pack_bf16(v[4 * i + 1]), pack_bf16(v[4 * i + 2]), pack_bf16(v[4 * i + 3]));
   } else {
-    static_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    static_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i)
+      dst[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y), __float_as_uint(v[2 * i + 1].x),
+                          __float_as_uint(v[2 * i + 1].y));
   }
 }
 
@@ -147,32 +215,43 @@ __device__ __forceinline__ Scale block_scale(float absmax, int code) {
     else
       s = fmaxf(absmax * (code == BSMM_E4M3 ? 1.f / 448.f : 1.f / 57344.f), 1e-10f);
     sc.s = s;
-    sc.inv = block_recip(s);
+    sc.inv = s >= 0x1p-80f && s <= 0x1p126f ? __frcp_rn(s) : 0.f;  // block_recip's number
     sc.stored = __float_as_uint(s);
   }
   return sc;
 }
 
-// Codes of eight elements of one block, in memory order.
+// Codes of a thread's elements of one block, in memory order.
 template <bool POW2>
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], const Scale& sc, int code) {
-  if constexpr (!POW2) {
-    if (code == BSMM_INT8 && sc.inv != 0.f) {
-      // |x / s| <= 127 (1 + 2^-24): adding 1.5 * 2^23 rounds the quotient to an
-      // integer, ties to even, in the low bits of the sum; its low byte is the
-      // two's complement code
-      uint32_t w[8];
+__device__ __forceinline__ uint4 encode(const float2 (&v)[kFwdPer / 2], const Scale& sc, int code) {
+  constexpr int kPer = kFwdPer;
+  uint32_t w[kPer / 4];
+  if (!POW2 && code == BSMM_INT8 && sc.inv != 0.f) {
+    // |x / s| <= 127 (1 + 2^-23): adding 1.5 * 2^23 rounds the quotient to an
+    // integer, ties to even, in the low bits of the sum; its low byte is the
+    // two's complement code
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 q = quot2_rn_int(make_float2(v[i], v[i + 1]), sc.s, sc.inv);
-        w[i] = __float_as_uint(q.x + 12582912.f);
-        w[i + 1] = __float_as_uint(q.y + 12582912.f);
-      }
-      return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
-                        __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
+    for (int i = 0; i < kPer / 4; ++i) {
+      const float2 a = __fadd2_rn(quot2_rn_int(v[2 * i], sc.s, sc.inv), both(12582912.f));
+      const float2 b = __fadd2_rn(quot2_rn_int(v[2 * i + 1], sc.s, sc.inv), both(12582912.f));
+      w[i] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                         __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+    }
+  } else {
+    float2 q[kPer / 2];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) q[i] = POW2 ? __fmul2_rn(v[i], both(sc.inv)) : quot2<false>(v[i].x, v[i].y, sc);
+    if (code == BSMM_E4M3) {
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i)
+        w[i] = cvt_e4m3x2(q[2 * i].x, q[2 * i].y) | (cvt_e4m3x2(q[2 * i + 1].x, q[2 * i + 1].y) << 16);
+    } else {  // E5M2, or INT8 with a scale outside quotient.cuh's range
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i)
+        w[i] = pack4(q[2 * i].x, q[2 * i].y, q[2 * i + 1].x, q[2 * i + 1].y, POW2 ? BSMM_E5M2 : code);
     }
   }
-  return make_uint2(encode4<POW2>(v[0], v[1], v[2], v[3], sc, code), encode4<POW2>(v[4], v[5], v[6], v[7], sc, code));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ float ue8m0_value(uint32_t b) {
@@ -196,35 +275,49 @@ __device__ __forceinline__ float2 fp8_pair(uint32_t two) {
 
 // Four codes of one word as values code * s.
 template <int CODE>
-__device__ __forceinline__ void values4(uint32_t w, float s, float* v) {
+__device__ __forceinline__ void values4(uint32_t w, float s, float2* v) {
   if constexpr (CODE == BSMM_INT8) {
     // the byte with its sign bit flipped is code + 128: as the low mantissa
     // bits of 2^23 it is exact, and so is the subtraction
     const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)) - 8388736.f) * s;
+    for (int i = 0; i < 2; ++i) {
+      const float2 c = make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + 2 * i)),
+                                   __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 + 2 * i)));
+      v[i] = __fmul2_rn(__fadd2_rn(c, both(-8388736.f)), both(s));
+    }
   } else {
-    const float2 lo = fp8_pair<CODE>(w & 0xFFFFu), hi = fp8_pair<CODE>(w >> 16);
-    v[0] = lo.x * s;
-    v[1] = lo.y * s;
-    v[2] = hi.x * s;
-    v[3] = hi.y * s;
+    v[0] = __fmul2_rn(fp8_pair<CODE>(w & 0xFFFFu), both(s));
+    v[1] = __fmul2_rn(fp8_pair<CODE>(w >> 16), both(s));
   }
 }
 
 // ---------------------------------------------------------------------------
 // Gated activation
 // ---------------------------------------------------------------------------
-// Largest of the `W` neighbouring lanes' values (W = 4 or 16; the lanes of one
-// block are all in the loop or all out of it).
-template <int W>
-__device__ __forceinline__ float lanes_max(float m) {
-  const unsigned lane = threadIdx.x & 31u;
-  const unsigned mask = ((1u << W) - 1u) << (lane & ~static_cast<unsigned>(W - 1));
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-  return m;
+// A thread's columns and rows.  The columns are cut into tiles (blockIdx.y) of
+// `width` threads each, and a CTA takes kThreads / width rows at a time; width
+// is a multiple of the lanes of a block, which thus share a row and a warp.
+struct Strips {
+  int width, rows;  // threads across a tile, rows of a CTA
+  int tiles;
+};
+struct Strip {
+  int64_t row, step;
+  int col;
+  bool on;
+  __device__ __forceinline__ Strip(const Strips& s, int per, int I) {
+    const int r = static_cast<int>(threadIdx.x) / s.width, c = static_cast<int>(threadIdx.x) - r * s.width;
+    row = static_cast<int64_t>(blockIdx.x) * s.rows + r;
+    step = static_cast<int64_t>(gridDim.x) * s.rows;
+    col = (static_cast<int>(blockIdx.y) * s.width + c) * per;
+    on = r < s.rows && col < I;
+  }
+};
+Strips strips(int64_t I, int per, int lanes) {  // lanes: of one block
+  const int64_t groups = I / per, tiles = ceil_div(groups, kThreads);
+  const int64_t width = ceil_div(ceil_div(groups, tiles), lanes) * lanes;
+  return Strips{static_cast<int>(width), static_cast<int>(kThreads / width), static_cast<int>(ceil_div(groups, width))};
 }
 
 struct GatedFwd {
@@ -239,98 +332,79 @@ struct GatedFwd {
   uint8_t* codes;
   void* scales;
   int code;
+  Strips strips;
 };
 
 constexpr int kKeepNone = 0, kKeepMx = 1, kKeepF32 = 2;
 
+// The next row's elements are loaded before this row's are worked on.
 template <typename In, int KEEP, int ACT, bool HQ>
-__device__ __forceinline__ void gated_fwd_one(const GatedFwd& p, int64_t row, int col, const Raw8<In>& rg,
-                                              const Raw8<In>& ru) {
-  const int I = p.I;
-  float g[8], u[8];
-  rg.values(g);
-  ru.values(u);
+__global__ void __launch_bounds__(kThreads, sizeof(In) == 2 ? 3 : 2) gated_fwd(const GatedFwd p) {
+  constexpr int kPer = kFwdPer;
+  constexpr bool POW2 = KEEP == kKeepMx;
+  constexpr int kBlock = POW2 ? 32 : 128, W = kBlock / kPer;
+  const Strip k(p.strips, kPer, p.I);
+  if (!k.on) return;
   const unsigned lane = threadIdx.x & 31u;
-  if constexpr (KEEP != kKeepNone) {
-    constexpr int W = KEEP == kKeepMx ? 4 : 16;
-    constexpr bool POW2 = KEEP == kKeepMx;
-    const Scale sg = block_scale<POW2>(lanes_max<W>(rg.absmax()), p.code);
-    const Scale su = block_scale<POW2>(lanes_max<W>(ru.absmax()), p.code);
-    uint8_t* dst = p.codes + row * 2 * I + col;
-    *reinterpret_cast<uint2*>(dst) = encode8<POW2>(g, sg, p.code);
-    *reinterpret_cast<uint2*>(dst + I) = encode8<POW2>(u, su, p.code);
-    if ((lane & (W - 1)) == 0) {
-      const int nb = I / (8 * W);  // blocks of gate in a row, as many of up after them
-      const int64_t at = row * 2 * nb + col / (8 * W);
-      if constexpr (POW2) {
-        static_cast<uint8_t*>(p.scales)[at] = static_cast<uint8_t>(sg.stored);
-        static_cast<uint8_t*>(p.scales)[at + nb] = static_cast<uint8_t>(su.stored);
-      } else {
-        static_cast<uint32_t*>(p.scales)[at] = sg.stored;
-        static_cast<uint32_t*>(p.scales)[at + nb] = su.stored;
+  const int64_t I = p.I;
+  const int64_t nb = I / kBlock;  // blocks of gate in a row, as many of up after them
+  const In* x = static_cast<const In*>(p.x) + k.row * p.ld + k.col;
+  uint8_t* codes = p.codes + k.row * 2 * I + k.col;
+  uint8_t* scales = static_cast<uint8_t*>(p.scales) + (k.row * 2 * nb + k.col / kBlock) * (POW2 ? 1 : 4);
+  uint8_t* h = static_cast<uint8_t*>(p.h) + (k.row * I + k.col) * (HQ ? 1 : 2);
+  Raw<In, kPer> rg, ru;
+  if (k.row < p.M) {
+    rg.load(x);
+    ru.load(x + I);
+  }
+  for (int64_t row = k.row; row < p.M; row += k.step) {
+    float2 g[kPer / 2], u[kPer / 2];
+    rg.values(g);
+    ru.values(u);
+    float mg = 0.f, mu = 0.f;
+    if constexpr (KEEP != kKeepNone) absmax2<W>(rg, ru, mg, mu);
+    x += k.step * p.ld;
+    if (row + k.step < p.M) {
+      rg.load(x);
+      ru.load(x + I);
+    }
+    if constexpr (KEEP != kKeepNone) {
+      const Scale sg = block_scale<POW2>(mg, p.code);
+      const Scale su = block_scale<POW2>(mu, p.code);
+      *reinterpret_cast<uint4*>(codes) = encode<POW2>(g, sg, p.code);
+      *reinterpret_cast<uint4*>(codes + I) = encode<POW2>(u, su, p.code);
+      if ((lane & (W - 1)) == 0) {
+        if constexpr (POW2) {
+          scales[0] = static_cast<uint8_t>(sg.stored);
+          scales[nb] = static_cast<uint8_t>(su.stored);
+        } else {
+          reinterpret_cast<uint32_t*>(scales)[0] = sg.stored;
+          reinterpret_cast<uint32_t*>(scales)[nb] = su.stored;
+        }
       }
+      codes += k.step * 2 * I;
+      scales += k.step * 2 * nb * (POW2 ? 1 : 4);
     }
-  }
-  float h[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = act_value<ACT>(g[i]) * u[i];
-  if constexpr (HQ) {
-    float m = 0.f;
+    for (int i = 0; i < kPer / 2; ++i) u[i] = __fmul2_rn(act2<ACT>(g[i]), u[i]);  // h
+    if constexpr (HQ) {
+      float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(h[i]));
-    const Scale sh = block_scale<true>(lanes_max<4>(m), p.h_code);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.h) + row * I + col) = encode8<true>(h, sh, p.h_code);
-    if ((lane & 3u) == 0) {
-      const int kb = col / 32;
-      const int w = static_cast<int>(row & 127);
-      const int64_t at = p.h_atoms ? ((row >> 7) * p.h_ks4 + (kb >> 2)) * 512 + (w & 31) * 16 + (w >> 5) * 4 + (kb & 3)
-                                   : row * (I / 32) + kb;
-      p.h_scales[at] = static_cast<uint8_t>(sh.stored);
+      for (int i = 0; i < kPer / 2; ++i) m = fmaxf(m, fmaxf(fabsf(u[i].x), fabsf(u[i].y)));
+      const Scale sh = block_scale<true>(lanes_max<32 / kPer>(m), p.h_code);
+      *reinterpret_cast<uint4*>(h) = encode<true>(u, sh, p.h_code);
+      if ((lane & (32 / kPer - 1)) == 0) {
+        const int kb = k.col / 32;
+        const int w = static_cast<int>(row & 127);
+        const int64_t at = p.h_atoms
+                               ? ((row >> 7) * p.h_ks4 + (kb >> 2)) * 512 + (w & 31) * 16 + (w >> 5) * 4 + (kb & 3)
+                               : row * (I / 32) + kb;
+        p.h_scales[at] = static_cast<uint8_t>(sh.stored);
+      }
+    } else {
+      store<__nv_bfloat16>(h, u);
     }
-  } else {
-    store8<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p.h) + row * I + col, h);
-  }
-}
-
-// Threads step over the rows' groups of 8 columns; two groups a turn, both
-// loaded before either is worked on.
-template <typename In, int KEEP, int ACT, bool HQ>
-__global__ void __launch_bounds__(kThreads) gated_fwd(const GatedFwd p) {
-  const int G = p.I / 8;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  const int64_t step_row = step / G;
-  const int step_grp = static_cast<int>(step % G);
-  int64_t row = first / G;
-  int grp = static_cast<int>(first % G);
-  const In* x = static_cast<const In*>(p.x);
-  while (row < p.M) {
-    const int64_t row0 = row;
-    const int col0 = grp * 8;
-    row += step_row;
-    grp += step_grp;
-    if (grp >= G) {
-      grp -= G;
-      ++row;
-    }
-    const int64_t row1 = row;
-    const int col1 = grp * 8;
-    row += step_row;
-    grp += step_grp;
-    if (grp >= G) {
-      grp -= G;
-      ++row;
-    }
-    const bool two = row1 < p.M;
-    Raw8<In> g0, u0, g1, u1;
-    g0.load(x + row0 * p.ld + col0);
-    u0.load(x + row0 * p.ld + p.I + col0);
-    if (two) {
-      g1.load(x + row1 * p.ld + col1);
-      u1.load(x + row1 * p.ld + p.I + col1);
-    }
-    gated_fwd_one<In, KEEP, ACT, HQ>(p, row0, col0, g0, u0);
-    if (two) gated_fwd_one<In, KEEP, ACT, HQ>(p, row1, col1, g1, u1);
+    h += k.step * I * (HQ ? 1 : 2);
   }
 }
 
@@ -342,83 +416,88 @@ struct GatedBwd {
   __nv_bfloat16* h;  // may be null
   int64_t M;
   int I;
+  Strips strips;
 };
 
 template <typename D, int CODE, bool POW2, int ACT>
-__global__ void __launch_bounds__(kThreads) gated_bwd(const GatedBwd p) {
-  constexpr int kBlock = POW2 ? 32 : 128;
-  const int I = p.I, G = I / 8, nb = I / kBlock;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  const int64_t step_row = step / G;
-  const int step_grp = static_cast<int>(step % G);
-  int64_t row = first / G;
-  int grp = static_cast<int>(first % G);
-  while (row < p.M) {
-    const int col = grp * 8;
-    const uint8_t* src = p.codes + row * 2 * I + col;
-    const uint2 cg = __ldcs(reinterpret_cast<const uint2*>(src));
-    const uint2 cu = __ldcs(reinterpret_cast<const uint2*>(src + I));
-    Raw8<D> rd;
-    rd.load(static_cast<const D*>(p.dh) + row * I + col);
-    const int64_t at = row * 2 * nb + col / kBlock;
-    float sg, su;
+__global__ void __launch_bounds__(kThreads, sizeof(D) == 2 ? 4 : 3) gated_bwd(const GatedBwd p) {
+  constexpr int kPer = kBwdPer, kBlock = POW2 ? 32 : 128;
+  const Strip k(p.strips, kPer, p.I);
+  if (!k.on) return;
+  const int64_t I = p.I, nb = I / kBlock;
+  const uint8_t* codes = p.codes + k.row * 2 * I + k.col;
+  const uint8_t* scales = static_cast<const uint8_t*>(p.scales) + (k.row * 2 * nb + k.col / kBlock) * (POW2 ? 1 : 4);
+  const D* dhp = static_cast<const D*>(p.dh) + k.row * I + k.col;
+  D* d = static_cast<D*>(p.d) + k.row * 2 * I + k.col;
+  __nv_bfloat16* h = p.h + (p.h ? k.row * I + k.col : 0);
+  uint2 cg, cu;
+  uint32_t sg, su;  // as stored
+  Raw<D, kPer> dh;
+  auto load = [&]() {
+    cg = __ldcs(reinterpret_cast<const uint2*>(codes));
+    cu = __ldcs(reinterpret_cast<const uint2*>(codes + I));
+    dh.load(dhp);
     if constexpr (POW2) {
-      sg = ue8m0_value(__ldg(static_cast<const uint8_t*>(p.scales) + at));
-      su = ue8m0_value(__ldg(static_cast<const uint8_t*>(p.scales) + at + nb));
+      sg = __ldg(scales);
+      su = __ldg(scales + nb);
     } else {
-      sg = __ldg(static_cast<const float*>(p.scales) + at);
-      su = __ldg(static_cast<const float*>(p.scales) + at + nb);
+      sg = __ldg(reinterpret_cast<const uint32_t*>(scales));
+      su = __ldg(reinterpret_cast<const uint32_t*>(scales) + nb);
     }
-    float g[8], u[8], dh[8], h[8];
-    values4<CODE>(cg.x, sg, g);
-    values4<CODE>(cg.y, sg, g + 4);
-    values4<CODE>(cu.x, su, u);
-    values4<CODE>(cu.y, su, u + 4);
-    rd.values(dh);
+  };
+  if (k.row < p.M) load();
+  for (int64_t row = k.row; row < p.M; row += k.step) {
+    const float vg = POW2 ? ue8m0_value(sg) : __uint_as_float(sg), vu = POW2 ? ue8m0_value(su) : __uint_as_float(su);
+    float2 g[kPer / 2], u[kPer / 2], v[kPer / 2], f[kPer / 2];
+    values4<CODE>(cg.x, vg, g);
+    values4<CODE>(cg.y, vg, g + 2);
+    values4<CODE>(cu.x, vu, u);
+    values4<CODE>(cu.y, vu, u + 2);
+    dh.values(v);
+    codes += k.step * 2 * I;
+    scales += k.step * 2 * nb * (POW2 ? 1 : 4);
+    dhp += k.step * I;
+    if (row + k.step < p.M) load();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float f, df;
-      act_slope<ACT>(g[i], f, df);
-      h[i] = f * u[i];
-      g[i] = dh[i] * u[i] * df;
-      u[i] = dh[i] * f;
+    for (int i = 0; i < kPer / 2; ++i) {
+      float2 df;
+      act_slope2<ACT>(g[i], f[i], df);
+      g[i] = __fmul2_rn(__fmul2_rn(v[i], u[i]), df);
+      u[i] = __fmul2_rn(f[i], u[i]);  // h
+      f[i] = __fmul2_rn(v[i], f[i]);
     }
-    D* dst = static_cast<D*>(p.d) + row * 2 * I + col;
-    store8<D>(dst, g);
-    store8<D>(dst + I, u);
-    if (p.h) store8<__nv_bfloat16>(p.h + row * I + col, h);
-    row += step_row;
-    grp += step_grp;
-    if (grp >= G) {
-      grp -= G;
-      ++row;
+    store<D>(d, g);
+    store<D>(d + I, f);
+    if (p.h) {
+      store<__nv_bfloat16>(h, u);
+      h += k.step * I;
     }
+    d += k.step * 2 * I;
   }
 }
 
-// Enough CTAs to fill the SMs with resident threads, no more than the work.
-unsigned gated_grid(int64_t groups, int per_thread, const DeviceCtx* ctx) {
-  const int64_t want = ceil_div(groups, static_cast<int64_t>(kThreads) * per_thread);
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, static_cast<int64_t>(ctx->num_sms) * 8)));
+// Enough CTAs to fill the SMs (`resident` on each), no more than the rows ask for.
+dim3 gated_grid(const Strips& s, int64_t M, int resident, const DeviceCtx* ctx) {
+  const int64_t want = ceil_div(M, s.rows), full = ceil_div(static_cast<int64_t>(ctx->num_sms) * resident, s.tiles);
+  return dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min(want, full))), static_cast<unsigned>(s.tiles));
 }
 
 template <typename In, int KEEP, int ACT>
-void launch_fwd(const GatedFwd& p, bool hq, unsigned grid, cudaStream_t s) {
+void launch_fwd(const GatedFwd& p, bool hq, dim3 grid, cudaStream_t s) {
   if (hq)
     gated_fwd<In, KEEP, ACT, true><<<grid, kThreads, 0, s>>>(p);
   else
     gated_fwd<In, KEEP, ACT, false><<<grid, kThreads, 0, s>>>(p);
 }
 template <typename In, int KEEP>
-void launch_fwd(const GatedFwd& p, int act, bool hq, unsigned grid, cudaStream_t s) {
+void launch_fwd(const GatedFwd& p, int act, bool hq, dim3 grid, cudaStream_t s) {
   if (act == BSMM_SILU)
     launch_fwd<In, KEEP, BSMM_SILU>(p, hq, grid, s);
   else
     launch_fwd<In, KEEP, BSMM_GELU>(p, hq, grid, s);
 }
 template <typename In>
-void launch_fwd(const GatedFwd& p, int keep, int act, bool hq, unsigned grid, cudaStream_t s) {
+void launch_fwd(const GatedFwd& p, int keep, int act, bool hq, dim3 grid, cudaStream_t s) {
   if (keep == kKeepNone)
     launch_fwd<In, kKeepNone>(p, act, hq, grid, s);
   else if (keep == kKeepMx)
@@ -428,14 +507,14 @@ void launch_fwd(const GatedFwd& p, int keep, int act, bool hq, unsigned grid, cu
 }
 
 template <typename D, int CODE, bool POW2>
-void launch_bwd(const GatedBwd& p, int act, unsigned grid, cudaStream_t s) {
+void launch_bwd(const GatedBwd& p, int act, dim3 grid, cudaStream_t s) {
   if (act == BSMM_SILU)
     gated_bwd<D, CODE, POW2, BSMM_SILU><<<grid, kThreads, 0, s>>>(p);
   else
     gated_bwd<D, CODE, POW2, BSMM_GELU><<<grid, kThreads, 0, s>>>(p);
 }
 template <typename D>
-void launch_bwd(const GatedBwd& p, int code, bool pow2, int act, unsigned grid, cudaStream_t s) {
+void launch_bwd(const GatedBwd& p, int code, bool pow2, int act, dim3 grid, cudaStream_t s) {
   if (code == BSMM_INT8)
     launch_bwd<D, BSMM_INT8, false>(p, act, grid, s);
   else if (code == BSMM_E4M3)
@@ -558,8 +637,9 @@ cudaError_t launch_gated_act(const GatedRequest& r, cudaStream_t s) {
   const bool hq = r.h_type != BSMM_BF16;
   const int keep = !r.codes ? kKeepNone : (r.scale == BSMM_SCALE_UE8M0 ? kKeepMx : kKeepF32);
   const GatedFwd p{r.x,      r.M,       r.ld, static_cast<int>(r.I), r.h,    static_cast<uint8_t*>(r.h_scales),
-                   r.h_type, r.h_atoms, r.h_ks4, static_cast<uint8_t*>(r.codes), r.scales, r.code};
-  const unsigned grid = gated_grid(r.M * (r.I / 8), 2, ctx);
+                   r.h_type, r.h_atoms, r.h_ks4, static_cast<uint8_t*>(r.codes), r.scales, r.code,
+                   strips(r.I, kFwdPer, keep == kKeepF32 ? 128 / kFwdPer : 32 / kFwdPer)};
+  const dim3 grid = gated_grid(p.strips, r.M, r.x_bf16 ? 3 : 2, ctx);
   {
     TraceScope tr("gated_fwd", s);
     if (r.x_bf16)
@@ -574,8 +654,8 @@ cudaError_t launch_gated_act_backward(const GatedBackwardRequest& r, cudaStream_
   const DeviceCtx* ctx = device_ctx();
   if (!ctx) return cudaErrorInitializationError;
   const GatedBwd p{r.dh, static_cast<const uint8_t*>(r.codes), r.scales, r.d, static_cast<__nv_bfloat16*>(r.h),
-                   r.M,  static_cast<int>(r.I)};
-  const unsigned grid = gated_grid(r.M * (r.I / 8), 1, ctx);
+                   r.M,  static_cast<int>(r.I), strips(r.I, kBwdPer, 1)};
+  const dim3 grid = gated_grid(p.strips, r.M, r.d_bf16 ? 4 : 3, ctx);
   {
     TraceScope tr("gated_bwd", s);
     if (r.d_bf16)
