@@ -543,11 +543,13 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const int* ids, int
   }
   __syncthreads();
   for (int k = tid; k < G; k += kSortThreads) {
-    int run = 0;
+    int n[kSortWarps], run = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) n[w] = hist[w * G + k];
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const int n = hist[w * G + k];
       hist[w * G + k] = static_cast<uint16_t>(run);
-      run += n;
+      run += n[w];
     }
     first[k] = run;
     tile0[k] = (run + kTileRows - 1) / kTileRows;
@@ -615,14 +617,12 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const int* ids, int
 // ---------------------------------------------------------------------------
 // Staged copies
 // ---------------------------------------------------------------------------
-// BYTES (16 or 8) of a row into shared memory, asynchronously; `bytes` of them
-// are read, the rest are zeros.
+// BYTES (16 or 4) into shared memory, asynchronously; `bytes` of them are read,
+// the rest are zeros.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes) {
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-  else if constexpr (BYTES == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -641,103 +641,115 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-// Four 8 x 8 matrices of 16-bit elements, transposed; lane 8 i + r gives the
-// address of row r of matrix i.
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-// Eight bf16 of a row from column c, zeros from `limit` on, into shared memory:
-// asynchronously when rows are 16-byte aligned (VEC), else element by element.
-template <bool VEC>
+// Eight bf16 of a row from column c, zeros from `limit` on, into shared memory.
 __device__ __forceinline__ void stage8(uint32_t dst, const bf16* row, int64_t c, int64_t limit) {
-  if constexpr (VEC) {
-    const bool in = c < limit;
-    copy_async<16>(dst, in ? row + c : row, in ? 16 : 0);
-  } else {
-    uint32_t w[4];
-    load_row<8, false>(row, c, limit, w);
-    st_shared16(dst, w);
-  }
-}
-
-// Four of them (rows of R elements need R % 4 == 0 for VEC).
-template <bool VEC>
-__device__ __forceinline__ void stage4(uint32_t dst, const bf16* row, int64_t c, int64_t limit) {
-  if constexpr (VEC) {
-    const bool in = c < limit;
-    copy_async<8>(dst, in ? row + c : row, in ? 8 : 0);
-  } else {
-    uint32_t w[2];
-    load_row<4, false>(row, c, limit, w);
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(w[0]), "r"(w[1]) : "memory");
-  }
+  uint32_t w[4];
+  load_row<8, false>(row, c, limit, w);
+  st_shared16(dst, w);
 }
 
 constexpr int kChunk = 64;  // columns of a stage
 
+// An operand of the tensor cores (tcgen05) staged in shared memory: ROWS rows
+// of E bf16 (16, 32 or a multiple of 64), in blocks of up to 64 columns, each
+// swizzled over its own width of 32, 64 or 128 bytes.  A row's 16-byte pieces
+// stay within its own line of a block, so an asynchronous copy of a row fills
+// one line (scattered over core matrices instead, the copies ran at half the
+// speed).  The MMA can read it with rows along M or N and columns along the
+// contraction, or the other way round.  Bases are 1024-byte aligned.
+template <int ROWS, int E>
+struct Staged {
+  static constexpr int kE = E < 64 ? E : 64;
+  static constexpr uint32_t kWidth = kE * 2, kBlock = ROWS * kWidth;
+  static constexpr uint32_t kLayout = kE == 16 ? 6 : (kE == 32 ? 4 : 2), kMask = kE == 16 ? 1 : (kE == 32 ? 3 : 7);
+  static constexpr int kBytes = ROWS * E * 2;
+  static __device__ __forceinline__ uint32_t at(int row, int piece) {
+    const uint32_t o = row * kWidth + (piece % (kE / 8)) * 16;
+    return (piece / (kE / 8)) * kBlock + (o ^ (((o >> 7) & kMask) << 4));
+  }
+  // Descriptor of the 16 contraction elements of step s: rows along M or N ...
+  static __device__ __forceinline__ uint64_t along_pieces(uint32_t base, int s) {
+    return smem_desc(base + (s / (kE / 16)) * kBlock + (s % (kE / 16)) * 32, 16, 8 * kWidth, kLayout);
+  }
+  // ... and rows along the contraction (needs the operand's transpose bit).
+  static __device__ __forceinline__ uint64_t along_rows(uint32_t base, int s) {
+    return smem_desc(base + s * 16 * kWidth, kBlock, 8 * kWidth, kLayout);
+  }
+};
+// Barriers and the like at the end of a kernel's shared memory (the operands
+// start it: nothing may come before them and shift their alignment).
+template <int BARS>
+struct Control {
+  uint64_t done[BARS];
+  uint32_t tmem;
+  int abort_flag;
+};
+// Instruction descriptor: bf16 x bf16 -> binary32, M = 128.
+__device__ __forceinline__ constexpr uint32_t mma_shape(int n, bool a_rows_are_k, bool b_rows_are_k) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_rows_are_k ? 1u << 15 : 0u) | (b_rows_are_k ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// What the waits of a kernel need.
+struct Waits {
+  int* status;
+  uint64_t timeout_ns;
+};
+constexpr int kSiteDown = 41, kSiteUp = 42, kSiteGrads = 43;
+
 // ---------------------------------------------------------------------------
 // u = W x for a tile of 128 tokens of one adapter
 // ---------------------------------------------------------------------------
-// As adapter_down, but the operands come through a ring of kStages stages of
-// 64 contraction columns, so that the bytes in flight do not depend on
-// registers: a lane's own pieces of x are copied to and read from places of its
-// own; the adapter's weights, which all row tiles of the CTA share, are read
-// once per CTA.
-//
-// Weights of a stage in shared memory: TRANS = false, row r's eight 16-byte
-// pieces, the halves swapped in odd rows; TRANS = true, the 64 rows of R
-// elements at a pitch of 2 RP + 16 bytes, in the order in which the MMA takes
-// them (see the load), so that each ldmatrix reads eight consecutive rows:
-// both without bank conflicts.
-template <int NT, bool TRANS>
+// For rows that TMA cannot take (not 16-byte aligned).  The tile's rows of x
+// (gathered: the tokens are sorted, not moved) and the adapter's weights are
+// staged element by element, 64 contraction columns a stage; one thread issues
+// the tcgen05 MMAs (M = 128 tokens, N = the padded rank) on each stage, and the
+// sums stay in tensor memory.  The contraction is split over the CTAs of a
+// cluster, whose sums meet in a fixed order.
+template <int RP, bool TRANS>
 struct DownTile {
-  static constexpr int kMT = NT <= 8 ? 2 : 1;
-  static constexpr int kWR = 8 / kMT, kWK = kMT;  // warps along rows and along the contraction
-  static constexpr int kStages = 4;
-  static constexpr int kXBytes = kTileRows * kChunk * 2;
-  static constexpr int kPitch = TRANS ? NT * 16 + 16 : kChunk * 2;  // of the weights' rows
-  static constexpr int kWBytes = (TRANS ? kChunk : NT * 8) * kPitch;
+  static constexpr int kStages = RP <= 32 ? 5 : (RP <= 64 ? 4 : 3);  // two CTAs to an SM
+  using X = Staged<kTileRows, kChunk>;
+  using W = Staged<TRANS ? kChunk : RP, TRANS ? RP : kChunk>;
+  static constexpr int kWPieces = (TRANS ? RP : kChunk) / 8;
+  static constexpr int kXBytes = X::kBytes, kWBytes = W::kBytes;
   static constexpr int kStageBytes = kXBytes + kWBytes;
-  static constexpr int kRing = kStages * kStageBytes, kSums = kWK * kTileRows * NT * 8 * 4;
-  static constexpr int kSmem = kRing > kSums ? kRing : kSums;
+  static constexpr int kPitch = RP + 4;  // of the sums' rows, in floats
+  static constexpr int kRing = kStages * kStageBytes;
+  static_assert(kTileRows * kPitch * 4 <= kRing, "the sums reuse the ring");
+  using Ctl = Control<kStages>;
+  static constexpr int kSmem = kRing + static_cast<int>(sizeof(Ctl));
+  static constexpr int kTmem = RP < 32 ? 32 : RP;
 };
 
 struct DownSorted {
   Down d;
   Order o;
+  Waits w;
 };
 
-template <int NT, bool TRANS, bool VEC>
+template <int RP, bool TRANS>
 __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__ DownSorted ps) {
-  using Cfg = DownTile<NT, TRANS>;
-  constexpr int MT = Cfg::kMT, WK = Cfg::kWK, kCols = NT * 8, kHalves = 2 / WK;
-  constexpr int kPitch = Cfg::kPitch;
-  extern __shared__ __align__(128) uint8_t ring[];
+  using Cfg = DownTile<RP, TRANS>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
   const Down& p = ps.d;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int wr = warp / WK, wk = warp % WK;
   const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
   const uint32_t ring_at = smem_u32(ring);
 
-  // the padding of the weights' stages: ranks R .. 8 NT are never copied
-  if (p.R < kCols) {
-    for (int st = 0; st < Cfg::kStages; ++st) {
-      uint8_t* w = ring + st * Cfg::kStageBytes + Cfg::kXBytes;
+  if (p.R < RP) {  // the padding of the weights' stages is never copied
+    for (int st = 0; st < S; ++st)
       for (int i = tid * 16; i < Cfg::kWBytes; i += 256 * 16)
-        *reinterpret_cast<uint4*>(w + i) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __syncthreads();
+        *reinterpret_cast<uint4*>(ring + st * Cfg::kStageBytes + Cfg::kXBytes + i) = make_uint4(0u, 0u, 0u, 0u);
   }
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&ctl.done[i], 1);
+    ctl.abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
   const Tile tile = ps.o.tiles[blockIdx.x];
@@ -747,133 +759,105 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
       p.u[static_cast<int64_t>(ps.o.perm[tile.start + i / p.R]) * p.R + i % p.R] = 0.f;
     return;
   }
+  if (warp == 0) {
+    tmem_alloc(&ctl.tmem, Cfg::kTmem);
+    tmem_relinquish();
+  }
   const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
-  const bf16* xr[MT][2];
+  const int piece = tid & 7;
+  const bf16* xr[4];  // this thread copies piece tid % 8 of rows tid / 8 + 32 i
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = wr * MT * 16 + m * 16 + h * 8 + g;  // rows past the tile repeat its last one and are not stored
-      xr[m][h] = p.x + ps.o.perm[tile.start + min(i, tile.count - 1)] * p.ld;
-    }
+  for (int i = 0; i < 4; ++i)  // rows past the tile repeat its last one and are not stored
+    xr[i] = p.x + ps.o.perm[tile.start + min((tid >> 3) + 32 * i, tile.count - 1)] * p.ld;
   const int64_t chunks = (p.C + kChunk - 1) / kChunk;
   const int64_t c_begin = chunks * rank / cs, c_end = chunks * (rank + 1) / cs;
   const int n = static_cast<int>(c_end - c_begin);
 
-  auto issue = [&](int c) {  // chunk c of this CTA's range into stage c % kStages
-    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
+  auto issue = [&](int c) {  // chunk c of this CTA's range into stage c % S
+    const uint32_t at = ring_at + (c % S) * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
     const int64_t k = (c_begin + c) * kChunk;
 #pragma unroll
-    for (int hh = 0; hh < kHalves; ++hh)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          stage8<VEC>(at + (((hh * MT + m) * 2 + h) * 256 + tid) * 16, xr[m][h],
-                      k + (kHalves == 2 ? hh : wk) * 32 + 8 * q, p.C);
-    const uint32_t wt = at + Cfg::kXBytes;
+    for (int i = 0; i < 4; ++i)
+      stage8(at + Cfg::X::at((tid >> 3) + 32 * i, piece), xr[i], k + piece * 8, p.C);
     if constexpr (!TRANS) {
-      for (int i = tid; i < p.R * 8; i += 256) {
-        const int r = i >> 3, piece = i & 7;
-        stage8<VEC>(wt + r * kPitch + ((piece ^ ((r & 1) * 4)) * 16), w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C);
-      }
+      for (int r = tid >> 3; r < p.R; r += 32)
+        stage8(wt + Cfg::W::at(r, piece), w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C);
     } else {
-      // row c = 32 half + 8 a + 4 s + 2 b + e goes to place 32 half + (2 s + b) 8 + 2 a + e
-      const int pieces = (p.R + 3) / 4;
-      for (int i = tid; i < kChunk * pieces; i += 256) {
-        const int cc = i / pieces, piece = i - cc * pieces;
-        const int place = (cc & 32) + ((cc >> 1) & 3) * 8 + ((cc >> 3) & 3) * 2 + (cc & 1);
-        stage4<VEC>(wt + place * kPitch + piece * 8, w + (k + cc) * p.R, piece * 4, k + cc < p.C ? p.R : 0);
+      for (int i = tid; i < kChunk * Cfg::kWPieces; i += 256) {
+        const int c64 = i / Cfg::kWPieces, pr = i % Cfg::kWPieces;
+        if (pr * 8 < p.R)
+          stage8(wt + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0);
       }
     }
   };
-
-  float acc[MT][NT][4];
+  bool ok = true;
+  auto wait_done = [&](int c) {  // the MMAs on chunk c have read their stage
+    ok = mbar_wait(&ctl.done[c % S], static_cast<uint32_t>(c / S) & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status,
+                   kSiteDown) && ok;
+  };
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-#pragma unroll
-  for (int c = 0; c < Cfg::kStages - 1; ++c) {
+  for (int c = 0; c < S - 1; ++c)
     if (c < n) issue(c);
-    copy_commit();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  int c = 0;
+  for (; c < n; ++c) {
+    fence_proxy_async_smem();
+    if (__syncthreads_or(!ok)) break;  // stage c is there for all (or the CTA gives up together)
+    if (tid == 0) {
+      const uint32_t at = ring_at + (c % S) * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
+#pragma unroll
+      for (int s = 0; s < kChunk / 16; ++s)
+        mma_f16(tmem, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
+                mma_shape(RP, false, TRANS), (c > 0 || s > 0) ? 1u : 0u);
+      tc_commit(&ctl.done[c % S]);
+    }
+    if (c + S - 1 < n) {
+      if (c > 0) wait_done(c - 1);
+      issue(c + S - 1);
+    }
   }
-  for (int c = 0; c < n; ++c) {
-    copy_wait<Cfg::kStages - 2>();
-    __syncthreads();  // stage c is there for all; stage c - 1 has been read by all
-    if (c + Cfg::kStages - 1 < n) issue(c + Cfg::kStages - 1);
-    copy_commit();
-    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
-    const uint32_t wt = at + Cfg::kXBytes;
+  if (c > 0) wait_done(c - 1);  // every MMA before it too
+  __syncthreads();
+  tc_fence_after();
+  float* sums = reinterpret_cast<float*>(ring);  // [kTileRows][kPitch]
+  {
+    constexpr int kHalf = RP < 32 ? RP : RP / 2;  // columns of a warp: warps 4..7 take the second half
+    if (RP >= 32 || warp < 4) {
+      float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
+      const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-    for (int hh = 0; hh < kHalves; ++hh) {
-      const int half = kHalves == 2 ? hh : wk;
-      uint4 xa[MT][2];
+      for (int j = 0; j < kHalf; j += 16) {
+        uint32_t v[16];
+        tmem_ld16(src + j, v);
+        tmem_wait_ld();
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) xa[m][h] = ld_shared16(at + (((hh * MT + m) * 2 + h) * 256 + tid) * 16);
-      if constexpr (!TRANS) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int r = j * 8 + g;
-          const uint4 b = ld_shared16(wt + r * kPitch + (((half * 4 + q) ^ ((r & 1) * 4)) * 16));
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, b.x, b.y);
-            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, b.z, b.w);
-          }
-        }
-      } else {
-        // one ldmatrix: both halves of steps 0 and 1 of n-tile j (matrix i = 2 s + b)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint32_t b[4];
-          ldmatrix_x4_trans(wt + (half * 32 + lane) * kPitch + j * 16, b);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma_bf16(acc[m][j], xa[m][0].x, xa[m][1].x, xa[m][0].y, xa[m][1].y, b[0], b[1]);
-            mma_bf16(acc[m][j], xa[m][0].z, xa[m][1].z, xa[m][0].w, xa[m][1].w, b[2], b[3]);
-          }
-        }
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<uint4*>(dst + j + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
       }
     }
   }
-  copy_wait<0>();
+  tc_fence_before();
   __syncthreads();
-  float* sums = reinterpret_cast<float*>(ring);  // [WK][kTileRows][kCols]
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        *reinterpret_cast<float2*>(sums + (wk * kTileRows + wr * MT * 16 + m * 16 + h * 8 + g) * kCols + j * 8 + 2 * q) =
-            make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-  __syncthreads();
-  if constexpr (WK == 2) {
-    for (int i = tid; i < kTileRows * kCols; i += 256) sums[i] += sums[kTileRows * kCols + i];
-  }
+  if (warp == 0) tmem_dealloc(tmem, Cfg::kTmem);
   if (cs > 1) {
     __syncwarp();
     cluster_sync();
-  } else {
-    __syncthreads();
   }
   const int total = tile.count * p.R, share = (total + cs - 1) / cs;
   const int e_end = min(total, (rank + 1) * share);
   for (int e = rank * share + tid; e < e_end; e += 256) {
-    const int r = e / p.R, c = e - r * p.R;
+    const int r = e / p.R, col = e - r * p.R;
     float v = 0.f;
     if (cs > 1) {
-      const uint32_t addr = smem_u32(sums + r * kCols + c);
+      const uint32_t addr = smem_u32(sums + r * Cfg::kPitch + col);
       for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
     } else {
-      v = sums[r * kCols + c];
+      v = sums[r * Cfg::kPitch + col];
     }
-    p.u[static_cast<int64_t>(ps.o.perm[tile.start + r]) * p.R + c] = v;
+    p.u[static_cast<int64_t>(ps.o.perm[tile.start + r]) * p.R + col] = v;
   }
   __syncwarp();
   if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
@@ -882,230 +866,254 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
 // ---------------------------------------------------------------------------
 // out = base + s W u for a tile of 128 tokens of one adapter
 // ---------------------------------------------------------------------------
-// As adapter_up, with base and the weights through a ring of stages of 64
-// columns.  Weights of a stage: TRANS = false, the 64 rows of R elements in the
-// order in which the MMA takes them, at a pitch of 2 RP bytes (+ 32 from RP =
-// 32 on); TRANS = true, R rows of 64 columns at a pitch of 192 bytes.  Either
-// way the fragment loads meet no bank conflicts.
-template <int KT, typename Y, bool TRANS>
+// The tile's u is split once into TERMS bf16 terms in shared memory (three for
+// binary32 outputs, which keep its 24 bits; two, 16 bits, for bf16 ones).
+// Chunks of 64 columns then stream through: one thread issues the tcgen05 MMAs
+// of chunk c + 1 into one of two accumulators in tensor memory, and each warp
+// adds chunk c's 32 rows x 32 columns to base in shared memory and writes them
+// out along the rows.
+template <int RP, typename Y, bool TRANS>
 struct UpTile {
-  static constexpr int kMT = KT <= 4 && !(KT == 4 && sizeof(Y) == 4) ? 2 : 1;
-  static constexpr int kWR = 8 / kMT, kWN = kMT;
-  static constexpr int kStages = sizeof(Y) == 4 ? 3 : 4;
+  static constexpr int TERMS = sizeof(Y) == 4 ? 3 : 2;
+  static constexpr bool kTwo = sizeof(Y) == 2 ? RP <= 64 : RP <= 32;  // two CTAs fit an SM
+  static constexpr int kYStages = sizeof(Y) == 2 ? (RP <= 32 ? 4 : 3) : (kTwo || RP == 128 ? 2 : 4);
+  static constexpr int kWStages = kYStages + 1;
+  using U = Staged<kTileRows, RP>;  // one term
+  using W = Staged<TRANS ? RP : kChunk, TRANS ? kChunk : RP>;
+  static constexpr int kWPieces = (TRANS ? kChunk : RP) / 8;
+  static constexpr int kUBytes = TERMS * U::kBytes, kWBytes = W::kBytes;
   static constexpr int kYBytes = kTileRows * kChunk * static_cast<int>(sizeof(Y));
-  static constexpr int kPitch = TRANS ? 192 : KT * 32 + (KT >= 2 ? 32 : 0);  // of the weights' rows
-  static constexpr int kWBytes = (TRANS ? KT * 16 : kChunk) * kPitch;
-  static constexpr int kStageBytes = kYBytes + kWBytes;
-  static constexpr int kSmem = kStages * kStageBytes;
+  using Ctl = Control<2>;
+  static constexpr int kCtlAt = kUBytes + kWStages * kWBytes + kYStages * kYBytes;
+  static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
 };
 
 struct UpSorted {
   Up d;
   Order o;
+  Waits w;
   int chunks_per_cta;
 };
 
-template <int KT, typename Y, bool TRANS, bool VEC>
+// 16 bytes of a row of Y from column c as one staged piece, and back.
+template <typename Y>
+__device__ __forceinline__ void stage_piece(uint32_t dst, const Y* row, int64_t c, int64_t limit) {
+  if constexpr (sizeof(Y) == 2) {
+    stage8(dst, row, c, limit);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = c + i < limit ? __float_as_uint(row[c + i]) : 0u;
+    st_shared16(dst, w);
+  }
+}
+template <typename Y>
+__device__ __forceinline__ void write_piece(Y* row, int64_t c, int64_t limit, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 16 / static_cast<int>(sizeof(Y)); ++i)
+    if (c + i < limit) {
+      if constexpr (sizeof(Y) == 2)
+        reinterpret_cast<uint16_t*>(row)[c + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+      else
+        row[c + i] = __uint_as_float(w[i]);
+    }
+}
+
+template <int RP, typename Y, bool TRANS>
 __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ UpSorted ps) {
-  using Cfg = UpTile<KT, Y, TRANS>;
-  constexpr int MT = Cfg::kMT, WN = Cfg::kWN, kGroups = 2 / WN, RP = KT * 16;
-  constexpr int TERMS = sizeof(Y) == 4 ? 3 : 2;
-  constexpr int kPieces = sizeof(Y) / 2;  // 16-byte pieces of a lane's 8 columns
-  constexpr int kPitch = Cfg::kPitch;
-  extern __shared__ __align__(128) uint8_t ring[];
+  using Cfg = UpTile<RP, Y, TRANS>;
+  constexpr int TERMS = Cfg::TERMS, YS = Cfg::kYStages, WS = Cfg::kWStages;
+  constexpr int kPer = 16 / static_cast<int>(sizeof(Y));  // elements of a piece
+  constexpr int kRowPieces = 32 / kPer;                   // of a warp's 32 columns
+  constexpr int kCopies = kRowPieces;                     // pieces a lane copies: 32 rows x kRowPieces / 32 lanes
+  extern __shared__ __align__(1024) uint8_t smem[];
+  typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(smem + Cfg::kCtlAt);
   const Up& p = ps.d;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int wr = warp / WN, wn = warp % WN;
-  const uint32_t ring_at = smem_u32(ring);
+  const uint32_t u_at = smem_u32(smem), w_at = u_at + Cfg::kUBytes;
+  // the warp's corner of a base stage: 32 rows x 32 columns
+  const int row0 = (warp & 3) * 32, colw = (warp >> 2) * 32;
+  constexpr int kCorner = 32 * 32 * static_cast<int>(sizeof(Y));
+  const uint32_t y_at = w_at + WS * Cfg::kWBytes + warp * kCorner;
+  // pieces are swizzled so that neither a row's pieces (copies) nor a column of
+  // pieces (one row to a lane) meets a bank twice
+  auto corner = [&](int row, int piece) -> uint32_t {
+    if constexpr (sizeof(Y) == 2) return row * 64 + ((piece ^ ((row >> 1) & 3)) * 16);
+    return row * 128 + ((piece ^ (row & 7)) * 16);
+  };
 
   const Tile tile = ps.o.tiles[blockIdx.x];  // of two launches before, done before the last one released this one
   if (tile.count == 0) return;
   const int64_t chunks = (p.C + kChunk - 1) / kChunk;
   const int64_t c_begin = static_cast<int64_t>(blockIdx.y) * ps.chunks_per_cta;
   const int n = static_cast<int>(min(static_cast<int64_t>(ps.chunks_per_cta), chunks - c_begin));
-  const bool plain = tile.adapter < 0;  // no product: out = base
-  const bf16* w = p.w + static_cast<int64_t>(plain ? 0 : tile.adapter) * p.R * p.C;
+  const Y* base = static_cast<const Y*>(p.base);
+  Y* out = static_cast<Y*>(p.out);
 
-  int64_t row[MT][2];
-  bool live[MT][2];
+  if (tile.adapter < 0) {  // no product: out = base
+    const int64_t c0 = c_begin * kChunk, c1 = min(p.C, c0 + static_cast<int64_t>(n) * kChunk);
+    constexpr int kRows = sizeof(Y) == 2 ? 4 : 2;  // loaded before any is stored
+    for (int64_t c = c0 + lane * 8; c < c1; c += 256)
+      for (int r = warp * kRows; r < tile.count; r += 8 * kRows) {
+        float v[kRows][8];
+        int64_t at[kRows];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < kRows; ++i) {
+          at[i] = r + i < tile.count ? ps.o.perm[tile.start + r + i] : -1;
+          if (base && at[i] >= 0)
+            load_out<Y, false>(base + at[i] * p.ld_base, c, p.C, v[i]);
+          else
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = wr * MT * 16 + m * 16 + h * 8 + g;
-      live[m][h] = i < tile.count;
-      row[m][h] = ps.o.perm[tile.start + min(i, tile.count - 1)];
-    }
-  if (p.R < RP) {  // the padding of the weights' stages
-    for (int st = 0; st < Cfg::kStages; ++st) {
-      uint8_t* s = ring + st * Cfg::kStageBytes + Cfg::kYBytes;
-      for (int i = tid * 16; i < Cfg::kWBytes; i += 256 * 16)
-        *reinterpret_cast<uint4*>(s + i) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __syncthreads();
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (at[i] >= 0) store_out<Y, false>(out + at[i] * p.ld_out, c, p.C, v[i]);
+      }
+    return;
   }
-  auto issue = [&](int c) {
-    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
+  if (warp == 0) {
+    tmem_alloc(&ctl.tmem, 2 * kChunk);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(&ctl.done[0], 1);
+    mbar_init(&ctl.done[1], 1);
+    ctl.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (p.R < RP) {  // the padding of the weights' stages is never copied
+    for (int i = tid * 16; i < WS * Cfg::kWBytes; i += 256 * 16)
+      *reinterpret_cast<uint4*>(smem + Cfg::kUBytes + i) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
+  int copy_row[kCopies];  // the tokens whose pieces this lane copies
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int r = row0 + i * (32 / kRowPieces) + lane / kRowPieces;
+    copy_row[i] = r < tile.count ? ps.o.perm[tile.start + r] : -1;
+  }
+  auto issue_w = [&](int c) {
+    const uint32_t at = w_at + (c % WS) * Cfg::kWBytes;
     const int64_t k = (c_begin + c) * kChunk;
-    if (p.base) {
-#pragma unroll
-      for (int cg = 0; cg < kGroups; ++cg)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t col = k + (kGroups == 2 ? cg : wn) * 32 + 8 * q;
-            const Y* src = static_cast<const Y*>(p.base) + row[m][h] * p.ld_base;
-            const uint32_t dst = at + ((((cg * MT + m) * 2 + h) * kPieces) * 256 + tid) * 16;
-            if constexpr (VEC) {
-              const bool in = col < p.C;
-#pragma unroll
-              for (int e = 0; e < kPieces; ++e)
-                copy_async<16>(dst + e * 256 * 16, in ? src + col + e * (16 / sizeof(Y)) : src, in ? 16 : 0);
-            } else {
-              float v[8];
-              load_out<Y, false>(src, col, p.C, v);
-              uint32_t bits[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) bits[e] = __float_as_uint(v[e]);
-              if constexpr (sizeof(Y) == 2) {
-                const uint32_t b[4] = {pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
-                st_shared16(dst, b);
-              } else {
-                const uint32_t b0[4] = {bits[0], bits[1], bits[2], bits[3]}, b1[4] = {bits[4], bits[5], bits[6], bits[7]};
-                st_shared16(dst, b0);
-                st_shared16(dst + 256 * 16, b1);
-              }
-            }
-          }
-    }
-    if (plain) return;
-    const uint32_t wt = at + Cfg::kYBytes;
     if constexpr (!TRANS) {
-      // column c = 32 group + 8 a + 2 j + e goes to place 32 group + 8 j + 2 a + e
-      const int pieces = (p.R + 3) / 4;
-      for (int i = tid; i < kChunk * pieces; i += 256) {
-        const int cc = i / pieces, piece = i - cc * pieces;
-        const int place = (cc & 32) + ((cc >> 1) & 3) * 8 + ((cc >> 3) & 3) * 2 + (cc & 1);
-        stage4<VEC>(wt + place * kPitch + piece * 8, w + (k + cc) * p.R, piece * 4, k + cc < p.C ? p.R : 0);
+      for (int i = tid; i < kChunk * Cfg::kWPieces; i += 256) {
+        const int c64 = i / Cfg::kWPieces, pr = i % Cfg::kWPieces;
+        if (pr * 8 < p.R)
+          stage8(at + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0);
       }
     } else {
-      for (int i = tid; i < p.R * 8; i += 256) {
-        const int r = i >> 3, piece = i & 7;
-        stage8<VEC>(wt + r * kPitch + piece * 16, w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C);
-      }
+      for (int r = tid >> 3; r < p.R; r += 32)
+        stage8(at + Cfg::W::at(r, tid & 7), w + static_cast<int64_t>(r) * p.C, k + (tid & 7) * 8, p.C);
     }
   };
+  auto issue_y = [&](int c) {
+    if (!base) return;
+    const uint32_t at = y_at + (c % YS) * Cfg::kYBytes;
+    const int64_t k = (c_begin + c) * kChunk + colw;
 #pragma unroll
-  for (int c = 0; c < Cfg::kStages - 1; ++c) {
-    if (c < n) issue(c);
-    copy_commit();
+    for (int i = 0; i < kCopies; ++i) {
+      const int r = i * (32 / kRowPieces) + lane / kRowPieces, piece = lane % kRowPieces;
+      if (copy_row[i] >= 0)
+        stage_piece<Y>(at + corner(r, piece), base + copy_row[i] * p.ld_base, k + piece * kPer, p.C);
+    }
+  };
+  auto issue_mma = [&](int c) {  // one thread
+    const uint32_t at = w_at + (c % WS) * Cfg::kWBytes;
+    const uint32_t d = ctl.tmem + (c & 1) * kChunk;
+#pragma unroll
+    for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+      for (int s = 0; s < RP / 16; ++s)
+        mma_f16(d, Cfg::U::along_pieces(u_at + k * Cfg::U::kBytes, s),
+                TRANS ? Cfg::W::along_rows(at, s) : Cfg::W::along_pieces(at, s), mma_shape(kChunk, false, TRANS),
+                (k < TERMS - 1 || s > 0) ? 1u : 0u);
+    tc_commit(&ctl.done[c & 1]);
+  };
+  // the weights run a chunk ahead of base
+  issue_w(0);
+#pragma unroll
+  for (int c = 0; c < YS - 1; ++c) {
+    if (c + 1 < n) issue_w(c + 1);
+    if (c < n) issue_y(c);
   }
-  const float sc = plain ? 0.f : (p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f);
+  const float sc = p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f;
   grid_dependency_wait();  // u is the launch before this one's
-  uint32_t ua[MT][KT][2][2][TERMS];
+  for (int i = tid; i < kTileRows * (RP / 8); i += 256) {
+    const int r = i / (RP / 8), pr = i % (RP / 8);
+    float v[8];
+    const float* src = p.u + (r < tile.count ? static_cast<int64_t>(ps.o.perm[tile.start + r]) : 0) * p.R;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int e = 0; e < 8; ++e) v[e] = r < tile.count && pr * 8 + e < p.R ? src[pr * 8 + e] : 0.f;
+    uint32_t t[4][TERMS];
 #pragma unroll
-    for (int ks = 0; ks < KT; ++ks)
+    for (int e = 0; e < 4; ++e) split_pair<TERMS>(v[2 * e], v[2 * e + 1], t[e]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = ks * 16 + 4 * q + e;
-          v[e] = !plain && r < p.R ? p.u[row[m][h] * p.R + r] : 0.f;
-        }
-        split_pair<TERMS>(v[0], v[1], ua[m][ks][h][0]);
-        split_pair<TERMS>(v[2], v[3], ua[m][ks][h][1]);
-      }
-  for (int c = 0; c < n; ++c) {
-    copy_wait<Cfg::kStages - 2>();
-    __syncthreads();
-    if (c + Cfg::kStages - 1 < n) issue(c + Cfg::kStages - 1);
-    copy_commit();
-    const uint32_t at = ring_at + (c % Cfg::kStages) * Cfg::kStageBytes;
-    const uint32_t wt = at + Cfg::kYBytes;
-#pragma unroll
-    for (int cg = 0; cg < kGroups; ++cg) {
-      const int group = kGroups == 2 ? cg : wn;
-      float acc[MT][4][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-      if (!plain) {
-#pragma unroll
-        for (int ks = 0; ks < KT; ++ks) {
-          uint32_t wb[4][2];
-          if constexpr (!TRANS) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint2 v = ld_shared8(wt + (group * 32 + j * 8 + g) * kPitch + ks * 32 + q * 8);
-              wb[j][0] = v.x;
-              wb[j][1] = v.y;
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int r = ks * 16 + (g / 2) * 4 + 2 * h + (g % 2);
-              const uint4 v = ld_shared16(wt + r * kPitch + (group * 4 + q) * 16);
-              wb[0][h] = transpose8x8(v.x);
-              wb[1][h] = transpose8x8(v.y);
-              wb[2][h] = transpose8x8(v.z);
-              wb[3][h] = transpose8x8(v.w);
-            }
-          }
-#pragma unroll
-          for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma_bf16(acc[m][j], ua[m][ks][0][0][k], ua[m][ks][1][0][k], ua[m][ks][0][1][k], ua[m][ks][1][1][k],
-                         wb[j][0], wb[j][1]);
-        }
-      }
-      const int64_t col = (c_begin + c) * kChunk + group * 32 + 8 * q;
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float y[8];
-          const uint32_t src = at + ((((cg * MT + m) * 2 + h) * kPieces) * 256 + tid) * 16;
-          if (p.base) {
-            const uint4 b = ld_shared16(src);
-            if constexpr (sizeof(Y) == 2) {
-              const uint32_t b4[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[2 * e] = __uint_as_float(b4[e] << 16);
-                y[2 * e + 1] = __uint_as_float(b4[e] & 0xFFFF0000u);
-              }
-            } else {
-              const uint4 b2 = ld_shared16(src + 256 * 16);
-              const uint32_t b8[8] = {b.x, b.y, b.z, b.w, b2.x, b2.y, b2.z, b2.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(b8[e]);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = 0.f;
-          }
-          if (!plain) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) y[2 * j + e] = fmaf(sc, acc[m][j][2 * h + e], y[2 * j + e]);
-          }
-          if (live[m][h]) store_out<Y, VEC>(static_cast<Y*>(p.out) + row[m][h] * p.ld_out, col, p.C, y);
-        }
+    for (int k = 0; k < TERMS; ++k) {
+      const uint32_t q[4] = {t[0][k], t[1][k], t[2][k], t[3][k]};
+      st_shared16(u_at + k * Cfg::U::kBytes + Cfg::U::at(r, pr), q);
     }
   }
-  copy_wait<0>();
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0) issue_mma(0);
+  bool ok = true;
+  int c = 0;
+  for (; c < n; ++c) {
+    fence_proxy_async_smem();
+    tc_fence_before();  // the reads of the accumulator that chunk c + 1 overwrites
+    if (__syncthreads_or(!ok)) break;
+    tc_fence_after();
+    if (tid == 0 && c + 1 < n) issue_mma(c + 1);
+    // the weights of chunk c - 1 have been read (its accumulator was waited for)
+    if (c + YS < n) issue_w(c + YS);
+    if (c + YS - 1 < n) issue_y(c + YS - 1);
+    ok = mbar_wait(&ctl.done[c & 1], static_cast<uint32_t>(c >> 1) & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status,
+                   kSiteUp);
+    tc_fence_after();
+    uint32_t d[32];
+    tmem_ld32(ctl.tmem + ((warp & 3) * 32u << 16) + (c & 1) * kChunk + colw, d);
+    tmem_wait_ld();
+    // lane: row row0 + lane, the warp's 32 columns
+    const uint32_t at = y_at + (c % YS) * Cfg::kYBytes;
+#pragma unroll
+    for (int j = 0; j < kRowPieces; ++j) {
+      const uint32_t a = at + corner(lane, j);
+      uint4 b = make_uint4(0u, 0u, 0u, 0u);
+      if (base) b = ld_shared16(a);
+      const uint32_t v[4] = {b.x, b.y, b.z, b.w};
+      uint32_t r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(Y) == 2)
+          r[e] = pack2(fmaf(sc, __uint_as_float(d[j * 8 + 2 * e]), __uint_as_float(v[e] << 16)),
+                       fmaf(sc, __uint_as_float(d[j * 8 + 2 * e + 1]), __uint_as_float(v[e] & 0xFFFF0000u)));
+        else
+          r[e] = __float_as_uint(fmaf(sc, __uint_as_float(d[j * 4 + e]), __uint_as_float(v[e])));
+      }
+      st_shared16(a, r);
+    }
+    __syncwarp();
+    const int64_t k = (c_begin + c) * kChunk + colw;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int r = i * (32 / kRowPieces) + lane / kRowPieces, piece = lane % kRowPieces;
+      const uint4 v = ld_shared16(at + corner(r, piece));
+      if (copy_row[i] >= 0) write_piece<Y>(out + copy_row[i] * p.ld_out, k + piece * kPer, p.C, v);
+    }
+    __syncwarp();  // before the next copies into this corner
+  }
+  if (c < n) {  // gave up: the MMAs in flight, bounded again, before their operands' memory goes
+    int never = 0;
+    mbar_wait(&ctl.done[c & 1], static_cast<uint32_t>(c >> 1) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(ctl.tmem, 2 * kChunk);
 }
 
 // ---------------------------------------------------------------------------
@@ -1115,8 +1123,8 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
 // written as [L][R][C] (dA) or [L][C][R] (dB); x is bf16 or an MXFP8
 // checkpoint.
 struct GradJob {
-  const float* coef;  // [T][R]
-  const void* x;      // [T][ld] bf16, or 8-bit codes
+  const bf16* coef;  // [T][TERMS][RP], in the sorted order
+  const void* x;     // [T][ld] bf16, or 8-bit codes
   const uint8_t* x_scales;  // null: bf16; else UE8M0 [T][C / 32]
   int64_t ld;
   void* out;
@@ -1128,16 +1136,51 @@ struct Grads {
   GradJob job[2];
   const float* scaling;
   Order o;
+  Waits w;
   int R, L;
   int e5m2;    // the codes' type
-  int coef16;  // the coefficients' rows are 16-byte aligned
+  int scale4;  // the scale bytes' rows are 4-byte aligned
 };
-constexpr int kGradCols = 128;  // columns of a CTA: 4 warps of 32
-constexpr int kGradRows = 64;   // tokens of a stage
+
+// The coefficients of both jobs in the sorted order, each split into TERMS bf16
+// terms and padded to RP ranks: once here, where every column tile of
+// adapter_grads would otherwise do it (half of that kernel's instructions).
+struct Terms {
+  const float* from[2];  // [T][R]
+  bf16* to[2];           // [T][TERMS][RP]
+  const int* perm;
+  int64_t T;
+  int R;
+};
+template <int RP, int TERMS>
+__global__ void __launch_bounds__(256) adapter_terms(const Terms p) {
+  constexpr int kPieces = RP / 8;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t at = i / kPieces;
+  const int r0 = static_cast<int>(i % kPieces) * 8;
+  if (at >= p.T) return;
+  const int64_t t = p.perm[at];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float* src = p.from[k] + t * p.R;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = r0 + e < p.R ? src[r0 + e] : 0.f;
+    uint32_t w[4][TERMS];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_pair<TERMS>(v[2 * e], v[2 * e + 1], w[e]);
+#pragma unroll
+    for (int m = 0; m < TERMS; ++m)
+      *reinterpret_cast<uint4*>(p.to[k] + (at * TERMS + m) * RP + r0) = make_uint4(w[0][m], w[1][m], w[2][m], w[3][m]);
+  }
+}
+constexpr int kGradCols = 128;  // columns of a CTA
+constexpr int kGradRows = 64;   // tokens of a block
 
 // Eight 8-bit codes times 2^e as bf16 pairs (exact).
-__device__ __forceinline__ void codes_to_bf16(uint2 c, uint32_t scale_byte, bool e5m2, uint32_t (&w)[4]) {
-  const float s = __uint_as_float(scale_byte == 0u ? 0x00400000u : (scale_byte == 255u ? 0x7FFFFFFFu : scale_byte << 23));
+__device__ __forceinline__ void codes_to_bf16(uint2 c, float s, bool e5m2, uint32_t (&w)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint16_t two = static_cast<uint16_t>((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
@@ -1154,241 +1197,32 @@ __device__ __forceinline__ void codes_to_bf16(uint2 c, uint32_t scale_byte, bool
   }
 }
 
-template <int MR, int TERMS>
+template <int RP, int TERMS>
 struct GradTile {
-  static constexpr int kStages = MR <= 2 ? 4 : (MR <= 4 ? 3 : 2);
-  static constexpr int kXBytes = kGradRows * kGradCols * 2;
-  static constexpr int kCoefBytes = kGradRows * MR * 16 * 4;
-  static constexpr int kStageBytes = kXBytes + kCoefBytes + 256;  // + scale bytes of a checkpoint's rows
-  static constexpr int kFragBytes = (kGradRows / 16) * MR * TERMS * 512;
-  // ring, coefficient fragments, and the decoded tile of a checkpoint
-  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kFragBytes + kXBytes;
-  static_assert(static_cast<size_t>(MR) * 16 * kGradCols * 4 <= kSmem, "the sums reuse the ring");
+  using X = Staged<kGradRows, kGradCols>;
+  using Coef = Staged<kGradRows, RP>;  // one term
+  static constexpr int kXBytes = X::kBytes;                               // a block of bf16
+  static constexpr int kCodeBytes = kGradRows * kGradCols + 256 * 2 * 4;  // of codes, and each copy's scale word
+  static constexpr int kStages = RP <= 16 ? 4 : (RP <= 32 || (RP <= 64 && TERMS == 2) ? 3 : 2);  // two CTAs to an SM (one from RP = 128 on)
+  static constexpr int kTermBytes = Coef::kBytes, kCoefBytes = TERMS * kTermBytes;
+  static constexpr int kIdxSlots = 8;
+  static constexpr int kPitch = RP + 4;  // of the sums' rows (one to a column), in floats
+  // bf16: the ring; codes: two decoded blocks and the ring.  Then the
+  // coefficients' ring and the blocks' token numbers.
+  static constexpr int kRingBf16 = kStages * kXBytes, kRingCodes = 2 * kXBytes + kStages * kCodeBytes;
+  static constexpr int kRing = kRingBf16 > kRingCodes ? kRingBf16 : kRingCodes;
+  static constexpr int kIdxAt = kRing + kStages * kCoefBytes;
+  using Ctl = Control<2>;
+  static constexpr int kCtlAt = kIdxAt + kIdxSlots * kGradRows * 4;
+  static_assert(kGradCols * kPitch * 4 <= kCtlAt, "the sums reuse the space before");
+  static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
+  static constexpr int kTmem = RP < 32 ? 32 : RP;
 };
 
-// One CTA: an adapter's tokens, taken 64 at a time from the sorted order, by
-// 128 columns; the blocks are dealt out over the CTAs of the cluster (y).  The
-// 8 warps are 4 across the columns x 2 across a block's tokens.  Tokens are the
-// contraction axis of both operands, so both reach the MMA transposed: x by
-// ldmatrix.trans from its staged tile, the coefficients as fragments that the
-// CTA splits into TERMS bf16 terms once for all its columns.  A block's sum is
-// added to the running one in binary32 outside the MMA (whose accumulation
-// truncates; adding every product there lost 1e-6 of the result over 8192
-// tokens).  Partial sums meet in a fixed order.
-template <int MR, int TERMS, typename G, bool VEC>
-__global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Grads p) {
-  using Cfg = GradTile<MR, TERMS>;
-  constexpr int kSteps = kGradRows / 16, RP = MR * 16;
-  constexpr bool kFlush = MR <= 4;
-  extern __shared__ __align__(128) uint8_t ring[];
-  uint32_t* frag = reinterpret_cast<uint32_t*>(ring + Cfg::kStages * Cfg::kStageBytes);
-  uint8_t* decoded = ring + Cfg::kStages * Cfg::kStageBytes + Cfg::kFragBytes;
-  float* sums = reinterpret_cast<float*>(ring);  // [RP][kGradCols], at the end
-  const uint32_t ring_at = smem_u32(ring);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int wc = warp & 3, wt = warp >> 2;
-  const bool second = blockIdx.x >= static_cast<unsigned>(p.job[0].tiles);
-  const GradJob& j = p.job[second ? 1 : 0];
-  const bool kept = j.x_scales != nullptr;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? p.job[0].tiles : 0)) * kGradCols;
-  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
-  const int a = static_cast<int>(blockIdx.z);
-
-  float acc[MR][4][4];
-#pragma unroll
-  for (int m = 0; m < MR; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
-
-  grid_dependency_wait();
-  // this CTA's blocks: number i of the adapter's blocks over all segments goes to rank i % cs
-  struct Walk {
-    int seg, pos, end, turn;
-  };
-  auto enter = [&](Walk& k) {  // the segment's range of this adapter
-    const int* s = p.o.starts + static_cast<int64_t>(k.seg) * (p.L + 2) + a;
-    k.pos = s[0];
-    k.end = s[1];
-  };
-  auto settle = [&](Walk& k) -> bool {  // to the next block of this rank; false: none is left
-    while (true) {
-      while (k.pos >= k.end) {
-        if (++k.seg >= p.o.segments) return false;
-        enter(k);
-      }
-      if (k.turn % cs == rank) return true;
-      ++k.turn;
-      k.pos += kGradRows;
-    }
-  };
-  Walk ahead{0, 0, 0, 0};
-  bool more = p.o.segments > 0;
-  if (more) {
-    enter(ahead);
-    more = settle(ahead);
-  }
-
-  // copies rows perm[pos .. end) (at most 64) into a stage; rows past them are zeros
-  auto issue = [&](int st, int pos, int end) {
-    const uint32_t at = ring_at + st * Cfg::kStageBytes;
-    const int rows = min(kGradRows, end - pos);
-    if (!kept) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = (tid >> 4) + 16 * i, piece = tid & 15;
-        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
-        stage8<VEC>(at + r * 256 + ((piece ^ (r & 7)) * 16), static_cast<const bf16*>(j.x) + t * j.ld, c0 + piece * 8,
-                    r < rows ? j.C : 0);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = (tid >> 3) + 32 * i, piece = tid & 7;
-        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
-        const int64_t c = c0 + piece * 16;
-        const bool in = r < rows && c < j.C;
-        const uint8_t* row = static_cast<const uint8_t*>(j.x) + t * j.ld;
-        copy_async<16>(at + r * 128 + piece * 16, in ? row + c : row, in ? 16 : 0);
-      }
-      if (tid < kGradRows) {  // the row's scale bytes of the tile's (up to) four blocks
-        const int64_t t = tid < rows ? p.o.perm[pos + tid] : 0;
-        uint32_t four = 0u;
-        const int64_t nb = j.C / 32;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (tid < rows && c0 / 32 + b < nb) four |= static_cast<uint32_t>(__ldg(j.x_scales + t * nb + c0 / 32 + b)) << (8 * b);
-        *reinterpret_cast<uint32_t*>(ring + st * Cfg::kStageBytes + Cfg::kXBytes + Cfg::kCoefBytes + tid * 4) = four;
-      }
-    }
-    // coefficients, 4 ranks at a time where rows are aligned, else one by one; ranks past R are zeros
-    const uint32_t ct = at + Cfg::kXBytes;
-    if (p.coef16) {
-      for (int i = tid; i < kGradRows * (RP / 4); i += 256) {
-        const int r = i / (RP / 4), piece = i % (RP / 4);
-        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
-        const bool in = r < rows && piece * 4 < p.R;
-        const float* row = j.coef + t * p.R;
-        copy_async<16>(ct + (r * RP + piece * 4) * 4, in ? row + piece * 4 : row, in ? 16 : 0);
-      }
-    } else {
-      for (int i = tid; i < kGradRows * RP; i += 256) {
-        const int r = i / RP, c = i % RP;
-        const int64_t t = r < rows ? p.o.perm[pos + r] : 0;
-        const bool in = r < rows && c < p.R;
-        const float* row = j.coef + t * p.R;
-        copy_async<4>(ct + i * 4, in ? row + c : row, in ? 4 : 0);
-      }
-    }
-  };
-
-  int issued = 0, done = 0;  // blocks
-  auto next = [&]() {
-    if (more) {
-      issue(issued % Cfg::kStages, ahead.pos, ahead.end);
-      ++issued;
-      ++ahead.turn;
-      ahead.pos += kGradRows;
-      more = settle(ahead);
-    }
-    copy_commit();
-  };
-#pragma unroll 1
-  for (int c = 0; c < Cfg::kStages - 1; ++c) next();
-  while (done < issued) {
-    copy_wait<Cfg::kStages - 2>();
-    __syncthreads();  // block `done` is there for all; the one before has been read by all
-    const int st = done % Cfg::kStages;
-    const uint8_t* stage = ring + st * Cfg::kStageBytes;
-    const float* coef = reinterpret_cast<const float*>(stage + Cfg::kXBytes);
-    // fragments: tokens 16 step + 8 (e / 2) + 2 q .., rank 16 m + 8 (e % 2) + g
-    for (int i = tid; i < kSteps * MR * 32; i += 256) {
-      const int fl = i & 31, fm = (i >> 5) % MR, fs = (i >> 5) / MR;
-      const int fg = fl >> 2, fq = fl & 3;
-      uint32_t w[4][TERMS];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float* v = coef + (fs * 16 + (e >> 1) * 8 + 2 * fq) * RP + fm * 16 + (e & 1) * 8 + fg;
-        split_pair<TERMS>(v[0], v[RP], w[e]);
-      }
-#pragma unroll
-      for (int k = 0; k < TERMS; ++k)
-        *reinterpret_cast<uint4*>(frag + (((fs * MR + fm) * TERMS + k) * 32 + fl) * 4) =
-            make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
-    }
-    if (kept) {  // decode into the bf16 tile: thread, row tid / 4, block tid % 4
-      const int r = tid >> 2, b = tid & 3;
-      const uint32_t sb = stage[Cfg::kXBytes + Cfg::kCoefBytes + r * 4 + b];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint2 c = *reinterpret_cast<const uint2*>(stage + r * 128 + b * 32 + i * 8);
-        uint32_t v[4];
-        codes_to_bf16(c, sb, p.e5m2 != 0, v);
-        *reinterpret_cast<uint4*>(decoded + r * 256 + (((b * 4 + i) ^ (r & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
-      }
-    }
-    __syncthreads();
-    next();  // into the stage of the block before
-    const uint32_t xt = kept ? smem_u32(decoded) : ring_at + st * Cfg::kStageBytes;
-    float part[MR][4][4];
-    if constexpr (kFlush) {
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) part[m][n][e] = 0.f;
-    }
-#pragma unroll
-    for (int s2 = 0; s2 < kSteps / 2; ++s2) {
-      const int s = 2 * s2 + wt;
-      uint32_t xb[2][4];  // [pair of n-tiles][tile 0 half 0, half 1, tile 1 half 0, half 1]
-#pragma unroll
-      for (int n2 = 0; n2 < 2; ++n2) {
-        const int r = s * 16 + (lane & 15), piece = wc * 4 + n2 * 2 + (lane >> 4);
-        ldmatrix_x4_trans(xt + r * 256 + ((piece ^ (r & 7)) * 16), xb[n2]);
-      }
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int k = TERMS - 1; k >= 0; --k) {
-          const uint4 f = *reinterpret_cast<const uint4*>(frag + (((s * MR + m) * TERMS + k) * 32 + lane) * 4);
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-            mma_bf16(kFlush ? part[m][n] : acc[m][n], f.x, f.y, f.z, f.w, xb[n / 2][(n % 2) * 2], xb[n / 2][(n % 2) * 2 + 1]);
-        }
-    }
-    if constexpr (kFlush) {
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][n][e] += part[m][n][e];
-    }
-    ++done;
-  }
-  copy_wait<0>();
-  __syncthreads();
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    if (wt == pass) {
-#pragma unroll
-      for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float* d = sums + (m * 16 + h * 8 + g) * kGradCols + wc * 32 + 8 * n + 2 * q + e;
-              *d = pass ? *d + acc[m][n][2 * h + e] : acc[m][n][2 * h + e];
-            }
-    }
-    __syncthreads();
-  }
+// A CTA's share of the sums of its cluster, times s[a], into the gradient.
+template <typename G>
+__device__ __forceinline__ void write_grad(const Grads& p, const GradJob& j, const float* sums, int pitch, int64_t c0,
+                                           int a, int rank, int cs, int threads) {
   if (cs > 1) {
     __syncwarp();
     cluster_sync();
@@ -1398,7 +1232,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
   const int n = p.R * cols, share = (n + cs - 1) / cs;
   const int e_end = min(n, (rank + 1) * share);
   G* out = static_cast<G*>(j.out) + static_cast<int64_t>(a) * p.R * j.C;
-  for (int e = rank * share + tid; e < e_end; e += 256) {
+  for (int e = rank * share + static_cast<int>(threadIdx.x); e < e_end; e += threads) {
     int r, c;
     if (j.out_cr) {
       c = e / p.R;
@@ -1409,10 +1243,10 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
     }
     float v = 0.f;
     if (cs > 1) {
-      const uint32_t addr = smem_u32(sums + r * kGradCols + c);
+      const uint32_t addr = smem_u32(sums + c * pitch + r);
       for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
     } else {
-      v = sums[r * kGradCols + c];
+      v = sums[c * pitch + r];
     }
     v *= s;
     const int64_t at = j.out_cr ? (c0 + c) * p.R + r : static_cast<int64_t>(r) * j.C + c0 + c;
@@ -1422,12 +1256,882 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       out[at] = v;
   }
   __syncwarp();
-  if (cs > 1) cluster_sync();
+  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// One CTA: an adapter's tokens, 64 at a time from the sorted order, by 128
+// columns of x; the blocks are dealt out over the CTAs of the cluster (y).
+// Tokens are the contraction, so both operands reach the tcgen05 MMAs as they
+// are copied, with their rows along it (M = the 128 columns, N = the padded
+// rank, TERMS MMAs of 16 tokens); codes are decoded in between, each by the
+// thread that copied it.
+template <int RP, int TERMS, typename G>
+__global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Grads p) {
+  using Cfg = GradTile<RP, TERMS>;
+  constexpr int S = Cfg::kStages, kSteps = kGradRows / 16;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kCtlAt);
+  const uint32_t ring_at = smem_u32(ring), coef_at = ring_at + Cfg::kRing, codes_at = ring_at + 2 * Cfg::kXBytes;
+  int* idx = reinterpret_cast<int*>(ring + Cfg::kIdxAt);  // [slot][row]: its token, or -1
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool second = blockIdx.x >= static_cast<unsigned>(p.job[0].tiles);
+  const GradJob& j = p.job[second ? 1 : 0];
+  const bool kept = j.x_scales != nullptr;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? p.job[0].tiles : 0)) * kGradCols;
+  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);  // cs: a power of two
+  const int a = static_cast<int>(blockIdx.z);
+
+  if (warp == 0) {
+    tmem_alloc(&ctl.tmem, Cfg::kTmem);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(&ctl.done[0], 1);
+    mbar_init(&ctl.done[1], 1);
+    ctl.abort_flag = 0;
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+
+  // this CTA's blocks: number i of the adapter's blocks over all segments goes to rank i % cs
+  int seg = 0, pos = 0, end = 0, turn = 0;
+  auto enter = [&]() {  // the segment's range of this adapter
+    const int* s = p.o.starts + static_cast<int64_t>(seg) * (p.L + 2) + a;
+    pos = s[0];
+    end = s[1];
+  };
+  auto settle = [&]() -> bool {  // to the next block of this rank; false: none is left
+    while (true) {
+      while (pos >= end) {
+        if (++seg >= p.o.segments) return false;
+        enter();
+      }
+      if ((turn & (cs - 1)) == rank) return true;
+      ++turn;
+      pos += kGradRows;
+    }
+  };
+  enter();
+  bool more = settle();
+  int found = 0;   // blocks whose tokens have been looked up
+  int token = -1;  // of row tid (tid < 64) of the last of them
+  int look_pos = 0, look_rows = 0;  // its place in the sorted order
+  auto look = [&]() {
+    if (!more) return;
+    if (tid < kGradRows) token = pos + tid < end ? p.o.perm[pos + tid] : -1;
+    look_pos = pos;
+    look_rows = min(kGradRows, end - pos);
+    ++found;
+    ++turn;
+    pos += kGradRows;
+    more = settle();
+  };
+  auto put = [&](int b) {  // the tokens of block b for all
+    if (tid < kGradRows) idx[(b % Cfg::kIdxSlots) * kGradRows + tid] = token;
+  };
+
+  auto issue_coef = [&](int b) {  // of the block looked up last
+    const uint32_t at = coef_at + (b % S) * Cfg::kCoefBytes;
+    constexpr int kRowPieces = TERMS * (RP / 8);
+    const bf16* src = j.coef + static_cast<int64_t>(look_pos) * (TERMS * RP);
+    for (int i = tid; i < kGradRows * kRowPieces; i += 256) {
+      const int r = i / kRowPieces, k = i % kRowPieces;
+      const bool in = r < look_rows;
+      copy_async<16>(at + (k / (RP / 8)) * Cfg::kTermBytes + Cfg::Coef::at(r, k % (RP / 8)), in ? src + i * 8 : src, in ? 16 : 0);
+    }
+  };
+  auto issue = [&](int b) {  // copies block b's x
+    const int* rows = idx + (b % Cfg::kIdxSlots) * kGradRows;
+    if (!kept) {
+      const uint32_t at = ring_at + (b % S) * Cfg::kXBytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (tid >> 4) + 16 * i, piece = tid & 15;
+        const int64_t t = rows[r];
+        stage8(at + Cfg::X::at(r, piece), static_cast<const bf16*>(j.x) + (t < 0 ? 0 : t) * j.ld, c0 + piece * 8,
+                    t < 0 ? 0 : j.C);
+      }
+    } else {  // each thread decodes what it copies
+      const uint32_t at = codes_at + (b % S) * Cfg::kCodeBytes;
+      const int64_t nb = j.C / 32;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = (tid >> 3) + 32 * i, piece = tid & 7;
+        const int64_t t = rows[r], c = c0 + piece * 16;
+        const bool in = t >= 0 && c < j.C;
+        const uint8_t* src = static_cast<const uint8_t*>(j.x) + (in ? t * j.ld + c : 0);
+        copy_async<16>(at + (i * 256 + tid) * 16, src, in ? 16 : 0);
+        const uint32_t sw = at + kGradRows * kGradCols + (i * 256 + tid) * 4;
+        const uint8_t* sb = j.x_scales + (in ? t * nb + c0 / 32 : 0);
+        if (p.scale4) {
+          copy_async<4>(sw, sb, in ? 4 : 0);
+        } else {
+          const uint32_t v = in ? static_cast<uint32_t>(__ldg(sb + piece / 2)) << (8 * (piece / 2)) : 0u;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sw), "r"(v) : "memory");
+        }
+      }
+    }
+  };
+  auto decode = [&](int b) {
+    const uint32_t src = codes_at + (b % S) * Cfg::kCodeBytes;
+    const uint32_t dst = ring_at + (b & 1) * Cfg::kXBytes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (tid >> 3) + 32 * i, piece = tid & 7;
+      const uint4 c = ld_shared16(src + (i * 256 + tid) * 16);
+      uint32_t sw;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw) : "r"(src + kGradRows * kGradCols + (i * 256 + tid) * 4) : "memory");
+      const uint32_t sb = (sw >> (8 * (piece / 2))) & 0xFFu;
+      const float s = __uint_as_float(sb == 0u ? 0x00400000u : (sb == 255u ? 0x7FFFFFFFu : sb << 23));
+      uint32_t w[4];
+      codes_to_bf16(make_uint2(c.x, c.y), s, p.e5m2 != 0, w);
+      st_shared16(dst + Cfg::X::at(r, piece * 2), w);
+      codes_to_bf16(make_uint2(c.z, c.w), s, p.e5m2 != 0, w);
+      st_shared16(dst + Cfg::X::at(r, piece * 2 + 1), w);
+    }
+  };
+
+  // the first blocks' tokens and copies
+#pragma unroll 1
+  for (int b = 0; b < S - 1; ++b) {
+    look();
+    if (b < found) {
+      put(b);
+      __syncthreads();
+      issue(b);
+      issue_coef(b);
+    }
+    copy_commit();
+  }
+  int issued = found;
+  look();  // one ahead of the copies
+  const uint32_t tmem = ctl.tmem;
+  bool ok = true;
+  int b = 0;
+  for (; b < issued; ++b) {
+    copy_wait<S - 2>();
+    if (kept) decode(b);  // into the half that the MMAs of block b - 2 read, waited for a turn ago
+    if (found > issued) put(issued);
+    fence_proxy_async_smem();
+    if (__syncthreads_or(!ok)) break;
+    if (tid == 0) {
+      const uint32_t xt = ring_at + (kept ? b & 1 : b % S) * Cfg::kXBytes;
+      const uint32_t ct = coef_at + (b % S) * Cfg::kCoefBytes;
+#pragma unroll
+      for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+          mma_f16(tmem, Cfg::X::along_rows(xt, s), Cfg::Coef::along_rows(ct + k * Cfg::kTermBytes, s),
+                  mma_shape(RP, true, true), (b > 0 || k < TERMS - 1 || s > 0) ? 1u : 0u);
+      tc_commit(&ctl.done[b & 1]);
+    }
+    if (b > 0)
+      ok = mbar_wait(&ctl.done[(b - 1) & 1], static_cast<uint32_t>((b - 1) >> 1) & 1u, p.w.timeout_ns, &ctl.abort_flag,
+                     p.w.status, kSiteGrads) && ok;
+    if (found > issued) {
+      issue(issued);
+      issue_coef(issued);
+      ++issued;
+      look();
+    }
+    copy_commit();
+  }
+  if (b > 0)
+    mbar_wait(&ctl.done[(b - 1) & 1], static_cast<uint32_t>((b - 1) >> 1) & 1u, p.w.timeout_ns, &ctl.abort_flag, p.w.status,
+              kSiteGrads);
+  copy_wait<0>();
+  __syncthreads();
+  tc_fence_after();
+  float* sums = reinterpret_cast<float*>(ring);  // [kGradCols][kPitch]: column, rank
+  {
+    constexpr int kHalf = RP < 32 ? RP : RP / 2;
+    if (RP >= 32 || warp < 4) {
+      float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
+      const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
+#pragma unroll
+      for (int k = 0; k < kHalf; k += 16) {
+        uint32_t v[16];
+        if (b > 0) {
+          tmem_ld16(src + k, v);
+          tmem_wait_ld();
+        } else {  // no block: zeros
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<uint4*>(dst + k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, Cfg::kTmem);
+  write_grad<G>(p, j, sums, Cfg::kPitch, c0, a, rank, cs, 256);
+}
+
+// ---------------------------------------------------------------------------
+// The same three with TMA: rows that are 16-byte aligned
+// ---------------------------------------------------------------------------
+// One warp feeds the stages: each of its lanes gathers four rows with one
+// instruction (the tokens are sorted, not moved), already in the swizzled form
+// that the MMA reads; another warp's first lane issues the MMAs.  No other warp
+// touches the streamed operand on its way: with asynchronous copies by all
+// threads, several instructions for every 16 bytes, the gradients of 8192 tokens
+// x 8192 columns took 137 us, bound by instruction issue.
+//
+// Weights come by TMA too where their rows are 16-byte aligned, else
+// (wtma = 0: ranks that are no multiple of 8) two warps stage them.
+struct Gather {
+  int4 r;
+  // rows pos + 4 i .. of the order, those from `count` on repeating the last one
+  __device__ __forceinline__ Gather(const int* perm, int start, int count, int i) {
+    r.x = perm[start + min(4 * i, count - 1)];
+    r.y = perm[start + min(4 * i + 1, count - 1)];
+    r.z = perm[start + min(4 * i + 2, count - 1)];
+    r.w = perm[start + min(4 * i + 3, count - 1)];
+  }
+};
+
+// Two warps (64 threads, i their number) stage rows of the weights that TMA
+// cannot: rows of R elements (64 of them, from row k) or R rows of 64 columns
+// (from column k); zeros past the array and past R.
+template <int RP, bool ROWS_OF_R>
+__device__ __forceinline__ void stage_weights(uint32_t at, const bf16* w, int64_t k, int64_t C, int R, int i) {
+  using W = Staged<ROWS_OF_R ? kChunk : RP, ROWS_OF_R ? RP : kChunk>;
+  constexpr int kPieces = (ROWS_OF_R ? RP : kChunk) / 8, kRows = ROWS_OF_R ? kChunk : RP;
+  for (int e = i; e < kRows * kPieces; e += 64) {
+    const int r = e / kPieces, piece = e % kPieces;
+    uint32_t v[4];
+    if constexpr (ROWS_OF_R)
+      load_row<8, false>(w + (k + r) * R, piece * 8, k + r < C ? R : 0, v);
+    else
+      load_row<8, false>(w + static_cast<int64_t>(r) * C, k + piece * 8, r < R ? C : 0, v);
+    st_shared16(at + W::at(r, piece), v);
+  }
+  fence_proxy_async_smem();
+}
+// ... and TMA otherwise (one thread): map {R or C, C or R, L}.
+template <int RP, bool ROWS_OF_R>
+__device__ __forceinline__ void load_weights(uint32_t at, const CUtensorMap* tm, uint64_t* bar, int64_t k, int adapter,
+                                             uint8_t* smem) {
+  using W = Staged<ROWS_OF_R ? kChunk : RP, ROWS_OF_R ? RP : kChunk>;
+  uint8_t* dst = smem + (at - smem_u32(smem));
+  if constexpr (ROWS_OF_R) {
+#pragma unroll
+    for (int b = 0; b < RP / W::kE; ++b) tma_load_3d(dst + b * W::kBlock, tm, bar, b * W::kE, static_cast<int>(k), adapter);
+  } else {
+    tma_load_3d(dst, tm, bar, static_cast<int>(k), 0, adapter);
+  }
+}
+
+template <int RP, bool TRANS>
+struct DownTma : DownTile<RP, TRANS> {
+  using Base = DownTile<RP, TRANS>;
+  struct Ctl {
+    uint64_t full[Base::kStages], empty[Base::kStages], done;
+    uint32_t tmem;
+    int abort_flag;
+  };
+  static constexpr int kSmem = Base::kRing + static_cast<int>(sizeof(Ctl));
+};
+struct DownTmaArgs {
+  CUtensorMap x, wm;
+  Down d;
+  Order o;
+  Waits w;
+  int wtma;
+};
+
+template <int RP, bool TRANS>
+__global__ void __launch_bounds__(128) adapter_down_tma(const __grid_constant__ DownTmaArgs ps) {
+  using Cfg = DownTma<RP, TRANS>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
+  const Down& p = ps.d;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
+  const uint32_t ring_at = smem_u32(ring);
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&ctl.full[i], ps.wtma ? 1 : 1 + 64);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    mbar_init(&ctl.done, 1);
+    ctl.abort_flag = 0;
+    fence_barrier_init();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const Tile tile = ps.o.tiles[blockIdx.x];
+  if (tile.count == 0) return;  // the whole cluster
+  if (tile.adapter < 0) {
+    for (int i = rank * 128 + tid; i < tile.count * p.R; i += cs * 128)
+      p.u[static_cast<int64_t>(ps.o.perm[tile.start + i / p.R]) * p.R + i % p.R] = 0.f;
+    return;
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl.tmem, Cfg::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  const int64_t chunks = (p.C + kChunk - 1) / kChunk;
+  const int64_t c_begin = chunks * rank / cs, c_end = chunks * (rank + 1) / cs;
+  const int n = static_cast<int>(c_end - c_begin);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteDown);
+  };
+  int c = 0;
+  if (warp == 0) {
+    const Gather g(ps.o.perm, tile.start, tile.count, lane);
+    for (; c < n; ++c) {
+      const int st = c % S;
+      if (c >= S && !wait(&ctl.empty[st], c / S - 1)) break;
+      const uint32_t at = ring_at + st * Cfg::kStageBytes;
+      const int64_t k = (c_begin + c) * kChunk;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctl.full[st], Cfg::kXBytes + (ps.wtma ? Cfg::kWBytes : 0));
+        if (ps.wtma) load_weights<RP, TRANS>(at + Cfg::kXBytes, &ps.wm, &ctl.full[st], k, tile.adapter, ring);
+      }
+      __syncwarp();
+      tma_gather4(at + lane * 512, &ps.x, &ctl.full[st], static_cast<int>(k), g.r);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (; c < n; ++c) {
+        const int st = c % S;
+        if (!wait(&ctl.full[st], c / S)) break;
+        tc_fence_after();
+        const uint32_t at = ring_at + st * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
+#pragma unroll
+        for (int s = 0; s < kChunk / 16; ++s)
+          mma_f16(tmem, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
+                  mma_shape(RP, false, TRANS), (c > 0 || s > 0) ? 1u : 0u);
+        tc_commit(&ctl.empty[st]);
+      }
+      tc_commit(&ctl.done);
+    }
+    __syncwarp();
+  } else if (!ps.wtma) {
+    const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
+    for (; c < n; ++c) {
+      const int st = c % S;
+      if (c >= S && !wait(&ctl.empty[st], c / S - 1)) break;
+      stage_weights<RP, TRANS>(ring_at + st * Cfg::kStageBytes + Cfg::kXBytes, w, (c_begin + c) * kChunk, p.C, p.R,
+                               tid - 64);
+      mbar_arrive(&ctl.full[st]);
+    }
+  }
+  __syncthreads();
+  wait(&ctl.done, 0);
+  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies in flight, bounded again
+    int never = 0;
+    for (int j = c > S ? c - S : 0; j < c; ++j)
+      mbar_wait(&ctl.full[j % S], static_cast<uint32_t>(j / S) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteDown);
+  }
+  __syncthreads();
+  tc_fence_after();
+  float* sums = reinterpret_cast<float*>(ring);  // [kTileRows][kPitch]
+  {
+    float* dst = sums + tid * Cfg::kPitch;
+#pragma unroll
+    for (int j = 0; j < RP; j += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + (warp * 32u << 16) + j, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<uint4*>(dst + j + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, Cfg::kTmem);
+  if (cs > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
+  const int total = tile.count * p.R, share = (total + cs - 1) / cs;
+  const int e_end = min(total, (rank + 1) * share);
+  for (int e = rank * share + tid; e < e_end; e += 128) {
+    const int r = e / p.R, col = e - r * p.R;
+    float v = 0.f;
+    if (cs > 1) {
+      const uint32_t addr = smem_u32(sums + r * Cfg::kPitch + col);
+      for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
+    } else {
+      v = sums[r * Cfg::kPitch + col];
+    }
+    p.u[static_cast<int64_t>(ps.o.perm[tile.start + r]) * p.R + col] = v;
+  }
+  __syncwarp();
+  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+template <int RP, typename Y, bool TRANS>
+struct UpTma : UpTile<RP, Y, TRANS> {
+  using Base = UpTile<RP, Y, TRANS>;
+  struct Ctl {
+    uint64_t wfull[Base::kWStages], wempty[Base::kWStages], yfull[Base::kYStages], yempty[Base::kYStages];
+    uint64_t dfull[2], dempty[2], ufull;
+    uint32_t tmem;
+    int abort_flag;
+  };
+  static constexpr int kSmem = Base::kCtlAt + static_cast<int>(sizeof(Ctl));
+};
+struct UpTmaArgs {
+  CUtensorMap y, out, wm;
+  Up d;
+  Order o;
+  Waits w;
+  int chunks_per_cta;
+  int wtma;
+};
+
+// Warp 0 feeds base and the weights, warp 1 issues the MMAs, warps 2 and 3
+// stage weights that TMA cannot; warps 4..7 own 32 rows each: they add the
+// product to base in place in its stage, from which four rows to an instruction
+// scatter to out.  Rows past a tile's tokens repeat its last one, in base and in
+// u, so that they write its row again with the same values.
+template <int RP, typename Y, bool TRANS>
+__global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ UpTmaArgs ps) {
+  using Cfg = UpTma<RP, Y, TRANS>;
+  constexpr int TERMS = Cfg::TERMS, YS = Cfg::kYStages, WS = Cfg::kWStages;
+  constexpr int kBlockCols = 128 / static_cast<int>(sizeof(Y));  // columns of a 128-byte row piece
+  constexpr int kBlocks = kChunk / kBlockCols;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(smem + Cfg::kCtlAt);
+  const Up& p = ps.d;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t u_at = smem_u32(smem), w_at = u_at + Cfg::kUBytes, y_at = w_at + WS * Cfg::kWBytes;
+
+  const Tile tile = ps.o.tiles[blockIdx.x];  // of two launches before, done before the last one released this one
+  if (tile.count == 0) return;
+  const int64_t chunks = (p.C + kChunk - 1) / kChunk;
+  const int64_t c_begin = static_cast<int64_t>(blockIdx.y) * ps.chunks_per_cta;
+  const int n = static_cast<int>(min(static_cast<int64_t>(ps.chunks_per_cta), chunks - c_begin));
+  const bool plain = tile.adapter < 0;  // no product: out = base
+  const bool has_base = p.base != nullptr;
+  if (tid == 0) {
+    for (int i = 0; i < WS; ++i) {
+      mbar_init(&ctl.wfull[i], ps.wtma ? 1 : 64);
+      mbar_init(&ctl.wempty[i], 1);
+    }
+    for (int i = 0; i < YS; ++i) {
+      mbar_init(&ctl.yfull[i], 1);
+      mbar_init(&ctl.yempty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.dfull[i], 1);
+      mbar_init(&ctl.dempty[i], 4);
+    }
+    mbar_init(&ctl.ufull, 128);
+    ctl.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl.tmem, 2 * kChunk);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteUp);
+  };
+  int c = 0;  // of the producer: chunks begun
+  if (warp == 0) {
+    const Gather g(ps.o.perm, tile.start, tile.count, lane);
+    for (; c < n; ++c) {
+      const int64_t k = (c_begin + c) * kChunk;
+      if (!plain && ps.wtma) {
+        const int st = c % WS;
+        if (c >= WS && !wait(&ctl.wempty[st], c / WS - 1)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl.wfull[st], Cfg::kWBytes);
+          load_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, &ps.wm, &ctl.wfull[st], k, tile.adapter, smem);
+        }
+      }
+      const int st = c % YS;
+      if (c >= YS && !wait(&ctl.yempty[st], c / YS - 1)) break;
+      if (!has_base) {
+        if (lane == 0) mbar_arrive(&ctl.yfull[st]);
+        continue;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.yfull[st], Cfg::kYBytes);
+      __syncwarp();
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+        tma_gather4(y_at + st * Cfg::kYBytes + b * (kTileRows * 128) + lane * 512, &ps.y, &ctl.yfull[st],
+                    static_cast<int>(k) + b * kBlockCols, g.r);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && !plain && wait(&ctl.ufull, 0)) {
+      for (int m = 0; m < n; ++m) {
+        const int st = m % WS;
+        if (!wait(&ctl.wfull[st], m / WS)) break;
+        if (m >= 2 && !wait(&ctl.dempty[m & 1], (m >> 1) - 1)) break;
+        tc_fence_after();
+        const uint32_t at = w_at + st * Cfg::kWBytes, d = tmem + (m & 1) * kChunk;
+#pragma unroll
+        for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+          for (int s = 0; s < RP / 16; ++s)
+            mma_f16(d, Cfg::U::along_pieces(u_at + k * Cfg::U::kBytes, s),
+                    TRANS ? Cfg::W::along_rows(at, s) : Cfg::W::along_pieces(at, s), mma_shape(kChunk, false, TRANS),
+                    (k < TERMS - 1 || s > 0) ? 1u : 0u);
+        tc_commit(&ctl.wempty[st]);
+        tc_commit(&ctl.dfull[m & 1]);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    if (!plain && !ps.wtma) {
+      const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
+      for (int m = 0; m < n; ++m) {
+        const int st = m % WS;
+        if (m >= WS && !wait(&ctl.wempty[st], m / WS - 1)) break;
+        stage_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, w, (c_begin + m) * kChunk, p.C, p.R, tid - 64);
+        mbar_arrive(&ctl.wfull[st]);
+      }
+    }
+  } else {
+    const int q = warp - 4, row = q * 32 + lane;  // this thread's row of the tile, and its lane of tensor memory
+    const int64_t token = ps.o.perm[tile.start + min(row, tile.count - 1)];
+    const Gather g(ps.o.perm, tile.start, tile.count, q * 8 + (lane & 7));
+    const float sc = plain ? 0.f : (p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f);
+    grid_dependency_wait();  // u is the launch before this one's
+    if (!plain) {
+      const float* src = p.u + token * p.R;
+#pragma unroll 1
+      for (int pr = 0; pr < RP / 8; ++pr) {
+        uint32_t t[4][TERMS];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = pr * 8 + 2 * e;
+          split_pair<TERMS>(r < p.R ? src[r] : 0.f, r + 1 < p.R ? src[r + 1] : 0.f, t[e]);
+        }
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) {
+          const uint32_t v[4] = {t[0][k], t[1][k], t[2][k], t[3][k]};
+          st_shared16(u_at + k * Cfg::U::kBytes + Cfg::U::at(row, pr), v);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&ctl.ufull);
+    }
+    bool ok = true;
+    int m = 0;
+    for (; m < n && ok; ++m) {
+      const int st = m % YS;
+      const uint32_t at = y_at + st * Cfg::kYBytes;
+      // (with no base, the stage must not be being scattered still: the producer has seen it empty)
+      ok = wait(&ctl.yfull[st], m / YS) && (plain || wait(&ctl.dfull[m & 1], m >> 1));
+      if (!plain || !has_base) {
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 32 columns at a time
+          uint32_t d[32];
+          if (!plain) {
+            tmem_ld32(tmem + (q * 32u << 16) + (m & 1) * kChunk + h * 32, d);
+            tmem_wait_ld();
+          }
+          constexpr int kPer = 16 / static_cast<int>(sizeof(Y)), kPieces = 32 / kPer;
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) {
+            const int piece = h * kPieces + j;  // of the row's chunk; 8 pieces to a 128-byte block
+            const uint32_t a = at + (piece / 8) * (kTileRows * 128) + row * 128 + (((piece & 7) ^ (row & 7)) * 16);
+            uint4 b = make_uint4(0u, 0u, 0u, 0u);
+            if (has_base) b = ld_shared16(a);
+            uint32_t v[4] = {b.x, b.y, b.z, b.w};
+            if (!plain) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(Y) == 2)
+                  v[e] = pack2(fmaf(sc, __uint_as_float(d[j * 8 + 2 * e]), __uint_as_float(v[e] << 16)),
+                               fmaf(sc, __uint_as_float(d[j * 8 + 2 * e + 1]), __uint_as_float(v[e] & 0xFFFF0000u)));
+                else
+                  v[e] = __float_as_uint(fmaf(sc, __uint_as_float(d[j * 4 + e]), __uint_as_float(v[e])));
+              }
+            }
+            st_shared16(a, v);
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (!plain && lane == 0) mbar_arrive(&ctl.dempty[m & 1]);
+      const int64_t k = (c_begin + m) * kChunk;
+      if (lane < 8 * kBlocks && k + (lane / 8) * kBlockCols < p.C)
+        tma_scatter4(&ps.out, at + (lane / 8) * (kTileRows * 128) + q * 4096 + (lane & 7) * 512,
+                     static_cast<int>(k) + (lane / 8) * kBlockCols, g.r);
+      bulk_commit();
+      bulk_wait_read<1>();  // the chunk before has left its stage
+      __syncwarp();
+      if (m > 0 && lane == 0) mbar_arrive(&ctl.yempty[(m - 1) % YS]);
+    }
+    bulk_wait<0>();
+  }
+  __syncthreads();
+  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies and MMAs in flight, bounded again
+    int never = 0;
+    for (int j = c > WS ? c - WS : 0; j < c && !plain && ps.wtma; ++j)
+      mbar_wait(&ctl.wfull[j % WS], static_cast<uint32_t>(j / WS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
+    for (int j = c > YS ? c - YS : 0; j < c; ++j)
+      mbar_wait(&ctl.yfull[j % YS], static_cast<uint32_t>(j / YS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 2 * kChunk);
+}
+
+template <int RP, int TERMS>
+struct GradTma : GradTile<RP, TERMS> {
+  using Base = GradTile<RP, TERMS>;
+  static constexpr int kStages = Base::kStages;
+  static constexpr int kStageBf16 = Base::kXBytes + Base::kCoefBytes;
+  static constexpr int kCodeBytes = kGradRows * kGradCols;
+  static constexpr int kStageCodes = kCodeBytes + Base::kCoefBytes;
+  // codes: two decoded blocks before the ring
+  static constexpr int kBf16 = kStages * kStageBf16, kCodes = 2 * Base::kXBytes + kStages * kStageCodes;
+  static constexpr int kRing = kBf16 > kCodes ? kBf16 : kCodes;
+  static_assert(kGradCols * Base::kPitch * 4 <= kRing, "the sums reuse the ring");
+  struct Ctl {
+    uint64_t full[kStages], empty[kStages], decoded[2], done;
+    uint32_t tmem;
+    int abort_flag;
+  };
+  static constexpr int kSmem = kRing + static_cast<int>(sizeof(Ctl));
+};
+struct GradTmaArgs {
+  CUtensorMap x[2];       // of the jobs: rows gathered (bf16 64 columns, codes 128)
+  CUtensorMap block, row; // the coefficients [2 T][TERMS RP]: 64 rows, and rows gathered
+  Grads g;
+  int64_t T;
+};
+
+// An adapter's blocks of 64 tokens that fall to one CTA of a cluster of cs (a
+// power of two): number i over all segments goes to rank i % cs.
+struct BlockWalk {
+  const Order& o;
+  int L, a, rank, cs;
+  int seg = -1, at = 0, end = 0, turn = 0;
+  int pos = 0, rows = 0;  // the current block
+  __device__ __forceinline__ BlockWalk(const Order& o_, int L_, int a_, int rank_, int cs_)
+      : o(o_), L(L_), a(a_), rank(rank_), cs(cs_) {}
+  __device__ __forceinline__ bool next() {
+    while (true) {
+      while (at >= end) {
+        if (++seg >= o.segments) return false;
+        const int* s = o.starts + static_cast<int64_t>(seg) * (L + 2) + a;
+        at = s[0];
+        end = s[1];
+      }
+      pos = at;
+      rows = min(kGradRows, end - at);
+      at += kGradRows;
+      if ((turn++ & (cs - 1)) == rank) return true;
+    }
+  }
+};
+
+// Warp 0 feeds x and the coefficients, warp 1 issues the MMAs; where x is a
+// checkpoint, warps 2..5 decode its codes between the two.  They also read the
+// sums out of tensor memory at the end.
+template <int RP, int TERMS, typename G>
+__global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
+  using Cfg = GradTma<RP, TERMS>;
+  using Coef = typename Cfg::Coef;
+  constexpr int S = Cfg::kStages, kSteps = kGradRows / 16;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
+  const Grads& p = ps.g;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int second = blockIdx.x >= static_cast<unsigned>(p.job[0].tiles) ? 1 : 0;
+  const GradJob& j = p.job[second];
+  const bool kept = j.x_scales != nullptr;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? p.job[0].tiles : 0)) * kGradCols;
+  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
+  const int a = static_cast<int>(blockIdx.z);
+  const uint32_t ring_at = smem_u32(ring) + (kept ? 2 * Cfg::kXBytes : 0);
+  const uint32_t stage_bytes = kept ? Cfg::kStageCodes : Cfg::kStageBf16;
+  const uint32_t coef_off = kept ? Cfg::kCodeBytes : Cfg::kXBytes;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    mbar_init(&ctl.decoded[0], 128);
+    mbar_init(&ctl.decoded[1], 128);
+    mbar_init(&ctl.done, 1);
+    ctl.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl.tmem, Cfg::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  grid_dependency_wait();
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity & 1u, p.w.timeout_ns, &ctl.abort_flag, p.w.status, kSiteGrads);
+  };
+  BlockWalk walk(p.o, p.L, a, rank, cs);
+  int b = 0;
+  if (warp == 0) {
+    const int T = static_cast<int>(ps.T);
+    // lane: four rows of x (bf16: of one of the two 64-column halves); rows past the block are past the array: zeros
+    const int group = kept ? lane & 15 : lane >> 1;
+    auto token = [&](int r) { return r < walk.rows ? p.o.perm[walk.pos + r] : T; };
+    bool more = walk.next();
+    int4 rows = make_int4(0, 0, 0, 0);
+    if (more) rows = make_int4(token(4 * group), token(4 * group + 1), token(4 * group + 2), token(4 * group + 3));
+    while (more) {
+      const int st = b % S;
+      if (b >= S && !wait(&ctl.empty[st], b / S - 1)) break;
+      const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], stage_bytes);
+      __syncwarp();
+      if (!kept)
+        tma_gather4(at + (lane & 1) * (kGradRows * 128) + group * 512, &ps.x[second], &ctl.full[st],
+                    static_cast<int>(c0) + (lane & 1) * 64, rows);
+      else if (lane < 16)
+        tma_gather4(at + group * 512, &ps.x[second], &ctl.full[st], static_cast<int>(c0), rows);
+      constexpr int kCoefBlocks = RP / Coef::kE;
+      const int row0 = second * T + walk.pos;
+      if (walk.rows == kGradRows) {
+        if (lane < TERMS * kCoefBlocks)
+          tma_load_2d(ct + (lane / kCoefBlocks) * Cfg::kTermBytes + (lane % kCoefBlocks) * Coef::kBlock, &ps.block,
+                      &ctl.full[st], lane * Coef::kE, row0);
+      } else {
+        for (int i = lane; i < TERMS * kCoefBlocks * (kGradRows / 4); i += 32) {
+          const int g4 = i % (kGradRows / 4), k = i / (kGradRows / 4);
+          auto at4 = [&](int e) { return 4 * g4 + e < walk.rows ? row0 + 4 * g4 + e : 2 * T; };
+          tma_gather4(ct + (k / kCoefBlocks) * Cfg::kTermBytes + (k % kCoefBlocks) * Coef::kBlock + g4 * 4 * Coef::kWidth,
+                      &ps.row, &ctl.full[st], k * Coef::kE, make_int4(at4(0), at4(1), at4(2), at4(3)));
+        }
+      }
+      ++b;
+      more = walk.next();
+      if (more) rows = make_int4(token(4 * group), token(4 * group + 1), token(4 * group + 2), token(4 * group + 3));
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      while (walk.next()) {
+        const int st = b % S;
+        if (!wait(&ctl.full[st], b / S)) break;
+        if (kept && !wait(&ctl.decoded[b & 1], b >> 1)) break;
+        tc_fence_after();
+        const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
+        const uint32_t xt = kept ? smem_u32(ring) + (b & 1) * Cfg::kXBytes : at;
+#pragma unroll
+        for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s)
+            mma_f16(tmem, Cfg::X::along_rows(xt, s), Coef::along_rows(ct + k * Cfg::kTermBytes, s),
+                    mma_shape(RP, true, true), (b > 0 || k < TERMS - 1 || s > 0) ? 1u : 0u);
+        tc_commit(&ctl.empty[st]);
+        ++b;
+      }
+      tc_commit(&ctl.done);
+    }
+    b = __shfl_sync(0xFFFFFFFFu, b, 0);
+  } else if (kept) {
+    // thread: rows (tid - 64) / 4 and 32 further, the 32 codes of block (tid - 64) % 4
+    const int r0 = (tid - 64) >> 2, blk = (tid - 64) & 3;
+    const int64_t nb = j.C / 32;
+    const bool in = c0 / 32 + blk < nb;
+    auto scale = [&](int r) -> uint32_t {
+      return in && r < walk.rows ? __ldg(j.x_scales + static_cast<int64_t>(p.o.perm[walk.pos + r]) * nb + c0 / 32 + blk) : 127u;
+    };
+    bool more = walk.next();
+    uint32_t s0 = 127u, s1 = 127u;
+    if (more) {
+      s0 = scale(r0);
+      s1 = scale(r0 + 32);
+    }
+    while (more) {
+      const int st = b % S;
+      const uint32_t f0 = s0, f1 = s1;
+      more = walk.next();
+      if (more) {
+        s0 = scale(r0);
+        s1 = scale(r0 + 32);
+      }
+      if (!wait(&ctl.full[st], b / S)) break;
+      if (b >= 2 && !wait(&ctl.empty[(b - 2) % S], (b - 2) / S)) break;  // the MMAs have read this half
+      const uint32_t src = ring_at + st * stage_bytes, dst = smem_u32(ring) + (b & 1) * Cfg::kXBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = r0 + 32 * h;
+        const uint32_t sb = h ? f1 : f0;
+        const float s = __uint_as_float(sb == 0u ? 0x00400000u : (sb == 255u ? 0x7FFFFFFFu : sb << 23));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 c = ld_shared16(src + r * 128 + (((blk * 2 + i) ^ (r & 7)) * 16));
+          uint32_t w[4];
+          codes_to_bf16(make_uint2(c.x, c.y), s, p.e5m2 != 0, w);
+          st_shared16(dst + Cfg::X::at(r, blk * 4 + i * 2), w);
+          codes_to_bf16(make_uint2(c.z, c.w), s, p.e5m2 != 0, w);
+          st_shared16(dst + Cfg::X::at(r, blk * 4 + i * 2 + 1), w);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&ctl.decoded[b & 1]);
+      ++b;
+    }
+  }
+  __syncthreads();
+  wait(&ctl.done, 0);
+  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies in flight, bounded again
+    int never = 0;
+    for (int i = b > S ? b - S : 0; i < b; ++i)
+      mbar_wait(&ctl.full[i % S], static_cast<uint32_t>(i / S) & 1u, p.w.timeout_ns, &never, p.w.status, kSiteGrads);
+  }
+  const int any = __syncthreads_or(warp == 1 && b > 0);
+  tc_fence_after();
+  float* sums = reinterpret_cast<float*>(ring);  // [kGradCols][kPitch]: column, rank
+  if (warp >= 2) {
+    const int q = warp & 3;  // the quarter of tensor memory that this warp can read
+    float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
+#pragma unroll
+    for (int k = 0; k < RP; k += 16) {
+      uint32_t v[16];
+      if (any) {
+        tmem_ld16(tmem + (q * 32u << 16) + k, v);
+        tmem_wait_ld();
+      } else {  // no block: zeros
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<uint4*>(dst + k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, Cfg::kTmem);
+  write_grad<G>(p, j, sums, Cfg::kPitch, c0, a, rank, cs, 192);
 }
 
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
 // A launch whose y extent is one cluster, and which may start while the launch
 // before it on the stream is still running (it waits for it itself).
 template <typename P>
@@ -1466,16 +2170,43 @@ cudaError_t launch(const char* name, void (*kernel)(P), const P& p, dim3 grid, i
 // adapter; below, taken as they come, several adapters to a tile.
 constexpr int64_t kSortFrom = 2048;
 
+constexpr CUtensorMapDataType kMapBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+
+// The weights' map for load_weights: rows of R elements {R, C, L} or of C {C, R, L}.
+template <int RP>
+bool weights_map(CUtensorMap* tm, const bf16* w, bool rows_of_r, int64_t C, int R, int L) {
+  if (!aligned(w, 16) || (rows_of_r ? R : C) % 8) return false;
+  return rows_of_r ? make_tmap_rows(tm, w, kMapBf16, 2, R, C, L, static_cast<uint64_t>(R) * 2, RP < 64 ? RP : 64, kChunk)
+                   : make_tmap_rows(tm, w, kMapBf16, 2, C, R, L, static_cast<uint64_t>(C) * 2, kChunk, RP);
+}
+
+// T rows of `cols` elements at a pitch of ld, gathered or scattered `box` columns at a time.
+bool rows_map(CUtensorMap* tm, const void* base, CUtensorMapDataType type, int elem, int64_t cols, int64_t T, int64_t ld,
+              int box) {
+  if (!aligned(base, 16) || ld * elem % 16) return false;
+  return make_tmap_rows(tm, base, type, elem, cols, T, 0, static_cast<uint64_t>(ld) * elem, box, 1);
+}
+
 template <int NT, bool TRANS, bool VEC>
 cudaError_t down_rank(Down p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
   if (o) {
-    using Cfg = DownTile<NT, TRANS>;
+    constexpr int RP = NT < 2 ? 16 : NT * 8;
     const int64_t slots = static_cast<int64_t>(o->segments) * o->tiles_per_segment;
     const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));  // likely in use
     unsigned cs = 1;
     while (cs < 8 && tiles * cs * 2 <= 2 * ctx->num_sms && p.C >= 4 * kChunk * static_cast<int64_t>(cs)) cs *= 2;
-    return launch("adapter_down_tile", adapter_down_tile<NT, TRANS, VEC>, DownSorted{p, *o},
-                  dim3(static_cast<unsigned>(slots), cs), 256, Cfg::kSmem, cs, true, s);
+    const dim3 grid(static_cast<unsigned>(slots), cs);
+    const Waits w{ctx->status, wait_timeout_ns()};
+    DownTmaArgs a{};
+    if (rows_map(&a.x, p.x, kMapBf16, 2, p.C, p.T, p.ld, kChunk)) {
+      a.d = p;
+      a.o = *o;
+      a.w = w;
+      a.wtma = weights_map<RP>(&a.wm, p.w, TRANS, p.C, p.R, p.L);
+      return launch("adapter_down_tma", adapter_down_tma<RP, TRANS>, a, grid, 128, DownTma<RP, TRANS>::kSmem, cs, true, s);
+    }
+    return launch("adapter_down_tile", adapter_down_tile<RP, TRANS>, DownSorted{p, *o, w}, grid, 256,
+                  DownTile<RP, TRANS>::kSmem, cs, true, s);
   }
   const int64_t chunks = ceil_div(p.C, 32);
   constexpr int WK = 8, U = NT <= 4 ? 4 : 2;
@@ -1500,15 +2231,28 @@ cudaError_t down(const Down& p, const Order* o, const DeviceCtx* ctx, cudaStream
 template <int KT, typename Y, bool TRANS, bool VEC>
 cudaError_t up_rank(Up p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
   if (o) {
-    using Cfg = UpTile<KT, Y, TRANS>;
+    constexpr int RP = KT * 16;
     const int64_t slots = static_cast<int64_t>(o->segments) * o->tiles_per_segment;
     const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));
     const int64_t chunks = ceil_div(p.C, kChunk);
     const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 2 * ctx->num_sms / tiles));
-    UpSorted u{p, *o, static_cast<int>(ceil_div(chunks, splits))};
-    return launch("adapter_up_tile", adapter_up_tile<KT, Y, TRANS, VEC>, u,
-                  dim3(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, u.chunks_per_cta))), 256,
-                  Cfg::kSmem, 1, true, s);
+    const int per_cta = static_cast<int>(ceil_div(chunks, splits));
+    const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, per_cta)));
+    const Waits w{ctx->status, wait_timeout_ns()};
+    constexpr CUtensorMapDataType kMapY = sizeof(Y) == 2 ? kMapBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    constexpr int kBox = 128 / static_cast<int>(sizeof(Y));
+    UpTmaArgs a{};
+    if (rows_map(&a.out, p.out, kMapY, sizeof(Y), p.C, p.T, p.ld_out, kBox) &&
+        (!p.base || rows_map(&a.y, p.base, kMapY, sizeof(Y), p.C, p.T, p.ld_base, kBox))) {
+      a.d = p;
+      a.o = *o;
+      a.w = w;
+      a.chunks_per_cta = per_cta;
+      a.wtma = weights_map<RP>(&a.wm, p.w, !TRANS, p.C, p.R, p.L);
+      return launch("adapter_up_tma", adapter_up_tma<RP, Y, TRANS>, a, grid, 256, UpTma<RP, Y, TRANS>::kSmem, 1, true, s);
+    }
+    return launch("adapter_up_tile", adapter_up_tile<RP, Y, TRANS>, UpSorted{p, *o, w, per_cta}, grid, 256,
+                  UpTile<RP, Y, TRANS>::kSmem, 1, true, s);
   }
   constexpr int WN = 4;
   p.cols_per_warp = 32;
@@ -1527,23 +2271,44 @@ cudaError_t up(const Up& p, const Order* o, const DeviceCtx* ctx, cudaStream_t s
   return up_rank<8, Y, TRANS, VEC>(p, o, ctx, s);
 }
 
-template <int MR, typename G, bool VEC>
-cudaError_t grads_rank(const Grads& p, int64_t T, const DeviceCtx* ctx, cudaStream_t s) {
+template <int RP, typename G>
+cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCtx* ctx, cudaStream_t s) {
   constexpr int TERMS = sizeof(G) == 4 ? 3 : 2;
+  const int64_t T = r.T;
+  bf16* terms_at = static_cast<bf16*>(r.terms);
+  p.job[0].coef = terms_at;
+  p.job[1].coef = terms_at + T * TERMS * RP;
+  const Terms terms{{r.d, r.u}, {terms_at, terms_at + T * TERMS * RP}, p.o.perm, T, p.R};
+  const cudaError_t e = launch("adapter_terms", adapter_terms<RP, TERMS>, terms,
+                               dim3(static_cast<unsigned>(ceil_div(T * (RP / 8), 256))), 256, 0, 1, true, s);
+  if (e != cudaSuccess) return e;
   const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
   unsigned cs = 1;
   while (cs < 8 && tiles * p.L * cs < 4 * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
-  return launch("adapter_grads", adapter_grads<MR, TERMS, G, VEC>, p,
-                dim3(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L)), 256, GradTile<MR, TERMS>::kSmem, cs,
-                true, s);
+  const dim3 grid(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L));
+  GradTmaArgs a{};
+  bool tma = true;
+  for (int k = 0; k < 2 && tma; ++k)
+    tma = p.job[k].x_scales
+              ? rows_map(&a.x[k], p.job[k].x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.job[k].C, T, p.job[k].ld, kGradCols)
+              : rows_map(&a.x[k], p.job[k].x, kMapBf16, 2, p.job[k].C, T, p.job[k].ld, 64);
+  constexpr int kE = RP < 64 ? RP : 64;
+  tma = tma && make_tmap_rows(&a.block, terms_at, kMapBf16, 2, TERMS * RP, 2 * T, 0, TERMS * RP * 2, kE, kGradRows) &&
+        make_tmap_rows(&a.row, terms_at, kMapBf16, 2, TERMS * RP, 2 * T, 0, TERMS * RP * 2, kE, 1);
+  if (tma) {
+    a.g = p;
+    a.T = T;
+    return launch("adapter_grads_tma", adapter_grads_tma<RP, TERMS, G>, a, grid, 192, GradTma<RP, TERMS>::kSmem, cs, true, s);
+  }
+  return launch("adapter_grads", adapter_grads<RP, TERMS, G>, p, grid, 256, GradTile<RP, TERMS>::kSmem, cs, true, s);
 }
 
-template <typename G, bool VEC>
-cudaError_t grads(const Grads& p, int64_t T, const DeviceCtx* ctx, cudaStream_t s) {
-  if (p.R <= 16) return grads_rank<1, G, VEC>(p, T, ctx, s);
-  if (p.R <= 32) return grads_rank<2, G, VEC>(p, T, ctx, s);
-  if (p.R <= 64) return grads_rank<4, G, VEC>(p, T, ctx, s);
-  return grads_rank<8, G, VEC>(p, T, ctx, s);
+template <typename G>
+cudaError_t grads(const Grads& p, const AdaptersBackwardRequest& r, const DeviceCtx* ctx, cudaStream_t s) {
+  if (p.R <= 16) return grads_rank<16, G>(p, r, ctx, s);
+  if (p.R <= 32) return grads_rank<32, G>(p, r, ctx, s);
+  if (p.R <= 64) return grads_rank<64, G>(p, r, ctx, s);
+  return grads_rank<128, G>(p, r, ctx, s);
 }
 
 // The order's arrays in the workspace.
@@ -1573,14 +2338,17 @@ cudaError_t sort(const int* ids, int64_t T, int L, const Order& o, cudaStream_t 
   return cudaGetLastError();
 }
 
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
 }  // namespace
 
 size_t adapter_order_bytes(int64_t T, int64_t L) {
   const int64_t segments = ceil_div(T, kSegment);
   return align_up(static_cast<size_t>(T) * 4, 256) + align_up(static_cast<size_t>(segments) * (L + 2) * 4, 256) +
          align_up(static_cast<size_t>(segments) * tiles_per_segment(T, static_cast<int>(L)) * sizeof(Tile), 256);
+}
+
+size_t adapter_terms_bytes(int64_t T, int64_t R) {
+  const int64_t rp = R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128));
+  return align_up(static_cast<size_t>(T) * 3 * rp * 2 * 2, 256);  // of binary32 gradients, for both
 }
 
 bool adapters_sorted(int64_t T, int64_t L) { return T >= kSortFrom && L <= kSortMaxL; }
@@ -1635,18 +2403,16 @@ cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStrea
   e = uv ? up<bf16, true, true>(u, o, ctx, s) : up<bf16, true, false>(u, o, ctx, s);
   if (e != cudaSuccess) return e;
   Grads p{};
-  p.job[0] = GradJob{r.d, r.x, r.x_scales, r.ld_x, r.da, r.K, static_cast<int>(ceil_div(r.K, kGradCols)), 0};
-  p.job[1] = GradJob{r.u, r.dy, nullptr, r.ld_dy, r.db, r.N, static_cast<int>(ceil_div(r.N, kGradCols)), 1};
+  p.job[0] = GradJob{nullptr, r.x, r.x_scales, r.ld_x, r.da, r.K, static_cast<int>(ceil_div(r.K, kGradCols)), 0};
+  p.job[1] = GradJob{nullptr, r.dy, nullptr, r.ld_dy, r.db, r.N, static_cast<int>(ceil_div(r.N, kGradCols)), 1};
   p.scaling = r.scaling;
   p.o = order;
   p.R = R;
   p.L = L;
   p.e5m2 = r.x_code == BSMM_E5M2;
-  p.coef16 = R % 4 == 0 && aligned(r.u, 16) && aligned(r.d, 16);
-  const bool xv = r.x_scales || (r.K % 8 == 0 && r.ld_x % 8 == 0 && aligned(r.x, 16));
-  const bool gv = xv && r.N % 8 == 0 && r.ld_dy % 8 == 0 && aligned(r.dy, 16);
-  if (r.grad_bf16) return gv ? grads<bf16, true>(p, r.T, ctx, s) : grads<bf16, false>(p, r.T, ctx, s);
-  return gv ? grads<float, true>(p, r.T, ctx, s) : grads<float, false>(p, r.T, ctx, s);
+  p.scale4 = r.x_scales && r.K % 128 == 0 && aligned(r.x_scales, 4);
+  p.w = Waits{ctx->status, wait_timeout_ns()};
+  return r.grad_bf16 ? grads<bf16>(p, r, ctx, s) : grads<float>(p, r, ctx, s);
 }
 
 }  // namespace bsmm

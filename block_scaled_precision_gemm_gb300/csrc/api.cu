@@ -69,8 +69,8 @@ const DeviceCtx* device_ctx() {
 
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
 
-bool make_tmap_3d(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, int elem_bytes, uint64_t d0,
-                  uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle128) {
+namespace {
+bool have_encode() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -79,7 +79,13 @@ bool make_tmap_3d(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, 
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
-  if (!g_encode) return false;
+  return g_encode != nullptr;
+}
+}  // namespace
+
+bool make_tmap_3d(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, int elem_bytes, uint64_t d0,
+                  uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle128) {
+  if (!have_encode()) return false;
   const cuuint64_t dims[3] = {d0, d1, d2};
   const cuuint64_t strides[2] = {d0 * elem_bytes, d0 * d1 * elem_bytes};
   const cuuint32_t box[3] = {b0, b1, 1};
@@ -88,6 +94,23 @@ bool make_tmap_3d(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, 
                               CU_TENSOR_MAP_INTERLEAVE_NONE,
                               swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_rows(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, int elem_bytes, uint64_t d0,
+                    uint64_t d1, uint64_t d2, uint64_t pitch, uint32_t b0, uint32_t b1) {
+  if (!have_encode()) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {pitch, pitch * d1};
+  const cuuint32_t box[3] = {b0, b1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const uint32_t width = b0 * static_cast<uint32_t>(elem_bytes);
+  const CUtensorMapSwizzle sw = width == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUresult r = g_encode(tm, dtype, d2 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -846,7 +869,8 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
 
 size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R, int64_t L) {
   if (T <= 0 || R <= 0 || L <= 0) return 0;
-  return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256) + adapter_order_bytes(T, L);
+  return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256) + adapter_order_bytes(T, L) +
+         adapter_terms_bytes(T, R);
 }
 
 bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* dy,
@@ -877,10 +901,10 @@ bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, i
   if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) +
                                         " bytes");
+  uint8_t* order = static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T) * R * 4, 256);
   const AdaptersBackwardRequest r{T, K, N, R, L, dy, ld_dy, x, ld_x, static_cast<const uint8_t*>(x_scales), x_type, A, B,
                                   ids, scaling, u, dx_base, ld_dx, dx, dA, dB, grad_type == BSMM_BF16,
-                                  static_cast<float*>(workspace),
-                                  static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T) * R * 4, 256)};
+                                  static_cast<float*>(workspace), order, order + adapter_order_bytes(T, L)};
   return launched(launch_adapters_backward(r, reinterpret_cast<cudaStream_t>(stream)), "adapters backward launch");
 }
 

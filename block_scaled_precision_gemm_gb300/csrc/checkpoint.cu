@@ -339,7 +339,7 @@ constexpr int kKeepNone = 0, kKeepMx = 1, kKeepF32 = 2;
 
 // The next row's elements are loaded before this row's are worked on.
 template <typename In, int KEEP, int ACT, bool HQ>
-__global__ void __launch_bounds__(kThreads, sizeof(In) == 2 ? 3 : 2) gated_fwd(const GatedFwd p) {
+__global__ void __launch_bounds__(kThreads, 2) gated_fwd(const GatedFwd p) {
   constexpr int kPer = kFwdPer;
   constexpr bool POW2 = KEEP == kKeepMx;
   constexpr int kBlock = POW2 ? 32 : 128, W = kBlock / kPer;
@@ -639,7 +639,7 @@ cudaError_t launch_gated_act(const GatedRequest& r, cudaStream_t s) {
   const GatedFwd p{r.x,      r.M,       r.ld, static_cast<int>(r.I), r.h,    static_cast<uint8_t*>(r.h_scales),
                    r.h_type, r.h_atoms, r.h_ks4, static_cast<uint8_t*>(r.codes), r.scales, r.code,
                    strips(r.I, kFwdPer, keep == kKeepF32 ? 128 / kFwdPer : 32 / kFwdPer)};
-  const dim3 grid = gated_grid(p.strips, r.M, r.x_bf16 ? 3 : 2, ctx);
+  const dim3 grid = gated_grid(p.strips, r.M, 2, ctx);
   {
     TraceScope tr("gated_fwd", s);
     if (r.x_bf16)

@@ -54,6 +54,12 @@ uint64_t wait_timeout_ns();
 bool make_tmap_3d(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, int elem_bytes, uint64_t d0,
                   uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle128);
 
+// Tensor map of 2 or 3 dimensions (d2 = 0: two), rows of d0 elements `pitch`
+// bytes apart (a multiple of 16), box {b0, b1, 1}; swizzled over b0's bytes (32,
+// 64 or 128).  A box one row high serves gathers and scatters of rows.
+bool make_tmap_rows(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, int elem_bytes, uint64_t d0,
+                    uint64_t d1, uint64_t d2, uint64_t pitch, uint32_t b0, uint32_t b1);
+
 // ---- kernel launchers (return cudaSuccess or the launch error) -----------
 struct QuantRequest {
   const void* x;
@@ -171,11 +177,14 @@ struct AdaptersBackwardRequest {
   bool grad_bf16;
   float* d;     // [T][R] scratch
   void* order;  // adapter_order_bytes of scratch
+  void* terms;  // adapter_terms_bytes of scratch
 };
 // Whether bsmm_adapters sorts its tokens (and needs the order's bytes), the
-// bytes, and the most adapters that can be sorted by.
+// bytes, those of the gradients' coefficients, and the most adapters that can
+// be sorted by.
 bool adapters_sorted(int64_t T, int64_t L);
 size_t adapter_order_bytes(int64_t T, int64_t L);
+size_t adapter_terms_bytes(int64_t T, int64_t R);
 int64_t adapters_sort_max();
 cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s);
 

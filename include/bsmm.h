@@ -576,7 +576,8 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
  *   dA [L, R, K], dB [L, N, R] of type grad_type (F32 or BF16), contiguous:
  *            overwritten; zero for an adapter without tokens.
  *   workspace  bsmm_adapters_backward_workspace_size() bytes, 256-byte
- *            aligned (holds d and the order of the tokens by their adapter).
+ *            aligned (holds d, the order of the tokens by their adapter, and d
+ *            and u in that order).
  *   L up to 1024 (BSMM_ERR_UNSUPPORTED beyond).
  * dA and dB need the tokens' sums only: T == 0 writes zeros. */
 size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R, int64_t L);

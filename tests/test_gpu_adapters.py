@@ -79,6 +79,9 @@ FORWARD = [  # T, K, N, R, L, ids, y
     (129, 160, 136, 128, 2, "runs", "bf16"), (300, 544, 264, 4, 5, "runs", "f32"), (777, 96, 160, 32, 5, "mixed", "bf16"),
     (2048, 264, 136, 16, 3, "runs", "bf16"), (2049, 71, 45, 7, 4, "mixed", "f32"), (2300, 128, 1032, 64, 4, "runs", "f32"),
     (2100, 64, 64, 128, 3, "mixed", "bf16"), (2050, 512, 40, 8, 40, "mixed", "bf16"), (40, 64, 64, 16, 3, "none", "bf16"),
+    (2500, 96, 80, 12, 3, "mixed", "f32"), (2200, 72, 328, 24, 4, "runs", "bf16"), (2048, 704, 96, 32, 2, "runs", "none"),
+    (8200, 64, 72, 16, 6, "mixed", "bf16"), (2176, 64, 200, 128, 2, "runs", "f32"), (2100, 64, 64, 16, 3, "none", "bf16"),
+    (2100, 36, 1000, 16, 1100, "mixed", "bf16"),
 ]
 
 
@@ -163,6 +166,8 @@ BACKWARD = [  # T, K, N, R, L, ids, x, grad
     (1333, 72, 64, 12, 3, "mixed", "bf16", "f32"), (700, 128, 96, 128, 2, "runs", "e4m3", "f32"),
     (2100, 96, 72, 64, 2, "runs", "e4m3", "bf16"), (2049, 45, 71, 7, 3, "mixed", "bf16", "f32"),
     (40, 64, 64, 16, 3, "none", "bf16", "f32"), (2060, 264, 200, 33, 5, "mixed", "bf16", "f32"),
+    (2304, 288, 320, 32, 2, "runs", "e5m2", "f32"), (8300, 96, 64, 16, 3, "mixed", "e4m3", "f32"),
+    (640, 160, 44, 16, 2, "runs", "e4m3", "bf16"), (2200, 72, 64, 24, 300, "mixed", "bf16", "f32"),
 ]
 
 
