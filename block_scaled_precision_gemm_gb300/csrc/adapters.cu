@@ -492,31 +492,79 @@ __global__ void __launch_bounds__(WN * 32) adapter_up(const Up p) {
 // tokens without an adapter come last, under adapter -1.
 constexpr int kSegment = 8192, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortRounds = kSegment / kSortThreads;
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128;  // of a tile
+constexpr int kGradRows = 64;   // of a block of the gradients
 constexpr int kSortMaxL = 1024;
 
 struct Tile {
-  int adapter, start, count, unused;  // rows perm[start .. start + count)
+  int adapter, start, count;  // tokens perm[start .. start + count)
+  int run;                    // 1: consecutive ones
 };
 
 // The sort's output in the caller's workspace.
 struct Order {
-  int* perm;      // [T]
-  int* starts;    // [segments][L + 2]: the first position of each adapter, of -1, and the segment's end
-  Tile* tiles;    // [segments][tiles_per_segment], unused ones with count 0
-  int tiles_per_segment, segments;
+  int* perm;     // [T]
+  Tile* tiles;   // [segments][tiles_per_segment] of 128 tokens, unused ones with count 0
+  Tile* blocks;  // [segments][blocks_per_segment] of 64 tokens, each adapter's together
+  int* starts;   // [segments][L + 1]: the first block of each adapter, and the one after the last's
+  int tiles_per_segment, blocks_per_segment, segments;
 };
 
-__host__ __device__ inline int tiles_per_segment(int64_t T, int L) {
+inline int pieces_per_segment(int64_t T, int L, int rows_of_one) {
   const int64_t rows = T < kSegment ? T : kSegment;
   const int64_t groups = L + 1 < rows ? L + 1 : rows;
-  return static_cast<int>((rows + kTileRows - 1) / kTileRows + groups);
+  return static_cast<int>((rows + rows_of_one - 1) / rows_of_one + groups);
+}
+
+// The pieces of `rows` tokens that the sorted groups fall into: count of group
+// k's in place of its tokens, then their exclusive sums.
+__device__ __forceinline__ void group_pieces(const int* first, int* piece0, int G, int rows) {
+  const int lane = threadIdx.x & 31;
+  const int per = (G + 31) / 32, k0 = lane * per, k1 = min(G, k0 + per);
+  auto count = [&](int k) { return (first[k + 1] - first[k] + rows - 1) / rows; };
+  int n = 0;
+  for (int k = k0; k < k1; ++k) n += count(k);
+  int p = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, p, d);
+    if (lane >= d) p += up;
+  }
+  p -= n;
+  for (int k = k0; k < k1; ++k) {
+    piece0[k] = p;
+    p += count(k);
+  }
+  if (k0 < G && k1 == G) piece0[G] = p;
+}
+
+// Writes them: piece i of all.
+__device__ __forceinline__ Tile sorted_piece(const int* first, const int* piece0, const uint16_t* perm, int G, int rows,
+                                             int s0, int i) {
+  Tile t{-1, 0, 0, 0};
+  if (i >= piece0[G]) return t;
+  int lo = 0, hi = G - 1;  // the last group whose first piece is at or before i
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (piece0[mid] <= i)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int at = first[lo] + (i - piece0[lo]) * rows;
+  t.adapter = lo == G - 1 ? -1 : lo;
+  t.start = s0 + at;
+  t.count = min(rows, first[lo + 1] - at);
+  t.run = perm[at + t.count - 1] - perm[at] == t.count - 1;  // a group's tokens are in ascending order
+  return t;
 }
 
 __global__ void __launch_bounds__(kSortThreads) adapter_sort(const int* ids, int64_t T, int L, Order o) {
-  extern __shared__ uint16_t hist[];  // [kSortWarps][L + 1]: tokens of each adapter, then those before the warp's
-  __shared__ int first[kSortMaxL + 2], tile0[kSortMaxL + 2];
+  // [kSortWarps][L + 1]: tokens of each adapter, then those before the warp's; then the order itself
+  extern __shared__ uint16_t hist[];
+  __shared__ int first[kSortMaxL + 2], tile0[kSortMaxL + 2], block0[kSortMaxL + 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = L + 1;
+  uint16_t* perm = hist + kSortWarps * G;
   const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kSegment;
   for (int i = tid; i < kSortWarps * G; i += kSortThreads) hist[i] = 0;
   int key[kSortRounds], rank[kSortRounds];
@@ -552,66 +600,45 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const int* ids, int
       run += n[w];
     }
     first[k] = run;
-    tile0[k] = (run + kTileRows - 1) / kTileRows;
   }
   __syncthreads();
   if (warp == 0) {  // exclusive sums over the adapters
     const int per = (G + 31) / 32, k0 = lane * per, k1 = min(G, k0 + per);
-    int n = 0, m = 0;
-    for (int k = k0; k < k1; ++k) {
-      n += first[k];
-      m += tile0[k];
-    }
-    int pn = n, pm = m;
+    int n = 0;
+    for (int k = k0; k < k1; ++k) n += first[k];
+    int p = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int un = __shfl_up_sync(0xFFFFFFFFu, pn, d), um = __shfl_up_sync(0xFFFFFFFFu, pm, d);
-      if (lane >= d) {
-        pn += un;
-        pm += um;
-      }
+      const int up = __shfl_up_sync(0xFFFFFFFFu, p, d);
+      if (lane >= d) p += up;
     }
-    pn -= n;
-    pm -= m;
+    p -= n;
     for (int k = k0; k < k1; ++k) {
-      const int cn = first[k], cm = tile0[k];
-      first[k] = pn;
-      tile0[k] = pm;
-      pn += cn;
-      pm += cm;
+      const int c = first[k];
+      first[k] = p;
+      p += c;
     }
-    if (k0 < G && k1 == G) {
-      first[G] = pn;
-      tile0[G] = pm;
-    }
+    if (k0 < G && k1 == G) first[G] = p;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kSortRounds; ++i)
-    if (key[i] >= 0)
-      o.perm[s0 + first[key[i]] + mine[key[i]] + rank[i]] =
-          static_cast<int>(s0) + (warp * kSortRounds + i) * 32 + lane;
-  int* starts = o.starts + static_cast<int64_t>(blockIdx.x) * (L + 2);
-  for (int k = tid; k <= G; k += kSortThreads) starts[k] = static_cast<int>(s0) + first[k];
-  Tile* tiles = o.tiles + static_cast<int64_t>(blockIdx.x) * o.tiles_per_segment;
-  for (int i = tid; i < o.tiles_per_segment; i += kSortThreads) {
-    Tile t{-1, 0, 0, 0};
-    if (i < tile0[G]) {
-      int lo = 0, hi = G - 1;  // the last group whose first tile is at or before i
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (tile0[mid] <= i)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      const int at = (i - tile0[lo]) * kTileRows;
-      t.adapter = lo == L ? -1 : lo;
-      t.start = static_cast<int>(s0) + first[lo] + at;
-      t.count = min(kTileRows, first[lo + 1] - first[lo] - at);
+    if (key[i] >= 0) {
+      const int at = first[key[i]] + mine[key[i]] + rank[i], t = (warp * kSortRounds + i) * 32 + lane;
+      perm[at] = static_cast<uint16_t>(t);
+      o.perm[s0 + at] = static_cast<int>(s0) + t;
     }
-    tiles[i] = t;
-  }
+  if (warp == 0) group_pieces(first, tile0, G, kTileRows);
+  if (warp == 1) group_pieces(first, block0, G, kGradRows);
+  __syncthreads();
+  Tile* tiles = o.tiles + static_cast<int64_t>(blockIdx.x) * o.tiles_per_segment;
+  for (int i = tid; i < o.tiles_per_segment; i += kSortThreads)
+    tiles[i] = sorted_piece(first, tile0, perm, G, kTileRows, static_cast<int>(s0), i);
+  if (!o.blocks) return;
+  Tile* blocks = o.blocks + static_cast<int64_t>(blockIdx.x) * o.blocks_per_segment;
+  for (int i = tid; i < o.blocks_per_segment; i += kSortThreads)
+    blocks[i] = sorted_piece(first, block0, perm, G, kGradRows, static_cast<int>(s0), i);
+  for (int k = tid; k <= L; k += kSortThreads) o.starts[static_cast<int64_t>(blockIdx.x) * (L + 1) + k] = block0[k];
 }
 
 // ---------------------------------------------------------------------------
@@ -1177,7 +1204,6 @@ __global__ void __launch_bounds__(256) adapter_terms(const Terms p) {
   }
 }
 constexpr int kGradCols = 128;  // columns of a CTA
-constexpr int kGradRows = 64;   // tokens of a block
 
 // Eight 8-bit codes times 2^e as bf16 pairs (exact).
 __device__ __forceinline__ void codes_to_bf16(uint2 c, float s, bool e5m2, uint32_t (&w)[4]) {
@@ -1217,6 +1243,42 @@ struct GradTile {
   static_assert(kGradCols * kPitch * 4 <= kCtlAt, "the sums reuse the space before");
   static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
   static constexpr int kTmem = RP < 32 ? 32 : RP;
+};
+
+// An adapter's blocks of 64 tokens that fall to one CTA of a cluster of cs:
+// every cs-th of each segment's.  The entry after the current one is always
+// being loaded.
+struct BlockWalk {
+  const Order& o;
+  int L, a, rank, cs;
+  int seg = -1, at = 0, end = 0;
+  Tile now, ahead;
+  bool have = false;
+  __device__ __forceinline__ BlockWalk(const Order& o_, int L_, int a_, int rank_, int cs_)
+      : o(o_), L(L_), a(a_), rank(rank_), cs(cs_) {
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    at += cs;
+    while (at >= end) {
+      if (++seg >= o.segments) {
+        have = false;
+        return;
+      }
+      const int* s = o.starts + static_cast<int64_t>(seg) * (L + 1) + a;
+      at = s[0] + rank;
+      end = s[1];
+    }
+    const int4 v = *reinterpret_cast<const int4*>(o.blocks + static_cast<int64_t>(seg) * o.blocks_per_segment + at);
+    ahead = Tile{v.x, v.y, v.z, v.w};
+    have = true;
+  }
+  __device__ __forceinline__ bool next() {
+    if (!have) return false;
+    now = ahead;
+    fetch();
+    return true;
+  }
 };
 
 // A CTA's share of the sums of its cluster, times s[a], into the gradient.
@@ -1278,7 +1340,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
   const GradJob& j = p.job[second ? 1 : 0];
   const bool kept = j.x_scales != nullptr;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? p.job[0].tiles : 0)) * kGradCols;
-  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);  // cs: a power of two
+  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
   const int a = static_cast<int>(blockIdx.z);
 
   if (warp == 0) {
@@ -1296,38 +1358,18 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
   tc_fence_after();
   grid_dependency_wait();
 
-  // this CTA's blocks: number i of the adapter's blocks over all segments goes to rank i % cs
-  int seg = 0, pos = 0, end = 0, turn = 0;
-  auto enter = [&]() {  // the segment's range of this adapter
-    const int* s = p.o.starts + static_cast<int64_t>(seg) * (p.L + 2) + a;
-    pos = s[0];
-    end = s[1];
-  };
-  auto settle = [&]() -> bool {  // to the next block of this rank; false: none is left
-    while (true) {
-      while (pos >= end) {
-        if (++seg >= p.o.segments) return false;
-        enter();
-      }
-      if ((turn & (cs - 1)) == rank) return true;
-      ++turn;
-      pos += kGradRows;
-    }
-  };
-  enter();
-  bool more = settle();
+  BlockWalk walk(p.o, p.L, a, rank, cs);
+  bool more = walk.next();
   int found = 0;   // blocks whose tokens have been looked up
   int token = -1;  // of row tid (tid < 64) of the last of them
   int look_pos = 0, look_rows = 0;  // its place in the sorted order
   auto look = [&]() {
     if (!more) return;
-    if (tid < kGradRows) token = pos + tid < end ? p.o.perm[pos + tid] : -1;
-    look_pos = pos;
-    look_rows = min(kGradRows, end - pos);
+    look_pos = walk.now.start;
+    look_rows = walk.now.count;
+    if (tid < kGradRows) token = tid < look_rows ? p.o.perm[look_pos + tid] : -1;
     ++found;
-    ++turn;
-    pos += kGradRows;
-    more = settle();
+    more = walk.next();
   };
   auto put = [&](int b) {  // the tokens of block b for all
     if (tid < kGradRows) idx[(b % Cfg::kIdxSlots) * kGradRows + tid] = token;
@@ -1476,34 +1518,42 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
 // ---------------------------------------------------------------------------
 // The same three with TMA: rows that are 16-byte aligned
 // ---------------------------------------------------------------------------
-// One warp feeds the stages: each of its lanes gathers four rows with one
-// instruction (the tokens are sorted, not moved), already in the swizzled form
-// that the MMA reads; another warp's first lane issues the MMAs.  No other warp
-// touches the streamed operand on its way: with asynchronous copies by all
-// threads, several instructions for every 16 bytes, the gradients of 8192 tokens
-// x 8192 columns took 137 us, bound by instruction issue.
+// One warp feeds the stages, in the swizzled form that the MMA reads; another
+// warp's first lane issues the MMAs.  Where a tile's tokens are consecutive, as
+// those of a long request are, TMA loads its rows at once; else helper warps
+// gather them by asynchronous copies that arrive on the stage's barrier
+// themselves.  (TMA's own gather of four rows takes about 49 cycles for 512
+// bytes: a quarter of what an SM needs, and slower than the copies.)  The
+// threads that copy then are few and do nothing else: with all threads copying
+// between barriers the gradients of 8192 tokens x 8192 columns took 137 us,
+// bound by instruction issue.
 //
 // Weights come by TMA too where their rows are 16-byte aligned, else
-// (wtma = 0: ranks that are no multiple of 8) two warps stage them.
-struct Gather {
-  int4 r;
-  // rows pos + 4 i .. of the order, those from `count` on repeating the last one
-  __device__ __forceinline__ Gather(const int* perm, int start, int count, int i) {
-    r.x = perm[start + min(4 * i, count - 1)];
-    r.y = perm[start + min(4 * i + 1, count - 1)];
-    r.z = perm[start + min(4 * i + 2, count - 1)];
-    r.w = perm[start + min(4 * i + 3, count - 1)];
-  }
-};
+// (wtma = 0: ranks that are no multiple of 8) the helpers stage them.
 
-// Two warps (64 threads, i their number) stage rows of the weights that TMA
+// Arrives on `bar` when this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// A 16-byte piece of a row from column c (16-byte aligned), zeros where !in or
+// past `limit`.
+template <typename E>
+__device__ __forceinline__ void gather16(uint32_t dst, const E* row, int64_t c, int64_t limit, bool in) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(E));
+  const int64_t left = in ? limit - c : 0;
+  const int bytes = left >= kPer ? 16 : (left > 0 ? static_cast<int>(left) * static_cast<int>(sizeof(E)) : 0);
+  copy_async<16>(dst, bytes > 0 ? row + c : row, bytes);
+}
+
+// `threads` helpers (i: this one's number) stage rows of the weights that TMA
 // cannot: rows of R elements (64 of them, from row k) or R rows of 64 columns
 // (from column k); zeros past the array and past R.
 template <int RP, bool ROWS_OF_R>
-__device__ __forceinline__ void stage_weights(uint32_t at, const bf16* w, int64_t k, int64_t C, int R, int i) {
+__device__ __forceinline__ void stage_weights(uint32_t at, const bf16* w, int64_t k, int64_t C, int R, int i,
+                                              int threads) {
   using W = Staged<ROWS_OF_R ? kChunk : RP, ROWS_OF_R ? RP : kChunk>;
   constexpr int kPieces = (ROWS_OF_R ? RP : kChunk) / 8, kRows = ROWS_OF_R ? kChunk : RP;
-  for (int e = i; e < kRows * kPieces; e += 64) {
+  for (int e = i; e < kRows * kPieces; e += threads) {
     const int r = e / kPieces, piece = e % kPieces;
     uint32_t v[4];
     if constexpr (ROWS_OF_R)
@@ -1539,7 +1589,7 @@ struct DownTma : DownTile<RP, TRANS> {
   static constexpr int kSmem = Base::kRing + static_cast<int>(sizeof(Ctl));
 };
 struct DownTmaArgs {
-  CUtensorMap x, wm;
+  CUtensorMap x, wm;  // 128 rows by 64 columns; the weights
   Down d;
   Order o;
   Waits w;
@@ -1547,32 +1597,33 @@ struct DownTmaArgs {
 };
 
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(128) adapter_down_tma(const __grid_constant__ DownTmaArgs ps) {
+__global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ DownTmaArgs ps) {
   using Cfg = DownTma<RP, TRANS>;
-  constexpr int S = Cfg::kStages;
+  constexpr int S = Cfg::kStages, kHelpers = 128;
   extern __shared__ __align__(1024) uint8_t ring[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
   const Down& p = ps.d;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
   const uint32_t ring_at = smem_u32(ring);
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&ctl.full[i], ps.wtma ? 1 : 1 + 64);
-      mbar_init(&ctl.empty[i], 1);
-    }
-    mbar_init(&ctl.done, 1);
-    ctl.abort_flag = 0;
-    fence_barrier_init();
-  }
   grid_dependency_wait();
   grid_launch_dependents();
   const Tile tile = ps.o.tiles[blockIdx.x];
   if (tile.count == 0) return;  // the whole cluster
   if (tile.adapter < 0) {
-    for (int i = rank * 128 + tid; i < tile.count * p.R; i += cs * 128)
+    for (int i = rank * 192 + tid; i < tile.count * p.R; i += cs * 192)
       p.u[static_cast<int64_t>(ps.o.perm[tile.start + i / p.R]) * p.R + i % p.R] = 0.f;
     return;
+  }
+  const bool run = tile.run != 0;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&ctl.full[i], 1 + (run ? 0 : kHelpers) + (ps.wtma ? 0 : kHelpers));
+      mbar_init(&ctl.empty[i], 1);
+    }
+    mbar_init(&ctl.done, 1);
+    ctl.abort_flag = 0;
+    fence_barrier_init();
   }
   if (warp == 1) {
     tmem_alloc(&ctl.tmem, Cfg::kTmem);
@@ -1586,28 +1637,30 @@ __global__ void __launch_bounds__(128) adapter_down_tma(const __grid_constant__ 
   const int64_t c_begin = chunks * rank / cs, c_end = chunks * (rank + 1) / cs;
   const int n = static_cast<int>(c_end - c_begin);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteDown);
+    return mbar_poll(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteDown);
   };
   int c = 0;
   if (warp == 0) {
-    const Gather g(ps.o.perm, tile.start, tile.count, lane);
-    for (; c < n; ++c) {
-      const int st = c % S;
-      if (c >= S && !wait(&ctl.empty[st], c / S - 1)) break;
-      const uint32_t at = ring_at + st * Cfg::kStageBytes;
-      const int64_t k = (c_begin + c) * kChunk;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&ctl.full[st], Cfg::kXBytes + (ps.wtma ? Cfg::kWBytes : 0));
+    const int first = ps.o.perm[tile.start];
+    if (lane == 0) {
+      for (; c < n; ++c) {
+        const int st = c % S;
+        if (c >= S && !wait(&ctl.empty[st], c / S - 1)) break;
+        const uint32_t at = ring_at + st * Cfg::kStageBytes;
+        const int64_t k = (c_begin + c) * kChunk;
+        mbar_arrive_expect_tx(&ctl.full[st], (run ? Cfg::kXBytes : 0) + (ps.wtma ? Cfg::kWBytes : 0));
+        // rows past the tile are another adapter's, or zeros: not stored
+        if (run) tma_load_2d(at, &ps.x, &ctl.full[st], static_cast<int>(k), first);
         if (ps.wtma) load_weights<RP, TRANS>(at + Cfg::kXBytes, &ps.wm, &ctl.full[st], k, tile.adapter, ring);
       }
-      __syncwarp();
-      tma_gather4(at + lane * 512, &ps.x, &ctl.full[st], static_cast<int>(k), g.r);
     }
+    __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       for (; c < n; ++c) {
         const int st = c % S;
         if (!wait(&ctl.full[st], c / S)) break;
+        fence_proxy_async_smem();  // what the helpers' copies wrote
         tc_fence_after();
         const uint32_t at = ring_at + st * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
 #pragma unroll
@@ -1619,16 +1672,32 @@ __global__ void __launch_bounds__(128) adapter_down_tma(const __grid_constant__ 
       tc_commit(&ctl.done);
     }
     __syncwarp();
-  } else if (!ps.wtma) {
+  } else if (!run || !ps.wtma) {
+    const int i = tid - 64;
     const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
+    const bf16* xr[8];  // piece i % 8 of rows i / 8 + 16 j; rows past the tile repeat its last one
+#pragma unroll
+    for (int j = 0; j < 8; ++j) xr[j] = p.x + ps.o.perm[tile.start + min((i >> 3) + 16 * j, tile.count - 1)] * p.ld;
     for (; c < n; ++c) {
       const int st = c % S;
       if (c >= S && !wait(&ctl.empty[st], c / S - 1)) break;
-      stage_weights<RP, TRANS>(ring_at + st * Cfg::kStageBytes + Cfg::kXBytes, w, (c_begin + c) * kChunk, p.C, p.R,
-                               tid - 64);
-      mbar_arrive(&ctl.full[st]);
+      const uint32_t at = ring_at + st * Cfg::kStageBytes;
+      const int64_t k = (c_begin + c) * kChunk;
+      if (!run) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          gather16(at + Cfg::X::at((i >> 3) + 16 * j, i & 7), xr[j], k + (i & 7) * 8, p.C, true);
+        copy_arrive(&ctl.full[st]);
+      }
+      if (!ps.wtma) {
+        stage_weights<RP, TRANS>(at + Cfg::kXBytes, w, k, p.C, p.R, i, kHelpers);
+        mbar_arrive(&ctl.full[st]);
+      }
     }
+    copy_commit();
+    copy_wait<0>();
   }
+  c = __shfl_sync(0xFFFFFFFFu, c, 0);
   __syncthreads();
   wait(&ctl.done, 0);
   if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies in flight, bounded again
@@ -1639,12 +1708,13 @@ __global__ void __launch_bounds__(128) adapter_down_tma(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   float* sums = reinterpret_cast<float*>(ring);  // [kTileRows][kPitch]
-  {
-    float* dst = sums + tid * Cfg::kPitch;
+  if (warp >= 2) {
+    const int q = warp & 3;  // the quarter of tensor memory that this warp can read
+    float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
     for (int j = 0; j < RP; j += 16) {
       uint32_t v[16];
-      tmem_ld16(tmem + (warp * 32u << 16) + j, v);
+      tmem_ld16(tmem + (q * 32u << 16) + j, v);
       tmem_wait_ld();
 #pragma unroll
       for (int e = 0; e < 16; e += 4)
@@ -1660,7 +1730,7 @@ __global__ void __launch_bounds__(128) adapter_down_tma(const __grid_constant__ 
   }
   const int total = tile.count * p.R, share = (total + cs - 1) / cs;
   const int e_end = min(total, (rank + 1) * share);
-  for (int e = rank * share + tid; e < e_end; e += 128) {
+  for (int e = rank * share + tid; e < e_end; e += 192) {
     const int r = e / p.R, col = e - r * p.R;
     float v = 0.f;
     if (cs > 1) {
@@ -1687,7 +1757,7 @@ struct UpTma : UpTile<RP, Y, TRANS> {
   static constexpr int kSmem = Base::kCtlAt + static_cast<int>(sizeof(Ctl));
 };
 struct UpTmaArgs {
-  CUtensorMap y, out, wm;
+  CUtensorMap y, out, wm;  // base by 128 rows, out by 32, of 128 bytes each; the weights
   Up d;
   Order o;
   Waits w;
@@ -1696,10 +1766,9 @@ struct UpTmaArgs {
 };
 
 // Warp 0 feeds base and the weights, warp 1 issues the MMAs, warps 2 and 3
-// stage weights that TMA cannot; warps 4..7 own 32 rows each: they add the
-// product to base in place in its stage, from which four rows to an instruction
-// scatter to out.  Rows past a tile's tokens repeat its last one, in base and in
-// u, so that they write its row again with the same values.
+// are the helpers; warps 4..7 own 32 rows each: they add the product to base in
+// place in its stage, and from there write 32 consecutive rows with one TMA
+// store, other rows in whole 128-byte pieces.
 template <int RP, typename Y, bool TRANS>
 __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ UpTmaArgs ps) {
   using Cfg = UpTma<RP, Y, TRANS>;
@@ -1719,13 +1788,15 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
   const int n = static_cast<int>(min(static_cast<int64_t>(ps.chunks_per_cta), chunks - c_begin));
   const bool plain = tile.adapter < 0;  // no product: out = base
   const bool has_base = p.base != nullptr;
+  const bool run = tile.run != 0;
+  constexpr int kHelpers = 64;
   if (tid == 0) {
     for (int i = 0; i < WS; ++i) {
-      mbar_init(&ctl.wfull[i], ps.wtma ? 1 : 64);
+      mbar_init(&ctl.wfull[i], ps.wtma ? 1 : kHelpers);
       mbar_init(&ctl.wempty[i], 1);
     }
     for (int i = 0; i < YS; ++i) {
-      mbar_init(&ctl.yfull[i], 1);
+      mbar_init(&ctl.yfull[i], run || !has_base ? 1 : kHelpers);
       mbar_init(&ctl.yempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1745,34 +1816,35 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteUp);
+    return mbar_poll(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteUp);
   };
-  int c = 0;  // of the producer: chunks begun
+  int c = 0;  // chunks begun
   if (warp == 0) {
-    const Gather g(ps.o.perm, tile.start, tile.count, lane);
-    for (; c < n; ++c) {
-      const int64_t k = (c_begin + c) * kChunk;
-      if (!plain && ps.wtma) {
-        const int st = c % WS;
-        if (c >= WS && !wait(&ctl.wempty[st], c / WS - 1)) break;
-        if (lane == 0) {
+    const int first = ps.o.perm[tile.start];
+    if (lane == 0) {
+      for (; c < n; ++c) {
+        const int64_t k = (c_begin + c) * kChunk;
+        if (!plain && ps.wtma) {
+          const int st = c % WS;
+          if (c >= WS && !wait(&ctl.wempty[st], c / WS - 1)) break;
           mbar_arrive_expect_tx(&ctl.wfull[st], Cfg::kWBytes);
           load_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, &ps.wm, &ctl.wfull[st], k, tile.adapter, smem);
         }
-      }
-      const int st = c % YS;
-      if (c >= YS && !wait(&ctl.yempty[st], c / YS - 1)) break;
-      if (!has_base) {
-        if (lane == 0) mbar_arrive(&ctl.yfull[st]);
-        continue;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&ctl.yfull[st], Cfg::kYBytes);
-      __syncwarp();
+        if (!run && has_base) continue;  // the helpers' part
+        const int st = c % YS;
+        if (c >= YS && !wait(&ctl.yempty[st], c / YS - 1)) break;
+        if (!has_base) {
+          mbar_arrive(&ctl.yfull[st]);
+          continue;
+        }
+        mbar_arrive_expect_tx(&ctl.yfull[st], Cfg::kYBytes);
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-        tma_gather4(y_at + st * Cfg::kYBytes + b * (kTileRows * 128) + lane * 512, &ps.y, &ctl.yfull[st],
-                    static_cast<int>(k) + b * kBlockCols, g.r);
+        for (int b = 0; b < kBlocks; ++b)  // rows past the tile are not written
+          tma_load_2d(y_at + st * Cfg::kYBytes + b * (kTileRows * 128), &ps.y, &ctl.yfull[st],
+                      static_cast<int>(k) + b * kBlockCols, first);
+      }
     }
+    __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && !plain && wait(&ctl.ufull, 0)) {
       for (int m = 0; m < n; ++m) {
@@ -1794,35 +1866,86 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
     }
     __syncwarp();
   } else if (warp < 4) {
-    if (!plain && !ps.wtma) {
-      const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
+    const int i = tid - 64;
+    const bool weights = !plain && !ps.wtma, rows = !run && has_base;
+    if (weights || rows) {
+      const bf16* w = p.w + static_cast<int64_t>(plain ? 0 : tile.adapter) * p.R * p.C;
+      const Y* base = static_cast<const Y*>(p.base);
+      int at_row[16];  // piece i % 8 of rows i / 8 + 8 j
+#pragma unroll
+      for (int j = 0; j < 16; ++j) at_row[j] = ps.o.perm[tile.start + min((i >> 3) + 8 * j, tile.count - 1)];
       for (int m = 0; m < n; ++m) {
-        const int st = m % WS;
-        if (m >= WS && !wait(&ctl.wempty[st], m / WS - 1)) break;
-        stage_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, w, (c_begin + m) * kChunk, p.C, p.R, tid - 64);
-        mbar_arrive(&ctl.wfull[st]);
+        const int64_t k = (c_begin + m) * kChunk;
+        if (weights) {
+          const int st = m % WS;
+          if (m >= WS && !wait(&ctl.wempty[st], m / WS - 1)) break;
+          stage_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, w, k, p.C, p.R, i, kHelpers);
+          mbar_arrive(&ctl.wfull[st]);
+        }
+        if (rows) {
+          const int st = m % YS;
+          if (m >= YS && !wait(&ctl.yempty[st], m / YS - 1)) break;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int r = (i >> 3) + 8 * j;
+              gather16(y_at + st * Cfg::kYBytes + b * (kTileRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) * 16),
+                       base + at_row[j] * p.ld_base, k + b * kBlockCols + (i & 7) * (kBlockCols / 8), p.C, r < tile.count);
+            }
+          copy_arrive(&ctl.yfull[st]);
+        }
       }
+      copy_commit();
+      copy_wait<0>();
     }
   } else {
     const int q = warp - 4, row = q * 32 + lane;  // this thread's row of the tile, and its lane of tensor memory
     const int64_t token = ps.o.perm[tile.start + min(row, tile.count - 1)];
-    const Gather g(ps.o.perm, tile.start, tile.count, q * 8 + (lane & 7));
+    const bool whole = run && q * 32 + 32 <= tile.count;  // 32 consecutive rows
+    const int row0 = __shfl_sync(0xFFFFFFFFu, static_cast<int>(token), 0);
+    int to[8];  // else: rows lane / 8 + 4 i, -1 past the tile
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = q * 32 + (lane >> 3) + 4 * i;
+      to[i] = r < tile.count ? ps.o.perm[tile.start + r] : -1;
+    }
+    Y* out = static_cast<Y*>(p.out);
     const float sc = plain ? 0.f : (p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f);
     grid_dependency_wait();  // u is the launch before this one's
     if (!plain) {
       const float* src = p.u + token * p.R;
+      const bool vec = p.R % 4 == 0 && (reinterpret_cast<uintptr_t>(p.u) & 15u) == 0;
+      constexpr int kAtOnce = RP / 8 < 4 ? RP / 8 : 4;  // pieces of 8 ranks loaded before any is split
 #pragma unroll 1
-      for (int pr = 0; pr < RP / 8; ++pr) {
-        uint32_t t[4][TERMS];
+      for (int p0 = 0; p0 < RP / 8; p0 += kAtOnce) {
+        float v[kAtOnce][8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = pr * 8 + 2 * e;
-          split_pair<TERMS>(r < p.R ? src[r] : 0.f, r + 1 < p.R ? src[r + 1] : 0.f, t[e]);
-        }
+        for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k) {
-          const uint32_t v[4] = {t[0][k], t[1][k], t[2][k], t[3][k]};
-          st_shared16(u_at + k * Cfg::U::kBytes + Cfg::U::at(row, pr), v);
+          for (int h = 0; h < 2; ++h) {
+            const int r = (p0 + i) * 8 + 4 * h;
+            if (vec) {
+              const float4 f = r < p.R ? *reinterpret_cast<const float4*>(src + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+              v[i][4 * h] = f.x;
+              v[i][4 * h + 1] = f.y;
+              v[i][4 * h + 2] = f.z;
+              v[i][4 * h + 3] = f.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[i][4 * h + e] = r + e < p.R ? src[r + e] : 0.f;
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          uint32_t t[4][TERMS];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_pair<TERMS>(v[i][2 * e], v[i][2 * e + 1], t[e]);
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            const uint32_t w[4] = {t[0][k], t[1][k], t[2][k], t[3][k]};
+            st_shared16(u_at + k * Cfg::U::kBytes + Cfg::U::at(row, p0 + i), w);
+          }
         }
       }
       fence_proxy_async_smem();
@@ -1833,7 +1956,6 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
     for (; m < n && ok; ++m) {
       const int st = m % YS;
       const uint32_t at = y_at + st * Cfg::kYBytes;
-      // (with no base, the stage must not be being scattered still: the producer has seen it empty)
       ok = wait(&ctl.yfull[st], m / YS) && (plain || wait(&ctl.dfull[m & 1], m >> 1));
       if (!plain || !has_base) {
         tc_fence_after();
@@ -1866,18 +1988,39 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
           }
         }
         tc_fence_before();
-        fence_proxy_async_smem();
       }
+      fence_proxy_async_smem();  // before a TMA store reads the stage
       __syncwarp();
       if (!plain && lane == 0) mbar_arrive(&ctl.dempty[m & 1]);
       const int64_t k = (c_begin + m) * kChunk;
-      if (lane < 8 * kBlocks && k + (lane / 8) * kBlockCols < p.C)
-        tma_scatter4(&ps.out, at + (lane / 8) * (kTileRows * 128) + q * 4096 + (lane & 7) * 512,
-                     static_cast<int>(k) + (lane / 8) * kBlockCols, g.r);
-      bulk_commit();
-      bulk_wait_read<1>();  // the chunk before has left its stage
-      __syncwarp();
-      if (m > 0 && lane == 0) mbar_arrive(&ctl.yempty[(m - 1) % YS]);
+      if (whole) {
+        if (lane < kBlocks && k + lane * kBlockCols < p.C)
+          tma_store_2d(&ps.out, at + lane * (kTileRows * 128) + q * 4096, static_cast<int>(k) + lane * kBlockCols, row0);
+        bulk_commit();
+        bulk_wait_read<1>();  // the chunk before has left its stage
+        __syncwarp();
+        if (m > 0 && lane == 0) mbar_arrive(&ctl.yempty[(m - 1) % YS]);
+      } else {
+        constexpr int kPer = 16 / static_cast<int>(sizeof(Y));
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          const int64_t col = k + b * kBlockCols + (lane & 7) * kPer;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = q * 32 + (lane >> 3) + 4 * i;
+            const uint4 v = ld_shared16(at + b * (kTileRows * 128) + r * 128 + (((lane & 7) ^ (r & 7)) * 16));
+            if (to[i] < 0 || col >= p.C) continue;
+            Y* dst = out + to[i] * p.ld_out;
+            if (col + kPer <= p.C)
+              *reinterpret_cast<uint4*>(dst + col) = v;
+            else
+              write_piece<Y>(dst, col, p.C, v);
+          }
+        }
+        fence_proxy_async_smem();  // the stage may be TMA's next
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.yempty[st]);
+      }
     }
     bulk_wait<0>();
   }
@@ -1886,7 +2029,7 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
     int never = 0;
     for (int j = c > WS ? c - WS : 0; j < c && !plain && ps.wtma; ++j)
       mbar_wait(&ctl.wfull[j % WS], static_cast<uint32_t>(j / WS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
-    for (int j = c > YS ? c - YS : 0; j < c; ++j)
+    for (int j = c > YS ? c - YS : 0; j < c && run && has_base; ++j)
       mbar_wait(&ctl.yfull[j % YS], static_cast<uint32_t>(j / YS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
   }
   tc_fence_before();
@@ -1899,8 +2042,8 @@ struct GradTma : GradTile<RP, TERMS> {
   using Base = GradTile<RP, TERMS>;
   static constexpr int kStages = Base::kStages;
   static constexpr int kStageBf16 = Base::kXBytes + Base::kCoefBytes;
-  static constexpr int kCodeBytes = kGradRows * kGradCols;
-  static constexpr int kStageCodes = kCodeBytes + Base::kCoefBytes;
+  static constexpr int kCodeBytes = kGradRows * kGradCols, kScaleBytes = 1024;  // (a row's four scale bytes: 256, padded)
+  static constexpr int kStageCodes = kCodeBytes + kScaleBytes + Base::kCoefBytes;
   // codes: two decoded blocks before the ring
   static constexpr int kBf16 = kStages * kStageBf16, kCodes = 2 * Base::kXBytes + kStages * kStageCodes;
   static constexpr int kRing = kBf16 > kCodes ? kBf16 : kCodes;
@@ -1913,40 +2056,17 @@ struct GradTma : GradTile<RP, TERMS> {
   static constexpr int kSmem = kRing + static_cast<int>(sizeof(Ctl));
 };
 struct GradTmaArgs {
-  CUtensorMap x[2];       // of the jobs: rows gathered (bf16 64 columns, codes 128)
-  CUtensorMap block, row; // the coefficients [2 T][TERMS RP]: 64 rows, and rows gathered
+  CUtensorMap x[2];   // of the jobs: 64 rows (bf16 64 columns, codes 128)
+  CUtensorMap coef;   // the coefficients [2 T][TERMS RP], 64 rows
   Grads g;
   int64_t T;
 };
 
-// An adapter's blocks of 64 tokens that fall to one CTA of a cluster of cs (a
-// power of two): number i over all segments goes to rank i % cs.
-struct BlockWalk {
-  const Order& o;
-  int L, a, rank, cs;
-  int seg = -1, at = 0, end = 0, turn = 0;
-  int pos = 0, rows = 0;  // the current block
-  __device__ __forceinline__ BlockWalk(const Order& o_, int L_, int a_, int rank_, int cs_)
-      : o(o_), L(L_), a(a_), rank(rank_), cs(cs_) {}
-  __device__ __forceinline__ bool next() {
-    while (true) {
-      while (at >= end) {
-        if (++seg >= o.segments) return false;
-        const int* s = o.starts + static_cast<int64_t>(seg) * (L + 2) + a;
-        at = s[0];
-        end = s[1];
-      }
-      pos = at;
-      rows = min(kGradRows, end - at);
-      at += kGradRows;
-      if ((turn++ & (cs - 1)) == rank) return true;
-    }
-  }
-};
-
-// Warp 0 feeds x and the coefficients, warp 1 issues the MMAs; where x is a
-// checkpoint, warps 2..5 decode its codes between the two.  They also read the
-// sums out of tensor memory at the end.
+// Warp 0 feeds x and the coefficients, warp 1 issues the MMAs; warps 2..5
+// gather the blocks that are not 64 consecutive tokens (with their
+// coefficients, zeros past the adapter's last token) and, where x is a
+// checkpoint, decode its codes between the two.  They also read the sums out
+// of tensor memory at the end.
 template <int RP, int TERMS, typename G>
 __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
   using Cfg = GradTma<RP, TERMS>;
@@ -1964,10 +2084,10 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
   const int a = static_cast<int>(blockIdx.z);
   const uint32_t ring_at = smem_u32(ring) + (kept ? 2 * Cfg::kXBytes : 0);
   const uint32_t stage_bytes = kept ? Cfg::kStageCodes : Cfg::kStageBf16;
-  const uint32_t coef_off = kept ? Cfg::kCodeBytes : Cfg::kXBytes;
+  const uint32_t coef_off = kept ? Cfg::kCodeBytes + Cfg::kScaleBytes : Cfg::kXBytes;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.full[i], 1 + 128);
       mbar_init(&ctl.empty[i], 1);
     }
     mbar_init(&ctl.decoded[0], 128);
@@ -1986,53 +2106,41 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
   const uint32_t tmem = ctl.tmem;
   grid_dependency_wait();
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait(bar, parity & 1u, p.w.timeout_ns, &ctl.abort_flag, p.w.status, kSiteGrads);
+    return mbar_poll(bar, parity & 1u, p.w.timeout_ns, &ctl.abort_flag, p.w.status, kSiteGrads);
   };
-  BlockWalk walk(p.o, p.L, a, rank, cs);
   int b = 0;
+  constexpr int kCoefBlocks = RP / Coef::kE, kCoefLoads = TERMS * kCoefBlocks;
   if (warp == 0) {
     const int T = static_cast<int>(ps.T);
-    // lane: four rows of x (bf16: of one of the two 64-column halves); rows past the block are past the array: zeros
-    const int group = kept ? lane & 15 : lane >> 1;
-    auto token = [&](int r) { return r < walk.rows ? p.o.perm[walk.pos + r] : T; };
-    bool more = walk.next();
-    int4 rows = make_int4(0, 0, 0, 0);
-    if (more) rows = make_int4(token(4 * group), token(4 * group + 1), token(4 * group + 2), token(4 * group + 3));
-    while (more) {
-      const int st = b % S;
-      if (b >= S && !wait(&ctl.empty[st], b / S - 1)) break;
-      const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
-      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], stage_bytes);
-      __syncwarp();
-      if (!kept)
-        tma_gather4(at + (lane & 1) * (kGradRows * 128) + group * 512, &ps.x[second], &ctl.full[st],
-                    static_cast<int>(c0) + (lane & 1) * 64, rows);
-      else if (lane < 16)
-        tma_gather4(at + group * 512, &ps.x[second], &ctl.full[st], static_cast<int>(c0), rows);
-      constexpr int kCoefBlocks = RP / Coef::kE;
-      const int row0 = second * T + walk.pos;
-      if (walk.rows == kGradRows) {
-        if (lane < TERMS * kCoefBlocks)
-          tma_load_2d(ct + (lane / kCoefBlocks) * Cfg::kTermBytes + (lane % kCoefBlocks) * Coef::kBlock, &ps.block,
-                      &ctl.full[st], lane * Coef::kE, row0);
-      } else {
-        for (int i = lane; i < TERMS * kCoefBlocks * (kGradRows / 4); i += 32) {
-          const int g4 = i % (kGradRows / 4), k = i / (kGradRows / 4);
-          auto at4 = [&](int e) { return 4 * g4 + e < walk.rows ? row0 + 4 * g4 + e : 2 * T; };
-          tma_gather4(ct + (k / kCoefBlocks) * Cfg::kTermBytes + (k % kCoefBlocks) * Coef::kBlock + g4 * 4 * Coef::kWidth,
-                      &ps.row, &ctl.full[st], k * Coef::kE, make_int4(at4(0), at4(1), at4(2), at4(3)));
+    if (lane == 0) {
+      BlockWalk walk(p.o, p.L, a, rank, cs);
+      while (walk.next()) {
+        const int st = b % S;
+        const bool run = walk.now.run && walk.now.count == kGradRows;
+        const int first = run ? p.o.perm[walk.now.start] : 0, row0 = second * T + walk.now.start;
+        if (b >= S && !wait(&ctl.empty[st], b / S - 1)) break;
+        const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
+        mbar_arrive_expect_tx(&ctl.full[st], run ? (kept ? Cfg::kCodeBytes : Cfg::kXBytes) + Cfg::kCoefBytes : 0);
+        if (run) {
+          tma_load_2d(at, &ps.x[second], &ctl.full[st], static_cast<int>(c0), first);
+          if (!kept) tma_load_2d(at + kGradRows * 128, &ps.x[second], &ctl.full[st], static_cast<int>(c0) + 64, first);
+#pragma unroll
+          for (int k = 0; k < kCoefLoads; ++k)
+            tma_load_2d(ct + (k / kCoefBlocks) * Cfg::kTermBytes + (k % kCoefBlocks) * Coef::kBlock, &ps.coef, &ctl.full[st],
+                        k * Coef::kE, row0);
         }
+        ++b;
       }
-      ++b;
-      more = walk.next();
-      if (more) rows = make_int4(token(4 * group), token(4 * group + 1), token(4 * group + 2), token(4 * group + 3));
     }
+    b = __shfl_sync(0xFFFFFFFFu, b, 0);
   } else if (warp == 1) {
     if (lane == 0) {
+      BlockWalk walk(p.o, p.L, a, rank, cs);
       while (walk.next()) {
         const int st = b % S;
         if (!wait(&ctl.full[st], b / S)) break;
         if (kept && !wait(&ctl.decoded[b & 1], b >> 1)) break;
+        fence_proxy_async_smem();  // what the helpers' copies wrote
         tc_fence_after();
         const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
         const uint32_t xt = kept ? smem_u32(ring) + (b & 1) * Cfg::kXBytes : at;
@@ -2048,50 +2156,100 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
       tc_commit(&ctl.done);
     }
     b = __shfl_sync(0xFFFFFFFFu, b, 0);
-  } else if (kept) {
-    // thread: rows (tid - 64) / 4 and 32 further, the 32 codes of block (tid - 64) % 4
-    const int r0 = (tid - 64) >> 2, blk = (tid - 64) & 3;
+  } else {
+    // The helpers run D blocks ahead with what they copy; a checkpoint's codes
+    // are decoded by the thread that copied them: rows i / 4 and 32 further,
+    // the 32 codes of block i % 4.
+    constexpr int D = S - 1;
+    const int i = tid - 64, r0 = i >> 2, blk = i & 3;
     const int64_t nb = j.C / 32;
-    const bool in = c0 / 32 + blk < nb;
-    auto scale = [&](int r) -> uint32_t {
-      return in && r < walk.rows ? __ldg(j.x_scales + static_cast<int64_t>(p.o.perm[walk.pos + r]) * nb + c0 / 32 + blk) : 127u;
-    };
-    bool more = walk.next();
-    uint32_t s0 = 127u, s1 = 127u;
-    if (more) {
-      s0 = scale(r0);
-      s1 = scale(r0 + 32);
-    }
-    while (more) {
-      const int st = b % S;
-      const uint32_t f0 = s0, f1 = s1;
-      more = walk.next();
-      if (more) {
-        s0 = scale(r0);
-        s1 = scale(r0 + 32);
-      }
-      if (!wait(&ctl.full[st], b / S)) break;
-      if (b >= 2 && !wait(&ctl.empty[(b - 2) % S], (b - 2) / S)) break;  // the MMAs have read this half
-      const uint32_t src = ring_at + st * stage_bytes, dst = smem_u32(ring) + (b & 1) * Cfg::kXBytes;
+    const bf16* coef = j.coef;
+    BlockWalk walk(p.o, p.L, a, rank, cs);
+    auto copy = [&](int d) {  // block d, where the walk is
+      const int st = d % S;
+      const Tile& w = walk.now;
+      const bool run = w.run && w.count == kGradRows;
+      const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
+      if (!run) {
+        if (!kept) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = r0 + 32 * h;
-        const uint32_t sb = h ? f1 : f0;
-        const float s = __uint_as_float(sb == 0u ? 0x00400000u : (sb == 255u ? 0x7FFFFFFFu : sb << 23));
+          for (int e = 0; e < 8; ++e) {
+            const int r = (i >> 4) + 8 * e, piece = i & 15;
+            const bool in = r < w.count;
+            const int64_t t = p.o.perm[w.start + (in ? r : 0)];
+            gather16(at + Cfg::X::at(r, piece), static_cast<const bf16*>(j.x) + t * j.ld, c0 + piece * 8, j.C, in);
+          }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 c = ld_shared16(src + r * 128 + (((blk * 2 + i) ^ (r & 7)) * 16));
-          uint32_t w[4];
-          codes_to_bf16(make_uint2(c.x, c.y), s, p.e5m2 != 0, w);
-          st_shared16(dst + Cfg::X::at(r, blk * 4 + i * 2), w);
-          codes_to_bf16(make_uint2(c.z, c.w), s, p.e5m2 != 0, w);
-          st_shared16(dst + Cfg::X::at(r, blk * 4 + i * 2 + 1), w);
+          for (int e = 0; e < 4; ++e) {
+            const int r = r0 + 32 * (e >> 1), piece = blk * 2 + (e & 1);
+            const bool in = r < w.count;
+            const int64_t t = p.o.perm[w.start + (in ? r : 0)];
+            gather16(at + r * 128 + ((piece ^ (r & 7)) * 16), static_cast<const uint8_t*>(j.x) + t * j.ld, c0 + piece * 16,
+                     j.C, in);
+          }
+        }
+        for (int e = i; e < kGradRows * TERMS * (RP / 8); e += 128) {
+          const int r = e / (TERMS * (RP / 8)), k = e % (TERMS * (RP / 8));
+          const bool in = r < w.count;
+          gather16(ct + (k / (RP / 8)) * Cfg::kTermBytes + Coef::at(r, k % (RP / 8)),
+                   coef + (static_cast<int64_t>(w.start) + (in ? r : 0)) * (TERMS * RP), k * 8, TERMS * RP, in);
         }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&ctl.decoded[b & 1]);
-      ++b;
+      if (kept && i < kGradRows) {  // row i's scale bytes of the tile's blocks
+        const bool in = i < w.count;
+        const uint8_t* sb = j.x_scales + (in ? static_cast<int64_t>(p.o.perm[w.start + i]) * nb + c0 / 32 : 0);
+        const uint32_t dst = at + Cfg::kCodeBytes + i * 4;
+        if (p.scale4) {
+          copy_async<4>(dst, sb, in ? 4 : 0);
+        } else {
+          uint32_t v = 0u;
+          for (int k = 0; k < 4 && in && c0 / 32 + k < nb; ++k) v |= static_cast<uint32_t>(__ldg(sb + k)) << (8 * k);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+        }
+      }
+      copy_arrive(&ctl.full[st]);
+    };
+    int d = 0;  // blocks copied
+    bool more = true, ok = true;
+    auto step = [&]() {
+      if (!more || !(more = walk.next())) return;
+      ok = d < S || wait(&ctl.empty[d % S], d / S - 1);
+      if (ok) copy(d++);
+    };
+    if (!kept) {
+      while (more && ok) step();
+    } else {
+      while (ok && more && d < D) step();
+      for (; b < d && ok; ++b) {
+        const int st = b % S;
+        ok = wait(&ctl.full[st], b / S) && (b < 2 || wait(&ctl.empty[(b - 2) % S], (b - 2) / S));
+        if (!ok) break;  // (the second: the MMAs have read this half of the decoded blocks)
+        const uint32_t src = ring_at + st * stage_bytes, dst = smem_u32(ring) + (b & 1) * Cfg::kXBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = r0 + 32 * h;
+          uint32_t sw;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw) : "r"(src + Cfg::kCodeBytes + r * 4) : "memory");
+          const uint32_t sb = (sw >> (8 * blk)) & 0xFFu;
+          const float s = __uint_as_float(sb == 0u ? 0x00400000u : (sb == 255u ? 0x7FFFFFFFu : sb << 23));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 c = ld_shared16(src + r * 128 + (((blk * 2 + e) ^ (r & 7)) * 16));
+            uint32_t w[4];
+            codes_to_bf16(make_uint2(c.x, c.y), s, p.e5m2 != 0, w);
+            st_shared16(dst + Cfg::X::at(r, blk * 4 + e * 2), w);
+            codes_to_bf16(make_uint2(c.z, c.w), s, p.e5m2 != 0, w);
+            st_shared16(dst + Cfg::X::at(r, blk * 4 + e * 2 + 1), w);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&ctl.decoded[b & 1]);
+        step();
+      }
     }
+    copy_commit();
+    copy_wait<0>();
   }
   __syncthreads();
   wait(&ctl.done, 0);
@@ -2180,11 +2338,11 @@ bool weights_map(CUtensorMap* tm, const bf16* w, bool rows_of_r, int64_t C, int 
                    : make_tmap_rows(tm, w, kMapBf16, 2, C, R, L, static_cast<uint64_t>(C) * 2, kChunk, RP);
 }
 
-// T rows of `cols` elements at a pitch of ld, gathered or scattered `box` columns at a time.
+// T rows of `cols` elements at a pitch of ld, by `rows` rows x `box` columns.
 bool rows_map(CUtensorMap* tm, const void* base, CUtensorMapDataType type, int elem, int64_t cols, int64_t T, int64_t ld,
-              int box) {
+              int box, int rows) {
   if (!aligned(base, 16) || ld * elem % 16) return false;
-  return make_tmap_rows(tm, base, type, elem, cols, T, 0, static_cast<uint64_t>(ld) * elem, box, 1);
+  return make_tmap_rows(tm, base, type, elem, cols, T, 0, static_cast<uint64_t>(ld) * elem, box, rows);
 }
 
 template <int NT, bool TRANS, bool VEC>
@@ -2198,12 +2356,12 @@ cudaError_t down_rank(Down p, const Order* o, const DeviceCtx* ctx, cudaStream_t
     const dim3 grid(static_cast<unsigned>(slots), cs);
     const Waits w{ctx->status, wait_timeout_ns()};
     DownTmaArgs a{};
-    if (rows_map(&a.x, p.x, kMapBf16, 2, p.C, p.T, p.ld, kChunk)) {
+    if (rows_map(&a.x, p.x, kMapBf16, 2, p.C, p.T, p.ld, kChunk, kTileRows)) {
       a.d = p;
       a.o = *o;
       a.w = w;
       a.wtma = weights_map<RP>(&a.wm, p.w, TRANS, p.C, p.R, p.L);
-      return launch("adapter_down_tma", adapter_down_tma<RP, TRANS>, a, grid, 128, DownTma<RP, TRANS>::kSmem, cs, true, s);
+      return launch("adapter_down_tma", adapter_down_tma<RP, TRANS>, a, grid, 192, DownTma<RP, TRANS>::kSmem, cs, true, s);
     }
     return launch("adapter_down_tile", adapter_down_tile<RP, TRANS>, DownSorted{p, *o, w}, grid, 256,
                   DownTile<RP, TRANS>::kSmem, cs, true, s);
@@ -2235,15 +2393,15 @@ cudaError_t up_rank(Up p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) 
     const int64_t slots = static_cast<int64_t>(o->segments) * o->tiles_per_segment;
     const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));
     const int64_t chunks = ceil_div(p.C, kChunk);
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 2 * ctx->num_sms / tiles));
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 4 * ctx->num_sms / tiles));  // two waves
     const int per_cta = static_cast<int>(ceil_div(chunks, splits));
     const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, per_cta)));
     const Waits w{ctx->status, wait_timeout_ns()};
     constexpr CUtensorMapDataType kMapY = sizeof(Y) == 2 ? kMapBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     constexpr int kBox = 128 / static_cast<int>(sizeof(Y));
     UpTmaArgs a{};
-    if (rows_map(&a.out, p.out, kMapY, sizeof(Y), p.C, p.T, p.ld_out, kBox) &&
-        (!p.base || rows_map(&a.y, p.base, kMapY, sizeof(Y), p.C, p.T, p.ld_base, kBox))) {
+    if (rows_map(&a.out, p.out, kMapY, sizeof(Y), p.C, p.T, p.ld_out, kBox, 32) &&
+        (!p.base || rows_map(&a.y, p.base, kMapY, sizeof(Y), p.C, p.T, p.ld_base, kBox, kTileRows))) {
       a.d = p;
       a.o = *o;
       a.w = w;
@@ -2290,11 +2448,11 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
   bool tma = true;
   for (int k = 0; k < 2 && tma; ++k)
     tma = p.job[k].x_scales
-              ? rows_map(&a.x[k], p.job[k].x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.job[k].C, T, p.job[k].ld, kGradCols)
-              : rows_map(&a.x[k], p.job[k].x, kMapBf16, 2, p.job[k].C, T, p.job[k].ld, 64);
+              ? rows_map(&a.x[k], p.job[k].x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.job[k].C, T, p.job[k].ld, kGradCols,
+                         kGradRows)
+              : rows_map(&a.x[k], p.job[k].x, kMapBf16, 2, p.job[k].C, T, p.job[k].ld, 64, kGradRows);
   constexpr int kE = RP < 64 ? RP : 64;
-  tma = tma && make_tmap_rows(&a.block, terms_at, kMapBf16, 2, TERMS * RP, 2 * T, 0, TERMS * RP * 2, kE, kGradRows) &&
-        make_tmap_rows(&a.row, terms_at, kMapBf16, 2, TERMS * RP, 2 * T, 0, TERMS * RP * 2, kE, 1);
+  tma = tma && make_tmap_rows(&a.coef, terms_at, kMapBf16, 2, TERMS * RP, 2 * T, 0, TERMS * RP * 2, kE, kGradRows);
   if (tma) {
     a.g = p;
     a.T = T;
@@ -2311,22 +2469,30 @@ cudaError_t grads(const Grads& p, const AdaptersBackwardRequest& r, const Device
   return grads_rank<128, G>(p, r, ctx, s);
 }
 
-// The order's arrays in the workspace.
-Order order_at(void* workspace, int64_t T, int L) {
+// The order's arrays in the workspace (the blocks last: only the gradients need them).
+Order order_at(void* workspace, int64_t T, int L, bool blocks, size_t* bytes = nullptr) {
   Order o{};
   o.segments = static_cast<int>(ceil_div(T, kSegment));
-  o.tiles_per_segment = tiles_per_segment(T, L);
-  uint8_t* p = static_cast<uint8_t*>(workspace);
-  o.perm = reinterpret_cast<int*>(p);
-  p += align_up(static_cast<size_t>(T) * 4, 256);
-  o.starts = reinterpret_cast<int*>(p);
-  p += align_up(static_cast<size_t>(o.segments) * (L + 2) * 4, 256);
-  o.tiles = reinterpret_cast<Tile*>(p);
+  o.tiles_per_segment = pieces_per_segment(T, L, kTileRows);
+  o.blocks_per_segment = pieces_per_segment(T, L, kGradRows);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    void* p = static_cast<uint8_t*>(workspace) + at;
+    at += align_up(n, 256);
+    return p;
+  };
+  o.perm = static_cast<int*>(take(static_cast<size_t>(T) * 4));
+  o.tiles = static_cast<Tile*>(take(static_cast<size_t>(o.segments) * o.tiles_per_segment * sizeof(Tile)));
+  if (blocks) {
+    o.blocks = static_cast<Tile*>(take(static_cast<size_t>(o.segments) * o.blocks_per_segment * sizeof(Tile)));
+    o.starts = static_cast<int*>(take(static_cast<size_t>(o.segments) * (L + 1) * 4));
+  }
+  if (bytes) *bytes = at;
   return o;
 }
 
 cudaError_t sort(const int* ids, int64_t T, int L, const Order& o, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(kSortWarps) * (L + 1) * 2;
+  const size_t smem = static_cast<size_t>(kSortWarps) * (L + 1) * 2 + kSegment * 2;
   if (smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(adapter_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -2340,10 +2506,10 @@ cudaError_t sort(const int* ids, int64_t T, int L, const Order& o, cudaStream_t 
 
 }  // namespace
 
-size_t adapter_order_bytes(int64_t T, int64_t L) {
-  const int64_t segments = ceil_div(T, kSegment);
-  return align_up(static_cast<size_t>(T) * 4, 256) + align_up(static_cast<size_t>(segments) * (L + 2) * 4, 256) +
-         align_up(static_cast<size_t>(segments) * tiles_per_segment(T, static_cast<int>(L)) * sizeof(Tile), 256);
+size_t adapter_order_bytes(int64_t T, int64_t L, bool gradients) {
+  size_t bytes = 0;
+  order_at(nullptr, T, static_cast<int>(L), gradients, &bytes);
+  return bytes;
 }
 
 size_t adapter_terms_bytes(int64_t T, int64_t R) {
@@ -2363,7 +2529,7 @@ cudaError_t launch_adapters(const AdaptersRequest& r, cudaStream_t s) {
   const Order* o = nullptr;
   cudaError_t e;
   if (adapters_sorted(r.T, r.L)) {
-    order = order_at(r.workspace, r.T, L);
+    order = order_at(r.workspace, r.T, L, false);
     o = &order;
     e = sort(r.ids, r.T, L, order, s);
     if (e != cudaSuccess) return e;
@@ -2390,7 +2556,7 @@ cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStrea
     if (e == cudaSuccess) e = cudaMemsetAsync(r.db, 0, static_cast<size_t>(r.L) * R * r.N * g, s);
     return e;
   }
-  const Order order = order_at(r.order, r.T, L);  // the gradients always go by it
+  const Order order = order_at(r.order, r.T, L, true);  // the gradients always go by it
   cudaError_t e = sort(r.ids, r.T, L, order, s);
   if (e != cudaSuccess) return e;
   const Order* o = adapters_sorted(r.T, r.L) ? &order : nullptr;

@@ -837,7 +837,7 @@ bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 
 size_t bsmm_adapters_workspace_size(int64_t T, int64_t L) {
   if (T <= 0 || L <= 0 || !adapters_sorted(T, L)) return 0;
-  return adapter_order_bytes(T, L);
+  return adapter_order_bytes(T, L, false);
 }
 
 bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* x, int64_t ld_x,
@@ -869,7 +869,7 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
 
 size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R, int64_t L) {
   if (T <= 0 || R <= 0 || L <= 0) return 0;
-  return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256) + adapter_order_bytes(T, L) +
+  return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256) + adapter_order_bytes(T, L, true) +
          adapter_terms_bytes(T, R);
 }
 
@@ -904,7 +904,7 @@ bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, i
   uint8_t* order = static_cast<uint8_t*>(workspace) + align_up(static_cast<size_t>(T) * R * 4, 256);
   const AdaptersBackwardRequest r{T, K, N, R, L, dy, ld_dy, x, ld_x, static_cast<const uint8_t*>(x_scales), x_type, A, B,
                                   ids, scaling, u, dx_base, ld_dx, dx, dA, dB, grad_type == BSMM_BF16,
-                                  static_cast<float*>(workspace), order, order + adapter_order_bytes(T, L)};
+                                  static_cast<float*>(workspace), order, order + adapter_order_bytes(T, L, true)};
   return launched(launch_adapters_backward(r, reinterpret_cast<cudaStream_t>(stream)), "adapters backward launch");
 }
 

@@ -56,7 +56,7 @@ bool make_tmap_3d(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, 
 
 // Tensor map of 2 or 3 dimensions (d2 = 0: two), rows of d0 elements `pitch`
 // bytes apart (a multiple of 16), box {b0, b1, 1}; swizzled over b0's bytes (32,
-// 64 or 128).  A box one row high serves gathers and scatters of rows.
+// 64 or 128).
 bool make_tmap_rows(CUtensorMap* tm, const void* base, CUtensorMapDataType dtype, int elem_bytes, uint64_t d0,
                     uint64_t d1, uint64_t d2, uint64_t pitch, uint32_t b0, uint32_t b1);
 
@@ -183,7 +183,7 @@ struct AdaptersBackwardRequest {
 // bytes, those of the gradients' coefficients, and the most adapters that can
 // be sorted by.
 bool adapters_sorted(int64_t T, int64_t L);
-size_t adapter_order_bytes(int64_t T, int64_t L);
+size_t adapter_order_bytes(int64_t T, int64_t L, bool gradients);
 size_t adapter_terms_bytes(int64_t T, int64_t R);
 int64_t adapters_sort_max();
 cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s);

@@ -90,6 +90,34 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// mbar_wait that polls without the suspend-time hint, for a warp that has
+// little else to do and whose phases complete every microsecond or less.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort,
+                                          int* status, int site) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_test(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > timeout_ns) {
+      *abort = 1;
+      record_timeout(status, site);
+      return false;
+    }
+  }
+}
+
 // --------------------------------------------------------------------------
 // TMA / bulk copies
 // --------------------------------------------------------------------------
@@ -115,22 +143,10 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, const void* 
                : "memory");
 }
 
-// Four rows of a 2-D array (a tensor map with a box one row high) from column x
-// on, into consecutive rows of shared memory, and back.  Rows past the array
-// read as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, uint64_t* bar, int x, int4 r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-      "%4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(tm), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_scatter4(const CUtensorMap* tm, uint32_t src, int x, int4 r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.tile::scatter4.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];" ::"l"(
-          tm),
-      "r"(src), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
-      : "memory");
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tm), "r"(src), "r"(x),
+               "r"(y)
+               : "memory");
 }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* tm, uint64_t* bar, int x, int y) {
   asm volatile(
