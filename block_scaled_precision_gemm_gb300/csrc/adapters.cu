@@ -53,6 +53,34 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
+// Sum over the cluster's CTAs (up to 8, in order) of the value at this CTA's
+// shared address; all loads are under way before the first is added.
+__device__ __forceinline__ float cluster_sum(const float* p, int cs) {
+  const uint32_t addr = smem_u32(p);
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = k < cs ? ld_shared_cluster_f32(mapa_shared(addr, k)) : 0.f;
+  float s = v[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) s += v[k];
+  return s;
+}
+__device__ __forceinline__ float4 cluster_sum4(const float* p, int cs) {  // 16-byte aligned
+  const uint32_t addr = smem_u32(p);
+  float4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = k < cs ? ld_shared_cluster_v4(mapa_shared(addr, k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 s = v[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    s.x += v[k].x;
+    s.y += v[k].y;
+    s.z += v[k].z;
+    s.w += v[k].w;
+  }
+  return s;
+}
+
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 
@@ -139,7 +167,7 @@ __device__ __forceinline__ int down_col(int j, int n, int nt) {
 // memory, over the cluster through distributed shared memory, each CTA summing
 // a share of the tile.
 template <int NT, int WK, bool TRANS, bool VEC, int UNROLL>
-__global__ void __launch_bounds__(WK * 32) adapter_down(const Down p) {
+__global__ void __launch_bounds__(WK * 32, NT <= 2 ? 3 : (NT <= 4 ? 2 : 1)) adapter_down(const Down p) {
   constexpr int MT = 1, kRows = 16, kCols = NT * 8;
   extern __shared__ float part[];  // [WK][kRows][kCols]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -274,14 +302,7 @@ __global__ void __launch_bounds__(WK * 32) adapter_down(const Down p) {
   const int e_end = min(n, (rank + 1) * share);
   for (int e = rank * share + tid; e < e_end; e += kThreads) {
     const int r = e / p.R, c = e - r * p.R;
-    float v = 0.f;
-    if (cs > 1) {
-      const uint32_t addr = smem_u32(part + r * kCols + c);
-      for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
-    } else {
-      v = part[r * kCols + c];
-    }
-    p.u[(row0 + r) * p.R + c] = v;
+    p.u[(row0 + r) * p.R + c] = cs > 1 ? cluster_sum(part + r * kCols + c, cs) : part[r * kCols + c];
   }
   __syncwarp();
   if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
@@ -498,7 +519,7 @@ constexpr int kSortMaxL = 1024;
 
 struct Tile {
   int adapter, start, count;  // tokens perm[start .. start + count)
-  int run;                    // 1: consecutive ones
+  int run;                    // the first of them where they are consecutive, else -1
 };
 
 // The sort's output in the caller's workspace.
@@ -541,7 +562,7 @@ __device__ __forceinline__ void group_pieces(const int* first, int* piece0, int 
 // Writes them: piece i of all.
 __device__ __forceinline__ Tile sorted_piece(const int* first, const int* piece0, const uint16_t* perm, int G, int rows,
                                              int s0, int i) {
-  Tile t{-1, 0, 0, 0};
+  Tile t{-1, 0, 0, -1};
   if (i >= piece0[G]) return t;
   int lo = 0, hi = G - 1;  // the last group whose first piece is at or before i
   while (lo < hi) {
@@ -555,7 +576,8 @@ __device__ __forceinline__ Tile sorted_piece(const int* first, const int* piece0
   t.adapter = lo == G - 1 ? -1 : lo;
   t.start = s0 + at;
   t.count = min(rows, first[lo + 1] - at);
-  t.run = perm[at + t.count - 1] - perm[at] == t.count - 1;  // a group's tokens are in ascending order
+  // (a group's tokens are in ascending order)
+  t.run = perm[at + t.count - 1] - perm[at] == t.count - 1 ? s0 + perm[at] : -1;
   return t;
 }
 
@@ -749,6 +771,38 @@ struct DownTile {
   static constexpr int kTmem = RP < 32 ? 32 : RP;
 };
 
+// A CTA's share of the sums of its cluster into the rows of u that the tile's
+// tokens have: four ranks at a time.
+template <int RP>
+__device__ __forceinline__ void write_sums(float* u, int R, const int* tokens, int count, const float* sums, int rank,
+                                           int cs, int threads) {
+  constexpr int kPitch = RP + 4, kQuads = RP / 4;
+  if (cs > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
+  const int total = count * kQuads, share = (total + cs - 1) / cs;
+  const int end = min(total, (rank + 1) * share);
+#pragma unroll 2
+  for (int e = rank * share + static_cast<int>(threadIdx.x); e < end; e += threads) {
+    const int r = e / kQuads, c = (e % kQuads) * 4;
+    if (c >= R) continue;
+    const float* at = sums + r * kPitch + c;
+    const float4 v = cs > 1 ? cluster_sum4(at, cs) : *reinterpret_cast<const float4*>(at);
+    float* dst = u + static_cast<int64_t>(tokens[r]) * R + c;
+    if (R % 4 == 0 && (reinterpret_cast<uintptr_t>(u) & 15u) == 0) {
+      *reinterpret_cast<float4*>(dst) = v;
+    } else {
+      const float s[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + k < R) dst[k] = s[k];
+    }
+  }
+  __syncwarp();
+  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
+}
+
 struct DownSorted {
   Down d;
   Order o;
@@ -869,25 +923,7 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, Cfg::kTmem);
-  if (cs > 1) {
-    __syncwarp();
-    cluster_sync();
-  }
-  const int total = tile.count * p.R, share = (total + cs - 1) / cs;
-  const int e_end = min(total, (rank + 1) * share);
-  for (int e = rank * share + tid; e < e_end; e += 256) {
-    const int r = e / p.R, col = e - r * p.R;
-    float v = 0.f;
-    if (cs > 1) {
-      const uint32_t addr = smem_u32(sums + r * Cfg::kPitch + col);
-      for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
-    } else {
-      v = sums[r * Cfg::kPitch + col];
-    }
-    p.u[static_cast<int64_t>(ps.o.perm[tile.start + r]) * p.R + col] = v;
-  }
-  __syncwarp();
-  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
+  write_sums<RP>(p.u, p.R, ps.o.perm + tile.start, tile.count, sums, rank, cs, 256);
 }
 
 // ---------------------------------------------------------------------------
@@ -1150,8 +1186,8 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
 // written as [L][R][C] (dA) or [L][C][R] (dB); x is bf16 or an MXFP8
 // checkpoint.
 struct GradJob {
-  const bf16* coef;  // [T][TERMS][RP], in the sorted order
-  const void* x;     // [T][ld] bf16, or 8-bit codes
+  const uint8_t* coef;  // each block's coefficients, as they are staged
+  const void* x;        // [T][ld] bf16, or 8-bit codes
   const uint8_t* x_scales;  // null: bf16; else UE8M0 [T][C / 32]
   int64_t ld;
   void* out;
@@ -1169,38 +1205,44 @@ struct Grads {
   int scale4;  // the scale bytes' rows are 4-byte aligned
 };
 
-// The coefficients of both jobs in the sorted order, each split into TERMS bf16
-// terms and padded to RP ranks: once here, where every column tile of
-// adapter_grads would otherwise do it (half of that kernel's instructions).
+// The coefficients of both jobs for every block of 64 sorted tokens, split into
+// TERMS bf16 terms, padded to RP ranks and with zeros past the block's tokens,
+// laid out as the MMA reads them: once here, where every column tile of the
+// gradients would otherwise do it, and one bulk copy brings a block's in (as
+// tensor loads of 32-byte rows they were most of the rows that TMA had to move).
+template <int RP, int TERMS>
+struct CoefImage {
+  using Term = Staged<kGradRows, RP>;
+  static constexpr int kTermBytes = Term::kBytes, kBytes = TERMS * kTermBytes;
+};
 struct Terms {
   const float* from[2];  // [T][R]
-  bf16* to[2];           // [T][TERMS][RP]
+  uint8_t* to[2];        // [blocks] images
+  const Tile* blocks;
   const int* perm;
-  int64_t T;
   int R;
 };
 template <int RP, int TERMS>
 __global__ void __launch_bounds__(256) adapter_terms(const Terms p) {
+  using Image = CoefImage<RP, TERMS>;
   constexpr int kPieces = RP / 8;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t at = i / kPieces;
-  const int r0 = static_cast<int>(i % kPieces) * 8;
-  if (at >= p.T) return;
-  const int64_t t = p.perm[at];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float* src = p.from[k] + t * p.R;
+  const Tile b = p.blocks[blockIdx.x];
+  if (b.count == 0 || b.adapter < 0) return;
+  for (int i = threadIdx.x; i < 2 * kGradRows * kPieces; i += 256) {
+    const int job = i / (kGradRows * kPieces), row = i / kPieces % kGradRows, piece = i % kPieces;
+    const float* src = p.from[job] + (row < b.count ? static_cast<int64_t>(p.perm[b.start + row]) * p.R : 0) + piece * 8;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = r0 + e < p.R ? src[r0 + e] : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = row < b.count && piece * 8 + e < p.R ? src[e] : 0.f;
     uint32_t w[4][TERMS];
 #pragma unroll
     for (int e = 0; e < 4; ++e) split_pair<TERMS>(v[2 * e], v[2 * e + 1], w[e]);
+    uint8_t* dst = p.to[job] + static_cast<int64_t>(blockIdx.x) * Image::kBytes + Image::Term::at(row, piece);
 #pragma unroll
-    for (int m = 0; m < TERMS; ++m)
-      *reinterpret_cast<uint4*>(p.to[k] + (at * TERMS + m) * RP + r0) = make_uint4(w[0][m], w[1][m], w[2][m], w[3][m]);
+    for (int k = 0; k < TERMS; ++k)
+      *reinterpret_cast<uint4*>(dst + k * Image::kTermBytes) = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
   }
 }
 constexpr int kGradCols = 128;  // columns of a CTA
@@ -1226,11 +1268,12 @@ __device__ __forceinline__ void codes_to_bf16(uint2 c, float s, bool e5m2, uint3
 template <int RP, int TERMS>
 struct GradTile {
   using X = Staged<kGradRows, kGradCols>;
-  using Coef = Staged<kGradRows, RP>;  // one term
+  using Image = CoefImage<RP, TERMS>;
+  using Coef = typename Image::Term;
   static constexpr int kXBytes = X::kBytes;                               // a block of bf16
   static constexpr int kCodeBytes = kGradRows * kGradCols + 256 * 2 * 4;  // of codes, and each copy's scale word
   static constexpr int kStages = RP <= 16 ? 4 : (RP <= 32 || (RP <= 64 && TERMS == 2) ? 3 : 2);  // two CTAs to an SM (one from RP = 128 on)
-  static constexpr int kTermBytes = Coef::kBytes, kCoefBytes = TERMS * kTermBytes;
+  static constexpr int kTermBytes = Image::kTermBytes, kCoefBytes = Image::kBytes;
   static constexpr int kIdxSlots = 8;
   static constexpr int kPitch = RP + 4;  // of the sums' rows (one to a column), in floats
   // bf16: the ring; codes: two decoded blocks and the ring.  Then the
@@ -1253,6 +1296,7 @@ struct BlockWalk {
   int L, a, rank, cs;
   int seg = -1, at = 0, end = 0;
   Tile now, ahead;
+  int64_t index = 0, index_ahead = 0;  // their places in the list
   bool have = false;
   __device__ __forceinline__ BlockWalk(const Order& o_, int L_, int a_, int rank_, int cs_)
       : o(o_), L(L_), a(a_), rank(rank_), cs(cs_) {
@@ -1269,13 +1313,15 @@ struct BlockWalk {
       at = s[0] + rank;
       end = s[1];
     }
-    const int4 v = *reinterpret_cast<const int4*>(o.blocks + static_cast<int64_t>(seg) * o.blocks_per_segment + at);
+    index_ahead = static_cast<int64_t>(seg) * o.blocks_per_segment + at;
+    const int4 v = *reinterpret_cast<const int4*>(o.blocks + index_ahead);
     ahead = Tile{v.x, v.y, v.z, v.w};
     have = true;
   }
   __device__ __forceinline__ bool next() {
     if (!have) return false;
     now = ahead;
+    index = index_ahead;
     fetch();
     return true;
   }
@@ -1291,31 +1337,26 @@ __device__ __forceinline__ void write_grad(const Grads& p, const GradJob& j, con
   }
   const float s = p.scaling ? __ldg(p.scaling + a) : 1.f;
   const int cols = static_cast<int>(min(static_cast<int64_t>(kGradCols), j.C - c0));
-  const int n = p.R * cols, share = (n + cs - 1) / cs;
-  const int e_end = min(n, (rank + 1) * share);
+  const int quads = (p.R + 3) / 4, n = quads * cols, share = (n + cs - 1) / cs;
+  const int end = min(n, (rank + 1) * share);
   G* out = static_cast<G*>(j.out) + static_cast<int64_t>(a) * p.R * j.C;
-  for (int e = rank * share + static_cast<int>(threadIdx.x); e < e_end; e += threads) {
-    int r, c;
-    if (j.out_cr) {
-      c = e / p.R;
-      r = e - c * p.R;
-    } else {
-      r = e / cols;
-      c = e - r * cols;
-    }
-    float v = 0.f;
-    if (cs > 1) {
-      const uint32_t addr = smem_u32(sums + c * pitch + r);
-      for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
-    } else {
-      v = sums[c * pitch + r];
-    }
-    v *= s;
-    const int64_t at = j.out_cr ? (c0 + c) * p.R + r : static_cast<int64_t>(r) * j.C + c0 + c;
-    if constexpr (sizeof(G) == 2)
-      out[at] = __float2bfloat16_rn(v);
-    else
-      out[at] = v;
+#pragma unroll 2
+  for (int e = rank * share + static_cast<int>(threadIdx.x); e < end; e += threads) {
+    // four ranks of a column; neighbouring lanes on neighbouring addresses
+    const int c = j.out_cr ? e / quads : e % cols, r = (j.out_cr ? e % quads : e / cols) * 4;
+    const float* at = sums + c * pitch + r;
+    const float4 v = cs > 1 ? cluster_sum4(at, cs) : *reinterpret_cast<const float4*>(at);
+    const float q[4] = {v.x * s, v.y * s, v.z * s, v.w * s};
+    const int64_t step = j.out_cr ? 1 : j.C;
+    G* dst = out + (j.out_cr ? (c0 + c) * p.R + r : static_cast<int64_t>(r) * j.C + c0 + c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r + k < p.R) {
+        if constexpr (sizeof(G) == 2)
+          dst[k * step] = __float2bfloat16_rn(q[k]);
+        else
+          dst[k * step] = q[k];
+      }
   }
   __syncwarp();
   if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
@@ -1362,12 +1403,11 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
   bool more = walk.next();
   int found = 0;   // blocks whose tokens have been looked up
   int token = -1;  // of row tid (tid < 64) of the last of them
-  int look_pos = 0, look_rows = 0;  // its place in the sorted order
+  int64_t look_index = 0;
   auto look = [&]() {
     if (!more) return;
-    look_pos = walk.now.start;
-    look_rows = walk.now.count;
-    if (tid < kGradRows) token = tid < look_rows ? p.o.perm[look_pos + tid] : -1;
+    look_index = walk.index;
+    if (tid < kGradRows) token = tid < walk.now.count ? p.o.perm[walk.now.start + tid] : -1;
     ++found;
     more = walk.next();
   };
@@ -1377,13 +1417,8 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
 
   auto issue_coef = [&](int b) {  // of the block looked up last
     const uint32_t at = coef_at + (b % S) * Cfg::kCoefBytes;
-    constexpr int kRowPieces = TERMS * (RP / 8);
-    const bf16* src = j.coef + static_cast<int64_t>(look_pos) * (TERMS * RP);
-    for (int i = tid; i < kGradRows * kRowPieces; i += 256) {
-      const int r = i / kRowPieces, k = i % kRowPieces;
-      const bool in = r < look_rows;
-      copy_async<16>(at + (k / (RP / 8)) * Cfg::kTermBytes + Cfg::Coef::at(r, k % (RP / 8)), in ? src + i * 8 : src, in ? 16 : 0);
-    }
+    const uint8_t* src = j.coef + look_index * Cfg::kCoefBytes;
+    for (int i = tid * 16; i < Cfg::kCoefBytes; i += 256 * 16) copy_async<16>(at + i, src + i, 16);
   };
   auto issue = [&](int b) {  // copies block b's x
     const int* rows = idx + (b % Cfg::kIdxSlots) * kGradRows;
@@ -1615,7 +1650,7 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
       p.u[static_cast<int64_t>(ps.o.perm[tile.start + i / p.R]) * p.R + i % p.R] = 0.f;
     return;
   }
-  const bool run = tile.run != 0;
+  const bool run = tile.run >= 0;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&ctl.full[i], 1 + (run ? 0 : kHelpers) + (ps.wtma ? 0 : kHelpers));
@@ -1641,7 +1676,6 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
   };
   int c = 0;
   if (warp == 0) {
-    const int first = ps.o.perm[tile.start];
     if (lane == 0) {
       for (; c < n; ++c) {
         const int st = c % S;
@@ -1650,7 +1684,7 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
         const int64_t k = (c_begin + c) * kChunk;
         mbar_arrive_expect_tx(&ctl.full[st], (run ? Cfg::kXBytes : 0) + (ps.wtma ? Cfg::kWBytes : 0));
         // rows past the tile are another adapter's, or zeros: not stored
-        if (run) tma_load_2d(at, &ps.x, &ctl.full[st], static_cast<int>(k), first);
+        if (run) tma_load_2d(at, &ps.x, &ctl.full[st], static_cast<int>(k), tile.run);
         if (ps.wtma) load_weights<RP, TRANS>(at + Cfg::kXBytes, &ps.wm, &ctl.full[st], k, tile.adapter, ring);
       }
     }
@@ -1724,25 +1758,7 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, Cfg::kTmem);
-  if (cs > 1) {
-    __syncwarp();
-    cluster_sync();
-  }
-  const int total = tile.count * p.R, share = (total + cs - 1) / cs;
-  const int e_end = min(total, (rank + 1) * share);
-  for (int e = rank * share + tid; e < e_end; e += 192) {
-    const int r = e / p.R, col = e - r * p.R;
-    float v = 0.f;
-    if (cs > 1) {
-      const uint32_t addr = smem_u32(sums + r * Cfg::kPitch + col);
-      for (int k = 0; k < cs; ++k) v += ld_shared_cluster_f32(mapa_shared(addr, k));
-    } else {
-      v = sums[r * Cfg::kPitch + col];
-    }
-    p.u[static_cast<int64_t>(ps.o.perm[tile.start + r]) * p.R + col] = v;
-  }
-  __syncwarp();
-  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
+  write_sums<RP>(p.u, p.R, ps.o.perm + tile.start, tile.count, sums, rank, cs, 192);
 }
 
 template <int RP, typename Y, bool TRANS>
@@ -1788,7 +1804,7 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
   const int n = static_cast<int>(min(static_cast<int64_t>(ps.chunks_per_cta), chunks - c_begin));
   const bool plain = tile.adapter < 0;  // no product: out = base
   const bool has_base = p.base != nullptr;
-  const bool run = tile.run != 0;
+  const bool run = tile.run >= 0;
   constexpr int kHelpers = 64;
   if (tid == 0) {
     for (int i = 0; i < WS; ++i) {
@@ -1820,7 +1836,6 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
   };
   int c = 0;  // chunks begun
   if (warp == 0) {
-    const int first = ps.o.perm[tile.start];
     if (lane == 0) {
       for (; c < n; ++c) {
         const int64_t k = (c_begin + c) * kChunk;
@@ -1841,7 +1856,7 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)  // rows past the tile are not written
           tma_load_2d(y_at + st * Cfg::kYBytes + b * (kTileRows * 128), &ps.y, &ctl.yfull[st],
-                      static_cast<int>(k) + b * kBlockCols, first);
+                      static_cast<int>(k) + b * kBlockCols, tile.run);
       }
     }
     __syncwarp();
@@ -2055,20 +2070,19 @@ struct GradTma : GradTile<RP, TERMS> {
   };
   static constexpr int kSmem = kRing + static_cast<int>(sizeof(Ctl));
 };
+constexpr int kGradHelpers = 256;
 struct GradTmaArgs {
   CUtensorMap x[2];   // of the jobs: 64 rows (bf16 64 columns, codes 128)
-  CUtensorMap coef;   // the coefficients [2 T][TERMS RP], 64 rows
   Grads g;
-  int64_t T;
 };
 
-// Warp 0 feeds x and the coefficients, warp 1 issues the MMAs; warps 2..5
-// gather the blocks that are not 64 consecutive tokens (with their
-// coefficients, zeros past the adapter's last token) and, where x is a
-// checkpoint, decode its codes between the two.  They also read the sums out
-// of tensor memory at the end.
+// Warp 0 feeds x and the coefficients, warp 1 issues the MMAs; the helper warps
+// gather the blocks that are not 64 consecutive tokens (zeros past the
+// adapter's last) and, where x is a checkpoint, decode its codes between the
+// two.  The first
+// four of them also read the sums out of tensor memory at the end.
 template <int RP, int TERMS, typename G>
-__global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
+__global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
   using Cfg = GradTma<RP, TERMS>;
   using Coef = typename Cfg::Coef;
   constexpr int S = Cfg::kStages, kSteps = kGradRows / 16;
@@ -2087,11 +2101,11 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
   const uint32_t coef_off = kept ? Cfg::kCodeBytes + Cfg::kScaleBytes : Cfg::kXBytes;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&ctl.full[i], 1 + 128);
+      mbar_init(&ctl.full[i], 1 + kGradHelpers);
       mbar_init(&ctl.empty[i], 1);
     }
-    mbar_init(&ctl.decoded[0], 128);
-    mbar_init(&ctl.decoded[1], 128);
+    mbar_init(&ctl.decoded[0], kGradHelpers);
+    mbar_init(&ctl.decoded[1], kGradHelpers);
     mbar_init(&ctl.done, 1);
     ctl.abort_flag = 0;
     fence_barrier_init();
@@ -2109,26 +2123,22 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
     return mbar_poll(bar, parity & 1u, p.w.timeout_ns, &ctl.abort_flag, p.w.status, kSiteGrads);
   };
   int b = 0;
-  constexpr int kCoefBlocks = RP / Coef::kE, kCoefLoads = TERMS * kCoefBlocks;
   if (warp == 0) {
-    const int T = static_cast<int>(ps.T);
     if (lane == 0) {
       BlockWalk walk(p.o, p.L, a, rank, cs);
       while (walk.next()) {
         const int st = b % S;
-        const bool run = walk.now.run && walk.now.count == kGradRows;
-        const int first = run ? p.o.perm[walk.now.start] : 0, row0 = second * T + walk.now.start;
+        const bool run = walk.now.run >= 0 && walk.now.count == kGradRows;
+        const int first = walk.now.run;
+        const uint8_t* coef = j.coef + walk.index * Cfg::kCoefBytes;
         if (b >= S && !wait(&ctl.empty[st], b / S - 1)) break;
-        const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
-        mbar_arrive_expect_tx(&ctl.full[st], run ? (kept ? Cfg::kCodeBytes : Cfg::kXBytes) + Cfg::kCoefBytes : 0);
+        const uint32_t at = ring_at + st * stage_bytes;
+        mbar_arrive_expect_tx(&ctl.full[st], Cfg::kCoefBytes + (run ? (kept ? Cfg::kCodeBytes : Cfg::kXBytes) : 0));
         if (run) {
           tma_load_2d(at, &ps.x[second], &ctl.full[st], static_cast<int>(c0), first);
           if (!kept) tma_load_2d(at + kGradRows * 128, &ps.x[second], &ctl.full[st], static_cast<int>(c0) + 64, first);
-#pragma unroll
-          for (int k = 0; k < kCoefLoads; ++k)
-            tma_load_2d(ct + (k / kCoefBlocks) * Cfg::kTermBytes + (k % kCoefBlocks) * Coef::kBlock, &ps.coef, &ctl.full[st],
-                        k * Coef::kE, row0);
         }
+        bulk_load(ring + (at + coef_off - smem_u32(ring)), coef, Cfg::kCoefBytes, &ctl.full[st]);
         ++b;
       }
     }
@@ -2158,47 +2168,41 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
     b = __shfl_sync(0xFFFFFFFFu, b, 0);
   } else {
     // The helpers run D blocks ahead with what they copy; a checkpoint's codes
-    // are decoded by the thread that copied them: rows i / 4 and 32 further,
-    // the 32 codes of block i % 4.
+    // are decoded by the thread that copied them: row i / 4, the 32 codes of
+    // block i % 4.
     constexpr int D = S - 1;
     const int i = tid - 64, r0 = i >> 2, blk = i & 3;
     const int64_t nb = j.C / 32;
-    const bf16* coef = j.coef;
     BlockWalk walk(p.o, p.L, a, rank, cs);
     auto copy = [&](int d) {  // block d, where the walk is
       const int st = d % S;
       const Tile& w = walk.now;
-      const bool run = w.run && w.count == kGradRows;
-      const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
+      const bool run = w.run >= 0 && w.count == kGradRows;
+      const uint32_t at = ring_at + st * stage_bytes;
       if (!run) {
         if (!kept) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = (i >> 4) + 8 * e, piece = i & 15;
+          for (int e = 0; e < 4; ++e) {
+            const int r = (i >> 4) + 16 * e, piece = i & 15;
             const bool in = r < w.count;
             const int64_t t = p.o.perm[w.start + (in ? r : 0)];
             gather16(at + Cfg::X::at(r, piece), static_cast<const bf16*>(j.x) + t * j.ld, c0 + piece * 8, j.C, in);
           }
         } else {
+          const bool in = r0 < w.count;
+          const int64_t t = p.o.perm[w.start + (in ? r0 : 0)];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = r0 + 32 * (e >> 1), piece = blk * 2 + (e & 1);
-            const bool in = r < w.count;
-            const int64_t t = p.o.perm[w.start + (in ? r : 0)];
+          for (int e = 0; e < 2; ++e) {
+            const int r = r0, piece = blk * 2 + e;
             gather16(at + r * 128 + ((piece ^ (r & 7)) * 16), static_cast<const uint8_t*>(j.x) + t * j.ld, c0 + piece * 16,
                      j.C, in);
           }
         }
-        for (int e = i; e < kGradRows * TERMS * (RP / 8); e += 128) {
-          const int r = e / (TERMS * (RP / 8)), k = e % (TERMS * (RP / 8));
-          const bool in = r < w.count;
-          gather16(ct + (k / (RP / 8)) * Cfg::kTermBytes + Coef::at(r, k % (RP / 8)),
-                   coef + (static_cast<int64_t>(w.start) + (in ? r : 0)) * (TERMS * RP), k * 8, TERMS * RP, in);
-        }
       }
       if (kept && i < kGradRows) {  // row i's scale bytes of the tile's blocks
         const bool in = i < w.count;
-        const uint8_t* sb = j.x_scales + (in ? static_cast<int64_t>(p.o.perm[w.start + i]) * nb + c0 / 32 : 0);
+        const int64_t tok = !in ? 0 : (w.run >= 0 ? w.run + i : p.o.perm[w.start + i]);
+        const uint8_t* sb = j.x_scales + (in ? tok * nb + c0 / 32 : 0);
         const uint32_t dst = at + Cfg::kCodeBytes + i * 4;
         if (p.scale4) {
           copy_async<4>(dst, sb, in ? 4 : 0);
@@ -2226,22 +2230,18 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
         ok = wait(&ctl.full[st], b / S) && (b < 2 || wait(&ctl.empty[(b - 2) % S], (b - 2) / S));
         if (!ok) break;  // (the second: the MMAs have read this half of the decoded blocks)
         const uint32_t src = ring_at + st * stage_bytes, dst = smem_u32(ring) + (b & 1) * Cfg::kXBytes;
+        uint32_t sw;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw) : "r"(src + Cfg::kCodeBytes + r0 * 4) : "memory");
+        const uint32_t sb = (sw >> (8 * blk)) & 0xFFu;
+        const float s = __uint_as_float(sb == 0u ? 0x00400000u : (sb == 255u ? 0x7FFFFFFFu : sb << 23));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = r0 + 32 * h;
-          uint32_t sw;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw) : "r"(src + Cfg::kCodeBytes + r * 4) : "memory");
-          const uint32_t sb = (sw >> (8 * blk)) & 0xFFu;
-          const float s = __uint_as_float(sb == 0u ? 0x00400000u : (sb == 255u ? 0x7FFFFFFFu : sb << 23));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint4 c = ld_shared16(src + r * 128 + (((blk * 2 + e) ^ (r & 7)) * 16));
-            uint32_t w[4];
-            codes_to_bf16(make_uint2(c.x, c.y), s, p.e5m2 != 0, w);
-            st_shared16(dst + Cfg::X::at(r, blk * 4 + e * 2), w);
-            codes_to_bf16(make_uint2(c.z, c.w), s, p.e5m2 != 0, w);
-            st_shared16(dst + Cfg::X::at(r, blk * 4 + e * 2 + 1), w);
-          }
+        for (int e = 0; e < 2; ++e) {
+          const uint4 c = ld_shared16(src + r0 * 128 + (((blk * 2 + e) ^ (r0 & 7)) * 16));
+          uint32_t w[4];
+          codes_to_bf16(make_uint2(c.x, c.y), s, p.e5m2 != 0, w);
+          st_shared16(dst + Cfg::X::at(r0, blk * 4 + e * 2), w);
+          codes_to_bf16(make_uint2(c.z, c.w), s, p.e5m2 != 0, w);
+          st_shared16(dst + Cfg::X::at(r0, blk * 4 + e * 2 + 1), w);
         }
         fence_proxy_async_smem();
         mbar_arrive(&ctl.decoded[b & 1]);
@@ -2261,7 +2261,7 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
   const int any = __syncthreads_or(warp == 1 && b > 0);
   tc_fence_after();
   float* sums = reinterpret_cast<float*>(ring);  // [kGradCols][kPitch]: column, rank
-  if (warp >= 2) {
+  if (warp >= 2 && warp < 6) {
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
@@ -2282,7 +2282,7 @@ __global__ void __launch_bounds__(192) adapter_grads_tma(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, Cfg::kTmem);
-  write_grad<G>(p, j, sums, Cfg::kPitch, c0, a, rank, cs, 192);
+  write_grad<G>(p, j, sums, Cfg::kPitch, c0, a, rank, cs, 64 + kGradHelpers);
 }
 
 // ---------------------------------------------------------------------------
@@ -2433,16 +2433,17 @@ template <int RP, typename G>
 cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCtx* ctx, cudaStream_t s) {
   constexpr int TERMS = sizeof(G) == 4 ? 3 : 2;
   const int64_t T = r.T;
-  bf16* terms_at = static_cast<bf16*>(r.terms);
-  p.job[0].coef = terms_at;
-  p.job[1].coef = terms_at + T * TERMS * RP;
-  const Terms terms{{r.d, r.u}, {terms_at, terms_at + T * TERMS * RP}, p.o.perm, T, p.R};
-  const cudaError_t e = launch("adapter_terms", adapter_terms<RP, TERMS>, terms,
-                               dim3(static_cast<unsigned>(ceil_div(T * (RP / 8), 256))), 256, 0, 1, true, s);
+  const int64_t all = static_cast<int64_t>(p.o.segments) * p.o.blocks_per_segment;
+  uint8_t* images[2] = {static_cast<uint8_t*>(r.terms), static_cast<uint8_t*>(r.terms) + all * CoefImage<RP, TERMS>::kBytes};
+  p.job[0].coef = images[0];
+  p.job[1].coef = images[1];
+  const Terms terms{{r.d, r.u}, {images[0], images[1]}, p.o.blocks, p.o.perm, p.R};
+  const cudaError_t e = launch("adapter_terms", adapter_terms<RP, TERMS>, terms, dim3(static_cast<unsigned>(all)), 256, 0, 1,
+                               true, s);
   if (e != cudaSuccess) return e;
   const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
   unsigned cs = 1;
-  while (cs < 8 && tiles * p.L * cs < 4 * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
+  while (cs < 8 && tiles * p.L * cs < 3 * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
   const dim3 grid(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L));
   GradTmaArgs a{};
   bool tma = true;
@@ -2451,12 +2452,9 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
               ? rows_map(&a.x[k], p.job[k].x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.job[k].C, T, p.job[k].ld, kGradCols,
                          kGradRows)
               : rows_map(&a.x[k], p.job[k].x, kMapBf16, 2, p.job[k].C, T, p.job[k].ld, 64, kGradRows);
-  constexpr int kE = RP < 64 ? RP : 64;
-  tma = tma && make_tmap_rows(&a.coef, terms_at, kMapBf16, 2, TERMS * RP, 2 * T, 0, TERMS * RP * 2, kE, kGradRows);
   if (tma) {
     a.g = p;
-    a.T = T;
-    return launch("adapter_grads_tma", adapter_grads_tma<RP, TERMS, G>, a, grid, 192, GradTma<RP, TERMS>::kSmem, cs, true, s);
+    return launch("adapter_grads_tma", adapter_grads_tma<RP, TERMS, G>, a, grid, 64 + kGradHelpers, GradTma<RP, TERMS>::kSmem, cs, true, s);
   }
   return launch("adapter_grads", adapter_grads<RP, TERMS, G>, p, grid, 256, GradTile<RP, TERMS>::kSmem, cs, true, s);
 }
@@ -2512,9 +2510,10 @@ size_t adapter_order_bytes(int64_t T, int64_t L, bool gradients) {
   return bytes;
 }
 
-size_t adapter_terms_bytes(int64_t T, int64_t R) {
+size_t adapter_terms_bytes(int64_t T, int64_t R, int64_t L) {
   const int64_t rp = R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128));
-  return align_up(static_cast<size_t>(T) * 3 * rp * 2 * 2, 256);  // of binary32 gradients, for both
+  const int64_t blocks = ceil_div(T, kSegment) * pieces_per_segment(T, static_cast<int>(L), kGradRows);
+  return static_cast<size_t>(blocks) * 2 * 3 * kGradRows * rp * 2;  // three terms: of binary32 gradients
 }
 
 bool adapters_sorted(int64_t T, int64_t L) { return T >= kSortFrom && L <= kSortMaxL; }

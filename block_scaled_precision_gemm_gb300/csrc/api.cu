@@ -870,7 +870,7 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
 size_t bsmm_adapters_backward_workspace_size(int64_t T, int64_t R, int64_t L) {
   if (T <= 0 || R <= 0 || L <= 0) return 0;
   return align_up(static_cast<size_t>(T) * static_cast<size_t>(R) * 4, 256) + adapter_order_bytes(T, L, true) +
-         adapter_terms_bytes(T, R);
+         adapter_terms_bytes(T, R, L);
 }
 
 bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* dy,

@@ -184,7 +184,7 @@ struct AdaptersBackwardRequest {
 // be sorted by.
 bool adapters_sorted(int64_t T, int64_t L);
 size_t adapter_order_bytes(int64_t T, int64_t L, bool gradients);
-size_t adapter_terms_bytes(int64_t T, int64_t R);
+size_t adapter_terms_bytes(int64_t T, int64_t R, int64_t L);
 int64_t adapters_sort_max();
 cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s);
 
