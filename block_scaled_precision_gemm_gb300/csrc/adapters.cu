@@ -2055,16 +2055,18 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
 template <int RP, int TERMS>
 struct GradTma : GradTile<RP, TERMS> {
   using Base = GradTile<RP, TERMS>;
-  static constexpr int kStages = Base::kStages;
+  // RP = 16: three CTAs fit an SM, whose starts and ends overlap
+  static constexpr int kStages = RP <= 16 ? 3 : Base::kStages;
+  static constexpr int kDecoded = RP <= 16 ? 1 : 2;  // decoded blocks of a checkpoint
   static constexpr int kStageBf16 = Base::kXBytes + Base::kCoefBytes;
   static constexpr int kCodeBytes = kGradRows * kGradCols, kScaleBytes = 1024;  // (a row's four scale bytes: 256, padded)
   static constexpr int kStageCodes = kCodeBytes + kScaleBytes + Base::kCoefBytes;
-  // codes: two decoded blocks before the ring
-  static constexpr int kBf16 = kStages * kStageBf16, kCodes = 2 * Base::kXBytes + kStages * kStageCodes;
+  // codes: the decoded blocks before the ring
+  static constexpr int kBf16 = kStages * kStageBf16, kCodes = kDecoded * Base::kXBytes + kStages * kStageCodes;
   static constexpr int kRing = kBf16 > kCodes ? kBf16 : kCodes;
   static_assert(kGradCols * Base::kPitch * 4 <= kRing, "the sums reuse the ring");
   struct Ctl {
-    uint64_t full[kStages], empty[kStages], decoded[2], done;
+    uint64_t full[kStages], empty[kStages], decoded[kDecoded], done;
     uint32_t tmem;
     int abort_flag;
   };
@@ -2085,7 +2087,7 @@ template <int RP, int TERMS, typename G>
 __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
   using Cfg = GradTma<RP, TERMS>;
   using Coef = typename Cfg::Coef;
-  constexpr int S = Cfg::kStages, kSteps = kGradRows / 16;
+  constexpr int S = Cfg::kStages, ND = Cfg::kDecoded, kSteps = kGradRows / 16;
   extern __shared__ __align__(1024) uint8_t ring[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
   const Grads& p = ps.g;
@@ -2096,7 +2098,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
   const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? p.job[0].tiles : 0)) * kGradCols;
   const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);
   const int a = static_cast<int>(blockIdx.z);
-  const uint32_t ring_at = smem_u32(ring) + (kept ? 2 * Cfg::kXBytes : 0);
+  const uint32_t ring_at = smem_u32(ring) + (kept ? ND * Cfg::kXBytes : 0);
   const uint32_t stage_bytes = kept ? Cfg::kStageCodes : Cfg::kStageBf16;
   const uint32_t coef_off = kept ? Cfg::kCodeBytes + Cfg::kScaleBytes : Cfg::kXBytes;
   if (tid == 0) {
@@ -2104,8 +2106,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
       mbar_init(&ctl.full[i], 1 + kGradHelpers);
       mbar_init(&ctl.empty[i], 1);
     }
-    mbar_init(&ctl.decoded[0], kGradHelpers);
-    mbar_init(&ctl.decoded[1], kGradHelpers);
+    for (int i = 0; i < ND; ++i) mbar_init(&ctl.decoded[i], kGradHelpers);
     mbar_init(&ctl.done, 1);
     ctl.abort_flag = 0;
     fence_barrier_init();
@@ -2149,11 +2150,11 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
       while (walk.next()) {
         const int st = b % S;
         if (!wait(&ctl.full[st], b / S)) break;
-        if (kept && !wait(&ctl.decoded[b & 1], b >> 1)) break;
+        if (kept && !wait(&ctl.decoded[b % ND], b / ND)) break;
         fence_proxy_async_smem();  // what the helpers' copies wrote
         tc_fence_after();
         const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
-        const uint32_t xt = kept ? smem_u32(ring) + (b & 1) * Cfg::kXBytes : at;
+        const uint32_t xt = kept ? smem_u32(ring) + (b % ND) * Cfg::kXBytes : at;
 #pragma unroll
         for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
@@ -2227,9 +2228,9 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
       while (ok && more && d < D) step();
       for (; b < d && ok; ++b) {
         const int st = b % S;
-        ok = wait(&ctl.full[st], b / S) && (b < 2 || wait(&ctl.empty[(b - 2) % S], (b - 2) / S));
-        if (!ok) break;  // (the second: the MMAs have read this half of the decoded blocks)
-        const uint32_t src = ring_at + st * stage_bytes, dst = smem_u32(ring) + (b & 1) * Cfg::kXBytes;
+        ok = wait(&ctl.full[st], b / S) && (b < ND || wait(&ctl.empty[(b - ND) % S], (b - ND) / S));
+        if (!ok) break;  // (the second: the MMAs have read the decoded block that this one replaces)
+        const uint32_t src = ring_at + st * stage_bytes, dst = smem_u32(ring) + (b % ND) * Cfg::kXBytes;
         uint32_t sw;
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw) : "r"(src + Cfg::kCodeBytes + r0 * 4) : "memory");
         const uint32_t sb = (sw >> (8 * blk)) & 0xFFu;
@@ -2244,7 +2245,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
           st_shared16(dst + Cfg::X::at(r0, blk * 4 + e * 2 + 1), w);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&ctl.decoded[b & 1]);
+        mbar_arrive(&ctl.decoded[b % ND]);
         step();
       }
     }
@@ -2443,7 +2444,7 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
   if (e != cudaSuccess) return e;
   const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
   unsigned cs = 1;
-  while (cs < 8 && tiles * p.L * cs < 3 * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
+  while (cs < 8 && tiles * p.L * cs < 4 * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
   const dim3 grid(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L));
   GradTmaArgs a{};
   bool tma = true;
