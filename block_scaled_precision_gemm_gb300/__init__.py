@@ -117,7 +117,7 @@ _SIGS = {
     "bsmm_gated_act_backward": ([_P, _INT, _I64, _I64, _INT, _P, _INT, _P, _INT, _P, _P, _P], _INT),
     "bsmm_linear_backward_checkpoint": ([_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P, _SZ, _P],
                                         _INT),
-    "bsmm_adapters_workspace_size": ([_I64, _I64], _SZ),
+    "bsmm_adapters_workspace_size": ([_I64, _I64, _I64], _SZ),
     "bsmm_adapters": ([_I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _I64, _INT, _P, _P, _SZ,
                        _P], _INT),
     "bsmm_adapters_backward_workspace_size": ([_I64, _I64, _I64], _SZ),
@@ -674,29 +674,34 @@ def gated_act(gate_up, act="silu", h_type="e4m3", code="int8", scale="f32", h_sc
 
     Returns ``(h, h_scales, codes, scales)``; ``h_scales`` is None for
     bfloat16, ``codes`` and ``scales`` are None when nothing is kept."""
-    _want(gate_up, "gate_up", dtypes=_FLOATS)
-    if gate_up.dim() != 2 or gate_up.shape[1] % 2:
-        raise ValueError("gate_up must be a 2-D float32 or bfloat16 tensor [M, 2 I]")
-    M, I = gate_up.shape
-    I //= 2
     ht = BF16 if h_type == "bf16" else _code(h_type)
     quantized = ht != BF16
     c, s = (-1 if code is None else _code(code)), _scale(scale)
     block, scale_dtype = _checkpoint_scales(s)
-    if h is not None:
-        _want(h, "h", (M, I), dtypes=(torch.bfloat16,) if not quantized else None, itemsize=1 if quantized else None)
-    if h_scales is not None:
-        if h_scales_are_atoms:
-            _want(h_scales, "h_scales", min_bytes=scale_atoms_size(1, M, I, ht, SCALE_UE8M0))
-        else:
-            _want(h_scales, "h_scales", (M, I // 32), itemsize=1)
-    if code is None:
-        codes = scales = None
-    if codes is not None:
-        _want(codes, "codes", (M, 2 * I), itemsize=1)
-    if scales is not None:
-        _want(scales, "scales", (M, 2 * I // block), itemsize=scale_dtype.itemsize)
-    dev = _on_device(gate_up=gate_up, h=h, h_scales=h_scales, codes=codes, scales=scales)
+    if (h is None and h_scales is None and codes is None and scales is None and _current(gate_up) and gate_up.dim() == 2
+            and gate_up.dtype in _FLOATS and gate_up.is_contiguous() and gate_up.shape[1] % 2 == 0):
+        dev, (M, I) = gate_up.device, gate_up.shape
+        I //= 2
+    else:
+        _want(gate_up, "gate_up", dtypes=_FLOATS)
+        if gate_up.dim() != 2 or gate_up.shape[1] % 2:
+            raise ValueError("gate_up must be a 2-D float32 or bfloat16 tensor [M, 2 I]")
+        M, I = gate_up.shape
+        I //= 2
+        if h is not None:
+            _want(h, "h", (M, I), dtypes=(torch.bfloat16,) if not quantized else None, itemsize=1 if quantized else None)
+        if h_scales is not None:
+            if h_scales_are_atoms:
+                _want(h_scales, "h_scales", min_bytes=scale_atoms_size(1, M, I, ht, SCALE_UE8M0))
+            else:
+                _want(h_scales, "h_scales", (M, I // 32), itemsize=1)
+        if code is None:
+            codes = scales = None
+        if codes is not None:
+            _want(codes, "codes", (M, 2 * I), itemsize=1)
+        if scales is not None:
+            _want(scales, "scales", (M, 2 * I // block), itemsize=scale_dtype.itemsize)
+        dev = _on_device(gate_up=gate_up, h=h, h_scales=h_scales, codes=codes, scales=scales)
     if h is None:
         h = _empty((M, I), torch.uint8 if quantized else torch.bfloat16, dev, stream)
     if quantized and h_scales is None:
@@ -719,19 +724,26 @@ def gated_act_backward(dh, codes, scales, act="silu", code="int8", scale="f32", 
     """Backward of :func:`gated_act` from its checkpoint: returns
     ``(d_gate_up, h)``, ``d_gate_up`` [M, 2 I] of ``dh``'s type and ``h`` the
     recomputed bfloat16 activation (None without ``return_h``)."""
-    _want(dh, "dh", dtypes=_FLOATS)
-    if dh.dim() != 2:
-        raise ValueError("dh must be a 2-D float32 or bfloat16 tensor [M, I]")
-    M, I = dh.shape
     c, s = _code(code), _scale(scale)
     block, scale_dtype = _checkpoint_scales(s)
-    _want(codes, "codes", (M, 2 * I), itemsize=1)
-    _want(scales, "scales", (M, 2 * I // block), itemsize=scale_dtype.itemsize)
-    if d_gate_up is not None:
-        _want(d_gate_up, "d_gate_up", (M, 2 * I), dtypes=(dh.dtype,))
-    if h is not None:
-        _want(h, "h", (M, I), dtypes=(torch.bfloat16,))
-    dev = _on_device(dh=dh, codes=codes, scales=scales, d_gate_up=d_gate_up, h=h)
+    fit = False
+    if (d_gate_up is None and h is None and _current(dh) and dh.dim() == 2 and dh.dtype in _FLOATS and dh.is_contiguous()
+            and isinstance(codes, torch.Tensor) and codes.element_size() == 1
+            and isinstance(scales, torch.Tensor) and scales.element_size() == scale_dtype.itemsize):
+        dev, (M, I) = dh.device, dh.shape
+        fit = (_fits(codes, codes.dtype, (M, 2 * I), dev) and _fits(scales, scales.dtype, (M, 2 * I // block), dev))
+    if not fit:
+        _want(dh, "dh", dtypes=_FLOATS)
+        if dh.dim() != 2:
+            raise ValueError("dh must be a 2-D float32 or bfloat16 tensor [M, I]")
+        M, I = dh.shape
+        _want(codes, "codes", (M, 2 * I), itemsize=1)
+        _want(scales, "scales", (M, 2 * I // block), itemsize=scale_dtype.itemsize)
+        if d_gate_up is not None:
+            _want(d_gate_up, "d_gate_up", (M, 2 * I), dtypes=(dh.dtype,))
+        if h is not None:
+            _want(h, "h", (M, I), dtypes=(torch.bfloat16,))
+        dev = _on_device(dh=dh, codes=codes, scales=scales, d_gate_up=d_gate_up, h=h)
     if d_gate_up is None:
         d_gate_up = _empty((M, 2 * I), dh.dtype, dev, stream)
     if return_h and h is None:
@@ -747,34 +759,43 @@ def linear_backward_checkpoint(dY, W, x_codes, x_scales, x_code="e4m3", x_scale=
     """:func:`linear_backward` with X kept in 8 bits (:func:`quantize` with
     blocks of 1 x 32 UE8M0 or 1 x 128 F32): returns ``(dX, dW)`` in bfloat16."""
     bf16 = (torch.bfloat16,)
-    for t, n in ((dY, "dY"), (W, "W")):
-        _want(t, n, dtypes=bf16)
-        if t.dim() != 2:
-            raise ValueError(f"{n} must be a 2-D bfloat16 tensor")
-    M, N = dY.shape
-    K = W.shape[1]
     c, s = _code(x_code), _scale(x_scale)
     block, scale_dtype = _checkpoint_scales(s)
-    _want(W, "W", (N, K))
-    _want(x_codes, "x_codes", (M, K), itemsize=1)
-    if K % block == 0:  # else the library says why
-        _want(x_scales, "x_scales", (M, K // block), itemsize=scale_dtype.itemsize)
-    if dX is not None:
-        _want(dX, "dX", (M, K), dtypes=bf16)
-    if dW is not None:
-        _want(dW, "dW", (N, K), dtypes=bf16)
-    if workspace is not None:
-        _want(workspace, "workspace")
-    dev = _on_device(dY=dY, W=W, x_codes=x_codes, x_scales=x_scales, dX=dX, dW=dW, workspace=workspace)
+    fit = False
+    if (dX is None and dW is None and workspace is None and _current(dY) and dY.dim() == 2 and isinstance(W, torch.Tensor)
+            and W.dim() == 2 and isinstance(x_codes, torch.Tensor) and x_codes.element_size() == 1
+            and isinstance(x_scales, torch.Tensor) and x_scales.element_size() == scale_dtype.itemsize):
+        dev, (M, N), K = dY.device, dY.shape, W.shape[1]
+        fit = (K % block == 0 and _fits(dY, torch.bfloat16, (M, N), dev) and _fits(W, torch.bfloat16, (N, K), dev)
+               and _fits(x_codes, x_codes.dtype, (M, K), dev) and _fits(x_scales, x_scales.dtype, (M, K // block), dev))
+    if not fit:
+        for t, n in ((dY, "dY"), (W, "W")):
+            _want(t, n, dtypes=bf16)
+            if t.dim() != 2:
+                raise ValueError(f"{n} must be a 2-D bfloat16 tensor")
+        M, N = dY.shape
+        K = W.shape[1]
+        _want(W, "W", (N, K))
+        _want(x_codes, "x_codes", (M, K), itemsize=1)
+        if K % block == 0:  # else the library says why
+            _want(x_scales, "x_scales", (M, K // block), itemsize=scale_dtype.itemsize)
+        if dX is not None:
+            _want(dX, "dX", (M, K), dtypes=bf16)
+        if dW is not None:
+            _want(dW, "dW", (N, K), dtypes=bf16)
+        if workspace is not None:
+            _want(workspace, "workspace")
+        dev = _on_device(dY=dY, W=W, x_codes=x_codes, x_scales=x_scales, dX=dX, dW=dW, workspace=workspace)
     if dX is None:
         dX = _empty((M, K), torch.bfloat16, dev, stream)
     if dW is None:
         dW = _empty((N, K), torch.bfloat16, dev, stream)
     if workspace is None:
         workspace = _empty(max(linear_backward_workspace_size(M, N, K), 1), torch.uint8, dev, stream)
-    _check(lib().bsmm_linear_backward_checkpoint(_ptr(dY), _ptr(W), _ptr(x_codes), c, _ptr(x_scales), s, M, N, K,
-                                                 _code(fp8), _ptr(dX), _ptr(dW), _ptr(workspace), _nbytes(workspace),
-                                                 _stream(stream)), "bsmm_linear_backward_checkpoint")
+    _check(lib().bsmm_linear_backward_checkpoint(dY.data_ptr(), W.data_ptr(), x_codes.data_ptr(), c, x_scales.data_ptr(),
+                                                 s, M, N, K, _code(fp8), dX.data_ptr(), dW.data_ptr(),
+                                                 workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev)),
+           "bsmm_linear_backward_checkpoint")
     return dX, dW
 
 
@@ -808,8 +829,8 @@ def _adapter_weights(a, b, ids, scaling, T):
     return L, R, K, N
 
 
-def adapters_workspace_size(T, L) -> int:
-    return lib().bsmm_adapters_workspace_size(T, L)
+def adapters_workspace_size(T, R, L) -> int:
+    return lib().bsmm_adapters_workspace_size(T, R, L)
 
 
 def adapters(x, a, b, ids, y=None, scaling=None, out=None, u=None, out_dtype=torch.bfloat16, workspace=None,
@@ -859,7 +880,7 @@ def adapters(x, a, b, ids, y=None, scaling=None, out=None, u=None, out_dtype=tor
     if u is None:
         u = _empty((T, R), torch.float32, dev, stream)
     if workspace is None:
-        need = adapters_workspace_size(T, L)
+        need = adapters_workspace_size(T, R, L)
         if need:
             workspace = _empty((need,), torch.uint8, dev, stream)
     _check(lib().bsmm_adapters(T, K, N, R, L, x.data_ptr(), ld_x, a.data_ptr(), b.data_ptr(), ids.data_ptr(),

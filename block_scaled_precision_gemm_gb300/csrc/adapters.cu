@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -140,7 +141,7 @@ __device__ __forceinline__ int adapter_of(const int* ids, int64_t t, int64_t T, 
 }
 
 // ---------------------------------------------------------------------------
-// u = W[id] x: a long contraction into R sums per token
+// Few tokens: both products in one launch, tokens taken as they come
 // ---------------------------------------------------------------------------
 struct Down {
   const bf16* x;  // [T][ld]
@@ -150,167 +151,7 @@ struct Down {
   float* u;  // [T][R]
   int64_t T, C;
   int R, L;
-  int rows_per_tile;  // rows of a warp's tile in use (<= 16 MT)
 };
-
-// Column of the result that accumulator column n of n-tile j holds.
-template <bool TRANS>
-__device__ __forceinline__ int down_col(int j, int n, int nt) {
-  if constexpr (!TRANS) return j * 8 + n;
-  if (nt == 1) return n;
-  return (j / 2) * 16 + (n / 2) * 4 + 2 * (j % 2) + (n % 2);
-}
-
-// For few tokens, taken as they come.  A CTA takes up to 16 rows; the
-// contraction is split over its WK warps and over the CTAs of the cluster.  The
-// partial sums are added in a fixed order: over the warps through shared
-// memory, over the cluster through distributed shared memory, each CTA summing
-// a share of the tile.
-template <int NT, int WK, bool TRANS, bool VEC, int UNROLL>
-__global__ void __launch_bounds__(WK * 32, NT <= 2 ? 3 : (NT <= 4 ? 2 : 1)) adapter_down(const Down p) {
-  constexpr int MT = 1, kRows = 16, kCols = NT * 8;
-  extern __shared__ float part[];  // [WK][kRows][kCols]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int wk = warp;
-  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);  // a cluster spans y
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_tile;
-  const int tile_rows = p.rows_per_tile;
-
-  int id = -1;  // lane i: the adapter of the warp's row i
-  if (lane < tile_rows) id = adapter_of(p.ids, row0 + lane, p.T, p.L);
-
-  float* mine = part + wk * kRows * kCols;
-#pragma unroll
-  for (int i = lane; i < MT * 16 * kCols; i += 32) mine[i] = 0.f;
-  __syncwarp();
-
-  const bf16* xr[MT][2];
-  bool use[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = m * 16 + h * 8 + g;
-      use[m][h] = __shfl_sync(0xFFFFFFFFu, id, i) >= 0;
-      xr[m][h] = p.x + (use[m][h] ? row0 + i : 0) * p.ld;
-    }
-  // this warp's chunks of 32 along the contraction
-  const int64_t chunks = (p.C + 31) / 32;
-  const int64_t parts = static_cast<int64_t>(cs) * WK, at = static_cast<int64_t>(rank) * WK + wk;
-  const int64_t k_begin = chunks * at / parts * 32, k_end = chunks * (at + 1) / parts * 32;
-
-  unsigned left = __ballot_sync(0xFFFFFFFFu, id >= 0);
-  while (left) {
-    const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
-    const unsigned same = __ballot_sync(0xFFFFFFFFu, id == a);
-    left &= ~same;
-    const bf16* w = p.w + static_cast<int64_t>(a) * p.R * p.C;
-    float acc[MT][NT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-#pragma unroll UNROLL
-    for (int64_t k = k_begin; k < k_end; k += 32) {
-      // lane q's 8 columns of the chunk are k + 8 q ..; MMA step s takes words
-      // 2 s and 2 s + 1 of them as its logical columns 2q.. and 2q + 8..
-      uint32_t xa[MT][2][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (use[m][h])
-            load_row<8, VEC>(xr[m][h], k + 8 * q, p.C, xa[m][h]);
-          else
-            xa[m][h][0] = xa[m][h][1] = xa[m][h][2] = xa[m][h][3] = 0u;
-        }
-      uint32_t wb[NT][4];  // [n-tile][2 s + half]
-      if constexpr (!TRANS) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int r = j * 8 + g;
-          if (r < p.R)
-            load_row<8, VEC>(w + static_cast<int64_t>(r) * p.C, k + 8 * q, p.C, wb[j]);
-          else
-            wb[j][0] = wb[j][1] = wb[j][2] = wb[j][3] = 0u;
-        }
-      } else {
-#pragma unroll
-        for (int sh = 0; sh < 4; ++sh) {  // step s = sh / 2, half = sh % 2
-          const int64_t c = k + (g / 2) * 8 + sh * 2 + (g % 2);  // the row of W that logical row g of this half is
-          const bf16* row = w + c * p.R;
-          const int64_t lim = c < p.C ? p.R : 0;
-          if constexpr (NT == 1) {
-            uint32_t v[1];
-            load_row<2, VEC>(row, 2 * q, lim, v);
-            wb[0][sh] = transpose8x8(v[0]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < NT; j += 2) {
-              uint32_t v[2];
-              load_row<4, VEC>(row, j * 8 + 4 * q, lim, v);
-              wb[j][sh] = transpose8x8(v[0]);
-              wb[j + 1][sh] = transpose8x8(v[1]);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            mma_bf16(acc[m][j], xa[m][0][2 * s], xa[m][1][2 * s], xa[m][0][2 * s + 1], xa[m][1][2 * s + 1],
-                     wb[j][2 * s], wb[j][2 * s + 1]);
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = m * 16 + h * 8 + g;
-        if ((same >> i) & 1u) {
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) mine[i * kCols + down_col<TRANS>(j, 2 * q + e, NT)] = acc[m][j][2 * h + e];
-        }
-      }
-  }
-  __syncthreads();
-  constexpr int kThreads = WK * 32, kElems = kRows * kCols;
-  if constexpr (WK > 1) {  // over the warps
-    for (int i = tid; i < kElems; i += kThreads) {
-      float v = part[i];
-#pragma unroll
-      for (int w = 1; w < WK; ++w) v += part[w * kElems + i];
-      part[i] = v;
-    }
-  }
-  if (cs > 1) {
-    __syncwarp();
-    cluster_sync();
-  } else {
-    __syncthreads();
-  }
-  grid_launch_dependents();
-  const int rows_here = static_cast<int>(min(static_cast<int64_t>(tile_rows), p.T - row0));
-  const int n = rows_here * p.R, share = (n + cs - 1) / cs;
-  const int e_end = min(n, (rank + 1) * share);
-  for (int e = rank * share + tid; e < e_end; e += kThreads) {
-    const int r = e / p.R, c = e - r * p.R;
-    p.u[(row0 + r) * p.R + c] = cs > 1 ? cluster_sum(part + r * kCols + c, cs) : part[r * kCols + c];
-  }
-  __syncwarp();
-  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
-}
-
-// ---------------------------------------------------------------------------
-// out = base + s[id] W[id] u: R products into a long row
-// ---------------------------------------------------------------------------
 struct Up {
   const float* u;  // [T][R]
   const bf16* w;   // TRANS = false: [L][C][R] (R contiguous); true: [L][R][C]
@@ -322,8 +163,6 @@ struct Up {
   int64_t ld_out;
   int64_t T, C;
   int R, L;
-  int rows_per_tile;
-  int cols_per_warp;  // a multiple of 32
 };
 
 // Eight consecutive elements of a row as binary32 (zeros from `limit` on).
@@ -379,83 +218,229 @@ __device__ __forceinline__ void store_out(Y* row, int64_t c, int64_t limit, cons
   }
 }
 
-// A warp holds its rows' u as A fragments, split into TERMS bf16 terms so that
-// u keeps its binary32 precision (three terms for binary32 outputs, 16 bits of
-// it for bf16 ones), and runs along its columns, 32 at a time: lane q of each
-// row ends up with 8 consecutive outputs.
-template <int KT, int WN, typename Y, bool TRANS, bool VEC>
-__global__ void __launch_bounds__(WN * 32) adapter_up(const Up p) {
-  constexpr int MT = 1;
-  constexpr int TERMS = sizeof(Y) == 4 ? 3 : 2;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Column of the result that accumulator column n of n-tile j holds.
+template <bool TRANS>
+__device__ __forceinline__ int down_col(int j, int n, int nt) {
+  if constexpr (!TRANS) return j * 8 + n;
+  if (nt == 1) return n;
+  return (j / 2) * 16 + (n / 2) * 4 + 2 * (j % 2) + (n % 2);
+}
+
+struct Rows {
+  Down d;
+  Up u;               // its u is d's
+  int rows_per_tile;  // of a cluster, at most 16
+};
+
+// Asks for `bytes` from p on to be brought to the L2 cache, by a warp.
+__device__ __forceinline__ void prefetch_span(const void* p, int64_t bytes, int lane) {
+  const uint8_t* at = static_cast<const uint8_t*>(p);
+  for (int64_t i = lane * 128; i < bytes; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+}
+__device__ __forceinline__ void prefetch_rows(const void* p, int rows, int64_t pitch, int64_t bytes, int lane) {
+  const uint8_t* at = static_cast<const uint8_t*>(p);
+  for (int r = lane; r < rows; r += 32)
+    for (int64_t i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + r * pitch + i));
+}
+
+// A cluster takes up to 16 rows.  First their u: the contraction is split over
+// the cluster's CTAs and each CTA's 8 warps, and the partial sums are added in
+// a fixed order, over the warps in shared memory, over the cluster through
+// distributed shared memory (each CTA sums them all, and stores a share).  Then
+// the outputs' columns are split over the CTAs and warps: a warp holds the
+// rows' u as A fragments, split into TERMS bf16 terms so that u keeps its
+// binary32 precision (three terms for binary32 outputs, 16 bits of it for bf16
+// ones), and takes 32 columns at a time: lane q of each row ends up with 8
+// consecutive outputs.  At these sizes latency is what counts: one launch, and
+// no trip of u through memory (two launches took 13 + 10 us for 64 requests of
+// 4096 x 4096 and rank 16).
+template <int NT, typename Y, bool TRANS, bool VEC, int UNROLL>
+__global__ void __launch_bounds__(256, NT <= 2 && !TRANS ? 3 : (NT <= 4 ? 2 : 1)) adapter_rows(const __grid_constant__ Rows pr) {
+  constexpr int WK = 8, kRows = 16, kCols = NT * 8;
+  constexpr int KT = (NT + 1) / 2, TERMS = sizeof(Y) == 4 ? 3 : 2;
+  extern __shared__ float part[];  // [WK][kRows][kCols] partial sums, then u: [kRows][KT * 16]
+  float* whole = part + WK * kRows * kCols;
+  const Down& p = pr.d;
+  const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int tile_rows = p.rows_per_tile;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tile_rows;
-  const int64_t n_begin = (static_cast<int64_t>(blockIdx.y) * WN + warp) * p.cols_per_warp;
-  const int64_t n_end = min(n_begin + p.cols_per_warp, p.C);
+  const int rank = static_cast<int>(blockIdx.y), cs = static_cast<int>(gridDim.y);  // a cluster spans y
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * pr.rows_per_tile;
+  grid_launch_dependents();
 
-  int id = -1;
-  if (lane < tile_rows) id = adapter_of(p.ids, row0 + lane, p.T, p.L);
+  int id = -1;  // lane i: the adapter of row i
+  if (lane < pr.rows_per_tile) id = adapter_of(p.ids, row0 + lane, p.T, p.L);
   const unsigned any = __ballot_sync(0xFFFFFFFFu, id >= 0);
-
-  int64_t row[MT][2];
-  bool live[MT][2], has[MT][2];
-  float sc[MT][2];
+  bool use[2];
+  const bf16* xr[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int h = 0; h < 2; ++h) {
+    use[h] = (any >> (h * 8 + g)) & 1u;
+    xr[h] = p.x + (use[h] ? row0 + h * 8 + g : 0) * p.ld;
+  }
+  {
+    float* mine = part + wk * kRows * kCols;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = m * 16 + h * 8 + g;
-      row[m][h] = row0 + i;
-      live[m][h] = i < tile_rows && row[m][h] < p.T;
-      const int a = __shfl_sync(0xFFFFFFFFu, id, i);
-      has[m][h] = a >= 0;
-      sc[m][h] = a >= 0 ? (p.scaling ? __ldg(p.scaling + a) : 1.f) : 0.f;
-    }
-  grid_dependency_wait();  // u is the launch before this one's
-  // fragment of step ks: lane q's four consecutive ranks 16 ks + 4 q ..
-  uint32_t ua[MT][KT][2][2][TERMS];  // [m][ks][row half][rank pair][term]
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int ks = 0; ks < KT; ++ks)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = ks * 16 + 4 * q + e;
-          v[e] = has[m][h] && r < p.R ? p.u[row[m][h] * p.R + r] : 0.f;
-        }
-        split_pair<TERMS>(v[0], v[1], ua[m][ks][h][0]);
-        split_pair<TERMS>(v[2], v[3], ua[m][ks][h][1]);
-      }
-
-  for (int64_t n = n_begin; n < n_end; n += 32) {
-    float y[MT][2][8];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (p.base && live[m][h])
-          load_out<Y, VEC>(static_cast<const Y*>(p.base) + row[m][h] * p.ld_base, n + 8 * q, p.C, y[m][h]);
-        else
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[m][h][e] = 0.f;
-      }
+    for (int i = lane; i < kRows * kCols; i += 32) mine[i] = 0.f;
+    __syncwarp();
+    // this warp's chunks of 32 along the contraction
+    const int64_t chunks = (p.C + 31) / 32;
+    const int64_t parts = static_cast<int64_t>(cs) * WK, at = static_cast<int64_t>(rank) * WK + wk;
+    const int64_t k_begin = chunks * at / parts * 32, k_end = chunks * (at + 1) / parts * 32;
+    // the weights that this warp comes to after its first adapter's
     unsigned left = any;
+    for (bool first = true; left; first = false) {
+      const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
+      left &= ~__ballot_sync(0xFFFFFFFFu, id == a);
+      if (!first) {
+        const bf16* w = p.w + static_cast<int64_t>(a) * p.R * p.C;
+        const int64_t cols = min(k_end, p.C) - k_begin;
+        if constexpr (TRANS)
+          prefetch_span(w + k_begin * p.R, cols * p.R * 2, lane);
+        else
+          prefetch_rows(w + k_begin, p.R, p.C * 2, cols * 2, lane);
+      }
+      const bf16* w = pr.u.w + static_cast<int64_t>(a) * pr.u.R * pr.u.C;
+      for (int64_t n = at * 32; n < pr.u.C; n += parts * 32) {
+        const int64_t cols = min(static_cast<int64_t>(32), pr.u.C - n);
+        if constexpr (TRANS)
+          prefetch_rows(w + n, pr.u.R, pr.u.C * 2, cols * 2, lane);
+        else
+          prefetch_span(w + n * pr.u.R, cols * pr.u.R * 2, lane);
+      }
+    }
+    left = any;
     while (left) {
       const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
       const unsigned same = __ballot_sync(0xFFFFFFFFu, id == a);
       left &= ~same;
       const bf16* w = p.w + static_cast<int64_t>(a) * p.R * p.C;
-      float acc[MT][4][4];
+      float acc[NT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll UNROLL
+      for (int64_t k = k_begin; k < k_end; k += 32) {
+        // lane q's 8 columns of the chunk are k + 8 q ..; MMA step s takes words
+        // 2 s and 2 s + 1 of them as its logical columns 2q.. and 2q + 8..
+        uint32_t xa[2][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+        for (int h = 0; h < 2; ++h) {
+          if (use[h])
+            load_row<8, VEC>(xr[h], k + 8 * q, p.C, xa[h]);
+          else
+            xa[h][0] = xa[h][1] = xa[h][2] = xa[h][3] = 0u;
+        }
+        uint32_t wb[NT][4];  // [n-tile][2 s + half]
+        if constexpr (!TRANS) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const int r = j * 8 + g;
+            if (r < p.R)
+              load_row<8, VEC>(w + static_cast<int64_t>(r) * p.C, k + 8 * q, p.C, wb[j]);
+            else
+              wb[j][0] = wb[j][1] = wb[j][2] = wb[j][3] = 0u;
+          }
+        } else {
+#pragma unroll
+          for (int sh = 0; sh < 4; ++sh) {  // step s = sh / 2, half = sh % 2
+            const int64_t c = k + (g / 2) * 8 + sh * 2 + (g % 2);  // the row of W that logical row g of this half is
+            const bf16* row = w + c * p.R;
+            const int64_t lim = c < p.C ? p.R : 0;
+            if constexpr (NT == 1) {
+              uint32_t v[1];
+              load_row<2, VEC>(row, 2 * q, lim, v);
+              wb[0][sh] = transpose8x8(v[0]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < NT; j += 2) {
+                uint32_t v[2];
+                load_row<4, VEC>(row, j * 8 + 4 * q, lim, v);
+                wb[j][sh] = transpose8x8(v[0]);
+                wb[j + 1][sh] = transpose8x8(v[1]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mma_bf16(acc[j], xa[0][2 * s], xa[1][2 * s], xa[0][2 * s + 1], xa[1][2 * s + 1], wb[j][2 * s],
+                     wb[j][2 * s + 1]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = h * 8 + g;
+        if ((same >> i) & 1u) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mine[i * kCols + down_col<TRANS>(j, 2 * q + e, NT)] = acc[j][2 * h + e];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < kRows * kCols; i += 256) {  // over the warps
+    float v = part[i];
+#pragma unroll
+    for (int w = 1; w < WK; ++w) v += part[w * kRows * kCols + i];
+    part[i] = v;
+  }
+  if (cs > 1) {
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  const int rows_here = static_cast<int>(min(static_cast<int64_t>(pr.rows_per_tile), p.T - row0));
+  for (int i = tid; i < kRows * KT * 16; i += 256) {  // over the cluster
+    const int r = i / (KT * 16), c = i % (KT * 16);
+    float v = 0.f;
+    if (c < p.R && r < rows_here) v = cs > 1 ? cluster_sum(part + r * kCols + c, cs) : part[r * kCols + c];
+    whole[i] = v;
+    if (c < p.R && r < rows_here && r % cs == rank) p.u[(row0 + r) * p.R + c] = v;
+  }
+  __syncthreads();
+
+  const Up& o = pr.u;
+  // fragment of step ks: lane q's four consecutive ranks 16 ks + 4 q ..
+  uint32_t ua[KT][2][2][TERMS];  // [ks][row half][rank pair][term]
+  float sc[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int a = __shfl_sync(0xFFFFFFFFu, id, h * 8 + g);
+    sc[h] = a >= 0 ? (o.scaling ? __ldg(o.scaling + a) : 1.f) : 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KT; ++ks) {
+      const float4 v = *reinterpret_cast<const float4*>(whole + (h * 8 + g) * KT * 16 + ks * 16 + 4 * q);
+      split_pair<TERMS>(v.x, v.y, ua[ks][h][0]);
+      split_pair<TERMS>(v.z, v.w, ua[ks][h][1]);
+    }
+  }
+  const int64_t step = static_cast<int64_t>(cs) * WK * 32;
+  for (int64_t n = (static_cast<int64_t>(rank) * WK + wk) * 32; n < o.C; n += step) {
+    float y[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (o.base && h * 8 + g < rows_here)
+        load_out<Y, VEC>(static_cast<const Y*>(o.base) + (row0 + h * 8 + g) * o.ld_base, n + 8 * q, o.C, y[h]);
+      else
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[h][e] = 0.f;
+    }
+    unsigned left = any;
+    while (left) {
+      const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
+      const unsigned same = __ballot_sync(0xFFFFFFFFu, id == a);
+      left &= ~same;
+      const bf16* w = o.w + static_cast<int64_t>(a) * o.R * o.C;
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KT; ++ks) {
         uint32_t wb[4][2];  // [n-tile][half]
@@ -463,14 +448,14 @@ __global__ void __launch_bounds__(WN * 32) adapter_up(const Up p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // accumulator column g of n-tile j is column (g / 2) * 8 + 2 j + g % 2
             const int64_t c = n + (g / 2) * 8 + 2 * j + (g % 2);
-            load_row<4, VEC>(w + c * p.R, ks * 16 + 4 * q, c < p.C ? p.R : 0, wb[j]);
+            load_row<4, VEC>(w + c * o.R, ks * 16 + 4 * q, c < o.C ? o.R : 0, wb[j]);
           }
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // logical rank g of half h is 16 ks + (g / 2) * 4 + 2 h + g % 2
             const int r = ks * 16 + (g / 2) * 4 + 2 * h + (g % 2);
             uint32_t v[4];
-            load_row<8, VEC>(w + static_cast<int64_t>(r) * p.C, n + 8 * q, r < p.R ? p.C : 0, v);
+            load_row<8, VEC>(w + static_cast<int64_t>(r) * o.C, n + 8 * q, r < o.R ? o.C : 0, v);
 #pragma unroll
             for (int j = 0; j < 4; ++j) wb[j][h] = transpose8x8(v[j]);
           }
@@ -478,30 +463,25 @@ __global__ void __launch_bounds__(WN * 32) adapter_up(const Up p) {
 #pragma unroll
         for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_bf16(acc[m][j], ua[m][ks][0][0][k], ua[m][ks][1][0][k], ua[m][ks][0][1][k], ua[m][ks][1][1][k],
-                       wb[j][0], wb[j][1]);
+          for (int j = 0; j < 4; ++j)
+            mma_bf16(acc[j], ua[ks][0][0][k], ua[ks][1][0][k], ua[ks][0][1][k], ua[ks][1][1][k], wb[j][0], wb[j][1]);
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int h = 0; h < 2; ++h)
+        if ((same >> (h * 8 + g)) & 1u) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if ((same >> (m * 16 + h * 8 + g)) & 1u) {
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                y[m][h][2 * j + e] = fmaf(sc[m][h], acc[m][j][2 * h + e], y[m][h][2 * j + e]);
-          }
+            for (int e = 0; e < 2; ++e) y[h][2 * j + e] = fmaf(sc[h], acc[j][2 * h + e], y[h][2 * j + e]);
+        }
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (live[m][h]) store_out<Y, VEC>(static_cast<Y*>(p.out) + row[m][h] * p.ld_out, n + 8 * q, p.C, y[m][h]);
+    for (int h = 0; h < 2; ++h)
+      if (h * 8 + g < rows_here)
+        store_out<Y, VEC>(static_cast<Y*>(o.out) + (row0 + h * 8 + g) * o.ld_out, n + 8 * q, o.C, y[h]);
   }
+  __syncwarp();
+  if (cs > 1) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -581,29 +561,41 @@ __device__ __forceinline__ Tile sorted_piece(const int* first, const int* piece0
   return t;
 }
 
-__global__ void __launch_bounds__(kSortThreads) adapter_sort(const int* ids, int64_t T, int L, Order o) {
+struct SortArgs {
+  const int* ids;
+  int64_t T;
+  int L;
+  Order o;
+};
+__global__ void __launch_bounds__(kSortThreads) adapter_sort(const SortArgs p) {
+  const int* ids = p.ids;
+  const int64_t T = p.T;
+  const int L = p.L;
+  const Order& o = p.o;
   // [kSortWarps][L + 1]: tokens of each adapter, then those before the warp's; then the order itself
   extern __shared__ uint16_t hist[];
   __shared__ int first[kSortMaxL + 2], tile0[kSortMaxL + 2], block0[kSortMaxL + 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = L + 1;
   uint16_t* perm = hist + kSortWarps * G;
   const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kSegment;
+  grid_launch_dependents();
   for (int i = tid; i < kSortWarps * G; i += kSortThreads) hist[i] = 0;
+  const int rounds = static_cast<int>(min(static_cast<int64_t>(kSegment), T - s0) + kSortThreads - 1) / kSortThreads;
   int key[kSortRounds], rank[kSortRounds];
 #pragma unroll
   for (int i = 0; i < kSortRounds; ++i) {
-    const int64_t t = s0 + (warp * kSortRounds + i) * 32 + lane;
+    const int64_t t = s0 + (warp * rounds + i) * 32 + lane;
     key[i] = -1;
-    if (t < T) {
+    if (i < rounds && t < T) {
       const int a = __ldg(ids + t);
       key[i] = a >= 0 && a < L ? a : L;
     }
   }
   __syncthreads();
-  grid_launch_dependents();
   uint16_t* mine = hist + warp * G;
 #pragma unroll
   for (int i = 0; i < kSortRounds; ++i) {
+    if (i >= rounds) break;
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, key[i]);
     const unsigned before = peers & ((1u << lane) - 1u);
     if (key[i] >= 0) rank[i] = mine[key[i]] + __popc(before);
@@ -646,13 +638,14 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const int* ids, int
 #pragma unroll
   for (int i = 0; i < kSortRounds; ++i)
     if (key[i] >= 0) {
-      const int at = first[key[i]] + mine[key[i]] + rank[i], t = (warp * kSortRounds + i) * 32 + lane;
+      const int at = first[key[i]] + mine[key[i]] + rank[i], t = (warp * rounds + i) * 32 + lane;
       perm[at] = static_cast<uint16_t>(t);
       o.perm[s0 + at] = static_cast<int>(s0) + t;
     }
   if (warp == 0) group_pieces(first, tile0, G, kTileRows);
   if (warp == 1) group_pieces(first, block0, G, kGradRows);
   __syncthreads();
+  grid_dependency_wait();  // (beside adapter_rows: its end is then part of this launch's)
   Tile* tiles = o.tiles + static_cast<int64_t>(blockIdx.x) * o.tiles_per_segment;
   for (int i = tid; i < o.tiles_per_segment; i += kSortThreads)
     tiles[i] = sorted_piece(first, tile0, perm, G, kTileRows, static_cast<int>(s0), i);
@@ -746,6 +739,34 @@ struct Waits {
 };
 constexpr int kSiteDown = 41, kSiteUp = 42, kSiteGrads = 43;
 
+// A long sum is dealt to kSums accumulators of RP columns each in tensor memory,
+// joined here in order: the tensor cores add with truncation, and its drift
+// grows with the number of additions into one accumulator (4096 contraction
+// columns into one: 2e-6 of the result, against 1e-6 for sums in registers).
+template <int RP>
+struct Sums {
+  static constexpr int kSums = RP <= 64 ? 4 : 2;
+  static constexpr int kTmem = kSums * RP < 32 ? 32 : kSums * RP;
+};
+// 16 columns from tensor memory, of the first n accumulators, to dst.
+template <int RP>
+__device__ __forceinline__ void read_sums16(uint32_t tmem, int n, float* dst) {
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < Sums<RP>::kSums; ++k)
+    if (k < n) {
+      uint32_t w[16];
+      tmem_ld16(tmem + k * RP, w);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
+    }
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+}
+
 // ---------------------------------------------------------------------------
 // u = W x for a tile of 128 tokens of one adapter
 // ---------------------------------------------------------------------------
@@ -768,7 +789,7 @@ struct DownTile {
   static_assert(kTileRows * kPitch * 4 <= kRing, "the sums reuse the ring");
   using Ctl = Control<kStages>;
   static constexpr int kSmem = kRing + static_cast<int>(sizeof(Ctl));
-  static constexpr int kTmem = RP < 32 ? 32 : RP;
+  static constexpr int kSums = Sums<RP>::kSums, kTmem = Sums<RP>::kTmem;
 };
 
 // A CTA's share of the sums of its cluster into the rows of u that the tile's
@@ -891,8 +912,8 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
       const uint32_t at = ring_at + (c % S) * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
 #pragma unroll
       for (int s = 0; s < kChunk / 16; ++s)
-        mma_f16(tmem, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
-                mma_shape(RP, false, TRANS), (c > 0 || s > 0) ? 1u : 0u);
+        mma_f16(tmem + (c % Cfg::kSums) * RP, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
+                mma_shape(RP, false, TRANS), (c >= Cfg::kSums || s > 0) ? 1u : 0u);
       tc_commit(&ctl.done[c % S]);
     }
     if (c + S - 1 < n) {
@@ -910,14 +931,7 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int j = 0; j < kHalf; j += 16) {
-        uint32_t v[16];
-        tmem_ld16(src + j, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<uint4*>(dst + j + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-      }
+      for (int j = 0; j < kHalf; j += 16) read_sums16<RP>(src + j, c, dst + j);
     }
   }
   tc_fence_before();
@@ -1285,7 +1299,7 @@ struct GradTile {
   static constexpr int kCtlAt = kIdxAt + kIdxSlots * kGradRows * 4;
   static_assert(kGradCols * kPitch * 4 <= kCtlAt, "the sums reuse the space before");
   static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
-  static constexpr int kTmem = RP < 32 ? 32 : RP;
+  static constexpr int kSums = Sums<RP>::kSums, kTmem = Sums<RP>::kTmem;
 };
 
 // An adapter's blocks of 64 tokens that fall to one CTA of a cluster of cs:
@@ -1501,8 +1515,8 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-          mma_f16(tmem, Cfg::X::along_rows(xt, s), Cfg::Coef::along_rows(ct + k * Cfg::kTermBytes, s),
-                  mma_shape(RP, true, true), (b > 0 || k < TERMS - 1 || s > 0) ? 1u : 0u);
+          mma_f16(tmem + (b % Cfg::kSums) * RP, Cfg::X::along_rows(xt, s), Cfg::Coef::along_rows(ct + k * Cfg::kTermBytes, s),
+                  mma_shape(RP, true, true), (b >= Cfg::kSums || k < TERMS - 1 || s > 0) ? 1u : 0u);
       tc_commit(&ctl.done[b & 1]);
     }
     if (b > 0)
@@ -1529,19 +1543,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int k = 0; k < kHalf; k += 16) {
-        uint32_t v[16];
-        if (b > 0) {
-          tmem_ld16(src + k, v);
-          tmem_wait_ld();
-        } else {  // no block: zeros
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<uint4*>(dst + k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-      }
+      for (int k = 0; k < kHalf; k += 16) read_sums16<RP>(src + k, b, dst + k);
     }
   }
   tc_fence_before();
@@ -1699,8 +1701,8 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
         const uint32_t at = ring_at + st * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
 #pragma unroll
         for (int s = 0; s < kChunk / 16; ++s)
-          mma_f16(tmem, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
-                  mma_shape(RP, false, TRANS), (c > 0 || s > 0) ? 1u : 0u);
+          mma_f16(tmem + (c % Cfg::kSums) * RP, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
+                  mma_shape(RP, false, TRANS), (c >= Cfg::kSums || s > 0) ? 1u : 0u);
         tc_commit(&ctl.empty[st]);
       }
       tc_commit(&ctl.done);
@@ -1746,14 +1748,7 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int j = 0; j < RP; j += 16) {
-      uint32_t v[16];
-      tmem_ld16(tmem + (q * 32u << 16) + j, v);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<uint4*>(dst + j + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-    }
+    for (int j = 0; j < RP; j += 16) read_sums16<RP>(tmem + (q * 32u << 16) + j, n, dst + j);
   }
   tc_fence_before();
   __syncthreads();
@@ -2159,8 +2154,8 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
         for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
           for (int s = 0; s < kSteps; ++s)
-            mma_f16(tmem, Cfg::X::along_rows(xt, s), Coef::along_rows(ct + k * Cfg::kTermBytes, s),
-                    mma_shape(RP, true, true), (b > 0 || k < TERMS - 1 || s > 0) ? 1u : 0u);
+            mma_f16(tmem + (b % Cfg::kSums) * RP, Cfg::X::along_rows(xt, s), Coef::along_rows(ct + k * Cfg::kTermBytes, s),
+                    mma_shape(RP, true, true), (b >= Cfg::kSums || k < TERMS - 1 || s > 0) ? 1u : 0u);
         tc_commit(&ctl.empty[st]);
         ++b;
       }
@@ -2259,26 +2254,14 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
     for (int i = b > S ? b - S : 0; i < b; ++i)
       mbar_wait(&ctl.full[i % S], static_cast<uint32_t>(i / S) & 1u, p.w.timeout_ns, &never, p.w.status, kSiteGrads);
   }
-  const int any = __syncthreads_or(warp == 1 && b > 0);
+  const int blocks = __syncthreads_count(warp == 1 && lane < b);  // accumulators in use, if there are fewer than kSums
   tc_fence_after();
   float* sums = reinterpret_cast<float*>(ring);  // [kGradCols][kPitch]: column, rank
   if (warp >= 2 && warp < 6) {
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int k = 0; k < RP; k += 16) {
-      uint32_t v[16];
-      if (any) {
-        tmem_ld16(tmem + (q * 32u << 16) + k, v);
-        tmem_wait_ld();
-      } else {  // no block: zeros
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0u;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<uint4*>(dst + k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-    }
+    for (int k = 0; k < RP; k += 16) read_sums16<RP>(tmem + (q * 32u << 16) + k, blocks, dst + k);
   }
   tc_fence_before();
   __syncthreads();
@@ -2296,7 +2279,7 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 template <typename P>
 cudaError_t launch(const char* name, void (*kernel)(P), const P& p, dim3 grid, int threads, size_t smem, unsigned cluster_y,
                    bool overlap, cudaStream_t s) {
-  if (smem > 48 * 1024) {
+  if (smem > 32 * 1024) {  // (some have static shared memory beside it)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
@@ -2325,9 +2308,9 @@ cudaError_t launch(const char* name, void (*kernel)(P), const P& p, dim3 grid, i
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// From this many tokens on they are sorted and worked on in tiles of one
-// adapter; below, taken as they come, several adapters to a tile.
-constexpr int64_t kSortFrom = 2048;
+// T R (R padded to a power of two from 16 on) from which tokens are sorted and
+// worked on in tiles of one adapter; below, taken as they come.
+constexpr int64_t kSortFrom = 8192;
 
 constexpr CUtensorMapDataType kMapBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
@@ -2346,88 +2329,90 @@ bool rows_map(CUtensorMap* tm, const void* base, CUtensorMapDataType type, int e
   return make_tmap_rows(tm, base, type, elem, cols, T, 0, static_cast<uint64_t>(ld) * elem, box, rows);
 }
 
-template <int NT, bool TRANS, bool VEC>
-cudaError_t down_rank(Down p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
-  if (o) {
-    constexpr int RP = NT < 2 ? 16 : NT * 8;
-    const int64_t slots = static_cast<int64_t>(o->segments) * o->tiles_per_segment;
-    const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));  // likely in use
-    unsigned cs = 1;
-    while (cs < 8 && tiles * cs * 2 <= 2 * ctx->num_sms && p.C >= 4 * kChunk * static_cast<int64_t>(cs)) cs *= 2;
-    const dim3 grid(static_cast<unsigned>(slots), cs);
-    const Waits w{ctx->status, wait_timeout_ns()};
-    DownTmaArgs a{};
-    if (rows_map(&a.x, p.x, kMapBf16, 2, p.C, p.T, p.ld, kChunk, kTileRows)) {
-      a.d = p;
-      a.o = *o;
-      a.w = w;
-      a.wtma = weights_map<RP>(&a.wm, p.w, TRANS, p.C, p.R, p.L);
-      return launch("adapter_down_tma", adapter_down_tma<RP, TRANS>, a, grid, 192, DownTma<RP, TRANS>::kSmem, cs, true, s);
-    }
-    return launch("adapter_down_tile", adapter_down_tile<RP, TRANS>, DownSorted{p, *o, w}, grid, 256,
-                  DownTile<RP, TRANS>::kSmem, cs, true, s);
+template <int RP, bool TRANS>
+cudaError_t down(const Down& p, const Order& o, const DeviceCtx* ctx, cudaStream_t s) {
+  const int64_t slots = static_cast<int64_t>(o.segments) * o.tiles_per_segment;
+  const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));  // likely in use
+  unsigned cs = 1;
+  while (cs < 8 && tiles * cs * 2 <= 2 * ctx->num_sms && p.C >= 4 * kChunk * static_cast<int64_t>(cs)) cs *= 2;
+  const dim3 grid(static_cast<unsigned>(slots), cs);
+  const Waits w{ctx->status, wait_timeout_ns()};
+  DownTmaArgs a{};
+  if (rows_map(&a.x, p.x, kMapBf16, 2, p.C, p.T, p.ld, kChunk, kTileRows)) {
+    a.d = p;
+    a.o = o;
+    a.w = w;
+    a.wtma = weights_map<RP>(&a.wm, p.w, TRANS, p.C, p.R, p.L);
+    return launch("adapter_down_tma", adapter_down_tma<RP, TRANS>, a, grid, 192, DownTma<RP, TRANS>::kSmem, cs, true, s);
   }
-  const int64_t chunks = ceil_div(p.C, 32);
-  constexpr int WK = 8, U = NT <= 4 ? 4 : 2;
+  return launch("adapter_down_tile", adapter_down_tile<RP, TRANS>, DownSorted{p, o, w}, grid, 256,
+                DownTile<RP, TRANS>::kSmem, cs, true, s);
+}
+
+template <int RP, typename Y, bool TRANS>
+cudaError_t up(const Up& p, const Order& o, const DeviceCtx* ctx, cudaStream_t s) {
+  const int64_t slots = static_cast<int64_t>(o.segments) * o.tiles_per_segment;
+  const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));
+  const int64_t chunks = ceil_div(p.C, kChunk);
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 4 * ctx->num_sms / tiles));  // two waves
+  const int per_cta = static_cast<int>(ceil_div(chunks, splits));
+  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, per_cta)));
+  const Waits w{ctx->status, wait_timeout_ns()};
+  constexpr CUtensorMapDataType kMapY = sizeof(Y) == 2 ? kMapBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  constexpr int kBox = 128 / static_cast<int>(sizeof(Y));
+  UpTmaArgs a{};
+  if (rows_map(&a.out, p.out, kMapY, sizeof(Y), p.C, p.T, p.ld_out, kBox, 32) &&
+      (!p.base || rows_map(&a.y, p.base, kMapY, sizeof(Y), p.C, p.T, p.ld_base, kBox, kTileRows))) {
+    a.d = p;
+    a.o = o;
+    a.w = w;
+    a.chunks_per_cta = per_cta;
+    a.wtma = weights_map<RP>(&a.wm, p.w, !TRANS, p.C, p.R, p.L);
+    return launch("adapter_up_tma", adapter_up_tma<RP, Y, TRANS>, a, grid, 256, UpTma<RP, Y, TRANS>::kSmem, 1, true, s);
+  }
+  return launch("adapter_up_tile", adapter_up_tile<RP, Y, TRANS>, UpSorted{p, o, w, per_cta}, grid, 256,
+                UpTile<RP, Y, TRANS>::kSmem, 1, true, s);
+}
+
+template <int NT, typename Y, bool TRANS, bool VEC>
+cudaError_t rows(const Down& d, const Up& u, const DeviceCtx* ctx, cudaStream_t s) {
+  const int64_t chunks = std::max(ceil_div(d.C, 32), ceil_div(u.C, 32));
+  constexpr int U = NT <= 4 && !TRANS ? 4 : 2;
   unsigned cs = 8;
-  while (cs > 1 && chunks < static_cast<int64_t>(WK) * cs) cs /= 2;
-  p.rows_per_tile = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, ceil_div(p.T * cs, ctx->num_sms))));
-  const int64_t tiles = ceil_div(p.T, p.rows_per_tile);
-  const size_t smem = static_cast<size_t>(WK) * 16 * NT * 8 * 4;
-  return launch("adapter_down", adapter_down<NT, WK, TRANS, VEC, U>, p, dim3(static_cast<unsigned>(tiles), cs), WK * 32,
-                smem, cs, false, s);
+  while (cs > 1 && chunks < 8 * static_cast<int64_t>(cs)) cs /= 2;
+  const Rows p{d, u, static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, ceil_div(d.T * cs, ctx->num_sms))))};
+  const size_t smem = (8 * 16 * NT * 8 + 16 * ((NT + 1) / 2) * 16) * sizeof(float);
+  return launch("adapter_rows", adapter_rows<NT, Y, TRANS, VEC, U>, p,
+                dim3(static_cast<unsigned>(ceil_div(d.T, p.rows_per_tile)), cs), 256, smem, cs, false, s);
 }
 
-template <bool TRANS, bool VEC>
-cudaError_t down(const Down& p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
-  if (p.R <= 8) return down_rank<1, TRANS, VEC>(p, o, ctx, s);
-  if (p.R <= 16) return down_rank<2, TRANS, VEC>(p, o, ctx, s);
-  if (p.R <= 32) return down_rank<4, TRANS, VEC>(p, o, ctx, s);
-  if (p.R <= 64) return down_rank<8, TRANS, VEC>(p, o, ctx, s);
-  return down_rank<16, TRANS, VEC>(p, o, ctx, s);
-}
-
-template <int KT, typename Y, bool TRANS, bool VEC>
-cudaError_t up_rank(Up p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
+// Both products for tokens sorted by `o`, or (null) as they come.
+template <typename Y, bool TRANS>
+cudaError_t both_products(const Down& d, const Up& u, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
   if (o) {
-    constexpr int RP = KT * 16;
-    const int64_t slots = static_cast<int64_t>(o->segments) * o->tiles_per_segment;
-    const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));
-    const int64_t chunks = ceil_div(p.C, kChunk);
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 4 * ctx->num_sms / tiles));  // two waves
-    const int per_cta = static_cast<int>(ceil_div(chunks, splits));
-    const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, per_cta)));
-    const Waits w{ctx->status, wait_timeout_ns()};
-    constexpr CUtensorMapDataType kMapY = sizeof(Y) == 2 ? kMapBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    constexpr int kBox = 128 / static_cast<int>(sizeof(Y));
-    UpTmaArgs a{};
-    if (rows_map(&a.out, p.out, kMapY, sizeof(Y), p.C, p.T, p.ld_out, kBox, 32) &&
-        (!p.base || rows_map(&a.y, p.base, kMapY, sizeof(Y), p.C, p.T, p.ld_base, kBox, kTileRows))) {
-      a.d = p;
-      a.o = *o;
-      a.w = w;
-      a.chunks_per_cta = per_cta;
-      a.wtma = weights_map<RP>(&a.wm, p.w, !TRANS, p.C, p.R, p.L);
-      return launch("adapter_up_tma", adapter_up_tma<RP, Y, TRANS>, a, grid, 256, UpTma<RP, Y, TRANS>::kSmem, 1, true, s);
-    }
-    return launch("adapter_up_tile", adapter_up_tile<RP, Y, TRANS>, UpSorted{p, *o, w, per_cta}, grid, 256,
-                  UpTile<RP, Y, TRANS>::kSmem, 1, true, s);
+    auto run = [&](auto rp) {
+      constexpr int RP = decltype(rp)::value;
+      const cudaError_t e = down<RP, TRANS>(d, *o, ctx, s);
+      return e != cudaSuccess ? e : up<RP, Y, TRANS>(u, *o, ctx, s);
+    };
+    if (d.R <= 16) return run(std::integral_constant<int, 16>());
+    if (d.R <= 32) return run(std::integral_constant<int, 32>());
+    if (d.R <= 64) return run(std::integral_constant<int, 64>());
+    return run(std::integral_constant<int, 128>());
   }
-  constexpr int WN = 4;
-  p.cols_per_warp = 32;
-  const int64_t col_tiles = ceil_div(p.C, 32 * WN);
-  p.rows_per_tile =
-      static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, ceil_div(p.T * col_tiles, 4 * ctx->num_sms))));
-  const dim3 grid(static_cast<unsigned>(ceil_div(p.T, p.rows_per_tile)), static_cast<unsigned>(col_tiles));
-  return launch("adapter_up", adapter_up<KT, WN, Y, TRANS, VEC>, p, grid, WN * 32, 0, 1, true, s);
-}
-
-template <typename Y, bool TRANS, bool VEC>
-cudaError_t up(const Up& p, const Order* o, const DeviceCtx* ctx, cudaStream_t s) {
-  if (p.R <= 16) return up_rank<1, Y, TRANS, VEC>(p, o, ctx, s);
-  if (p.R <= 32) return up_rank<2, Y, TRANS, VEC>(p, o, ctx, s);
-  if (p.R <= 64) return up_rank<4, Y, TRANS, VEC>(p, o, ctx, s);
-  return up_rank<8, Y, TRANS, VEC>(p, o, ctx, s);
+  const size_t y = sizeof(Y);
+  const bool vec = d.R % 4 == 0 && d.C % 8 == 0 && d.ld % 8 == 0 && aligned(d.x, 16) && aligned(d.w, 16) && u.C % 8 == 0 &&
+                   u.ld_out * y % 16 == 0 && aligned(u.out, 16) && aligned(u.w, 16) &&
+                   (!u.base || (u.ld_base * y % 16 == 0 && aligned(u.base, 16)));
+  auto run = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    return vec ? rows<NT, Y, TRANS, true>(d, u, ctx, s) : rows<NT, Y, TRANS, false>(d, u, ctx, s);
+  };
+  if (d.R <= 8) return run(std::integral_constant<int, 1>());
+  if (d.R <= 16) return run(std::integral_constant<int, 2>());
+  if (d.R <= 32) return run(std::integral_constant<int, 4>());
+  if (d.R <= 64) return run(std::integral_constant<int, 8>());
+  return run(std::integral_constant<int, 16>());
 }
 
 template <int RP, typename G>
@@ -2490,17 +2475,11 @@ Order order_at(void* workspace, int64_t T, int L, bool blocks, size_t* bytes = n
   return o;
 }
 
-cudaError_t sort(const int* ids, int64_t T, int L, const Order& o, cudaStream_t s) {
+// overlap: beside the launch before it, which it waits for at its end.
+cudaError_t sort(const int* ids, int64_t T, int L, const Order& o, bool overlap, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(kSortWarps) * (L + 1) * 2 + kSegment * 2;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(adapter_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  {
-    TraceScope tr("adapter_sort", s);
-    adapter_sort<<<o.segments, kSortThreads, smem, s>>>(ids, T, L, o);
-  }
-  return cudaGetLastError();
+  return launch("adapter_sort", adapter_sort, SortArgs{ids, T, L, o}, dim3(static_cast<unsigned>(o.segments)), kSortThreads,
+                smem, 1, overlap, s);
 }
 
 }  // namespace
@@ -2517,7 +2496,11 @@ size_t adapter_terms_bytes(int64_t T, int64_t R, int64_t L) {
   return static_cast<size_t>(blocks) * 2 * 3 * kGradRows * rp * 2;  // three terms: of binary32 gradients
 }
 
-bool adapters_sorted(int64_t T, int64_t L) { return T >= kSortFrom && L <= kSortMaxL; }
+bool adapters_sorted(int64_t T, int64_t R, int64_t L) {
+  int64_t rp = 16;
+  while (rp < R) rp *= 2;
+  return T * rp >= kSortFrom && L <= kSortMaxL;
+}
 int64_t adapters_sort_max() { return kSortMaxL; }
 
 cudaError_t launch_adapters(const AdaptersRequest& r, cudaStream_t s) {
@@ -2526,23 +2509,16 @@ cudaError_t launch_adapters(const AdaptersRequest& r, cudaStream_t s) {
   const bf16 *a = static_cast<const bf16*>(r.a), *b = static_cast<const bf16*>(r.b);
   const int R = static_cast<int>(r.R), L = static_cast<int>(r.L);
   Order order{};
-  const Order* o = nullptr;
-  cudaError_t e;
-  if (adapters_sorted(r.T, r.L)) {
+  const bool sorted = adapters_sorted(r.T, r.R, r.L);
+  if (sorted) {
     order = order_at(r.workspace, r.T, L, false);
-    o = &order;
-    e = sort(r.ids, r.T, L, order, s);
+    const cudaError_t e = sort(r.ids, r.T, L, order, false, s);
     if (e != cudaSuccess) return e;
   }
-  const Down d{static_cast<const bf16*>(r.x), r.ld_x, a, r.ids, r.u, r.T, r.K, R, L, 16};
-  const bool dv = r.K % 8 == 0 && r.ld_x % 8 == 0 && aligned(r.x, 16) && aligned(a, 16);
-  e = dv ? down<false, true>(d, o, ctx, s) : down<false, false>(d, o, ctx, s);
-  if (e != cudaSuccess) return e;
-  const Up u{r.u, b, r.ids, r.scaling, r.y, r.ld_y, r.out, r.ld_out, r.T, r.N, R, L, 16, 32};
-  const bool uv = r.N % 8 == 0 && r.ld_out % 8 == 0 && aligned(r.out, 16) &&
-                  (!r.y || (r.ld_y % 8 == 0 && aligned(r.y, 16))) && R % 4 == 0 && aligned(b, 8);
-  if (r.y_bf16) return uv ? up<bf16, false, true>(u, o, ctx, s) : up<bf16, false, false>(u, o, ctx, s);
-  return uv ? up<float, false, true>(u, o, ctx, s) : up<float, false, false>(u, o, ctx, s);
+  const Down d{static_cast<const bf16*>(r.x), r.ld_x, a, r.ids, r.u, r.T, r.K, R, L};
+  const Up u{r.u, b, r.ids, r.scaling, r.y, r.ld_y, r.out, r.ld_out, r.T, r.N, R, L};
+  return r.y_bf16 ? both_products<bf16, false>(d, u, sorted ? &order : nullptr, ctx, s)
+                  : both_products<float, false>(d, u, sorted ? &order : nullptr, ctx, s);
 }
 
 cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s) {
@@ -2556,17 +2532,15 @@ cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStrea
     if (e == cudaSuccess) e = cudaMemsetAsync(r.db, 0, static_cast<size_t>(r.L) * R * r.N * g, s);
     return e;
   }
-  const Order order = order_at(r.order, r.T, L, true);  // the gradients always go by it
-  cudaError_t e = sort(r.ids, r.T, L, order, s);
-  if (e != cudaSuccess) return e;
-  const Order* o = adapters_sorted(r.T, r.L) ? &order : nullptr;
-  const Down d{static_cast<const bf16*>(r.dy), r.ld_dy, b, r.ids, r.d, r.T, r.N, R, L, 16};
-  const bool dv = r.N % 8 == 0 && r.ld_dy % 8 == 0 && aligned(r.dy, 16) && R % 4 == 0 && aligned(b, 8);
-  e = dv ? down<true, true>(d, o, ctx, s) : down<true, false>(d, o, ctx, s);
-  if (e != cudaSuccess) return e;
-  const Up u{r.d, a, r.ids, r.scaling, r.dx_base, r.ld_dx, r.dx, r.ld_dx, r.T, r.K, R, L, 16, 32};
-  const bool uv = r.K % 8 == 0 && r.ld_dx % 8 == 0 && aligned(r.dx, 16) && aligned(r.dx_base, 16) && aligned(a, 16);
-  e = uv ? up<bf16, true, true>(u, o, ctx, s) : up<bf16, true, false>(u, o, ctx, s);
+  // The gradients always go by the order; the products of few tokens do not,
+  // and the sort runs beside them.
+  const Order order = order_at(r.order, r.T, L, true);
+  const bool sorted = adapters_sorted(r.T, r.R, r.L);
+  const Down d{static_cast<const bf16*>(r.dy), r.ld_dy, b, r.ids, r.d, r.T, r.N, R, L};
+  const Up u{r.d, a, r.ids, r.scaling, r.dx_base, r.ld_dx, r.dx, r.ld_dx, r.T, r.K, R, L};
+  cudaError_t e = sorted ? sort(r.ids, r.T, L, order, false, s) : cudaSuccess;
+  if (e == cudaSuccess) e = both_products<bf16, true>(d, u, sorted ? &order : nullptr, ctx, s);
+  if (e == cudaSuccess && !sorted) e = sort(r.ids, r.T, L, order, true, s);
   if (e != cudaSuccess) return e;
   Grads p{};
   p.job[0] = GradJob{nullptr, r.x, r.x_scales, r.ld_x, r.da, r.K, static_cast<int>(ceil_div(r.K, kGradCols)), 0};

@@ -835,8 +835,8 @@ bsmm_status adapter_sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L)
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 }  // namespace
 
-size_t bsmm_adapters_workspace_size(int64_t T, int64_t L) {
-  if (T <= 0 || L <= 0 || !adapters_sorted(T, L)) return 0;
+size_t bsmm_adapters_workspace_size(int64_t T, int64_t R, int64_t L) {
+  if (T <= 0 || R <= 0 || R > 128 || L <= 0 || !adapters_sorted(T, R, L)) return 0;
   return adapter_order_bytes(T, L, false);
 }
 
@@ -858,7 +858,7 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
   if (!aligned_to(x, 2) || !aligned_to(A, 2) || !aligned_to(B, 2) || !aligned_to(ids, 4) || !aligned_to(scaling, 4) ||
       !aligned_to(y, ye) || !aligned_to(out, ye) || !aligned_to(u, 4))
     return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements");
-  const size_t need = bsmm_adapters_workspace_size(T, L);
+  const size_t need = bsmm_adapters_workspace_size(T, R, L);
   if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) +
                                         " bytes");

@@ -182,7 +182,7 @@ struct AdaptersBackwardRequest {
 // Whether bsmm_adapters sorts its tokens (and needs the order's bytes), the
 // bytes, those of the gradients' coefficients, and the most adapters that can
 // be sorted by.
-bool adapters_sorted(int64_t T, int64_t L);
+bool adapters_sorted(int64_t T, int64_t R, int64_t L);
 size_t adapter_order_bytes(int64_t T, int64_t L, bool gradients);
 size_t adapter_terms_bytes(int64_t T, int64_t R, int64_t L);
 int64_t adapters_sort_max();

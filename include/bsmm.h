@@ -551,7 +551,7 @@ bsmm_status bsmm_linear_backward_checkpoint(const void* dY, const void* W, const
  * Rows whose start is 16-byte aligned (K, N and pitches multiples of 8, R of
  * 4) are read and written in 16-byte pieces; others element by element.
  * Every sum has a fixed order. */
-size_t bsmm_adapters_workspace_size(int64_t T, int64_t L);
+size_t bsmm_adapters_workspace_size(int64_t T, int64_t R, int64_t L);
 
 bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, const void* x, int64_t ld_x,
                           const void* A, const void* B, const int32_t* ids, const float* scaling, const void* y,

@@ -164,8 +164,8 @@ def test_linear_library(lib, change, status):
 
 
 def test_workspace_query(lib):
-    assert bsmm.adapters_workspace_size(64, 64) == 0  # few tokens are not sorted
-    assert bsmm.adapters_workspace_size(8192, 4) >= 8192 * 4
+    assert bsmm.adapters_workspace_size(64, 16, 64) == 0  # few tokens are not sorted
+    assert bsmm.adapters_workspace_size(8192, 16, 4) >= 8192 * 4
     assert bsmm.adapters_backward_workspace_size(0, 8, 4) == 0
     assert bsmm.adapters_backward_workspace_size(100, 8, 4) >= 100 * 8 * 4 + 100 * 4
 
