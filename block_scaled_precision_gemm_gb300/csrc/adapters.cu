@@ -232,17 +232,6 @@ struct Rows {
   int rows_per_tile;  // of a cluster, at most 16
 };
 
-// Asks for `bytes` from p on to be brought to the L2 cache, by a warp.
-__device__ __forceinline__ void prefetch_span(const void* p, int64_t bytes, int lane) {
-  const uint8_t* at = static_cast<const uint8_t*>(p);
-  for (int64_t i = lane * 128; i < bytes; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
-}
-__device__ __forceinline__ void prefetch_rows(const void* p, int rows, int64_t pitch, int64_t bytes, int lane) {
-  const uint8_t* at = static_cast<const uint8_t*>(p);
-  for (int r = lane; r < rows; r += 32)
-    for (int64_t i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + r * pitch + i));
-}
-
 // A cluster takes up to 16 rows.  First their u: the contraction is split over
 // the cluster's CTAs and each CTA's 8 warps, and the partial sums are added in
 // a fixed order, over the warps in shared memory, over the cluster through
@@ -286,29 +275,7 @@ __global__ void __launch_bounds__(256, NT <= 2 && !TRANS ? 3 : (NT <= 4 ? 2 : 1)
     const int64_t chunks = (p.C + 31) / 32;
     const int64_t parts = static_cast<int64_t>(cs) * WK, at = static_cast<int64_t>(rank) * WK + wk;
     const int64_t k_begin = chunks * at / parts * 32, k_end = chunks * (at + 1) / parts * 32;
-    // the weights that this warp comes to after its first adapter's
     unsigned left = any;
-    for (bool first = true; left; first = false) {
-      const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
-      left &= ~__ballot_sync(0xFFFFFFFFu, id == a);
-      if (!first) {
-        const bf16* w = p.w + static_cast<int64_t>(a) * p.R * p.C;
-        const int64_t cols = min(k_end, p.C) - k_begin;
-        if constexpr (TRANS)
-          prefetch_span(w + k_begin * p.R, cols * p.R * 2, lane);
-        else
-          prefetch_rows(w + k_begin, p.R, p.C * 2, cols * 2, lane);
-      }
-      const bf16* w = pr.u.w + static_cast<int64_t>(a) * pr.u.R * pr.u.C;
-      for (int64_t n = at * 32; n < pr.u.C; n += parts * 32) {
-        const int64_t cols = min(static_cast<int64_t>(32), pr.u.C - n);
-        if constexpr (TRANS)
-          prefetch_rows(w + n, pr.u.R, pr.u.C * 2, cols * 2, lane);
-        else
-          prefetch_span(w + n * pr.u.R, cols * pr.u.R * 2, lane);
-      }
-    }
-    left = any;
     while (left) {
       const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
       const unsigned same = __ballot_sync(0xFFFFFFFFu, id == a);
@@ -567,6 +534,7 @@ struct SortArgs {
   int L;
   Order o;
 };
+template <int ROUNDS>  // 32 tokens each of a warp
 __global__ void __launch_bounds__(kSortThreads) adapter_sort(const SortArgs p) {
   const int* ids = p.ids;
   const int64_t T = p.T;
@@ -580,13 +548,12 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const SortArgs p) {
   const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kSegment;
   grid_launch_dependents();
   for (int i = tid; i < kSortWarps * G; i += kSortThreads) hist[i] = 0;
-  const int rounds = static_cast<int>(min(static_cast<int64_t>(kSegment), T - s0) + kSortThreads - 1) / kSortThreads;
-  int key[kSortRounds], rank[kSortRounds];
+  int key[ROUNDS], rank[ROUNDS];
 #pragma unroll
-  for (int i = 0; i < kSortRounds; ++i) {
-    const int64_t t = s0 + (warp * rounds + i) * 32 + lane;
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int64_t t = s0 + (warp * ROUNDS + i) * 32 + lane;
     key[i] = -1;
-    if (i < rounds && t < T) {
+    if (t < T) {
       const int a = __ldg(ids + t);
       key[i] = a >= 0 && a < L ? a : L;
     }
@@ -594,8 +561,7 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const SortArgs p) {
   __syncthreads();
   uint16_t* mine = hist + warp * G;
 #pragma unroll
-  for (int i = 0; i < kSortRounds; ++i) {
-    if (i >= rounds) break;
+  for (int i = 0; i < ROUNDS; ++i) {
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, key[i]);
     const unsigned before = peers & ((1u << lane) - 1u);
     if (key[i] >= 0) rank[i] = mine[key[i]] + __popc(before);
@@ -636,9 +602,9 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const SortArgs p) {
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSortRounds; ++i)
+  for (int i = 0; i < ROUNDS; ++i)
     if (key[i] >= 0) {
-      const int at = first[key[i]] + mine[key[i]] + rank[i], t = (warp * rounds + i) * 32 + lane;
+      const int at = first[key[i]] + mine[key[i]] + rank[i], t = (warp * ROUNDS + i) * 32 + lane;
       perm[at] = static_cast<uint16_t>(t);
       o.perm[s0 + at] = static_cast<int>(s0) + t;
     }
@@ -745,18 +711,19 @@ constexpr int kSiteDown = 41, kSiteUp = 42, kSiteGrads = 43;
 // columns into one: 2e-6 of the result, against 1e-6 for sums in registers).
 template <int RP>
 struct Sums {
-  static constexpr int kSums = RP <= 64 ? 4 : 2;
-  static constexpr int kTmem = kSums * RP < 32 ? 32 : kSums * RP;
+  static constexpr int kSums = RP <= 16 ? 8 : (RP <= 64 ? 4 : 2);
+  static constexpr int kTmem = kSums * RP;  // two CTAs to an SM have room, three for RP = 16
 };
-// 16 columns from tensor memory, of the first n accumulators, to dst.
-template <int RP>
+// 16 columns from tensor memory, of the first n accumulators and (LAST, n > 0)
+// the last one, to dst.
+template <int RP, bool LAST>
 __device__ __forceinline__ void read_sums16(uint32_t tmem, int n, float* dst) {
   float v[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] = 0.f;
 #pragma unroll
   for (int k = 0; k < Sums<RP>::kSums; ++k)
-    if (k < n) {
+    if (k < n || (LAST && n > 0 && k == Sums<RP>::kSums - 1)) {
       uint32_t w[16];
       tmem_ld16(tmem + k * RP, w);
       tmem_wait_ld();
@@ -931,7 +898,7 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int j = 0; j < kHalf; j += 16) read_sums16<RP>(src + j, c, dst + j);
+      for (int j = 0; j < kHalf; j += 16) read_sums16<RP, false>(src + j, c, dst + j);
     }
   }
   tc_fence_before();
@@ -1300,6 +1267,14 @@ struct GradTile {
   static_assert(kGradCols * kPitch * 4 <= kCtlAt, "the sums reuse the space before");
   static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
   static constexpr int kSums = Sums<RP>::kSums, kTmem = Sums<RP>::kTmem;
+  // Blocks take turns at the accumulators but the last, which is that of the
+  // coefficients' lower terms.
+  static __device__ __forceinline__ int sum_of(int block, int term) {
+    return term == 0 ? block % (kSums - 1) : kSums - 1;
+  }
+  static __device__ __forceinline__ bool continues(int block, int term, int step) {
+    return step > 0 || (term == 0 ? block >= kSums - 1 : block > 0 || term < TERMS - 1);
+  }
 };
 
 // An adapter's blocks of 64 tokens that fall to one CTA of a cluster of cs:
@@ -1515,8 +1490,8 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-          mma_f16(tmem + (b % Cfg::kSums) * RP, Cfg::X::along_rows(xt, s), Cfg::Coef::along_rows(ct + k * Cfg::kTermBytes, s),
-                  mma_shape(RP, true, true), (b >= Cfg::kSums || k < TERMS - 1 || s > 0) ? 1u : 0u);
+          mma_f16(tmem + Cfg::sum_of(b, k) * RP, Cfg::X::along_rows(xt, s), Cfg::Coef::along_rows(ct + k * Cfg::kTermBytes, s),
+                  mma_shape(RP, true, true), Cfg::continues(b, k, s) ? 1u : 0u);
       tc_commit(&ctl.done[b & 1]);
     }
     if (b > 0)
@@ -1543,7 +1518,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int k = 0; k < kHalf; k += 16) read_sums16<RP>(src + k, b, dst + k);
+      for (int k = 0; k < kHalf; k += 16) read_sums16<RP, true>(src + k, b, dst + k);
     }
   }
   tc_fence_before();
@@ -1748,7 +1723,7 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int j = 0; j < RP; j += 16) read_sums16<RP>(tmem + (q * 32u << 16) + j, n, dst + j);
+    for (int j = 0; j < RP; j += 16) read_sums16<RP, false>(tmem + (q * 32u << 16) + j, n, dst + j);
   }
   tc_fence_before();
   __syncthreads();
@@ -2154,8 +2129,8 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
         for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
           for (int s = 0; s < kSteps; ++s)
-            mma_f16(tmem + (b % Cfg::kSums) * RP, Cfg::X::along_rows(xt, s), Coef::along_rows(ct + k * Cfg::kTermBytes, s),
-                    mma_shape(RP, true, true), (b >= Cfg::kSums || k < TERMS - 1 || s > 0) ? 1u : 0u);
+            mma_f16(tmem + Cfg::sum_of(b, k) * RP, Cfg::X::along_rows(xt, s), Coef::along_rows(ct + k * Cfg::kTermBytes, s),
+                    mma_shape(RP, true, true), Cfg::continues(b, k, s) ? 1u : 0u);
         tc_commit(&ctl.empty[st]);
         ++b;
       }
@@ -2261,7 +2236,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int k = 0; k < RP; k += 16) read_sums16<RP>(tmem + (q * 32u << 16) + k, blocks, dst + k);
+    for (int k = 0; k < RP; k += 16) read_sums16<RP, true>(tmem + (q * 32u << 16) + k, blocks, dst + k);
   }
   tc_fence_before();
   __syncthreads();
@@ -2478,8 +2453,8 @@ Order order_at(void* workspace, int64_t T, int L, bool blocks, size_t* bytes = n
 // overlap: beside the launch before it, which it waits for at its end.
 cudaError_t sort(const int* ids, int64_t T, int L, const Order& o, bool overlap, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(kSortWarps) * (L + 1) * 2 + kSegment * 2;
-  return launch("adapter_sort", adapter_sort, SortArgs{ids, T, L, o}, dim3(static_cast<unsigned>(o.segments)), kSortThreads,
-                smem, 1, overlap, s);
+  return launch("adapter_sort", T <= 2 * kSortThreads ? adapter_sort<2> : adapter_sort<kSortRounds>, SortArgs{ids, T, L, o},
+                dim3(static_cast<unsigned>(o.segments)), kSortThreads, smem, 1, overlap, s);
 }
 
 }  // namespace
