@@ -475,6 +475,7 @@ struct Order {
   Tile* tiles;   // [segments][tiles_per_segment] of 128 tokens, unused ones with count 0
   Tile* blocks;  // [segments][blocks_per_segment] of 64 tokens, each adapter's together
   int* starts;   // [segments][L + 1]: the first block of each adapter, and the one after the last's
+  int* used;     // [segments]: tiles in use, the first of them
   int tiles_per_segment, blocks_per_segment, segments;
 };
 
@@ -615,6 +616,7 @@ __global__ void __launch_bounds__(kSortThreads) adapter_sort(const SortArgs p) {
   Tile* tiles = o.tiles + static_cast<int64_t>(blockIdx.x) * o.tiles_per_segment;
   for (int i = tid; i < o.tiles_per_segment; i += kSortThreads)
     tiles[i] = sorted_piece(first, tile0, perm, G, kTileRows, static_cast<int>(s0), i);
+  if (tid == 0) o.used[blockIdx.x] = tile0[G];
   if (!o.blocks) return;
   Tile* blocks = o.blocks + static_cast<int64_t>(blockIdx.x) * o.blocks_per_segment;
   for (int i = tid; i < o.blocks_per_segment; i += kSortThreads)
@@ -1734,142 +1736,203 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
 template <int RP, typename Y, bool TRANS>
 struct UpTma : UpTile<RP, Y, TRANS> {
   using Base = UpTile<RP, Y, TRANS>;
+  // one CTA to an SM: what the weights leave holds base, up to 8 chunks
+  static constexpr int kWStages = RP == 128 && sizeof(Y) == 4 ? 2 : 4;
+  static constexpr int kRoom = (226 * 1024 - Base::kUBytes - kWStages * Base::kWBytes) / Base::kYBytes;
+  static constexpr int kYStages = kRoom < 8 ? kRoom : 8;
+  static constexpr int kProducts = 4;  // accumulators
+  static constexpr int kCtlAt = Base::kUBytes + kWStages * Base::kWBytes + kYStages * Base::kYBytes;
   struct Ctl {
-    uint64_t wfull[Base::kWStages], wempty[Base::kWStages], yfull[Base::kYStages], yempty[Base::kYStages];
-    uint64_t dfull[2], dempty[2], ufull;
+    uint64_t wfull[kWStages], wempty[kWStages], yfull[kYStages], yempty[kYStages];
+    uint64_t dfull[kProducts], dempty[kProducts], ufull, uempty;
     uint32_t tmem;
     int abort_flag;
   };
-  static constexpr int kSmem = Base::kCtlAt + static_cast<int>(sizeof(Ctl));
+  static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
 };
 struct UpTmaArgs {
   CUtensorMap y, out, wm;  // base by 128 rows, out by 32, of 128 bytes each; the weights
   Up d;
   Order o;
   Waits w;
-  int chunks_per_cta;
   int wtma;
 };
 
-// Warp 0 feeds base and the weights, warp 1 issues the MMAs, warps 2 and 3
-// are the helpers; warps 4..7 own 32 rows each: they add the product to base in
-// place in its stage, and from there write 32 consecutive rows with one TMA
-// store, other rows in whole 128-byte pieces.
+// The tiles in use, in order, from number `n` on.
+struct TileWalk {
+  const Order& o;
+  int seg = 0, at = 0;
+  __device__ __forceinline__ TileWalk(const Order& o_, int64_t n) : o(o_) {
+    for (; n >= o.used[seg]; ++seg) n -= o.used[seg];
+    at = static_cast<int>(n);
+  }
+  __device__ __forceinline__ Tile get() const { return o.tiles[static_cast<int64_t>(seg) * o.tiles_per_segment + at]; }
+  __device__ __forceinline__ void next() {  // every segment has a tile
+    if (++at == o.used[seg]) {
+      ++seg;
+      at = 0;
+    }
+  }
+};
+
+// One CTA to an SM, each with an equal stretch of all tiles' chunks, so that
+// loads and stores go on at a steady rate from the first tile to the last (as
+// CTAs of a tile and 16 chunks each, in two waves, 8192 tokens of 8192 columns
+// and rank 64 took 61 us).  Warp 0 feeds base and the weights, warp 1 issues the
+// MMAs, warps 2 and 3 are the helpers, which gather a tile's rows of base that
+// are not consecutive; warps 4..7 and 8..11 take turns at the chunks: each warp
+// adds the product of 32 rows to base in place in its stage, and from there
+// writes 32 consecutive rows with one TMA store, other rows in whole 128-byte
+// pieces.  At a tile's start they split its u.
 template <int RP, typename Y, bool TRANS>
-__global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ UpTmaArgs ps) {
+__global__ void __launch_bounds__(384, 1) adapter_up_tma(const __grid_constant__ UpTmaArgs ps) {
   using Cfg = UpTma<RP, Y, TRANS>;
-  constexpr int TERMS = Cfg::TERMS, YS = Cfg::kYStages, WS = Cfg::kWStages;
+  constexpr int TERMS = Cfg::TERMS, YS = Cfg::kYStages, WS = Cfg::kWStages, DS = Cfg::kProducts;
   constexpr int kBlockCols = 128 / static_cast<int>(sizeof(Y));  // columns of a 128-byte row piece
   constexpr int kBlocks = kChunk / kBlockCols;
+  constexpr int kHelpers = 64, kTeams = 2;
+  constexpr bool kDefer = YS >= 5;  // a stage is given back with the team's next chunk: a store is rarely waited for
   extern __shared__ __align__(1024) uint8_t smem[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(smem + Cfg::kCtlAt);
   const Up& p = ps.d;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t u_at = smem_u32(smem), w_at = u_at + Cfg::kUBytes, y_at = w_at + WS * Cfg::kWBytes;
 
-  const Tile tile = ps.o.tiles[blockIdx.x];  // of two launches before, done before the last one released this one
-  if (tile.count == 0) return;
+  // this CTA's stretch (the tiles are of two launches before, done before the last one released this one)
   const int64_t chunks = (p.C + kChunk - 1) / kChunk;
-  const int64_t c_begin = static_cast<int64_t>(blockIdx.y) * ps.chunks_per_cta;
-  const int n = static_cast<int>(min(static_cast<int64_t>(ps.chunks_per_cta), chunks - c_begin));
-  const bool plain = tile.adapter < 0;  // no product: out = base
+  int64_t units = 0;
+  for (int i = 0; i < ps.o.segments; ++i) units += ps.o.used[i];
+  units *= chunks;
+  const int64_t u_begin = units * blockIdx.x / gridDim.x, u_end = units * (blockIdx.x + 1) / gridDim.x;
+  if (u_begin == u_end) return;
+  const int64_t tile_begin = u_begin / chunks;
   const bool has_base = p.base != nullptr;
-  const bool run = tile.run >= 0;
-  constexpr int kHelpers = 64;
   if (tid == 0) {
     for (int i = 0; i < WS; ++i) {
       mbar_init(&ctl.wfull[i], ps.wtma ? 1 : kHelpers);
       mbar_init(&ctl.wempty[i], 1);
     }
     for (int i = 0; i < YS; ++i) {
-      mbar_init(&ctl.yfull[i], run || !has_base ? 1 : kHelpers);
+      mbar_init(&ctl.yfull[i], 1 + kHelpers);
       mbar_init(&ctl.yempty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < DS; ++i) {
       mbar_init(&ctl.dfull[i], 1);
       mbar_init(&ctl.dempty[i], 4);
     }
-    mbar_init(&ctl.ufull, 128);
+    mbar_init(&ctl.ufull, kTeams * 128);
+    mbar_init(&ctl.uempty, 1);
     ctl.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&ctl.tmem, 2 * kChunk);
+    tmem_alloc(&ctl.tmem, DS * kChunk);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
+  grid_launch_dependents();
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_poll(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteUp);
   };
-  int c = 0;  // chunks begun
-  if (warp == 0) {
-    if (lane == 0) {
-      for (; c < n; ++c) {
-        const int64_t k = (c_begin + c) * kChunk;
-        if (!plain && ps.wtma) {
-          const int st = c % WS;
-          if (c >= WS && !wait(&ctl.wempty[st], c / WS - 1)) break;
-          mbar_arrive_expect_tx(&ctl.wfull[st], Cfg::kWBytes);
-          load_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, &ps.wm, &ctl.wfull[st], k, tile.adapter, smem);
-        }
-        if (!run && has_base) continue;  // the helpers' part
-        const int st = c % YS;
-        if (c >= YS && !wait(&ctl.yempty[st], c / YS - 1)) break;
-        if (!has_base) {
-          mbar_arrive(&ctl.yfull[st]);
-          continue;
-        }
-        mbar_arrive_expect_tx(&ctl.yfull[st], Cfg::kYBytes);
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)  // rows past the tile are not written
-          tma_load_2d(y_at + st * Cfg::kYBytes + b * (kTileRows * 128), &ps.y, &ctl.yfull[st],
-                      static_cast<int>(k) + b * kBlockCols, tile.run);
-      }
+  // every role goes over the stretch by itself: f(tile, its first chunk, chunks) until false
+  auto for_tiles = [&](auto f) {
+    TileWalk walk(ps.o, tile_begin);
+    int64_t left = u_end - u_begin, c0 = u_begin - tile_begin * chunks;
+    while (true) {
+      const int64_t n = min(left, chunks - c0);
+      if (!f(walk.get(), c0, static_cast<int>(n)) || (left -= n) == 0) break;
+      c0 = 0;
+      walk.next();
     }
-    __syncwarp();
+  };
+  // chunks so far: of all tiles (base's ring), and of those with a product (the others')
+  int c = 0, m = 0;
+  if (warp == 0) {
+    if (lane == 0)
+      for_tiles([&](const Tile& tile, int64_t c0, int n) {
+        const bool plain = tile.adapter < 0;
+        const bool run = tile.run >= 0;
+        for (int i = 0; i < n; ++i) {
+          const int64_t k = (c0 + i) * kChunk;
+          if (!plain) {
+            if (ps.wtma) {
+              const int st = m % WS;
+              if (m >= WS && !wait(&ctl.wempty[st], m / WS - 1)) return false;
+              mbar_arrive_expect_tx(&ctl.wfull[st], Cfg::kWBytes);
+              load_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, &ps.wm, &ctl.wfull[st], k, tile.adapter, smem);
+            }
+            ++m;
+          }
+          const int st = c % YS;
+          if (c >= YS && !wait(&ctl.yempty[st], c / YS - 1)) return false;
+          if (run && has_base) {
+            mbar_arrive_expect_tx(&ctl.yfull[st], Cfg::kYBytes);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)  // rows past the tile are not written
+              tma_load_2d(y_at + st * Cfg::kYBytes + b * (kTileRows * 128), &ps.y, &ctl.yfull[st],
+                          static_cast<int>(k) + b * kBlockCols, tile.run);
+          } else {
+            mbar_arrive(&ctl.yfull[st]);
+          }
+          ++c;
+        }
+        return true;
+      });
+    c = __shfl_sync(0xFFFFFFFFu, c, 0);
+    m = __shfl_sync(0xFFFFFFFFu, m, 0);
   } else if (warp == 1) {
-    if (lane == 0 && !plain && wait(&ctl.ufull, 0)) {
-      for (int m = 0; m < n; ++m) {
-        const int st = m % WS;
-        if (!wait(&ctl.wfull[st], m / WS)) break;
-        if (m >= 2 && !wait(&ctl.dempty[m & 1], (m >> 1) - 1)) break;
-        tc_fence_after();
-        const uint32_t at = w_at + st * Cfg::kWBytes, d = tmem + (m & 1) * kChunk;
+    if (lane == 0) {
+      int tiles = 0;
+      for_tiles([&](const Tile& tile, int64_t, int n) {
+        if (tile.adapter < 0) return true;
+        if (!wait(&ctl.ufull, tiles++)) return false;
+        for (int i = 0; i < n; ++i, ++m) {
+          const int st = m % WS, ds = m % DS;
+          if (!wait(&ctl.wfull[st], m / WS) || (m >= DS && !wait(&ctl.dempty[ds], m / DS - 1))) return false;
+          tc_fence_after();
+          const uint32_t at = w_at + st * Cfg::kWBytes, d = tmem + ds * kChunk;
 #pragma unroll
-        for (int k = TERMS - 1; k >= 0; --k)
+          for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
-          for (int s = 0; s < RP / 16; ++s)
-            mma_f16(d, Cfg::U::along_pieces(u_at + k * Cfg::U::kBytes, s),
-                    TRANS ? Cfg::W::along_rows(at, s) : Cfg::W::along_pieces(at, s), mma_shape(kChunk, false, TRANS),
-                    (k < TERMS - 1 || s > 0) ? 1u : 0u);
-        tc_commit(&ctl.wempty[st]);
-        tc_commit(&ctl.dfull[m & 1]);
-      }
+            for (int s = 0; s < RP / 16; ++s)
+              mma_f16(d, Cfg::U::along_pieces(u_at + k * Cfg::U::kBytes, s),
+                      TRANS ? Cfg::W::along_rows(at, s) : Cfg::W::along_pieces(at, s), mma_shape(kChunk, false, TRANS),
+                      (k < TERMS - 1 || s > 0) ? 1u : 0u);
+          tc_commit(&ctl.wempty[st]);
+          tc_commit(&ctl.dfull[ds]);
+        }
+        tc_commit(&ctl.uempty);
+        return true;
+      });
     }
     __syncwarp();
   } else if (warp < 4) {
     const int i = tid - 64;
-    const bool weights = !plain && !ps.wtma, rows = !run && has_base;
-    if (weights || rows) {
+    const Y* base = static_cast<const Y*>(p.base);
+    for_tiles([&](const Tile& tile, int64_t c0, int n) {
+      const bool plain = tile.adapter < 0;
+      const bool weights = !plain && !ps.wtma, rows = tile.run < 0 && has_base;
       const bf16* w = p.w + static_cast<int64_t>(plain ? 0 : tile.adapter) * p.R * p.C;
-      const Y* base = static_cast<const Y*>(p.base);
       int at_row[16];  // piece i % 8 of rows i / 8 + 8 j
+      if (rows) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) at_row[j] = ps.o.perm[tile.start + min((i >> 3) + 8 * j, tile.count - 1)];
-      for (int m = 0; m < n; ++m) {
-        const int64_t k = (c_begin + m) * kChunk;
+        for (int j = 0; j < 16; ++j) at_row[j] = ps.o.perm[tile.start + min((i >> 3) + 8 * j, tile.count - 1)];
+      }
+      for (int e = 0; e < n; ++e, ++c) {
+        const int64_t k = (c0 + e) * kChunk;
         if (weights) {
           const int st = m % WS;
-          if (m >= WS && !wait(&ctl.wempty[st], m / WS - 1)) break;
+          if (m >= WS && !wait(&ctl.wempty[st], m / WS - 1)) return false;
           stage_weights<RP, !TRANS>(w_at + st * Cfg::kWBytes, w, k, p.C, p.R, i, kHelpers);
           mbar_arrive(&ctl.wfull[st]);
+          ++m;
         }
+        const int st = c % YS;
+        if (c >= YS && !wait(&ctl.yempty[st], c / YS - 1)) return false;
         if (rows) {
-          const int st = m % YS;
-          if (m >= YS && !wait(&ctl.yempty[st], m / YS - 1)) break;
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -1879,147 +1942,173 @@ __global__ void __launch_bounds__(256) adapter_up_tma(const __grid_constant__ Up
                        base + at_row[j] * p.ld_base, k + b * kBlockCols + (i & 7) * (kBlockCols / 8), p.C, r < tile.count);
             }
           copy_arrive(&ctl.yfull[st]);
+        } else {
+          mbar_arrive(&ctl.yfull[st]);
         }
       }
-      copy_commit();
-      copy_wait<0>();
-    }
+      return true;
+    });
+    copy_commit();
+    copy_wait<0>();
   } else {
-    const int q = warp - 4, row = q * 32 + lane;  // this thread's row of the tile, and its lane of tensor memory
-    const int64_t token = ps.o.perm[tile.start + min(row, tile.count - 1)];
-    const bool whole = run && q * 32 + 32 <= tile.count;  // 32 consecutive rows
-    const int row0 = __shfl_sync(0xFFFFFFFFu, static_cast<int>(token), 0);
-    int to[8];  // else: rows lane / 8 + 4 i, -1 past the tile
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = q * 32 + (lane >> 3) + 4 * i;
-      to[i] = r < tile.count ? ps.o.perm[tile.start + r] : -1;
-    }
+    const int team = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;  // the row of a tile, and lane of tensor memory
     Y* out = static_cast<Y*>(p.out);
-    const float sc = plain ? 0.f : (p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f);
+    int tiles = 0, held = -1;  // tiles with a product so far; the stage whose store is under way
+    auto release = [&]() {
+      __syncwarp();
+      if (held >= 0 && lane == 0) mbar_arrive(&ctl.yempty[held]);
+      held = -1;
+    };
     grid_dependency_wait();  // u is the launch before this one's
-    if (!plain) {
-      const float* src = p.u + token * p.R;
-      const bool vec = p.R % 4 == 0 && (reinterpret_cast<uintptr_t>(p.u) & 15u) == 0;
-      constexpr int kAtOnce = RP / 8 < 4 ? RP / 8 : 4;  // pieces of 8 ranks loaded before any is split
-#pragma unroll 1
-      for (int p0 = 0; p0 < RP / 8; p0 += kAtOnce) {
-        float v[kAtOnce][8];
+    for_tiles([&](const Tile& tile, int64_t c0, int n) {
+      const bool plain = tile.adapter < 0;
+      const bool run = tile.run >= 0;
+      const bool whole = run && q * 32 + 32 <= tile.count;  // 32 consecutive rows
+      const int last = tile.count - 1;
+      const int64_t token = run ? tile.run + min(row, last) : ps.o.perm[tile.start + min(row, last)];
+      int to[8];  // not whole: rows lane / 8 + 4 i, -1 past the tile
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = (p0 + i) * 8 + 4 * h;
-            if (vec) {
-              const float4 f = r < p.R ? *reinterpret_cast<const float4*>(src + r) : make_float4(0.f, 0.f, 0.f, 0.f);
-              v[i][4 * h] = f.x;
-              v[i][4 * h + 1] = f.y;
-              v[i][4 * h + 2] = f.z;
-              v[i][4 * h + 3] = f.w;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[i][4 * h + e] = r + e < p.R ? src[r + e] : 0.f;
-            }
-          }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          uint32_t t[4][TERMS];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split_pair<TERMS>(v[i][2 * e], v[i][2 * e + 1], t[e]);
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            const uint32_t w[4] = {t[0][k], t[1][k], t[2][k], t[3][k]};
-            st_shared16(u_at + k * Cfg::U::kBytes + Cfg::U::at(row, p0 + i), w);
-          }
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int r = q * 32 + (lane >> 3) + 4 * i;
+        to[i] = whole || r > last ? -1 : (run ? tile.run + r : ps.o.perm[tile.start + r]);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&ctl.ufull);
-    }
-    bool ok = true;
-    int m = 0;
-    for (; m < n && ok; ++m) {
-      const int st = m % YS;
-      const uint32_t at = y_at + st * Cfg::kYBytes;
-      ok = wait(&ctl.yfull[st], m / YS) && (plain || wait(&ctl.dfull[m & 1], m >> 1));
-      if (!plain || !has_base) {
-        tc_fence_after();
+      const float sc = plain ? 0.f : (p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f);
+      if (!plain) {
+        // each team splits half of the ranks' pieces of 8
+        const float* src = p.u + token * p.R;
+        const bool vec = p.R % 4 == 0 && (reinterpret_cast<uintptr_t>(p.u) & 15u) == 0;
+        constexpr int kHalf = RP / 16, kAtOnce = kHalf < 4 ? kHalf : 4;  // pieces loaded before any is split
+        if (!__all_sync(0xFFFFFFFFu, tiles == 0 || wait(&ctl.uempty, tiles - 1))) return false;
+        ++tiles;
+#pragma unroll 1
+        for (int p0 = team * kHalf; p0 < (team + 1) * kHalf; p0 += kAtOnce) {
+          float v[kAtOnce][8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 32 columns at a time
-          uint32_t d[32];
-          if (!plain) {
-            tmem_ld32(tmem + (q * 32u << 16) + (m & 1) * kChunk + h * 32, d);
-            tmem_wait_ld();
-          }
-          constexpr int kPer = 16 / static_cast<int>(sizeof(Y)), kPieces = 32 / kPer;
+          for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-          for (int j = 0; j < kPieces; ++j) {
-            const int piece = h * kPieces + j;  // of the row's chunk; 8 pieces to a 128-byte block
-            const uint32_t a = at + (piece / 8) * (kTileRows * 128) + row * 128 + (((piece & 7) ^ (row & 7)) * 16);
-            uint4 b = make_uint4(0u, 0u, 0u, 0u);
-            if (has_base) b = ld_shared16(a);
-            uint32_t v[4] = {b.x, b.y, b.z, b.w};
-            if (!plain) {
+            for (int h = 0; h < 2; ++h) {
+              const int r = (p0 + i) * 8 + 4 * h;
+              if (vec) {
+                const float4 f = r < p.R ? *reinterpret_cast<const float4*>(src + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[i][4 * h] = f.x;
+                v[i][4 * h + 1] = f.y;
+                v[i][4 * h + 2] = f.z;
+                v[i][4 * h + 3] = f.w;
+              } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (sizeof(Y) == 2)
-                  v[e] = pack2(fmaf(sc, __uint_as_float(d[j * 8 + 2 * e]), __uint_as_float(v[e] << 16)),
-                               fmaf(sc, __uint_as_float(d[j * 8 + 2 * e + 1]), __uint_as_float(v[e] & 0xFFFF0000u)));
-                else
-                  v[e] = __float_as_uint(fmaf(sc, __uint_as_float(d[j * 4 + e]), __uint_as_float(v[e])));
+                for (int e = 0; e < 4; ++e) v[i][4 * h + e] = r + e < p.R ? src[r + e] : 0.f;
               }
             }
-            st_shared16(a, v);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            uint32_t t[4][TERMS];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split_pair<TERMS>(v[i][2 * e], v[i][2 * e + 1], t[e]);
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+              const uint32_t w[4] = {t[0][k], t[1][k], t[2][k], t[3][k]};
+              st_shared16(u_at + k * Cfg::U::kBytes + Cfg::U::at(row, p0 + i), w);
+            }
           }
         }
-        tc_fence_before();
+        fence_proxy_async_smem();
+        mbar_arrive(&ctl.ufull);
       }
-      fence_proxy_async_smem();  // before a TMA store reads the stage
-      __syncwarp();
-      if (!plain && lane == 0) mbar_arrive(&ctl.dempty[m & 1]);
-      const int64_t k = (c_begin + m) * kChunk;
-      if (whole) {
-        if (lane < kBlocks && k + lane * kBlockCols < p.C)
-          tma_store_2d(&ps.out, at + lane * (kTileRows * 128) + q * 4096, static_cast<int>(k) + lane * kBlockCols, row0);
-        bulk_commit();
-        bulk_wait_read<1>();  // the chunk before has left its stage
-        __syncwarp();
-        if (m > 0 && lane == 0) mbar_arrive(&ctl.yempty[(m - 1) % YS]);
-      } else {
-        constexpr int kPer = 16 / static_cast<int>(sizeof(Y));
+      for (int i = 0; i < n; ++i, ++c, m += plain ? 0 : 1) {
+        if ((c & 1) != team) continue;
+        const int st = c % YS, ds = m % DS;
+        const uint32_t at = y_at + st * Cfg::kYBytes;
+        const bool ok = wait(&ctl.yfull[st], c / YS) && (plain || wait(&ctl.dfull[ds], m / DS));
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        if (!plain || !has_base) {
+          tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const int64_t col = k + b * kBlockCols + (lane & 7) * kPer;
+          for (int h = 0; h < 2; ++h) {  // 32 columns at a time
+            uint32_t d[32];
+            if (!plain) {
+              tmem_ld32(tmem + (q * 32u << 16) + ds * kChunk + h * 32, d);
+              tmem_wait_ld();
+            }
+            constexpr int kPer = 16 / static_cast<int>(sizeof(Y)), kPieces = 32 / kPer;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = q * 32 + (lane >> 3) + 4 * i;
-            const uint4 v = ld_shared16(at + b * (kTileRows * 128) + r * 128 + (((lane & 7) ^ (r & 7)) * 16));
-            if (to[i] < 0 || col >= p.C) continue;
-            Y* dst = out + to[i] * p.ld_out;
-            if (col + kPer <= p.C)
-              *reinterpret_cast<uint4*>(dst + col) = v;
-            else
-              write_piece<Y>(dst, col, p.C, v);
+            for (int j = 0; j < kPieces; ++j) {
+              const int piece = h * kPieces + j;  // of the row's chunk; 8 pieces to a 128-byte block
+              const uint32_t a = at + (piece / 8) * (kTileRows * 128) + row * 128 + (((piece & 7) ^ (row & 7)) * 16);
+              uint4 b = make_uint4(0u, 0u, 0u, 0u);
+              if (has_base) b = ld_shared16(a);
+              uint32_t v[4] = {b.x, b.y, b.z, b.w};
+              if (!plain) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if constexpr (sizeof(Y) == 2)
+                    v[e] = pack2(fmaf(sc, __uint_as_float(d[j * 8 + 2 * e]), __uint_as_float(v[e] << 16)),
+                                 fmaf(sc, __uint_as_float(d[j * 8 + 2 * e + 1]), __uint_as_float(v[e] & 0xFFFF0000u)));
+                  else
+                    v[e] = __float_as_uint(fmaf(sc, __uint_as_float(d[j * 4 + e]), __uint_as_float(v[e])));
+                }
+              }
+              st_shared16(a, v);
+            }
           }
+          tc_fence_before();
         }
-        fence_proxy_async_smem();  // the stage may be TMA's next
+        fence_proxy_async_smem();  // before a TMA store reads the stage
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.yempty[st]);
+        if (!plain && lane == 0) mbar_arrive(&ctl.dempty[ds]);
+        const int64_t k = (c0 + i) * kChunk;
+        if (whole) {
+          if (lane < kBlocks && k + lane * kBlockCols < p.C)
+            tma_store_2d(&ps.out, at + lane * (kTileRows * 128) + q * 4096, static_cast<int>(k) + lane * kBlockCols,
+                         tile.run + q * 32);
+          bulk_commit();
+          if constexpr (kDefer) {
+            bulk_wait_read<1>();
+            release();
+            held = st;
+          } else {
+            held = st;
+            bulk_wait_read<0>();
+            release();
+          }
+        } else {
+          constexpr int kPer = 16 / static_cast<int>(sizeof(Y));
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            const int64_t col = k + b * kBlockCols + (lane & 7) * kPer;
+#pragma unroll
+            for (int i8 = 0; i8 < 8; ++i8) {
+              const int r = q * 32 + (lane >> 3) + 4 * i8;
+              const uint4 v = ld_shared16(at + b * (kTileRows * 128) + r * 128 + (((lane & 7) ^ (r & 7)) * 16));
+              if (to[i8] < 0 || col >= p.C) continue;
+              Y* dst = out + to[i8] * p.ld_out;
+              if (col + kPer <= p.C)
+                *reinterpret_cast<uint4*>(dst + col) = v;
+              else
+                write_piece<Y>(dst, col, p.C, v);
+            }
+          }
+          fence_proxy_async_smem();  // the stage may be TMA's next
+          held = st;
+          release();
+        }
       }
-    }
+      bulk_wait_read<0>();
+      release();
+      return true;
+    });
     bulk_wait<0>();
   }
   __syncthreads();
   if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies and MMAs in flight, bounded again
     int never = 0;
-    for (int j = c > WS ? c - WS : 0; j < c && !plain && ps.wtma; ++j)
+    for (int j = m > WS ? m - WS : 0; j < m && ps.wtma; ++j)
       mbar_wait(&ctl.wfull[j % WS], static_cast<uint32_t>(j / WS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
-    for (int j = c > YS ? c - YS : 0; j < c && run && has_base; ++j)
+    for (int j = c > YS ? c - YS : 0; j < c; ++j)
       mbar_wait(&ctl.yfull[j % YS], static_cast<uint32_t>(j / YS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 2 * kChunk);
+  if (warp == 1) tmem_dealloc(tmem, DS * kChunk);
 }
 
 template <int RP, int TERMS>
@@ -2326,12 +2415,7 @@ cudaError_t down(const Down& p, const Order& o, const DeviceCtx* ctx, cudaStream
 
 template <int RP, typename Y, bool TRANS>
 cudaError_t up(const Up& p, const Order& o, const DeviceCtx* ctx, cudaStream_t s) {
-  const int64_t slots = static_cast<int64_t>(o.segments) * o.tiles_per_segment;
-  const int64_t tiles = ceil_div(p.T, kTileRows) + std::min<int64_t>(p.L, ceil_div(p.T, kTileRows));
-  const int64_t chunks = ceil_div(p.C, kChunk);
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 4 * ctx->num_sms / tiles));  // two waves
-  const int per_cta = static_cast<int>(ceil_div(chunks, splits));
-  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, per_cta)));
+  const int64_t chunks = ceil_div(p.C, kChunk), tiles = ceil_div(p.T, kTileRows);
   const Waits w{ctx->status, wait_timeout_ns()};
   constexpr CUtensorMapDataType kMapY = sizeof(Y) == 2 ? kMapBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   constexpr int kBox = 128 / static_cast<int>(sizeof(Y));
@@ -2341,10 +2425,16 @@ cudaError_t up(const Up& p, const Order& o, const DeviceCtx* ctx, cudaStream_t s
     a.d = p;
     a.o = o;
     a.w = w;
-    a.chunks_per_cta = per_cta;
     a.wtma = weights_map<RP>(&a.wm, p.w, !TRANS, p.C, p.R, p.L);
-    return launch("adapter_up_tma", adapter_up_tma<RP, Y, TRANS>, a, grid, 256, UpTma<RP, Y, TRANS>::kSmem, 1, true, s);
+    const int64_t ctas = std::min<int64_t>(ctx->num_sms, ceil_div(tiles * chunks, 2));
+    return launch("adapter_up_tma", adapter_up_tma<RP, Y, TRANS>, a, dim3(static_cast<unsigned>(ctas)), 384,
+                  UpTma<RP, Y, TRANS>::kSmem, 1, true, s);
   }
+  const int64_t slots = static_cast<int64_t>(o.segments) * o.tiles_per_segment;
+  const int64_t likely = tiles + std::min<int64_t>(p.L, tiles);  // in use
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 4 * ctx->num_sms / likely));  // two waves
+  const int per_cta = static_cast<int>(ceil_div(chunks, splits));
+  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(ceil_div(chunks, per_cta)));
   return launch("adapter_up_tile", adapter_up_tile<RP, Y, TRANS>, UpSorted{p, o, w, per_cta}, grid, 256,
                 UpTile<RP, Y, TRANS>::kSmem, 1, true, s);
 }
@@ -2442,6 +2532,7 @@ Order order_at(void* workspace, int64_t T, int L, bool blocks, size_t* bytes = n
   };
   o.perm = static_cast<int*>(take(static_cast<size_t>(T) * 4));
   o.tiles = static_cast<Tile*>(take(static_cast<size_t>(o.segments) * o.tiles_per_segment * sizeof(Tile)));
+  o.used = static_cast<int*>(take(static_cast<size_t>(o.segments) * 4));
   if (blocks) {
     o.blocks = static_cast<Tile*>(take(static_cast<size_t>(o.segments) * o.blocks_per_segment * sizeof(Tile)));
     o.starts = static_cast<int*>(take(static_cast<size_t>(o.segments) * (L + 1) * 4));
