@@ -713,25 +713,26 @@ constexpr int kSiteDown = 41, kSiteUp = 42, kSiteGrads = 43;
 // columns into one: 2e-6 of the result, against 1e-6 for sums in registers).
 template <int RP>
 struct Sums {
-  static constexpr int kSums = RP <= 16 ? 8 : (RP <= 64 ? 4 : 2);
+  static constexpr int kSums = RP <= 32 ? 8 : (RP <= 64 ? 4 : 2);
   static constexpr int kTmem = kSums * RP;  // two CTAs to an SM have room, three for RP = 16
 };
-// 16 columns from tensor memory, of the first n accumulators and (LAST, n > 0)
-// the last one, to dst.
-template <int RP, bool LAST>
+// Adds 16 columns from tensor memory.
+__device__ __forceinline__ void add_sums16(uint32_t tmem, float (&v)[16]) {
+  uint32_t w[16];
+  tmem_ld16(tmem, w);
+  tmem_wait_ld();
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
+}
+// 16 columns of the first n accumulators, to dst.
+template <int RP>
 __device__ __forceinline__ void read_sums16(uint32_t tmem, int n, float* dst) {
   float v[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] = 0.f;
 #pragma unroll
   for (int k = 0; k < Sums<RP>::kSums; ++k)
-    if (k < n || (LAST && n > 0 && k == Sums<RP>::kSums - 1)) {
-      uint32_t w[16];
-      tmem_ld16(tmem + k * RP, w);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
-    }
+    if (k < n) add_sums16(tmem + k * RP, v);
 #pragma unroll
   for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
 }
@@ -750,7 +751,6 @@ struct DownTile {
   static constexpr int kStages = RP <= 32 ? 5 : (RP <= 64 ? 4 : 3);  // two CTAs to an SM
   using X = Staged<kTileRows, kChunk>;
   using W = Staged<TRANS ? kChunk : RP, TRANS ? RP : kChunk>;
-  static constexpr int kWPieces = (TRANS ? RP : kChunk) / 8;
   static constexpr int kXBytes = X::kBytes, kWBytes = W::kBytes;
   static constexpr int kStageBytes = kXBytes + kWBytes;
   static constexpr int kPitch = RP + 4;  // of the sums' rows, in floats
@@ -854,8 +854,9 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
       for (int r = tid >> 3; r < p.R; r += 32)
         stage8(wt + Cfg::W::at(r, piece), w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C);
     } else {
-      for (int i = tid; i < kChunk * Cfg::kWPieces; i += 256) {
-        const int c64 = i / Cfg::kWPieces, pr = i % Cfg::kWPieces;
+      constexpr int kPieces = RP / 8;
+      for (int i = tid; i < kChunk * kPieces; i += 256) {
+        const int c64 = i / kPieces, pr = i % kPieces;
         if (pr * 8 < p.R)
           stage8(wt + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0);
       }
@@ -900,7 +901,7 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int j = 0; j < kHalf; j += 16) read_sums16<RP, false>(src + j, c, dst + j);
+      for (int j = 0; j < kHalf; j += 16) read_sums16<RP>(src + j, c, dst + j);
     }
   }
   tc_fence_before();
@@ -926,7 +927,6 @@ struct UpTile {
   static constexpr int kWStages = kYStages + 1;
   using U = Staged<kTileRows, RP>;  // one term
   using W = Staged<TRANS ? RP : kChunk, TRANS ? kChunk : RP>;
-  static constexpr int kWPieces = (TRANS ? kChunk : RP) / 8;
   static constexpr int kUBytes = TERMS * U::kBytes, kWBytes = W::kBytes;
   static constexpr int kYBytes = kTileRows * kChunk * static_cast<int>(sizeof(Y));
   using Ctl = Control<2>;
@@ -1045,8 +1045,9 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
     const uint32_t at = w_at + (c % WS) * Cfg::kWBytes;
     const int64_t k = (c_begin + c) * kChunk;
     if constexpr (!TRANS) {
-      for (int i = tid; i < kChunk * Cfg::kWPieces; i += 256) {
-        const int c64 = i / Cfg::kWPieces, pr = i % Cfg::kWPieces;
+      constexpr int kPieces = RP / 8;
+      for (int i = tid; i < kChunk * kPieces; i += 256) {
+        const int c64 = i / kPieces, pr = i % kPieces;
         if (pr * 8 < p.R)
           stage8(at + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0);
       }
@@ -1256,7 +1257,7 @@ struct GradTile {
   static constexpr int kXBytes = X::kBytes;                               // a block of bf16
   static constexpr int kCodeBytes = kGradRows * kGradCols + 256 * 2 * 4;  // of codes, and each copy's scale word
   static constexpr int kStages = RP <= 16 ? 4 : (RP <= 32 || (RP <= 64 && TERMS == 2) ? 3 : 2);  // two CTAs to an SM (one from RP = 128 on)
-  static constexpr int kTermBytes = Image::kTermBytes, kCoefBytes = Image::kBytes;
+  static constexpr int kCoefBytes = Image::kBytes;
   static constexpr int kIdxSlots = 8;
   static constexpr int kPitch = RP + 4;  // of the sums' rows (one to a column), in floats
   // bf16: the ring; codes: two decoded blocks and the ring.  Then the
@@ -1268,14 +1269,50 @@ struct GradTile {
   static constexpr int kCtlAt = kIdxAt + kIdxSlots * kGradRows * 4;
   static_assert(kGradCols * kPitch * 4 <= kCtlAt, "the sums reuse the space before");
   static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
-  static constexpr int kSums = Sums<RP>::kSums, kTmem = Sums<RP>::kTmem;
-  // Blocks take turns at the accumulators but the last, which is that of the
-  // coefficients' lower terms.
-  static __device__ __forceinline__ int sum_of(int block, int term) {
-    return term == 0 ? block % (kSums - 1) : kSums - 1;
+  // A block's terms side by side are one operand of TERMS RP columns: one MMA
+  // takes them all, and reads x once (one each, and x was read from shared
+  // memory three times: 8192 tokens, 8192 columns, rank 16, 73 us).  Blocks take
+  // turns at the sets of accumulators.  Where a set is too wide for two of them
+  // the terms go one by one, the lower ones to the last accumulator.
+  static constexpr bool kWide = TERMS * RP <= 128;
+  static constexpr int kTmem = Sums<RP>::kTmem;
+  static constexpr int kSetCols = kWide ? TERMS * RP : RP, kSets = kWide ? kTmem / kSetCols : Sums<RP>::kSums - 1;
+  static __device__ __forceinline__ void block(uint32_t tmem, int b, uint32_t x, uint32_t coef) {
+    const uint32_t d = tmem + (b % kSets) * kSetCols;
+    if constexpr (kWide) {
+#pragma unroll
+      for (int s = 0; s < kGradRows / 16; ++s)
+        mma_f16(d, X::along_rows(x, s), Coef::along_rows(coef, s), mma_shape(TERMS * RP, true, true),
+                (b >= kSets || s > 0) ? 1u : 0u);
+    } else {
+#pragma unroll
+      for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+        for (int s = 0; s < kGradRows / 16; ++s)
+          mma_f16(k == 0 ? d : tmem + kSets * RP, X::along_rows(x, s), Coef::along_rows(coef + k * Image::kTermBytes, s),
+                  mma_shape(RP, true, true),
+                  (s > 0 || (k == 0 ? b >= kSets : b > 0 || k < TERMS - 1)) ? 1u : 0u);
+    }
   }
-  static __device__ __forceinline__ bool continues(int block, int term, int step) {
-    return step > 0 || (term == 0 ? block >= kSums - 1 : block > 0 || term < TERMS - 1);
+  // 16 columns of n blocks' sums, to dst.
+  static __device__ __forceinline__ void read_sums16(uint32_t tmem, int n, float* dst) {
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    if constexpr (kWide) {
+#pragma unroll
+      for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+        for (int s = 0; s < kSets; ++s)
+          if (s < n) add_sums16(tmem + s * kSetCols + k * RP, v);
+    } else {
+      if (n > 0) add_sums16(tmem + kSets * RP, v);
+#pragma unroll
+      for (int s = 0; s < kSets; ++s)
+        if (s < n) add_sums16(tmem + s * RP, v);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
   }
 };
 
@@ -1362,7 +1399,7 @@ __device__ __forceinline__ void write_grad(const Grads& p, const GradJob& j, con
 template <int RP, int TERMS, typename G>
 __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Grads p) {
   using Cfg = GradTile<RP, TERMS>;
-  constexpr int S = Cfg::kStages, kSteps = kGradRows / 16;
+  constexpr int S = Cfg::kStages;
   extern __shared__ __align__(1024) uint8_t ring[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kCtlAt);
   const uint32_t ring_at = smem_u32(ring), coef_at = ring_at + Cfg::kRing, codes_at = ring_at + 2 * Cfg::kXBytes;
@@ -1488,12 +1525,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
     if (tid == 0) {
       const uint32_t xt = ring_at + (kept ? b & 1 : b % S) * Cfg::kXBytes;
       const uint32_t ct = coef_at + (b % S) * Cfg::kCoefBytes;
-#pragma unroll
-      for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-          mma_f16(tmem + Cfg::sum_of(b, k) * RP, Cfg::X::along_rows(xt, s), Cfg::Coef::along_rows(ct + k * Cfg::kTermBytes, s),
-                  mma_shape(RP, true, true), Cfg::continues(b, k, s) ? 1u : 0u);
+      Cfg::block(tmem, b, xt, ct);
       tc_commit(&ctl.done[b & 1]);
     }
     if (b > 0)
@@ -1520,7 +1552,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int k = 0; k < kHalf; k += 16) read_sums16<RP, true>(src + k, b, dst + k);
+      for (int k = 0; k < kHalf; k += 16) Cfg::read_sums16(src + k, b, dst + k);
     }
   }
   tc_fence_before();
@@ -1725,7 +1757,7 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int j = 0; j < RP; j += 16) read_sums16<RP, false>(tmem + (q * 32u << 16) + j, n, dst + j);
+    for (int j = 0; j < RP; j += 16) read_sums16<RP>(tmem + (q * 32u << 16) + j, n, dst + j);
   }
   tc_fence_before();
   __syncthreads();
@@ -2146,7 +2178,7 @@ template <int RP, int TERMS, typename G>
 __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
   using Cfg = GradTma<RP, TERMS>;
   using Coef = typename Cfg::Coef;
-  constexpr int S = Cfg::kStages, ND = Cfg::kDecoded, kSteps = kGradRows / 16;
+  constexpr int S = Cfg::kStages, ND = Cfg::kDecoded;
   extern __shared__ __align__(1024) uint8_t ring[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
   const Grads& p = ps.g;
@@ -2214,12 +2246,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
         tc_fence_after();
         const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
         const uint32_t xt = kept ? smem_u32(ring) + (b % ND) * Cfg::kXBytes : at;
-#pragma unroll
-        for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s)
-            mma_f16(tmem + Cfg::sum_of(b, k) * RP, Cfg::X::along_rows(xt, s), Coef::along_rows(ct + k * Cfg::kTermBytes, s),
-                    mma_shape(RP, true, true), Cfg::continues(b, k, s) ? 1u : 0u);
+        Cfg::block(tmem, b, xt, ct);
         tc_commit(&ctl.empty[st]);
         ++b;
       }
@@ -2325,7 +2352,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int k = 0; k < RP; k += 16) read_sums16<RP, true>(tmem + (q * 32u << 16) + k, blocks, dst + k);
+    for (int k = 0; k < RP; k += 16) Cfg::read_sums16(tmem + (q * 32u << 16) + k, blocks, dst + k);
   }
   tc_fence_before();
   __syncthreads();
