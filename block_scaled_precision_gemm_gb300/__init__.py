@@ -634,12 +634,14 @@ def _fits(t, dtype, shape, dev) -> bool:
     """Whether a tensor is all that its checks ask for.  A call whose tensors
     all fit skips the checks that say what is wrong; one that does not goes
     through them (small calls spend most of their time on the host)."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-            and t.is_contiguous())
+    try:
+        return t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous()
+    except AttributeError:  # not a tensor
+        return False
 
 
 def _current(t) -> bool:
-    return isinstance(t, torch.Tensor) and t.is_cuda and t.device.index == torch.cuda.current_device()
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == torch._C._cuda_getDevice()
 
 
 def _empty(shape, dtype, dev, stream):
