@@ -2399,10 +2399,6 @@ cudaError_t launch(const char* name, void (*kernel)(P), const P& p, dim3 grid, i
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// T R (R padded to a power of two from 16 on) from which tokens are sorted and
-// worked on in tiles of one adapter; below, taken as they come.
-constexpr int64_t kSortFrom = 8192;
-
 constexpr CUtensorMapDataType kMapBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
 // The weights' map for load_weights: rows of R elements {R, C, L} or of C {C, R, L}.
@@ -2443,6 +2439,7 @@ cudaError_t down(const Down& p, const Order& o, const DeviceCtx* ctx, cudaStream
 template <int RP, typename Y, bool TRANS>
 cudaError_t up(const Up& p, const Order& o, const DeviceCtx* ctx, cudaStream_t s) {
   const int64_t chunks = ceil_div(p.C, kChunk), tiles = ceil_div(p.T, kTileRows);
+  const int64_t slots = static_cast<int64_t>(o.segments) * o.tiles_per_segment;  // the most tiles that there can be
   const Waits w{ctx->status, wait_timeout_ns()};
   constexpr CUtensorMapDataType kMapY = sizeof(Y) == 2 ? kMapBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   constexpr int kBox = 128 / static_cast<int>(sizeof(Y));
@@ -2453,11 +2450,10 @@ cudaError_t up(const Up& p, const Order& o, const DeviceCtx* ctx, cudaStream_t s
     a.o = o;
     a.w = w;
     a.wtma = weights_map<RP>(&a.wm, p.w, !TRANS, p.C, p.R, p.L);
-    const int64_t ctas = std::min<int64_t>(ctx->num_sms, ceil_div(tiles * chunks, 2));
+    const int64_t ctas = std::min<int64_t>(ctx->num_sms, ceil_div(slots * chunks, 2));
     return launch("adapter_up_tma", adapter_up_tma<RP, Y, TRANS>, a, dim3(static_cast<unsigned>(ctas)), 384,
                   UpTma<RP, Y, TRANS>::kSmem, 1, true, s);
   }
-  const int64_t slots = static_cast<int64_t>(o.segments) * o.tiles_per_segment;
   const int64_t likely = tiles + std::min<int64_t>(p.L, tiles);  // in use
   const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(ceil_div(chunks, 4), 4 * ctx->num_sms / likely));  // two waves
   const int per_cta = static_cast<int>(ceil_div(chunks, splits));
@@ -2589,10 +2585,20 @@ size_t adapter_terms_bytes(int64_t T, int64_t R, int64_t L) {
   return static_cast<size_t>(blocks) * 2 * 3 * kGradRows * rp * 2;  // three terms: of binary32 gradients
 }
 
+// Whether tokens are sorted and worked on in tiles of one adapter, or taken as
+// they come.  As they come costs a pass over the weights per adapter met among
+// 16 tokens, so T R min(L, 16); sorted costs two more launches and a tile, full
+// or not, per adapter in use.  Measured, K = N = 4096, us as they come / sorted:
+//   R = 16, L = 8:    128: 18.4 / 21.6   384: 24.5 / 23.6   1024: 45 / 28
+//   R = 16, L = 64:   384: 36.8 / 50.2   777: 43.0 / 50.2   1024: 72 / 52
+//   R = 16, L = 512:  384: 53 / 153      2047: 143 / 288    4096: 264 / 264
+//   R = 32, L = 32:   128: 26.6 / 35.8   256: 40.9 / 33.8   1024: 78 / 36
+//   R = 64, L = 8:    64: 30.7 / 25.6    128: 43 / 25.6     1024: 137 / 31
+// The lines below are 0.2 ns a T R min(L, 16), and 3 us and 0.45 us a tile.
 bool adapters_sorted(int64_t T, int64_t R, int64_t L) {
   int64_t rp = 16;
   while (rp < R) rp *= 2;
-  return T * rp >= kSortFrom && L <= kSortMaxL;
+  return L <= kSortMaxL && T * rp * std::min<int64_t>(L, 16) >= 15000 + 2250 * std::min(L, T);
 }
 int64_t adapters_sort_max() { return kSortMaxL; }
 
