@@ -651,10 +651,14 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// Eight bf16 of a row from column c, zeros from `limit` on, into shared memory.
-__device__ __forceinline__ void stage8(uint32_t dst, const bf16* row, int64_t c, int64_t limit) {
+// Eight bf16 of a row from column c, zeros from `limit` on, into shared memory;
+// vec: rows are 16-byte aligned and end at a multiple of 8.
+__device__ __forceinline__ void stage8(uint32_t dst, const bf16* row, int64_t c, int64_t limit, bool vec = false) {
   uint32_t w[4];
-  load_row<8, false>(row, c, limit, w);
+  if (vec)
+    load_row<8, true>(row, c, limit, w);
+  else
+    load_row<8, false>(row, c, limit, w);
   st_shared16(dst, w);
 }
 
@@ -836,10 +840,10 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
   }
   const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
   const int piece = tid & 7;
-  const bf16* xr[4];  // this thread copies piece tid % 8 of rows tid / 8 + 32 i
-#pragma unroll
-  for (int i = 0; i < 4; ++i)  // rows past the tile repeat its last one and are not stored
-    xr[i] = p.x + ps.o.perm[tile.start + min((tid >> 3) + 32 * i, tile.count - 1)] * p.ld;
+  const bool w16 = (TRANS ? p.R : p.C) % 8 == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0;
+  const bool pairs = p.C % 2 == 0 && p.ld % 2 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 3u) == 0;
+  // a warp copies 16 rows, two columns a lane; rows past the tile repeat its last one and are not stored
+  const int token = ps.o.perm[tile.start + min(warp * 16 + (lane & 15), tile.count - 1)];
   const int64_t chunks = (p.C + kChunk - 1) / kChunk;
   const int64_t c_begin = chunks * rank / cs, c_end = chunks * (rank + 1) / cs;
   const int n = static_cast<int>(c_end - c_begin);
@@ -847,18 +851,39 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
   auto issue = [&](int c) {  // chunk c of this CTA's range into stage c % S
     const uint32_t at = ring_at + (c % S) * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
     const int64_t k = (c_begin + c) * kChunk;
+    const int64_t col = k + 2 * lane;
+    uint32_t v[16];
+    auto row = [&](int r) { return p.x + static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, token, r)) * p.ld + col; };
+    if (pairs) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      stage8(at + Cfg::X::at((tid >> 3) + 32 * i, piece), xr[i], k + piece * 8, p.C);
+      for (int r = 0; r < 16; ++r) {
+        const bf16* at_row = row(r);
+        v[r] = col < p.C ? __ldg(reinterpret_cast<const unsigned int*>(at_row)) : 0u;
+      }
+    } else {
+      uint32_t hi[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const bf16* at_row = row(r);
+        v[r] = col < p.C ? raw16(at_row) : 0u;
+        hi[r] = col + 1 < p.C ? raw16(at_row + 1) : 0u;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] |= hi[r] << 16;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + Cfg::X::at(warp * 16 + r, lane >> 2) + (lane & 3) * 4), "r"(v[r])
+                   : "memory");
     if constexpr (!TRANS) {
       for (int r = tid >> 3; r < p.R; r += 32)
-        stage8(wt + Cfg::W::at(r, piece), w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C);
+        stage8(wt + Cfg::W::at(r, piece), w + static_cast<int64_t>(r) * p.C, k + piece * 8, p.C, w16);
     } else {
       constexpr int kPieces = RP / 8;
       for (int i = tid; i < kChunk * kPieces; i += 256) {
         const int c64 = i / kPieces, pr = i % kPieces;
         if (pr * 8 < p.R)
-          stage8(wt + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0);
+          stage8(wt + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0, w16);
       }
     }
   };
@@ -913,24 +938,26 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
 // ---------------------------------------------------------------------------
 // out = base + s W u for a tile of 128 tokens of one adapter
 // ---------------------------------------------------------------------------
-// The tile's u is split once into TERMS bf16 terms in shared memory (three for
-// binary32 outputs, which keep its 24 bits; two, 16 bits, for bf16 ones).
-// Chunks of 64 columns then stream through: one thread issues the tcgen05 MMAs
-// of chunk c + 1 into one of two accumulators in tensor memory, and each warp
-// adds chunk c's 32 rows x 32 columns to base in shared memory and writes them
-// out along the rows.
+// For outputs whose rows are not 16-byte aligned.  The tile's u is split once
+// into TERMS bf16 terms in shared memory (three for binary32 outputs, which keep
+// its 24 bits; two, 16 bits, for bf16 ones).  Chunks of 64 columns then stream
+// through: one thread issues the tcgen05 MMAs of chunk c + 1 into one of two
+// accumulators in tensor memory, while each warp loads its 32 rows x 32 columns
+// of base, lanes along the rows, takes chunk c's product through shared memory
+// to the same lanes, and stores the sum from there.  (With a lane's eight
+// elements in a row, as pieces of 16 bytes, an instruction touched 16 sectors
+// instead of 2 or 3: 6262 tokens of 6972 columns and rank 16 took 225 us.)
 template <int RP, typename Y, bool TRANS>
 struct UpTile {
   static constexpr int TERMS = sizeof(Y) == 4 ? 3 : 2;
-  static constexpr bool kTwo = sizeof(Y) == 2 ? RP <= 64 : RP <= 32;  // two CTAs fit an SM
-  static constexpr int kYStages = sizeof(Y) == 2 ? (RP <= 32 ? 4 : 3) : (kTwo || RP == 128 ? 2 : 4);
-  static constexpr int kWStages = kYStages + 1;
+  static constexpr int kWStages = 3;
   using U = Staged<kTileRows, RP>;  // one term
   using W = Staged<TRANS ? RP : kChunk, TRANS ? kChunk : RP>;
   static constexpr int kUBytes = TERMS * U::kBytes, kWBytes = W::kBytes;
   static constexpr int kYBytes = kTileRows * kChunk * static_cast<int>(sizeof(Y));
+  static constexpr int kPitch = 34;  // of a warp's 32 rows of products, in floats
   using Ctl = Control<2>;
-  static constexpr int kCtlAt = kUBytes + kWStages * kWBytes + kYStages * kYBytes;
+  static constexpr int kCtlAt = kUBytes + kWStages * kWBytes + 8 * 32 * kPitch * 4;
   static constexpr int kSmem = kCtlAt + static_cast<int>(sizeof(Ctl));
 };
 
@@ -941,18 +968,7 @@ struct UpSorted {
   int chunks_per_cta;
 };
 
-// 16 bytes of a row of Y from column c as one staged piece, and back.
-template <typename Y>
-__device__ __forceinline__ void stage_piece(uint32_t dst, const Y* row, int64_t c, int64_t limit) {
-  if constexpr (sizeof(Y) == 2) {
-    stage8(dst, row, c, limit);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = c + i < limit ? __float_as_uint(row[c + i]) : 0u;
-    st_shared16(dst, w);
-  }
-}
+// 16 bytes of a row of Y, up to its end.
 template <typename Y>
 __device__ __forceinline__ void write_piece(Y* row, int64_t c, int64_t limit, uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -967,27 +983,17 @@ __device__ __forceinline__ void write_piece(Y* row, int64_t c, int64_t limit, ui
 }
 
 template <int RP, typename Y, bool TRANS>
-__global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ UpSorted ps) {
+__global__ void __launch_bounds__(256, 2) adapter_up_tile(const __grid_constant__ UpSorted ps) {
   using Cfg = UpTile<RP, Y, TRANS>;
-  constexpr int TERMS = Cfg::TERMS, YS = Cfg::kYStages, WS = Cfg::kWStages;
-  constexpr int kPer = 16 / static_cast<int>(sizeof(Y));  // elements of a piece
-  constexpr int kRowPieces = 32 / kPer;                   // of a warp's 32 columns
-  constexpr int kCopies = kRowPieces;                     // pieces a lane copies: 32 rows x kRowPieces / 32 lanes
+  constexpr int TERMS = Cfg::TERMS, WS = Cfg::kWStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(smem + Cfg::kCtlAt);
   const Up& p = ps.d;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t u_at = smem_u32(smem), w_at = u_at + Cfg::kUBytes;
-  // the warp's corner of a base stage: 32 rows x 32 columns
+  // a warp's 32 rows and 32 columns of a chunk, and its products
   const int row0 = (warp & 3) * 32, colw = (warp >> 2) * 32;
-  constexpr int kCorner = 32 * 32 * static_cast<int>(sizeof(Y));
-  const uint32_t y_at = w_at + WS * Cfg::kWBytes + warp * kCorner;
-  // pieces are swizzled so that neither a row's pieces (copies) nor a column of
-  // pieces (one row to a lane) meets a bank twice
-  auto corner = [&](int row, int piece) -> uint32_t {
-    if constexpr (sizeof(Y) == 2) return row * 64 + ((piece ^ ((row >> 1) & 3)) * 16);
-    return row * 128 + ((piece ^ (row & 7)) * 16);
-  };
+  float* mine = reinterpret_cast<float*>(smem + Cfg::kUBytes + WS * Cfg::kWBytes) + warp * 32 * Cfg::kPitch;
 
   const Tile tile = ps.o.tiles[blockIdx.x];  // of two launches before, done before the last one released this one
   if (tile.count == 0) return;
@@ -999,24 +1005,22 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
 
   if (tile.adapter < 0) {  // no product: out = base
     const int64_t c0 = c_begin * kChunk, c1 = min(p.C, c0 + static_cast<int64_t>(n) * kChunk);
-    constexpr int kRows = sizeof(Y) == 2 ? 4 : 2;  // loaded before any is stored
-    for (int64_t c = c0 + lane * 8; c < c1; c += 256)
-      for (int r = warp * kRows; r < tile.count; r += 8 * kRows) {
-        float v[kRows][8];
-        int64_t at[kRows];
+    const int r0 = warp * 16 + (lane & 15);  // a warp's 16 rows, all of their loads under way at once
+    const int token = r0 < tile.count ? ps.o.perm[tile.start + r0] : -1;
+    for (int64_t c = c0; c < c1; c += 32) {
+      const int64_t col = c + lane;
+      Y y[16];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          at[i] = r + i < tile.count ? ps.o.perm[tile.start + r + i] : -1;
-          if (base && at[i] >= 0)
-            load_out<Y, false>(base + at[i] * p.ld_base, c, p.C, v[i]);
-          else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (at[i] >= 0) store_out<Y, false>(out + at[i] * p.ld_out, c, p.C, v[i]);
+      for (int r = 0; r < 16; ++r) {
+        const int64_t t = __shfl_sync(0xFFFFFFFFu, token, r);
+        y[r] = base && t >= 0 && col < c1 ? base[t * p.ld_base + col] : Y(0.f);
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int64_t t = __shfl_sync(0xFFFFFFFFu, token, r);
+        if (t >= 0 && col < c1) out[t * p.ld_out + col] = y[r];
+      }
+    }
     return;
   }
   if (warp == 0) {
@@ -1035,12 +1039,8 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
   }
   __syncthreads();
   const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
-  int copy_row[kCopies];  // the tokens whose pieces this lane copies
-#pragma unroll
-  for (int i = 0; i < kCopies; ++i) {
-    const int r = row0 + i * (32 / kRowPieces) + lane / kRowPieces;
-    copy_row[i] = r < tile.count ? ps.o.perm[tile.start + r] : -1;
-  }
+  const bool w16 = (TRANS ? p.C : p.R) % 8 == 0 && (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0;
+  const int token = row0 + lane < tile.count ? ps.o.perm[tile.start + row0 + lane] : -1;  // of row `lane`
   auto issue_w = [&](int c) {
     const uint32_t at = w_at + (c % WS) * Cfg::kWBytes;
     const int64_t k = (c_begin + c) * kChunk;
@@ -1049,22 +1049,11 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
       for (int i = tid; i < kChunk * kPieces; i += 256) {
         const int c64 = i / kPieces, pr = i % kPieces;
         if (pr * 8 < p.R)
-          stage8(at + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0);
+          stage8(at + Cfg::W::at(c64, pr), w + (k + c64) * p.R, pr * 8, k + c64 < p.C ? p.R : 0, w16);
       }
     } else {
       for (int r = tid >> 3; r < p.R; r += 32)
-        stage8(at + Cfg::W::at(r, tid & 7), w + static_cast<int64_t>(r) * p.C, k + (tid & 7) * 8, p.C);
-    }
-  };
-  auto issue_y = [&](int c) {
-    if (!base) return;
-    const uint32_t at = y_at + (c % YS) * Cfg::kYBytes;
-    const int64_t k = (c_begin + c) * kChunk + colw;
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int r = i * (32 / kRowPieces) + lane / kRowPieces, piece = lane % kRowPieces;
-      if (copy_row[i] >= 0)
-        stage_piece<Y>(at + corner(r, piece), base + copy_row[i] * p.ld_base, k + piece * kPer, p.C);
+        stage8(at + Cfg::W::at(r, tid & 7), w + static_cast<int64_t>(r) * p.C, k + (tid & 7) * 8, p.C, w16);
     }
   };
   auto issue_mma = [&](int c) {  // one thread
@@ -1079,13 +1068,8 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
                 (k < TERMS - 1 || s > 0) ? 1u : 0u);
     tc_commit(&ctl.done[c & 1]);
   };
-  // the weights run a chunk ahead of base
   issue_w(0);
-#pragma unroll
-  for (int c = 0; c < YS - 1; ++c) {
-    if (c + 1 < n) issue_w(c + 1);
-    if (c < n) issue_y(c);
-  }
+  if (n > 1) issue_w(1);
   const float sc = p.scaling ? __ldg(p.scaling + tile.adapter) : 1.f;
   grid_dependency_wait();  // u is the launch before this one's
   for (int i = tid; i < kTileRows * (RP / 8); i += 256) {
@@ -1108,6 +1092,18 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
   __syncthreads();
   tc_fence_after();
   if (tid == 0) issue_mma(0);
+  // base runs a chunk ahead, in registers
+  auto load_y = [&](int c, Y(&y)[32]) {
+    const int64_t col = (c_begin + c) * kChunk + colw + lane;
+    const bool in = base && c < n && col < p.C;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const int64_t t = __shfl_sync(0xFFFFFFFFu, token, r);
+      y[r] = in && t >= 0 ? base[t * p.ld_base + col] : Y(0.f);
+    }
+  };
+  Y y[32];
+  load_y(0, y);
   bool ok = true;
   int c = 0;
   for (; c < n; ++c) {
@@ -1116,43 +1112,30 @@ __global__ void __launch_bounds__(256) adapter_up_tile(const __grid_constant__ U
     if (__syncthreads_or(!ok)) break;
     tc_fence_after();
     if (tid == 0 && c + 1 < n) issue_mma(c + 1);
+    const int64_t col = (c_begin + c) * kChunk + colw + lane;
+    const bool in = col < p.C;
+    Y ahead[32];
+    load_y(c + 1, ahead);
     // the weights of chunk c - 1 have been read (its accumulator was waited for)
-    if (c + YS < n) issue_w(c + YS);
-    if (c + YS - 1 < n) issue_y(c + YS - 1);
+    if (c + 2 < n) issue_w(c + 2);
     ok = mbar_wait(&ctl.done[c & 1], static_cast<uint32_t>(c >> 1) & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status,
                    kSiteUp);
+    __syncwarp();
     tc_fence_after();
     uint32_t d[32];
     tmem_ld32(ctl.tmem + ((warp & 3) * 32u << 16) + (c & 1) * kChunk + colw, d);
     tmem_wait_ld();
-    // lane: row row0 + lane, the warp's 32 columns
-    const uint32_t at = y_at + (c % YS) * Cfg::kYBytes;
 #pragma unroll
-    for (int j = 0; j < kRowPieces; ++j) {
-      const uint32_t a = at + corner(lane, j);
-      uint4 b = make_uint4(0u, 0u, 0u, 0u);
-      if (base) b = ld_shared16(a);
-      const uint32_t v[4] = {b.x, b.y, b.z, b.w};
-      uint32_t r[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(Y) == 2)
-          r[e] = pack2(fmaf(sc, __uint_as_float(d[j * 8 + 2 * e]), __uint_as_float(v[e] << 16)),
-                       fmaf(sc, __uint_as_float(d[j * 8 + 2 * e + 1]), __uint_as_float(v[e] & 0xFFFF0000u)));
-        else
-          r[e] = __float_as_uint(fmaf(sc, __uint_as_float(d[j * 4 + e]), __uint_as_float(v[e])));
-      }
-      st_shared16(a, r);
-    }
+    for (int e = 0; e < 32; ++e) mine[lane * Cfg::kPitch + e] = __uint_as_float(d[e]);
     __syncwarp();
-    const int64_t k = (c_begin + c) * kChunk + colw;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int r = i * (32 / kRowPieces) + lane / kRowPieces, piece = lane % kRowPieces;
-      const uint4 v = ld_shared16(at + corner(r, piece));
-      if (copy_row[i] >= 0) write_piece<Y>(out + copy_row[i] * p.ld_out, k + piece * kPer, p.C, v);
+    for (int r = 0; r < 32; ++r) {
+      const int64_t t = __shfl_sync(0xFFFFFFFFu, token, r);
+      const float v = fmaf(sc, mine[r * Cfg::kPitch + lane], static_cast<float>(y[r]));
+      if (in && t >= 0) out[t * p.ld_out + col] = static_cast<Y>(v);
+      y[r] = ahead[r];
     }
-    __syncwarp();  // before the next copies into this corner
+    __syncwarp();  // before the next products
   }
   if (c < n) {  // gave up: the MMAs in flight, bounded again, before their operands' memory goes
     int never = 0;
@@ -2517,7 +2500,8 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
   if (e != cudaSuccess) return e;
   const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
   unsigned cs = 1;
-  while (cs < 8 && tiles * p.L * cs < 4 * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
+  constexpr int kResident = RP <= 16 ? 3 : (RP <= 64 ? 2 : 1);  // CTAs to an SM
+  while (cs < 8 && tiles * p.L * cs < (kResident + 1) * ctx->num_sms && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
   const dim3 grid(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L));
   GradTmaArgs a{};
   bool tma = true;
