@@ -1,26 +1,32 @@
 // Low-rank adapters of many requests beside a shared projection, and their
 // backward pass.
 //
-//   u[t]   = A[id[t]] x[t]                       adapter_down
-//   out[t] = y[t] + s[id[t]] B[id[t]] u[t]       adapter_up
-//   d[t]   = B[id[t]]^T dy[t]                    adapter_down, transposed weights
-//   dx[t]  = dx_base[t] + s[id[t]] A[id[t]]^T d[t]   adapter_up, transposed weights
-//   dA[l]  = s[l] sum_t d[t] x[t]^T, dB[l] = s[l] sum_t dy[t] u[t]^T   adapter_grads
+//   u[t]   = A[id[t]] x[t]                       adapter_down_*
+//   out[t] = y[t] + s[id[t]] B[id[t]] u[t]       adapter_up_*
+//   d[t]   = B[id[t]]^T dy[t]                    adapter_down_*, transposed weights
+//   dx[t]  = dx_base[t] + s[id[t]] A[id[t]]^T d[t]   adapter_up_*, transposed weights
+//   dA[l]  = s[l] sum_t d[t] x[t]^T, dB[l] = s[l] sum_t dy[t] u[t]^T   adapter_grads*
 //
 // With ranks R of a few tens every product has about R operations per byte of
-// the streamed operand, so all of them are bound by memory, not by the tensor
-// cores.  The kernels therefore go from global memory straight into the
-// fragments of warp-level bf16 MMAs (m16n8k16, FP32 sums): the contraction
-// order and the order of the output columns are free, so they are permuted
-// until each lane's share of an operand row is 16 consecutive bytes and the
-// fragments need no shared memory and no shuffles.
+// the streamed operand, so many tokens are bound by memory, few by latency.
 //
-// Few tokens are taken as they come, and those of different adapters share MMA
-// tiles: a warp loops over the distinct adapters among its rows; each
-// adapter's product goes to accumulators of its own, of which only the rows
-// that belong to it are taken, so that an infinity or NaN in one adapter's
-// weights or in one token stays in the rows it belongs to.  Many tokens are
-// sorted first, and a tile has one adapter.
+// Few tokens are taken as they come, in one launch (adapter_rows), straight
+// from global memory into the fragments of warp-level bf16 MMAs (m16n8k16): the
+// contraction order and the order of the output columns are free, so they are
+// permuted until each lane's share of an operand row is 16 consecutive bytes and
+// the fragments need no shared memory and no shuffles.  Tokens of different
+// adapters share MMA tiles: a warp loops over the distinct adapters among its
+// rows; each adapter's product goes to accumulators of its own, of which only
+// the rows that belong to it are taken, so that an infinity or NaN in one
+// adapter's weights or in one token stays in the rows it belongs to.
+//
+// Many tokens are sorted by adapter first (adapter_sort; their rows are not
+// moved), and a tile of 128, or a block of 64 for the gradients, has one
+// adapter.  The kernels named *_tma then feed tcgen05 MMAs: tokens that are
+// consecutive by one TMA load of the tile's rows, others by helper warps'
+// asynchronous copies.  Rows that are not 16-byte aligned, which TMA cannot
+// address, go element by element through adapter_down_tile, adapter_up_tile and
+// adapter_grads.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -242,7 +248,7 @@ struct Rows {
 // ones), and takes 32 columns at a time: lane q of each row ends up with 8
 // consecutive outputs.  At these sizes latency is what counts: one launch, and
 // no trip of u through memory (two launches took 13 + 10 us for 64 requests of
-// 4096 x 4096 and rank 16).
+// 4096 x 4096 and rank 16, cold; this one 16, and one token 7.5).
 template <int NT, typename Y, bool TRANS, bool VEC, int UNROLL>
 __global__ void __launch_bounds__(256, NT <= 2 && !TRANS ? 3 : (NT <= 4 ? 2 : 1)) adapter_rows(const __grid_constant__ Rows pr) {
   constexpr int WK = 8, kRows = 16, kCols = NT * 8;
@@ -457,7 +463,9 @@ __global__ void __launch_bounds__(256, NT <= 2 && !TRANS ? 3 : (NT <= 4 ? 2 : 1)
 // For many tokens the rows are worked on in tiles of one adapter each.  Every
 // segment of kSegment tokens is sorted by adapter on its own (a stable
 // counting sort in one CTA), which keeps the cost linear in T; a segment's
-// tokens without an adapter come last, under adapter -1.
+// tokens without an adapter come last, under adapter -1.  A latency of 6 us at
+// 8192 tokens (a warp's eight rounds of match and count), 4 up to 2048 tokens,
+// which take two.
 constexpr int kSegment = 8192, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortRounds = kSegment / kSortThreads;
 constexpr int kTileRows = 128;  // of a tile
@@ -1377,8 +1385,8 @@ __device__ __forceinline__ void write_grad(const Grads& p, const GradJob& j, con
 // columns of x; the blocks are dealt out over the CTAs of the cluster (y).
 // Tokens are the contraction, so both operands reach the tcgen05 MMAs as they
 // are copied, with their rows along it (M = the 128 columns, N = the padded
-// rank, TERMS MMAs of 16 tokens); codes are decoded in between, each by the
-// thread that copied it.
+// TERMS ranks); codes are decoded in between, each by the thread that copied it.
+// For rows that are not 16-byte aligned; the others go to adapter_grads_tma.
 template <int RP, int TERMS, typename G>
 __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Grads p) {
   using Cfg = GradTile<RP, TERMS>;
@@ -1625,6 +1633,12 @@ struct DownTmaArgs {
   int wtma;
 };
 
+// M = the tile's 128 tokens, N = the padded rank; the contraction is split over
+// a cluster's CTAs while those of all tiles run at once (two to an SM), and the
+// sums meet through distributed shared memory in a fixed order.  8192 tokens of
+// 8192 columns, rank 64: 33 us, 134 MB of x at 4.1 TB/s (with half the CTAs 38,
+// with twice 43: the loads take some 22 us, the CTAs' start, their sums' way to
+// shared memory and across the cluster the rest).
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ DownTmaArgs ps) {
   using Cfg = DownTma<RP, TRANS>;
@@ -1793,7 +1807,7 @@ struct TileWalk {
 // One CTA to an SM, each with an equal stretch of all tiles' chunks, so that
 // loads and stores go on at a steady rate from the first tile to the last (as
 // CTAs of a tile and 16 chunks each, in two waves, 8192 tokens of 8192 columns
-// and rank 64 took 61 us).  Warp 0 feeds base and the weights, warp 1 issues the
+// and rank 64 took 61 us; this takes 54, 5.0 TB/s in and out).  Warp 0 feeds base and the weights, warp 1 issues the
 // MMAs, warps 2 and 3 are the helpers, which gather a tile's rows of base that
 // are not consecutive; warps 4..7 and 8..11 take turns at the chunks: each warp
 // adds the product of 32 rows to base in place in its stage, and from there
@@ -2155,8 +2169,11 @@ struct GradTmaArgs {
 // Warp 0 feeds x and the coefficients, warp 1 issues the MMAs; the helper warps
 // gather the blocks that are not 64 consecutive tokens (zeros past the
 // adapter's last) and, where x is a checkpoint, decode its codes between the
-// two.  The first
-// four of them also read the sums out of tensor memory at the end.
+// two.  The first four of them also read the sums out of tensor memory at the
+// end.  8192 tokens of 4 adapters, 8192 x 8192, rank 16, x in FP8, binary32
+// gradients: 62 us, 201 MB of x and dy at 3.2 TB/s.  A quarter of it is CTAs
+// starting and ending (512 of them on 456 places); within, each block waits in
+// turn for its copy, the decoding and its MMAs.
 template <int RP, int TERMS, typename G>
 __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
   using Cfg = GradTma<RP, TERMS>;

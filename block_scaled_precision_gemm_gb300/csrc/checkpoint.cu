@@ -337,7 +337,10 @@ struct GatedFwd {
 
 constexpr int kKeepNone = 0, kKeepMx = 1, kKeepF32 = 2;
 
-// The next row's elements are loaded before this row's are worked on.
+// The next row's elements are loaded before this row's are worked on.  8192 rows
+// of I = 8192 in bf16, SiLU, h in E4M3, INT8 kept: 82 us, 475 MB at 5.8 TB/s
+// (0.85 of a copy's rate), issue 59 % busy.  GELU takes erfc's instructions:
+// 7111 x 3968 75 us, 2.5 times its floor.
 template <typename In, int KEEP, int ACT, bool HQ>
 __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const GatedFwd p) {
   constexpr int kPer = kFwdPer;
@@ -419,6 +422,8 @@ struct GatedBwd {
   Strips strips;
 };
 
+// 8192 rows of I = 8192, INT8 kept, dh in bf16, h written too: 101 us, 675 MB at
+// 6.7 TB/s, a copy's rate.
 template <typename D, int CODE, bool POW2, int ACT>
 __global__ void __launch_bounds__(kThreads, sizeof(D) == 2 ? 4 : 3) gated_bwd(const GatedBwd p) {
   constexpr int kPer = kBwdPer, kBlock = POW2 ? 32 : 128;
@@ -528,7 +533,10 @@ void launch_bwd(const GatedBwd& p, int code, bool pow2, int act, dim3 grid, cuda
 // ---------------------------------------------------------------------------
 // 128 x 128 tiles of codes staged in shared memory; a thread owns two adjacent
 // columns of one block of 32 rows, takes their values, the two maxima and
-// scales, and stages the transposed codes for whole-line stores.
+// scales, and stages the transposed codes for whole-line stores.  16384 x 8192,
+// E4M3 kept: 80 us, 277 MB at 3.5 TB/s, bound by the wait for each tile's codes
+// (three CTAs to an SM, one tile each) and issue, 48 % busy; 5 % of the call,
+// whose two products take 1370 us.
 struct Requant {
   const uint8_t* x;
   const void* scales;

@@ -82,6 +82,9 @@ FORWARD = [  # T, K, N, R, L, ids, y
     (2500, 96, 80, 12, 3, "mixed", "f32"), (2200, 72, 328, 24, 4, "runs", "bf16"), (2048, 704, 96, 32, 2, "runs", "none"),
     (8200, 64, 72, 16, 6, "mixed", "bf16"), (2176, 64, 200, 128, 2, "runs", "f32"), (2100, 64, 64, 16, 3, "none", "bf16"),
     (2100, 36, 1000, 16, 1100, "mixed", "bf16"),
+    # sorted with a few tokens to a tile, and as they come with many adapters
+    (300, 128, 200, 64, 40, "mixed", "bf16"), (260, 201, 136, 128, 12, "mixed", "f32"), (96, 264, 136, 16, 64, "mixed", "f32"),
+    (700, 136, 72, 8, 300, "mixed", "f32"), (1500, 72, 99, 16, 200, "mixed", "bf16"),
 ]
 
 
@@ -168,6 +171,7 @@ BACKWARD = [  # T, K, N, R, L, ids, x, grad
     (40, 64, 64, 16, 3, "none", "bf16", "f32"), (2060, 264, 200, 33, 5, "mixed", "bf16", "f32"),
     (2304, 288, 320, 32, 2, "runs", "e5m2", "f32"), (8300, 96, 64, 16, 3, "mixed", "e4m3", "f32"),
     (640, 160, 44, 16, 2, "runs", "e4m3", "bf16"), (2200, 72, 64, 24, 300, "mixed", "bf16", "f32"),
+    (900, 64, 72, 8, 100, "mixed", "bf16", "f32"), (300, 96, 128, 32, 60, "mixed", "e4m3", "f32"),
 ]
 
 
