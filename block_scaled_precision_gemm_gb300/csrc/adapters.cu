@@ -2519,14 +2519,22 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
                                true, s);
   if (e != cudaSuccess) return e;
   const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
-  // Clusters split the blocks while all CTAs fit the SMs at once: each costs
-  // some 5 us of latency, which a second wave adds (8192 tokens of 4096 columns,
-  // rank 16, 4 adapters: 34.7 us against 45.0 with twice the CTAs; 2000 tokens
-  // 14.2 against 24.5; 8192 columns, unsplit 67.5 against 69.5).
+  // Clusters split an adapter's blocks.  Few blocks: while all CTAs fit the SMs
+  // at once, since each costs some 5 us of latency that a second wave adds (2000
+  // tokens of 4096 columns, rank 16, 4 adapters: 14.2 us, with four times the
+  // CTAs 24.5).  More: a little beyond (1 adapter of 8192 tokens and columns: 61
+  // us with 512 CTAs on 456 places, 72 with half, 70 with twice).  Many, of
+  // several adapters: one more wave, as requests are of all sizes and the
+  // longest adapter decides (8192 tokens and columns, 4 adapters in random
+  // shares: split 51..70 us, unsplit 70..82).
   constexpr int kResident = RP <= 16 ? 3 : (RP <= 64 ? 2 : 1);  // CTAs to an SM
   const int64_t places = kResident * ctx->num_sms;
   unsigned cs = 1;
-  while (cs < 8 && tiles * p.L * cs * 2 <= places && blocks >= 2 * static_cast<int64_t>(cs)) cs *= 2;
+  auto most = [&]() {
+    const int64_t each = blocks / cs;
+    return each > 16 && p.L > 1 ? 11 * places / 4 : (each > 8 ? 5 * places / 4 : places);
+  };
+  while (cs < 8 && blocks >= 2 * static_cast<int64_t>(cs) && tiles * p.L * cs * 2 <= most()) cs *= 2;
   const dim3 grid(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L));
   GradTmaArgs a{};
   bool tma = true;

@@ -172,6 +172,9 @@ BACKWARD = [  # T, K, N, R, L, ids, x, grad
     (2304, 288, 320, 32, 2, "runs", "e5m2", "f32"), (8300, 96, 64, 16, 3, "mixed", "e4m3", "f32"),
     (640, 160, 44, 16, 2, "runs", "e4m3", "bf16"), (2200, 72, 64, 24, 300, "mixed", "bf16", "f32"),
     (900, 64, 72, 8, 100, "mixed", "bf16", "f32"), (300, 96, 128, 32, 60, "mixed", "e4m3", "f32"),
+    # sums of several rounds
+    (16000, 64, 72, 16, 1, "runs", "bf16", "f32"), (27000, 32, 40, 64, 1, "runs", "e4m3", "f32"),
+    (16000, 64, 64, 24, 1, "mixed", "e4m3", "f32"), (27000, 32, 40, 128, 1, "mixed", "bf16", "f32"),
 ]
 
 
