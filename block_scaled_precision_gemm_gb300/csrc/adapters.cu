@@ -1266,44 +1266,66 @@ struct GradTile {
   // takes them all, and reads x once (one each, and x was read from shared
   // memory three times: 8192 tokens, 8192 columns, rank 16, 73 us).  Blocks take
   // turns at the sets of accumulators.  Where a set is too wide for two of them
-  // the terms go one by one, the lower ones to the last accumulator.
-  static constexpr bool kWide = TERMS * RP <= 128;
-  static constexpr int kTmem = Sums<RP>::kTmem;
-  static constexpr int kSetCols = kWide ? TERMS * RP : RP, kSets = kWide ? kTmem / kSetCols : Sums<RP>::kSums - 1;
-  static __device__ __forceinline__ void block(uint32_t tmem, int b, uint32_t x, uint32_t coef) {
-    const uint32_t d = tmem + (b % kSets) * kSetCols;
+  // the terms go one by one, the lower ones to an accumulator of their own.
+  // Binary32 gradients of many blocks add each round's sets to RP more columns,
+  // in registers on the way, so that no accumulator takes more than 48 additions
+  // (128 of them left dB 1.5e-6 of its norm off; 48, 6.5e-7 at most).
+  static constexpr bool kWide = TERMS * RP <= 128, kRounds = TERMS == 3;
+  static constexpr int kTmem = RP <= 16 && !kRounds ? 128 : (RP == 128 && kRounds ? 512 : 256);
+  static constexpr int kSetCols = kWide ? TERMS * RP : RP;
+  static constexpr int kSets = (kTmem - (kRounds ? RP : 0) - (kWide ? 0 : RP)) / kSetCols;
+  static constexpr int kLower = kSets * kSetCols, kTotal = kTmem - RP;  // columns: the lower terms', the rounds'
+  static constexpr int kRound = 12 * kSets;                             // blocks
+  // Block b, the n-th of its round.
+  static __device__ __forceinline__ void block(uint32_t tmem, int b, int n, uint32_t x, uint32_t coef) {
+    const uint32_t d = tmem + (n % kSets) * kSetCols;
     if constexpr (kWide) {
 #pragma unroll
       for (int s = 0; s < kGradRows / 16; ++s)
         mma_f16(d, X::along_rows(x, s), Coef::along_rows(coef, s), mma_shape(TERMS * RP, true, true),
-                (b >= kSets || s > 0) ? 1u : 0u);
+                (n >= kSets || s > 0) ? 1u : 0u);
     } else {
 #pragma unroll
       for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
         for (int s = 0; s < kGradRows / 16; ++s)
-          mma_f16(k == 0 ? d : tmem + kSets * RP, X::along_rows(x, s), Coef::along_rows(coef + k * Image::kTermBytes, s),
+          mma_f16(k == 0 ? d : tmem + kLower, X::along_rows(x, s), Coef::along_rows(coef + k * Image::kTermBytes, s),
                   mma_shape(RP, true, true),
-                  (s > 0 || (k == 0 ? b >= kSets : b > 0 || k < TERMS - 1)) ? 1u : 0u);
+                  (s > 0 || (k == 0 ? n >= kSets : b > 0 || k < TERMS - 1)) ? 1u : 0u);
     }
   }
-  // 16 columns of n blocks' sums, to dst.
-  static __device__ __forceinline__ void read_sums16(uint32_t tmem, int n, float* dst) {
+  // 16 columns of a round's n blocks.
+  static __device__ __forceinline__ void add_round16(uint32_t tmem, int n, float (&v)[16]) {
+#pragma unroll
+    for (int k = kWide ? TERMS - 1 : 0; k >= 0; --k)
+#pragma unroll
+      for (int s = 0; s < kSets; ++s)
+        if (s < n) add_sums16(tmem + s * kSetCols + k * RP, v);
+  }
+  // After a round: its sums to those of the rounds before (`more`: there are some).
+  static __device__ __forceinline__ void end_round(uint32_t tmem, bool more) {
+#pragma unroll
+    for (int c = 0; c < RP; c += 16) {
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      add_round16(tmem + c, kSets, v);
+      if (more) add_sums16(tmem + kTotal + c, v);
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e]);
+      tmem_st16(tmem + kTotal + c, w);
+    }
+    tmem_wait_st();
+  }
+  // 16 columns of all of b blocks, `rounds` rounds of which have ended, to dst.
+  static __device__ __forceinline__ void read_sums16(uint32_t tmem, int b, int rounds, float* dst) {
     float v[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = 0.f;
-    if constexpr (kWide) {
-#pragma unroll
-      for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-        for (int s = 0; s < kSets; ++s)
-          if (s < n) add_sums16(tmem + s * kSetCols + k * RP, v);
-    } else {
-      if (n > 0) add_sums16(tmem + kSets * RP, v);
-#pragma unroll
-      for (int s = 0; s < kSets; ++s)
-        if (s < n) add_sums16(tmem + s * RP, v);
-    }
+    if (!kWide && b > 0) add_sums16(tmem + kLower, v);
+    add_round16(tmem, b - rounds * kRound, v);
+    if (rounds > 0) add_sums16(tmem + kTotal, v);
 #pragma unroll
     for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
   }
@@ -1518,7 +1540,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
     if (tid == 0) {
       const uint32_t xt = ring_at + (kept ? b & 1 : b % S) * Cfg::kXBytes;
       const uint32_t ct = coef_at + (b % S) * Cfg::kCoefBytes;
-      Cfg::block(tmem, b, xt, ct);
+      Cfg::block(tmem, b, b, xt, ct);
       tc_commit(&ctl.done[b & 1]);
     }
     if (b > 0)
@@ -1545,7 +1567,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int k = 0; k < kHalf; k += 16) Cfg::read_sums16(src + k, b, dst + k);
+      for (int k = 0; k < kHalf; k += 16) Cfg::read_sums16(src + k, b, 0, dst + k);
     }
   }
   tc_fence_before();
@@ -2146,9 +2168,11 @@ __global__ void __launch_bounds__(384, 1) adapter_up_tma(const __grid_constant__
 template <int RP, int TERMS>
 struct GradTma : GradTile<RP, TERMS> {
   using Base = GradTile<RP, TERMS>;
-  // RP = 16: three CTAs fit an SM, whose starts and ends overlap
-  static constexpr int kStages = RP <= 16 ? 3 : Base::kStages;
-  static constexpr int kDecoded = RP <= 16 ? 1 : 2;  // decoded blocks of a checkpoint
+  // bf16 gradients of up to 16 ranks: three CTAs fit an SM; binary32 ones need
+  // the tensor memory of two for their sets of accumulators
+  static constexpr int kResident = RP <= 16 && TERMS == 2 ? 3 : (RP <= 64 ? 2 : 1);
+  static constexpr int kStages = kResident == 3 ? 3 : Base::kStages;
+  static constexpr int kDecoded = kResident == 3 ? 1 : 2;  // decoded blocks of a checkpoint
   static constexpr int kStageBf16 = Base::kXBytes + Base::kCoefBytes;
   static constexpr int kCodeBytes = kGradRows * kGradCols, kScaleBytes = 1024;  // (a row's four scale bytes: 256, padded)
   static constexpr int kStageCodes = kCodeBytes + kScaleBytes + Base::kCoefBytes;
@@ -2157,7 +2181,7 @@ struct GradTma : GradTile<RP, TERMS> {
   static constexpr int kRing = kBf16 > kCodes ? kBf16 : kCodes;
   static_assert(kGradCols * Base::kPitch * 4 <= kRing, "the sums reuse the ring");
   struct Ctl {
-    uint64_t full[kStages], empty[kStages], decoded[kDecoded], done;
+    uint64_t full[kStages], empty[kStages], decoded[kDecoded], done, ended;
     uint32_t tmem;
     int abort_flag;
   };
@@ -2173,12 +2197,12 @@ struct GradTmaArgs {
 // gather the blocks that are not 64 consecutive tokens (zeros past the
 // adapter's last) and, where x is a checkpoint, decode its codes between the
 // two.  The first four of them also read the sums out of tensor memory at the
-// end.  8192 tokens of 4 adapters, 8192 x 8192, rank 16, x in FP8, binary32
-// gradients: 62 us, 201 MB of x and dy at 3.2 TB/s.  A quarter of it is CTAs
-// starting and ending (512 of them on 456 places); within, each block waits in
-// turn for its copy, the decoding and its MMAs.
+// end.  8192 tokens of 4 adapters in random shares, 8192 x 8192, rank 16, x in
+// FP8, binary32 gradients: 66..86 us, 201 MB of x and dy at 2.3..3.0 TB/s: each
+// block waits in turn for its copy, the decoding and its MMAs, and CTAs start and
+// end (1024 of them on 304 places).
 template <int RP, int TERMS, typename G>
-__global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
+__global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kResident) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
   using Cfg = GradTma<RP, TERMS>;
   using Coef = typename Cfg::Coef;
   constexpr int S = Cfg::kStages, ND = Cfg::kDecoded;
@@ -2202,6 +2226,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
     }
     for (int i = 0; i < ND; ++i) mbar_init(&ctl.decoded[i], kGradHelpers);
     mbar_init(&ctl.done, 1);
+    mbar_init(&ctl.ended, 128);
     ctl.abort_flag = 0;
     fence_barrier_init();
   }
@@ -2242,14 +2267,19 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
     if (lane == 0) {
       BlockWalk walk(p.o, p.L, a, rank, cs);
       while (walk.next()) {
-        const int st = b % S;
+        const int st = b % S, n = Cfg::kRounds ? b % Cfg::kRound : b;
+        if (Cfg::kRounds && b > 0 && n == 0) {  // a round has ended
+          tc_commit(&ctl.done);
+          if (!wait(&ctl.ended, b / Cfg::kRound - 1)) break;
+          tc_fence_after();
+        }
         if (!wait(&ctl.full[st], b / S)) break;
         if (kept && !wait(&ctl.decoded[b % ND], b / ND)) break;
         fence_proxy_async_smem();  // what the helpers' copies wrote
         tc_fence_after();
         const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
         const uint32_t xt = kept ? smem_u32(ring) + (b % ND) * Cfg::kXBytes : at;
-        Cfg::block(tmem, b, xt, ct);
+        Cfg::block(tmem, b, n, xt, ct);
         tc_commit(&ctl.empty[st]);
         ++b;
       }
@@ -2306,18 +2336,32 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
     };
     int d = 0;  // blocks copied
     bool more = true, ok = true;
+    auto all = [](bool v) { return __all_sync(0xFFFFFFFFu, v) != 0; };  // a warp gives up together
+    // before a round's first block, in the warps that read the sums: the round before
+    auto end_round = [&](int block) {
+      if (!Cfg::kRounds || warp >= 6 || block == 0 || block % Cfg::kRound) return;
+      const int r = block / Cfg::kRound - 1;
+      if (!(ok = all(wait(&ctl.done, r)))) return;
+      tc_fence_after();
+      Cfg::end_round(tmem + ((warp & 3) * 32u << 16), r > 0);
+      tc_fence_before();
+      mbar_arrive(&ctl.ended);
+    };
     auto step = [&]() {
       if (!more || !(more = walk.next())) return;
-      ok = d < S || wait(&ctl.empty[d % S], d / S - 1);
+      if (!kept) end_round(d);
+      ok = ok && all(d < S || wait(&ctl.empty[d % S], d / S - 1));
       if (ok) copy(d++);
     };
     if (!kept) {
       while (more && ok) step();
+      b = d;
     } else {
       while (ok && more && d < D) step();
       for (; b < d && ok; ++b) {
         const int st = b % S;
-        ok = wait(&ctl.full[st], b / S) && (b < ND || wait(&ctl.empty[(b - ND) % S], (b - ND) / S));
+        end_round(b);
+        ok = ok && all(wait(&ctl.full[st], b / S) && (b < ND || wait(&ctl.empty[(b - ND) % S], (b - ND) / S)));
         if (!ok) break;  // (the second: the MMAs have read the decoded block that this one replaces)
         const uint32_t src = ring_at + st * stage_bytes, dst = smem_u32(ring) + (b % ND) * Cfg::kXBytes;
         uint32_t sw;
@@ -2342,20 +2386,21 @@ __global__ void __launch_bounds__(64 + kGradHelpers) adapter_grads_tma(const __g
     copy_wait<0>();
   }
   __syncthreads();
-  wait(&ctl.done, 0);
+  const int rounds = Cfg::kRounds && b > 0 ? (b - 1) / Cfg::kRound : 0;  // ended before the last one
+  wait(&ctl.done, rounds);
   if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies in flight, bounded again
     int never = 0;
     for (int i = b > S ? b - S : 0; i < b; ++i)
       mbar_wait(&ctl.full[i % S], static_cast<uint32_t>(i / S) & 1u, p.w.timeout_ns, &never, p.w.status, kSiteGrads);
   }
-  const int blocks = __syncthreads_count(warp == 1 && lane < b);  // accumulators in use, if there are fewer than kSums
+  __syncthreads();
   tc_fence_after();
   float* sums = reinterpret_cast<float*>(ring);  // [kGradCols][kPitch]: column, rank
   if (warp >= 2 && warp < 6) {
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int k = 0; k < RP; k += 16) Cfg::read_sums16(tmem + (q * 32u << 16) + k, blocks, dst + k);
+    for (int k = 0; k < RP; k += 16) Cfg::read_sums16(tmem + (q * 32u << 16) + k, b, rounds, dst + k);
   }
   tc_fence_before();
   __syncthreads();
@@ -2524,11 +2569,11 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
   // tokens of 4096 columns, rank 16, 4 adapters: 14.2 us, with four times the
   // CTAs 24.5).  More: a little beyond (1 adapter of 8192 tokens and columns: 61
   // us with 512 CTAs on 456 places, 72 with half, 70 with twice).  Many, of
-  // several adapters: one more wave, as requests are of all sizes and the
-  // longest adapter decides (8192 tokens and columns, 4 adapters in random
-  // shares: split 51..70 us, unsplit 70..82).
-  constexpr int kResident = RP <= 16 ? 3 : (RP <= 64 ? 2 : 1);  // CTAs to an SM
-  const int64_t places = kResident * ctx->num_sms;
+  // several adapters: up to 2.75 CTAs a place, as requests are of all sizes and
+  // the longest adapter decides (8192 tokens and columns, 4 adapters in random
+  // shares: split in two 51..70 us, whole 70..82, in four 63..78; measured with
+  // three CTAs to an SM).
+  const int64_t places = GradTma<RP, TERMS>::kResident * ctx->num_sms;
   unsigned cs = 1;
   auto most = [&]() {
     const int64_t each = blocks / cs;
