@@ -1269,7 +1269,7 @@ struct GradTile {
   // the terms go one by one, the lower ones to an accumulator of their own.
   // Binary32 gradients of many blocks add each round's sets to RP more columns,
   // in registers on the way, so that no accumulator takes more than 48 additions
-  // (128 of them left dB 1.5e-6 of its norm off; 48, 6.5e-7 at most).
+  // (64 of them left dB 1.0e-6 of its norm off; 48, 6.5e-7 at most).
   static constexpr bool kWide = TERMS * RP <= 128, kRounds = TERMS == 3;
   static constexpr int kTmem = RP <= 16 && !kRounds ? 128 : (RP == 128 && kRounds ? 512 : 256);
   static constexpr int kSetCols = kWide ? TERMS * RP : RP;
