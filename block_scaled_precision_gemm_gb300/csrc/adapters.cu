@@ -127,7 +127,10 @@ __device__ __forceinline__ void load_row(const bf16* row, int64_t c, int64_t lim
 
 // v as a sum of TERMS bf16 numbers (each the rounding of what is left): two
 // keep 16 bits of the significand, three all 24.  pair(v0, v1)[k] packs term
-// k of both.
+// k of both.  u and d take three into the second product, which is thus one of
+// binary32 numbers whatever the outputs' type: with 16 bits of u every
+// thousandth bf16 output was its neighbour, and where base and product cancel
+// the error was as large as the result.
 template <int TERMS>
 __device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&w)[TERMS]) {
 #pragma unroll
@@ -232,6 +235,8 @@ __device__ __forceinline__ int down_col(int j, int n, int nt) {
   return (j / 2) * 16 + (n / 2) * 4 + 2 * (j % 2) + (n % 2);
 }
 
+constexpr int kTerms = 3;  // of u and d in the second product
+
 struct Rows {
   Down d;
   Up u;               // its u is d's
@@ -243,16 +248,15 @@ struct Rows {
 // a fixed order, over the warps in shared memory, over the cluster through
 // distributed shared memory (each CTA sums them all, and stores a share).  Then
 // the outputs' columns are split over the CTAs and warps: a warp holds the
-// rows' u as A fragments, split into TERMS bf16 terms so that u keeps its
-// binary32 precision (three terms for binary32 outputs, 16 bits of it for bf16
-// ones), and takes 32 columns at a time: lane q of each row ends up with 8
+// rows' u as A fragments, split into three bf16 terms so that u keeps its
+// binary32 precision, and takes 32 columns at a time: lane q of each row ends up with 8
 // consecutive outputs.  At these sizes latency is what counts: one launch, and
 // no trip of u through memory (two launches took 13 + 10 us for 64 requests of
 // 4096 x 4096 and rank 16, cold; this one 16, and one token 7.5).
 template <int NT, typename Y, bool TRANS, bool VEC, int UNROLL>
 __global__ void __launch_bounds__(256, NT <= 2 && !TRANS ? 3 : (NT <= 4 ? 2 : 1)) adapter_rows(const __grid_constant__ Rows pr) {
   constexpr int WK = 8, kRows = 16, kCols = NT * 8;
-  constexpr int KT = (NT + 1) / 2, TERMS = sizeof(Y) == 4 ? 3 : 2;
+  constexpr int KT = (NT + 1) / 2, TERMS = kTerms;
   extern __shared__ __align__(16) float part[];  // [WK][kRows][kCols] partial sums, then u: [kRows][KT * 16]
   float* whole = part + WK * kRows * kCols;
   const Down& p = pr.d;
@@ -949,9 +953,8 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
 // out = base + s W u for a tile of 128 tokens of one adapter
 // ---------------------------------------------------------------------------
 // For outputs whose rows are not 16-byte aligned.  The tile's u is split once
-// into TERMS bf16 terms in shared memory (three for binary32 outputs, which keep
-// its 24 bits; two, 16 bits, for bf16 ones).  Chunks of 64 columns then stream
-// through: one thread issues the tcgen05 MMAs of chunk c + 1 into one of two
+// into three bf16 terms in shared memory, which keep its 24 bits.  Chunks of 64
+// columns then stream through: one thread issues the tcgen05 MMAs of chunk c + 1 into one of two
 // accumulators in tensor memory, while each warp loads its 32 rows x 32 columns
 // of base, lanes along the rows, takes chunk c's product through shared memory
 // to the same lanes, and stores the sum from there.  (With a lane's eight
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
 // 2.4 TB/s.)
 template <int RP, typename Y, bool TRANS>
 struct UpTile {
-  static constexpr int TERMS = sizeof(Y) == 4 ? 3 : 2;
+  static constexpr int TERMS = kTerms;
   static constexpr int kWStages = 3;
   using U = Staged<kTileRows, RP>;  // one term
   using W = Staged<TRANS ? RP : kChunk, TRANS ? kChunk : RP>;
@@ -1792,7 +1795,7 @@ template <int RP, typename Y, bool TRANS>
 struct UpTma : UpTile<RP, Y, TRANS> {
   using Base = UpTile<RP, Y, TRANS>;
   // one CTA to an SM: what the weights leave holds base, up to 8 chunks
-  static constexpr int kWStages = RP == 128 && sizeof(Y) == 4 ? 2 : 4;
+  static constexpr int kWStages = RP == 128 ? (sizeof(Y) == 4 ? 2 : 3) : 4;
   static constexpr int kRoom = (226 * 1024 - Base::kUBytes - kWStages * Base::kWBytes) / Base::kYBytes;
   static constexpr int kYStages = kRoom < 8 ? kRoom : 8;
   static constexpr int kProducts = 4;  // accumulators
