@@ -125,21 +125,41 @@ __device__ __forceinline__ void load_row(const bf16* row, int64_t c, int64_t lim
   }
 }
 
-// v as a sum of TERMS bf16 numbers (each the rounding of what is left): two
-// keep 16 bits of the significand, three all 24.  pair(v0, v1)[k] packs term
-// k of both.  u and d take three into the second product, which is thus one of
+// v as a sum of TERMS bf16 numbers: two keep 16 bits of the significand, three
+// all 24.  u and d take three into the second product, which is thus one of
 // binary32 numbers whatever the outputs' type: with 16 bits of u every
 // thousandth bf16 output was its neighbour, and where base and product cancel
 // the error was as large as the result.
+//
+// What the terms multiply may be infinite, and v too, so every term has v's
+// sign and none is zero: each but the last is what is left cut off (not rounded,
+// which could give the next one the other sign, or pass bf16's largest number),
+// and in a zero's place goes 2^-126, which is below 2^-24 of any v that gets it.
+// Infinity times v is then one infinity, not their difference, nor infinity
+// times zero.  (A v below 2^-100 in magnitude keeps its zeros.)
+template <int TERMS>
+__device__ __forceinline__ void split_one(float v, float (&t)[TERMS]) {
+  const uint32_t b = __float_as_uint(v), magnitude = b & 0x7FFFFFFFu;
+  const float least = magnitude >= (27u << 23) ? __uint_as_float((b & 0x80000000u) | (1u << 23)) : 0.f;
+  t[0] = __uint_as_float(magnitude > 0x7F800000u ? 0x7FFF0000u : b & 0xFFFF0000u);
+  float left = magnitude < 0x7F800000u ? v - t[0] : 0.f;
+#pragma unroll
+  for (int k = 1; k < TERMS; ++k) {
+    const float cut = k + 1 < TERMS ? __uint_as_float(__float_as_uint(left) & 0xFFFF0000u) : left;
+    t[k] = cut == 0.f ? least : cut;
+    left -= cut;
+  }
+}
+// Term k of both in w[k] (the last ones rounded).
 template <int TERMS>
 __device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&w)[TERMS]) {
+  float t0[TERMS], t1[TERMS];
+  split_one<TERMS>(v0, t0);
+  split_one<TERMS>(v1, t1);
 #pragma unroll
-  for (int k = 0; k < TERMS; ++k) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-    w[k] = *reinterpret_cast<const uint32_t*>(&h);
-    v0 -= __uint_as_float(w[k] << 16);
-    v1 -= __uint_as_float(w[k] & 0xFFFF0000u);
-  }
+  for (int k = 0; k + 1 < TERMS; ++k) w[k] = __byte_perm(__float_as_uint(t0[k]), __float_as_uint(t1[k]), 0x7632);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(t0[TERMS - 1], t1[TERMS - 1]);
+  w[TERMS - 1] = *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // The adapter of row t, or -1 for none (also for an id outside [0, L)).

@@ -538,7 +538,10 @@ bsmm_status bsmm_linear_backward_checkpoint(const void* dY, const void* W, const
  *            number may be in use.
  *   ids [T] int32; an id outside [0, L) means no adapter: u[t] = 0, out[t] =
  *            y[t].  Rows never mix: an infinity or NaN in a token or in an
- *            adapter reaches only the tokens that use it.
+ *            adapter reaches only the tokens that use it.  Infinities give
+ *            what the formulas give, here and in the backward: NaN only where
+ *            two of them cancel or one meets a zero (or a u or d below 2^-100
+ *            in magnitude, which may count as one).
  *   x [T, K] bfloat16 at a row pitch of ld_x, A [L, R, K] and B [L, N, R]
  *            bfloat16, contiguous.  1 <= R <= 128; any K, N >= 1.
  *   scaling  binary32 [L], or NULL for 1.
