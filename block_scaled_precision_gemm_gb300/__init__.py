@@ -197,6 +197,29 @@ def _on_device(**named) -> torch.device:
     return dev
 
 
+def _empty(shape, dtype, dev, stream):
+    """An output of a call on `stream`.  It comes from that stream's own pool:
+    memory of the current stream's may still be in use there by earlier work,
+    which nothing makes `stream` wait for.  The caller goes on with it on the
+    current stream, so the allocator is told of that one too."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(dev.index):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if t.numel():
+        t.record_stream(here)
+    return t
+
+
+def _scratch(nbytes, dev, stream):
+    """A workspace, from the pool of the one stream that uses it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -266,7 +289,7 @@ class trace:
         return False
 
 
-def _quantize_job(x, block, code, scale, transpose, codes, scales):
+def _quantize_job(x, block, code, scale, transpose, codes, scales, stream):
     """Checked arguments of one quantization, its outputs (allocated where
     not given) and the C job that describes it."""
     _want(x, "x", dtypes=_FLOATS)
@@ -285,9 +308,9 @@ def _quantize_job(x, block, code, scale, transpose, codes, scales):
         _want(scales, "scales", (srows, scols), itemsize=scale_dtype.itemsize)
     dev = _on_device(x=x, codes=codes, scales=scales)
     if codes is None:
-        codes = torch.empty((orows, width), dtype=torch.int8 if c == INT8 else torch.uint8, device=dev)
+        codes = _empty((orows, width), torch.int8 if c == INT8 else torch.uint8, dev, stream)
     if scales is None:
-        scales = torch.empty((srows, scols), dtype=scale_dtype, device=dev)
+        scales = _empty((srows, scols), scale_dtype, dev, stream)
     job = _QuantizeJob(_ptr(x), BF16 if x.dtype == torch.bfloat16 else F32, rows, cols, cols, br, bc, c, s,
                        1 if transpose else 0, _ptr(codes), ocols, _ptr(scales), scols)
     return job, codes, scales
@@ -300,7 +323,7 @@ def quantize(x: torch.Tensor, block, code="e4m3", scale="f32", transpose=False, 
     Returns ``(codes, scales)``: codes uint8 (int8 for INT8; E2M1 packed two
     per byte) of shape [rows, cols] (or [cols, rows] transposed), scales
     float32 or uint8 of shape [rows/br, cols/bc] (or transposed)."""
-    j, codes, scales = _quantize_job(x, block, code, scale, transpose, codes, scales)
+    j, codes, scales = _quantize_job(x, block, code, scale, transpose, codes, scales, stream)
     _check(lib().bsmm_quantize(j.x, j.x_type, j.rows, j.cols, j.ld_x, j.block_rows, j.block_cols, j.code_type,
                                j.scale_type, j.transpose_out, j.codes, j.ld_codes, j.scales, j.ld_scales,
                                _stream(stream)), "bsmm_quantize")
@@ -315,7 +338,7 @@ def quantize_batch(jobs, stream=None):
     ``codes``, ``scales`` optional).  Returns the ``(codes, scales)`` pairs in
     job order."""
     prepared = [_quantize_job(j["x"], j["block"], j.get("code", "e4m3"), j.get("scale", "f32"),
-                              j.get("transpose", False), j.get("codes"), j.get("scales")) for j in jobs]
+                              j.get("transpose", False), j.get("codes"), j.get("scales"), stream) for j in jobs]
     arr = (_QuantizeJob * max(len(prepared), 1))(*[p[0] for p in prepared])
     _check(lib().bsmm_quantize_batch(arr, len(prepared), _stream(stream)), "bsmm_quantize_batch")
     return [(p[1], p[2]) for p in prepared]
@@ -344,9 +367,9 @@ def gemm(a, b, a_scales, b_scales, a_type="e4m3", b_type="e4m3", scale="ue8m0", 
         _want(workspace, "workspace")
     dev = _on_device(a=a, b=b, a_scales=a_scales, b_scales=b_scales, y=y, workspace=workspace)
     if y is None:
-        y = torch.empty((Bn, M, N), dtype=out_dtype, device=dev)
+        y = _empty((Bn, M, N), out_dtype, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(gemm_workspace_size(Bn, M, N, K, at), 1), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(gemm_workspace_size(Bn, M, N, K, at), 1), dev, stream)
     _check(lib().bsmm_gemm(Bn, M, N, K, _ptr(a), at, _ptr(b), bt, _ptr(a_scales), a_scales.shape[-1],
                            _ptr(b_scales), b_scales.shape[-1], _scale(scale), _ptr(y),
                            BF16 if y.dtype == torch.bfloat16 else F32, _ptr(workspace), _nbytes(workspace),
@@ -427,7 +450,7 @@ def gemm_grouped(a, b, a_scales, b_scales, group_n=128, group_k=128, a_type="e4m
         _want(y, "y", (M, N), dtypes=(torch.float32,))
     dev = _on_device(a=a, b=b, a_scales=a_scales, b_scales=b_scales, y=y)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=dev)
+        y = _empty((M, N), torch.float32, dev, stream)
     _check(lib().bsmm_gemm_grouped(M, N, K, _ptr(a), _code(a_type), _ptr(b), _code(b_type), _ptr(a_scales),
                                    _ptr(b_scales), group_n, group_k, _ptr(y), _stream(stream)),
            "bsmm_gemm_grouped")
@@ -461,10 +484,9 @@ def int8_channel(x, w, return_acc=False, out=None, workspace=None, stream=None) 
     dev = _on_device(x=x, w=w, workspace=workspace, **{f"out_{k}": t for k, t in o.items()})
     for k in ("x_q", "x_scales", "w_q", "w_scales", "y") + (("acc",) if return_acc else ()):
         if k not in o:
-            o[k] = torch.empty(want[k][0], dtype=want[k][1][0], device=dev)
+            o[k] = _empty(want[k][0], want[k][1][0], dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(int8_channel_workspace_size(Bn, D_in, D_out), 1), dtype=torch.uint8,
-                                device=dev)
+        workspace = _scratch(max(int8_channel_workspace_size(Bn, D_in, D_out), 1), dev, stream)
     _check(lib().bsmm_int8_channel(_ptr(x), _ptr(w), Bn, D_in, D_out, _ptr(o["x_q"]), _ptr(o["x_scales"]),
                                    _ptr(o["w_q"]), _ptr(o["w_scales"]), _ptr(o["y"]), _ptr(o.get("acc")),
                                    _ptr(workspace), _nbytes(workspace), _stream(stream)), "bsmm_int8_channel")
@@ -497,11 +519,11 @@ def linear_backward(dY, W, X, fp8="e5m2", dX=None, dW=None, workspace=None, stre
         _want(workspace, "workspace")
     dev = _on_device(dY=dY, W=W, X=X, dX=dX, dW=dW, workspace=workspace)
     if dX is None:
-        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dX = _empty((M, K), torch.bfloat16, dev, stream)
     if dW is None:
-        dW = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        dW = _empty((N, K), torch.bfloat16, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(linear_backward_workspace_size(M, N, K), 1), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(linear_backward_workspace_size(M, N, K), 1), dev, stream)
     _check(lib().bsmm_linear_backward(_ptr(dY), _ptr(W), _ptr(X), M, N, K, _code(fp8), _ptr(dX), _ptr(dW),
                                       _ptr(workspace), _nbytes(workspace), _stream(stream)), "bsmm_linear_backward")
     return dX, dW
@@ -541,9 +563,9 @@ def quantize_atoms(x, code="e4m3", scale="ue8m0", batches=1, transpose=False, co
         _want(atoms, "atoms")
     dev = _on_device(x=x, codes=codes, atoms=atoms)
     if codes is None:
-        codes = torch.empty((batches * rows, _code_bytes(c, K)), dtype=torch.uint8, device=dev)
+        codes = _empty((batches * rows, _code_bytes(c, K)), torch.uint8, dev, stream)
     if atoms is None:
-        atoms = torch.empty(max(scale_atoms_size(batches, rows, K, c, s), 1), dtype=torch.uint8, device=dev)
+        atoms = _empty(max(scale_atoms_size(batches, rows, K, c, s), 1), torch.uint8, dev, stream)
     _check(lib().bsmm_quantize_atoms(_ptr(x), BF16 if x.dtype == torch.bfloat16 else F32, batches, rows, K,
                                      1 if transpose else 0, c, s, _ptr(codes), _ptr(atoms), _nbytes(atoms),
                                      _stream(stream)), "bsmm_quantize_atoms")
@@ -563,9 +585,9 @@ def gemm_atoms(a, b, a_atoms, b_atoms, a_type="e4m3", b_type="e4m3", scale="ue8m
         _want(workspace, "workspace")
     dev = _on_device(a=a, b=b, a_atoms=a_atoms, b_atoms=b_atoms, y=y, workspace=workspace)
     if y is None:
-        y = torch.empty((Bn, M, N), dtype=out_dtype, device=dev)
+        y = _empty((Bn, M, N), out_dtype, dev, stream)
     if workspace is None and at == E2M1:
-        workspace = torch.empty(max(gemm_workspace_size(Bn, M, N, K, at), 1), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(gemm_workspace_size(Bn, M, N, K, at), 1), dev, stream)
     _check(lib().bsmm_gemm_atoms(Bn, M, N, K, _ptr(a), at, _ptr(b), bt, _ptr(a_atoms), _ptr(b_atoms),
                                  sc, _ptr(y), BF16 if y.dtype == torch.bfloat16 else F32,
                                  _ptr(workspace), _nbytes(workspace), _stream(stream)),
@@ -606,12 +628,12 @@ def linear_backward_quantized(dy_n, dy_n_scales, w_t, w_t_scales, dy_t, dy_t_sca
     dev = _on_device(dy_n=dy_n, dy_n_scales=dy_n_scales, w_t=w_t, w_t_scales=w_t_scales, dy_t=dy_t,
                      dy_t_scales=dy_t_scales, x_t=x_t, x_t_scales=x_t_scales, dX=dX, dW=dW, workspace=workspace)
     if dX is None:
-        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dX = _empty((M, K), torch.bfloat16, dev, stream)
     if dW is None:
-        dW = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        dW = _empty((N, K), torch.bfloat16, dev, stream)
     need = lib().bsmm_linear_backward_quantized_workspace_size(M, N, K, 1 if scales_are_atoms else 0)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _scratch(need, dev, stream)
     _check(lib().bsmm_linear_backward_quantized(M, N, K, c, _ptr(dy_n), _ptr(dy_n_scales), _ptr(w_t),
                                                 _ptr(w_t_scales), _ptr(dy_t), _ptr(dy_t_scales), _ptr(x_t),
                                                 _ptr(x_t_scales), 1 if scales_are_atoms else 0, _ptr(dX), _ptr(dW),
@@ -642,15 +664,6 @@ def _fits(t, dtype, shape, dev) -> bool:
 
 def _current(t) -> bool:
     return isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == torch._C._cuda_getDevice()
-
-
-def _empty(shape, dtype, dev, stream):
-    """An output or scratch tensor for a call on `stream`: where that is not
-    the current stream, the allocator is told that the memory is in use there."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None and t.numel():
-        t.record_stream(stream)
-    return t
 
 
 def _at(t):
@@ -793,7 +806,7 @@ def linear_backward_checkpoint(dY, W, x_codes, x_scales, x_code="e4m3", x_scale=
     if dW is None:
         dW = _empty((N, K), torch.bfloat16, dev, stream)
     if workspace is None:
-        workspace = _empty(max(linear_backward_workspace_size(M, N, K), 1), torch.uint8, dev, stream)
+        workspace = _scratch(max(linear_backward_workspace_size(M, N, K), 1), dev, stream)
     _check(lib().bsmm_linear_backward_checkpoint(dY.data_ptr(), W.data_ptr(), x_codes.data_ptr(), c, x_scales.data_ptr(),
                                                  s, M, N, K, _code(fp8), dX.data_ptr(), dW.data_ptr(),
                                                  workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev)),
@@ -884,7 +897,7 @@ def adapters(x, a, b, ids, y=None, scaling=None, out=None, u=None, out_dtype=tor
     if workspace is None:
         need = adapters_workspace_size(T, R, L)
         if need:
-            workspace = _empty((need,), torch.uint8, dev, stream)
+            workspace = _scratch(need, dev, stream)
     _check(lib().bsmm_adapters(T, K, N, R, L, x.data_ptr(), ld_x, a.data_ptr(), b.data_ptr(), ids.data_ptr(),
                                _at(scaling), _at(y), ld_y, out.data_ptr(), ld_out, BF16 if dtype is bf16 else F32,
                                u.data_ptr(), _at(workspace), _nbytes(workspace), _raw_stream(stream, dev)),
@@ -958,7 +971,7 @@ def adapters_backward(dy, x, a, b, ids, u, scaling=None, dx_base=None, x_scales=
     if db is None:
         db = _empty((L, N, R), grad_dtype, dev, stream)
     if workspace is None:
-        workspace = _empty(max(adapters_backward_workspace_size(T, R, L), 1), torch.uint8, dev, stream)
+        workspace = _scratch(max(adapters_backward_workspace_size(T, R, L), 1), dev, stream)
     _check(lib().bsmm_adapters_backward(T, K, N, R, L, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, xt, _at(x_scales),
                                         a.data_ptr(), b.data_ptr(), ids.data_ptr(), _at(scaling), u.data_ptr(),
                                         _at(dx_base), K, dx.data_ptr(), da.data_ptr(), db.data_ptr(),
