@@ -1055,6 +1055,7 @@ __global__ void __launch_bounds__(256, 2) adapter_up_tile(const __grid_constant_
         if (t >= 0 && col < c1) out[t * p.ld_out + col] = y[r];
       }
     }
+    grid_dependency_wait();  // a launch is over when its u is there too, also where no tile needs it
     return;
   }
   if (warp == 0) {

@@ -1,0 +1,45 @@
+"""The launches that work on many tokens, each of which may start before the
+one ahead of it ends: what follows a call on its stream finds all of the call's
+outputs, whatever the tokens' adapters."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _bsmm():
+    import block_scaled_precision_gemm_gb300 as bsmm
+    return bsmm
+
+
+@pytest.mark.parametrize("K,N", [(67, 45), (1031, 45), (64, 72)])
+@pytest.mark.parametrize("some", [False, True])
+def test_tokens_without_adapters(K, N, some):
+    """No token has an adapter, or only the last one of 2100: u is zero and out
+    is y by the time that the next work of the stream reads them, in calls
+    that follow each other on one workspace."""
+    bsmm = _bsmm()
+    T, R, L = 2100, 16, 3
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x, a, b, y, dy, base = (torch.randn(*s, device="cuda", generator=g).bfloat16()
+                            for s in ((T, K), (L, R, K), (L, N, R), (T, N), (T, N), (T, K)))
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    if some:
+        ids[-1] = 1
+    ws = torch.empty(bsmm.adapters_workspace_size(T, R, L), dtype=torch.uint8, device="cuda")
+    back = torch.empty(bsmm.adapters_backward_workspace_size(T, R, L), dtype=torch.uint8, device="cuda")
+    out, u, dx = torch.empty_like(y), torch.empty((T, R), device="cuda"), torch.empty_like(base)
+    seen = []
+    for _ in range(20):
+        u.fill_(float("nan"))
+        out.fill_(float("nan"))
+        bsmm.adapters(x, a, b, ids, y=y, out=out, u=u, workspace=ws)
+        seen.append((u.clone(), out.clone()))
+        _, da, db = bsmm.adapters_backward(dy, x, a, b, ids, u, dx_base=base, dx=dx, workspace=back)
+        seen[-1] += (dx.clone(), da, db)
+    for su, so, sx, da, db in seen:
+        assert not su[:-1].any() and torch.equal(so[:-1], y[:-1]) and torch.equal(sx[:-1], base[:-1])
+        assert bool(su[-1].all()) == some and bool(da[1].any()) == some and bool(db[1].any()) == some
+        assert not da[::2].any() and not db[::2].any()
+    assert bsmm.check_device_status()[0] == 0
