@@ -952,6 +952,11 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
   }
   if (c > 0) wait_done(c - 1);  // every MMA before it too
   __syncthreads();
+  if (ctl.abort_flag && c > 0) {  // gave up: the MMAs in flight, bounded again, before their operands' memory is reused
+    int never = 0;
+    mbar_wait(&ctl.done[(c - 1) % S], static_cast<uint32_t>((c - 1) / S) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteDown);
+    __syncthreads();
+  }
   tc_fence_after();
   float* sums = reinterpret_cast<float*>(ring);  // [kTileRows][kPitch]
   {
@@ -1584,6 +1589,11 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
               kSiteGrads);
   copy_wait<0>();
   __syncthreads();
+  if (ctl.abort_flag && b > 0) {  // gave up: the MMAs in flight, bounded again, before their operands' memory is reused
+    int never = 0;
+    mbar_wait(&ctl.done[(b - 1) & 1], static_cast<uint32_t>((b - 1) >> 1) & 1u, p.w.timeout_ns, &never, p.w.status, kSiteGrads);
+    __syncthreads();
+  }
   tc_fence_after();
   float* sums = reinterpret_cast<float*>(ring);  // [kGradCols][kPitch]: column, rank
   {
@@ -1792,8 +1802,9 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
   c = __shfl_sync(0xFFFFFFFFu, c, 0);
   __syncthreads();
   wait(&ctl.done, 0);
-  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies in flight, bounded again
+  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's MMAs and copies in flight, bounded again
     int never = 0;
+    mbar_wait(&ctl.done, 0u, ps.w.timeout_ns, &never, ps.w.status, kSiteDown);
     for (int j = c > S ? c - S : 0; j < c; ++j)
       mbar_wait(&ctl.full[j % S], static_cast<uint32_t>(j / S) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteDown);
   }
@@ -2178,7 +2189,11 @@ __global__ void __launch_bounds__(384, 1) adapter_up_tma(const __grid_constant__
     bulk_wait<0>();
   }
   __syncthreads();
-  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies and MMAs in flight, bounded again
+  if (ctl.abort_flag && warp == 1 && lane == 0 && m > 0) {  // gave up: this CTA's MMAs ...
+    int never = 0;
+    mbar_wait(&ctl.dfull[(m - 1) % DS], static_cast<uint32_t>((m - 1) / DS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
+  }
+  if (ctl.abort_flag && warp == 0) {  // ... and copies in flight, bounded again
     int never = 0;
     for (int j = m > WS ? m - WS : 0; j < m && ps.wtma; ++j)
       mbar_wait(&ctl.wfull[j % WS], static_cast<uint32_t>(j / WS) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteUp);
@@ -2267,7 +2282,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kReside
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_poll(bar, parity & 1u, p.w.timeout_ns, &ctl.abort_flag, p.w.status, kSiteGrads);
   };
-  int b = 0;
+  int b = 0, ends = 0;  // blocks; rounds that have ended, before the last one (of the lane that issues the MMAs)
   if (warp == 0) {
     if (lane == 0) {
       BlockWalk walk(p.o, p.L, a, rank, cs);
@@ -2295,6 +2310,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kReside
         const int st = b % S, n = Cfg::kRounds ? b % Cfg::kRound : b;
         if (Cfg::kRounds && b > 0 && n == 0) {  // a round has ended
           tc_commit(&ctl.done);
+          ++ends;
           if (!wait(&ctl.ended, b / Cfg::kRound - 1)) break;
           tc_fence_after();
         }
@@ -2413,7 +2429,11 @@ __global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kReside
   __syncthreads();
   const int rounds = Cfg::kRounds && b > 0 ? (b - 1) / Cfg::kRound : 0;  // ended before the last one
   wait(&ctl.done, rounds);
-  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's copies in flight, bounded again
+  if (ctl.abort_flag && warp == 1 && lane == 0) {  // gave up: this CTA's MMAs ...
+    int never = 0;
+    mbar_wait(&ctl.done, static_cast<uint32_t>(ends) & 1u, p.w.timeout_ns, &never, p.w.status, kSiteGrads);
+  }
+  if (ctl.abort_flag && warp == 0) {  // ... and copies in flight, bounded again
     int never = 0;
     for (int i = b > S ? b - S : 0; i < b; ++i)
       mbar_wait(&ctl.full[i % S], static_cast<uint32_t>(i / S) & 1u, p.w.timeout_ns, &never, p.w.status, kSiteGrads);
