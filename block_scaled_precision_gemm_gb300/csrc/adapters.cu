@@ -2261,7 +2261,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kReside
   const uint32_t coef_off = kept ? Cfg::kCodeBytes + Cfg::kScaleBytes : Cfg::kXBytes;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&ctl.full[i], 1 + kGradHelpers);
+      mbar_init(&ctl.full[i], 1 + kGradHelpers + (kept && !p.scale4 ? kGradRows : 0));
       mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < ND; ++i) mbar_init(&ctl.decoded[i], kGradHelpers);
@@ -2371,6 +2371,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kReside
           uint32_t v = 0u;
           for (int k = 0; k < 4 && in && c0 / 32 + k < nb; ++k) v |= static_cast<uint32_t>(__ldg(sb + k)) << (8 * k);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+          mbar_arrive(&ctl.full[st]);  // an arrival for the store: the one below is for asynchronous copies only
         }
       }
       copy_arrive(&ctl.full[st]);

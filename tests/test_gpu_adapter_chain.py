@@ -43,3 +43,31 @@ def test_tokens_without_adapters(K, N, some):
         assert bool(su[-1].all()) == some and bool(da[1].any()) == some and bool(db[1].any()) == some
         assert not da[::2].any() and not db[::2].any()
     assert bsmm.check_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("K", [32, 96, 160, 416, 256])
+@pytest.mark.parametrize("R,grad", [(8, torch.float32), (16, torch.bfloat16), (64, torch.float32)])
+@pytest.mark.parametrize("order", ["mixed", "runs"])
+def test_checkpoint_like_its_values(K, R, grad, order):
+    """Codes and scales, whose rows may end inside a 4-byte word, give the bits
+    that their values, exact in bfloat16, give: a scale read before it is there
+    would not."""
+    bsmm = _bsmm()
+    T, N, L = 4200, 136, 3
+    g = torch.Generator(device="cuda").manual_seed(K + R)
+    wide = torch.exp2(torch.randint(-20, 20, (T, K // 32), device="cuda", generator=g).float()).repeat_interleave(32, 1)
+    codes, scales = bsmm.quantize(torch.randn(T, K, device="cuda", generator=g) * wide, (1, 32), "e4m3", "ue8m0")
+    values = codes.view(torch.float8_e4m3fn).float() * torch.exp2(scales.float() - 127).repeat_interleave(32, 1)
+    x = values.bfloat16()
+    assert torch.equal(x.float(), values)
+    a, b, dy = (torch.randn(*s, device="cuda", generator=g).bfloat16() for s in ((L, R, K), (L, N, R), (T, N)))
+    u = torch.randn(T, R, device="cuda", generator=g)
+    ids = torch.randint(-1, L, (T,), device="cuda", dtype=torch.int32, generator=g)
+    if order == "runs":
+        ids = ids.sort().values
+    ref = bsmm.adapters_backward(dy, x, a, b, ids, u, grad_dtype=grad)
+    for _ in range(5):
+        got = bsmm.adapters_backward(dy, codes, a, b, ids, u, x_scales=scales, grad_dtype=grad)
+        for p, q in zip(ref, got):
+            assert torch.equal(p, q)
+    assert bsmm.check_device_status()[0] == 0
