@@ -1559,6 +1559,10 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
   int issued = found;
   look();  // one ahead of the copies
   const uint32_t tmem = ctl.tmem;
+  auto wait_done = [&](int block) {  // the MMAs on it have read their operands
+    return mbar_wait(&ctl.done[block & 1], static_cast<uint32_t>(block >> 1) & 1u, p.w.timeout_ns, &ctl.abort_flag,
+                     p.w.status, kSiteGrads);
+  };
   bool ok = true;
   int b = 0;
   for (; b < issued; ++b) {
@@ -1567,15 +1571,22 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
     if (found > issued) put(issued);
     fence_proxy_async_smem();
     if (__syncthreads_or(!ok)) break;
+    const int n = Cfg::kRounds ? b % Cfg::kRound : b;
+    if (Cfg::kRounds && b > 0 && n == 0) {  // a round has ended
+      ok = wait_done(b - 1);
+      tc_fence_after();
+      if (ok && warp < 4) Cfg::end_round(tmem + ((warp & 3) * 32u << 16), b > Cfg::kRound);
+      tc_fence_before();
+      if (__syncthreads_or(!ok)) break;
+      tc_fence_after();
+    }
     if (tid == 0) {
       const uint32_t xt = ring_at + (kept ? b & 1 : b % S) * Cfg::kXBytes;
       const uint32_t ct = coef_at + (b % S) * Cfg::kCoefBytes;
-      Cfg::block(tmem, b, b, xt, ct);
+      Cfg::block(tmem, b, n, xt, ct);
       tc_commit(&ctl.done[b & 1]);
     }
-    if (b > 0)
-      ok = mbar_wait(&ctl.done[(b - 1) & 1], static_cast<uint32_t>((b - 1) >> 1) & 1u, p.w.timeout_ns, &ctl.abort_flag,
-                     p.w.status, kSiteGrads) && ok;
+    if (b > 0) ok = wait_done(b - 1) && ok;
     if (found > issued) {
       issue(issued);
       issue_coef(issued);
@@ -1584,9 +1595,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
     }
     copy_commit();
   }
-  if (b > 0)
-    mbar_wait(&ctl.done[(b - 1) & 1], static_cast<uint32_t>((b - 1) >> 1) & 1u, p.w.timeout_ns, &ctl.abort_flag, p.w.status,
-              kSiteGrads);
+  if (b > 0) wait_done(b - 1);
   copy_wait<0>();
   __syncthreads();
   if (ctl.abort_flag && b > 0) {  // gave up: the MMAs in flight, bounded again, before their operands' memory is reused
@@ -1595,6 +1604,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
     __syncthreads();
   }
   tc_fence_after();
+  const int rounds = Cfg::kRounds && b > 0 ? (b - 1) / Cfg::kRound : 0;  // ended before the last one
   float* sums = reinterpret_cast<float*>(ring);  // [kGradCols][kPitch]: column, rank
   {
     constexpr int kHalf = RP < 32 ? RP : RP / 2;
@@ -1602,7 +1612,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int k = 0; k < kHalf; k += 16) Cfg::read_sums16(src + k, b, 0, dst + k);
+      for (int k = 0; k < kHalf; k += 16) Cfg::read_sums16(src + k, b, rounds, dst + k);
     }
   }
   tc_fence_before();
