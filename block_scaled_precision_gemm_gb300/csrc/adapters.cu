@@ -2248,9 +2248,9 @@ struct GradTmaArgs {
 // adapter's last) and, where x is a checkpoint, decode its codes between the
 // two.  The first four of them also read the sums out of tensor memory at the
 // end.  8192 tokens of 4 adapters in random shares, 8192 x 8192, rank 16, x in
-// FP8, binary32 gradients: 66..86 us, 201 MB of x and dy at 2.3..3.0 TB/s: each
+// FP8, binary32 gradients: 61..76 us, 201 MB of x and dy at 2.6..3.3 TB/s: each
 // block waits in turn for its copy, the decoding and its MMAs, and CTAs start and
-// end (1024 of them on 304 places).
+// end (1024 of them, two to a cluster, on 304 places).
 template <int RP, int TERMS, typename G>
 __global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kResident) adapter_grads_tma(const __grid_constant__ GradTmaArgs ps) {
   using Cfg = GradTma<RP, TERMS>;
@@ -2619,24 +2619,6 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
   const cudaError_t e = launch("adapter_terms", adapter_terms<RP, TERMS>, terms, dim3(static_cast<unsigned>(all)), 256, 0, 1,
                                true, s);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
-  // Clusters split an adapter's blocks.  Few blocks: while all CTAs fit the SMs
-  // at once, since each costs some 5 us of latency that a second wave adds (2000
-  // tokens of 4096 columns, rank 16, 4 adapters: 14.2 us, with four times the
-  // CTAs 24.5).  More: a little beyond (1 adapter of 8192 tokens and columns: 61
-  // us with 512 CTAs on 456 places, 72 with half, 70 with twice).  Many, of
-  // several adapters: up to 2.75 CTAs a place, as requests are of all sizes and
-  // the longest adapter decides (8192 tokens and columns, 4 adapters in random
-  // shares: split in two 51..70 us, whole 70..82, in four 63..78; measured with
-  // three CTAs to an SM).
-  const int64_t places = GradTma<RP, TERMS>::kResident * ctx->num_sms;
-  unsigned cs = 1;
-  auto most = [&]() {
-    const int64_t each = blocks / cs;
-    return each > 16 && p.L > 1 ? 11 * places / 4 : (each > 8 ? 5 * places / 4 : places);
-  };
-  while (cs < 8 && blocks >= 2 * static_cast<int64_t>(cs) && tiles * p.L * cs * 2 <= most()) cs *= 2;
-  const dim3 grid(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L));
   GradTmaArgs a{};
   bool tma = true;
   for (int k = 0; k < 2 && tma; ++k)
@@ -2644,6 +2626,33 @@ cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCt
               ? rows_map(&a.x[k], p.job[k].x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.job[k].C, T, p.job[k].ld, kGradCols,
                          kGradRows)
               : rows_map(&a.x[k], p.job[k].x, kMapBf16, 2, p.job[k].C, T, p.job[k].ld, 64, kGradRows);
+  const int64_t tiles = p.job[0].tiles + p.job[1].tiles, blocks = ceil_div(T, static_cast<int64_t>(kGradRows) * p.L);
+  // Clusters split an adapter's blocks.  Few blocks: while all CTAs fit the SMs
+  // at once, since each costs some 5 us of latency that a second wave adds (2000
+  // tokens of 4096 columns, rank 16, 4 adapters: 18 us, in two 24, in four 33).
+  // More: a little beyond.  Many, of several adapters: several CTAs a place, as
+  // requests are of all sizes and the longest adapter decides; the more so where
+  // a block takes longer than its copy, because its codes are decoded or its
+  // rows staged element by element.  8192 tokens and columns, binary32
+  // gradients (two CTAs to an SM, 304 places), whole / in two / in four, means over
+  // six draws of the shares, traced:
+  //   1 adapter, codes   (128 CTAs whole)     115 / 72 / 72
+  //   2 adapters, codes  (256)                 91 / 71 / 74
+  //   4, codes           (512)                 78 / 73 / 91     rank 64: 114 / 107 / 132
+  //   4, bf16            (512)                 63 / 68 / 86
+  //   4, odd widths      (512)                255 / 215 / 230
+  //   8, codes           (1024)                72 / 87 / 127
+  //   4 of 4096 columns, codes (256)           69 / 48 / 51
+  // Bf16 gradients of ranks up to 16 (456 places) of 4 adapters' codes: 74 / 62 / 72.
+  const int64_t places = GradTma<RP, TERMS>::kResident * ctx->num_sms;
+  const bool slow_blocks = p.job[0].x_scales || !tma;
+  unsigned cs = 1;
+  auto most = [&]() {
+    const int64_t each = blocks / cs;
+    return each > 16 && p.L > 1 ? (slow_blocks ? 7 * places / 2 : 11 * places / 4) : (each > 8 ? 5 * places / 4 : places);
+  };
+  while (cs < 8 && blocks >= 2 * static_cast<int64_t>(cs) && tiles * p.L * cs * 2 <= most()) cs *= 2;
+  const dim3 grid(static_cast<unsigned>(tiles), cs, static_cast<unsigned>(p.L));
   if (tma) {
     a.g = p;
     return launch("adapter_grads_tma", adapter_grads_tma<RP, TERMS, G>, a, grid, 64 + kGradHelpers, GradTma<RP, TERMS>::kSmem, cs, true, s);
