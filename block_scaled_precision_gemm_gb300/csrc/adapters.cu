@@ -2714,18 +2714,27 @@ size_t adapter_terms_bytes(int64_t T, int64_t R, int64_t L) {
 
 // Whether tokens are sorted and worked on in tiles of one adapter, or taken as
 // they come.  As they come costs a pass over the weights per adapter met among
-// 16 tokens, so T R min(L, 16); sorted costs two more launches and a tile, full
-// or not, per adapter in use.  Measured, K = N = 4096, us as they come / sorted:
-//   R = 16, L = 8:    128: 18.4 / 21.6   384: 24.5 / 23.6   1024: 45 / 28
-//   R = 16, L = 64:   384: 36.8 / 50.2   777: 43.0 / 50.2   1024: 72 / 52
-//   R = 16, L = 512:  384: 53 / 153      2047: 143 / 288    4096: 264 / 264
-//   R = 32, L = 32:   128: 26.6 / 35.8   256: 40.9 / 33.8   1024: 78 / 36
-//   R = 64, L = 8:    64: 30.7 / 25.6    128: 43 / 25.6     1024: 137 / 31
-// The lines below are 0.2 ns a T R min(L, 16), and 3 us and 0.45 us a tile.
+// 16 tokens, so T R min(L, 16) or a little less, and from 16 tokens of high
+// ranks on a second wave of clusters; sorted costs two more launches and a tile,
+// full or not, per adapter in use.  Measured, K = N = 4096, tokens spread over all
+// adapters, us as they come / sorted, traced (R = 16 up to 16 ranks and so on):
+//   R = 16, L = 1:    512: 15 / 22     1024: 25 / 24     2047: 37 / 28
+//   R = 16, L = 8:    128: 18 / 22      384: 27 / 24     1024: 47 / 28
+//   R = 16, L = 64:   384: 41 / 52      777: 47 / 52     1024: 72 / 52
+//   R = 16, L = 512:  384: 55 / 159    2047: 150 / 302   4096: 274 / 273   8192: 504 / 267
+//   R = 32, L = 32:   128: 29 / 36      256: 42 / 36     1024: 82 / 38
+//   R = 64, L = 1:      8: 14 / 22       64: 25 / 24      192: 29 / 24
+//   R = 64, L = 8:      8: 16 / 26       64: 35 / 26      128: 49 / 26     1024: 150 / 34
+//   R = 128, L = 4:     8: 20 / 26       32: 39 / 26      128: 61 / 28
+// The lines below are right at each of these (ties aside) and, of lines of this
+// form, lose least over some 600 points at three pairs of widths (they do not
+// look at the widths: with wide outputs of many adapters a tile costs more,
+// 2048 x 8192, R = 16, L = 64, 1024 tokens: 90 / 122).
 bool adapters_sorted(int64_t T, int64_t R, int64_t L) {
   int64_t rp = 16;
   while (rp < R) rp *= 2;
-  return L <= kSortMaxL && T * rp * std::min<int64_t>(L, 16) >= 15000 + 2250 * std::min(L, T);
+  return L <= kSortMaxL &&
+         rp * (25 * std::min<int64_t>(T, 16) + T * std::min<int64_t>(L, 12)) >= 30000 + 2500 * std::min(L, T);
 }
 int64_t adapters_sort_max() { return kSortMaxL; }
 
