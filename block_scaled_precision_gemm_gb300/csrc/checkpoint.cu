@@ -37,9 +37,8 @@ constexpr int kThreads = 256;
 
 constexpr int kFwdPer = 16, kBwdPer = 8;  // columns of a thread
 
-// exp and the reciprocal by their approximate forms (2 ulp, subnormals flushed):
-// h and the gradients are rounded to bf16 or 8 bits right after, or are within
-// 2^-20 of their magnitude as binary32.
+// exp and the reciprocal by their approximate forms (2 ulp, subnormals flushed);
+// what each function below makes of them is said there.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -52,49 +51,119 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// 1 / (1 + exp(-g)) of a pair
-__device__ __forceinline__ float2 sigmoid2(float2 g) {
-  const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
-  const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(1.f));
-  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+// x log2(e) of a pair, and what its rounding left times ln 2: exp(x) =
+// 2^t (1 + rest).  Without the rest the error grows with |x|, as |x| 2^-24.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = static_cast<float>(1.44269504088896340736 - static_cast<double>(kLog2e));
+constexpr float kLn2 = 0.69314718055994531f;
+__device__ __forceinline__ void exponent2(float2 x, float2& t, float2& rest) {
+  t = __fmul2_rn(x, both(kLog2e));
+  rest = __ffma2_rn(x, both(kLog2e), make_float2(-t.x, -t.y));
+  rest = __fmul2_rn(__ffma2_rn(x, both(kLog2eLow), rest), both(kLn2));
+}
+__device__ __forceinline__ float2 negative(float2 x) { return make_float2(-x.x, -x.y); }
+
+// The gradients take each of act(g) and the two terms of its derivative within
+// 2^-20 of itself, for all g that the activation does not make subnormal.  h,
+// which is rounded to bf16 or 8 bits in the forward, goes without the corrections
+// for rounded arguments: within 2^-21 + |g| 2^-23 (SiLU) or g^2 2^-23 (GELU) there.
+
+// SiLU, f = g p with p = 1 / (1 + exp(-g)), and its derivative p + f (1 - p), of
+// a pair.  With e = exp(-g), 1 - p is e p, which keeps its precision where p is
+// close to 1.  Below g = -87 the reciprocal would be subnormal, and flushed: that
+// is silu2_wide's.
+template <bool SLOPE>
+__device__ __forceinline__ void silu2(float2 g, float2& f, float2& df) {
+  float2 t, rest;
+  exponent2(negative(g), t, rest);
+  float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+  if constexpr (SLOPE) e = __ffma2_rn(e, rest, e);
+  const float2 d = __fadd2_rn(e, both(1.f));
+  const float2 p = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  f = __fmul2_rn(g, p);
+  if constexpr (SLOPE) df = __ffma2_rn(f, __fmul2_rn(e, p), p);
+}
+// For any g (f and derivative of the one, then of the other): below -64, p is
+// exp(g) to 2^-92 of it, and goes 64 powers of two higher until the last product.
+__device__ __noinline__ float4 silu2_wide(float2 g) {
+  float2 f, df, t, rest;
+  silu2<true>(make_float2(fmaxf(g.x, -80.f), fmaxf(g.y, -80.f)), f, df);
+  exponent2(g, t, rest);
+  float2 q = make_float2(ex2_approx(64.f + t.x), ex2_approx(64.f + t.y));
+  q = __ffma2_rn(q, rest, q);
+  return make_float4(g.x < -64.f ? g.x * q.x * 0x1p-64f : f.x, g.x < -64.f ? fmaf(g.x, q.x, q.x) * 0x1p-64f : df.x,
+                     g.y < -64.f ? g.y * q.y * 0x1p-64f : f.y, g.y < -64.f ? fmaf(g.y, q.y, q.y) * 0x1p-64f : df.y);
 }
 
-// g Phi(g), Phi through erfc so that its lower tail keeps its relative
-// precision.
-__device__ __forceinline__ float gelu(float g) { return 0.5f * g * erfcf(g * -0.70710678118654752f); }
-
-// g Phi(g) and its derivative.  In the lower tail erfc(x) turns a relative
-// error of x into 2 x^2 times as much; x = -g / sqrt(2) is therefore corrected
-// for its rounding to first order, by the density that the derivative needs
-// anyway.
-__device__ __forceinline__ void gelu_slope(float g, float& f, float& df) {
+// GELU, f = g Phi(g) and its derivative Phi + g times the density, of a pair.
+// Phi is taken through erfc so that its lower tail keeps its relative precision.
+// There erfc(x) turns a relative error of x into 2 x^2 times as much: for the
+// gradients x = -g / sqrt(2) is corrected for its rounding to first order, by
+// the density that they need anyway, and the density's exponent for that of g^2.
+template <bool SLOPE>
+__device__ __forceinline__ void gelu2(float2 g, float2& f, float2& df) {
   constexpr float c = 0.70710678118654752f;
-  constexpr float c_lo = static_cast<float>(0.70710678118654752440 - static_cast<double>(c));
-  const float density = 0.39894228040143268f * __expf(-0.5f * g * g);
-  const float x = -g * c;
-  const float dx = fmaf(-g, c_lo, fmaf(-g, c, -x));
-  const float cdf = 0.5f * erfcf(x) - 1.41421356237309505f * dx * density;
-  f = g * cdf;
-  df = cdf + g * density;
-}
-
-// act(g) of a pair.
-template <int ACT>
-__device__ __forceinline__ float2 act2(float2 g) {
-  if constexpr (ACT == BSMM_SILU) return __fmul2_rn(g, sigmoid2(g));
-  return make_float2(gelu(g.x), gelu(g.y));
-}
-
-// act(g) and its derivative of a pair.
-template <int ACT>
-__device__ __forceinline__ void act_slope2(float2 g, float2& f, float2& df) {
-  if constexpr (ACT == BSMM_SILU) {
-    const float2 p = sigmoid2(g);
-    f = __fmul2_rn(g, p);
-    df = __ffma2_rn(f, __ffma2_rn(p, both(-1.f), both(1.f)), p);  // p + g p (1 - p)
+  constexpr float c_low = static_cast<float>(0.70710678118654752440 - static_cast<double>(c));
+  if constexpr (!SLOPE) {
+    f = make_float2(0.5f * g.x * erfcf(g.x * -c), 0.5f * g.y * erfcf(g.y * -c));
   } else {
-    gelu_slope(g.x, f.x, df.x);
-    gelu_slope(g.y, f.y, df.y);
+    const float2 x = __fmul2_rn(g, both(-c));
+    float2 phi = __fmul2_rn(make_float2(erfcf(x.x), erfcf(x.y)), both(0.5f));
+    const float2 gg = __fmul2_rn(g, g), half = __fmul2_rn(gg, both(-0.5f));
+    float2 t, rest;
+    exponent2(half, t, rest);
+    rest = __ffma2_rn(__ffma2_rn(g, g, negative(gg)), both(-0.5f), rest);
+    float2 density = __fmul2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(0.39894228040143268f));
+    density = __ffma2_rn(density, rest, density);
+    const float2 off = __ffma2_rn(g, both(-c_low), __ffma2_rn(g, both(-c), negative(x)));
+    phi = __ffma2_rn(__fmul2_rn(off, both(-1.41421356237309505f)), density, phi);
+    df = __ffma2_rn(g, density, phi);
+    f = __fmul2_rn(g, phi);
+  }
+}
+// For any g: with E = exp(-g^2 / 2) the tail beyond |g| is E erfcx(|g| / sqrt 2)
+// / 2.  E is the square of exp(-g^2 / 4), times what the rounding of g^2 left; the
+// lower tail's products take its two factors last, so that nothing is subnormal
+// before the result is.
+__device__ __noinline__ float2 gelu_wide(float g) {
+  const float m = fminf(fabsf(g), 20.f), mm = m * m;  // beyond, E is zero
+  const float e1 = expf(-0.25f * mm), e2 = e1 * fmaf(-0.5f, fmaf(m, m, -mm), 1.f);
+  const float half = 0.5f * erfcxf(fabsf(g) * 0.70710678118654752f), density = 0.39894228040143268f * g;
+  const float phi = fmaf(-half * e1, e2, 1.f);  // of |g|
+  return g < 0.f ? make_float2(g * half * e1 * e2, (half + density) * e1 * e2)
+                 : make_float2(g * phi, fmaf(density * e1, e2, phi));
+}
+
+// Up to this magnitude of g the narrow forms hold; h's, whose SiLU alone would be
+// flushed, likewise.
+template <int ACT>
+__device__ __forceinline__ constexpr float narrow() { return ACT == BSMM_SILU ? 80.f : 12.f; }
+
+// act(g) and its derivative (SLOPE) of pairs.
+template <int ACT, bool SLOPE, int kPairs>
+__device__ __forceinline__ void act_pairs(const float2 (&g)[kPairs], bool wide, float2 (&f)[kPairs], float2 (&df)[kPairs]) {
+  if (wide && (SLOPE || ACT == BSMM_SILU)) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      if constexpr (ACT == BSMM_SILU) {
+        const float4 v = silu2_wide(g[i]);
+        f[i] = make_float2(v.x, v.z);
+        if constexpr (SLOPE) df[i] = make_float2(v.y, v.w);
+      } else if constexpr (SLOPE) {
+        const float2 a = gelu_wide(g[i].x), b = gelu_wide(g[i].y);
+        f[i] = make_float2(a.x, b.x);
+        df[i] = make_float2(a.y, b.y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const float2 x = g[i];  // (f may be g's array)
+      if constexpr (ACT == BSMM_SILU)
+        silu2<SLOPE>(x, f[i], df[i]);
+      else
+        gelu2<SLOPE>(x, f[i], df[i]);
+    }
   }
 }
 
@@ -167,6 +236,23 @@ __device__ __forceinline__ void absmax2(const RawF32& g, const RawF32& u, float&
   };
   mg = lanes_max<W>(fold(g));
   mu = lanes_max<W>(fold(u));
+}
+
+// The largest magnitude of a thread's own elements.
+__device__ __forceinline__ float own_absmax(const RawBf16& r) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < RawBf16::kWords; ++i)
+    m = bf16x2_max_abs(m, bf16x2_max_abs(bf16x2_max_abs(r.w[i].x, r.w[i].y), bf16x2_max_abs(r.w[i].z, r.w[i].w)));
+  return bf16_lo_abs(bf16x2_max_abs(m, m >> 16));
+}
+__device__ __forceinline__ float own_absmax(const RawF32& r) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < RawF32::kWords; ++i)
+    m = fmaxf(m, fmaxf(fmaxf(fabsf(__uint_as_float(r.w[i].x)), fabsf(__uint_as_float(r.w[i].y))),
+                       fmaxf(fabsf(__uint_as_float(r.w[i].z)), fabsf(__uint_as_float(r.w[i].w)))));
+  return m;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
@@ -365,7 +451,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const GatedFwd p) {
     rg.values(g);
     ru.values(u);
     float mg = 0.f, mu = 0.f;
-    if constexpr (KEEP != kKeepNone) absmax2<W>(rg, ru, mg, mu);
+    if constexpr (KEEP != kKeepNone)
+      absmax2<W>(rg, ru, mg, mu);
+    else
+      mg = own_absmax(rg);
+    const bool wide = mg > narrow<ACT>();
     x += k.step * p.ld;
     if (row + k.step < p.M) {
       rg.load(x);
@@ -388,8 +478,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const GatedFwd p) {
       codes += k.step * 2 * I;
       scales += k.step * 2 * nb * (POW2 ? 1 : 4);
     }
+    act_pairs<ACT, false>(g, wide, g, g);
 #pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) u[i] = __fmul2_rn(act2<ACT>(g[i]), u[i]);  // h
+    for (int i = 0; i < kPer / 2; ++i) u[i] = __fmul2_rn(g[i], u[i]);  // h
     if constexpr (HQ) {
       float m = 0.f;
 #pragma unroll
@@ -453,7 +544,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(D) == 2 ? 4 : 3) gated_bwd(co
   if (k.row < p.M) load();
   for (int64_t row = k.row; row < p.M; row += k.step) {
     const float vg = POW2 ? ue8m0_value(sg) : __uint_as_float(sg), vu = POW2 ? ue8m0_value(su) : __uint_as_float(su);
-    float2 g[kPer / 2], u[kPer / 2], v[kPer / 2], f[kPer / 2];
+    float2 g[kPer / 2], u[kPer / 2], v[kPer / 2], f[kPer / 2], df[kPer / 2];
+    const bool wide = !(vg * qmax_of(CODE) <= narrow<ACT>());
     values4<CODE>(cg.x, vg, g);
     values4<CODE>(cg.y, vg, g + 2);
     values4<CODE>(cu.x, vu, u);
@@ -463,11 +555,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(D) == 2 ? 4 : 3) gated_bwd(co
     scales += k.step * 2 * nb * (POW2 ? 1 : 4);
     dhp += k.step * I;
     if (row + k.step < p.M) load();
+    act_pairs<ACT, true>(g, wide, f, df);
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) {
-      float2 df;
-      act_slope2<ACT>(g[i], f[i], df);
-      g[i] = __fmul2_rn(__fmul2_rn(v[i], u[i]), df);
+      g[i] = __fmul2_rn(__fmul2_rn(v[i], u[i]), df[i]);
       u[i] = __fmul2_rn(f[i], u[i]);  // h
       f[i] = __fmul2_rn(v[i], f[i]);
     }

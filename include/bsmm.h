@@ -496,6 +496,9 @@ typedef enum bsmm_act {
  *            all-zero block 1), at most an ulp from bsmm_quantize's quotient.
  *   I a multiple of 32, of 128 for a checkpoint with F32 scales.
  *   Pointers (but for h_scales and scales) and row pitches 16-byte aligned.
+ *   Before its rounding to h_type, h is within 2^-20 + |g| 2^-23 (SiLU) or
+ *   2^-20 + g^2 2^-23 (GELU, g < 0) of its value; act below 2^-126 is a
+ *   binary32 subnormal.
  *   Inputs are taken to be finite, as bsmm_quantize takes them. */
 bsmm_status bsmm_gated_act(const void* gate_up, bsmm_dtype x_type, int64_t M, int64_t I, int64_t ld_x, bsmm_act act,
                            bsmm_dtype h_type, void* h, void* h_scales, int h_scales_are_atoms, bsmm_dtype code_type,
@@ -503,7 +506,10 @@ bsmm_status bsmm_gated_act(const void* gate_up, bsmm_dtype x_type, int64_t M, in
 
 /* Its backward pass from the checkpoint (g, u the values of its codes):
  *   d_gate = dh * u * act'(g),  d_up = dh * act(g),  h = act(g) * u,
- * each computed in binary32 and rounded once.
+ * each computed in binary32 and rounded once: act(g) and each of the two terms
+ * that act'(g) is the sum of (p and g p (1 - p) for SiLU, p the logistic
+ * function; the CDF and g times the density for GELU) is within 2^-20 of itself,
+ * in the tails too.
  *
  *   dh [M, I] and d_gate_up [M, 2 I] of type d_type (F32 or BF16), contiguous.
  *   h        BF16 [M, I]: the down projection's input again, for its weight

@@ -1,0 +1,102 @@
+"""bsmm_gated_act and its backward where the activation nearly vanishes or is
+nearly the identity: relative errors, with no absolute allowance but what
+binary32's smallest numbers need.
+
+SiLU and GELU and both terms of their derivatives (p and g p (1 - p), Phi and g
+times the density) are each held to 2^-20 of themselves: exp to 2^-22, a
+reciprocal or erfc to 2^-22, three roundings.  Products with dh and u add three
+roundings of 2^-24.  An activation below 2^-126 is a multiple of 2^-149."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import formats as F
+
+pytestmark = pytest.mark.gpu
+
+REL = 2.0 ** -20 + 2.0 ** -22
+TINY = 2.0 ** -148  # of a subnormal act, times the factor after it, or of a subnormal result
+
+
+def _bsmm():
+    import block_scaled_precision_gemm_gb300 as bsmm
+    return bsmm
+
+
+def act64(g, act):
+    """act(g) and the two terms of its derivative, on float64 tensors."""
+    if act == "silu":
+        p = torch.exp(torch.clamp(g, max=0)) / (1 + torch.exp(-g.abs()))
+        q = torch.exp(torch.clamp(-g, max=0)) / (1 + torch.exp(-g.abs()))  # 1 - p
+        return g * p, p, g * p * q
+    cdf = 0.5 * torch.special.erfc(-g * 0.5 ** 0.5)
+    return g * cdf, cdf, g * torch.exp(-0.5 * g * g) * (2 * np.pi) ** -0.5
+
+
+def inside(got, ref, tol, what):
+    spacing = 2.0 ** -133 if got.dtype == torch.bfloat16 else 0.0
+    bad = ~((got.double() - ref).abs() <= tol + spacing / 2)
+    assert not bad.any(), (what, int(bad.sum()), [float(v[bad].flatten()[0]) for v in (got.double(), ref, tol)])
+
+
+@pytest.mark.parametrize("act,largest", [("silu", [1, 4, 10, 20, 40, 60, 79, 81, 86, 90, 100, 130, 1e4]),
+                                         ("gelu", [1, 2, 4, 8, 10, 12, 13, 14, 20, 100, 1e20])])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3 f32", "e4m3 ue8m0", "e5m2 ue8m0"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_backward(act, largest, fmt, dtype):
+    bsmm = _bsmm()
+    code, scale = (fmt.split() + ["f32"])[:2]
+    I, rows = 1024, 8
+    M = rows * len(largest)
+    g = torch.Generator().manual_seed(len(largest))
+    block = 128 if scale == "f32" else 32
+    if code == "int8":
+        codes = torch.randint(-127, 128, (M, 2 * I), generator=g, dtype=torch.int16).to(torch.int8)
+        values, qmax = codes.double(), 127.0
+    else:
+        codes = torch.randint(0, 256, (M, 2 * I), generator=g, dtype=torch.int16).to(torch.uint8)
+        codes[(codes & 0x7F) >= (0x7F if code == "e4m3" else 0x7C)] = 0x38
+        values, qmax = torch.from_numpy(F.decode(codes.numpy(), code).astype(np.float64)), 448.0 if code == "e4m3" else 57344.0
+    top = torch.tensor(largest, dtype=torch.float64).repeat_interleave(rows)[:, None].expand(M, I // block)
+    s = torch.cat([top / qmax, torch.full((M, I // block), 3.0 / qmax, dtype=torch.float64)], 1).float()
+    if scale == "ue8m0":
+        stored = (torch.log2(s).ceil() + 127).clamp(0, 254).to(torch.uint8)
+        s = torch.exp2(stored.float() - 127)
+    else:
+        stored = s
+    v = (values.view(M, -1, block) * s.double()[..., None]).float().view(M, 2 * I).double()
+    gate, up = v[:, :I], v[:, I:]
+    dh = torch.randn(M, I, generator=g).to(dtype)
+    d, h = bsmm.gated_act_backward(dh.cuda(), codes.cuda(), stored.cuda(), act=act, code=code, scale=scale, return_h=True)
+    f, a, b = act64(gate, act)
+    w, wu = dh.double(), dh.double() * up
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    out = d.cpu()
+    ref = w * f
+    inside(out[:, I:], ref, (REL + half) * ref.abs() + TINY * (1 + w.abs()), "d_up")
+    ref = wu * (a + b)
+    inside(out[:, :I], ref, REL * wu.abs() * (a.abs() + b.abs()) + half * ref.abs() + TINY * (1 + wu.abs()), "d_gate")
+    ref = f * up
+    inside(h.cpu(), ref, (REL + 2.0 ** -8) * ref.abs() + TINY * (1 + up.abs()), "h")
+
+
+@pytest.mark.parametrize("code,scale", [(None, "f32"), ("int8", "f32"), ("e4m3", "ue8m0")])
+@pytest.mark.parametrize("act,low,high", [("silu", -102.0, -60.0), ("silu", -12.0, 110.0), ("gelu", -13.5, -8.0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_forward(act, low, high, code, scale, dtype):
+    """h of vanishing activations times large numbers."""
+    bsmm = _bsmm()
+    M, I = 5, 4096
+    gate = torch.linspace(low, high, I).expand(M, I)
+    up = 1e30 * (1 + torch.rand(M, I, generator=torch.Generator().manual_seed(2)))
+    x = torch.cat([gate, up], 1).to(dtype)
+    f = act64(x[:, :I].double(), act)[0]
+    ref, tiny = f * x[:, I:].double(), TINY * (1 + x[:, I:].double().abs())
+    h, _, _, _ = bsmm.gated_act(x.cuda(), act=act, h_type="bf16", code=code, scale=scale)
+    inside(h.cpu(), ref, (2.0 ** -8 + 2.0 ** -15) * ref.abs() + tiny, "bf16")
+    # E4M3: half a unit of 3 bits; a block's maximum is 256 times its smallest normal code at least
+    q, qs, _, _ = bsmm.gated_act(x.cuda(), act=act, h_type="e4m3", code=code, scale=scale)
+    s = torch.exp2(qs.cpu().double() - 127).repeat_interleave(32, 1)
+    got = torch.from_numpy(F.decode(q.cpu().numpy(), "e4m3").astype(np.float64)) * s
+    inside(got, ref, 2.0 ** -4 * (1 + 2.0 ** -12) * ref.abs() + tiny + s * 2.0 ** -10, "e4m3")
