@@ -1408,7 +1408,13 @@ __device__ __forceinline__ void write_grad(const Grads& p, const GradJob& j, con
     __syncwarp();
     cluster_sync();
   }
-  const float s = p.scaling ? __ldg(p.scaling + a) : 1.f;
+  // an adapter without tokens has gradients of zero whatever its scaling is
+  bool any = false;
+  for (int seg = 0; seg < p.o.segments && !any; ++seg) {
+    const int* starts = p.o.starts + static_cast<int64_t>(seg) * (p.L + 1) + a;
+    any = starts[1] > starts[0];
+  }
+  const float s = any && p.scaling ? __ldg(p.scaling + a) : 1.f;
   const int cols = static_cast<int>(min(static_cast<int64_t>(kGradCols), j.C - c0));
   const int quads = (p.R + 3) / 4, n = quads * cols, share = (n + cs - 1) / cs;
   const int end = min(n, (rank + 1) * share);

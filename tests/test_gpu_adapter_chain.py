@@ -71,3 +71,24 @@ def test_checkpoint_like_its_values(K, R, grad, order):
         for p, q in zip(ref, got):
             assert torch.equal(p, q)
     assert bsmm.check_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("T,K,N", [(8, 64, 40), (8, 63, 41), (2100, 64, 72), (16500, 67, 45)])
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+def test_gradients_of_adapters_without_tokens(T, K, N, grad):
+    """Zero, also where the scaling is no finite number; the last tokens alone
+    use adapter 1."""
+    bsmm = _bsmm()
+    R, L = 16, 4
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, a, b, dy = (torch.randn(*s, device="cuda", generator=g).bfloat16() for s in ((T, K), (L, R, K), (L, N, R), (T, N)))
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    ids[-5:] = 1
+    u = torch.randn(T, R, device="cuda", generator=g)
+    scaling = torch.tensor([float("nan"), 0.5, float("inf"), -float("inf")], device="cuda")
+    _, da, db = bsmm.adapters_backward(dy, x, a, b, ids, u, scaling=scaling, grad_dtype=grad)
+    for t in (da, db):
+        assert not t[[0, 2, 3]].any() and bool(torch.isfinite(t[1].float()).all()) and bool(t[1].any())
+    scaling[1] = float("nan")
+    _, da, db = bsmm.adapters_backward(dy, x, a, b, ids, u, scaling=scaling, grad_dtype=grad)
+    assert bool(da[1].isnan().all()) and bool(db[1].isnan().all()) and not da[::2].any() and not db[::2].any()
