@@ -381,9 +381,10 @@ __device__ __forceinline__ void values4(uint32_t w, float s, float2* v) {
 // ---------------------------------------------------------------------------
 // Gated activation
 // ---------------------------------------------------------------------------
-// A thread's columns and rows.  The columns are cut into tiles (blockIdx.y) of
-// `width` threads each, and a CTA takes kThreads / width rows at a time; width
-// is a multiple of the lanes of a block, which thus share a row and a warp.
+// A thread's columns and rows.  The columns are cut into tiles (blockIdx.x, which
+// has room for any number of them) of `width` threads each, and a CTA takes
+// kThreads / width rows at a time; width is a multiple of the lanes of a block,
+// which thus share a row and a warp.
 struct Strips {
   int width, rows;  // threads across a tile, rows of a CTA
   int tiles;
@@ -394,9 +395,9 @@ struct Strip {
   bool on;
   __device__ __forceinline__ Strip(const Strips& s, int per, int I) {
     const int r = static_cast<int>(threadIdx.x) / s.width, c = static_cast<int>(threadIdx.x) - r * s.width;
-    row = static_cast<int64_t>(blockIdx.x) * s.rows + r;
-    step = static_cast<int64_t>(gridDim.x) * s.rows;
-    col = (static_cast<int>(blockIdx.y) * s.width + c) * per;
+    row = static_cast<int64_t>(blockIdx.y) * s.rows + r;
+    step = static_cast<int64_t>(gridDim.y) * s.rows;
+    col = (static_cast<int>(blockIdx.x) * s.width + c) * per;
     on = r < s.rows && col < I;
   }
 };
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(D) == 2 ? 4 : 3) gated_bwd(co
 // Enough CTAs to fill the SMs (`resident` on each), no more than the rows ask for.
 dim3 gated_grid(const Strips& s, int64_t M, int resident, const DeviceCtx* ctx) {
   const int64_t want = ceil_div(M, s.rows), full = ceil_div(static_cast<int64_t>(ctx->num_sms) * resident, s.tiles);
-  return dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min(want, full))), static_cast<unsigned>(s.tiles));
+  return dim3(static_cast<unsigned>(s.tiles), static_cast<unsigned>(std::max<int64_t>(1, std::min(want, full))));
 }
 
 template <typename In, int KEEP, int ACT>
