@@ -280,7 +280,9 @@ __device__ __forceinline__ void store(void* p, const float2 (&v)[kPairs]) {
 // UE8M0: the smallest power of two 2^e with absmax <= qmax 2^e.  Both formats'
 // qmax is 1.75 times a power of two, so e follows from absmax's exponent and
 // whether its significand is above 1.75: bsmm_quantize's rule (whose rounded
-// ratio absmax / qmax is 1 only when absmax = qmax) without its division.
+// ratio absmax / qmax is a power of two only when absmax is qmax times one)
+// without its division.  One number is an exception: the first above qmax
+// 2^-127, whose ratio is subnormal and rounds to 2^-127.
 // F32: binary32(absmax * binary32(1 / qmax)), one product where bsmm_quantize
 // divides; at most one ulp away.
 template <bool POW2>
@@ -289,7 +291,8 @@ __device__ __forceinline__ Scale block_scale(float absmax, int code) {
   if constexpr (POW2) {
     const uint32_t bits = __float_as_uint(absmax);
     const int top = code == BSMM_E4M3 ? 8 : 15;
-    int e = static_cast<int>(bits >> 23) - top + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    int e = static_cast<int>((bits + 0x1FFFFFu) >> 23) - top;  // (the sum carries above 1.75)
+    if (bits == ((static_cast<uint32_t>(top) << 23) | 0x600001u)) e = 0;
     e = absmax == 0.f ? 127 : max(e, 0);  // biased
     sc.stored = static_cast<uint32_t>(e);
     sc.s = 0.f;  // not used: codes are x * inv
