@@ -137,29 +137,37 @@ __device__ __forceinline__ void load_row(const bf16* row, int64_t c, int64_t lim
 // and in a zero's place goes 2^-126, which is below 2^-24 of any v that gets it.
 // Infinity times v is then one infinity, not their difference, nor infinity
 // times zero.  (A v below 2^-100 in magnitude keeps its zeros.)
+//
+// In few instructions (u is split anew for every tile): a zero, like the NaN
+// that infinity leaves, loses against 2^-126 in a maximum.
 template <int TERMS>
-__device__ __forceinline__ void split_one(float v, float (&t)[TERMS]) {
-  const uint32_t b = __float_as_uint(v), magnitude = b & 0x7FFFFFFFu;
-  const float least = magnitude >= (27u << 23) ? __uint_as_float((b & 0x80000000u) | (1u << 23)) : 0.f;
-  t[0] = __uint_as_float(magnitude > 0x7F800000u ? 0x7FFF0000u : b & 0xFFFF0000u);
-  float left = magnitude < 0x7F800000u ? v - t[0] : 0.f;
+__device__ __forceinline__ void split_one(float v, uint32_t (&t)[TERMS]) {
+  constexpr uint32_t kTop = 0xFFFF0000u;
+  asm("add.f32 %0, %0, 0f80000000;" : "+f"(v));  // a NaN of any bits becomes the one whose top half is a NaN
+  const uint32_t b = __float_as_uint(v), sign = b & 0x80000000u;
+  const float least = fabsf(v) >= 0x1p-100f ? 0x1p-126f : 0.f;
+  t[0] = b & kTop;
+  float left = v - __uint_as_float(t[0]);
 #pragma unroll
   for (int k = 1; k < TERMS; ++k) {
-    const float cut = k + 1 < TERMS ? __uint_as_float(__float_as_uint(left) & 0xFFFF0000u) : left;
-    t[k] = cut == 0.f ? least : cut;
-    left -= cut;
+    t[k] = __float_as_uint(fmaxf(fabsf(left), least)) | sign;
+    if (k + 1 == TERMS) break;
+    t[k] &= kTop;
+    left -= __uint_as_float(t[k]);
   }
 }
-// Term k of both in w[k] (the last ones rounded).
+// Term k of both in w[k] (of two the last ones rounded; of three they are exact).
 template <int TERMS>
 __device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&w)[TERMS]) {
-  float t0[TERMS], t1[TERMS];
+  uint32_t t0[TERMS], t1[TERMS];
   split_one<TERMS>(v0, t0);
   split_one<TERMS>(v1, t1);
 #pragma unroll
-  for (int k = 0; k + 1 < TERMS; ++k) w[k] = __byte_perm(__float_as_uint(t0[k]), __float_as_uint(t1[k]), 0x7632);
-  const __nv_bfloat162 h = __floats2bfloat162_rn(t0[TERMS - 1], t1[TERMS - 1]);
-  w[TERMS - 1] = *reinterpret_cast<const uint32_t*>(&h);
+  for (int k = 0; k < TERMS; ++k) w[k] = __byte_perm(t0[k], t1[k], 0x7632);
+  if constexpr (TERMS == 2) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(t0[1]), __uint_as_float(t1[1]));
+    w[1] = *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 
 // The adapter of row t, or -1 for none (also for an id outside [0, L)).
