@@ -280,7 +280,7 @@ struct Rows {
 // binary32 precision, and takes 32 columns at a time: lane q of each row ends up with 8
 // consecutive outputs.  At these sizes latency is what counts: one launch, and
 // no trip of u through memory (two launches took 13 + 10 us for 64 requests of
-// 4096 x 4096 and rank 16, cold; this one 16, and one token 7.5).
+// 4096 x 4096 and rank 16, cold; this one 17, and one token 7.6).
 template <int NT, typename Y, bool TRANS, bool VEC, int UNROLL>
 __global__ void __launch_bounds__(256, NT <= 2 && !TRANS ? 3 : (NT <= 4 ? 2 : 1)) adapter_rows(const __grid_constant__ Rows pr) {
   constexpr int WK = 8, kRows = 16, kCols = NT * 8;
@@ -992,8 +992,8 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
 // of base, lanes along the rows, takes chunk c's product through shared memory
 // to the same lanes, and stores the sum from there.  (With a lane's eight
 // elements in a row, as pieces of 16 bytes, an instruction touched 16 sectors
-// instead of 2 or 3: 6262 tokens of 6972 columns and rank 16 took 225 us; now 74,
-// 2.4 TB/s.)
+// instead of 2 or 3: 6262 tokens of 6972 columns and rank 16 took 225 us; now 72,
+// 2.5 TB/s.)
 template <int RP, typename Y, bool TRANS>
 struct UpTile {
   static constexpr int TERMS = kTerms;
@@ -1892,12 +1892,13 @@ struct TileWalk {
 // One CTA to an SM, each with an equal stretch of all tiles' chunks, so that
 // loads and stores go on at a steady rate from the first tile to the last (as
 // CTAs of a tile and 16 chunks each, in two waves, 8192 tokens of 8192 columns
-// and rank 64 took 61 us; this takes 54, 5.0 TB/s in and out).  Warp 0 feeds base and the weights, warp 1 issues the
-// MMAs, warps 2 and 3 are the helpers, which gather a tile's rows of base that
-// are not consecutive; warps 4..7 and 8..11 take turns at the chunks: each warp
-// adds the product of 32 rows to base in place in its stage, and from there
-// writes 32 consecutive rows with one TMA store, other rows in whole 128-byte
-// pieces.  At a tile's start they split its u.
+// and rank 64 took 61 us; this took 55, and takes 57, 4.9 TB/s in and out, since
+// u has three terms and signs for infinities).  Warp 0 feeds base and the
+// weights, warp 1 issues the MMAs, warps 2 and 3 are the helpers, which gather a
+// tile's rows of base that are not consecutive; warps 4..7 and 8..11 take turns
+// at the chunks: each warp adds the product of 32 rows to base in place in its
+// stage, and from there writes 32 consecutive rows with one TMA store, other rows
+// in whole 128-byte pieces.  At a tile's start they split its u.
 template <int RP, typename Y, bool TRANS>
 __global__ void __launch_bounds__(384, 1) adapter_up_tma(const __grid_constant__ UpTmaArgs ps) {
   using Cfg = UpTma<RP, Y, TRANS>;
@@ -2623,7 +2624,7 @@ cudaError_t both_products(const Down& d, const Up& u, const Order* o, const Devi
 
 template <int RP, typename G>
 cudaError_t grads_rank(Grads p, const AdaptersBackwardRequest& r, const DeviceCtx* ctx, cudaStream_t s) {
-  constexpr int TERMS = sizeof(G) == 4 ? 3 : 2;
+  constexpr int TERMS = sizeof(G) == 4 ? 3 : 2;  // two hold a coefficient to 2^-16, bf16's own rounding is 2^-9
   const int64_t T = r.T;
   const int64_t all = static_cast<int64_t>(p.o.segments) * p.o.blocks_per_segment;
   uint8_t* images[2] = {static_cast<uint8_t*>(r.terms), static_cast<uint8_t*>(r.terms) + all * CoefImage<RP, TERMS>::kBytes};

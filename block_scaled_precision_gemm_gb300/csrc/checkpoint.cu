@@ -2,9 +2,10 @@
 // inputs as block-scaled codes, its backward pass from those codes, and the
 // requantization of a kept GEMM operand along its other axis.
 //
-// A checkpoint is what bsmm_quantize writes: 8-bit codes with a binary32 scale
-// per 1 x 128 block or a UE8M0 scale per 1 x 32 block.  The value a code stands
-// for is binary32(code * scale).
+// A checkpoint has the form that bsmm_quantize writes: 8-bit codes with a
+// binary32 scale per 1 x 128 block or a UE8M0 scale per 1 x 32 block.  The value
+// a code stands for is binary32(code * scale).  (The binary32 scales written
+// here may be an ulp from bsmm_quantize's: see block_scale.)
 //
 // Kernels:
 //   gated_fwd     h = act(gate) * up, quantized per 1 x 32 (or bf16); gate and
@@ -66,7 +67,7 @@ __device__ __forceinline__ float2 negative(float2 x) { return make_float2(-x.x, 
 // The gradients take each of act(g) and the two terms of its derivative within
 // 2^-20 of itself, for all g that the activation does not make subnormal.  h,
 // which is rounded to bf16 or 8 bits in the forward, goes without the corrections
-// for rounded arguments: within 2^-21 + |g| 2^-23 (SiLU) or g^2 2^-23 (GELU) there.
+// for rounded arguments: within 2^-20 + |g| 2^-23 (SiLU) or g^2 2^-23 (GELU) there.
 
 // SiLU, f = g p with p = 1 / (1 + exp(-g)), and its derivative p + f (1 - p), of
 // a pair.  With e = exp(-g), 1 - p is e p, which keeps its precision where p is
@@ -428,8 +429,8 @@ struct GatedFwd {
 constexpr int kKeepNone = 0, kKeepMx = 1, kKeepF32 = 2;
 
 // The next row's elements are loaded before this row's are worked on.  8192 rows
-// of I = 8192 in bf16, SiLU, h in E4M3, INT8 kept: 82 us, 475 MB at 5.8 TB/s
-// (0.85 of a copy's rate), issue 59 % busy.  GELU takes erfc's instructions:
+// of I = 8192 in bf16, SiLU, h in E4M3, INT8 kept: 83 us, 475 MB at 5.7 TB/s
+// (0.84 of a copy's rate), issue 59 % busy.  GELU takes erfc's instructions:
 // 7111 x 3968 75 us, 2.5 times its floor.
 template <typename In, int KEEP, int ACT, bool HQ>
 __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const GatedFwd p) {
@@ -517,8 +518,8 @@ struct GatedBwd {
   Strips strips;
 };
 
-// 8192 rows of I = 8192, INT8 kept, dh in bf16, h written too: 101 us, 675 MB at
-// 6.7 TB/s, a copy's rate.
+// 8192 rows of I = 8192, INT8 kept, dh in bf16, h written too: SiLU 101 us, 675 MB
+// at 6.7 TB/s, a copy's rate; GELU 160 (MXFP8 170), erfc's instructions.
 template <typename D, int CODE, bool POW2, int ACT>
 __global__ void __launch_bounds__(kThreads, sizeof(D) == 2 ? 4 : 3) gated_bwd(const GatedBwd p) {
   constexpr int kPer = kBwdPer, kBlock = POW2 ? 32 : 128;

@@ -583,7 +583,9 @@ bsmm_status bsmm_adapters(int64_t T, int64_t K, int64_t N, int64_t R, int64_t L,
  *   dx_base  bfloat16 [T, K], the shared projection's dX, or NULL for 0; dx
  *            bfloat16 [T, K], may be dx_base itself.  Both at a pitch of ld_dx.
  *   dA [L, R, K], dB [L, N, R] of type grad_type (F32 or BF16), contiguous:
- *            overwritten; zero for an adapter without tokens.
+ *            overwritten; zero for an adapter without tokens.  F32 ones sum
+ *            products of binary32 d and u; BF16 ones take d and u to 2^-16 of
+ *            themselves before the sums are rounded.
  *   workspace  bsmm_adapters_backward_workspace_size() bytes, 256-byte
  *            aligned (holds d, the order of the tokens by their adapter, and d
  *            and u in that order).
