@@ -751,16 +751,6 @@ struct Waits {
 };
 constexpr int kSiteDown = 41, kSiteUp = 42, kSiteGrads = 43;
 
-// A long sum is dealt to kSums accumulators of RP columns each in tensor memory,
-// joined here in order: the tensor cores add with truncation, whose drift grows
-// with the number of additions into one accumulator (u of 8192 columns: over
-// 1.4e-6 of its norm off with one, 2.4e-7 with four, as close as sums in
-// registers).
-template <int RP>
-struct Sums {
-  static constexpr int kSums = RP <= 32 ? 8 : (RP <= 64 ? 4 : 2);
-  static constexpr int kTmem = kSums * RP;  // two CTAs to an SM have room, three for RP = 16
-};
 // Adds 16 columns from tensor memory.
 __device__ __forceinline__ void add_sums16(uint32_t tmem, float (&v)[16]) {
   uint32_t w[16];
@@ -769,18 +759,54 @@ __device__ __forceinline__ void add_sums16(uint32_t tmem, float (&v)[16]) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
 }
-// 16 columns of the first n accumulators, to dst.
+// A long sum is dealt to kSums accumulators of RP columns each in tensor memory,
+// joined here in order: the tensor cores add with truncation, whose drift grows
+// with the number of additions into one accumulator (u of 8192 columns: over
+// 1.4e-6 of its norm off with one, 2.4e-7 with four, as close as sums in
+// registers).  Where a CTA's share is longer than kRound chunks, so many at a time
+// are added to RP more columns, in registers on the way: no accumulator takes
+// more than 48 additions (with as many as there were, u of 8192 columns, of more
+// tokens than leave a cluster for a tile, was 1.1e-6 off at rank 16, 2.3e-6 at 64
+// and 4.6e-6 at 128).
 template <int RP>
-__device__ __forceinline__ void read_sums16(uint32_t tmem, int n, float* dst) {
-  float v[16];
+struct Sums {
+  static constexpr int kSums = RP <= 16 ? 8 : 256 / RP - 1;
+  static constexpr int kTotal = kSums * RP;  // the rounds' columns
+  static constexpr int kTmem = 256;          // two CTAs to an SM have room
+  static constexpr int kRound = 8 * kSums;  // chunks
+  // Rounds that have ended before the last one, of n chunks.
+  static __device__ __forceinline__ int rounds(int n) { return n > 0 ? (n - 1) / kRound : 0; }
+  // After a round: its sums to those of the rounds before (`more`: there are some).
+  static __device__ __forceinline__ void end_round(uint32_t tmem, bool more) {
+#pragma unroll 1
+    for (int c = 0; c < RP; c += 16) {
+      float v[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = 0.f;
+      for (int e = 0; e < 16; ++e) v[e] = 0.f;
 #pragma unroll
-  for (int k = 0; k < Sums<RP>::kSums; ++k)
-    if (k < n) add_sums16(tmem + k * RP, v);
+      for (int k = 0; k < kSums; ++k) add_sums16(tmem + k * RP + c, v);
+      if (more) add_sums16(tmem + kTotal + c, v);
+      uint32_t w[16];
 #pragma unroll
-  for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-}
+      for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e]);
+      tmem_st16(tmem + kTotal + c, w);
+    }
+    tmem_wait_st();
+  }
+  // 16 columns of all of n chunks, to dst.
+  static __device__ __forceinline__ void read16(uint32_t tmem, int n, float* dst) {
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+    const int ended = rounds(n), last = n - ended * kRound;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k)
+      if (k < last) add_sums16(tmem + k * RP, v);
+    if (ended > 0) add_sums16(tmem + kTotal, v);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // u = W x for a tile of 128 tokens of one adapter
@@ -803,7 +829,7 @@ struct DownTile {
   static_assert(kTileRows * kPitch * 4 <= kRing, "the sums reuse the ring");
   using Ctl = Control<kStages>;
   static constexpr int kSmem = kRing + static_cast<int>(sizeof(Ctl));
-  static constexpr int kSums = Sums<RP>::kSums, kTmem = Sums<RP>::kTmem;
+  using Acc = Sums<RP>;
 };
 
 // A CTA's share of the sums of its cluster into the rows of u that the tile's
@@ -847,6 +873,7 @@ struct DownSorted {
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__ DownSorted ps) {
   using Cfg = DownTile<RP, TRANS>;
+  using Acc = typename Cfg::Acc;
   constexpr int S = Cfg::kStages;
   extern __shared__ __align__(1024) uint8_t ring[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
@@ -875,7 +902,7 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
     return;
   }
   if (warp == 0) {
-    tmem_alloc(&ctl.tmem, Cfg::kTmem);
+    tmem_alloc(&ctl.tmem, Acc::kTmem);
     tmem_relinquish();
   }
   const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
@@ -945,12 +972,22 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
   for (; c < n; ++c) {
     fence_proxy_async_smem();
     if (__syncthreads_or(!ok)) break;  // stage c is there for all (or the CTA gives up together)
+    const int of_round = c % Acc::kRound;
+    if (c > 0 && of_round == 0) {  // a round has ended
+      wait_done(c - 1);
+      tc_fence_after();
+      if (ok && warp < 4) Acc::end_round(tmem + ((warp & 3) * 32u << 16), c > Acc::kRound);
+      tc_fence_before();
+      if (__syncthreads_or(!ok)) break;
+      tc_fence_after();
+    }
     if (tid == 0) {
       const uint32_t at = ring_at + (c % S) * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
 #pragma unroll
       for (int s = 0; s < kChunk / 16; ++s)
-        mma_f16(tmem + (c % Cfg::kSums) * RP, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
-                mma_shape(RP, false, TRANS), (c >= Cfg::kSums || s > 0) ? 1u : 0u);
+        mma_f16(tmem + (of_round % Acc::kSums) * RP, Cfg::X::along_pieces(at, s),
+                TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s), mma_shape(RP, false, TRANS),
+                (of_round >= Acc::kSums || s > 0) ? 1u : 0u);
       tc_commit(&ctl.done[c % S]);
     }
     if (c + S - 1 < n) {
@@ -973,12 +1010,12 @@ __global__ void __launch_bounds__(256) adapter_down_tile(const __grid_constant__
       float* dst = sums + ((warp & 3) * 32 + lane) * Cfg::kPitch + (warp >> 2) * kHalf;
       const uint32_t src = tmem + ((warp & 3) * 32u << 16) + (warp >> 2) * kHalf;
 #pragma unroll
-      for (int j = 0; j < kHalf; j += 16) read_sums16<RP>(src + j, c, dst + j);
+      for (int j = 0; j < kHalf; j += 16) Acc::read16(src + j, c, dst + j);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, Cfg::kTmem);
+  if (warp == 0) tmem_dealloc(tmem, Acc::kTmem);
   write_sums<RP>(p.u, p.R, ps.o.perm + tile.start, tile.count, sums, rank, cs, 256);
 }
 
@@ -1702,7 +1739,7 @@ template <int RP, bool TRANS>
 struct DownTma : DownTile<RP, TRANS> {
   using Base = DownTile<RP, TRANS>;
   struct Ctl {
-    uint64_t full[Base::kStages], empty[Base::kStages], done;
+    uint64_t full[Base::kStages], empty[Base::kStages], done, ended;
     uint32_t tmem;
     int abort_flag;
   };
@@ -1725,6 +1762,7 @@ struct DownTmaArgs {
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ DownTmaArgs ps) {
   using Cfg = DownTma<RP, TRANS>;
+  using Acc = typename Cfg::Acc;
   constexpr int S = Cfg::kStages, kHelpers = 128;
   extern __shared__ __align__(1024) uint8_t ring[];
   typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(ring + Cfg::kRing);
@@ -1747,11 +1785,12 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
       mbar_init(&ctl.empty[i], 1);
     }
     mbar_init(&ctl.done, 1);
+    mbar_init(&ctl.ended, kHelpers);
     ctl.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&ctl.tmem, Cfg::kTmem);
+    tmem_alloc(&ctl.tmem, Acc::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -1766,7 +1805,7 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_poll(bar, parity & 1u, ps.w.timeout_ns, &ctl.abort_flag, ps.w.status, kSiteDown);
   };
-  int c = 0;
+  int c = 0, ends = 0;  // chunks; rounds that have ended, before the last one (of the lane that issues the MMAs)
   if (warp == 0) {
     if (lane == 0) {
       for (; c < n; ++c) {
@@ -1783,30 +1822,55 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
+      int of_round = 0;
       for (; c < n; ++c) {
         const int st = c % S;
+        if (of_round == Acc::kRound) {  // a round has ended
+          tc_commit(&ctl.done);
+          ++ends;
+          if (!wait(&ctl.ended, ends - 1)) break;
+          tc_fence_after();
+          of_round = 0;
+        }
         if (!wait(&ctl.full[st], c / S)) break;
         fence_proxy_async_smem();  // what the helpers' copies wrote
         tc_fence_after();
         const uint32_t at = ring_at + st * Cfg::kStageBytes, wt = at + Cfg::kXBytes;
 #pragma unroll
         for (int s = 0; s < kChunk / 16; ++s)
-          mma_f16(tmem + (c % Cfg::kSums) * RP, Cfg::X::along_pieces(at, s), TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s),
-                  mma_shape(RP, false, TRANS), (c >= Cfg::kSums || s > 0) ? 1u : 0u);
+          mma_f16(tmem + (of_round % Acc::kSums) * RP, Cfg::X::along_pieces(at, s),
+                  TRANS ? Cfg::W::along_rows(wt, s) : Cfg::W::along_pieces(wt, s), mma_shape(RP, false, TRANS),
+                  (of_round >= Acc::kSums || s > 0) ? 1u : 0u);
+        ++of_round;
         tc_commit(&ctl.empty[st]);
       }
       tc_commit(&ctl.done);
     }
     __syncwarp();
-  } else if (!run || !ps.wtma) {
+  } else {
+    // before a round's first chunk: the sums of the round before
+    auto end_round = [&](int chunk) {
+      const int r = chunk / Acc::kRound - 1;
+      if (!__all_sync(0xFFFFFFFFu, wait(&ctl.done, r))) return false;
+      tc_fence_after();
+      Acc::end_round(tmem + ((warp & 3) * 32u << 16), r > 0);
+      tc_fence_before();
+      mbar_arrive(&ctl.ended);
+      return true;
+    };
+    const bool copies = !run || !ps.wtma;  // else there are only rounds to end
     const int i = tid - 64;
     const bf16* w = p.w + static_cast<int64_t>(tile.adapter) * p.R * p.C;
     const bf16* xr[8];  // piece i % 8 of rows i / 8 + 16 j; rows past the tile repeat its last one
+    if (copies) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) xr[j] = p.x + ps.o.perm[tile.start + min((i >> 3) + 16 * j, tile.count - 1)] * p.ld;
-    for (; c < n; ++c) {
+      for (int j = 0; j < 8; ++j) xr[j] = p.x + ps.o.perm[tile.start + min((i >> 3) + 16 * j, tile.count - 1)] * p.ld;
+    }
+    for (c = copies ? 0 : Acc::kRound; c < n; c += copies ? 1 : Acc::kRound) {
+      if (c > 0 && c % Acc::kRound == 0 && !end_round(c)) break;
+      if (!copies) continue;
       const int st = c % S;
-      if (c >= S && !wait(&ctl.empty[st], c / S - 1)) break;
+      if (!__all_sync(0xFFFFFFFFu, c < S || wait(&ctl.empty[st], c / S - 1))) break;
       const uint32_t at = ring_at + st * Cfg::kStageBytes;
       const int64_t k = (c_begin + c) * kChunk;
       if (!run) {
@@ -1825,10 +1889,13 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
   }
   c = __shfl_sync(0xFFFFFFFFu, c, 0);
   __syncthreads();
-  wait(&ctl.done, 0);
-  if (ctl.abort_flag && warp == 0) {  // gave up: this CTA's MMAs and copies in flight, bounded again
+  wait(&ctl.done, Acc::rounds(n));
+  if (ctl.abort_flag && warp == 1 && lane == 0) {  // gave up: this CTA's MMAs ...
     int never = 0;
-    mbar_wait(&ctl.done, 0u, ps.w.timeout_ns, &never, ps.w.status, kSiteDown);
+    mbar_wait(&ctl.done, static_cast<uint32_t>(ends) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteDown);
+  }
+  if (ctl.abort_flag && warp == 0) {  // ... and copies in flight, bounded again
+    int never = 0;
     for (int j = c > S ? c - S : 0; j < c; ++j)
       mbar_wait(&ctl.full[j % S], static_cast<uint32_t>(j / S) & 1u, ps.w.timeout_ns, &never, ps.w.status, kSiteDown);
   }
@@ -1839,11 +1906,11 @@ __global__ void __launch_bounds__(192) adapter_down_tma(const __grid_constant__ 
     const int q = warp & 3;  // the quarter of tensor memory that this warp can read
     float* dst = sums + (q * 32 + lane) * Cfg::kPitch;
 #pragma unroll
-    for (int j = 0; j < RP; j += 16) read_sums16<RP>(tmem + (q * 32u << 16) + j, n, dst + j);
+    for (int j = 0; j < RP; j += 16) Acc::read16(tmem + (q * 32u << 16) + j, n, dst + j);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, Cfg::kTmem);
+  if (warp == 1) tmem_dealloc(tmem, Acc::kTmem);
   write_sums<RP>(p.u, p.R, ps.o.perm + tile.start, tile.count, sums, rank, cs, 192);
 }
 

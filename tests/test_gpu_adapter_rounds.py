@@ -63,3 +63,31 @@ def test_long_sums_of_one_adapter(T, K, N, R, L, x_code):
     _, ha, hb = bsmm.adapters_backward(dy, x, a, b, ids, u, scaling=scaling, grad_dtype=torch.bfloat16, **kw)
     assert _rel(ha[k], wa) < 2.0 ** -9 and _rel(hb[k], wb) < 2.0 ** -9
     assert bsmm.check_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("T,K", [(20000, 8192), (20000, 8191), (40000, 16384), (24000, 6000)])
+@pytest.mark.parametrize("R", [16, 24, 64, 128])
+@pytest.mark.parametrize("order", ["runs", "mixed"])
+def test_long_contractions(T, K, R, order):
+    """u of so many tokens that a tile has one CTA, which ends its rounds over all
+    of K: 48 additions to an accumulator, as for the gradients.  Consecutive
+    tokens, whose rows come by TMA alone, and scattered ones."""
+    bsmm = _bsmm()
+    N, L = 64, 2
+    g = torch.Generator(device="cuda").manual_seed(T + K + R)
+    x, b = (torch.randn(*s, device="cuda", generator=g).bfloat16() for s in ((T, K), (L, N, R)))
+    a = (torch.randn(L, R, K, device="cuda", generator=g) * K ** -0.5).bfloat16()
+    ids = (torch.arange(T, device="cuda") * L // T if order == "runs" else torch.arange(T, device="cuda") % L).int()
+    out, u = bsmm.adapters(x, a, b, ids, out_dtype=torch.float32)
+    want = torch.empty(T, R, dtype=torch.float64, device="cuda")
+    for k in range(L):
+        want[ids == k] = x[ids == k].double() @ a[k].double().t()
+    assert _rel(u, want) < 1e-6
+    # d, seen through dA (x of FP8 adds its own part: 3e-7)
+    dy, db = x, a.transpose(1, 2).contiguous()  # N = K here
+    small, s = bsmm.quantize(torch.randn(T, 64, device="cuda", generator=g), (1, 32), "e4m3", "ue8m0")
+    x64 = (small.view(torch.float8_e4m3fn).float() * torch.exp2(s.float() - 127).repeat_interleave(32, 1)).double()
+    _, da, _ = bsmm.adapters_backward(dy, small, b[:, :, :].transpose(1, 2).contiguous(), db, ids, u, x_scales=s)
+    for k in range(L):
+        assert _rel(da[k], want[ids == k].t() @ x64[ids == k]) < 1e-6
+    assert bsmm.check_device_status()[0] == 0
