@@ -759,13 +759,14 @@ __device__ __forceinline__ void add_sums16(uint32_t tmem, float (&v)[16]) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(w[e]);
 }
+
 // A long sum is dealt to kSums accumulators of RP columns each in tensor memory,
 // joined here in order: the tensor cores add with truncation, whose drift grows
 // with the number of additions into one accumulator (u of 8192 columns: over
 // 1.4e-6 of its norm off with one, 2.4e-7 with four, as close as sums in
 // registers).  Where a CTA's share is longer than kRound chunks, so many at a time
 // are added to RP more columns, in registers on the way: no accumulator takes
-// more than 48 additions (with as many as there were, u of 8192 columns, of more
+// more than 32 additions (with as many as there were, u of 8192 columns, of more
 // tokens than leave a cluster for a tile, was 1.1e-6 off at rank 16, 2.3e-6 at 64
 // and 4.6e-6 at 128).
 template <int RP>
@@ -1342,17 +1343,19 @@ struct GradTile {
   // memory three times: 8192 tokens, 8192 columns, rank 16, 73 us).  Blocks take
   // turns at the sets of accumulators.  Where a set is too wide for two of them
   // the terms go one by one, the lower ones to an accumulator of their own.
-  // Binary32 gradients of many blocks add each round's sets to RP more columns,
-  // in registers on the way, so that no accumulator takes more than 48 additions
-  // (64 of them left dB 1.0e-6 of its norm off; 48, 6.5e-7 at most).
+  // Binary32 gradients of many blocks add each round's accumulators to RP more
+  // columns, in registers on the way, so that none takes more than 32 additions
+  // (64 of them left dB 1.0e-6 of its norm off, 48 7.5e-7, 32 4.8e-7 in the same
+  // time), the lower terms', 2^-8 as large, 128 (kept on over all 1025 blocks of
+  // 65600 tokens it left dB of rank 128 1.1e-6 off).
   static constexpr bool kWide = TERMS * RP <= 128, kRounds = TERMS == 3;
   static constexpr int kTmem = RP <= 16 && !kRounds ? 128 : (RP == 128 && kRounds ? 512 : 256);
   static constexpr int kSetCols = kWide ? TERMS * RP : RP;
   static constexpr int kSets = (kTmem - (kRounds ? RP : 0) - (kWide ? 0 : RP)) / kSetCols;
   static constexpr int kLower = kSets * kSetCols, kTotal = kTmem - RP;  // columns: the lower terms', the rounds'
-  static constexpr int kRound = 12 * kSets;                             // blocks
-  // Block b, the n-th of its round.
-  static __device__ __forceinline__ void block(uint32_t tmem, int b, int n, uint32_t x, uint32_t coef) {
+  static constexpr int kRound = 8 * kSets;                              // blocks
+  // The n-th block of a round.
+  static __device__ __forceinline__ void block(uint32_t tmem, int n, uint32_t x, uint32_t coef) {
     const uint32_t d = tmem + (n % kSets) * kSetCols;
     if constexpr (kWide) {
 #pragma unroll
@@ -1366,11 +1369,12 @@ struct GradTile {
         for (int s = 0; s < kGradRows / 16; ++s)
           mma_f16(k == 0 ? d : tmem + kLower, X::along_rows(x, s), Coef::along_rows(coef + k * Image::kTermBytes, s),
                   mma_shape(RP, true, true),
-                  (s > 0 || (k == 0 ? n >= kSets : b > 0 || k < TERMS - 1)) ? 1u : 0u);
+                  (s > 0 || (k == 0 ? n >= kSets : n > 0 || k < TERMS - 1)) ? 1u : 0u);
     }
   }
   // 16 columns of a round's n blocks.
   static __device__ __forceinline__ void add_round16(uint32_t tmem, int n, float (&v)[16]) {
+    if (!kWide && n > 0) add_sums16(tmem + kLower, v);
 #pragma unroll
     for (int k = kWide ? TERMS - 1 : 0; k >= 0; --k)
 #pragma unroll
@@ -1379,7 +1383,7 @@ struct GradTile {
   }
   // After a round: its sums to those of the rounds before (`more`: there are some).
   static __device__ __forceinline__ void end_round(uint32_t tmem, bool more) {
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < RP; c += 16) {
       float v[16];
 #pragma unroll
@@ -1398,7 +1402,6 @@ struct GradTile {
     float v[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = 0.f;
-    if (!kWide && b > 0) add_sums16(tmem + kLower, v);
     add_round16(tmem, b - rounds * kRound, v);
     if (rounds > 0) add_sums16(tmem + kTotal, v);
 #pragma unroll
@@ -1634,7 +1637,7 @@ __global__ void __launch_bounds__(256) adapter_grads(const __grid_constant__ Gra
     if (tid == 0) {
       const uint32_t xt = ring_at + (kept ? b & 1 : b % S) * Cfg::kXBytes;
       const uint32_t ct = coef_at + (b % S) * Cfg::kCoefBytes;
-      Cfg::block(tmem, b, n, xt, ct);
+      Cfg::block(tmem, n, xt, ct);
       tc_commit(&ctl.done[b & 1]);
     }
     if (b > 0) ok = wait_done(b - 1) && ok;
@@ -2412,7 +2415,7 @@ __global__ void __launch_bounds__(64 + kGradHelpers, GradTma<RP, TERMS>::kReside
         tc_fence_after();
         const uint32_t at = ring_at + st * stage_bytes, ct = at + coef_off;
         const uint32_t xt = kept ? smem_u32(ring) + (b % ND) * Cfg::kXBytes : at;
-        Cfg::block(tmem, b, n, xt, ct);
+        Cfg::block(tmem, n, xt, ct);
         tc_commit(&ctl.empty[st]);
         ++b;
       }

@@ -1,7 +1,7 @@
 """Gradients of long sums: all tokens of one adapter, so many that every CTA
-ends several rounds of its accumulators (a round is 60 blocks of 64 tokens for
-ranks up to 16 and 24 beyond, and a cluster of at most 8 CTAs shares the
-blocks).
+ends several rounds of its accumulators (a round is at most 60 blocks of 64
+tokens for ranks up to 16 and 24 beyond, and a cluster of at most 8 CTAs shares
+the blocks); and contractions over many columns.
 
 The 2-norm of a binary32 gradient's error is held to 1e-6 of its norm.  The
 tensor cores cut off what does not fit: an addition loses 2^-24 of the running
@@ -65,12 +65,32 @@ def test_long_sums_of_one_adapter(T, K, N, R, L, x_code):
     assert bsmm.check_device_status()[0] == 0
 
 
+@pytest.mark.parametrize("T,K,N", [(262144, 512, 512), (262144, 511, 513)])
+def test_lower_terms_of_high_ranks(T, K, N):
+    """Ranks above 32 sum the coefficients' lower terms, 2^-8 of them, in an
+    accumulator of their own, which has to end its rounds too: here a CTA takes
+    1024 blocks or more of the one adapter in use, 8200 additions without rounds."""
+    bsmm = _bsmm()
+    R, L = 128, 8
+    g = torch.Generator(device="cuda").manual_seed(N)
+
+    def rnd(*s, k=1.0):
+        return (torch.randn(*s, device="cuda", generator=g) * k).bfloat16()
+
+    x, dy, a, b = rnd(T, K), rnd(T, N), rnd(L, R, K, k=K ** -0.5), rnd(L, N, R, k=R ** -0.5)
+    u = torch.randn(T, R, device="cuda", generator=g)
+    ids = torch.full((T,), 2, dtype=torch.int32, device="cuda")
+    _, da, db = bsmm.adapters_backward(dy, x, a, b, ids, u)
+    assert _rel(da[2], (dy.double() @ b[2].double()).t() @ x.double()) < 1e-6
+    assert _rel(db[2], dy.double().t() @ u.double()) < 1e-6
+
+
 @pytest.mark.parametrize("T,K", [(20000, 8192), (20000, 8191), (40000, 16384), (24000, 6000)])
 @pytest.mark.parametrize("R", [16, 24, 64, 128])
 @pytest.mark.parametrize("order", ["runs", "mixed"])
 def test_long_contractions(T, K, R, order):
     """u of so many tokens that a tile has one CTA, which ends its rounds over all
-    of K: 48 additions to an accumulator, as for the gradients.  Consecutive
+    of K: at most 48 additions to an accumulator, as for the gradients.  Consecutive
     tokens, whose rows come by TMA alone, and scattered ones."""
     bsmm = _bsmm()
     N, L = 64, 2
