@@ -1962,7 +1962,7 @@ struct TileWalk {
 // One CTA to an SM, each with an equal stretch of all tiles' chunks, so that
 // loads and stores go on at a steady rate from the first tile to the last (as
 // CTAs of a tile and 16 chunks each, in two waves, 8192 tokens of 8192 columns
-// and rank 64 took 61 us; this took 55, and takes 57, 4.9 TB/s in and out, since
+// and rank 64 took 61 us; this took 55, and takes 58, 4.8 TB/s in and out, since
 // u has three terms and signs for infinities).  Warp 0 feeds base and the
 // weights, warp 1 issues the MMAs, warps 2 and 3 are the helpers, which gather a
 // tile's rows of base that are not consecutive; warps 4..7 and 8..11 take turns
