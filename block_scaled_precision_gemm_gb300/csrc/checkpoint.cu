@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "blockquant.cuh"
 #include "internal.h"
@@ -85,15 +86,26 @@ __device__ __forceinline__ void silu2(float2 g, float2& f, float2& df) {
   if constexpr (SLOPE) df = __ffma2_rn(f, __fmul2_rn(e, p), p);
 }
 // For any g (f and derivative of the one, then of the other): below -64, p is
-// exp(g) to 2^-92 of it, and goes 64 powers of two higher until the last product.
+// exp(g) to 2^-92 of it, and goes 64 powers of two higher until the last product;
+// above 64 it is 1.  The exponents are those of g cut to [-512, 64], where p is
+// zero and 1 already: the largest numbers' are infinite.  A gate of minus infinity
+// (the lowest bf16 number becomes one in an E4M3 checkpoint) counts as the lowest
+// number: act is zero there, as its limit is.
 __device__ __noinline__ float4 silu2_wide(float2 g) {
   float2 f, df, t, rest;
-  silu2<true>(make_float2(fmaxf(g.x, -80.f), fmaxf(g.y, -80.f)), f, df);
-  exponent2(g, t, rest);
+  silu2<true>(make_float2(fminf(fmaxf(g.x, -64.f), 64.f), fminf(fmaxf(g.y, -64.f), 64.f)), f, df);
+  exponent2(make_float2(fmaxf(fminf(g.x, 0.f), -512.f), fmaxf(fminf(g.y, 0.f), -512.f)), t, rest);
   float2 q = make_float2(ex2_approx(64.f + t.x), ex2_approx(64.f + t.y));
   q = __ffma2_rn(q, rest, q);
-  return make_float4(g.x < -64.f ? g.x * q.x * 0x1p-64f : f.x, g.x < -64.f ? fmaf(g.x, q.x, q.x) * 0x1p-64f : df.x,
-                     g.y < -64.f ? g.y * q.y * 0x1p-64f : f.y, g.y < -64.f ? fmaf(g.y, q.y, q.y) * 0x1p-64f : df.y);
+  auto pick = [](float x, float p64, float fx, float dx) {
+    if (x < -64.f) {
+      x = fmaxf(x, -FLT_MAX);
+      return make_float2(x * p64 * 0x1p-64f, fmaf(x, p64, p64) * 0x1p-64f);
+    }
+    return x > 64.f ? make_float2(x, 1.f) : make_float2(fx, dx);
+  };
+  const float2 a = pick(g.x, q.x, f.x, df.x), b = pick(g.y, q.y, f.y, df.y);
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // GELU, f = g Phi(g) and its derivative Phi + g times the density, of a pair.
@@ -125,11 +137,12 @@ __device__ __forceinline__ void gelu2(float2 g, float2& f, float2& df) {
 // For any g: with E = exp(-g^2 / 2) the tail beyond |g| is E erfcx(|g| / sqrt 2)
 // / 2.  E is the square of exp(-g^2 / 4), times what the rounding of g^2 left; the
 // lower tail's products take its two factors last, so that nothing is subnormal
-// before the result is.
+// before the result is.  Minus infinity is as in silu2_wide.
 __device__ __noinline__ float2 gelu_wide(float g) {
+  if (g < -FLT_MAX) g = -FLT_MAX;
   const float m = fminf(fabsf(g), 20.f), mm = m * m;  // beyond, E is zero
   const float e1 = expf(-0.25f * mm), e2 = e1 * fmaf(-0.5f, fmaf(m, m, -mm), 1.f);
-  const float half = 0.5f * erfcxf(fabsf(g) * 0.70710678118654752f), density = 0.39894228040143268f * g;
+  const float half = 0.5f * erfcxf(fabsf(g) * 0.70710678118654752f), density = 0.39894228040143268f * copysignf(m, g);
   const float phi = fmaf(-half * e1, e2, 1.f);  // of |g|
   return g < 0.f ? make_float2(g * half * e1 * e2, (half + density) * e1 * e2)
                  : make_float2(g * phi, fmaf(density * e1, e2, phi));

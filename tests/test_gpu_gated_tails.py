@@ -36,7 +36,7 @@ def act64(g, act):
 
 def inside(got, ref, tol, what):
     spacing = 2.0 ** -133 if got.dtype == torch.bfloat16 else 0.0
-    bad = ~((got.double() - ref).abs() <= tol + spacing / 2)
+    bad = ~(((got.double() - ref).abs() <= tol + spacing / 2) | (got.double() == ref))  # (infinities are equal)
     assert not bad.any(), (what, int(bad.sum()), [float(v[bad].flatten()[0]) for v in (got.double(), ref, tol)])
 
 
@@ -100,3 +100,43 @@ def test_forward(act, low, high, code, scale, dtype):
     s = torch.exp2(qs.cpu().double() - 127).repeat_interleave(32, 1)
     got = torch.from_numpy(F.decode(q.cpu().numpy(), "e4m3").astype(np.float64)) * s
     inside(got, ref, 2.0 ** -4 * (1 + 2.0 ** -12) * ref.abs() + tiny + s * 2.0 ** -10, "e4m3")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_largest_numbers(act, dtype):
+    """Gates up to bfloat16's largest magnitude, as masks write them, and the
+    infinities that an E4M3 checkpoint makes of the largest: zero below, the
+    identity above, forward and backward, beside ordinary numbers."""
+    bsmm = _bsmm()
+    top = (2 - 2.0 ** -7) * 2.0 ** 127
+    special = torch.tensor([-top, -2.5e38, -2.3e38, -1e38, -1e20, -600.0, top, 2.5e38, 2.3e38, 1e38, 1e20, 600.0])
+    I = 32 * len(special)
+    gate = torch.randn(4, len(special), 32, generator=torch.Generator().manual_seed(3))
+    gate[:, :, 7] = special
+    gate = gate.view(4, I).to(dtype)
+    up = torch.full((4, I), 0.5).to(dtype)
+    f = act64(gate.double(), act)[0]
+    f[gate < -500] = 0
+    f[gate > 500] = gate[gate > 500].double()
+    x = torch.cat([gate, up], 1).cuda()
+    for code, scale in ((None, "f32"), ("int8", "f32"), ("e4m3", "ue8m0")):
+        h, _, codes, scales = bsmm.gated_act(x, act=act, h_type="bf16", code=code, scale=scale)
+        inside(h.cpu(), f * 0.5, (2.0 ** -8 + 2.0 ** -15) * (f * 0.5).abs() + TINY, "h")
+    # every block has one of them: in the checkpoint they stand beside zeros
+    dh = torch.full((4, I), 0.25, device="cuda").to(dtype)
+    d, h = bsmm.gated_act_backward(dh, codes, scales, act=act, code=code, scale=scale, return_h=True)
+    v = torch.from_numpy(F.decode(codes.cpu().numpy(), code).astype(np.float64)).view(4, -1, 32)
+    v = (v * torch.exp2(scales.cpu().double() - 127)[..., None]).view(4, 2 * I).float().double()
+    assert bool(v.isinf().any())  # E4M3 rounds the largest numbers up to 2^128
+    g, u = v[:, :I], v[:, I:]
+    big = g.abs() > 500
+    small = torch.where(big, torch.zeros_like(g), g)
+    f, p, q = act64(small, act)
+    f = torch.where(big, g.clamp(min=0), f)
+    slope, terms = (torch.where(big, (g > 0).double(), t) for t in (p + q, p.abs() + q.abs()))
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    out = d.cpu()
+    inside(out[:, I:], 0.25 * f, (REL + half) * (0.25 * f).abs() + TINY, "d_up")
+    inside(out[:, :I], 0.25 * u * slope, 0.25 * u * (REL * terms + half * slope.abs()) + TINY, "d_gate")
+    inside(h.cpu(), f * u, (REL + 2.0 ** -8) * (f * u).abs() + TINY, "h again")
