@@ -102,7 +102,7 @@ __device__ __noinline__ float4 silu2_wide(float2 g) {
       x = fmaxf(x, -FLT_MAX);
       return make_float2(x * p64 * 0x1p-64f, fmaf(x, p64, p64) * 0x1p-64f);
     }
-    return x > 64.f ? make_float2(x, 1.f) : make_float2(fx, dx);
+    return x <= 64.f ? make_float2(fx, dx) : make_float2(x, x > 64.f ? 1.f : x);  // (a NaN stays one)
   };
   const float2 a = pick(g.x, q.x, f.x, df.x), b = pick(g.y, q.y, f.y, df.y);
   return make_float4(a.x, a.y, b.x, b.y);

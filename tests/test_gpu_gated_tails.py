@@ -140,3 +140,32 @@ def test_the_largest_numbers(act, dtype):
     inside(out[:, I:], 0.25 * f, (REL + half) * (0.25 * f).abs() + TINY, "d_up")
     inside(out[:, :I], 0.25 * u * slope, 0.25 * u * (REL * terms + half * slope.abs()) + TINY, "d_gate")
     inside(h.cpu(), f * u, (REL + 2.0 ** -8) * (f * u).abs() + TINY, "h again")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("largest", [1.0, 300.0])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nan_stays_where_it_is(act, largest, dtype):
+    """A NaN gate or up gives NaN in its own place and nowhere else, beside large
+    numbers or not; so does a NaN code of a checkpoint."""
+    bsmm = _bsmm()
+    M, I = 3, 256
+    g = torch.Generator().manual_seed(4)
+    x = torch.rand(M, 2 * I, generator=g).to(dtype)
+    x[:, ::32] = largest
+    x[0, 5], x[1, 70], x[2, I + 9] = float("nan"), float("nan"), float("nan")
+    want = torch.zeros(M, I, dtype=torch.bool)
+    want[0, 5] = want[1, 70] = want[2, 9] = True
+    for code, scale in ((None, "f32"), ("int8", "f32"), ("e5m2", "ue8m0")):
+        h, _, _, _ = bsmm.gated_act(x.cuda(), act=act, h_type="bf16", code=code, scale=scale)
+        assert torch.equal(h.isnan().cpu(), want), code
+    clean = torch.nan_to_num(x.float(), nan=0.25).to(dtype)
+    _, _, codes, scales = bsmm.gated_act(clean.cuda(), act=act, code="e4m3", scale="ue8m0")
+    codes[0, 5], codes[1, 70], codes[2, I + 9] = 0x7F, 0x7F, 0x7F
+    dh = torch.rand(M, I, generator=g).to(dtype) + 0.5
+    d, h = bsmm.gated_act_backward(dh.cuda(), codes, scales, act=act, code="e4m3", scale="ue8m0", return_h=True)
+    assert torch.equal(h.isnan().cpu(), want)
+    nan = d.isnan().cpu()
+    assert torch.equal(nan[:, :I], want)  # d_gate takes both
+    want[2, 9] = False
+    assert torch.equal(nan[:, I:], want)  # d_up takes the gate
