@@ -509,7 +509,8 @@ bsmm_status bsmm_gated_act(const void* gate_up, bsmm_dtype x_type, int64_t M, in
  * each computed in binary32 and rounded once: act(g) and each of the two terms
  * that act'(g) is the sum of (p and g p (1 - p) for SiLU, p the logistic
  * function; the CDF and g times the density for GELU) is within 2^-20 of itself,
- * in the tails too.
+ * in the tails too.  A gate of minus infinity, which E4M3 codes make of the
+ * lowest numbers, has act(g) = act'(g) = 0, their limits; a NaN stays one.
  *
  *   dh [M, I] and d_gate_up [M, 2 I] of type d_type (F32 or BF16), contiguous.
  *   h        BF16 [M, I]: the down projection's input again, for its weight
