@@ -24,12 +24,16 @@ Entry points (see ``include/bsmm.h`` for the full contract):
 * :func:`linear_backward_checkpoint`  :func:`linear_backward` from an 8-bit X
 * :func:`adapters`, :func:`adapters_backward`  low-rank adapters of many
                           requests beside a shared projection
+* :func:`route`, :func:`expert_gemm`, :func:`expert_combine` and their
+                          backward calls: a mixture of MXFP8 experts
+* :func:`adamw`           AdamW over many tensors, states in 32 or 8 bits
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -40,6 +44,8 @@ __all__ = [
     "scale_atoms_size", "quantize_atoms", "gemm_atoms", "linear_backward_quantized",
     "gated_act", "gated_act_backward", "linear_backward_checkpoint", "adapters", "adapters_backward",
     "adapters_workspace_size", "adapters_backward_workspace_size",
+    "route", "route_backward", "expert_gemm", "expert_backward", "expert_combine", "expert_combine_backward", "adamw",
+    "route_workspace_size", "expert_backward_workspace_size",
     "set_wait_timeout_ns", "version",
     "F32", "BF16", "E4M3", "E5M2", "E2M1", "INT8", "SCALE_F32", "SCALE_UE8M0", "SCALE_UE4M3",
 ]
@@ -74,6 +80,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F64 = ctypes.c_double
 
 
 class _QuantizeJob(ctypes.Structure):
@@ -123,6 +130,16 @@ _SIGS = {
     "bsmm_adapters_backward_workspace_size": ([_I64, _I64, _I64], _SZ),
     "bsmm_adapters_backward": ([_I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _P, _P, _P, _P, _P,
                                 _I64, _P, _P, _P, _INT, _P, _SZ, _P], _INT),
+    "bsmm_route_workspace_size": ([_I64, _I64], _SZ),
+    "bsmm_route": ([_I64, _I64, _INT, _P, _INT, _I64, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P], _INT),
+    "bsmm_route_backward": ([_I64, _I64, _INT, _P, _INT, _I64, _INT, _P, _P, _P, _P, _P], _INT),
+    "bsmm_expert_gemm": ([_I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _P, _P], _INT),
+    "bsmm_expert_backward_workspace_size": ([_I64, _I64, _I64, _I64], _SZ),
+    "bsmm_expert_backward": ([_I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _INT, _P, _P, _P, _SZ, _P], _INT),
+    "bsmm_expert_combine": ([_I64, _I64, _INT, _I64, _P, _P, _P, _P, _INT, _P], _INT),
+    "bsmm_expert_combine_backward": ([_I64, _I64, _INT, _I64, _P, _INT, _P, _P, _P, _P, _P, _P], _INT),
+    "bsmm_adamw": ([_I64, _P, _P, _INT, _P, _INT, _P, _P, _INT, _P, _P, _P, _F64, _F64, _F64, _F64, _F64, _I64, _F64, _P,
+                    _P], _INT),
 }
 
 
@@ -979,3 +996,291 @@ def adapters_backward(dy, x, a, b, ids, u, scaling=None, dx_base=None, x_scales=
                                         workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)),
            "bsmm_adapters_backward")
     return dx, da, db
+
+
+# --------------------------------------------------------------------------- #
+# Mixture of experts                                                          #
+# --------------------------------------------------------------------------- #
+
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+_BF16 = (torch.bfloat16,)
+
+
+def _same_device(dev, **named):
+    for n, t in named.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
+
+
+def route_workspace_size(T, E) -> int:
+    return lib().bsmm_route_workspace_size(T, E)
+
+
+def route(logits, k, renormalize=True, weights=None, ids=None, offsets=None, rows=None, slots=None, workspace=None,
+          stream=None):
+    """The ``k`` experts of each token and the tokens' layout by expert.
+
+    ``logits`` [T, E] float32 or bfloat16, rows at any pitch.  Returns
+    ``(weights, ids, offsets, rows, slots)``: the softmax of the ``k`` largest
+    logits [T, k] float32 (over those, or without ``renormalize`` over all E),
+    their experts [T, k] int32 (-1 where nothing is left to choose), and the
+    (token, choice) pairs by expert: ``offsets`` [E + 1], ``rows`` [T k] (the
+    token of each slot) and ``slots`` [T, k] (the slot of each pair) int32."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D float32 or bfloat16 tensor [T, E]")
+    (T, E), k = logits.shape, int(k)
+    ld = _rows(logits, "logits", (T, E), _FLOATS)
+    outs = (("weights", weights, (T, k), _F32), ("ids", ids, (T, k), _I32), ("offsets", offsets, (E + 1,), _I32),
+            ("rows", rows, (T * k,), _I32), ("slots", slots, (T, k), _I32))
+    for n, t, shape, dtypes in outs:
+        if t is not None:
+            _want(t, n, shape, dtypes=dtypes)
+    if workspace is not None:
+        _want(workspace, "workspace")
+    dev = logits.device
+    if not _current(logits):
+        raise ValueError(f"logits is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    _same_device(dev, **{n: t for n, t, _, _ in outs}, workspace=workspace)
+    _on_device(**{n: t for n, t, _, _ in outs}, workspace=workspace)
+    if k < 0:
+        raise ValueError("k must not be negative")
+    weights, ids, offsets, rows, slots = (_empty(shape, dtypes[0], dev, stream) if t is None else t
+                                          for _, t, shape, dtypes in outs)
+    if workspace is None:
+        need = route_workspace_size(T, E)
+        if need:
+            workspace = _scratch(need, dev, stream)
+    _check(lib().bsmm_route(T, E, k, logits.data_ptr(), BF16 if logits.dtype is torch.bfloat16 else F32, ld,
+                            1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
+                            rows.data_ptr(), slots.data_ptr(), _at(workspace), _nbytes(workspace),
+                            _raw_stream(stream, dev)), "bsmm_route")
+    return weights, ids, offsets, rows, slots
+
+
+def route_backward(d_weights, logits, ids, weights, renormalize=True, d_logits=None, stream=None):
+    """Backward of :func:`route`: ``d_logits`` [T, E] of the logits' type."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D float32 or bfloat16 tensor [T, E]")
+    T, E = logits.shape
+    ld = _rows(logits, "logits", (T, E), _FLOATS)
+    _want(ids, "ids", dtypes=_I32)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must be an int32 tensor [{T}, k]")
+    k = ids.shape[1]
+    _want(weights, "weights", (T, k), dtypes=_F32)
+    _want(d_weights, "d_weights", (T, k), dtypes=_F32)
+    if d_logits is not None:
+        _want(d_logits, "d_logits", (T, E), dtypes=(logits.dtype,))
+    dev = _on_device(ids=ids, weights=weights, d_weights=d_weights, d_logits=d_logits)
+    _same_device(dev, logits=logits)
+    if d_logits is None:
+        d_logits = _empty((T, E), logits.dtype, dev, stream)
+    _check(lib().bsmm_route_backward(T, E, k, logits.data_ptr(), BF16 if logits.dtype is torch.bfloat16 else F32, ld,
+                                     1 if renormalize else 0, d_weights.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                                     d_logits.data_ptr(), _raw_stream(stream, dev)), "bsmm_route_backward")
+    return d_logits
+
+
+def expert_gemm(x, x_scales, w, w_atoms, offsets, rows=None, x_type="e4m3", w_type="e4m3", y=None, stream=None):
+    """``y[s] = w[e] @ x[rows[s]]`` for the slots ``offsets[e] <= s <
+    offsets[e + 1]`` of every expert ``e``, MXFP8: y [S, N] bfloat16.
+
+    ``x`` [X, K] codes with scale bytes ``x_scales`` [X, K / 32]; ``w``
+    [E, N, K] codes with ``w_atoms`` as :func:`quantize_atoms` writes them for
+    E batches; ``offsets`` [E + 1] and ``rows`` [S] int32 (None: slot s is row
+    s of x).  Slots of no expert are left as they are in ``y``."""
+    xt, wt = _code(x_type), _code(w_type)
+    _want(x, "x", itemsize=1)
+    _want(w, "w", itemsize=1)
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x and w must be code tensors [X, K] and [E, N, K]")
+    (X, K), (E, N) = x.shape, w.shape[:2]
+    _want(w, "w", (E, N, K))
+    _want(x_scales, "x_scales", itemsize=1)
+    if K % 32 == 0:  # else the library says why
+        _want(x_scales, "x_scales", (X, K // 32))
+        _want(w_atoms, "w_atoms", min_bytes=scale_atoms_size(E, N, K, wt, SCALE_UE8M0))
+    S = _expert_slots(offsets, rows, E, X)
+    if y is not None:
+        _want(y, "y", (S, N), dtypes=_BF16)
+    dev = _on_device(x=x, x_scales=x_scales, w=w, w_atoms=w_atoms, offsets=offsets, rows=rows, y=y)
+    if y is None:
+        y = _empty((S, N), torch.bfloat16, dev, stream)
+    _check(lib().bsmm_expert_gemm(S, X, E, N, K, x.data_ptr(), xt, x_scales.data_ptr(), w.data_ptr(), wt,
+                                  w_atoms.data_ptr(), offsets.data_ptr(), _at(rows), y.data_ptr(),
+                                  _raw_stream(stream, dev)), "bsmm_expert_gemm")
+    return y
+
+
+def _expert_slots(offsets, rows, E, X) -> int:
+    _want(offsets, "offsets", (E + 1,), dtypes=_I32)
+    if rows is None:
+        return X
+    _want(rows, "rows", dtypes=_I32)
+    if rows.dim() != 1:
+        raise ValueError("rows must be a 1-D int32 tensor [S]")
+    return rows.shape[0]
+
+
+def expert_backward_workspace_size(S, E, N, K) -> int:
+    return lib().bsmm_expert_backward_workspace_size(S, E, N, K)
+
+
+def expert_backward(dY, W, X, offsets, rows=None, fp8="e5m2", dX=None, dW=None, workspace=None, stream=None):
+    """:func:`linear_backward` by expert, from bfloat16 ``dY`` [S, N], ``W``
+    [E, N, K] and ``X`` [rows of x, K]: returns ``(dX, dW)``, ``dX`` [S, K] by
+    slot (:func:`expert_combine` without weights sums it by token) and ``dW``
+    [E, N, K], bfloat16."""
+    for t, n, dims in ((dY, "dY", 2), (W, "W", 3), (X, "X", 2)):
+        _want(t, n, dtypes=_BF16)
+        if t.dim() != dims:
+            raise ValueError("dY, W and X must be bfloat16 tensors [S, N], [E, N, K] and [rows, K]")
+    E, N, K = W.shape
+    _want(X, "X", (X.shape[0], K))
+    S = _expert_slots(offsets, rows, E, X.shape[0])
+    _want(dY, "dY", (S, N))
+    if dX is not None:
+        _want(dX, "dX", (S, K), dtypes=_BF16)
+    if dW is not None:
+        _want(dW, "dW", (E, N, K), dtypes=_BF16)
+    if workspace is not None:
+        _want(workspace, "workspace")
+    dev = _on_device(dY=dY, W=W, X=X, offsets=offsets, rows=rows, dX=dX, dW=dW, workspace=workspace)
+    if dX is None:
+        dX = _empty((S, K), torch.bfloat16, dev, stream)
+    if dW is None:
+        dW = _empty((E, N, K), torch.bfloat16, dev, stream)
+    if workspace is None:
+        workspace = _scratch(max(expert_backward_workspace_size(S, E, N, K), 1), dev, stream)
+    _check(lib().bsmm_expert_backward(S, X.shape[0], E, N, K, dY.data_ptr(), W.data_ptr(), X.data_ptr(),
+                                      offsets.data_ptr(), _at(rows), _code(fp8), dX.data_ptr(), dW.data_ptr(),
+                                      workspace.data_ptr(), _nbytes(workspace), _raw_stream(stream, dev)),
+           "bsmm_expert_backward")
+    return dX, dW
+
+
+def _combined(y, slots, weights):
+    _want(y, "y", dtypes=_BF16)
+    _want(slots, "slots", dtypes=_I32)
+    if y.dim() != 2 or slots.dim() != 2:
+        raise ValueError("y and slots must be a bfloat16 tensor [S, N] and an int32 tensor [T, k]")
+    (S, N), (T, k) = y.shape, slots.shape
+    if weights is not None:
+        _want(weights, "weights", (T, k), dtypes=_F32)
+    return S, N, T, k
+
+
+def expert_combine(y, slots, weights=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """``out[t] = sum over j of weights[t, j] * y[slots[t, j]]`` (weights None:
+    1; a slot outside y has no part): ``out`` [T, N] float32 or bfloat16."""
+    S, N, T, k = _combined(y, slots, weights)
+    dtype = out_dtype if out is None else out.dtype
+    if dtype not in _FLOATS:
+        raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {dtype}")
+    if out is not None:
+        _want(out, "out", (T, N))
+    dev = _on_device(y=y, slots=slots, weights=weights, out=out)
+    if out is None:
+        out = _empty((T, N), dtype, dev, stream)
+    _check(lib().bsmm_expert_combine(T, S, k, N, y.data_ptr(), slots.data_ptr(), _at(weights), out.data_ptr(),
+                                     BF16 if dtype is torch.bfloat16 else F32, _raw_stream(stream, dev)),
+           "bsmm_expert_combine")
+    return out
+
+
+def expert_combine_backward(d_out, y, slots, weights=None, dy=None, d_weights=None, stream=None):
+    """Backward of :func:`expert_combine`: returns ``(dy, d_weights)``, ``dy``
+    [S, N] bfloat16 (slots that do not occur are left as they are) and
+    ``d_weights`` [T, k] float32 (None without weights)."""
+    S, N, T, k = _combined(y, slots, weights)
+    _want(d_out, "d_out", (T, N), dtypes=_FLOATS)
+    if dy is not None:
+        _want(dy, "dy", (S, N), dtypes=_BF16)
+    if d_weights is not None:
+        _want(d_weights, "d_weights", (T, k), dtypes=_F32)
+    dev = _on_device(y=y, slots=slots, weights=weights, d_out=d_out, dy=dy, d_weights=d_weights)
+    if dy is None:
+        dy = _empty((S, N), torch.bfloat16, dev, stream)
+    if d_weights is None and weights is not None:
+        d_weights = _empty((T, k), torch.float32, dev, stream)
+    _check(lib().bsmm_expert_combine_backward(T, S, k, N, d_out.data_ptr(),
+                                              BF16 if d_out.dtype is torch.bfloat16 else F32, y.data_ptr(),
+                                              slots.data_ptr(), _at(weights), dy.data_ptr(), _at(d_weights),
+                                              _raw_stream(stream, dev)), "bsmm_expert_combine_backward")
+    return dy, d_weights
+
+
+# --------------------------------------------------------------------------- #
+# AdamW                                                                       #
+# --------------------------------------------------------------------------- #
+
+def _tensor_list(ts, name, sizes, dtypes=None, itemsize=None):
+    """A list of contiguous CUDA tensors of one type, on the current device:
+    their addresses and that type.  Whole lists are checked at a time, as an
+    optimizer's many small tensors spend their time on the host."""
+    for t in ts:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must hold torch.Tensors")
+    kinds = {t.dtype for t in ts}
+    if len(kinds) > 1:
+        raise ValueError(f"{name} must be of one type, got {' and '.join(sorted(str(k) for k in kinds))}")
+    dtype = next(iter(kinds), None)
+    if dtype is not None and dtypes is not None and dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
+    if dtype is not None and itemsize is not None and dtype.itemsize != itemsize:
+        raise ValueError(f"{name} must have {itemsize}-byte elements, got {dtype}")
+    if sizes is not None:
+        got = list(map(torch.Tensor.numel, ts))
+        if got != sizes:
+            if len(got) != len(sizes):
+                raise ValueError(f"{name} holds {len(got)} tensors, {len(sizes)} needed")
+            i = next(i for i in range(len(got)) if got[i] != sizes[i])
+            raise ValueError(f"{name}[{i}] holds {got[i]} numbers, {sizes[i]} needed")
+    here = set(map(torch.Tensor.get_device, ts))
+    if here and (-1 in here or here != {torch._C._cuda_getDevice()}):
+        raise ValueError(f"{name} must be CUDA tensors on the current device")
+    if not all(map(torch.Tensor.is_contiguous, ts)):
+        raise ValueError(f"{name} must be contiguous")
+    return array("Q", map(torch.Tensor.data_ptr, ts)), dtype
+
+
+def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=1.0, m_scales=None,
+          v_scales=None, copies=None, hyper=None, stream=None):
+    """One AdamW step on lists of tensors, in place, in one launch per 96.
+
+    ``params`` and ``grads`` float32 or bfloat16.  ``m`` and ``v`` float32, or
+    with ``m_scales`` and ``v_scales`` (float32, one per 128 numbers) E4M3 codes
+    of ``m`` and of ``sqrt(v)``; zeros start a run.  ``copies`` receives the
+    updated parameters in bfloat16.  ``hyper``, a float32 tensor ``(lr, step,
+    grad_scale)`` on the device, takes the place of those arguments when the
+    kernels run (a captured step's schedule)."""
+    params = list(params)
+    if any(not isinstance(t, torch.Tensor) for t in params):
+        raise TypeError("params must hold torch.Tensors")
+    sizes = list(map(torch.Tensor.numel, params))
+    if (m_scales is None) != (v_scales is None):
+        raise ValueError("m_scales and v_scales go together")
+    bits8 = m_scales is not None
+    pp, pt = _tensor_list(params, "params", None, _FLOATS)
+    gg, gt = _tensor_list(grads, "grads", sizes, _FLOATS)
+    mm, mt = _tensor_list(m, "m", sizes, None if bits8 else _F32, 1 if bits8 else None)
+    vv, vt = _tensor_list(v, "v", sizes, None if bits8 else _F32, 1 if bits8 else None)
+    ms = vs = cc = None
+    if bits8:
+        blocks = [(n + 127) // 128 for n in sizes]
+        ms, _ = _tensor_list(m_scales, "m_scales", blocks, _F32)
+        vs, _ = _tensor_list(v_scales, "v_scales", blocks, _F32)
+    if copies is not None:
+        cc, _ = _tensor_list(copies, "copies", sizes, _BF16)
+    if hyper is not None:
+        _want(hyper, "hyper", (3,), dtypes=_F32)
+        _on_device(hyper=hyper)
+    if not params:
+        return
+    n = array("q", sizes)
+    at = [None if a is None else a.buffer_info()[0] for a in (n, pp, gg, mm, vv, ms, vs, cc)]
+    _check(lib().bsmm_adamw(len(sizes), at[0], at[1], BF16 if pt is torch.bfloat16 else F32, at[2],
+                            BF16 if gt is torch.bfloat16 else F32, at[3], at[4], E4M3 if bits8 else F32, at[5], at[6],
+                            at[7], lr, betas[0], betas[1], eps, weight_decay, int(step), grad_scale, _at(hyper),
+                            _raw_stream(stream, params[0].device)), "bsmm_adamw")

@@ -2,6 +2,7 @@
 // factory and dispatch to the kernels.  No exception crosses this boundary.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdio>
 #include <cstring>
@@ -906,6 +907,199 @@ bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, i
                                   ids, scaling, u, dx_base, ld_dx, dx, dA, dB, grad_type == BSMM_BF16,
                                   static_cast<float*>(workspace), order, order + adapter_order_bytes(T, L, true)};
   return launched(launch_adapters_backward(r, reinterpret_cast<cudaStream_t>(stream)), "adapters backward launch");
+}
+
+namespace {
+bsmm_status route_sizes(int64_t T, int64_t E, int k, bsmm_dtype type, int64_t ld) {
+  if (T < 0 || E < 0 || k < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  if (type != BSMM_F32 && type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "logits_type must be F32 or BF16");
+  if (E < 1 || k < 1 || k > E) return fail(BSMM_ERR_SHAPE, "k must be between 1 and E");
+  if (E > kExpertsMax || k > 32) return fail(BSMM_ERR_UNSUPPORTED, "up to 1024 experts, up to 32 a token");
+  if (T > INT32_MAX / k) return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  if (T > 0 && ld < E) return fail(BSMM_ERR_SHAPE, "ld < E");
+  return BSMM_OK;
+}
+bsmm_status expert_sizes(int64_t S, int64_t X, int64_t E, int64_t N, int64_t K, bool by_rows) {
+  if (S < 0 || X < 0 || E < 0 || N < 0 || K < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  if (E < 1 || N < 1 || K < 1 || N % 32 || K % 32)
+    return fail(BSMM_ERR_SHAPE, "E must be at least 1, N and K multiples of 32");
+  if (E > kExpertsMax) return fail(BSMM_ERR_UNSUPPORTED, "up to 1024 experts");
+  // tile numbers, rows of tensor maps and scale-atom rows are 32-bit
+  if (S > (1 << 30) || X > INT32_MAX || N > (1 << 20) || K > (1 << 20) || E * N > INT32_MAX ||
+      E * ceil_div(N, 256) * 2 * ceil_div(K, 128) * 4 > INT32_MAX || E * ceil_div(K, 256) * 2 * ceil_div(N, 128) * 4 > INT32_MAX ||
+      (S / 256 + E) * ceil_div(std::max(N, K), 256) > INT32_MAX ||
+      (S / 128 + E) * ceil_div(std::max(N, K), 256) * 8 > INT32_MAX)
+    return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  if (S > 0 && (by_rows ? X < 1 : X < S)) return fail(BSMM_ERR_SHAPE, by_rows ? "x has no rows" : "x has fewer rows than slots");
+  return BSMM_OK;
+}
+bsmm_status combine_sizes(int64_t T, int64_t S, int k, int64_t N, bsmm_dtype type) {
+  if (T < 0 || S < 0 || k < 0 || N < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  if (type != BSMM_F32 && type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "the token's rows must be F32 or BF16");
+  if (k < 1 || N < 1) return fail(BSMM_ERR_SHAPE, "k and N must be at least 1");
+  if (k > 32) return fail(BSMM_ERR_UNSUPPORTED, "up to 32 experts a token");
+  if (T > INT32_MAX / k || S > INT32_MAX || N > (1 << 24)) return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  return BSMM_OK;
+}
+}  // namespace
+
+size_t bsmm_route_workspace_size(int64_t T, int64_t E) {
+  if (T <= 0 || E <= 0 || E > kExpertsMax) return 0;
+  return route_bytes(T, E);
+}
+
+bsmm_status bsmm_route(int64_t T, int64_t E, int k, const void* logits, bsmm_dtype logits_type, int64_t ld,
+                       int renormalize, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* slots,
+                       void* workspace, size_t workspace_bytes, bsmm_stream_t stream) {
+  const bsmm_status st = route_sizes(T, E, k, logits_type, ld);
+  if (st != BSMM_OK) return st;
+  if (!offsets || (T > 0 && (!logits || !ids || !weights || !rows || !slots)))
+    return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned_to(logits, logits_type == BSMM_BF16 ? 2 : 4) || !aligned_to(ids, 4) || !aligned_to(weights, 4) ||
+      !aligned_to(offsets, 4) || !aligned_to(rows, 4) || !aligned_to(slots, 4))
+    return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return launched(cudaMemsetAsync(offsets, 0, (E + 1) * 4, s), "route launch");
+  const size_t need = bsmm_route_workspace_size(T, E);
+  if (need && (!workspace || workspace_bytes < need || !aligned_to(workspace, 256)))
+    return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) + " bytes");
+  const RouteRequest r{T,   E,       k,       logits, logits_type == BSMM_BF16, ld, renormalize != 0,
+                       ids, weights, offsets, rows,   slots,                    workspace};
+  return launched(launch_route(r, s), "route launch");
+}
+
+bsmm_status bsmm_route_backward(int64_t T, int64_t E, int k, const void* logits, bsmm_dtype logits_type, int64_t ld,
+                                int renormalize, const float* d_weights, const int32_t* ids, const float* weights,
+                                void* d_logits, bsmm_stream_t stream) {
+  const bsmm_status st = route_sizes(T, E, k, logits_type, ld);
+  if (st != BSMM_OK) return st;
+  if (T == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if ((!logits && !renormalize) || !d_weights || !ids || !weights || !d_logits)
+    return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  const size_t le = logits_type == BSMM_BF16 ? 2 : 4;
+  if (!aligned_to(logits, le) || !aligned_to(d_weights, 4) || !aligned_to(ids, 4) || !aligned_to(weights, 4) ||
+      !aligned_to(d_logits, le))
+    return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements");
+  const RouteBackwardRequest r{T, E, k, logits, logits_type == BSMM_BF16, ld, renormalize != 0, d_weights, ids, weights,
+                               d_logits};
+  return launched(launch_route_backward(r, reinterpret_cast<cudaStream_t>(stream)), "route backward launch");
+}
+
+bsmm_status bsmm_expert_gemm(int64_t S, int64_t X, int64_t E, int64_t N, int64_t K, const void* x, bsmm_dtype x_type,
+                             const void* x_scales, const void* w, bsmm_dtype w_type, const void* w_atoms,
+                             const int32_t* offsets, const int32_t* rows, void* y, bsmm_stream_t stream) {
+  if ((x_type != BSMM_E4M3 && x_type != BSMM_E5M2) || (w_type != BSMM_E4M3 && w_type != BSMM_E5M2))
+    return fail(BSMM_ERR_INVALID_ARG, "x_type and w_type must be E4M3 or E5M2");
+  const bsmm_status st = expert_sizes(S, X, E, N, K, rows != nullptr);
+  if (st != BSMM_OK) return st;
+  if (S == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if (!x || !x_scales || !w || !w_atoms || !offsets || !y) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(w_atoms) || !aligned16(y) || !aligned_to(offsets, 4) ||
+      !aligned_to(rows, 4))
+    return fail(BSMM_ERR_ALIGNMENT, "x, w, w_atoms and y must be 16-byte aligned, offsets and rows 4-byte");
+  const ExpertGemmRequest r{S, X, E, N, K, x, x_type, static_cast<const uint8_t*>(x_scales), w, w_type, w_atoms, offsets,
+                            rows, y};
+  return launched(launch_expert_gemm(r, reinterpret_cast<cudaStream_t>(stream)), "expert gemm launch");
+}
+
+size_t bsmm_expert_backward_workspace_size(int64_t S, int64_t E, int64_t N, int64_t K) {
+  if (S <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
+  return expert_backward_bytes(S, E, N, K);
+}
+
+bsmm_status bsmm_expert_backward(int64_t S, int64_t X_rows, int64_t E, int64_t N, int64_t K, const void* dY,
+                                 const void* W, const void* X, const int32_t* offsets, const int32_t* rows,
+                                 bsmm_dtype fp8_type, void* dX, void* dW, void* workspace, size_t workspace_bytes,
+                                 bsmm_stream_t stream) {
+  if (fp8_type != BSMM_E5M2 && fp8_type != BSMM_E4M3) return fail(BSMM_ERR_INVALID_ARG, "fp8_type must be E5M2 or E4M3");
+  const bsmm_status st = expert_sizes(S, X_rows, E, N, K, rows != nullptr);
+  if (st != BSMM_OK) return st;
+  if (!dW) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(dW)) return fail(BSMM_ERR_ALIGNMENT, "dY, W, X, dX and dW must be 16-byte aligned, offsets and rows 4-byte");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (S == 0) return launched(cudaMemsetAsync(dW, 0, static_cast<size_t>(E) * N * K * 2, s), "expert backward launch");
+  if (!dY || !W || !X || !offsets || !dX) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(dY) || !aligned16(W) || !aligned16(X) || !aligned16(dX) || !aligned_to(offsets, 4) || !aligned_to(rows, 4))
+    return fail(BSMM_ERR_ALIGNMENT, "dY, W, X, dX and dW must be 16-byte aligned, offsets and rows 4-byte");
+  const size_t need = bsmm_expert_backward_workspace_size(S, E, N, K);
+  if (!workspace || workspace_bytes < need || !aligned_to(workspace, 256))
+    return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) + " bytes");
+  const ExpertBackwardRequest r{S, X_rows, E, N, K, dY, W, X, offsets, rows, fp8_type, dX, dW, workspace};
+  return launched(launch_expert_backward(r, s), "expert backward launch");
+}
+
+bsmm_status bsmm_expert_combine(int64_t T, int64_t S, int k, int64_t N, const void* y, const int32_t* slots,
+                                const float* weights, void* out, bsmm_dtype out_type, bsmm_stream_t stream) {
+  const bsmm_status st = combine_sizes(T, S, k, N, out_type);
+  if (st != BSMM_OK) return st;
+  if (T == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if ((S > 0 && !y) || !slots || !out) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned_to(y, 2) || !aligned_to(slots, 4) || !aligned_to(weights, 4) || !aligned_to(out, out_type == BSMM_BF16 ? 2 : 4))
+    return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements");
+  const CombineRequest r{T, S, N, k, y, slots, weights, out, out_type == BSMM_BF16};
+  return launched(launch_combine(r, reinterpret_cast<cudaStream_t>(stream)), "combine launch");
+}
+
+bsmm_status bsmm_expert_combine_backward(int64_t T, int64_t S, int k, int64_t N, const void* d_out, bsmm_dtype d_type,
+                                         const void* y, const int32_t* slots, const float* weights, void* dy,
+                                         float* d_weights, bsmm_stream_t stream) {
+  const bsmm_status st = combine_sizes(T, S, k, N, d_type);
+  if (st != BSMM_OK) return st;
+  if (T == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  if (!d_out || !slots || (S > 0 && !dy) || (S > 0 && d_weights && !y)) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (d_weights && !weights) return fail(BSMM_ERR_INVALID_ARG, "d_weights without weights");
+  if (!aligned_to(d_out, d_type == BSMM_BF16 ? 2 : 4) || !aligned_to(y, 2) || !aligned_to(slots, 4) ||
+      !aligned_to(weights, 4) || !aligned_to(dy, 2) || !aligned_to(d_weights, 4))
+    return fail(BSMM_ERR_ALIGNMENT, "a pointer is not aligned to its elements");
+  const CombineBackwardRequest r{T, S, N, k, d_out, d_type == BSMM_BF16, y, slots, weights, dy, d_weights};
+  return launched(launch_combine_backward(r, reinterpret_cast<cudaStream_t>(stream)), "combine backward launch");
+}
+
+bsmm_status bsmm_adamw(int64_t count, const int64_t* n, void* const* p, bsmm_dtype p_type, const void* const* grads,
+                       bsmm_dtype g_type, void* const* m, void* const* v, bsmm_dtype state_type,
+                       float* const* m_scales, float* const* v_scales, void* const* copies, double lr, double beta1,
+                       double beta2, double eps, double weight_decay, int64_t step, double grad_scale,
+                       const float* hyper, bsmm_stream_t stream) {
+  if (count < 0) return fail(BSMM_ERR_INVALID_ARG, "negative size");
+  if ((p_type != BSMM_F32 && p_type != BSMM_BF16) || (g_type != BSMM_F32 && g_type != BSMM_BF16))
+    return fail(BSMM_ERR_INVALID_ARG, "p_type and g_type must be F32 or BF16");
+  if (state_type != BSMM_F32 && state_type != BSMM_E4M3) return fail(BSMM_ERR_INVALID_ARG, "state_type must be F32 or E4M3");
+  if (!(lr >= 0 && weight_decay >= 0 && eps >= 0 && beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1))
+    return fail(BSMM_ERR_INVALID_ARG, "lr, weight_decay and eps must not be negative, the betas in [0, 1)");
+  if (!hyper && step < 1) return fail(BSMM_ERR_INVALID_ARG, "step counts from 1");
+  if (count == 0) {
+    set_error("");
+    return BSMM_OK;
+  }
+  const bool bits8 = state_type == BSMM_E4M3;
+  if (!n || !p || !grads || !m || !v || (bits8 && (!m_scales || !v_scales))) return fail(BSMM_ERR_INVALID_ARG, "null pointer");
+  if (!aligned_to(hyper, 4)) return fail(BSMM_ERR_ALIGNMENT, "hyper must be 4-byte aligned");
+  const size_t pe = p_type == BSMM_BF16 ? 2 : 4, ge = g_type == BSMM_BF16 ? 2 : 4, se = bits8 ? 1 : 4;
+  for (int64_t i = 0; i < count; ++i) {
+    auto which = [i] { return "tensor " + std::to_string(i) + ": "; };
+    if (n[i] < 0) return fail(BSMM_ERR_INVALID_ARG, which() + "negative size");
+    if (n[i] == 0) continue;
+    if (!p[i] || !grads[i] || !m[i] || !v[i] || (bits8 && (!m_scales[i] || !v_scales[i])))
+      return fail(BSMM_ERR_INVALID_ARG, which() + "null pointer");
+    if (!aligned_to(p[i], pe) || !aligned_to(grads[i], ge) || !aligned_to(m[i], se) || !aligned_to(v[i], se) ||
+        (bits8 && (!aligned_to(m_scales[i], 4) || !aligned_to(v_scales[i], 4))) || (copies && !aligned_to(copies[i], 2)))
+      return fail(BSMM_ERR_ALIGNMENT, which() + "a pointer is not aligned to its elements");
+  }
+  const AdamwRequest r{count, n,      p,   p_type == BSMM_BF16, grads, g_type == BSMM_BF16, m,    v,          bits8, m_scales,
+                       v_scales, copies, lr,  beta1, beta2, eps, weight_decay, step, grad_scale, hyper};
+  return launched(launch_adamw(r, reinterpret_cast<cudaStream_t>(stream)), "adamw launch");
 }
 
 size_t bsmm_linear_backward_quantized_workspace_size(int64_t M, int64_t N, int64_t K, int scales_are_atoms) {

@@ -1,0 +1,967 @@
+// Products grouped by expert with ragged numbers of rows, MXFP8 on CTA pairs.
+//
+//   bsmm_expert_gemm      y[s, f] = sum_c x[row(s), c] W[e, f, c], e the expert
+//                         whose segment [offsets[e], offsets[e+1]) holds s
+//   bsmm_expert_backward  dX the same way from dY and W^T; dW[e, n, k] =
+//                         sum of dY[s, n] X[row(s), k] over the expert's rows
+//
+// The segment lengths are read on the GPU: no size of a segment is known on
+// the host, so one persistent launch walks a list of tiles that every CTA
+// derives from the offsets.
+//
+// A tile is 256 features x up to 256 rows.  The features (a weight's rows) are
+// the MMA's M and the ragged rows its N, which an instruction may set to any
+// multiple of 32: a segment of 40 rows costs instructions of N = 64, not a
+// 256-row tile, and a decode step's few rows cost little beside the weights'
+// bytes.  dW has the same form with features k, "rows" n and the contraction
+// over a segment, so one kernel computes all three products and stores them
+// the same way (MMA column = output row, lanes along the output's contiguous
+// axis).
+//
+// Per pair of CTAs: CTA r loads 128 of the 256 feature rows (A) and half of
+// the tile's rows (B) per 128-byte contraction block, the leader issues
+// tcgen05.mma.cta_group::2 kind::mxf8f6f4.block_scale into one 256-column
+// FP32 accumulator in each CTA's tensor memory.
+//   warp 0      TMA: A, its scale atoms, B (by box, or by gathered rows)
+//   warp 1      MMA (leader)
+//   warps 2, 3  B's scales: from row-major bytes (any rows, gathered too) or
+//               from atoms into shared memory, four contraction blocks at a
+//               time (one release to the leader per 512 columns: a release at
+//               cluster scope is about 1.2k cycles, four blocks' MMAs 2.2k)
+//   warps 4-19  epilogue: accumulator -> registers -> bfloat16 rows
+// Sums are FP32 over the whole contraction and are rounded to bfloat16 once.
+// Every wait is bounded; on expiry a CTA records the site and winds down.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "blockquant.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace bsmm {
+namespace {
+
+constexpr int PF = 256;      // features of a tile (128 per CTA)
+constexpr int PJ = 256;      // most rows of a tile
+constexpr int KB = 128;      // contraction bytes per stage
+constexpr int STAGES = 6;
+constexpr int THREADS = 640;
+constexpr int EPI_WARPS = 16;
+constexpr int A_BYTES = 128 * KB, B_BYTES = 128 * KB, SFA_BYTES = 512;
+constexpr int SG = 4;        // contraction blocks per group of B's scales
+constexpr int SGROUPS = 2;
+constexpr int SFB_TILE = 1024;  // two atoms
+constexpr int TMEM_COLS = 512, SF_COL0 = 256, SF_COLS = 12;
+
+constexpr int OFF_A = 0;
+constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
+constexpr int OFF_SFA = OFF_B + STAGES * B_BYTES;
+constexpr int OFF_SFB = OFF_SFA + STAGES * SFA_BYTES;
+constexpr int OFF_TILES = OFF_SFB + SGROUPS * SG * SFB_TILE;
+constexpr int OFF_BAR = OFF_TILES + ((kExpertsMax + 1) * 4 + 15) / 16 * 16;
+constexpr int N_BARS = 2 * STAGES + 2 + 2 * SGROUPS + 1;
+constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16 + 1024;
+static_assert(SMEM <= 232448, "shared memory budget");
+static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
+
+enum Site { kSiteProducer = 51, kSiteMma = 52, kSiteMmaScales = 53, kSiteMmaTmem = 54, kSiteScales = 55,
+            kSiteEpilogue = 56, kSiteDrain = 57, kSiteDone = 58 };
+
+struct ExpertParams {
+  int E, F;           // experts; features (output columns)
+  int f_tiles;
+  int ks4;            // scale atoms from one row tile of A to the next
+  int a_rt;           // row tiles of 128 per expert in A's atoms
+  const int* offsets;  // [E + 1], clamped to [0, S]
+  int S;
+  // segments' rows are B's rows (y[s]): the contraction is C long
+  int C, k_tiles;
+  const int* rows;    // B's row of s, or null: s itself
+  int X;              // rows of B
+  const uint8_t* b_scales;  // row-major [X][C / 32], or B's atoms (grad)
+  int64_t b_pitch;
+  int b_vec;          // rows of b_scales are 16-byte aligned
+  // segments are the contraction (grad): B has J rows per expert, A and B hold
+  // the segments padded to multiples of 128 from pads[e] on
+  int J, j_tiles;
+  const int* pads;
+  int b_ks4;
+  __nv_bfloat16* y;   // [S][F], or [E][J][F]
+  uint32_t idesc;     // without N
+  int* status;
+  uint64_t timeout_ns;
+};
+
+// One tile: its expert, first feature, first output row, number of output
+// rows, MMA columns (rows rounded up to 32), contraction start and blocks.
+struct Tile {
+  int e, f0, out0, live, nn, b0, c0, k_tiles;
+};
+
+__device__ __forceinline__ int2 segment(const int* offsets, int e, int S) {
+  const int lo = min(max(__ldg(offsets + e), 0), S);
+  return make_int2(lo, min(max(__ldg(offsets + e + 1), lo), S));
+}
+
+template <bool GRAD>
+__device__ __forceinline__ Tile tile_of(const ExpertParams& p, const int* starts, int u) {
+  Tile t;
+  if constexpr (GRAD) {
+    const int per = p.j_tiles * p.f_tiles;
+    t.e = u / per;
+    const int r = u - t.e * per;
+    const int f = r / p.j_tiles;
+    t.f0 = f * PF;
+    t.b0 = (r - f * p.j_tiles) * PJ;
+    t.live = min(PJ, p.J - t.b0);
+    t.out0 = t.e * p.J + t.b0;
+    t.c0 = __ldg(p.pads + t.e);
+    t.k_tiles = (__ldg(p.pads + t.e + 1) - t.c0) / KB;
+  } else {
+    int lo = 0, hi = p.E;  // the expert with starts[e] <= u < starts[e + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= u) lo = mid; else hi = mid;
+    }
+    t.e = lo;
+    const int2 s = segment(p.offsets, lo, p.S);
+    const int j_tiles = (s.y - s.x + PJ - 1) / PJ;
+    const int r = u - starts[lo];
+    const int f = r / j_tiles;
+    t.f0 = f * PF;
+    t.b0 = s.x + (r - f * j_tiles) * PJ;
+    t.live = min(PJ, s.y - t.b0);
+    t.out0 = t.b0;
+    t.c0 = 0;
+    t.k_tiles = p.k_tiles;
+  }
+  t.nn = (t.live + 31) & ~31;
+  return t;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <bool GRAD, bool GATHER>
+__global__ void __launch_bounds__(THREADS, 1)
+    expert_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSFA,
+                const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB16,
+                const __grid_constant__ ExpertParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem + OFF_A;
+  uint8_t* sB = smem + OFF_B;
+  uint8_t* sSFA = smem + OFF_SFA;
+  uint8_t* sSFB = smem + OFF_SFB;
+  int* starts = reinterpret_cast<int*>(smem + OFF_TILES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 1;
+  uint64_t* sfull = tempty + 1;
+  uint64_t* sempty = sfull + SGROUPS;
+  uint64_t* done = sempty + SGROUPS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int never_abort_storage = 0;
+  volatile int* never_abort = &never_abort_storage;
+  __shared__ int warp_sums[THREADS / 32];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * EPI_WARPS);
+    for (int g = 0; g < SGROUPS; ++g) {
+      mbar_init(&sfull[g], 4);
+      mbar_init(&sempty[g], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tmem_holder, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  // first tile of each expert: an exclusive sum over the experts, two a thread
+  int tiles;
+  if constexpr (GRAD) {
+    tiles = p.E * p.j_tiles * p.f_tiles;
+  } else {
+    static_assert(kExpertsMax <= 2 * THREADS, "two experts a thread");
+    int n[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 2 * static_cast<int>(threadIdx.x) + i;
+      n[i] = 0;
+      if (e < p.E) {
+        const int2 s = segment(p.offsets, e, p.S);
+        n[i] = (s.y - s.x + PJ - 1) / PJ * p.f_tiles;
+      }
+    }
+    int sum = n[0] + n[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sums[warp] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+    const int first = before + sum - n[0] - n[1];
+    if (2 * static_cast<int>(threadIdx.x) <= p.E) starts[2 * threadIdx.x] = first;
+    if (2 * static_cast<int>(threadIdx.x) + 1 <= p.E) starts[2 * threadIdx.x + 1] = first + n[0];
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers initialized before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  if constexpr (!GRAD) tiles = starts[p.E];
+
+  // 640 threads with 96 registers each: the epilogue's 64 sums and the scale
+  // warps' 16 words and 4 row pointers both fit, so nothing is moved between
+  // the warpgroups.
+  if (warp < 4) {
+    if (warp == 0) {
+      // ------------------------------------------------------- producer (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < tiles; u += ncl) {
+        const Tile t = tile_of<GRAD>(p, starts, u);
+        const int half = t.nn >> 1;
+        const uint32_t tx = 2 * (A_BYTES + SFA_BYTES + half * KB);
+        const int atom_row = GRAD ? 4 * ((2 * (t.f0 / PF) + static_cast<int>(rank)) * p.ks4 + t.c0 / KB)
+                                  : 4 * ((t.e * p.a_rt + 2 * (t.f0 / PF) + static_cast<int>(rank)) * p.ks4);
+        const int row0 = t.b0 + static_cast<int>(rank) * half;
+        int r0 = 0, r1 = 0, r2 = 0, r3 = 0;
+        if constexpr (GATHER) {
+          // this lane's four rows; past the segment, and for a row that is
+          // none of B's, one that exists (its column is not stored, or is the
+          // caller's to ignore)
+          const int last = t.b0 + t.live - 1;
+          r0 = min(max(__ldg(p.rows + min(row0 + 4 * lane, last)), 0), p.X - 1);
+          r1 = min(max(__ldg(p.rows + min(row0 + 4 * lane + 1, last)), 0), p.X - 1);
+          r2 = min(max(__ldg(p.rows + min(row0 + 4 * lane + 2, last)), 0), p.X - 1);
+          r3 = min(max(__ldg(p.rows + min(row0 + 4 * lane + 3, last)), 0), p.X - 1);
+        }
+        for (int kt = 0; kt < t.k_tiles; ++kt) {
+          if (GATHER || lane == 0)
+            ok = mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteProducer);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
+          const int x = t.c0 + kt * KB;
+          if (lane == 0) {
+            if (leader) mbar_arrive_expect_tx(&full[stage], tx);
+            tma_load_3d_pair(sA + stage * A_BYTES, &tmA, full_leader, x, t.f0 + static_cast<int>(rank) * 128,
+                             GRAD ? 0 : t.e);
+            tma_load_3d_pair(sSFA + stage * SFA_BYTES, &tmSFA, full_leader, 0, atom_row + 4 * kt, 0);
+            if constexpr (!GATHER) {
+              if (t.nn == PJ) {
+                tma_load_3d_pair(sB + stage * B_BYTES, &tmB, full_leader, x, row0, 0);
+              } else {
+                for (int i = 0; i < half; i += 16)
+                  tma_load_3d_pair(sB + stage * B_BYTES + i * KB, &tmB16, full_leader, x, row0 + i, 0);
+              }
+            }
+          }
+          if constexpr (GATHER) {
+            __syncwarp();
+            if (4 * lane < half)
+              tma_gather4_pair(sB + stage * B_BYTES + lane * 4 * KB, &tmB, full_leader, x, r0, r1, r2, r3);
+          }
+          if (!leader && lane == 0) mbar_arrive_cluster(full_leader);
+          issued |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every stage this CTA filled must have been released by the leader's
+      // MMA (its multicast arrivals on our empty[] have landed) before any
+      // CTA of the pair winds down.
+      if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s)
+          if ((issued >> s) & 1u)
+            mbar_wait(&empty[s], (last_par >> s) & 1u, p.timeout_ns, ok ? never_abort : abort_flag, p.status,
+                      kSiteDrain);
+        if (leader) {
+          for (int s = 0; s < STAGES; ++s)
+            if ((issued >> s) & 1u)
+              mbar_wait(&full[s], (last_par >> s) & 1u, p.timeout_ns, never_abort, p.status, kSiteDrain);
+        } else if (!ok) {
+          // The peer cannot observe the leader's barrier; after giving up, give
+          // its own copies in flight time to land before the CTA winds down.
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 2000000ull) {
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------- MMA issuer (leader)
+      if (leader && lane == 0) {
+        int stage = 0, g = 0;
+        uint32_t phase = 0, tph = 0, gph = 0;
+        bool ok = true;
+        for (int u = cid; ok && u < tiles; u += ncl) {
+          const Tile t = tile_of<GRAD>(p, starts, u);
+          if (t.k_tiles == 0) continue;
+          if (!mbar_wait(tempty, tph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteMmaTmem)) break;
+          tc_fence_after();
+          const uint32_t idesc0 = p.idesc | (static_cast<uint32_t>(t.nn >> 3) << 17);
+          for (int kt = 0; kt < t.k_tiles; ++kt) {
+            if (((kt & (SG - 1)) == 0 &&
+                 !mbar_wait_acq_cluster(&sfull[g], gph, p.timeout_ns, abort_flag, p.status, kSiteMmaScales)) ||
+                !mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag, p.status, kSiteMma)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t a_d = smem_desc(smem_u32(sA + stage * A_BYTES), 16, 1024, 2);
+            const uint64_t b_d = smem_desc(smem_u32(sB + stage * B_BYTES), 16, 1024, 2);
+            const uint32_t sfa_t = tmem + static_cast<uint32_t>(SF_COL0 + stage * SF_COLS);
+            const uint32_t sfb_t = sfa_t + 4;
+            tc_cp_sf_pair(sfa_t, smem_desc(smem_u32(sSFA + stage * SFA_BYTES), 0, 128, 0));
+            const uint64_t sfb_d = smem_desc(smem_u32(sSFB + (g * SG + (kt & (SG - 1))) * SFB_TILE), 0, 128, 0);
+            tc_cp_sf_pair(sfb_t, sfb_d);
+            if (t.nn > 128) tc_cp_sf_pair(sfb_t + 4, desc_add(sfb_d, 512));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_mxf8_pair(tmem, desc_add(a_d, 32 * k), desc_add(b_d, 32 * k),
+                            idesc0 | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa_t, sfb_t,
+                            (kt > 0 || k > 0) ? 1u : 0u);
+            tc_commit_pair_mc(&empty[stage], 0x3);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if ((kt & (SG - 1)) == SG - 1 || kt + 1 == t.k_tiles) {
+              tc_commit_pair_mc(&sempty[g], 0x3);
+              if (++g == SGROUPS) {
+                g = 0;
+                gph ^= 1u;
+              }
+            }
+          }
+          if (!ok) break;
+          tc_commit_pair_mc(tfull, 0x3);
+          tph ^= 1u;
+        }
+        tc_commit_pair_mc(done, 0x1);
+        mbar_wait(done, 0, p.timeout_ns, never_abort, p.status, kSiteDone);
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------- B's scales (both CTAs)
+      // Warp 2 + a fills atom a (tile rows 128 a ..): the word of row w, a
+      // contraction block's four scales, at (w % 32) * 16 + (w / 32) * 4, so a
+      // lane's rows lane, lane + 32, .. make its 16 bytes.
+      const int a = warp - 2;
+      int g = 0;
+      uint32_t gph = 0, used = 0, last_par = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < tiles; u += ncl) {
+        const Tile t = tile_of<GRAD>(p, starts, u);
+        const bool mine = t.nn > 128 * a;
+        const uint8_t* src[4] = {nullptr, nullptr, nullptr, nullptr};
+        if (mine) {
+          if constexpr (GRAD) {
+            src[0] = p.b_scales + (static_cast<int64_t>(t.b0 / 128 + a) * p.b_ks4 + t.c0 / KB) * 512 + lane * 16;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              int r = t.b0 + min(128 * a + 32 * i + lane, t.live - 1);
+              if constexpr (GATHER) r = min(max(__ldg(p.rows + r), 0), p.X - 1);
+              src[i] = p.b_scales + static_cast<int64_t>(r) * p.b_pitch;
+            }
+          }
+        }
+        for (int k0 = 0; k0 < t.k_tiles; k0 += SG) {
+          uint4 w[SG];
+          if (mine) {
+            if constexpr (GRAD) {
+#pragma unroll
+              for (int j = 0; j < SG; ++j)
+                if (k0 + j < t.k_tiles) w[j] = __ldg(reinterpret_cast<const uint4*>(src[0] + (k0 + j) * 512));
+            } else if (p.b_vec && k0 + SG <= t.k_tiles) {
+              uint4 v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + 4 * k0));
+              w[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+              w[1] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+              w[2] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+              w[3] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+            } else {
+              // bytes; past the contraction the neutral scale
+              const int blocks = p.C / 32;
+#pragma unroll
+              for (int j = 0; j < SG; ++j) {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  v[i] = 0;
+#pragma unroll
+                  for (int b = 0; b < 4; ++b) {
+                    const int kb = 4 * (k0 + j) + b;
+                    v[i] |= (kb < blocks ? static_cast<uint32_t>(__ldg(src[i] + kb)) : 127u) << (8 * b);
+                  }
+                }
+                w[j] = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+          }
+          if (!mbar_wait(&sempty[g], gph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteScales)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (mine) {
+            uint8_t* dst = sSFB + g * SG * SFB_TILE + a * 512 + lane * 16;
+#pragma unroll
+            for (int j = 0; j < SG; ++j)
+              if (k0 + j < t.k_tiles) *reinterpret_cast<uint4*>(dst + j * SFB_TILE) = w[j];
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[g]), 0));
+          used |= 1u << g;
+          last_par = (last_par & ~(1u << g)) | (gph << g);
+          if (++g == SGROUPS) {
+            g = 0;
+            gph ^= 1u;
+          }
+        }
+      }
+      // the leader's arrivals on our sempty[] have landed before we wind down
+      if (lane == 0 && ok)
+        for (int i = 0; i < SGROUPS; ++i)
+          if ((used >> i) & 1u)
+            mbar_wait(&sempty[i], (last_par >> i) & 1u, p.timeout_ns, never_abort, p.status, kSiteDrain);
+      __syncwarp();
+    }
+  } else {
+    // --------------------------------------------------------- epilogue (both CTAs)
+    const int ew = warp - 4;
+    const int q = warp & 3;  // TMEM lane quarter: 32 features
+    const int g = ew >> 2;   // 64 of the tile's rows
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g * 64);
+    const bool odd = lane & 1;
+    uint32_t tph = 0;
+    for (int u = cid; u < tiles; u += ncl) {
+      const Tile t = tile_of<GRAD>(p, starts, u);
+      const int f = t.f0 + static_cast<int>(rank) * 128 + q * 32 + (lane & ~1);
+      const int live = f < p.F ? min(t.live - g * 64, 64) : 0;
+      // lane pairs exchange halves: even lanes store even rows, odd lanes odd
+      // ones, two features each
+      __nv_bfloat16* dst = p.y + static_cast<int64_t>(t.out0 + g * 64 + (odd ? 1 : 0)) * p.F + f;
+      uint32_t v[32];  // bfloat16 pairs: this lane's feature in rows 2 c and 2 c + 1
+      if (t.k_tiles > 0) {
+        if (!mbar_wait(tfull, tph, p.timeout_ns, abort_flag, p.status, kSiteEpilogue)) break;
+        tph ^= 1u;
+        tc_fence_after();
+        if (live > 0) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r0[16], r1[16];
+            tmem_ld16(taddr + 32 * h, r0);
+            tmem_ld16(taddr + 32 * h + 16, r1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              v[16 * h + j] = bf16x2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
+              v[16 * h + 8 + j] = bf16x2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(tempty), 0));
+      } else {  // an expert without rows: its sums are empty
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = 0u;
+      }
+      if (live <= 0) continue;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, v[c], 1);
+        const uint32_t pair = odd ? __byte_perm(got, v[c], 0x7632) : __byte_perm(v[c], got, 0x5410);
+        if (2 * c + (odd ? 1 : 0) < live) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(2 * c) * p.F) = pair;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no signal may target a CTA that has exited
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The backward's operands
+// ---------------------------------------------------------------------------
+// Padded starts of the segments (multiples of 128) and, per padded tile of 128
+// rows, its first row and number of rows (0: none).
+__global__ void __launch_bounds__(1024) expert_plan(const int* offsets, int E, int S, int tiles, int* pads, int2* table) {
+  __shared__ int sums[32];
+  __shared__ int ends[kExpertsMax];
+  __shared__ int lows[kExpertsMax];
+  __shared__ int lens[kExpertsMax];
+  const int e = threadIdx.x, lane = e & 31;
+  int2 s = make_int2(0, 0);
+  if (e < E) s = segment(offsets, e, S);
+  const int n = (s.y - s.x + 127) / 128;
+  int sum = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) sums[e >> 5] = sum;
+  __syncthreads();
+  for (int w = 0; w < (e >> 5); ++w) sum += sums[w];
+  // segments that overlap (offsets that fall) do not fit the table: what is
+  // past its end is left out
+  const int end = min(sum, tiles), begin = min(sum - n, tiles);
+  ends[e] = end;
+  lows[e] = s.x;
+  lens[e] = s.y - s.x;
+  if (e < E) pads[e] = begin * 128;
+  if (e == E - 1) pads[E] = end * 128;
+  __syncthreads();
+  for (int i = e; i < tiles; i += 1024) {
+    int lo = -1, hi = E - 1;  // the first expert that ends past i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > i) hi = mid; else lo = mid;
+    }
+    int2 t = make_int2(0, 0);
+    if (ends[hi] > i) {
+      const int k = i - (hi ? ends[hi - 1] : 0);
+      t = make_int2(lows[hi] + 128 * k, min(128, lens[hi] - 128 * k));
+    }
+    table[i] = t;
+  }
+}
+
+// bf16 rows quantized in blocks of 32 down the rows, tiles of 128 rows x 128
+// columns, into transposed codes [columns][padded rows] and scale atoms: the
+// contraction-major operands of dW and dX.  dY is quantized along its rows
+// too, from the same tile.
+struct SegQuant {
+  const __nv_bfloat16* x;
+  int cols, col_tiles;
+  const int* rows;   // gathered, or null
+  int X;             // rows of x
+  const int2* table;  // padded tiles, or null: every `per` rows are a segment
+  int per, per_tiles;
+  int tiles;         // padded row tiles
+  uint8_t* codes;    // [segment group][cols][pitch]
+  int64_t pitch, group_codes;  // group: all tiles (table), or one segment
+  uint8_t* atoms;
+  int ks4;           // atoms per row tile of 128 columns
+  int64_t group_atoms;
+  uint8_t* row_codes;   // null: not along the rows
+  uint8_t* row_scales;  // [rows][cols / 32]
+};
+struct SegJobs {
+  SegQuant job[3];
+  int first[4];  // first tile of each job, and their end
+};
+
+constexpr int QSTAGES = 2;
+constexpr int QTILE = 128 * 256;
+constexpr int QSMEM = QSTAGES * QTILE + 128 * 144;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+template <int CODE>
+__global__ void __launch_bounds__(256) expert_quant(const __grid_constant__ SegJobs jobs) {
+  extern __shared__ __align__(16) uint8_t qsmem[];
+  uint8_t* ostg = qsmem + QSTAGES * QTILE;  // 128 columns x 128 codes, rows of 144 bytes
+  __shared__ __align__(16) uint8_t sstg[512];
+  const int t = threadIdx.x;
+  const int total = jobs.first[3];
+
+  struct Where {
+    const SegQuant* q;
+    int tile, src, live, c0;
+  };
+  auto where = [&](int u) {
+    Where w;
+    const int k = u < jobs.first[1] ? 0 : (u < jobs.first[2] ? 1 : 2);
+    w.q = &jobs.job[k];
+    const int r = u - jobs.first[k];
+    w.tile = r / w.q->col_tiles;
+    w.c0 = (r - w.tile * w.q->col_tiles) * 128;
+    if (w.q->table) {
+      const int2 s = __ldg(w.q->table + w.tile);
+      w.src = s.x;
+      w.live = s.y;
+    } else {
+      const int e = w.tile / w.q->per_tiles, i = w.tile - e * w.q->per_tiles;
+      w.src = e * w.q->per + i * 128;
+      w.live = min(128, w.q->per - i * 128);
+    }
+    return w;
+  };
+  // 16-byte chunk j of the thread: row (t + 256 j) / 16, columns 8 (t % 16) ..;
+  // rows past the segment and columns past the array become zeros
+  auto load = [&](int u, int st) {
+    if (u < total) {
+      const Where w = where(u);
+      const uint32_t base = smem_u32(qsmem + st * QTILE);
+      const int c = w.c0 + 8 * (t & 15);
+      if (w.live > 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = (t >> 4) + 16 * j;
+          const bool real = r < w.live && c < w.q->cols;
+          int row = w.src + (r < w.live ? r : 0);
+          if (w.q->rows) row = min(max(__ldg(w.q->rows + row), 0), w.q->X - 1);
+          // the chunk's place is rotated by its row, so that reads along rows
+          // and down columns both spread over the banks
+          cp_async16(base + r * 256 + (((t & 15) ^ (r & 15)) * 16),
+                     w.q->x + static_cast<int64_t>(row) * w.q->cols + (real ? c : 0), real);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  load(blockIdx.x, 0);
+  int st = 0;
+  for (int u = blockIdx.x; u < total; u += gridDim.x, st ^= 1) {
+    load(u + gridDim.x, st ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const Where w = where(u);
+    const SegQuant& q = *w.q;
+    if (w.live > 0) {
+      const uint8_t* tile = qsmem + st * QTILE;
+      if (q.row_codes) {
+        // along the rows: four lanes cover a row's 128 columns, so that the
+        // codes leave as whole 128-byte lines
+        const int blk = t & 3;
+        const int col = w.c0 + 32 * blk;
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+          const int r = (t >> 2) + 64 * pass;
+          uint4 v[4];
+          uint32_t m = 0u;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[j] = *reinterpret_cast<const uint4*>(tile + r * 256 + (((4 * blk + j) ^ (r & 15)) * 16));
+            m = bf16x2_max_abs(m, bf16x2_max_abs(bf16x2_max_abs(v[j].x, v[j].y), bf16x2_max_abs(v[j].z, v[j].w)));
+          }
+          const Scale sc = make_scale(fmaxf(bf16_lo_abs(m), bf16_hi_abs(m)), CODE, BSMM_SCALE_UE8M0);
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[2 * j] = encode4<true>(__uint_as_float(v[j].x << 16), __uint_as_float(v[j].x & 0xFFFF0000u),
+                                     __uint_as_float(v[j].y << 16), __uint_as_float(v[j].y & 0xFFFF0000u), sc, CODE);
+            o[2 * j + 1] = encode4<true>(__uint_as_float(v[j].z << 16), __uint_as_float(v[j].z & 0xFFFF0000u),
+                                         __uint_as_float(v[j].w << 16), __uint_as_float(v[j].w & 0xFFFF0000u), sc, CODE);
+          }
+          if (r < w.live && col < q.cols) {
+            const int64_t row = w.src + r;
+            uint4* dst = reinterpret_cast<uint4*>(q.row_codes + row * q.cols + col);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            q.row_scales[row * (q.cols / 32) + col / 32] = static_cast<uint8_t>(sc.stored);
+          }
+        }
+      }
+      // down the rows: thread t takes columns 2 (t % 64), + 1 and the 32-row
+      // block t / 64
+      const int cp = t & 63, blk = t >> 6;
+      uint32_t v[32];
+      uint32_t m = 0u;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        const int row = 32 * blk + r;
+        v[r] = *reinterpret_cast<const uint32_t*>(tile + row * 256 + (((cp >> 2) ^ (row & 15)) * 16) + (cp & 3) * 4);
+        m = bf16x2_max_abs(m, v[r]);
+      }
+      const Scale s0 = make_scale(bf16_lo_abs(m), CODE, BSMM_SCALE_UE8M0);
+      const Scale s1 = make_scale(bf16_hi_abs(m), CODE, BSMM_SCALE_UE8M0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o0[4], o1[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t* x = v + 16 * h + 4 * j;
+          o0[j] = encode4<true>(__uint_as_float(x[0] << 16), __uint_as_float(x[1] << 16), __uint_as_float(x[2] << 16),
+                                __uint_as_float(x[3] << 16), s0, CODE);
+          o1[j] = encode4<true>(__uint_as_float(x[0] & 0xFFFF0000u), __uint_as_float(x[1] & 0xFFFF0000u),
+                                __uint_as_float(x[2] & 0xFFFF0000u), __uint_as_float(x[3] & 0xFFFF0000u), s1, CODE);
+        }
+        uint8_t* o = ostg + 2 * cp * 144 + 32 * blk + 16 * h;
+        *reinterpret_cast<uint4*>(o) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+        *reinterpret_cast<uint4*>(o + 144) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+      }
+      const int c0 = 2 * cp, c1 = c0 + 1;
+      sstg[(c0 & 31) * 16 + (c0 >> 5) * 4 + blk] = static_cast<uint8_t>(s0.stored);
+      sstg[(c1 & 31) * 16 + (c1 >> 5) * 4 + blk] = static_cast<uint8_t>(s1.stored);
+    }
+    __syncthreads();  // the tile has been read, the codes are staged
+    if (w.live > 0) {
+      const int group = q.table ? 0 : w.tile / q.per_tiles, at = q.table ? w.tile : w.tile - group * q.per_tiles;
+      uint8_t* out = q.codes + group * q.group_codes + static_cast<int64_t>(w.c0) * q.pitch + at * 128;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = (t >> 3) + 32 * j;
+        if (w.c0 + c < q.cols)
+          *reinterpret_cast<uint4*>(out + c * q.pitch + (t & 7) * 16) =
+              *reinterpret_cast<const uint4*>(ostg + c * 144 + (t & 7) * 16);
+      }
+      if (t < 32)  // columns past the array were zeros: their scale is the neutral one
+        *reinterpret_cast<uint4*>(q.atoms + group * q.group_atoms +
+                                  (static_cast<int64_t>(w.c0 / 128) * q.ks4 + at) * 512 + t * 16) =
+            *reinterpret_cast<const uint4*>(sstg + t * 16);
+    }
+    // the next tile's staging writes come after the next __syncthreads of the
+    // loop (behind the wait for its copies), which orders them after these reads
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+std::atomic<int> g_clusters[64] = {};
+
+uint32_t f8_code(int dtype) { return dtype == BSMM_E5M2 ? 1u : 0u; }
+
+// kind::mxf8f6f4: E4M3 = 0 / E5M2 = 1, UE8M0 scales (bit 23), M = 256 (pair); N per tile.
+uint32_t expert_idesc(int a_type, int b_type) {
+  return (f8_code(a_type) << 7) | (f8_code(b_type) << 10) | (1u << 23) | (static_cast<uint32_t>(PF >> 4) << 24);
+}
+
+template <bool GRAD, bool GATHER>
+cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tsa, const CUtensorMap& tb, const CUtensorMap& tb16,
+                         ExpertParams p, int64_t most_tiles, const DeviceCtx* ctx, const char* name, cudaStream_t s) {
+  auto kern = expert_gemm<GRAD, GATHER>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (ctx->device < 0 || ctx->device >= 64) return cudaErrorInvalidDevice;
+  int most = g_clusters[ctx->device].load(std::memory_order_relaxed);
+  if (most == 0) {
+    cfg.gridDim = dim3(2 * (ctx->num_sms / 2));
+    e = cudaOccupancyMaxActiveClusters(&most, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (most <= 0) return cudaErrorInvalidConfiguration;
+    g_clusters[ctx->device].store(most, std::memory_order_relaxed);
+  }
+  p.status = ctx->status;
+  p.timeout_ns = wait_timeout_ns();
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(most_tiles, most))));
+  TraceScope tr(name, s);
+  e = cudaLaunchKernelEx(&cfg, kern, ta, tsa, tb, tb16, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// y[s] = A[e] B[row(s)]: A codes [E][F][a_pitch] with atoms [E][a_rt][ks4].
+cudaError_t launch_segments(int E, int F, int C, int64_t a_pitch, const void* a, const void* a_atoms, const void* b,
+                            const uint8_t* b_scales, int S, int X, const int* offsets, const int* rows, void* y,
+                            uint32_t idesc, const char* name, cudaStream_t s) {
+  const DeviceCtx* ctx = device_ctx();
+  if (!ctx) return cudaErrorInitializationError;
+  ExpertParams p{};
+  p.E = E;
+  p.F = F;
+  p.f_tiles = static_cast<int>(ceil_div(F, PF));
+  p.ks4 = static_cast<int>(ceil_div(C, KB));
+  p.a_rt = 2 * p.f_tiles;
+  p.offsets = offsets;
+  p.S = S;
+  p.C = C;
+  p.k_tiles = p.ks4;
+  p.rows = rows;
+  p.X = X;
+  p.b_scales = b_scales;
+  p.b_pitch = C / 32;
+  p.b_vec = p.b_pitch % 16 == 0 && reinterpret_cast<uintptr_t>(b_scales) % 16 == 0;
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.idesc = idesc;
+  CUtensorMap ta, tsa, tb, tb16;
+  if (!make_tmap_rows(&ta, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a_pitch, F, E, a_pitch, KB, 128) ||
+      !make_tmap_3d(&tsa, a_atoms, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128,
+                    static_cast<uint64_t>(E) * p.a_rt * p.ks4 * 4, 1, 128, 4, false) ||
+      !(rows ? make_tmap_rows(&tb, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, C, X, 0, C, KB, 1)
+             : make_tmap_rows(&tb, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, C, X, 1, C, KB, 128)) ||
+      !make_tmap_rows(&tb16, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, C, X, 1, C, KB, 16))
+    return cudaErrorInvalidValue;
+  // a segment's last tile may be partial: at most one more per expert
+  const int64_t most = (S / PJ + std::min(E, S)) * static_cast<int64_t>(p.f_tiles);
+  return rows ? launch_tiles<false, true>(ta, tsa, tb, tb16, p, most, ctx, name, s)
+              : launch_tiles<false, false>(ta, tsa, tb, tb16, p, most, ctx, name, s);
+}
+
+struct BackwardParts {
+  size_t dyn, dyn_s, wt, wt_s, dyt, dyt_s, xt, xt_s, pads, table, total;
+  int64_t Np, Sp;
+};
+BackwardParts backward_parts(int64_t S, int64_t E, int64_t N, int64_t K) {
+  BackwardParts b{};
+  b.Np = ceil_div(N, 128) * 128;
+  // each segment rounded up to 128 rows: at most 127 more than its own
+  b.Sp = ceil_div(S + 127 * std::min(E, S), 128) * 128;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at = align_up(at + bytes, 256);
+    return r;
+  };
+  const size_t k_rt = 2 * ceil_div(K, 256), n_rt = 2 * ceil_div(N, 256);
+  b.dyn = take(static_cast<size_t>(S) * N);
+  b.dyn_s = take(static_cast<size_t>(S) * (N / 32));
+  b.wt = take(static_cast<size_t>(E) * K * b.Np);
+  b.wt_s = take(static_cast<size_t>(E) * k_rt * (b.Np / 128) * 512);
+  b.dyt = take(static_cast<size_t>(N) * b.Sp);
+  b.dyt_s = take(n_rt * (b.Sp / 128) * 512);
+  b.xt = take(static_cast<size_t>(K) * b.Sp);
+  b.xt_s = take(k_rt * (b.Sp / 128) * 512);
+  b.pads = take((E + 1) * 4);
+  b.table = take(b.Sp / 128 * 8);
+  b.total = at;
+  return b;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm(const ExpertGemmRequest& r, cudaStream_t s) {
+  return launch_segments(static_cast<int>(r.E), static_cast<int>(r.N), static_cast<int>(r.K), r.K, r.w, r.w_atoms, r.x,
+                         r.x_scales, static_cast<int>(r.S), static_cast<int>(r.X), r.offsets, r.rows, r.y,
+                         expert_idesc(r.w_type, r.x_type), r.rows ? "expert_gemm (gathered)" : "expert_gemm", s);
+}
+
+size_t expert_backward_bytes(int64_t S, int64_t E, int64_t N, int64_t K) { return backward_parts(S, E, N, K).total; }
+
+cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t s) {
+  const DeviceCtx* ctx = device_ctx();
+  if (!ctx) return cudaErrorInitializationError;
+  const BackwardParts b = backward_parts(r.S, r.E, r.N, r.K);
+  uint8_t* ws = static_cast<uint8_t*>(r.workspace);
+  int* pads = reinterpret_cast<int*>(ws + b.pads);
+  int2* table = reinterpret_cast<int2*>(ws + b.table);
+  const int row_tiles = static_cast<int>(b.Sp / 128);
+  {
+    TraceScope tr("expert_plan", s);
+    expert_plan<<<1, 1024, 0, s>>>(r.offsets, static_cast<int>(r.E), static_cast<int>(r.S), row_tiles, pads, table);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  const int n_tiles = static_cast<int>(ceil_div(r.N, 128)), k_tiles = static_cast<int>(ceil_div(r.K, 128));
+  SegJobs jobs{};
+  SegQuant& w = jobs.job[0];
+  w.x = static_cast<const __nv_bfloat16*>(r.W);
+  w.cols = static_cast<int>(r.K);
+  w.col_tiles = k_tiles;
+  w.per = static_cast<int>(r.N);
+  w.per_tiles = n_tiles;
+  w.tiles = static_cast<int>(r.E) * n_tiles;
+  w.codes = ws + b.wt;
+  w.pitch = b.Np;
+  w.group_codes = r.K * b.Np;
+  w.atoms = ws + b.wt_s;
+  w.ks4 = n_tiles;
+  w.group_atoms = 2 * ceil_div(r.K, 256) * n_tiles * 512;
+  SegQuant& d = jobs.job[1];
+  d.x = static_cast<const __nv_bfloat16*>(r.dY);
+  d.cols = static_cast<int>(r.N);
+  d.col_tiles = n_tiles;
+  d.X = static_cast<int>(r.S);
+  d.table = table;
+  d.tiles = row_tiles;
+  d.codes = ws + b.dyt;
+  d.pitch = b.Sp;
+  d.atoms = ws + b.dyt_s;
+  d.ks4 = row_tiles;
+  d.row_codes = ws + b.dyn;
+  d.row_scales = ws + b.dyn_s;
+  SegQuant& x = jobs.job[2];
+  x = d;
+  x.x = static_cast<const __nv_bfloat16*>(r.X);
+  x.cols = static_cast<int>(r.K);
+  x.col_tiles = k_tiles;
+  x.rows = r.rows;
+  x.X = static_cast<int>(r.X_rows);
+  x.codes = ws + b.xt;
+  x.atoms = ws + b.xt_s;
+  x.row_codes = x.row_scales = nullptr;
+  for (int i = 0; i < 3; ++i) jobs.first[i + 1] = jobs.first[i] + jobs.job[i].tiles * jobs.job[i].col_tiles;
+  auto quant = r.fp8 == BSMM_E4M3 ? expert_quant<BSMM_E4M3> : expert_quant<BSMM_E5M2>;
+  e = cudaFuncSetAttribute(quant, cudaFuncAttributeMaxDynamicSharedMemorySize, QSMEM);
+  if (e != cudaSuccess) return e;
+  {
+    TraceScope tr("expert_quant", s);
+    quant<<<std::min(jobs.first[3], 2 * ctx->num_sms), 256, QSMEM, s>>>(jobs);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  const uint32_t idesc = expert_idesc(r.fp8, r.fp8);
+  e = launch_segments(static_cast<int>(r.E), static_cast<int>(r.K), static_cast<int>(r.N), b.Np, ws + b.wt, ws + b.wt_s,
+                      ws + b.dyn, ws + b.dyn_s, static_cast<int>(r.S), static_cast<int>(r.S), r.offsets, nullptr, r.dX,
+                      idesc, "expert_gemm (dX)", s);
+  if (e != cudaSuccess) return e;
+
+  ExpertParams p{};
+  p.E = static_cast<int>(r.E);
+  p.F = static_cast<int>(r.K);
+  p.f_tiles = static_cast<int>(ceil_div(r.K, PF));
+  p.ks4 = row_tiles;
+  p.offsets = r.offsets;
+  p.S = static_cast<int>(r.S);
+  p.b_scales = ws + b.dyt_s;
+  p.b_ks4 = row_tiles;
+  p.J = static_cast<int>(r.N);
+  p.j_tiles = static_cast<int>(ceil_div(r.N, PJ));
+  p.pads = pads;
+  p.y = static_cast<__nv_bfloat16*>(r.dW);
+  p.idesc = idesc;
+  CUtensorMap ta, tsa, tb, tb16;
+  if (!make_tmap_rows(&ta, ws + b.xt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b.Sp, r.K, 1, b.Sp, KB, 128) ||
+      !make_tmap_3d(&tsa, ws + b.xt_s, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128,
+                    static_cast<uint64_t>(2 * p.f_tiles) * row_tiles * 4, 1, 128, 4, false) ||
+      !make_tmap_rows(&tb, ws + b.dyt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b.Sp, r.N, 1, b.Sp, KB, 128) ||
+      !make_tmap_rows(&tb16, ws + b.dyt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b.Sp, r.N, 1, b.Sp, KB, 16))
+    return cudaErrorInvalidValue;
+  return launch_tiles<true, false>(ta, tsa, tb, tb16, p, static_cast<int64_t>(p.E) * p.j_tiles * p.f_tiles, ctx,
+                                   "expert_gemm (dW)", s);
+}
+
+}  // namespace bsmm

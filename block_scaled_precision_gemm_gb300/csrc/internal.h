@@ -188,6 +188,114 @@ size_t adapter_terms_bytes(int64_t T, int64_t R, int64_t L);
 int64_t adapters_sort_max();
 cudaError_t launch_adapters_backward(const AdaptersBackwardRequest& r, cudaStream_t s);
 
+// ---- products grouped by expert (experts.cu) -------------------------------
+constexpr int kExpertsMax = 1024;
+struct ExpertGemmRequest {
+  int64_t S, X, E, N, K;
+  const void* x;  // [X][K] codes
+  int x_type;
+  const uint8_t* x_scales;  // [X][K / 32]
+  const void* w;            // [E][N][K] codes
+  int w_type;
+  const void* w_atoms;
+  const int* offsets;  // [E + 1]
+  const int* rows;     // null: row s of x
+  void* y;             // [S][N] bf16
+};
+cudaError_t launch_expert_gemm(const ExpertGemmRequest& r, cudaStream_t s);
+
+struct ExpertBackwardRequest {
+  int64_t S, X_rows, E, N, K;
+  const void* dY;  // [S][N] bf16
+  const void* W;   // [E][N][K] bf16
+  const void* X;   // [X_rows][K] bf16
+  const int* offsets;
+  const int* rows;
+  int fp8;
+  void* dX;
+  void* dW;
+  void* workspace;  // expert_backward_bytes
+};
+size_t expert_backward_bytes(int64_t S, int64_t E, int64_t N, int64_t K);
+cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t s);
+
+// ---- router (router.cu) -----------------------------------------------------
+struct RouteRequest {
+  int64_t T, E;
+  int k;
+  const void* logits;  // [T][ld]
+  bool bf16;
+  int64_t ld;
+  bool renormalize;
+  int* ids;        // [T][k]
+  float* weights;  // [T][k]
+  int* offsets;    // [E + 1]
+  int* rows;       // [T k]
+  int* slots;      // [T][k]
+  void* workspace;  // route_bytes
+};
+size_t route_bytes(int64_t T, int64_t E);
+cudaError_t launch_route(const RouteRequest& r, cudaStream_t s);
+
+struct RouteBackwardRequest {
+  int64_t T, E;
+  int k;
+  const void* logits;
+  bool bf16;  // of logits and d_logits
+  int64_t ld;
+  bool renormalize;
+  const float* d_weights;
+  const int* ids;
+  const float* weights;
+  void* d_logits;  // [T][E]
+};
+cudaError_t launch_route_backward(const RouteBackwardRequest& r, cudaStream_t s);
+
+struct CombineRequest {
+  int64_t T, S, N;
+  int k;
+  const void* y;  // [S][N] bf16
+  const int* slots;
+  const float* weights;  // null: 1
+  void* out;
+  bool bf16;
+};
+cudaError_t launch_combine(const CombineRequest& r, cudaStream_t s);
+
+struct CombineBackwardRequest {
+  int64_t T, S, N;
+  int k;
+  const void* d_out;  // [T][N]
+  bool bf16;
+  const void* y;
+  const int* slots;
+  const float* weights;  // null: 1
+  void* dy;              // [S][N] bf16
+  float* d_weights;      // null: not wanted
+};
+cudaError_t launch_combine_backward(const CombineBackwardRequest& r, cudaStream_t s);
+
+// ---- AdamW (adamw.cu) ---------------------------------------------------------
+struct AdamwRequest {
+  int64_t count;
+  const int64_t* n;
+  void* const* p;
+  bool p_bf16;
+  const void* const* g;
+  bool g_bf16;
+  void* const* m;
+  void* const* v;
+  bool bits8;
+  float* const* m_scales;
+  float* const* v_scales;
+  void* const* copies;  // null: none
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  double grad_scale;
+  const float* hyper;
+};
+cudaError_t launch_adamw(const AdamwRequest& r, cudaStream_t s);
+
 // Block-scaled formats of bsmm_gemm.
 enum MxFormat { kFmtMXF8 = 0, kFmtNVF4 = 1, kFmtMXF4 = 2 };
 // Scale relayout into the tensor-core scale-factor atoms (see gemm_tc.cu).

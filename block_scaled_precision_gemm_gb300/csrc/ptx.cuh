@@ -411,6 +411,16 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* t
       "l"(tm), "r"(x), "r"(y), "r"(z), "r"(mbar_cluster_addr)
       : "memory");
 }
+// Four rows of a 2-D array (its map's box is one row high), each 128 bytes from
+// column x, to consecutive rows of the destination.
+__device__ __forceinline__ void tma_gather4_pair(void* dst, const CUtensorMap* tm, uint32_t mbar_cluster_addr, int x,
+                                                 int r0, int r1, int r2, int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+      "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(tm), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(mbar_cluster_addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // one warp per CTA
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                "r"(ncols)

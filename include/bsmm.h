@@ -601,6 +601,146 @@ bsmm_status bsmm_adapters_backward(int64_t T, int64_t K, int64_t N, int64_t R, i
                                    void* dA, void* dB, bsmm_dtype grad_type, void* workspace, size_t workspace_bytes,
                                    bsmm_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Mixture of experts                                                        */
+/* ------------------------------------------------------------------------ */
+
+/* No counterpart on the pages.  A layer of E experts, of which each of T
+ * tokens uses k: bsmm_route chooses them and lays the S = T k (token, choice)
+ * pairs out by expert, bsmm_expert_gemm multiplies every expert's rows with its
+ * own MXFP8 weights, bsmm_gated_act works on those rows as on any, and
+ * bsmm_expert_combine sums each token's k results.  No size of an expert's
+ * share is needed on the host: the offsets stay on the GPU, and every call can
+ * be captured into a graph.  Every sum has a fixed order.
+ *
+ * Layout: expert e's pairs are the slots offsets[e] .. offsets[e+1] - 1, in the
+ * pairs' order (token first); rows[s] is the token of slot s, slots[t k + j]
+ * the slot of token t's j-th choice.
+ *
+ * bsmm_route, for each token:
+ *   logits [T, E] F32 or BF16 at a row pitch of ld elements.
+ *   ids [T, k]  the k largest logits' experts, falling; of equal ones the
+ *            lowest index first.  Minus infinity and NaN are never chosen: where
+ *            fewer than k are left, ids = -1 and weights = 0.
+ *   weights  binary32 [T, k]: exp(l_id - m) / sum, m the largest logit, the sum
+ *            over the chosen (renormalize = 1) or over all E (0, the softmax's
+ *            own values; NaN counts as minus infinity).  A chosen plus infinity
+ *            gives NaN weights, as the formula does.
+ *   offsets [E + 1], rows [T k], slots [T, k]  the layout above; an id of -1 has
+ *            no slot (-1), and rows past offsets[E] are -1.
+ *   E up to 1024, k up to 32 and at most E; T k below 2^31.
+ *   workspace  bsmm_route_workspace_size() bytes, 256-byte aligned (0 for few
+ *            tokens).  Pointers aligned to their elements. */
+size_t bsmm_route_workspace_size(int64_t T, int64_t E);
+
+bsmm_status bsmm_route(int64_t T, int64_t E, int k, const void* logits, bsmm_dtype logits_type, int64_t ld,
+                       int renormalize, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* slots,
+                       void* workspace, size_t workspace_bytes, bsmm_stream_t stream);
+
+/* Its backward pass, from d_weights [T, k] and the forward's ids and weights:
+ * with mean = sum over j of weights d_weights,
+ *   renormalize = 1  d_logits[id_j] = weights_j (d_weights_j - mean), else 0;
+ *   renormalize = 0  d_logits[i] = -p_i mean, p the softmax of the logits, and
+ *                    weights_j d_weights_j besides at id_j.
+ * d_logits [T, E] of the logits' type, contiguous: overwritten.  An id outside
+ * [0, E) has no part.  The logits are read for renormalize = 0 only. */
+bsmm_status bsmm_route_backward(int64_t T, int64_t E, int k, const void* logits, bsmm_dtype logits_type, int64_t ld,
+                                int renormalize, const float* d_weights, const int32_t* ids, const float* weights,
+                                void* d_logits, bsmm_stream_t stream);
+
+/* y[s] = W_e x[row(s)] for every slot s of every expert e, FP32 sums rounded
+ * once to bfloat16.
+ *
+ *   x [X, K] codes (E4M3 or E5M2), UE8M0 scales x_scales [X, K / 32] row-major,
+ *            as bsmm_quantize or bsmm_gated_act writes them.
+ *   w [E, N, K] codes, w_atoms their scales in the atom layout, as
+ *            bsmm_quantize_atoms writes them for E batches.
+ *   offsets [E + 1] int32, not falling.  Values outside [0, S] count as the
+ *            nearest of the two.  Slots outside every segment are left as they
+ *            are in y.
+ *   rows [S] int32 or NULL for row(s) = s (then X >= S).  A row outside
+ *            [0, X) gives unspecified values in its own slot.
+ *   y [S, N] bfloat16.
+ *   N and K multiples of 32; E up to 1024; codes, w_atoms and y 16-byte
+ *            aligned, offsets and rows 4-byte. */
+bsmm_status bsmm_expert_gemm(int64_t S, int64_t X, int64_t E, int64_t N, int64_t K, const void* x, bsmm_dtype x_type,
+                             const void* x_scales, const void* w, bsmm_dtype w_type, const void* w_atoms,
+                             const int32_t* offsets, const int32_t* rows, void* y, bsmm_stream_t stream);
+
+/* bsmm_linear_backward by expert, from bfloat16 dY [S, N], W [E, N, K] and
+ * X [X_rows, K]:
+ *   dX[s] = W_e^T dY[s]                dY and W quantized along N
+ *   dW_e  = sum of dY[s] X[row(s)]^T   dY and X quantized along the expert's
+ *                                      slots, in blocks of 32 from its first;
+ *                                      the last block may be shorter
+ * dX [S, K] bfloat16 is by slot: bsmm_expert_combine without weights sums it by
+ * token.  Slots outside every segment are left as they are in dX.  dW
+ * [E, N, K] bfloat16 is overwritten, with zeros for an expert without slots.
+ * offsets, rows, N, K and E as in bsmm_expert_gemm; fp8_type as in
+ * bsmm_linear_backward.  All pointers but offsets and rows 16-byte aligned;
+ * workspace bsmm_expert_backward_workspace_size() bytes, 256-byte aligned (the
+ * quantized operands).  S == 0 writes zeros to dW. */
+size_t bsmm_expert_backward_workspace_size(int64_t S, int64_t E, int64_t N, int64_t K);
+
+bsmm_status bsmm_expert_backward(int64_t S, int64_t X_rows, int64_t E, int64_t N, int64_t K, const void* dY,
+                                 const void* W, const void* X, const int32_t* offsets, const int32_t* rows,
+                                 bsmm_dtype fp8_type, void* dX, void* dW, void* workspace, size_t workspace_bytes,
+                                 bsmm_stream_t stream);
+
+/* out[t] = sum over j of weights[t, j] y[slots[t, j]], in binary32, rounded once.
+ *   y [S, N] bfloat16; slots [T, k]; a slot outside [0, S) has no part.
+ *   weights binary32 [T, k], or NULL for 1.  out [T, N] F32 or BF16.
+ *   k up to 32; any N >= 1; pointers aligned to their elements. */
+bsmm_status bsmm_expert_combine(int64_t T, int64_t S, int k, int64_t N, const void* y, const int32_t* slots,
+                                const float* weights, void* out, bsmm_dtype out_type, bsmm_stream_t stream);
+
+/* Its backward pass, from d_out [T, N] of type d_type (F32 or BF16):
+ *   dy[slots[t, j]] = weights[t, j] d_out[t]    bfloat16 [S, N]
+ *   d_weights[t, j] = sum over n of d_out[t, n] y[slots[t, j], n]   (0 without a slot)
+ * d_weights (binary32 [T, k]) may be NULL, and is with weights NULL.  No slot
+ * may occur twice; those that do not occur are left as they are in dy. */
+bsmm_status bsmm_expert_combine_backward(int64_t T, int64_t S, int k, int64_t N, const void* d_out, bsmm_dtype d_type,
+                                         const void* y, const int32_t* slots, const float* weights, void* dy,
+                                         float* d_weights, bsmm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* AdamW over many tensors                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* One step of AdamW on `count` tensors, launched together (up to 96 a launch).
+ * No counterpart on the pages.  In binary32, every operation rounded on its
+ * own, with b1, b2 and c = 1 - b rounded from binary64:
+ *
+ *   g = grad_scale grad                m = b1 m + c1 g
+ *   v = b2 v + (c2 g) g                d = sqrt(v) root2 + eps
+ *   p = p decay - rate (m / d)
+ *   decay = 1 - lr weight_decay, rate = lr / (1 - beta1^step),
+ *   root2 = 1 / sqrt(1 - beta2^step), each computed in binary64 and rounded once.
+ *
+ *   n        numbers of each tensor; the arrays of pointers have count entries
+ *            and are read, like n, during the call (host memory).
+ *   p        parameters of type p_type (F32 or BF16), grads of type g_type.
+ *   m, v     state_type F32: binary32.  E4M3: codes of m and of sqrt(v), each
+ *            with a binary32 scale per 128 consecutive numbers (m_scales,
+ *            v_scales: ceil(n / 128); the last block may be shorter), scale =
+ *            max(absmax * binary32(1 / 448), 2^-126), 1 for a block of zeros; the codes are
+ *            bsmm_quantize's for that scale, but a root that is not zero never
+ *            rounds to zero (a second moment lost beside a first moment that is
+ *            not would divide by eps).  Codes and scales of zeros start a run.
+ *   copies   NULL, or bfloat16 copies of the updated parameters (what the GEMMs
+ *            read); single entries may be NULL.
+ *   step     from 1 on.  lr, weight_decay, eps >= 0; 0 <= beta < 1.
+ *   hyper    NULL, or three binary32 numbers on the device, lr, step and
+ *            grad_scale, which are read when the call's kernels run and take
+ *            the place of the arguments: a captured call's schedule.
+ * Tensors are updated in place; no two may overlap.  Inputs are taken to be
+ * finite.  Pointers aligned to their elements. */
+bsmm_status bsmm_adamw(int64_t count, const int64_t* n, void* const* p, bsmm_dtype p_type, const void* const* grads,
+                       bsmm_dtype g_type, void* const* m, void* const* v, bsmm_dtype state_type,
+                       float* const* m_scales, float* const* v_scales, void* const* copies, double lr, double beta1,
+                       double beta2, double eps, double weight_decay, int64_t step, double grad_scale,
+                       const float* hyper, bsmm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
