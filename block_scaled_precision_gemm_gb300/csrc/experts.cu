@@ -25,9 +25,10 @@
 //   warp 0      TMA: A, its scale atoms, B (by box, or by gathered rows)
 //   warp 1      MMA (leader)
 //   warps 2, 3  B's scales: from row-major bytes (any rows, gathered too) or
-//               from atoms into shared memory, four contraction blocks at a
-//               time (one release to the leader per 512 columns: a release at
-//               cluster scope is about 1.2k cycles, four blocks' MMAs 2.2k)
+//               from atoms into shared memory, eight contraction blocks at a
+//               time: a row's 32 bytes are one sector, and the release to the
+//               leader, about 1.2k cycles at cluster scope, comes once in
+//               eight blocks' 4k cycles of MMAs
 //   warps 4-19  epilogue: accumulator -> registers -> bfloat16 rows
 // Sums are FP32 over the whole contraction and are rounded to bfloat16 once.
 // Every wait is bounded; on expiry a CTA records the site and winds down.
@@ -50,7 +51,7 @@ constexpr int STAGES = 6;
 constexpr int THREADS = 640;
 constexpr int EPI_WARPS = 16;
 constexpr int A_BYTES = 128 * KB, B_BYTES = 128 * KB, SFA_BYTES = 512;
-constexpr int SG = 4;        // contraction blocks per group of B's scales
+constexpr int SG = 8;        // contraction blocks per group of B's scales
 constexpr int SGROUPS = 2;
 constexpr int SFB_TILE = 1024;  // two atoms
 constexpr int TMEM_COLS = 512, SF_COL0 = 256, SF_COLS = 12;
@@ -60,7 +61,7 @@ constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
 constexpr int OFF_SFA = OFF_B + STAGES * B_BYTES;
 constexpr int OFF_SFB = OFF_SFA + STAGES * SFA_BYTES;
 constexpr int OFF_TILES = OFF_SFB + SGROUPS * SG * SFB_TILE;
-constexpr int OFF_BAR = OFF_TILES + ((kExpertsMax + 1) * 4 + 15) / 16 * 16;
+constexpr int OFF_BAR = OFF_TILES + ((kExpertsMax + 1) * 12 + 15) / 16 * 16;  // starts and segments
 constexpr int N_BARS = 2 * STAGES + 2 + 2 * SGROUPS + 1;
 constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16 + 1024;
 static_assert(SMEM <= 232448, "shared memory budget");
@@ -82,7 +83,7 @@ struct ExpertParams {
   int X;              // rows of B
   const uint8_t* b_scales;  // row-major [X][C / 32], or B's atoms (grad)
   int64_t b_pitch;
-  int b_vec;          // rows of b_scales are 16-byte aligned
+  int b_vec, b_word;  // rows of b_scales are 16-byte (4-byte) aligned
   // segments are the contraction (grad): B has J rows per expert, A and B hold
   // the segments padded to multiples of 128 from pads[e] on
   int J, j_tiles;
@@ -106,7 +107,7 @@ __device__ __forceinline__ int2 segment(const int* offsets, int e, int S) {
 }
 
 template <bool GRAD>
-__device__ __forceinline__ Tile tile_of(const ExpertParams& p, const int* starts, int u) {
+__device__ __forceinline__ Tile tile_of(const ExpertParams& p, const int* starts, const int2* segs, int u) {
   Tile t;
   if constexpr (GRAD) {
     const int per = p.j_tiles * p.f_tiles;
@@ -126,7 +127,7 @@ __device__ __forceinline__ Tile tile_of(const ExpertParams& p, const int* starts
       if (starts[mid] <= u) lo = mid; else hi = mid;
     }
     t.e = lo;
-    const int2 s = segment(p.offsets, lo, p.S);
+    const int2 s = segs[lo];
     const int j_tiles = (s.y - s.x + PJ - 1) / PJ;
     const int r = u - starts[lo];
     const int f = r / j_tiles;
@@ -140,6 +141,10 @@ __device__ __forceinline__ Tile tile_of(const ExpertParams& p, const int* starts
   t.nn = (t.live + 31) & ~31;
   return t;
 }
+
+// A value that all lanes hold, in a form that the compiler knows to be
+// warp-uniform.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -157,7 +162,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* sB = smem + OFF_B;
   uint8_t* sSFA = smem + OFF_SFA;
   uint8_t* sSFB = smem + OFF_SFB;
-  int* starts = reinterpret_cast<int*>(smem + OFF_TILES);
+  int2* segs = reinterpret_cast<int2*>(smem + OFF_TILES);
+  int* starts = reinterpret_cast<int*>(segs + kExpertsMax);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
@@ -171,8 +177,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* never_abort = &never_abort_storage;
   __shared__ int warp_sums[THREADS / 32];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  // broadcasts, so that the compiler knows them to be warp-uniform
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t rank = __shfl_sync(0xffffffffu, cluster_ctarank(), 0);
   const bool leader = rank == 0;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
@@ -209,6 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       n[i] = 0;
       if (e < p.E) {
         const int2 s = segment(p.offsets, e, p.S);
+        segs[e] = s;
         n[i] = (s.y - s.x + PJ - 1) / PJ * p.f_tiles;
       }
     }
@@ -239,16 +247,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp < 4) {
     if (warp == 0) {
       // ------------------------------------------------------- producer (both CTAs)
+      const uint32_t issue = elect_one();
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0), mine = smem_u32(full);
+      const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB), sfa0 = smem_u32(sSFA);
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_par = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       for (int u = cid; ok && u < tiles; u += ncl) {
-        const Tile t = tile_of<GRAD>(p, starts, u);
-        const int half = t.nn >> 1;
+        const Tile t = tile_of<GRAD>(p, starts, segs, u);
+        const int k_tiles = GRAD ? uniform(t.k_tiles) : p.k_tiles;
+        const int nn = uniform(t.nn), half = nn >> 1;
+        const int c0 = GRAD ? uniform(t.c0) : 0, f0 = uniform(t.f0), e = GRAD ? 0 : uniform(t.e);
         const uint32_t tx = 2 * (A_BYTES + SFA_BYTES + half * KB);
-        const int atom_row = GRAD ? 4 * ((2 * (t.f0 / PF) + static_cast<int>(rank)) * p.ks4 + t.c0 / KB)
-                                  : 4 * ((t.e * p.a_rt + 2 * (t.f0 / PF) + static_cast<int>(rank)) * p.ks4);
-        const int row0 = t.b0 + static_cast<int>(rank) * half;
+        const int atom_row = 4 * ((e * p.a_rt + 2 * (f0 / PF) + static_cast<int>(rank)) * p.ks4 + c0 / KB);
+        const int f_row = f0 + static_cast<int>(rank) * 128;
+        const int row0 = uniform(t.b0) + static_cast<int>(rank) * half;
         int r0 = 0, r1 = 0, r2 = 0, r3 = 0;
         if constexpr (GATHER) {
           // this lane's four rows; past the segment, and for a row that is
@@ -260,39 +273,34 @@ __global__ void __launch_bounds__(THREADS, 1)
           r2 = min(max(__ldg(p.rows + min(row0 + 4 * lane + 2, last)), 0), p.X - 1);
           r3 = min(max(__ldg(p.rows + min(row0 + 4 * lane + 3, last)), 0), p.X - 1);
         }
-        for (int kt = 0; kt < t.k_tiles; ++kt) {
-          if (GATHER || lane == 0)
-            ok = mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteProducer);
-          ok = __all_sync(0xffffffffu, ok);
+        for (int kt = 0; kt < k_tiles; ++kt) {
+          if (!ready)
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteProducer));
           if (!ok) break;
-          const uint32_t full_leader = mapa_shared(smem_u32(&full[stage]), 0);
-          const int x = t.c0 + kt * KB;
-          if (lane == 0) {
-            if (leader) mbar_arrive_expect_tx(&full[stage], tx);
-            tma_load_3d_pair(sA + stage * A_BYTES, &tmA, full_leader, x, t.f0 + static_cast<int>(rank) * 128,
-                             GRAD ? 0 : t.e);
-            tma_load_3d_pair(sSFA + stage * SFA_BYTES, &tmSFA, full_leader, 0, atom_row + 4 * kt, 0);
-            if constexpr (!GATHER) {
-              if (t.nn == PJ) {
-                tma_load_3d_pair(sB + stage * B_BYTES, &tmB, full_leader, x, row0, 0);
-              } else {
-                for (int i = 0; i < half; i += 16)
-                  tma_load_3d_pair(sB + stage * B_BYTES + i * KB, &tmB16, full_leader, x, row0 + i, 0);
-              }
-            }
-          }
+          const uint32_t bar = full0 + 8 * stage;
+          const int x = c0 + kt * KB;
+          if (leader) mbar_arrive_expect_tx_if(issue, mine + 8 * stage, tx);
+          tma_load_3d_pair_if(issue, a0 + stage * A_BYTES, &tmA, bar, x, f_row, e);
+          tma_load_3d_pair_if(issue, sfa0 + stage * SFA_BYTES, &tmSFA, bar, 0, atom_row + 4 * kt, 0);
           if constexpr (GATHER) {
             __syncwarp();
             if (4 * lane < half)
-              tma_gather4_pair(sB + stage * B_BYTES + lane * 4 * KB, &tmB, full_leader, x, r0, r1, r2, r3);
+              tma_gather4_pair(sB + stage * B_BYTES + lane * 4 * KB, &tmB, bar, x, r0, r1, r2, r3);
+          } else if (nn == PJ) {
+            tma_load_3d_pair_if(issue, b0 + stage * B_BYTES, &tmB, bar, x, row0, 0);
+          } else {
+            for (int i = 0; i < half; i += 16)
+              tma_load_3d_pair_if(issue, b0 + stage * B_BYTES + i * KB, &tmB16, bar, x, row0 + i, 0);
           }
-          if (!leader && lane == 0) mbar_arrive_cluster(full_leader);
+          if (!leader && lane == 0) mbar_arrive_cluster(bar);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
+          ready = __all_sync(0xffffffffu, mbar_test(&empty[stage], phase ^ 1u));
         }
       }
       // Every stage this CTA filled must have been released by the leader's
@@ -318,56 +326,61 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------- MMA issuer (leader)
-      if (leader && lane == 0) {
+      if (leader) {
+        // the whole warp, one lane of it issuing (elect_one)
+        const uint32_t issue = elect_one();
         int stage = 0, g = 0;
         uint32_t phase = 0, tph = 0, gph = 0;
-        bool ok = true;
+        bool ok = true, ready = false, scales_ready = false;
+        const uint64_t a_d0 = smem_desc(smem_u32(sA), 16, 1024, 2), b_d0 = smem_desc(smem_u32(sB), 16, 1024, 2);
+        const uint64_t sfa_d0 = smem_desc(smem_u32(sSFA), 0, 128, 0), sfb_d0 = smem_desc(smem_u32(sSFB), 0, 128, 0);
         for (int u = cid; ok && u < tiles; u += ncl) {
-          const Tile t = tile_of<GRAD>(p, starts, u);
-          if (t.k_tiles == 0) continue;
-          if (!mbar_wait(tempty, tph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteMmaTmem)) break;
+          const Tile t = tile_of<GRAD>(p, starts, segs, u);
+          const int k_tiles = GRAD ? uniform(t.k_tiles) : p.k_tiles;
+          const int nn = uniform(t.nn);
+          if (k_tiles == 0) continue;
+          if (!__all_sync(0xffffffffu, mbar_wait(tempty, tph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteMmaTmem))) break;
           tc_fence_after();
-          const uint32_t idesc0 = p.idesc | (static_cast<uint32_t>(t.nn >> 3) << 17);
-          for (int kt = 0; kt < t.k_tiles; ++kt) {
-            if (((kt & (SG - 1)) == 0 &&
-                 !mbar_wait_acq_cluster(&sfull[g], gph, p.timeout_ns, abort_flag, p.status, kSiteMmaScales)) ||
-                !mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag, p.status, kSiteMma)) {
-              ok = false;
-              break;
-            }
+          const uint32_t i0 = p.idesc | (static_cast<uint32_t>(nn >> 3) << 17);
+          const uint32_t i1 = i0 | (1u << 4) | (1u << 29), i2 = i0 | (2u << 4) | (2u << 29), i3 = i0 | (3u << 4) | (3u << 29);
+          for (int kt = 0; kt < k_tiles; ++kt) {
+            if ((kt & (SG - 1)) == 0 && !scales_ready)
+              ok = __all_sync(0xffffffffu, mbar_spin_acq_cluster(&sfull[g], gph, p.timeout_ns, abort_flag, p.status,
+                                                                 kSiteMmaScales));
+            if (ok && !ready)
+              ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag, p.status, kSiteMma));
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t a_d = smem_desc(smem_u32(sA + stage * A_BYTES), 16, 1024, 2);
-            const uint64_t b_d = smem_desc(smem_u32(sB + stage * B_BYTES), 16, 1024, 2);
+            const uint64_t a_d = desc_add(a_d0, stage * A_BYTES), b_d = desc_add(b_d0, stage * B_BYTES);
+            const uint64_t sfb_d = desc_add(sfb_d0, (g * SG + (kt & (SG - 1))) * SFB_TILE);
             const uint32_t sfa_t = tmem + static_cast<uint32_t>(SF_COL0 + stage * SF_COLS);
             const uint32_t sfb_t = sfa_t + 4;
-            tc_cp_sf_pair(sfa_t, smem_desc(smem_u32(sSFA + stage * SFA_BYTES), 0, 128, 0));
-            const uint64_t sfb_d = smem_desc(smem_u32(sSFB + (g * SG + (kt & (SG - 1))) * SFB_TILE), 0, 128, 0);
-            tc_cp_sf_pair(sfb_t, sfb_d);
-            if (t.nn > 128) tc_cp_sf_pair(sfb_t + 4, desc_add(sfb_d, 512));
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_mxf8_pair(tmem, desc_add(a_d, 32 * k), desc_add(b_d, 32 * k),
-                            idesc0 | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa_t, sfb_t,
-                            (kt > 0 || k > 0) ? 1u : 0u);
-            tc_commit_pair_mc(&empty[stage], 0x3);
+            tc_cp_sf_pair_if(issue, sfa_t, desc_add(sfa_d0, stage * SFA_BYTES));
+            tc_cp_sf_pair_if(issue, sfb_t, sfb_d);
+            if (nn > 128) tc_cp_sf_pair_if(issue, sfb_t + 4, desc_add(sfb_d, 512));
+            mma_mxf8_pair_x4_if(issue, tmem, a_d, b_d, i0, i1, i2, i3, sfa_t, sfb_t, kt > 0 ? 1u : 0u);
+            tc_commit_pair_mc_if(issue, &empty[stage], 0x3);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
             }
-            if ((kt & (SG - 1)) == SG - 1 || kt + 1 == t.k_tiles) {
-              tc_commit_pair_mc(&sempty[g], 0x3);
+            // looked at a block ahead, so that its latency passes meanwhile
+            ready = __all_sync(0xffffffffu, mbar_test(&full[stage], phase));
+            if ((kt & (SG - 1)) == SG - 1 || kt + 1 == k_tiles) {
+              tc_commit_pair_mc_if(issue, &sempty[g], 0x3);
               if (++g == SGROUPS) {
                 g = 0;
                 gph ^= 1u;
               }
+              scales_ready = __all_sync(0xffffffffu, mbar_test_acq_cluster(&sfull[g], gph));
             }
           }
           if (!ok) break;
-          tc_commit_pair_mc(tfull, 0x3);
+          tc_commit_pair_mc_if(issue, tfull, 0x3);
           tph ^= 1u;
         }
-        tc_commit_pair_mc(done, 0x1);
-        mbar_wait(done, 0, p.timeout_ns, never_abort, p.status, kSiteDone);
+        tc_commit_pair_mc_if(issue, done, 0x1);
+        if (issue) mbar_wait(done, 0, p.timeout_ns, never_abort, p.status, kSiteDone);
       }
       __syncwarp();
     } else {
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t gph = 0, used = 0, last_par = 0;
       bool ok = true;
       for (int u = cid; ok && u < tiles; u += ncl) {
-        const Tile t = tile_of<GRAD>(p, starts, u);
+        const Tile t = tile_of<GRAD>(p, starts, segs, u);
         const bool mine = t.nn > 128 * a;
         const uint8_t* src[4] = {nullptr, nullptr, nullptr, nullptr};
         if (mine) {
@@ -395,29 +408,38 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
-        for (int k0 = 0; k0 < t.k_tiles; k0 += SG) {
-          uint4 w[SG];
-          if (mine) {
-            if constexpr (GRAD) {
+        // the words of the group from block k0 on, as this lane stores them
+        uint4 w[SG];
+        auto load = [&](int k0) {
+          if (!mine || k0 >= t.k_tiles) return;
+          if constexpr (GRAD) {
 #pragma unroll
-              for (int j = 0; j < SG; ++j)
-                if (k0 + j < t.k_tiles) w[j] = __ldg(reinterpret_cast<const uint4*>(src[0] + (k0 + j) * 512));
-            } else if (p.b_vec && k0 + SG <= t.k_tiles) {
+            for (int j = 0; j < SG; ++j)
+              if (k0 + j < t.k_tiles) w[j] = __ldg(reinterpret_cast<const uint4*>(src[0] + (k0 + j) * 512));
+          } else if (p.b_vec && k0 + SG <= t.k_tiles) {
+#pragma unroll
+            for (int h = 0; h < SG; h += 4) {
               uint4 v[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + 4 * k0));
-              w[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
-              w[1] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
-              w[2] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
-              w[3] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
-            } else {
-              // bytes; past the contraction the neutral scale
-              const int blocks = p.C / 32;
+              for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + 4 * (k0 + h)));
+              w[h] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+              w[h + 1] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+              w[h + 2] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+              w[h + 3] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+            }
+          } else {
+            // words where a row's scales are whole ones, else bytes; past the
+            // contraction the neutral scale
+            const int blocks = p.C / 32;
 #pragma unroll
-              for (int j = 0; j < SG; ++j) {
-                uint32_t v[4];
+            for (int j = 0; j < SG; ++j) {
+              if (k0 + j >= t.k_tiles) break;
+              uint32_t v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 4; ++i) {
+                if (p.b_word) {
+                  v[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i]) + k0 + j);
+                } else {
                   v[i] = 0;
 #pragma unroll
                   for (int b = 0; b < 4; ++b) {
@@ -425,11 +447,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     v[i] |= (kb < blocks ? static_cast<uint32_t>(__ldg(src[i] + kb)) : 127u) << (8 * b);
                   }
                 }
-                w[j] = make_uint4(v[0], v[1], v[2], v[3]);
               }
+              w[j] = make_uint4(v[0], v[1], v[2], v[3]);
             }
           }
-          if (!mbar_wait(&sempty[g], gph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteScales)) ok = false;
+        };
+        load(0);
+        for (int k0 = 0; k0 < t.k_tiles; k0 += SG) {
+          if (lane == 0) ok = mbar_poll(&sempty[g], gph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteScales);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (mine) {
@@ -439,6 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (k0 + j < t.k_tiles) *reinterpret_cast<uint4*>(dst + j * SFB_TILE) = w[j];
           }
           fence_proxy_async_smem();
+          load(k0 + SG);  // in flight while the release takes its time
           __syncwarp();
           if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[g]), 0));
           used |= 1u << g;
@@ -465,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool odd = lane & 1;
     uint32_t tph = 0;
     for (int u = cid; u < tiles; u += ncl) {
-      const Tile t = tile_of<GRAD>(p, starts, u);
+      const Tile t = tile_of<GRAD>(p, starts, segs, u);
       const int f = t.f0 + static_cast<int>(rank) * 128 + q * 32 + (lane & ~1);
       const int live = f < p.F ? min(t.live - g * 64, 64) : 0;
       // lane pairs exchange halves: even lanes store even rows, odd lanes odd
@@ -813,6 +839,7 @@ cudaError_t launch_segments(int E, int F, int C, int64_t a_pitch, const void* a,
   p.b_scales = b_scales;
   p.b_pitch = C / 32;
   p.b_vec = p.b_pitch % 16 == 0 && reinterpret_cast<uintptr_t>(b_scales) % 16 == 0;
+  p.b_word = p.b_pitch % 4 == 0 && reinterpret_cast<uintptr_t>(b_scales) % 4 == 0;
   p.y = static_cast<__nv_bfloat16*>(y);
   p.idesc = idesc;
   CUtensorMap ta, tsa, tb, tb16;

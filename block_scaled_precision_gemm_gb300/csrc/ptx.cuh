@@ -490,6 +490,64 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, u
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
       : "memory");
 }
+// The issuing instructions below in a form that a whole converged warp
+// executes and one lane (issue != 0) performs: the branch to one thread is a
+// predicate, so that descriptors and loop counters stay warp-uniform values.
+// (Issued from a one-thread branch, a stage's three copies, four MMAs and
+// commit took 540 cycles of moving operands into uniform registers.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+// The four MMAs of a 128-byte contraction block: operand descriptors 32 bytes
+// apart, i0 .. i3 the instruction descriptors with scale bytes 0 .. 3.
+__device__ __forceinline__ void mma_mxf8_pair_x4_if(uint32_t issue, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                    uint32_t i0, uint32_t i1, uint32_t i2, uint32_t i3,
+                                                    uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 q, %10, 0;\n setp.ne.b32 p, %9, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%7], [%8], p;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], a, b, %4, [%7], [%8], t;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], a, b, %5, [%7], [%8], t;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n"
+      " @q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], a, b, %6, [%7], [%8], t;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(i0), "r"(i1), "r"(i2), "r"(i3), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate),
+      "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair_if(uint32_t issue, uint32_t dst, const CUtensorMap* tm,
+                                                    uint32_t mbar_cluster_addr, int x, int y, int z) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
+      " @q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];\n}\n" ::"r"(dst),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(mbar_cluster_addr), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t issue, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+      "r"(bytes), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void tc_cp_sf_pair_if(uint32_t issue, uint32_t taddr, uint64_t sdesc) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(taddr),
+      "l"(sdesc), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair_mc_if(uint32_t issue, uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+          smem_u32(bar)),
+      "h"(mask), "r"(issue)
+      : "memory");
+}
 // Scale-factor copy (32 rows x 128 bits, replicated to the four lane
 // quarters) issued by the leader of a CTA pair: each CTA's tensor memory
 // receives the atom at the same shared-memory offset of that CTA.
