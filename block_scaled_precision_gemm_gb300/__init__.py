@@ -45,7 +45,7 @@ __all__ = [
     "gated_act", "gated_act_backward", "linear_backward_checkpoint", "adapters", "adapters_backward",
     "adapters_workspace_size", "adapters_backward_workspace_size",
     "route", "route_backward", "expert_gemm", "expert_backward", "expert_combine", "expert_combine_backward", "adamw",
-    "route_workspace_size", "expert_backward_workspace_size",
+    "route_workspace_size", "expert_gemm_workspace_size", "expert_backward_workspace_size",
     "set_wait_timeout_ns", "version",
     "F32", "BF16", "E4M3", "E5M2", "E2M1", "INT8", "SCALE_F32", "SCALE_UE8M0", "SCALE_UE4M3",
 ]
@@ -133,7 +133,8 @@ _SIGS = {
     "bsmm_route_workspace_size": ([_I64, _I64], _SZ),
     "bsmm_route": ([_I64, _I64, _INT, _P, _INT, _I64, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P], _INT),
     "bsmm_route_backward": ([_I64, _I64, _INT, _P, _INT, _I64, _INT, _P, _P, _P, _P, _P], _INT),
-    "bsmm_expert_gemm": ([_I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _P, _P], _INT),
+    "bsmm_expert_gemm_workspace_size": ([_I64, _I64, _I64, _INT], _SZ),
+    "bsmm_expert_gemm": ([_I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _P, _P, _SZ, _P], _INT),
     "bsmm_expert_backward_workspace_size": ([_I64, _I64, _I64, _I64], _SZ),
     "bsmm_expert_backward": ([_I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _INT, _P, _P, _P, _SZ, _P], _INT),
     "bsmm_expert_combine": ([_I64, _I64, _INT, _I64, _P, _P, _P, _P, _INT, _P], _INT),
@@ -1082,7 +1083,12 @@ def route_backward(d_weights, logits, ids, weights, renormalize=True, d_logits=N
     return d_logits
 
 
-def expert_gemm(x, x_scales, w, w_atoms, offsets, rows=None, x_type="e4m3", w_type="e4m3", y=None, stream=None):
+def expert_gemm_workspace_size(S, E, K, by_rows=True) -> int:
+    return lib().bsmm_expert_gemm_workspace_size(S, E, K, 1 if by_rows else 0)
+
+
+def expert_gemm(x, x_scales, w, w_atoms, offsets, rows=None, x_type="e4m3", w_type="e4m3", y=None, workspace=None,
+                stream=None):
     """``y[s] = w[e] @ x[rows[s]]`` for the slots ``offsets[e] <= s <
     offsets[e + 1]`` of every expert ``e``, MXFP8: y [S, N] bfloat16.
 
@@ -1104,12 +1110,18 @@ def expert_gemm(x, x_scales, w, w_atoms, offsets, rows=None, x_type="e4m3", w_ty
     S = _expert_slots(offsets, rows, E, X)
     if y is not None:
         _want(y, "y", (S, N), dtypes=_BF16)
-    dev = _on_device(x=x, x_scales=x_scales, w=w, w_atoms=w_atoms, offsets=offsets, rows=rows, y=y)
+    if workspace is not None:
+        _want(workspace, "workspace")
+    dev = _on_device(x=x, x_scales=x_scales, w=w, w_atoms=w_atoms, offsets=offsets, rows=rows, y=y, workspace=workspace)
     if y is None:
         y = _empty((S, N), torch.bfloat16, dev, stream)
+    if workspace is None and rows is not None:
+        need = expert_gemm_workspace_size(S, E, K)
+        if need:
+            workspace = _scratch(need, dev, stream)
     _check(lib().bsmm_expert_gemm(S, X, E, N, K, x.data_ptr(), xt, x_scales.data_ptr(), w.data_ptr(), wt,
-                                  w_atoms.data_ptr(), offsets.data_ptr(), _at(rows), y.data_ptr(),
-                                  _raw_stream(stream, dev)), "bsmm_expert_gemm")
+                                  w_atoms.data_ptr(), offsets.data_ptr(), _at(rows), y.data_ptr(), _at(workspace),
+                                  _nbytes(workspace), _raw_stream(stream, dev)), "bsmm_expert_gemm")
     return y
 
 

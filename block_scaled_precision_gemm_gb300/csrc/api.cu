@@ -988,9 +988,15 @@ bsmm_status bsmm_route_backward(int64_t T, int64_t E, int k, const void* logits,
   return launched(launch_route_backward(r, reinterpret_cast<cudaStream_t>(stream)), "route backward launch");
 }
 
+size_t bsmm_expert_gemm_workspace_size(int64_t S, int64_t E, int64_t K, int by_rows) {
+  if (S <= 0 || E <= 0 || K <= 0 || !by_rows) return 0;
+  return expert_gemm_bytes(S, E, K);
+}
+
 bsmm_status bsmm_expert_gemm(int64_t S, int64_t X, int64_t E, int64_t N, int64_t K, const void* x, bsmm_dtype x_type,
                              const void* x_scales, const void* w, bsmm_dtype w_type, const void* w_atoms,
-                             const int32_t* offsets, const int32_t* rows, void* y, bsmm_stream_t stream) {
+                             const int32_t* offsets, const int32_t* rows, void* y, void* workspace,
+                             size_t workspace_bytes, bsmm_stream_t stream) {
   if ((x_type != BSMM_E4M3 && x_type != BSMM_E5M2) || (w_type != BSMM_E4M3 && w_type != BSMM_E5M2))
     return fail(BSMM_ERR_INVALID_ARG, "x_type and w_type must be E4M3 or E5M2");
   const bsmm_status st = expert_sizes(S, X, E, N, K, rows != nullptr);
@@ -1003,8 +1009,11 @@ bsmm_status bsmm_expert_gemm(int64_t S, int64_t X, int64_t E, int64_t N, int64_t
   if (!aligned16(x) || !aligned16(w) || !aligned16(w_atoms) || !aligned16(y) || !aligned_to(offsets, 4) ||
       !aligned_to(rows, 4))
     return fail(BSMM_ERR_ALIGNMENT, "x, w, w_atoms and y must be 16-byte aligned, offsets and rows 4-byte");
+  const size_t need = bsmm_expert_gemm_workspace_size(S, E, K, rows != nullptr);
+  if (need && (!workspace || workspace_bytes < need || !aligned_to(workspace, 256)))
+    return fail(BSMM_ERR_WORKSPACE, "workspace must be 256-byte aligned and at least " + std::to_string(need) + " bytes");
   const ExpertGemmRequest r{S, X, E, N, K, x, x_type, static_cast<const uint8_t*>(x_scales), w, w_type, w_atoms, offsets,
-                            rows, y};
+                            rows, y, workspace};
   return launched(launch_expert_gemm(r, reinterpret_cast<cudaStream_t>(stream)), "expert gemm launch");
 }
 

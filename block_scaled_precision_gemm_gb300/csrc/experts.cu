@@ -543,6 +543,44 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
+// Rows gathered ahead of the product
+// ---------------------------------------------------------------------------
+// x's codes and scales by slot.  The TMA's gather of four rows at a time takes
+// about 70 cycles an instruction and a CTA, and is paid again for every tile of
+// features, so from 64 rows a tile on it outlasts the MMAs; a pass ahead costs
+// about 8 us and the copy's bytes.  Measured (us, gathered by the producer /
+// ahead; 32 experts of 4096 x 2048): 48 rows an expert 68 / 76, 64 78 / 76, 128
+// 105 / 78, 256 214 / 95; 8 experts of 2048 x 4096: 48 rows 29 / 35, 128 37 / 37,
+// 256 87 / 48.  Rows that crowd on few experts move the crossing down (32
+// experts, 48 rows: 80 / 74), so it is set at 48 rows an expert.
+__global__ void __launch_bounds__(256) expert_gather(const uint8_t* x, const uint8_t* scales, const int* rows, int S,
+                                                     int X, int K, uint8_t* out, uint8_t* out_scales) {
+  const int units = K / 16, blocks = K / 32;
+  const int lane = threadIdx.x & 31;
+  for (int s = blockIdx.x * 8 + (threadIdx.x >> 5); s < S; s += gridDim.x * 8) {
+    const int row = min(max(__ldg(rows + s), 0), X - 1);
+    const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(row) * K);
+    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(s) * K);
+    int i = lane;
+    for (; i + 96 < units; i += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __ldg(src + i + 32 * j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dst[i + 32 * j] = v[j];
+    }
+    for (; i < units; i += 32) dst[i] = __ldg(src + i);
+    const uint8_t* ssrc = scales + static_cast<int64_t>(row) * blocks;
+    uint8_t* sdst = out_scales + static_cast<int64_t>(s) * blocks;
+    if (blocks % 4 == 0 && reinterpret_cast<uintptr_t>(scales) % 4 == 0)
+      for (int j = lane; j < blocks / 4; j += 32)
+        reinterpret_cast<uint32_t*>(sdst)[j] = __ldg(reinterpret_cast<const uint32_t*>(ssrc) + j);
+    else
+      for (int j = lane; j < blocks; j += 32) sdst[j] = __ldg(ssrc + j);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // The backward's operands
 // ---------------------------------------------------------------------------
 // Padded starts of the segments (multiples of 128) and, per padded tile of 128
@@ -888,10 +926,41 @@ BackwardParts backward_parts(int64_t S, int64_t E, int64_t N, int64_t K) {
 
 }  // namespace
 
+// Whether rows are gathered ahead of the product: above 48 rows an expert, see
+// expert_gather.
+bool expert_gathers_ahead(int64_t S, int64_t E) { return S > 48 * E; }
+
+size_t expert_gemm_bytes(int64_t S, int64_t E, int64_t K) {
+  if (!expert_gathers_ahead(S, E)) return 0;
+  return align_up(static_cast<size_t>(S) * K, 256) + align_up(static_cast<size_t>(S) * (K / 32), 256);
+}
+
 cudaError_t launch_expert_gemm(const ExpertGemmRequest& r, cudaStream_t s) {
-  return launch_segments(static_cast<int>(r.E), static_cast<int>(r.N), static_cast<int>(r.K), r.K, r.w, r.w_atoms, r.x,
-                         r.x_scales, static_cast<int>(r.S), static_cast<int>(r.X), r.offsets, r.rows, r.y,
-                         expert_idesc(r.w_type, r.x_type), r.rows ? "expert_gemm (gathered)" : "expert_gemm", s);
+  const void* x = r.x;
+  const uint8_t* scales = r.x_scales;
+  const int* rows = r.rows;
+  int64_t X = r.X;
+  if (rows && expert_gathers_ahead(r.S, r.E)) {
+    const DeviceCtx* ctx = device_ctx();
+    if (!ctx) return cudaErrorInitializationError;
+    uint8_t* codes = static_cast<uint8_t*>(r.workspace);
+    uint8_t* sc = codes + align_up(static_cast<size_t>(r.S) * r.K, 256);
+    {
+      TraceScope tr("expert_gather", s);
+      expert_gather<<<static_cast<unsigned>(std::min<int64_t>(ceil_div(r.S, 8), 8 * ctx->num_sms)), 256, 0, s>>>(
+          static_cast<const uint8_t*>(x), scales, rows, static_cast<int>(r.S), static_cast<int>(X), static_cast<int>(r.K),
+          codes, sc);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    x = codes;
+    scales = sc;
+    rows = nullptr;
+    X = r.S;
+  }
+  return launch_segments(static_cast<int>(r.E), static_cast<int>(r.N), static_cast<int>(r.K), r.K, r.w, r.w_atoms, x,
+                         scales, static_cast<int>(r.S), static_cast<int>(X), r.offsets, rows, r.y,
+                         expert_idesc(r.w_type, r.x_type), rows ? "expert_gemm (gathered)" : "expert_gemm", s);
 }
 
 size_t expert_backward_bytes(int64_t S, int64_t E, int64_t N, int64_t K) { return backward_parts(S, E, N, K).total; }

@@ -201,7 +201,9 @@ struct ExpertGemmRequest {
   const int* offsets;  // [E + 1]
   const int* rows;     // null: row s of x
   void* y;             // [S][N] bf16
+  void* workspace;     // expert_gemm_bytes, with rows
 };
+size_t expert_gemm_bytes(int64_t S, int64_t E, int64_t K);
 cudaError_t launch_expert_gemm(const ExpertGemmRequest& r, cudaStream_t s);
 
 struct ExpertBackwardRequest {

@@ -662,10 +662,16 @@ bsmm_status bsmm_route_backward(int64_t T, int64_t E, int k, const void* logits,
  *            [0, X) gives unspecified values in its own slot.
  *   y [S, N] bfloat16.
  *   N and K multiples of 32; E up to 1024; codes, w_atoms and y 16-byte
- *            aligned, offsets and rows 4-byte. */
+ *            aligned, offsets and rows 4-byte.
+ *   workspace  bsmm_expert_gemm_workspace_size() bytes, 256-byte aligned: many
+ *            rows are gathered ahead of the product (0 otherwise; by_rows says
+ *            whether rows is given). */
+size_t bsmm_expert_gemm_workspace_size(int64_t S, int64_t E, int64_t K, int by_rows);
+
 bsmm_status bsmm_expert_gemm(int64_t S, int64_t X, int64_t E, int64_t N, int64_t K, const void* x, bsmm_dtype x_type,
                              const void* x_scales, const void* w, bsmm_dtype w_type, const void* w_atoms,
-                             const int32_t* offsets, const int32_t* rows, void* y, bsmm_stream_t stream);
+                             const int32_t* offsets, const int32_t* rows, void* y, void* workspace,
+                             size_t workspace_bytes, bsmm_stream_t stream);
 
 /* bsmm_linear_backward by expert, from bfloat16 dY [S, N], W [E, N, K] and
  * X [X_rows, K]:

@@ -143,10 +143,11 @@ def test_route_backward_library(lib, change, want):
     (dict(E=1025), bsmm.ERR_UNSUPPORTED), (dict(X=9), bsmm.ERR_SHAPE), (dict(X=0, rows=fake), bsmm.ERR_SHAPE),
     (dict(E=1024, N=1 << 20, K=1 << 20), bsmm.ERR_SHAPE), (dict(S=(1 << 30) + 1, X=(1 << 30) + 1), bsmm.ERR_SHAPE),
     (dict(x=None), bsmm.ERR_INVALID_ARG), (dict(off=None), bsmm.ERR_INVALID_ARG), (dict(x=ctypes.c_void_p(4104)), bsmm.ERR_ALIGNMENT),
-    (dict(rows=odd), bsmm.ERR_ALIGNMENT), (dict(S=0, x=None, y=None), bsmm.OK)])
+    (dict(rows=odd), bsmm.ERR_ALIGNMENT), (dict(S=4000, rows=fake), bsmm.ERR_WORKSPACE),
+    (dict(S=4000, rows=fake, ws=fake, wb=64), bsmm.ERR_WORKSPACE), (dict(S=0, x=None, y=None), bsmm.OK)])
 def test_expert_gemm_library(lib, change, want):
     assert status(lib.bsmm_expert_gemm, dict(S=10, X=10, E=4, N=64, K=128, x=fake, xt=bsmm.E4M3, xs=fake, w=fake, wt=bsmm.E4M3,
-                                             a=fake, off=fake, rows=None, y=fake, stream=None), change) == want
+                                             a=fake, off=fake, rows=None, y=fake, ws=None, wb=0, stream=None), change) == want
 
 
 @pytest.mark.parametrize("change,want", [
@@ -198,6 +199,8 @@ def test_adamw_library(lib, change, want):
 def test_workspace_queries(lib):
     assert bsmm.route_workspace_size(4, 64) == 0  # few tokens take one launch
     assert bsmm.route_workspace_size(100000, 64) > 0 and bsmm.route_workspace_size(0, 64) == 0
+    assert bsmm.expert_gemm_workspace_size(8, 4, 64) == 0 and bsmm.expert_gemm_workspace_size(4000, 4, 64, False) == 0
+    assert bsmm.expert_gemm_workspace_size(4000, 4, 64) >= 4000 * 66
     assert bsmm.expert_backward_workspace_size(0, 4, 64, 64) == 0
     assert bsmm.expert_backward_workspace_size(100, 4, 64, 64) >= 100 * 64 + 4 * 64 * 64 + 2 * 64 * 100
 

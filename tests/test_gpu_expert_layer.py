@@ -217,14 +217,15 @@ def test_nothing_is_written_outside(T, k, E, N, K):
     x, xs = bsmm.quantize(xv, (1, 32), "e4m3", "ue8m0")
     wq, wa = bsmm.quantize_atoms(W.view(E * N, K), batches=E)
     y = Guarded((S, N), b16)
-    bsmm.expert_gemm(x, xs, wq.view(E, N, K), wa, off.t, rows=rows.t, y=y.t)
+    gw = Guarded((max(bsmm.expert_gemm_workspace_size(S, E, K), 256),), torch.uint8)
+    bsmm.expert_gemm(x, xs, wq.view(E, N, K), wa, off.t, rows=rows.t, y=y.t, workspace=gw.t)
     dX, dW = Guarded((S, K), b16), Guarded((E, N, K), b16)
     bw = Guarded((bsmm.expert_backward_workspace_size(S, E, N, K),), torch.uint8)
     bsmm.expert_backward(dY, W, xv, off.t, rows=rows.t, dX=dX.t, dW=dW.t, workspace=bw.t)
     out, dy, dw = Guarded((T, N), b16), Guarded((S, N), b16), Guarded((T, k), f32)
     bsmm.expert_combine(y.t, slots.t, w.t, out=out.t)
     bsmm.expert_combine_backward(rnd(T, N), y.t, slots.t, w.t, dy=dy.t, d_weights=dw.t)
-    for m in (w, ids, off, rows, slots, ws, dl, y, dX, dW, bw, out, dy, dw):
+    for m in (w, ids, off, rows, slots, ws, dl, y, gw, dX, dW, bw, out, dy, dw):
         m.check()
     n = 5 * T + 3
     ts = [Guarded((n,), t) for t in (f32, b16, torch.uint8, torch.uint8, b16)]
