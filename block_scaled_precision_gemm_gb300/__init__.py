@@ -1227,34 +1227,65 @@ def expert_combine_backward(d_out, y, slots, weights=None, dy=None, d_weights=No
 # AdamW                                                                       #
 # --------------------------------------------------------------------------- #
 
-def _tensor_list(ts, name, sizes, dtypes=None, itemsize=None):
+def _lists():
+    """The compiled part of the binding."""
+    global _LISTS
+    if _LISTS is None:
+        try:
+            from . import _tensor_lists
+        except ImportError as e:
+            raise RuntimeError("_tensor_lists.so is missing: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _LISTS = _tensor_lists
+    return _LISTS
+
+
+_LISTS = None
+
+
+def _tensor_list(ts, name, sizes, per=1, dtypes=None, itemsize=None):
     """A list of contiguous CUDA tensors of one type, on the current device:
-    their addresses and that type.  Whole lists are checked at a time, as an
-    optimizer's many small tensors spend their time on the host."""
+    their addresses and sizes (64-bit words) and that type.  ``sizes``: those of
+    another list, of which each tensor holds ceil(size / per) numbers."""
+    ts = list(ts)
+    dev = ts[0].get_device() if ts and isinstance(ts[0], torch.Tensor) else -1
+    found = None
+    if not ts or (dev >= 0 and dev == torch._C._cuda_getDevice()):
+        found = _lists().addresses(ts, dev, sizes, per)
+    if found is None or (ts and not _list_type(found[2], dtypes, itemsize)):
+        _explain_list(ts, name, sizes, per, dtypes, itemsize)
+    return found
+
+
+def _list_type(dtype, dtypes, itemsize) -> bool:
+    return (dtypes is None or dtype in dtypes) and (itemsize is None or dtype.itemsize == itemsize)
+
+
+def _explain_list(ts, name, sizes, per, dtypes, itemsize):
+    """Raises for what is wrong with a list of tensors."""
     for t in ts:
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must hold torch.Tensors")
     kinds = {t.dtype for t in ts}
     if len(kinds) > 1:
         raise ValueError(f"{name} must be of one type, got {' and '.join(sorted(str(k) for k in kinds))}")
-    dtype = next(iter(kinds), None)
-    if dtype is not None and dtypes is not None and dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
-    if dtype is not None and itemsize is not None and dtype.itemsize != itemsize:
-        raise ValueError(f"{name} must have {itemsize}-byte elements, got {dtype}")
+    for dtype in kinds:
+        if not _list_type(dtype, dtypes, None):
+            raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dtype}")
+        if not _list_type(dtype, None, itemsize):
+            raise ValueError(f"{name} must have {itemsize}-byte elements, got {dtype}")
     if sizes is not None:
-        got = list(map(torch.Tensor.numel, ts))
-        if got != sizes:
-            if len(got) != len(sizes):
-                raise ValueError(f"{name} holds {len(got)} tensors, {len(sizes)} needed")
-            i = next(i for i in range(len(got)) if got[i] != sizes[i])
-            raise ValueError(f"{name}[{i}] holds {got[i]} numbers, {sizes[i]} needed")
-    here = set(map(torch.Tensor.get_device, ts))
-    if here and (-1 in here or here != {torch._C._cuda_getDevice()}):
+        want = [(n + per - 1) // per for n in array("q", sizes)]
+        if len(ts) != len(want):
+            raise ValueError(f"{name} holds {len(ts)} tensors, {len(want)} needed")
+        for i, (t, n) in enumerate(zip(ts, want)):
+            if t.numel() != n:
+                raise ValueError(f"{name}[{i}] holds {t.numel()} numbers, {n} needed")
+    if not all(t.is_cuda and t.get_device() == torch._C._cuda_getDevice() for t in ts):
         raise ValueError(f"{name} must be CUDA tensors on the current device")
-    if not all(map(torch.Tensor.is_contiguous, ts)):
+    if not all(t.layout is torch.strided and t.is_contiguous() for t in ts):
         raise ValueError(f"{name} must be contiguous")
-    return array("Q", map(torch.Tensor.data_ptr, ts)), dtype
+    raise ValueError(f"{name} must be tensors with memory of their own")
 
 
 def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=1.0, m_scales=None,
@@ -1268,31 +1299,25 @@ def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     grad_scale)`` on the device, takes the place of those arguments when the
     kernels run (a captured step's schedule)."""
     params = list(params)
-    if any(not isinstance(t, torch.Tensor) for t in params):
-        raise TypeError("params must hold torch.Tensors")
-    sizes = list(map(torch.Tensor.numel, params))
     if (m_scales is None) != (v_scales is None):
         raise ValueError("m_scales and v_scales go together")
     bits8 = m_scales is not None
-    pp, pt = _tensor_list(params, "params", None, _FLOATS)
-    gg, gt = _tensor_list(grads, "grads", sizes, _FLOATS)
-    mm, mt = _tensor_list(m, "m", sizes, None if bits8 else _F32, 1 if bits8 else None)
-    vv, vt = _tensor_list(v, "v", sizes, None if bits8 else _F32, 1 if bits8 else None)
+    pp, n, pt = _tensor_list(params, "params", None, dtypes=_FLOATS)
+    gg, _, gt = _tensor_list(grads, "grads", n, dtypes=_FLOATS)
+    mm, _, _ = _tensor_list(m, "m", n, dtypes=None if bits8 else _F32, itemsize=1 if bits8 else None)
+    vv, _, _ = _tensor_list(v, "v", n, dtypes=None if bits8 else _F32, itemsize=1 if bits8 else None)
     ms = vs = cc = None
     if bits8:
-        blocks = [(n + 127) // 128 for n in sizes]
-        ms, _ = _tensor_list(m_scales, "m_scales", blocks, _F32)
-        vs, _ = _tensor_list(v_scales, "v_scales", blocks, _F32)
+        ms, _, _ = _tensor_list(m_scales, "m_scales", n, 128, dtypes=_F32)
+        vs, _, _ = _tensor_list(v_scales, "v_scales", n, 128, dtypes=_F32)
     if copies is not None:
-        cc, _ = _tensor_list(copies, "copies", sizes, _BF16)
+        cc, _, _ = _tensor_list(copies, "copies", n, dtypes=_BF16)
     if hyper is not None:
         _want(hyper, "hyper", (3,), dtypes=_F32)
         _on_device(hyper=hyper)
     if not params:
         return
-    n = array("q", sizes)
-    at = [None if a is None else a.buffer_info()[0] for a in (n, pp, gg, mm, vv, ms, vs, cc)]
-    _check(lib().bsmm_adamw(len(sizes), at[0], at[1], BF16 if pt is torch.bfloat16 else F32, at[2],
-                            BF16 if gt is torch.bfloat16 else F32, at[3], at[4], E4M3 if bits8 else F32, at[5], at[6],
-                            at[7], lr, betas[0], betas[1], eps, weight_decay, int(step), grad_scale, _at(hyper),
+    _check(lib().bsmm_adamw(len(params), n, pp, BF16 if pt is torch.bfloat16 else F32, gg,
+                            BF16 if gt is torch.bfloat16 else F32, mm, vv, E4M3 if bits8 else F32, ms, vs, cc,
+                            lr, betas[0], betas[1], eps, weight_decay, int(step), grad_scale, _at(hyper),
                             _raw_stream(stream, params[0].device)), "bsmm_adamw")

@@ -1,4 +1,5 @@
-"""Builds libbsmm.so in-tree with nvcc for sm_103a.
+"""Builds libbsmm.so in-tree with nvcc for sm_103a, and _tensor_lists.so, the
+part of the Python binding that is compiled against torch.
 
 Each translation unit is compiled in parallel into ``_build/`` at the repository
 root; the shared library is linked into this package directory.  A unit is
@@ -13,12 +14,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsmm.so")
+LISTS = os.path.join(PKG, "_tensor_lists.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -42,6 +45,19 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _lists_command(src: str) -> list[str]:
+    """Compiles and links _tensor_lists.so with the host compiler."""
+    import torch
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    base = os.path.dirname(torch.__file__)
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(base, "include"),
+            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], src, "-o", LISTS,
+            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (as needed) and link libbsmm.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -59,6 +75,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if ptxas_info:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
+    units = len(jobs)
+    src = os.path.join(CSRC, "tensor_lists.cpp")
+    if force or not os.path.exists(LISTS) or os.path.getmtime(LISTS) < os.path.getmtime(src):
+        jobs.append(_lists_command(src))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -67,8 +87,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 print(" ".join(cmd))
                 print(r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError(f"nvcc failed for {cmd[-3]}")
-    if jobs or not os.path.exists(LIB):
+                raise RuntimeError(f"{os.path.basename(cmd[0])} failed for "
+                                   f"{next(a for a in cmd if a.endswith(('.cu', '.cpp')))}")
+    if units or not os.path.exists(LIB):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode:

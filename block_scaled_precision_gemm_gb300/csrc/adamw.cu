@@ -10,8 +10,8 @@
 //
 // Bound by memory: 28 bytes a number with binary32 tensors, 14 to 16 with
 // states in 8 bits.  The tensors' addresses are kernel parameters (up to
-// kTensors a launch), cut into chunks of 4096 numbers that the blocks take in
-// turn: small tensors share a launch and large ones spread over all SMs.
+// kTensors a launch), cut into chunks of 2048 or 4096 numbers that the blocks
+// take in turn: small tensors share a launch and large ones spread over all SMs.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -24,7 +24,8 @@ namespace bsmm {
 namespace {
 
 constexpr int kTensors = 96;
-constexpr int kChunk = 4096;
+template <bool BITS8>
+constexpr int kChunk = BITS8 ? 2048 : 4096;
 constexpr int kThreads = 256;
 
 struct AdamTensor {
@@ -52,23 +53,40 @@ struct Factors {
   float decay, rate, root2, scale;
 };
 
-__device__ __forceinline__ void move(float& p, float g, float& m, float& v, const AdamParams& a, const Factors& f) {
+// Returns the root of the new v.
+__device__ __forceinline__ float move(float& p, float g, float& m, float& v, const AdamParams& a, const Factors& f) {
   g = __fmul_rn(g, f.scale);
   m = __fadd_rn(__fmul_rn(a.b1, m), __fmul_rn(a.c1, g));
   v = __fadd_rn(__fmul_rn(a.b2, v), __fmul_rn(__fmul_rn(a.c2, g), g));
-  const float den = __fadd_rn(__fmul_rn(__fsqrt_rn(v), f.root2), a.eps);
+  const float root = __fsqrt_rn(v);
+  const float den = __fadd_rn(__fmul_rn(root, f.root2), a.eps);
   p = __fsub_rn(__fmul_rn(p, f.decay), __fmul_rn(f.rate, __fdiv_rn(m, den)));
+  return root;
 }
 
+// Four consecutive numbers as they are in memory, and their values.
 template <typename T>
-__device__ __forceinline__ float4 load4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return __ldcs(reinterpret_cast<const float4*>(p));
-  } else {
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
+struct Four;
+template <>
+struct Four<float> {
+  using Raw = float4;
+  __device__ static float4 value(const Raw& r) { return r; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+  __device__ static float4 value(const Raw& u) {
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xFFFF0000u));
   }
+};
+template <typename T>
+__device__ __forceinline__ typename Four<T>::Raw load4_raw(const T* p) {
+  return __ldcs(reinterpret_cast<const typename Four<T>::Raw*>(p));
+}
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+  return Four<T>::value(load4_raw(p));
 }
 template <typename T>
 __device__ __forceinline__ float load1(const T* p) {
@@ -128,8 +146,18 @@ __device__ __forceinline__ uint32_t root_codes(float4 r, const Scale& s) {
   return c;
 }
 
+// A warp's two blocks of 128 numbers, four a lane, as loaded ahead.
+template <typename P, typename G>
+struct Ahead {
+  typename Four<P>::Raw p[2];
+  typename Four<G>::Raw g[2];
+  uint32_t m[2], v[2];
+  float ms[2], vs[2];
+};
+
 template <typename P, typename G, bool BITS8>
-__global__ void __launch_bounds__(kThreads) adamw(const __grid_constant__ AdamParams a) {
+__global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 1) adamw(const __grid_constant__ AdamParams a) {
+  constexpr int CHUNK = kChunk<BITS8>;
   __shared__ Factors shared;
   Factors f{a.decay, a.rate, a.root2, a.scale};
   if (a.hyper) {
@@ -144,23 +172,30 @@ __global__ void __launch_bounds__(kThreads) adamw(const __grid_constant__ AdamPa
     f = shared;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t chunk = blockIdx.x; chunk < a.first[a.count]; chunk += gridDim.x) {
-    int lo = 0, hi = a.count;  // the tensor with first[lo] <= chunk < first[lo + 1]
+  const int64_t chunks = a.first[a.count];
+  int64_t chunk = blockIdx.x;
+  // the tensor with first[i] <= c < first[i + 1], from tensor lo on
+  auto tensor_of = [&](int lo, int64_t c) {
+    if (c < a.first[lo + 1]) return lo;
+    int hi = a.count;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (a.first[mid] <= chunk) lo = mid; else hi = mid;
+      if (a.first[mid] <= c) lo = mid; else hi = mid;
     }
-    const AdamTensor& t = a.t[lo];
-    const int64_t at = (chunk - a.first[lo]) * kChunk;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), t.n - at));
-    P* p = static_cast<P*>(t.p) + at;
-    const G* g = static_cast<const G*>(t.g) + at;
-    __nv_bfloat16* copy = t.copy ? t.copy + at : nullptr;
-    const bool wide = (a.wide[lo >> 5] >> (lo & 31)) & 1u;
-    if constexpr (!BITS8) {
+    return lo;
+  };
+  if constexpr (!BITS8) {
+    for (int ti = 0; chunk < chunks; chunk += gridDim.x) {
+      ti = tensor_of(ti, chunk);
+      const AdamTensor& t = a.t[ti];
+      const int64_t at = (chunk - a.first[ti]) * CHUNK;
+      const int n = static_cast<int>(min(static_cast<int64_t>(CHUNK), t.n - at));
+      P* p = static_cast<P*>(t.p) + at;
+      const G* g = static_cast<const G*>(t.g) + at;
+      __nv_bfloat16* copy = t.copy ? t.copy + at : nullptr;
       float* m = static_cast<float*>(t.m) + at;
       float* v = static_cast<float*>(t.v) + at;
-      if (wide && n == kChunk) {
+      if (n == CHUNK && ((a.wide[ti >> 5] >> (ti & 31)) & 1u)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float4 pp[2], gg[2], mm[2], vv[2];
@@ -195,49 +230,77 @@ __global__ void __launch_bounds__(kThreads) adamw(const __grid_constant__ AdamPa
           if (copy) copy[i] = __float2bfloat16_rn(pp);
         }
       }
-    } else {
-      // a warp a block of 128: four numbers a lane
+    }
+  } else {
+    // A warp a block of 128: four numbers a lane.  A whole chunk's numbers are
+    // loaded while the chunk before is computed (about 650 instructions a warp).
+    using Four_p = Four<P>;
+    using Four_g = Four<G>;
+    auto fetch = [&](int ti, int64_t c, Ahead<P, G>& x) {
+      const AdamTensor& t = a.t[ti];
+      const int64_t at = (c - a.first[ti]) * CHUNK;
+      if (t.n - at < CHUNK || !((a.wide[ti >> 5] >> (ti & 31)) & 1u)) return false;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int b = warp + 8 * j;
+        const int64_t i = at + 128 * b + 4 * lane;
+        x.p[j] = load4_raw(static_cast<const P*>(t.p) + i);
+        x.g[j] = load4_raw(static_cast<const G*>(t.g) + i);
+        x.m[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
+        x.v[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
+        x.ms[j] = t.ms[at / 128 + b];
+        x.vs[j] = t.vs[at / 128 + b];
+      }
+      return true;
+    };
+    Ahead<P, G> x, next;
+    int ti = 0;
+    bool whole = false;
+    if (chunk < chunks) {
+      ti = tensor_of(0, chunk);
+      whole = fetch(ti, chunk, x);
+    }
+    while (chunk < chunks) {
+      const int64_t after = chunk + gridDim.x;
+      int ti_next = ti;
+      bool whole_next = false;
+      if (after < chunks) {
+        ti_next = tensor_of(ti, after);
+        whole_next = fetch(ti_next, after, next);
+      }
+      const AdamTensor& t = a.t[ti];
+      const int64_t at = (chunk - a.first[ti]) * CHUNK;
+      P* p = static_cast<P*>(t.p) + at;
+      __nv_bfloat16* copy = t.copy ? t.copy + at : nullptr;
       uint8_t* m = static_cast<uint8_t*>(t.m) + at;
       uint8_t* v = static_cast<uint8_t*>(t.v) + at;
       float* ms = t.ms + at / 128;
       float* vs = t.vs + at / 128;
-      if (wide && n == kChunk) {
+      if (whole) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float4 pp[2], gg[2];
-          uint32_t mc[2], vc[2];
-          float sm[2], sv[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int b = warp + 8 * (2 * h + j), i = 128 * b + 4 * lane;
-            pp[j] = load4(p + i);
-            gg[j] = load4(g + i);
-            mc[j] = __ldcs(reinterpret_cast<const uint32_t*>(m + i));
-            vc[j] = __ldcs(reinterpret_cast<const uint32_t*>(v + i));
-            sm[j] = ms[b];
-            sv[j] = vs[b];
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int b = warp + 8 * (2 * h + j), i = 128 * b + 4 * lane;
-            float4 mm = e4m3_values(mc[j]), vv = e4m3_values(vc[j]);
-            mm = make_float4(__fmul_rn(mm.x, sm[j]), __fmul_rn(mm.y, sm[j]), __fmul_rn(mm.z, sm[j]), __fmul_rn(mm.w, sm[j]));
-            vv = make_float4(__fmul_rn(vv.x, sv[j]), __fmul_rn(vv.y, sv[j]), __fmul_rn(vv.z, sv[j]), __fmul_rn(vv.w, sv[j]));
-            vv = make_float4(__fmul_rn(vv.x, vv.x), __fmul_rn(vv.y, vv.y), __fmul_rn(vv.z, vv.z), __fmul_rn(vv.w, vv.w));
-            move(pp[j].x, gg[j].x, mm.x, vv.x, a, f);
-            move(pp[j].y, gg[j].y, mm.y, vv.y, a, f);
-            move(pp[j].z, gg[j].z, mm.z, vv.z, a, f);
-            move(pp[j].w, gg[j].w, mm.w, vv.w, a, f);
-            const float4 r = make_float4(__fsqrt_rn(vv.x), __fsqrt_rn(vv.y), __fsqrt_rn(vv.z), __fsqrt_rn(vv.w));
-            const Scale s = state_scale(block_max(mm)), q = state_scale(block_max(r));
-            store4(p + i, pp[j]);
-            if (copy) store4(copy + i, pp[j]);
-            __stcs(reinterpret_cast<uint32_t*>(m + i), encode4<false>(mm.x, mm.y, mm.z, mm.w, s, BSMM_E4M3));
-            __stcs(reinterpret_cast<uint32_t*>(v + i), root_codes(r, q));
-            if (lane == 0) ms[b] = s.s, vs[b] = q.s;
-          }
+        for (int j = 0; j < 2; ++j) {
+          const int b = warp + 8 * j, i = 128 * b + 4 * lane;
+          const float sm = x.ms[j], sv = x.vs[j];
+          float4 pp = Four_p::value(x.p[j]);
+          const float4 gg = Four_g::value(x.g[j]);
+          float4 mm = e4m3_values(x.m[j]), vv = e4m3_values(x.v[j]), r;
+          mm = make_float4(__fmul_rn(mm.x, sm), __fmul_rn(mm.y, sm), __fmul_rn(mm.z, sm), __fmul_rn(mm.w, sm));
+          vv = make_float4(__fmul_rn(vv.x, sv), __fmul_rn(vv.y, sv), __fmul_rn(vv.z, sv), __fmul_rn(vv.w, sv));
+          vv = make_float4(__fmul_rn(vv.x, vv.x), __fmul_rn(vv.y, vv.y), __fmul_rn(vv.z, vv.z), __fmul_rn(vv.w, vv.w));
+          r.x = move(pp.x, gg.x, mm.x, vv.x, a, f);
+          r.y = move(pp.y, gg.y, mm.y, vv.y, a, f);
+          r.z = move(pp.z, gg.z, mm.z, vv.z, a, f);
+          r.w = move(pp.w, gg.w, mm.w, vv.w, a, f);
+          const Scale s = state_scale(block_max(mm)), q = state_scale(block_max(r));
+          store4(p + i, pp);
+          if (copy) store4(copy + i, pp);
+          __stcs(reinterpret_cast<uint32_t*>(m + i), encode4<false>(mm.x, mm.y, mm.z, mm.w, s, BSMM_E4M3));
+          __stcs(reinterpret_cast<uint32_t*>(v + i), root_codes(r, q));
+          if (lane == 0) ms[b] = s.s, vs[b] = q.s;
         }
       } else {
+        const int n = static_cast<int>(min(static_cast<int64_t>(CHUNK), t.n - at));
+        const G* g = static_cast<const G*>(t.g) + at;
         for (int b = warp; 128 * b < n; b += kThreads / 32) {
           const float sm = ms[b], sv = vs[b];
           float mm[4], rr[4];
@@ -250,8 +313,7 @@ __global__ void __launch_bounds__(kThreads) adamw(const __grid_constant__ AdamPa
               float vv = __fmul_rn(e4m3_values(v[i]).x, sv);
               vv = __fmul_rn(vv, vv);
               mm[j] = __fmul_rn(e4m3_values(m[i]).x, sm);
-              move(pp, load1(g + i), mm[j], vv, a, f);
-              rr[j] = __fsqrt_rn(vv);
+              rr[j] = move(pp, load1(g + i), mm[j], vv, a, f);
               store1(p + i, pp);
               if (copy) copy[i] = __float2bfloat16_rn(pp);
             }
@@ -268,6 +330,10 @@ __global__ void __launch_bounds__(kThreads) adamw(const __grid_constant__ AdamPa
           if (lane == 0) ms[b] = s.s, vs[b] = q.s;
         }
       }
+      x = next;
+      chunk = after;
+      ti = ti_next;
+      whole = whole_next;
     }
   }
 }
@@ -313,11 +379,11 @@ cudaError_t launch_adamw(const AdamwRequest& r, cudaStream_t s) {
                         reinterpret_cast<uintptr_t>(t.m) % state == 0 && reinterpret_cast<uintptr_t>(t.v) % state == 0 &&
                         reinterpret_cast<uintptr_t>(t.copy) % 8 == 0;
       if (wide) a.wide[a.count >> 5] |= 1u << (a.count & 31);
-      a.first[a.count + 1] = a.first[a.count] + ceil_div(t.n, kChunk);
+      a.first[a.count + 1] = a.first[a.count] + ceil_div(t.n, r.bits8 ? kChunk<true> : kChunk<false>);
       ++a.count;
     }
     if (a.count == 0) break;
-    const int64_t grid = std::min<int64_t>(a.first[a.count], 8 * ctx->num_sms);
+    const int64_t grid = std::min<int64_t>(a.first[a.count], (r.bits8 ? 3 : 8) * ctx->num_sms);
     TraceScope tr(r.bits8 ? "adamw (8 bits)" : "adamw", s);
     kern<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();

@@ -19,6 +19,14 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 // --------------------------------------------------------------------------
+// Launches that overlap the end of the kernel before (programmatic stream
+// serialization): the earlier kernel says that its successor's blocks may
+// start, and those wait for its memory before they touch it.
+// --------------------------------------------------------------------------
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// --------------------------------------------------------------------------
 // Device status word: the first wait that gives up records its site code.
 // --------------------------------------------------------------------------
 __device__ __forceinline__ void record_timeout(int* status, int site) {

@@ -13,26 +13,85 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace bsmm {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kRouteBlocks = 304;  // most blocks of tokens (two per SM)
-constexpr int kRouteWarps = 8;
+constexpr int kRouteBlocks = 152;  // most blocks of tokens: one per SM, as each reads the others' counts
+constexpr int kPlaceThreads = 1024;
 
 __device__ __forceinline__ float bf16_value(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
-
-// A logit as an unsigned number in the same order; 0 for what is never chosen
-// (minus infinity and NaN).  -0 and 0 are equal.
-__device__ __forceinline__ uint32_t order_key(float l) {
-  l += 0.f;
-  const uint32_t b = __float_as_uint(l);
-  if (!(l > -INFINITY)) return 0u;
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
+
+// A logit as an unsigned number in the same order, minus infinity 0x007fffff.
+__device__ __forceinline__ uint32_t ordered(float l) {
+  const uint32_t b = __float_as_uint(l);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float ordered_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+
+// A logit and its place in one number, larger for a larger logit and for an
+// earlier place: no two are alike, so the largest of a warp says by itself
+// which lane holds it.  A bfloat16 logit leaves room for the place in 32 bits.
+template <bool BF16>
+struct Ranked;
+template <>
+struct Ranked<true> {
+  using Key = uint32_t;
+  __device__ static Key make(float l, int i) { return (ordered(l) & 0xFFFF0000u) | static_cast<uint32_t>(0xFFFF - i); }
+  __device__ static int place(Key k) { return 0xFFFF - static_cast<int>(k & 0xFFFFu); }
+  __device__ static bool none(Key k) { return k < 0x00800000u; }
+  __device__ static float value(Key k) {
+    return ordered_value((k & 0x80000000u) ? k & 0xFFFF0000u : k | 0xFFFFu);
+  }
+  __device__ static Key most(Key k) { return __reduce_max_sync(kAll, k); }
+};
+template <>
+struct Ranked<false> {
+  using Key = uint64_t;
+  __device__ static Key make(float l, int i) {
+    return (static_cast<uint64_t>(ordered(l)) << 32) | static_cast<uint32_t>(~i);
+  }
+  __device__ static int place(Key k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
+  __device__ static bool none(Key k) { return static_cast<uint32_t>(k >> 32) < 0x00800000u; }
+  __device__ static float value(Key k) { return ordered_value(static_cast<uint32_t>(k >> 32)); }
+  __device__ static Key most(Key k) {
+    const uint32_t hi = static_cast<uint32_t>(k >> 32), top = __reduce_max_sync(kAll, hi);
+    const uint32_t low = __reduce_max_sync(kAll, hi == top ? static_cast<uint32_t>(k) : 0u);
+    return (static_cast<uint64_t>(top) << 32) | low;
+  }
+};
+
+// N keys (1, 2, 4 or 8) into falling order, by Batcher's merge exchange.
+template <typename K>
+__device__ __forceinline__ void falling(K& a, K& b) {
+  const K lo = min(a, b);
+  a = max(a, b);
+  b = lo;
+}
+template <int N, typename K>
+__device__ __forceinline__ void sort_falling(K* k) {
+  if constexpr (N >= 2) {
+    sort_falling<N / 2>(k);
+    sort_falling<N / 2>(k + N / 2);
+    if constexpr (N == 2) {
+      falling(k[0], k[1]);
+    } else if constexpr (N == 4) {
+      falling(k[0], k[2]), falling(k[1], k[3]);
+      falling(k[1], k[2]);
+    } else {
+      falling(k[0], k[4]), falling(k[1], k[5]), falling(k[2], k[6]), falling(k[3], k[7]);
+      falling(k[2], k[4]), falling(k[3], k[5]);
+      falling(k[1], k[2]), falling(k[3], k[4]), falling(k[5], k[6]);
+    }
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -59,8 +118,17 @@ struct RouteParams {
   int64_t per_block;  // tokens
 };
 
+// A NaN as minus infinity, -0 as 0.
+__device__ __forceinline__ float plain(float l) { return fmaxf(l + 0.f, -INFINITY); }
+__device__ __forceinline__ uint32_t plain_pair(uint32_t w) {
+  const uint32_t zero = 0u, low = 0xFF80FF80u;
+  __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&zero));
+  v = __hmax2(v, *reinterpret_cast<const __nv_bfloat162*>(&low));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // The lane's VPL logits of a row: vectors of V consecutive ones, the lanes'
-// vectors side by side.  Past the row: minus infinity.
+// vectors side by side.  Past the row, and for a NaN: minus infinity; -0: 0.
 template <int VPL, bool BF16>
 struct RowLoad {
   static constexpr int V = BF16 ? (VPL < 8 ? VPL : 8) : (VPL < 4 ? VPL : 4);
@@ -72,7 +140,7 @@ struct RowLoad {
         const int i = index(j, lane);
         if constexpr (BF16 && V == 8) {
           const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at + i));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          const uint32_t w[4] = {plain_pair(u.x), plain_pair(u.y), plain_pair(u.z), plain_pair(u.w)};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             l[j + 2 * q] = __uint_as_float(w[q] << 16);
@@ -80,12 +148,12 @@ struct RowLoad {
           }
         } else if constexpr (!BF16 && V == 4) {
           const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + i));
-          l[j] = u.x, l[j + 1] = u.y, l[j + 2] = u.z, l[j + 3] = u.w;
+          l[j] = plain(u.x), l[j + 1] = plain(u.y), l[j + 2] = plain(u.z), l[j + 3] = plain(u.w);
         } else {
 #pragma unroll
           for (int q = 0; q < V; ++q)
-            l[j + q] = BF16 ? bf16_value(__ldg(static_cast<const unsigned short*>(base) + at + i + q))
-                            : __ldg(static_cast<const float*>(base) + at + i + q);
+            l[j + q] = plain(BF16 ? bf16_value(__ldg(static_cast<const unsigned short*>(base) + at + i + q))
+                                  : __ldg(static_cast<const float*>(base) + at + i + q));
         }
       }
     } else {
@@ -94,88 +162,110 @@ struct RowLoad {
         const int i = index(j, lane);
         l[j] = -INFINITY;
         if (i < E)
-          l[j] = BF16 ? bf16_value(__ldg(static_cast<const unsigned short*>(base) + at + i))
-                      : __ldg(static_cast<const float*>(base) + at + i);
+          l[j] = plain(BF16 ? bf16_value(__ldg(static_cast<const unsigned short*>(base) + at + i))
+                            : __ldg(static_cast<const float*>(base) + at + i));
       }
     }
   }
 };
 
 // One token by one warp: lane j < k returns its j-th choice (-1: none) and weight.
+// Every lane sorts its logits (groups of 8 of them); then each choice is the
+// largest of the lanes' first ones, and the lane that held it moves on.
 template <int VPL, bool BF16>
 __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane, int& id, float& weight) {
   using R = RowLoad<VPL, BF16>;
+  using Q = Ranked<BF16>;
+  using Key = typename Q::Key;
+  constexpr int G = VPL < 8 ? VPL : 8;
   float l[VPL];
   R::load(p.logits, t * p.ld, p.E, p.vec, lane, l);
-  uint32_t key[VPL];
+  Key key[VPL];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) key[j] = order_key(l[j]);
-  uint32_t mine = 0;  // this lane's largest key, and the first place of it
-  int place = 0;
-  auto rescan = [&] {
-    mine = 0;
+  for (int j = 0; j < VPL; ++j) key[j] = Q::make(l[j], R::index(j, lane));
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (key[j] > mine) mine = key[j], place = j;
-  };
-  rescan();
-  id = -1;
-  uint32_t got = 0, top = 0;
-  for (int n = 0; n < p.k; ++n) {
-    const uint32_t most = __reduce_max_sync(kAll, mine);
-    if (n == 0) top = most;
-    if (most == 0) break;
-    const uint32_t first = __reduce_min_sync(kAll, mine == most ? static_cast<uint32_t>(R::index(place, lane)) : ~0u);
-    if (lane == n) id = static_cast<int>(first), got = most;
-    if (mine == most && static_cast<uint32_t>(R::index(place, lane)) == first) {
+  for (int g = 0; g < VPL; g += G) sort_falling<G>(key + g);
+  Key got = 0, first = 0;
+  // `depth`: how many of a group's keys can still be asked for
+  auto round = [&](int n, int depth) {
+    Key mine = key[0];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (j == place) key[j] = 0;
-      rescan();
+    for (int g = G; g < VPL; g += G) mine = max(mine, key[g]);
+    const Key best = Q::most(mine);
+    if (n == 0) first = best;
+    if (lane == n) got = best;
+#pragma unroll
+    for (int g = 0; g < VPL; g += G) {
+      const bool taken = key[g] == best;
+#pragma unroll
+      for (int j = 0; j + 1 < G; ++j)
+        if (j < depth) key[g + j] = taken ? key[g + j + 1] : key[g + j];
+      if (G - 1 < depth) key[g + G - 1] = taken ? Key(0) : key[g + G - 1];
     }
+  };
+  if (p.k <= 8) {
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      if (n >= p.k) break;
+      round(n, 7 - n);
+    }
+  } else {
+    for (int n = 0; n < p.k; ++n) round(n, G);
   }
-  const float largest = key_value(top);
-  const float e = id >= 0 ? expf(key_value(got) - largest) : 0.f;
+  id = Q::none(got) ? -1 : Q::place(got);
+  const float largest = Q::value(first);
+  const float e = id >= 0 ? expf(Q::value(got) - largest) : 0.f;
   float part = e;
   if (!p.renormalize) {
     part = 0.f;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (l[j] > -INFINITY) part += expf(l[j] - largest);  // a NaN is none
+    for (int j = 0; j < VPL; ++j) part += expf(l[j] - largest);
   }
   const float sum = warp_sum(part);
   weight = id >= 0 ? __fdiv_rn(e, sum) : 0.f;
 }
 
-// The pairs [begin, end) by `warps` warps of this block, each a run of them:
-// counts by warp and expert, the runs' starts from them, then every pair's
-// place.  Lanes with the same expert rank by their order, so the layout is
-// stable.  start[e]: the first slot of this block's pairs of expert e.
-__device__ __forceinline__ void count_pairs(const int* ids, int64_t begin, int64_t end, int E, int* mine, int lane) {
-  for (int64_t i0 = begin; i0 < end; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int e = i < end ? ids[i] : -1;
-    const uint32_t same = __match_any_sync(kAll, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-  }
-}
-__device__ __forceinline__ void place_pairs(const int* ids, int64_t begin, int64_t end, int64_t pair0, int k, int* mine,
-                                            int lane, int* slots, int* rows) {
-  for (int64_t i0 = begin; i0 < end; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int e = i < end ? ids[i] : -1;
-    const uint32_t same = __match_any_sync(kAll, e);
-    int slot = -1;
-    if (e >= 0) slot = mine[e] + __popc(same & ((1u << lane) - 1));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-    if (i < end) {
-      slots[pair0 + i] = slot;
-      if (slot >= 0) rows[slot] = static_cast<int>((pair0 + i) / k);
+// The tokens [t0, t1) by WARPS warps, each a run of them.  counts [WARPS][E],
+// zero at the start, are left as the numbers of the block's pairs of an expert
+// in earlier runs; slots as a pair's rank in its own run and total [E] as the
+// block's numbers of pairs.  A token's experts differ, so its lanes count
+// without conflict and in the tokens' order: the layout is stable.
+template <int VPL, bool BF16, int WARPS>
+__device__ __forceinline__ void choose_tokens(const RouteParams& p, int64_t t0, int64_t t1, int64_t run, int* counts,
+                                              int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* mine = counts + warp * p.E;
+  const int64_t end = min(t1, t0 + run * (warp + 1));
+  for (int64_t t = t0 + run * warp; t < end; ++t) {
+    int id;
+    float w;
+    choose<VPL, BF16>(p, t, lane, id, w);
+    if (lane < p.k) {
+      const int64_t at = t * p.k + lane;
+      p.ids[at] = id;
+      p.weights[at] = w;
+      int rank = -1;
+      if (id >= 0) {
+        rank = mine[id];
+        mine[id] = rank + 1;
+      }
+      p.slots[at] = rank;
     }
+    __syncwarp();
   }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += 32 * WARPS) {
+    int n[WARPS], sum = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) n[w] = counts[w * p.E + e];
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      counts[w * p.E + e] = sum;
+      sum += n[w];
+    }
+    total[e] = sum;
+  }
+  __syncthreads();
 }
 
 // Exclusive sums over E values in shared memory, in place; returns their sum.
@@ -206,74 +296,84 @@ __device__ __forceinline__ int scan_experts(int* v, int E, int threads) {
   return carry;
 }
 
+// Warps of a block: fewer where a lane's keys need more registers.
+template <int VPL>
+constexpr int kChooseWarps = VPL >= 16 ? 16 : 32;
+
+// What is known of a token alone, and within its block: choices, weights, each
+// pair's rank among the block's pairs of its expert (in slots), and the counts.
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_choose(const RouteParams p) {
-  extern __shared__ int hist[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+__global__ void __launch_bounds__(32 * kChooseWarps<VPL>) route_choose(const RouteParams p) {
+  extern __shared__ int sm[];
+  constexpr int WARPS = kChooseWarps<VPL>;
+  int* total = sm + WARPS * p.E;
+  for (int i = threadIdx.x; i < WARPS * p.E; i += 32 * WARPS) sm[i] = 0;
   __syncthreads();
+  pdl_launch();
   const int64_t t0 = blockIdx.x * p.per_block, t1 = min(p.T, t0 + p.per_block);
-  for (int64_t t = t0 + warp; t < t1; t += kRouteWarps) {
-    int id;
-    float w;
-    choose<VPL, BF16>(p, t, lane, id, w);
-    if (lane < p.k) {
-      p.ids[t * p.k + lane] = id;
-      p.weights[t * p.k + lane] = w;
-      if (id >= 0) atomicAdd(hist + id, 1);
-    }
+  const int64_t run = (p.per_block + WARPS - 1) / WARPS;
+  choose_tokens<VPL, BF16, WARPS>(p, t0, t1, run, sm, total);
+  for (int e = threadIdx.x; e < p.E; e += 32 * WARPS) p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = total[e];
+  const uint32_t pairs = static_cast<uint32_t>((t1 - t0) * p.k), per_run = static_cast<uint32_t>(run * p.k);
+  for (uint32_t i = threadIdx.x; i < pairs; i += 32 * WARPS) {
+    const int id = p.ids[t0 * p.k + i];
+    if (id >= 0) p.slots[t0 * p.k + i] += sm[i / per_run * p.E + id];
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = hist[e];
 }
 
-__global__ void __launch_bounds__(32 * kRouteWarps) route_place(const RouteParams p) {
+// Each pair's slot from its rank: the experts' first slots and the pairs of
+// earlier blocks are sums over the blocks' counts.
+__global__ void __launch_bounds__(kPlaceThreads) route_place(const RouteParams p) {
   extern __shared__ int sm[];
-  constexpr int THREADS = 32 * kRouteWarps;
-  int* counts = sm;                        // [warps][E]
-  int* total = counts + kRouteWarps * p.E;  // [E], then the experts' first slots
-  int* before = total + p.E;               // [E] pairs of earlier blocks
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < (kRouteWarps + 2) * p.E; i += THREADS) sm[i] = 0;
+  int* total = sm;        // [E], then the experts' first slots
+  int* base = sm + p.E;   // [E] pairs of earlier blocks, then the first slots of this block
+  for (int i = threadIdx.x; i < 2 * p.E; i += kPlaceThreads) sm[i] = 0;
   __syncthreads();
-  // the histograms' column sums: `parts` threads share an expert
+  pdl_wait();  // launched before route_choose has ended
+  // `parts` threads share an expert's column
   int wide = 32;
-  while (wide < p.E && wide < THREADS) wide <<= 1;
-  const int parts = THREADS / wide, part = threadIdx.x / wide;
+  while (wide < p.E && wide < kPlaceThreads) wide <<= 1;
+  const int parts = kPlaceThreads / wide, part = threadIdx.x / wide;
   for (int e = threadIdx.x % wide; e < p.E; e += wide) {
     int all = 0, early = 0;
-#pragma unroll 8
-    for (int b = part; b < p.blocks; b += parts) {
-      const int n = __ldg(p.hist + static_cast<int64_t>(b) * p.E + e);
-      all += n;
-      early += b < static_cast<int>(blockIdx.x) ? n : 0;
+    for (int b0 = part; b0 < p.blocks; b0 += 16 * parts) {
+      int n[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int b = b0 + j * parts;
+        n[j] = b < p.blocks ? p.hist[static_cast<int64_t>(b) * p.E + e] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        all += n[j];
+        early += b0 + j * parts < static_cast<int>(blockIdx.x) ? n[j] : 0;
+      }
     }
     atomicAdd(total + e, all);
-    atomicAdd(before + e, early);
+    atomicAdd(base + e, early);
   }
-  const int64_t t0 = blockIdx.x * p.per_block, t1 = min(p.T, t0 + p.per_block);
-  const int64_t n = (t1 - t0) * p.k, pair0 = t0 * p.k;
-  const int64_t run = (n + 32 * kRouteWarps - 1) / (32 * kRouteWarps) * 32;
-  const int64_t begin = min(n, run * warp), end = min(n, begin + run);
-  const int* ids = p.ids + pair0;
-  count_pairs(ids, begin, end, p.E, counts + warp * p.E, lane);
   __syncthreads();
-  const int used = scan_experts(total, p.E, THREADS);
-  for (int e = threadIdx.x; e < p.E; e += THREADS) {
-    int at = total[e] + before[e];
-    for (int w = 0; w < kRouteWarps; ++w) {
-      const int c = counts[w * p.E + e];
-      counts[w * p.E + e] = at;
-      at += c;
-    }
+  const int used = scan_experts(total, p.E, kPlaceThreads);
+  for (int e = threadIdx.x; e < p.E; e += kPlaceThreads) {
+    base[e] += total[e];
     if (blockIdx.x == 0) p.offsets[e] = total[e];
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.E] = used;
   __syncthreads();
-  place_pairs(ids, begin, end, pair0, p.k, counts + warp * p.E, lane, p.slots, p.rows);
+  const int64_t t0 = blockIdx.x * p.per_block, t1 = min(p.T, t0 + p.per_block), pair0 = t0 * p.k;
+  const uint32_t pairs = static_cast<uint32_t>((t1 - t0) * p.k);
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < pairs; i += kPlaceThreads) {
+    const int id = p.ids[pair0 + i];
+    if (id >= 0) {
+      const int slot = base[id] + p.slots[pair0 + i];
+      p.slots[pair0 + i] = slot;
+      p.rows[slot] = static_cast<int>(t0 + i / static_cast<uint32_t>(p.k));
+    }
+  }
   // slots that no pair takes
-  for (int64_t i = used + blockIdx.x * static_cast<int64_t>(THREADS) + threadIdx.x; i < p.T * p.k;
-       i += static_cast<int64_t>(gridDim.x) * THREADS)
+  for (int64_t i = used + blockIdx.x * static_cast<int64_t>(kPlaceThreads) + threadIdx.x; i < p.T * p.k;
+       i += static_cast<int64_t>(gridDim.x) * kPlaceThreads)
     p.rows[i] = -1;
 }
 
@@ -284,46 +384,23 @@ template <int VPL, bool BF16>
 __global__ void __launch_bounds__(32 * kFewWarps) route_few(const RouteParams p) {
   extern __shared__ int sm[];
   constexpr int THREADS = 32 * kFewWarps;
-  const int n = static_cast<int>(p.T) * p.k;
-  int* counts = sm;                       // [warps][E]
-  int* total = counts + kFewWarps * p.E;  // [E]
-  int* ids = total + p.E;                 // [n]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kFewWarps * p.E; i += THREADS) counts[i] = 0;
-  for (int64_t t = warp; t < p.T; t += kFewWarps) {
-    int id;
-    float w;
-    choose<VPL, BF16>(p, t, lane, id, w);
-    if (lane < p.k) {
-      ids[t * p.k + lane] = id;
-      p.ids[t * p.k + lane] = id;
-      p.weights[t * p.k + lane] = w;
-    }
-  }
+  int* total = sm + kFewWarps * p.E;
+  for (int i = threadIdx.x; i < kFewWarps * p.E; i += THREADS) sm[i] = 0;
   __syncthreads();
-  const int run = (n + 32 * kFewWarps - 1) / (32 * kFewWarps) * 32;
-  const int begin = min(n, run * warp), end = min(n, begin + run);
-  count_pairs(ids, begin, end, p.E, counts + warp * p.E, lane);
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += THREADS) {
-    int c = 0;
-    for (int w = 0; w < kFewWarps; ++w) c += counts[w * p.E + e];
-    total[e] = c;
-  }
-  __syncthreads();
+  const int64_t run = (p.T + kFewWarps - 1) / kFewWarps;
+  choose_tokens<VPL, BF16, kFewWarps>(p, 0, p.T, run, sm, total);
   const int used = scan_experts(total, p.E, THREADS);
-  for (int e = threadIdx.x; e < p.E; e += THREADS) {
-    int at = total[e];
-    p.offsets[e] = at;
-    for (int w = 0; w < kFewWarps; ++w) {
-      const int c = counts[w * p.E + e];
-      counts[w * p.E + e] = at;
-      at += c;
+  for (int e = threadIdx.x; e < p.E; e += THREADS) p.offsets[e] = total[e];
+  if (threadIdx.x == 0) p.offsets[p.E] = used;
+  const int n = static_cast<int>(p.T) * p.k, per_run = static_cast<int>(run) * p.k;
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    const int id = p.ids[i];
+    if (id >= 0) {
+      const int slot = total[id] + sm[i / per_run * p.E + id] + p.slots[i];
+      p.slots[i] = slot;
+      p.rows[slot] = i / p.k;
     }
   }
-  if (threadIdx.x == 0) p.offsets[p.E] = used;
-  __syncthreads();
-  place_pairs(ids, begin, end, 0, p.k, counts + warp * p.E, lane, p.slots, p.rows);
   for (int i = used + threadIdx.x; i < n; i += THREADS) p.rows[i] = -1;
 }
 
@@ -344,11 +421,11 @@ struct RouteBackwardParams {
 
 // A token by a warp.  dl = w_j (dw_j - mean) at the chosen, with mean = sum of
 // w dw; over all experts' softmax p, dl = -p mean besides, and w_j dw_j at the
-// chosen.
+// chosen.  The row passes through shared memory, where the chosen are added.
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(256) route_backward(const RouteBackwardParams p) {
   using R = RowLoad<VPL, BF16>;
-  extern __shared__ float rows_sm[];
+  extern __shared__ __align__(16) float rows_sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* row = rows_sm + warp * VPL * 32;
   for (int64_t t = blockIdx.x * static_cast<int64_t>(8) + warp; t < p.T; t += static_cast<int64_t>(gridDim.x) * 8) {
@@ -359,58 +436,75 @@ __global__ void __launch_bounds__(256) route_backward(const RouteBackwardParams 
       if (id < 0 || id >= p.E) id = -1;
       if (id >= 0) w = __ldg(p.weights + t * p.k + lane), dw = __ldg(p.d_weights + t * p.k + lane);
     }
+    float d[VPL];
+    if (!p.renormalize) R::load(p.logits, t * p.ld, p.E, p.vec, lane, d);
     const float wd = id >= 0 ? w * dw : 0.f;
     const float mean = warp_sum(wd);
-    float d[VPL];
     if (p.renormalize) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j) d[j] = 0.f;
     } else {
-      float l[VPL];
-      R::load(p.logits, t * p.ld, p.E, p.vec, lane, l);
-      uint32_t most = 0;
+      float largest = d[0];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) most = max(most, order_key(l[j]));
-      most = __reduce_max_sync(kAll, most);
-      const float largest = key_value(most);
+      for (int j = 1; j < VPL; ++j) largest = fmaxf(largest, d[j]);
+      largest = ordered_value(__reduce_max_sync(kAll, ordered(largest)));
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        d[j] = l[j] > -INFINITY ? expf(l[j] - largest) : 0.f;
+        d[j] = expf(d[j] - largest);
         sum += d[j];
       }
       sum = warp_sum(sum);
-      const float scale = most ? __fdiv_rn(-mean, sum) : 0.f;
+      const float scale = __fdiv_rn(-mean, sum);
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) d[j] *= scale;
+      for (int j = 0; j < VPL; ++j) d[j] = largest > -INFINITY ? d[j] * scale : 0.f;
     }
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) row[R::index(j, lane)] = d[j];
+    for (int j = 0; j < VPL; j += R::V) {
+      float* at = row + R::index(j, lane);
+      if constexpr (R::V >= 4) {
+#pragma unroll
+        for (int q = 0; q < R::V; q += 4)
+          *reinterpret_cast<float4*>(at + q) = make_float4(d[j + q], d[j + q + 1], d[j + q + 2], d[j + q + 3]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < R::V; ++q) at[q] = d[j + q];
+      }
+    }
     __syncwarp();
     const float at_chosen = p.renormalize ? w * (dw - mean) : wd;
-    for (int j = 0; j < p.k; ++j) {  // one after the other: the same expert twice adds up
-      if (lane == j && id >= 0) row[id] += at_chosen;
-      __syncwarp();
+    // at once where no expert occurs twice; else one after the other, so that
+    // its parts add up in their order
+    const uint32_t same = __match_any_sync(kAll, id >= 0 ? id : ~lane);
+    if (__all_sync(kAll, same == 1u << lane)) {
+      if (id >= 0) row[id] += at_chosen;
+    } else {
+      for (int j = 0; j < p.k; ++j) {
+        if (lane == j && id >= 0) row[id] += at_chosen;
+        __syncwarp();
+      }
     }
+    __syncwarp();
     if (BF16) {
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.d_logits) + t * p.ld_d;
       if (p.d_vec) {
         for (int i = 8 * lane; i < p.E; i += 256) {
-          uint32_t v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(row[i + 2 * q], row[i + 2 * q + 1]);
-            v[q] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          *reinterpret_cast<uint4*>(out + i) = make_uint4(v[0], v[1], v[2], v[3]);
+          const float4 a = *reinterpret_cast<const float4*>(row + i), b = *reinterpret_cast<const float4*>(row + i + 4);
+          *reinterpret_cast<uint4*>(out + i) =
+              make_uint4(pair_bf16(a.x, a.y), pair_bf16(a.z, a.w), pair_bf16(b.x, b.y), pair_bf16(b.z, b.w));
         }
       } else {
         for (int i = lane; i < p.E; i += 32) out[i] = __float2bfloat16_rn(row[i]);
       }
     } else {
       float* out = static_cast<float*>(p.d_logits) + t * p.ld_d;
-      for (int i = lane; i < p.E; i += 32) out[i] = row[i];
+      if (p.d_vec) {
+        for (int i = 4 * lane; i < p.E; i += 128)
+          *reinterpret_cast<float4*>(out + i) = *reinterpret_cast<const float4*>(row + i);
+      } else {
+        for (int i = lane; i < p.E; i += 32) out[i] = row[i];
+      }
     }
   }
 }
@@ -434,73 +528,93 @@ struct CombineParams {
 
 // W consecutive values (8, or 1 where rows are not 16-byte aligned).
 template <int W>
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, float (&v)[W]) {
-  if constexpr (W == 8) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+struct Raw {
+  using Type = unsigned short;
+  __device__ static Type load(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const unsigned short*>(p)); }
+  __device__ static void values(Type r, float (&v)[W]) { v[0] = bf16_value(r); }
+};
+template <>
+struct Raw<8> {
+  using Type = uint4;
+  __device__ static Type load(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ static void values(const Type& u, float (&v)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[2 * q] = __uint_as_float(w[q] << 16), v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
-  } else {
-    v[0] = bf16_value(__ldg(reinterpret_cast<const unsigned short*>(p)));
   }
+};
+template <int W>
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, float (&v)[W]) {
+  Raw<W>::values(Raw<W>::load(p), v);
 }
 template <int W>
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[W]) {
   if constexpr (W == 8) {
     uint32_t w[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
-      w[q] = *reinterpret_cast<const uint32_t*>(&b);
-    }
+    for (int q = 0; q < 4; ++q) w[q] = pair_bf16(v[2 * q], v[2 * q + 1]);
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     *p = __float2bfloat16_rn(v[0]);
   }
 }
 
-// A thread W columns of a token.  The slots of four choices at a time, so that
-// their rows are in flight together.
+// A block takes a token's columns from blockIdx.y * 2 W threads on, a thread W
+// of them and W others behind the block's first half; the rows of four choices
+// are in flight together.
 template <int W>
-__global__ void __launch_bounds__(256) combine(const CombineParams p) {
-  const int cols = p.N / W;
-  const int64_t total = p.T * cols;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t t = i / cols;
-    const int c = static_cast<int>(i - t * cols) * W;
-    float sum[W];
+__global__ void __launch_bounds__(128) combine(const CombineParams p) {
+  constexpr int U = 2;
+  const int c0 = (blockIdx.y * U * blockDim.x + threadIdx.x) * W;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    float sum[U][W];
 #pragma unroll
-    for (int q = 0; q < W; ++q) sum[q] = 0.f;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < W; ++q) sum[u][q] = 0.f;
     for (int j0 = 0; j0 < p.k; j0 += 4) {
-      float v[4][W], w[4];
+      typename Raw<W>::Type y[U][4];
+      float w[4];
+      int slot[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        w[j] = 0.f;
-        const int s = j0 + j < p.k ? __ldg(p.slots + t * p.k + j0 + j) : -1;
-        const bool real = s >= 0 && s < p.S;
-        if (real) {
-          load_bf16<W>(p.y + static_cast<int64_t>(s) * p.N + c, v[j]);
-          w[j] = p.weights ? __ldg(p.weights + t * p.k + j0 + j) : 1.f;
-        } else {
-#pragma unroll
-          for (int q = 0; q < W; ++q) v[j][q] = 0.f;
-        }
+        slot[j] = j0 + j < p.k ? __ldg(p.slots + t * p.k + j0 + j) : -1;
+        if (slot[j] >= p.S) slot[j] = -1;
+        w[j] = slot[j] >= 0 && p.weights ? __ldg(p.weights + t * p.k + j0 + j) : 1.f;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int q = 0; q < W; ++q) sum[q] = fmaf(w[j], v[j][q], sum[q]);
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u * blockDim.x * W;
+          if (slot[j] >= 0 && c < p.N) y[u][j] = Raw<W>::load(p.y + static_cast<int64_t>(slot[j]) * p.N + c);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (slot[j] < 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float v[W];
+          Raw<W>::values(y[u][j], v);
+#pragma unroll
+          for (int q = 0; q < W; ++q) sum[u][q] = fmaf(w[j], v[q], sum[u][q]);
+        }
+      }
     }
-    if (p.bf16) {
-      store_bf16<W>(static_cast<__nv_bfloat16*>(p.out) + t * p.N + c, sum);
-    } else {
-      float* out = static_cast<float*>(p.out) + t * p.N + c;
-      if constexpr (W == 8) {
-        reinterpret_cast<float4*>(out)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-        reinterpret_cast<float4*>(out)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * blockDim.x * W;
+      if (c >= p.N) break;
+      if (p.bf16) {
+        store_bf16<W>(static_cast<__nv_bfloat16*>(p.out) + t * p.N + c, sum[u]);
       } else {
-        out[0] = sum[0];
+        float* out = static_cast<float*>(p.out) + t * p.N + c;
+        if constexpr (W == 8) {
+          reinterpret_cast<float4*>(out)[0] = make_float4(sum[u][0], sum[u][1], sum[u][2], sum[u][3]);
+          reinterpret_cast<float4*>(out)[1] = make_float4(sum[u][4], sum[u][5], sum[u][6], sum[u][7]);
+        } else {
+          out[0] = sum[u][0];
+        }
       }
     }
   }
@@ -522,33 +636,51 @@ __global__ void __launch_bounds__(256) combine_backward(const CombineParams p) {
       if (slot[j] >= p.S) slot[j] = -1;
       w[j] = slot[j] >= 0 && p.weights ? __ldg(p.weights + t * p.k + j) : 1.f;
     }
-    for (int c = threadIdx.x * W; c < p.N; c += blockDim.x * W) {
-      float d[W];
-      if (p.bf16) {
-        load_bf16<W>(static_cast<const __nv_bfloat16*>(p.d_out) + t * p.N + c, d);
-      } else {
-        const float* src = static_cast<const float*>(p.d_out) + t * p.N + c;
-        if constexpr (W == 8) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
-          d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+    // U groups of columns at a time, all their rows in flight together
+    constexpr int U = KMAX <= 4 ? 2 : 1;
+    for (int c0 = threadIdx.x * W; c0 < p.N; c0 += U * blockDim.x * W) {
+      float d[U][W];
+      typename Raw<W>::Type y[U][KMAX];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * blockDim.x * W;
+        if (c >= p.N) break;
+        if (p.bf16) {
+          load_bf16<W>(static_cast<const __nv_bfloat16*>(p.d_out) + t * p.N + c, d[u]);
         } else {
-          d[0] = __ldg(src);
+          const float* src = static_cast<const float*>(p.d_out) + t * p.N + c;
+          if constexpr (W == 8) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+            d[u][0] = a.x, d[u][1] = a.y, d[u][2] = a.z, d[u][3] = a.w;
+            d[u][4] = b.x, d[u][5] = b.y, d[u][6] = b.z, d[u][7] = b.w;
+          } else {
+            d[u][0] = __ldg(src);
+          }
+        }
+        if (p.d_weights) {
+#pragma unroll
+          for (int j = 0; j < KMAX; ++j)
+            if (slot[j] >= 0) y[u][j] = Raw<W>::load(p.y + static_cast<int64_t>(slot[j]) * p.N + c);
         }
       }
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        if (slot[j] < 0) continue;
-        const int64_t at = static_cast<int64_t>(slot[j]) * p.N + c;
-        if (p.d_weights) {
-          float y[W];
-          load_bf16<W>(p.y + at, y);
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * blockDim.x * W;
+        if (c >= p.N) break;
 #pragma unroll
-          for (int q = 0; q < W; ++q) dot[j] = fmaf(y[q], d[q], dot[j]);
+        for (int j = 0; j < KMAX; ++j) {
+          if (slot[j] < 0) continue;
+          if (p.d_weights) {
+            float v[W];
+            Raw<W>::values(y[u][j], v);
+#pragma unroll
+            for (int q = 0; q < W; ++q) dot[j] = fmaf(v[q], d[u][q], dot[j]);
+          }
+          float g[W];
+#pragma unroll
+          for (int q = 0; q < W; ++q) g[q] = w[j] * d[u][q];
+          store_bf16<W>(p.dy + static_cast<int64_t>(slot[j]) * p.N + c, g);
         }
-        float g[W];
-#pragma unroll
-        for (int q = 0; q < W; ++q) g[q] = w[j] * d[q];
-        store_bf16<W>(p.dy + at, g);
       }
     }
     if (p.d_weights) {
@@ -591,23 +723,38 @@ struct RunRoute {
   static cudaError_t run(RouteParams& p, cudaStream_t s) {
     p.vec = whole_vectors<VPL, BF16>(p.logits, p.ld, p.E);
     if (p.T <= kFewTokens) {
-      const int smem = ((kFewWarps + 1) * p.E + static_cast<int>(p.T) * p.k) * 4;
-      const cudaError_t e =
-          cudaFuncSetAttribute(route_few<VPL, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
-      if (e != cudaSuccess) return e;
+      const int smem = (kFewWarps + 1) * p.E * 4;
+      if (smem > 40 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(route_few<VPL, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+      }
       TraceScope tr("route_few", s);
       route_few<VPL, BF16><<<1, 32 * kFewWarps, smem, s>>>(p);
       return cudaGetLastError();
     }
+    const int smem = (kChooseWarps<VPL> + 1) * p.E * 4;
+    cudaError_t e = cudaSuccess;
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(route_choose<VPL, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     {
       TraceScope tr("route_choose", s);
-      route_choose<VPL, BF16><<<p.blocks, 32 * kRouteWarps, p.E * 4, s>>>(p);
+      route_choose<VPL, BF16><<<p.blocks, 32 * kChooseWarps<VPL>, smem, s>>>(p);
     }
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    cudaLaunchAttribute overlap;
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.blocks));
+    cfg.blockDim = dim3(kPlaceThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(2 * p.E * 4);
+    cfg.stream = s;
+    cfg.attrs = &overlap;
+    cfg.numAttrs = 1;
     TraceScope tr("route_place", s);
-    route_place<<<p.blocks, 32 * kRouteWarps, (kRouteWarps + 2) * p.E * 4, s>>>(p);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, route_place, p);
   }
 };
 
@@ -632,8 +779,12 @@ bool wide_rows(int64_t N, std::initializer_list<const void*> ps) {
 
 template <int W>
 cudaError_t launch_combine_backward_w(const CombineParams& p, int sms, cudaStream_t s) {
-  const int threads = static_cast<int>(std::min<int64_t>(256, ceil_div(ceil_div(p.N, W), 32) * 32));
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.T, 16 * sms));
+  // Many tokens: more and smaller blocks, which wait less for one another
+  // (16384 tokens x 4 x 4096: 190 us with 64 threads, 195 with 128, 214 with 256);
+  // few: more threads a token (300 tokens: 4.4 us with 256, 6.8 with 64).
+  const int64_t most = p.T >= 4 * sms ? 64 : 256;
+  const int threads = static_cast<int>(std::min<int64_t>(most, ceil_div(ceil_div(p.N, W), 32) * 32));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.T, 64 * sms));
   TraceScope tr("combine_backward", s);
   if (p.k <= 1) combine_backward<W, 1><<<grid, threads, 0, s>>>(p);
   else if (p.k <= 2) combine_backward<W, 2><<<grid, threads, 0, s>>>(p);
@@ -665,7 +816,7 @@ cudaError_t launch_route(const RouteRequest& r, cudaStream_t s) {
   p.rows = r.rows;
   p.slots = r.slots;
   p.hist = static_cast<int*>(r.workspace);
-  p.per_block = std::max<int64_t>(kRouteWarps, ceil_div(r.T, kRouteBlocks));
+  p.per_block = std::max<int64_t>(32, ceil_div(r.T, kRouteBlocks));
   p.blocks = static_cast<int>(ceil_div(r.T, p.per_block));
   return by_experts<RunRoute>(r.E, r.bf16, p, s);
 }
@@ -685,7 +836,7 @@ cudaError_t launch_route_backward(const RouteBackwardRequest& r, cudaStream_t s)
   p.weights = r.weights;
   p.d_logits = r.d_logits;
   p.ld_d = r.E;
-  p.d_vec = wide_rows(r.E, {r.d_logits});
+  p.d_vec = wide_rows(r.E, {r.d_logits});  // whole rows of 8
   return by_experts<RunRouteBackward>(r.E, r.bf16, p, ctx->num_sms, s);
 }
 
@@ -703,12 +854,15 @@ cudaError_t launch_combine(const CombineRequest& r, cudaStream_t s) {
   p.out = r.out;
   p.bf16 = r.bf16;
   const bool wide = wide_rows(r.N, {r.y, r.out});
-  const int64_t blocks = std::min<int64_t>(ceil_div(r.T * (r.N / (wide ? 8 : 1)), 256), 64 * ctx->num_sms);
+  const int64_t vectors = r.N / (wide ? 8 : 1);  // a row's
+  const int threads = static_cast<int>(std::min<int64_t>(128, ceil_div(ceil_div(vectors, 2), 32) * 32));
+  const unsigned parts = static_cast<unsigned>(ceil_div(vectors, 2 * threads));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(r.T, std::max<int64_t>(1, 128 * ctx->num_sms / parts))), parts);
   TraceScope tr("combine", s);
   if (wide)
-    combine<8><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
+    combine<8><<<grid, threads, 0, s>>>(p);
   else
-    combine<1><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
+    combine<1><<<grid, threads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
