@@ -21,7 +21,8 @@
 // Per pair of CTAs: CTA r loads 128 of the 256 feature rows (A) and half of
 // the tile's rows (B) per 128-byte contraction block, the leader issues
 // tcgen05.mma.cta_group::2 kind::mxf8f6f4.block_scale into one 256-column
-// FP32 accumulator in each CTA's tensor memory.
+// FP32 accumulator in each CTA's tensor memory; tiles of at most 128 rows take
+// its halves in turn, so that one is read out under the next one's products.
 //   warp 0      TMA: A, its scale atoms, B (by box, or by gathered rows)
 //   warp 1      MMA (leader)
 //   warps 2, 3  B's scales: from row-major bytes (any rows, gathered too) or
@@ -36,6 +37,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "blockquant.cuh"
 #include "internal.h"
@@ -62,7 +64,7 @@ constexpr int OFF_SFA = OFF_B + STAGES * B_BYTES;
 constexpr int OFF_SFB = OFF_SFA + STAGES * SFA_BYTES;
 constexpr int OFF_TILES = OFF_SFB + SGROUPS * SG * SFB_TILE;
 constexpr int OFF_BAR = OFF_TILES + ((kExpertsMax + 1) * 12 + 15) / 16 * 16;  // starts and segments
-constexpr int N_BARS = 2 * STAGES + 2 + 2 * SGROUPS + 1;
+constexpr int N_BARS = 2 * STAGES + 4 + 2 * SGROUPS + 1;
 constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16 + 1024;
 static_assert(SMEM <= 232448, "shared memory budget");
 static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
@@ -85,10 +87,11 @@ struct ExpertParams {
   int64_t b_pitch;
   int b_vec, b_word;  // rows of b_scales are 16-byte (4-byte) aligned
   // segments are the contraction (grad): B has J rows per expert, A and B hold
-  // the segments padded to multiples of 128 from pads[e] on
+  // the segments padded to multiples of 128 one after the other, row_tiles in all
   int J, j_tiles;
-  const int* pads;
+  int row_tiles;
   int b_ks4;
+  int late_wait;      // the kernel before writes nothing that is read here
   __nv_bfloat16* y;   // [S][F], or [E][J][F]
   uint32_t idesc;     // without N
   int* status;
@@ -106,6 +109,41 @@ __device__ __forceinline__ int2 segment(const int* offsets, int e, int S) {
   return make_int2(lo, min(max(__ldg(offsets + e + 1), lo), S));
 }
 
+// starts[e], e up to E: the sum of count(e) over the experts before e, by THREADS
+// threads (to be read after a __syncthreads()).  Offsets that rise and fall may
+// count more than there is: the sums stop short of 2^30 then.
+__device__ __forceinline__ int capped_add(int a, int b) { return min(a + b, (1 << 30) - 1); }
+template <int THREADS, typename Count>
+__device__ __forceinline__ void expert_starts(int E, int* starts, Count&& count) {
+  __shared__ int warp_sums[THREADS / 32];
+  constexpr int PER = (kExpertsMax + THREADS) / THREADS;  // E + 1 places
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int n[PER], own = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = PER * static_cast<int>(threadIdx.x) + i;
+    n[i] = e < E ? count(e) : 0;
+    own = capped_add(own, n[i]);
+  }
+  int sum = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum = capped_add(sum, v);
+  }
+  if (lane == 31) warp_sums[warp] = sum;
+  __syncthreads();
+  int at = __shfl_up_sync(0xffffffffu, sum, 1);
+  if (lane == 0) at = 0;
+  for (int w = 0; w < warp; ++w) at = capped_add(at, warp_sums[w]);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = PER * static_cast<int>(threadIdx.x) + i;
+    if (e <= E) starts[e] = at;
+    at = capped_add(at, n[i]);
+  }
+}
+
 template <bool GRAD>
 __device__ __forceinline__ Tile tile_of(const ExpertParams& p, const int* starts, const int2* segs, int u) {
   Tile t;
@@ -118,8 +156,11 @@ __device__ __forceinline__ Tile tile_of(const ExpertParams& p, const int* starts
     t.b0 = (r - f * p.j_tiles) * PJ;
     t.live = min(PJ, p.J - t.b0);
     t.out0 = t.e * p.J + t.b0;
-    t.c0 = __ldg(p.pads + t.e);
-    t.k_tiles = (__ldg(p.pads + t.e + 1) - t.c0) / KB;
+    // segments that overlap (offsets that fall) do not fit the padded rows:
+    // what is past their end is left out
+    const int begin = min(starts[t.e], p.row_tiles), end = min(starts[t.e + 1], p.row_tiles);
+    t.c0 = begin * KB;
+    t.k_tiles = end - begin;
   } else {
     int lo = 0, hi = p.E;  // the expert with starts[e] <= u < starts[e + 1]
     while (hi - lo > 1) {
@@ -167,15 +208,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 1;
-  uint64_t* sfull = tempty + 1;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* sfull = tempty + 2;
   uint64_t* sempty = sfull + SGROUPS;
   uint64_t* done = sempty + SGROUPS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int never_abort_storage = 0;
   volatile int* never_abort = &never_abort_storage;
-  __shared__ int warp_sums[THREADS / 32];
 
   // broadcasts, so that the compiler knows them to be warp-uniform
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -185,11 +225,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 2);
+      mbar_init(&full[s], 1);  // the leader's arrival, which expects both CTAs' bytes
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * EPI_WARPS);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&tfull[h], 1);
+      mbar_init(&tempty[h], EPI_WARPS);  // half of the warps of both CTAs
+    }
     for (int g = 0; g < SGROUPS; ++g) {
       mbar_init(&sfull[g], 4);
       mbar_init(&sempty[g], 1);
@@ -199,47 +241,46 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_barrier_init();
     fence_proxy_async_smem();
   }
+  if (warp == 3 && lane == 0) {
+    tmap_prefetch(&tmA);
+    tmap_prefetch(&tmSFA);
+    tmap_prefetch(&tmB);
+    tmap_prefetch(&tmB16);
+  }
+  __syncwarp();
+  // both CTAs' barriers are initialized before any signal across: the two
+  // halves of the cluster's barrier, with what needs no signal between them
+  cluster_arrive_relaxed();
   if (warp == 2) {
     tmem_alloc_pair(tmem_holder, TMEM_COLS);
     tmem_relinquish_pair();
   }
-  // first tile of each expert: an exclusive sum over the experts, two a thread
-  int tiles;
+  // the first tile of each expert, or its first padded row tile
+  int tiles = 0;
   if constexpr (GRAD) {
     tiles = p.E * p.j_tiles * p.f_tiles;
+    expert_starts<THREADS>(p.E, starts, [&](int e) {
+      const int2 s = segment(p.offsets, e, p.S);
+      return (s.y - s.x + KB - 1) / KB;
+    });
   } else {
-    static_assert(kExpertsMax <= 2 * THREADS, "two experts a thread");
-    int n[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = 2 * static_cast<int>(threadIdx.x) + i;
-      n[i] = 0;
-      if (e < p.E) {
-        const int2 s = segment(p.offsets, e, p.S);
-        segs[e] = s;
-        n[i] = (s.y - s.x + PJ - 1) / PJ * p.f_tiles;
-      }
-    }
-    int sum = n[0] + n[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) warp_sums[warp] = sum;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sums[w];
-    const int first = before + sum - n[0] - n[1];
-    if (2 * static_cast<int>(threadIdx.x) <= p.E) starts[2 * threadIdx.x] = first;
-    if (2 * static_cast<int>(threadIdx.x) + 1 <= p.E) starts[2 * threadIdx.x + 1] = first + n[0];
+    expert_starts<THREADS>(p.E, starts, [&](int e) {
+      const int2 s = segment(p.offsets, e, p.S);
+      segs[e] = s;
+      return static_cast<int>(min(static_cast<int64_t>((s.y - s.x + PJ - 1) / PJ) * p.f_tiles, int64_t((1 << 30) - 1)));
+    });
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers initialized before any cross-CTA signal
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   if constexpr (!GRAD) tiles = starts[p.E];
+  // Launched before the kernel ahead has ended.  The weights' gradient reads
+  // nothing of the kernel ahead of it (dX), so it waits for it last: its blocks
+  // fill the SMs that dX's last tiles leave.
+  if (!p.late_wait) pdl_wait();
+  pdl_launch();
 
   // 640 threads with 96 registers each: the epilogue's 64 sums and the scale
   // warps' 16 words and 4 row pointers both fit, so nothing is moved between
@@ -258,7 +299,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int k_tiles = GRAD ? uniform(t.k_tiles) : p.k_tiles;
         const int nn = uniform(t.nn), half = nn >> 1;
         const int c0 = GRAD ? uniform(t.c0) : 0, f0 = uniform(t.f0), e = GRAD ? 0 : uniform(t.e);
-        const uint32_t tx = 2 * (A_BYTES + SFA_BYTES + half * KB);
+        // B's rows past the segment are not loaded: their columns of the
+        // accumulator are never stored, whatever they hold
+        const int live = uniform(t.live), need = min(half, max(0, live - static_cast<int>(rank) * half));
+        constexpr int UNIT = GATHER ? 4 : 16;  // rows of a load
+        const int loaded = nn == PJ && !GATHER ? 2 * half
+                                               : (min(live, half) + UNIT - 1) / UNIT * UNIT +
+                                                     (max(0, live - half) + UNIT - 1) / UNIT * UNIT;
+        const uint32_t tx = 2 * (A_BYTES + SFA_BYTES) + loaded * KB;
         const int atom_row = 4 * ((e * p.a_rt + 2 * (f0 / PF) + static_cast<int>(rank)) * p.ks4 + c0 / KB);
         const int f_row = f0 + static_cast<int>(rank) * 128;
         const int row0 = uniform(t.b0) + static_cast<int>(rank) * half;
@@ -285,15 +333,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           tma_load_3d_pair_if(issue, sfa0 + stage * SFA_BYTES, &tmSFA, bar, 0, atom_row + 4 * kt, 0);
           if constexpr (GATHER) {
             __syncwarp();
-            if (4 * lane < half)
+            if (4 * lane < need)
               tma_gather4_pair(sB + stage * B_BYTES + lane * 4 * KB, &tmB, bar, x, r0, r1, r2, r3);
           } else if (nn == PJ) {
             tma_load_3d_pair_if(issue, b0 + stage * B_BYTES, &tmB, bar, x, row0, 0);
           } else {
-            for (int i = 0; i < half; i += 16)
+            for (int i = 0; i < need; i += 16)
               tma_load_3d_pair_if(issue, b0 + stage * B_BYTES + i * KB, &tmB16, bar, x, row0 + i, 0);
           }
-          if (!leader && lane == 0) mbar_arrive_cluster(bar);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
@@ -329,8 +376,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (leader) {
         // the whole warp, one lane of it issuing (elect_one)
         const uint32_t issue = elect_one();
-        int stage = 0, g = 0;
-        uint32_t phase = 0, tph = 0, gph = 0;
+        int stage = 0, g = 0, narrow_half = 0;
+        uint32_t phase = 0, tph = 0, gph = 0;  // tph: a bit per half of the accumulator
         bool ok = true, ready = false, scales_ready = false;
         const uint64_t a_d0 = smem_desc(smem_u32(sA), 16, 1024, 2), b_d0 = smem_desc(smem_u32(sB), 16, 1024, 2);
         const uint64_t sfa_d0 = smem_desc(smem_u32(sSFA), 0, 128, 0), sfb_d0 = smem_desc(smem_u32(sSFB), 0, 128, 0);
@@ -339,34 +386,61 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int k_tiles = GRAD ? uniform(t.k_tiles) : p.k_tiles;
           const int nn = uniform(t.nn);
           if (k_tiles == 0) continue;
-          if (!__all_sync(0xffffffffu, mbar_wait(tempty, tph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteMmaTmem))) break;
+          const uint32_t halves = nn > PJ / 2 ? 3u : 1u << narrow_half;  // of the accumulator
+          for (int h = 0; ok && h < 2; ++h)
+            if ((halves >> h) & 1u)
+              ok = __all_sync(0xffffffffu, mbar_wait(&tempty[h], ((tph >> h) & 1u) ^ 1u, p.timeout_ns, abort_flag, p.status,
+                                                     kSiteMmaTmem));
+          if (!ok) break;
           tc_fence_after();
+          const uint32_t acc = tmem + (halves == 2u ? PJ / 2 : 0);
           const uint32_t i0 = p.idesc | (static_cast<uint32_t>(nn >> 3) << 17);
           const uint32_t i1 = i0 | (1u << 4) | (1u << 29), i2 = i0 | (2u << 4) | (2u << 29), i3 = i0 | (3u << 4) | (3u << 29);
-          for (int kt = 0; kt < k_tiles; ++kt) {
+          auto block = [&](int st, int kt) {
+            const uint64_t a_d = desc_add(a_d0, st * A_BYTES), b_d = desc_add(b_d0, st * B_BYTES);
+            const uint64_t sfb_d = desc_add(sfb_d0, (g * SG + (kt & (SG - 1))) * SFB_TILE);
+            const uint32_t sfa_t = tmem + static_cast<uint32_t>(SF_COL0 + st * SF_COLS);
+            const uint32_t sfb_t = sfa_t + 4;
+            tc_cp_sf_pair_if(issue, sfa_t, desc_add(sfa_d0, st * SFA_BYTES));
+            tc_cp_sf_pair_if(issue, sfb_t, sfb_d);
+            if (nn > 128) tc_cp_sf_pair_if(issue, sfb_t + 4, desc_add(sfb_d, 512));
+            mma_mxf8_pair_x4_if(issue, acc, a_d, b_d, i0, i1, i2, i3, sfa_t, sfb_t, kt > 0 ? 1u : 0u);
+            tc_commit_pair_mc_if(issue, &empty[st], 0x3);
+          };
+          // Two contraction blocks at a time: the barriers' latencies, about as
+          // long as a block's instructions, are paid once for both.
+          for (int kt = 0; kt < k_tiles; kt += 2) {
+            const bool two = kt + 1 < k_tiles;
+            const int next = stage + 1 == STAGES ? 0 : stage + 1;
+            const uint32_t next_phase = stage + 1 == STAGES ? phase ^ 1u : phase;
             if ((kt & (SG - 1)) == 0 && !scales_ready)
               ok = __all_sync(0xffffffffu, mbar_spin_acq_cluster(&sfull[g], gph, p.timeout_ns, abort_flag, p.status,
                                                                  kSiteMmaScales));
-            if (ok && !ready)
-              ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag, p.status, kSiteMma));
+            if (ok && !ready) {
+              bool there = mbar_wait(&full[stage], phase, p.timeout_ns, abort_flag, p.status, kSiteMma);
+              if (there && two) there = mbar_wait(&full[next], next_phase, p.timeout_ns, abort_flag, p.status, kSiteMma);
+              ok = __all_sync(0xffffffffu, there);
+            }
             if (!ok) break;
             tc_fence_after();
-            const uint64_t a_d = desc_add(a_d0, stage * A_BYTES), b_d = desc_add(b_d0, stage * B_BYTES);
-            const uint64_t sfb_d = desc_add(sfb_d0, (g * SG + (kt & (SG - 1))) * SFB_TILE);
-            const uint32_t sfa_t = tmem + static_cast<uint32_t>(SF_COL0 + stage * SF_COLS);
-            const uint32_t sfb_t = sfa_t + 4;
-            tc_cp_sf_pair_if(issue, sfa_t, desc_add(sfa_d0, stage * SFA_BYTES));
-            tc_cp_sf_pair_if(issue, sfb_t, sfb_d);
-            if (nn > 128) tc_cp_sf_pair_if(issue, sfb_t + 4, desc_add(sfb_d, 512));
-            mma_mxf8_pair_x4_if(issue, tmem, a_d, b_d, i0, i1, i2, i3, sfa_t, sfb_t, kt > 0 ? 1u : 0u);
-            tc_commit_pair_mc_if(issue, &empty[stage], 0x3);
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
+            block(stage, kt);
+            stage = next;
+            phase = next_phase;
+            if (two) {
+              block(stage, kt + 1);
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
             }
-            // looked at a block ahead, so that its latency passes meanwhile
-            ready = __all_sync(0xffffffffu, mbar_test(&full[stage], phase));
-            if ((kt & (SG - 1)) == SG - 1 || kt + 1 == k_tiles) {
+            // looked at two blocks ahead, so that the latency passes meanwhile
+            // (a tile that is left with one block finds the second barrier a
+            // tile early or waits for it)
+            const int after = stage + 1 == STAGES ? 0 : stage + 1;
+            const bool one = mbar_test(&full[stage], phase);
+            const bool both = mbar_test(&full[after], stage + 1 == STAGES ? phase ^ 1u : phase);
+            ready = __all_sync(0xffffffffu, one && both);
+            if ((kt & (SG - 1)) == SG - 2 || kt + 2 >= k_tiles) {
               tc_commit_pair_mc_if(issue, &sempty[g], 0x3);
               if (++g == SGROUPS) {
                 g = 0;
@@ -376,8 +450,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           if (!ok) break;
-          tc_commit_pair_mc_if(issue, tfull, 0x3);
-          tph ^= 1u;
+          for (int h = 0; h < 2; ++h)
+            if ((halves >> h) & 1u) tc_commit_pair_mc_if(issue, &tfull[h], 0x3);
+          tph ^= halves;
+          if (halves != 3u) narrow_half ^= 1;
         }
         tc_commit_pair_mc_if(issue, done, 0x1);
         if (issue) mbar_wait(done, 0, p.timeout_ns, never_abort, p.status, kSiteDone);
@@ -394,24 +470,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int u = cid; ok && u < tiles; u += ncl) {
         const Tile t = tile_of<GRAD>(p, starts, segs, u);
-        const bool mine = t.nn > 128 * a;
-        const uint8_t* src[4] = {nullptr, nullptr, nullptr, nullptr};
-        if (mine) {
-          if constexpr (GRAD) {
-            src[0] = p.b_scales + (static_cast<int64_t>(t.b0 / 128 + a) * p.b_ks4 + t.c0 / KB) * 512 + lane * 16;
-          } else {
+        // a narrow tile has one atom: the two warps take its groups in turn
+        const bool narrow = t.nn <= 128;
+        const int atom = narrow ? 0 : a, every = narrow ? 2 * SG : SG;
+        const uint8_t* src[4];
+        if constexpr (GRAD) {
+          src[0] = p.b_scales + (static_cast<int64_t>(t.b0 / 128 + atom) * p.b_ks4 + t.c0 / KB) * 512 + lane * 16;
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              int r = t.b0 + min(128 * a + 32 * i + lane, t.live - 1);
-              if constexpr (GATHER) r = min(max(__ldg(p.rows + r), 0), p.X - 1);
-              src[i] = p.b_scales + static_cast<int64_t>(r) * p.b_pitch;
-            }
+          for (int i = 0; i < 4; ++i) {
+            int r = t.b0 + min(128 * atom + 32 * i + lane, t.live - 1);
+            if constexpr (GATHER) r = min(max(__ldg(p.rows + r), 0), p.X - 1);
+            src[i] = p.b_scales + static_cast<int64_t>(r) * p.b_pitch;
           }
         }
         // the words of the group from block k0 on, as this lane stores them
         uint4 w[SG];
         auto load = [&](int k0) {
-          if (!mine || k0 >= t.k_tiles) return;
+          if (k0 >= t.k_tiles) return;
           if constexpr (GRAD) {
 #pragma unroll
             for (int j = 0; j < SG; ++j)
@@ -452,21 +528,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         };
-        load(0);
+        int due = narrow ? a * SG : 0;  // this warp's next group
+        load(due);
         for (int k0 = 0; k0 < t.k_tiles; k0 += SG) {
           if (lane == 0) ok = mbar_poll(&sempty[g], gph ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteScales);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          const bool mine = k0 == due;
           if (mine) {
-            uint8_t* dst = sSFB + g * SG * SFB_TILE + a * 512 + lane * 16;
+            uint8_t* dst = sSFB + g * SG * SFB_TILE + atom * 512 + lane * 16;
 #pragma unroll
             for (int j = 0; j < SG; ++j)
               if (k0 + j < t.k_tiles) *reinterpret_cast<uint4*>(dst + j * SFB_TILE) = w[j];
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
-          load(k0 + SG);  // in flight while the release takes its time
           __syncwarp();
           if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sfull[g]), 0));
+          if (mine) {
+            due += every;
+            load(due);
+          }
           used |= 1u << g;
           last_par = (last_par & ~(1u << g)) | (gph << g);
           if (++g == SGROUPS) {
@@ -486,20 +567,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     // --------------------------------------------------------- epilogue (both CTAs)
     const int ew = warp - 4;
     const int q = warp & 3;  // TMEM lane quarter: 32 features
-    const int g = ew >> 2;   // 64 of the tile's rows
+    const int g = ew >> 2;   // 64 of the accumulator's columns
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g * 64);
     const bool odd = lane & 1;
     uint32_t tph = 0;
+    int narrow_half = 0;
     for (int u = cid; u < tiles; u += ncl) {
       const Tile t = tile_of<GRAD>(p, starts, segs, u);
+      int row = g * 64;  // of the tile
+      if (t.nn <= PJ / 2 && t.k_tiles > 0) {
+        const bool other = (g >> 1) != narrow_half;
+        narrow_half ^= 1;
+        if (other) continue;
+        row = (g & 1) * 64;
+      }
       const int f = t.f0 + static_cast<int>(rank) * 128 + q * 32 + (lane & ~1);
-      const int live = f < p.F ? min(t.live - g * 64, 64) : 0;
+      const int live = f < p.F ? min(t.live - row, 64) : 0;
       // lane pairs exchange halves: even lanes store even rows, odd lanes odd
       // ones, two features each
-      __nv_bfloat16* dst = p.y + static_cast<int64_t>(t.out0 + g * 64 + (odd ? 1 : 0)) * p.F + f;
+      __nv_bfloat16* dst = p.y + static_cast<int64_t>(t.out0 + row + (odd ? 1 : 0)) * p.F + f;
       uint32_t v[32];  // bfloat16 pairs: this lane's feature in rows 2 c and 2 c + 1
       if (t.k_tiles > 0) {
-        if (!mbar_wait(tfull, tph, p.timeout_ns, abort_flag, p.status, kSiteEpilogue)) break;
+        if (!mbar_wait(&tfull[g >> 1], tph, p.timeout_ns, abort_flag, p.status, kSiteEpilogue)) break;
         tph ^= 1u;
         tc_fence_after();
         if (live > 0) {
@@ -518,7 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(tempty), 0));
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[g >> 1]), 0));
       } else {  // an expert without rows: its sums are empty
 #pragma unroll
         for (int c = 0; c < 32; ++c) v[c] = 0u;
@@ -533,9 +622,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
+  __syncwarp();
+  if (p.late_wait) pdl_wait();
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // no signal may target a CTA that has exited
+  cluster_arrive_relaxed();  // no signal may target a CTA that has exited; the
+  cluster_wait();            // stores need not have landed for that
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);
@@ -557,6 +648,7 @@ __global__ void __launch_bounds__(256) expert_gather(const uint8_t* x, const uin
                                                      int X, int K, uint8_t* out, uint8_t* out_scales) {
   const int units = K / 16, blocks = K / 32;
   const int lane = threadIdx.x & 31;
+  pdl_launch();
   for (int s = blockIdx.x * 8 + (threadIdx.x >> 5); s < S; s += gridDim.x * 8) {
     const int row = min(max(__ldg(rows + s), 0), X - 1);
     const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(row) * K);
@@ -583,148 +675,145 @@ __global__ void __launch_bounds__(256) expert_gather(const uint8_t* x, const uin
 // ---------------------------------------------------------------------------
 // The backward's operands
 // ---------------------------------------------------------------------------
-// Padded starts of the segments (multiples of 128) and, per padded tile of 128
-// rows, its first row and number of rows (0: none).
-__global__ void __launch_bounds__(1024) expert_plan(const int* offsets, int E, int S, int tiles, int* pads, int2* table) {
-  __shared__ int sums[32];
-  __shared__ int ends[kExpertsMax];
-  __shared__ int lows[kExpertsMax];
-  __shared__ int lens[kExpertsMax];
-  const int e = threadIdx.x, lane = e & 31;
-  int2 s = make_int2(0, 0);
-  if (e < E) s = segment(offsets, e, S);
-  const int n = (s.y - s.x + 127) / 128;
-  int sum = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += v;
-  }
-  if (lane == 31) sums[e >> 5] = sum;
-  __syncthreads();
-  for (int w = 0; w < (e >> 5); ++w) sum += sums[w];
-  // segments that overlap (offsets that fall) do not fit the table: what is
-  // past its end is left out
-  const int end = min(sum, tiles), begin = min(sum - n, tiles);
-  ends[e] = end;
-  lows[e] = s.x;
-  lens[e] = s.y - s.x;
-  if (e < E) pads[e] = begin * 128;
-  if (e == E - 1) pads[E] = end * 128;
-  __syncthreads();
-  for (int i = e; i < tiles; i += 1024) {
-    int lo = -1, hi = E - 1;  // the first expert that ends past i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (ends[mid] > i) hi = mid; else lo = mid;
-    }
-    int2 t = make_int2(0, 0);
-    if (ends[hi] > i) {
-      const int k = i - (hi ? ends[hi - 1] : 0);
-      t = make_int2(lows[hi] + 128 * k, min(128, lens[hi] - 128 * k));
-    }
-    table[i] = t;
-  }
-}
-
 // bf16 rows quantized in blocks of 32 down the rows, tiles of 128 rows x 128
 // columns, into transposed codes [columns][padded rows] and scale atoms: the
 // contraction-major operands of dW and dX.  dY is quantized along its rows
-// too, from the same tile.
+// too, from the same tile.  A tile's segment and rows come from the offsets: each
+// block sums the segments' padded lengths itself (about 1 us; a kernel that
+// wrote a table ahead took 3).
 struct SegQuant {
   const __nv_bfloat16* x;
   int cols, col_tiles;
-  const int* rows;   // gathered, or null
+  const int* rows;   // X: gathered, or null
   int X;             // rows of x
-  const int2* table;  // padded tiles, or null: every `per` rows are a segment
-  int per, per_tiles;
+  int per, per_tiles;  // W: every `per` rows are a segment
   int tiles;         // padded row tiles
   uint8_t* codes;    // [segment group][cols][pitch]
-  int64_t pitch, group_codes;  // group: all tiles (table), or one segment
+  int64_t pitch, group_codes;  // group: all tiles, or one segment (W)
   uint8_t* atoms;
   int ks4;           // atoms per row tile of 128 columns
   int64_t group_atoms;
-  uint8_t* row_codes;   // null: not along the rows
+  uint8_t* row_codes;   // dY: along the rows too
   uint8_t* row_scales;  // [rows][cols / 32]
 };
+enum { kJobW, kJobDy, kJobX };  // rows per expert; by the offsets' segments, padded; the same, gathered
 struct SegJobs {
+  const int* offsets;
+  int E, S;
   SegQuant job[3];
   int first[4];  // first tile of each job, and their end
 };
 
-constexpr int QSTAGES = 2;
+// One tile a block at a time and four blocks an SM, whose phases overlap: the
+// next tile is fetched while the codes leave (32768 rows x 16 experts of 4096 x
+// 4096, 1.7 GB: 330 us; two tiles a block and two blocks an SM 345).
 constexpr int QTILE = 128 * 256;
-constexpr int QSMEM = QSTAGES * QTILE + 128 * 144;
+constexpr int QSMEM = QTILE + 128 * 144;
+constexpr int QBLOCKS = 4;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
 template <int CODE>
-__global__ void __launch_bounds__(256) expert_quant(const __grid_constant__ SegJobs jobs) {
+__global__ void __launch_bounds__(256, QBLOCKS) expert_quant(const __grid_constant__ SegJobs jobs) {
   extern __shared__ __align__(16) uint8_t qsmem[];
-  uint8_t* ostg = qsmem + QSTAGES * QTILE;  // 128 columns x 128 codes, rows of 144 bytes
+  uint8_t* ostg = qsmem + QTILE;  // 128 columns x 128 codes, rows of 144 bytes
   __shared__ __align__(16) uint8_t sstg[512];
+  __shared__ int starts[kExpertsMax + 1];
   const int t = threadIdx.x;
+  pdl_launch();
+  expert_starts<256>(jobs.E, starts, [&](int e) {
+    const int2 s = segment(jobs.offsets, e, jobs.S);
+    return (s.y - s.x + 127) / 128;
+  });
+  __syncthreads();
   const int total = jobs.first[3];
 
+  // Every use of a job is compiled for that job: its sizes are then operands
+  // from the kernel's parameters, and the branches that it does not take are
+  // gone (through a pointer to the job, the loop took 386 us where it takes 343).
+  auto with_job = [&](int u, auto&& f) {
+    if (u < jobs.first[1]) f(std::integral_constant<int, 0>());
+    else if (u < jobs.first[2]) f(std::integral_constant<int, 1>());
+    else f(std::integral_constant<int, 2>());
+  };
   struct Where {
-    const SegQuant* q;
     int tile, src, live, c0;
   };
-  auto where = [&](int u) {
+  int expert = 0;
+  int2 rows = segment(jobs.offsets, 0, jobs.S);  // of the expert
+  auto where = [&](auto job, int u) {
+    constexpr int J = decltype(job)::value;
+    const SegQuant& q = jobs.job[J];
     Where w;
-    const int k = u < jobs.first[1] ? 0 : (u < jobs.first[2] ? 1 : 2);
-    w.q = &jobs.job[k];
-    const int r = u - jobs.first[k];
-    w.tile = r / w.q->col_tiles;
-    w.c0 = (r - w.tile * w.q->col_tiles) * 128;
-    if (w.q->table) {
-      const int2 s = __ldg(w.q->table + w.tile);
-      w.src = s.x;
-      w.live = s.y;
+    const int r = u - jobs.first[J];
+    w.tile = r / q.col_tiles;
+    w.c0 = (r - w.tile * q.col_tiles) * 128;
+    if constexpr (J != kJobW) {
+      // the last expert that starts at or before the tile, often the one before's
+      if (w.tile < starts[expert] || w.tile >= starts[expert + 1]) {
+        int lo = 0, hi = jobs.E;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (starts[mid] <= w.tile) lo = mid; else hi = mid;
+        }
+        expert = lo;
+        rows = segment(jobs.offsets, lo, jobs.S);
+      }
+      w.src = w.live = 0;
+      if (w.tile < starts[jobs.E]) {
+        const int row = 128 * (w.tile - starts[expert]);
+        w.src = rows.x + row;
+        w.live = min(128, rows.y - rows.x - row);
+      }
     } else {
-      const int e = w.tile / w.q->per_tiles, i = w.tile - e * w.q->per_tiles;
-      w.src = e * w.q->per + i * 128;
-      w.live = min(128, w.q->per - i * 128);
+      const int e = w.tile / q.per_tiles, i = w.tile - e * q.per_tiles;
+      w.src = e * q.per + i * 128;
+      w.live = min(128, q.per - i * 128);
     }
     return w;
   };
   // 16-byte chunk j of the thread: row (t + 256 j) / 16, columns 8 (t % 16) ..;
   // rows past the segment and columns past the array become zeros
-  auto load = [&](int u, int st) {
-    if (u < total) {
-      const Where w = where(u);
-      const uint32_t base = smem_u32(qsmem + st * QTILE);
-      const int c = w.c0 + 8 * (t & 15);
-      if (w.live > 0) {
+  auto load = [&](auto job, const Where& w) {
+    constexpr int J = decltype(job)::value;
+    const SegQuant& q = jobs.job[J];
+    const uint32_t base = smem_u32(qsmem);
+    const int c = w.c0 + 8 * (t & 15);
+    if (w.live <= 0) return;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = (t >> 4) + 16 * j;
-          const bool real = r < w.live && c < w.q->cols;
-          int row = w.src + (r < w.live ? r : 0);
-          if (w.q->rows) row = min(max(__ldg(w.q->rows + row), 0), w.q->X - 1);
-          // the chunk's place is rotated by its row, so that reads along rows
-          // and down columns both spread over the banks
-          cp_async16(base + r * 256 + (((t & 15) ^ (r & 15)) * 16),
-                     w.q->x + static_cast<int64_t>(row) * w.q->cols + (real ? c : 0), real);
-        }
-      }
+    for (int j = 0; j < 8; ++j) {
+      const int r = (t >> 4) + 16 * j;
+      const bool real = r < w.live && c < q.cols;
+      int row = w.src + (r < w.live ? r : 0);
+      if constexpr (J == kJobX)
+        if (q.rows) row = min(max(__ldg(q.rows + row), 0), q.X - 1);
+      // the chunk's place is rotated by its row, so that reads along rows
+      // and down columns both spread over the banks
+      cp_async16(base + r * 256 + (((t & 15) ^ (r & 15)) * 16), q.x + static_cast<int64_t>(row) * q.cols + (real ? c : 0),
+                 real);
     }
+  };
+  auto fetch = [&](int u) {
+    Where w{};
+    if (u < total)
+      with_job(u, [&](auto job) {
+        w = where(job, u);
+        load(job, w);
+      });
     asm volatile("cp.async.commit_group;" ::: "memory");
+    return w;
   };
 
-  load(blockIdx.x, 0);
-  int st = 0;
-  for (int u = blockIdx.x; u < total; u += gridDim.x, st ^= 1) {
-    load(u + gridDim.x, st ^ 1);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();
-    const Where w = where(u);
-    const SegQuant& q = *w.q;
+  int u = blockIdx.x;
+  Where w = fetch(u), next{};
+  auto quantize = [&](auto job) {
+    constexpr int J = decltype(job)::value;
+    const SegQuant& q = jobs.job[J];
     if (w.live > 0) {
-      const uint8_t* tile = qsmem + st * QTILE;
-      if (q.row_codes) {
+      const uint8_t* tile = qsmem;
+      if constexpr (J == kJobDy) {
         // along the rows: four lanes cover a row's 128 columns, so that the
         // codes leave as whole 128-byte lines
         const int blk = t & 3;
@@ -790,9 +879,10 @@ __global__ void __launch_bounds__(256) expert_quant(const __grid_constant__ SegJ
       sstg[(c1 & 31) * 16 + (c1 >> 5) * 4 + blk] = static_cast<uint8_t>(s1.stored);
     }
     __syncthreads();  // the tile has been read, the codes are staged
+    next = fetch(u + static_cast<int>(gridDim.x));
     if (w.live > 0) {
-      const int group = q.table ? 0 : w.tile / q.per_tiles, at = q.table ? w.tile : w.tile - group * q.per_tiles;
-      uint8_t* out = q.codes + group * q.group_codes + static_cast<int64_t>(w.c0) * q.pitch + at * 128;
+      const int group = J == kJobW ? w.tile / q.per_tiles : 0, place = w.tile - group * q.per_tiles;
+      uint8_t* out = q.codes + group * q.group_codes + static_cast<int64_t>(w.c0) * q.pitch + place * 128;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = (t >> 3) + 32 * j;
@@ -802,11 +892,18 @@ __global__ void __launch_bounds__(256) expert_quant(const __grid_constant__ SegJ
       }
       if (t < 32)  // columns past the array were zeros: their scale is the neutral one
         *reinterpret_cast<uint4*>(q.atoms + group * q.group_atoms +
-                                  (static_cast<int64_t>(w.c0 / 128) * q.ks4 + at) * 512 + t * 16) =
+                                  (static_cast<int64_t>(w.c0 / 128) * q.ks4 + place) * 512 + t * 16) =
             *reinterpret_cast<const uint4*>(sstg + t * 16);
     }
-    // the next tile's staging writes come after the next __syncthreads of the
-    // loop (behind the wait for its copies), which orders them after these reads
+  };
+
+  for (; u < total; u += gridDim.x) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // (also between the last tile's reads of the staged codes and the writes
+    // over them)
+    __syncthreads();
+    with_job(u, quantize);
+    w = next;
   }
 }
 
@@ -824,12 +921,13 @@ uint32_t expert_idesc(int a_type, int b_type) {
 
 template <bool GRAD, bool GATHER>
 cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tsa, const CUtensorMap& tb, const CUtensorMap& tb16,
-                         ExpertParams p, int64_t most_tiles, const DeviceCtx* ctx, const char* name, cudaStream_t s) {
+                         ExpertParams p, int64_t most_tiles, bool overlap, const DeviceCtx* ctx, const char* name,
+                         cudaStream_t s) {
   auto kern = expert_gemm<GRAD, GATHER>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -837,6 +935,8 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tsa, const CU
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (ctx->device < 0 || ctx->device >= 64) return cudaErrorInvalidDevice;
@@ -848,6 +948,7 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tsa, const CU
     if (most <= 0) return cudaErrorInvalidConfiguration;
     g_clusters[ctx->device].store(most, std::memory_order_relaxed);
   }
+  if (overlap) cfg.numAttrs = 2;
   p.status = ctx->status;
   p.timeout_ns = wait_timeout_ns();
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(most_tiles, most))));
@@ -857,9 +958,11 @@ cudaError_t launch_tiles(const CUtensorMap& ta, const CUtensorMap& tsa, const CU
 }
 
 // y[s] = A[e] B[row(s)]: A codes [E][F][a_pitch] with atoms [E][a_rt][ks4].
+// overlap: the kernel launched just before is this library's, and lets its
+// successor start early.
 cudaError_t launch_segments(int E, int F, int C, int64_t a_pitch, const void* a, const void* a_atoms, const void* b,
                             const uint8_t* b_scales, int S, int X, const int* offsets, const int* rows, void* y,
-                            uint32_t idesc, const char* name, cudaStream_t s) {
+                            uint32_t idesc, bool overlap, const char* name, cudaStream_t s) {
   const DeviceCtx* ctx = device_ctx();
   if (!ctx) return cudaErrorInitializationError;
   ExpertParams p{};
@@ -890,12 +993,12 @@ cudaError_t launch_segments(int E, int F, int C, int64_t a_pitch, const void* a,
     return cudaErrorInvalidValue;
   // a segment's last tile may be partial: at most one more per expert
   const int64_t most = (S / PJ + std::min(E, S)) * static_cast<int64_t>(p.f_tiles);
-  return rows ? launch_tiles<false, true>(ta, tsa, tb, tb16, p, most, ctx, name, s)
-              : launch_tiles<false, false>(ta, tsa, tb, tb16, p, most, ctx, name, s);
+  return rows ? launch_tiles<false, true>(ta, tsa, tb, tb16, p, most, overlap, ctx, name, s)
+              : launch_tiles<false, false>(ta, tsa, tb, tb16, p, most, overlap, ctx, name, s);
 }
 
 struct BackwardParts {
-  size_t dyn, dyn_s, wt, wt_s, dyt, dyt_s, xt, xt_s, pads, table, total;
+  size_t dyn, dyn_s, wt, wt_s, dyt, dyt_s, xt, xt_s, total;
   int64_t Np, Sp;
 };
 BackwardParts backward_parts(int64_t S, int64_t E, int64_t N, int64_t K) {
@@ -918,8 +1021,6 @@ BackwardParts backward_parts(int64_t S, int64_t E, int64_t N, int64_t K) {
   b.dyt_s = take(n_rt * (b.Sp / 128) * 512);
   b.xt = take(static_cast<size_t>(K) * b.Sp);
   b.xt_s = take(k_rt * (b.Sp / 128) * 512);
-  b.pads = take((E + 1) * 4);
-  b.table = take(b.Sp / 128 * 8);
   b.total = at;
   return b;
 }
@@ -940,7 +1041,8 @@ cudaError_t launch_expert_gemm(const ExpertGemmRequest& r, cudaStream_t s) {
   const uint8_t* scales = r.x_scales;
   const int* rows = r.rows;
   int64_t X = r.X;
-  if (rows && expert_gathers_ahead(r.S, r.E)) {
+  const bool ahead = rows && expert_gathers_ahead(r.S, r.E);
+  if (ahead) {
     const DeviceCtx* ctx = device_ctx();
     if (!ctx) return cudaErrorInitializationError;
     uint8_t* codes = static_cast<uint8_t*>(r.workspace);
@@ -960,7 +1062,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmRequest& r, cudaStream_t s) {
   }
   return launch_segments(static_cast<int>(r.E), static_cast<int>(r.N), static_cast<int>(r.K), r.K, r.w, r.w_atoms, x,
                          scales, static_cast<int>(r.S), static_cast<int>(X), r.offsets, rows, r.y,
-                         expert_idesc(r.w_type, r.x_type), rows ? "expert_gemm (gathered)" : "expert_gemm", s);
+                         expert_idesc(r.w_type, r.x_type), ahead, rows ? "expert_gemm (gathered)" : "expert_gemm", s);
 }
 
 size_t expert_backward_bytes(int64_t S, int64_t E, int64_t N, int64_t K) { return backward_parts(S, E, N, K).total; }
@@ -970,19 +1072,13 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
   if (!ctx) return cudaErrorInitializationError;
   const BackwardParts b = backward_parts(r.S, r.E, r.N, r.K);
   uint8_t* ws = static_cast<uint8_t*>(r.workspace);
-  int* pads = reinterpret_cast<int*>(ws + b.pads);
-  int2* table = reinterpret_cast<int2*>(ws + b.table);
   const int row_tiles = static_cast<int>(b.Sp / 128);
-  {
-    TraceScope tr("expert_plan", s);
-    expert_plan<<<1, 1024, 0, s>>>(r.offsets, static_cast<int>(r.E), static_cast<int>(r.S), row_tiles, pads, table);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-
   const int n_tiles = static_cast<int>(ceil_div(r.N, 128)), k_tiles = static_cast<int>(ceil_div(r.K, 128));
   SegJobs jobs{};
-  SegQuant& w = jobs.job[0];
+  jobs.offsets = r.offsets;
+  jobs.E = static_cast<int>(r.E);
+  jobs.S = static_cast<int>(r.S);
+  SegQuant& w = jobs.job[kJobW];
   w.x = static_cast<const __nv_bfloat16*>(r.W);
   w.cols = static_cast<int>(r.K);
   w.col_tiles = k_tiles;
@@ -995,12 +1091,11 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
   w.atoms = ws + b.wt_s;
   w.ks4 = n_tiles;
   w.group_atoms = 2 * ceil_div(r.K, 256) * n_tiles * 512;
-  SegQuant& d = jobs.job[1];
+  SegQuant& d = jobs.job[kJobDy];
   d.x = static_cast<const __nv_bfloat16*>(r.dY);
   d.cols = static_cast<int>(r.N);
   d.col_tiles = n_tiles;
   d.X = static_cast<int>(r.S);
-  d.table = table;
   d.tiles = row_tiles;
   d.codes = ws + b.dyt;
   d.pitch = b.Sp;
@@ -1008,7 +1103,7 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
   d.ks4 = row_tiles;
   d.row_codes = ws + b.dyn;
   d.row_scales = ws + b.dyn_s;
-  SegQuant& x = jobs.job[2];
+  SegQuant& x = jobs.job[kJobX];
   x = d;
   x.x = static_cast<const __nv_bfloat16*>(r.X);
   x.cols = static_cast<int>(r.K);
@@ -1017,14 +1112,13 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
   x.X = static_cast<int>(r.X_rows);
   x.codes = ws + b.xt;
   x.atoms = ws + b.xt_s;
-  x.row_codes = x.row_scales = nullptr;
   for (int i = 0; i < 3; ++i) jobs.first[i + 1] = jobs.first[i] + jobs.job[i].tiles * jobs.job[i].col_tiles;
   auto quant = r.fp8 == BSMM_E4M3 ? expert_quant<BSMM_E4M3> : expert_quant<BSMM_E5M2>;
-  e = cudaFuncSetAttribute(quant, cudaFuncAttributeMaxDynamicSharedMemorySize, QSMEM);
+  cudaError_t e = cudaFuncSetAttribute(quant, cudaFuncAttributeMaxDynamicSharedMemorySize, QSMEM);
   if (e != cudaSuccess) return e;
   {
     TraceScope tr("expert_quant", s);
-    quant<<<std::min(jobs.first[3], 2 * ctx->num_sms), 256, QSMEM, s>>>(jobs);
+    quant<<<std::min(jobs.first[3], QBLOCKS * ctx->num_sms), 256, QSMEM, s>>>(jobs);
   }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1032,7 +1126,7 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
   const uint32_t idesc = expert_idesc(r.fp8, r.fp8);
   e = launch_segments(static_cast<int>(r.E), static_cast<int>(r.K), static_cast<int>(r.N), b.Np, ws + b.wt, ws + b.wt_s,
                       ws + b.dyn, ws + b.dyn_s, static_cast<int>(r.S), static_cast<int>(r.S), r.offsets, nullptr, r.dX,
-                      idesc, "expert_gemm (dX)", s);
+                      idesc, true, "expert_gemm (dX)", s);
   if (e != cudaSuccess) return e;
 
   ExpertParams p{};
@@ -1046,7 +1140,8 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
   p.b_ks4 = row_tiles;
   p.J = static_cast<int>(r.N);
   p.j_tiles = static_cast<int>(ceil_div(r.N, PJ));
-  p.pads = pads;
+  p.row_tiles = row_tiles;
+  p.late_wait = 1;
   p.y = static_cast<__nv_bfloat16*>(r.dW);
   p.idesc = idesc;
   CUtensorMap ta, tsa, tb, tb16;
@@ -1056,7 +1151,7 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
       !make_tmap_rows(&tb, ws + b.dyt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b.Sp, r.N, 1, b.Sp, KB, 128) ||
       !make_tmap_rows(&tb16, ws + b.dyt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b.Sp, r.N, 1, b.Sp, KB, 16))
     return cudaErrorInvalidValue;
-  return launch_tiles<true, false>(ta, tsa, tb, tb16, p, static_cast<int64_t>(p.E) * p.j_tiles * p.f_tiles, ctx,
+  return launch_tiles<true, false>(ta, tsa, tb, tb16, p, static_cast<int64_t>(p.E) * p.j_tiles * p.f_tiles, true, ctx,
                                    "expert_gemm (dW)", s);
 }
 
