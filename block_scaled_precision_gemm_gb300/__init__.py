@@ -238,6 +238,30 @@ def _scratch(nbytes, dev, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
+def _lists():
+    """The compiled part of the binding."""
+    global _LISTS
+    if _LISTS is None:
+        try:
+            from . import _tensor_lists
+        except ImportError as e:
+            raise RuntimeError("_tensor_lists.so is missing: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _LISTS = _tensor_lists
+    return _LISTS
+
+
+_LISTS = None
+
+
+def _empties(dev, stream, *specs):
+    """Several outputs, ``specs`` being type, shape, type, shape, ...: in one call
+    where they come from the current stream's pool (see :func:`_empty`)."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(dev.index):
+        return _lists().empties(dev.index, *specs)
+    return [_empty(shape, dtype, dev, stream) for dtype, shape in zip(specs[::2], specs[1::2])]
+
+
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -1032,22 +1056,25 @@ def route(logits, k, renormalize=True, weights=None, ids=None, offsets=None, row
         raise ValueError("logits must be a 2-D float32 or bfloat16 tensor [T, E]")
     (T, E), k = logits.shape, int(k)
     ld = _rows(logits, "logits", (T, E), _FLOATS)
-    outs = (("weights", weights, (T, k), _F32), ("ids", ids, (T, k), _I32), ("offsets", offsets, (E + 1,), _I32),
-            ("rows", rows, (T * k,), _I32), ("slots", slots, (T, k), _I32))
-    for n, t, shape, dtypes in outs:
-        if t is not None:
-            _want(t, n, shape, dtypes=dtypes)
-    if workspace is not None:
-        _want(workspace, "workspace")
     dev = logits.device
     if not _current(logits):
         raise ValueError(f"logits is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    _same_device(dev, **{n: t for n, t, _, _ in outs}, workspace=workspace)
-    _on_device(**{n: t for n, t, _, _ in outs}, workspace=workspace)
     if k < 0:
         raise ValueError("k must not be negative")
-    weights, ids, offsets, rows, slots = (_empty(shape, dtypes[0], dev, stream) if t is None else t
-                                          for _, t, shape, dtypes in outs)
+    shapes = (torch.float32, (T, k), torch.int32, (T, k), torch.int32, (E + 1,), torch.int32, (T * k,), torch.int32, (T, k))
+    if weights is ids is offsets is rows is slots is workspace is None:
+        weights, ids, offsets, rows, slots = _empties(dev, stream, *shapes)
+    else:
+        outs = {"weights": weights, "ids": ids, "offsets": offsets, "rows": rows, "slots": slots}
+        for (n, t), dtype, shape in zip(outs.items(), shapes[::2], shapes[1::2]):
+            if t is not None:
+                _want(t, n, shape, dtypes=(dtype,))
+        if workspace is not None:
+            _want(workspace, "workspace")
+        _same_device(dev, **outs, workspace=workspace)
+        _on_device(**outs, workspace=workspace)
+        weights, ids, offsets, rows, slots = (_empty(shape, dtype, dev, stream) if t is None else t
+                                              for t, dtype, shape in zip(outs.values(), shapes[::2], shapes[1::2]))
     if workspace is None:
         need = route_workspace_size(T, E)
         if need:
@@ -1159,6 +1186,8 @@ def expert_backward(dY, W, X, offsets, rows=None, fp8="e5m2", dX=None, dW=None, 
     if workspace is not None:
         _want(workspace, "workspace")
     dev = _on_device(dY=dY, W=W, X=X, offsets=offsets, rows=rows, dX=dX, dW=dW, workspace=workspace)
+    if dX is None and dW is None:
+        dX, dW = _empties(dev, stream, torch.bfloat16, (S, K), torch.bfloat16, (E, N, K))
     if dX is None:
         dX = _empty((S, K), torch.bfloat16, dev, stream)
     if dW is None:
@@ -1226,22 +1255,6 @@ def expert_combine_backward(d_out, y, slots, weights=None, dy=None, d_weights=No
 # --------------------------------------------------------------------------- #
 # AdamW                                                                       #
 # --------------------------------------------------------------------------- #
-
-def _lists():
-    """The compiled part of the binding."""
-    global _LISTS
-    if _LISTS is None:
-        try:
-            from . import _tensor_lists
-        except ImportError as e:
-            raise RuntimeError("_tensor_lists.so is missing: build it first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
-        _LISTS = _tensor_lists
-    return _LISTS
-
-
-_LISTS = None
-
 
 def _tensor_list(ts, name, sizes, per=1, dtypes=None, itemsize=None):
     """A list of contiguous CUDA tensors of one type, on the current device:

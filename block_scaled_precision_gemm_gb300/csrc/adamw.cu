@@ -27,6 +27,7 @@ constexpr int kTensors = 96;
 template <bool BITS8>
 constexpr int kChunk = BITS8 ? 2048 : 4096;
 constexpr int kThreads = 256;
+constexpr int kBlocks8 = 3;  // blocks an SM, states in 8 bits
 
 struct AdamTensor {
   void* p;
@@ -47,6 +48,7 @@ struct AdamParams {
   float decay, rate, root2, scale;  // 1 - lr wd, lr / bias1, 1 / sqrt(bias2), of the gradient
   const float* hyper;              // device: lr, step, grad_scale instead
   double beta1, beta2, weight_decay;
+  float minus_zero;
 };
 
 struct Factors {
@@ -61,6 +63,27 @@ __device__ __forceinline__ float move(float& p, float g, float& m, float& v, con
   const float root = __fsqrt_rn(v);
   const float den = __fadd_rn(__fmul_rn(root, f.root2), a.eps);
   p = __fsub_rn(__fmul_rn(p, f.decay), __fmul_rn(f.rate, __fdiv_rn(m, den)));
+  return root;
+}
+
+// The same for two numbers, products and sums on the packed binary32 pipe.  The
+// compiler joins a packed product and a sum to one rounding, with .rn in PTX
+// too; so a product is a fused multiply-add of a -0 that it does not know.
+struct Packed {
+  float2 zero;  // -0
+  __device__ __forceinline__ float2 mul(float2 a, float2 b) const { return __ffma2_rn(a, b, zero); }
+  __device__ __forceinline__ float2 add(float2 a, float2 b) const { return __fadd2_rn(a, b); }
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 move2(const Packed& k, float2& p, float2 g, float2& m, float2& v, const AdamParams& a,
+                                        const Factors& f) {
+  g = k.mul(g, both(f.scale));
+  m = k.add(k.mul(both(a.b1), m), k.mul(both(a.c1), g));
+  v = k.add(k.mul(both(a.b2), v), k.mul(k.mul(both(a.c2), g), g));
+  const float2 root = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+  const float2 den = k.add(k.mul(root, both(f.root2)), both(a.eps));
+  const float2 q = make_float2(__fdiv_rn(m.x, den.x), __fdiv_rn(m.y, den.y));
+  p = k.add(k.mul(p, both(f.decay)), k.mul(both(-f.rate), q));
   return root;
 }
 
@@ -109,15 +132,19 @@ __device__ __forceinline__ void store1(T* p, float v) {
   else *p = __float2bfloat16_rn(v);
 }
 
-// Four E4M3 codes' values.
-__device__ __forceinline__ float4 e4m3_values(uint32_t c) {
+// Four E4M3 codes' values times a scale.
+__device__ __forceinline__ void e4m3_values(const Packed& k, uint32_t c, float s, float2& x, float2& y) {
   uint32_t lo, hi;
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
       : "=r"(lo), "=r"(hi)
       : "r"(c));
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return make_float4(x.x, x.y, y.x, y.y);
+  x = k.mul(__half22float2(*reinterpret_cast<const __half2*>(&lo)), both(s));
+  y = k.mul(__half22float2(*reinterpret_cast<const __half2*>(&hi)), both(s));
+}
+__device__ __forceinline__ float e4m3_value(const Packed& k, uint32_t c, float s) {
+  float2 x, y;
+  e4m3_values(k, c, s, x, y);
+  return x.x;
 }
 
 // The scale of a block of a state: absmax * binary32(1 / 448) (a block of
@@ -130,33 +157,58 @@ __device__ __forceinline__ Scale state_scale(float absmax) {
   return s;
 }
 
-__device__ __forceinline__ float block_max(float4 v) {
-  const float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+__device__ __forceinline__ float block_max(float2 a, float2 b) {
+  const float m = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
 
-// A root that rounds to zero takes the smallest code: a second moment of zero
-// beside a first moment that is none would divide by eps alone.
-__device__ __forceinline__ uint32_t root_codes(float4 r, const Scale& s) {
-  uint32_t c = encode4<false>(r.x, r.y, r.z, r.w, s, BSMM_E4M3);
-  if (r.x > 0.f && !(c & 0xFFu)) c |= 1u;
-  if (r.y > 0.f && !(c & 0xFF00u)) c |= 0x100u;
-  if (r.z > 0.f && !(c & 0xFF0000u)) c |= 0x10000u;
-  if (r.w > 0.f && !(c & 0xFF000000u)) c |= 0x1000000u;
-  return c;
+__device__ __forceinline__ uint32_t state_codes(float2 a, float2 b, const Scale& s) {
+  return encode4<false>(a.x, a.y, b.x, b.y, s, BSMM_E4M3);
 }
 
-// A warp's two blocks of 128 numbers, four a lane, as loaded ahead.
+// A root that rounds to zero takes the smallest code: a second moment of zero
+// beside a first moment that is none would divide by eps alone.  So a quotient
+// is at least 2^-9, the smallest code, times one for a root above zero (which is
+// 2^-75 at least, the root of the smallest number) and nothing for zero.
+__device__ __forceinline__ float at_least(float q, float low) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(q), "f"(fminf(low, 0x1p-9f)));
+  return r;
+}
+__device__ __forceinline__ uint32_t root_codes(const Packed& k, float2 a, float2 b, const Scale& s) {
+  float2 x, y;
+  if (s.inv != 0.f) {
+    x = quot2_rn_int(a, s.s, s.inv);
+    y = quot2_rn_int(b, s.s, s.inv);
+  } else {
+    x = make_float2(__fdiv_rn(a.x, s.s), __fdiv_rn(a.y, s.s));
+    y = make_float2(__fdiv_rn(b.x, s.s), __fdiv_rn(b.y, s.s));
+  }
+  a = k.mul(a, both(0x1p100f));
+  b = k.mul(b, both(0x1p100f));
+  return pack4(at_least(x.x, a.x), at_least(x.y, a.y), at_least(y.x, b.x), at_least(y.y, b.y), BSMM_E4M3);
+}
+
+// Two chunks' numbers in shared memory, as loaded ahead.  A thread copies and
+// reads its own places only: two blocks of 128 a warp, four numbers a lane.
 template <typename P, typename G>
-struct Ahead {
-  typename Four<P>::Raw p[2];
-  typename Four<G>::Raw g[2];
-  uint32_t m[2], v[2];
-  float ms[2], vs[2];
+struct Stage {
+  typename Four<P>::Raw p[2][kThreads];
+  typename Four<G>::Raw g[2][kThreads];
+  uint32_t m[2][kThreads], v[2][kThreads];
 };
+template <typename T>
+__device__ __forceinline__ void copy_async(T* dst, const void* src) {
+  constexpr int BYTES = sizeof(T);
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(src), "n"(BYTES) : "memory");
+}
 
 template <typename P, typename G, bool BITS8>
-__global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 1) adamw(const __grid_constant__ AdamParams a) {
+__global__ void __launch_bounds__(kThreads, BITS8 ? kBlocks8 : 1) adamw(const __grid_constant__ AdamParams a) {
   constexpr int CHUNK = kChunk<BITS8>;
   __shared__ Factors shared;
   Factors f{a.decay, a.rate, a.root2, a.scale};
@@ -233,41 +285,50 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 1) adamw(const __grid_co
     }
   } else {
     // A warp a block of 128: four numbers a lane.  A whole chunk's numbers are
-    // loaded while the chunk before is computed (about 650 instructions a warp).
-    using Four_p = Four<P>;
-    using Four_g = Four<G>;
-    auto fetch = [&](int ti, int64_t c, Ahead<P, G>& x) {
+    // copied to shared memory while the chunk before is computed (about 600
+    // instructions a warp): held in registers they leave room for fewer warps.
+    extern __shared__ __align__(16) uint8_t stages[];
+    Stage<P, G>* stage = reinterpret_cast<Stage<P, G>*>(stages);
+    float ms_next[2], vs_next[2];
+    auto fetch = [&](int ti, int64_t c, Stage<P, G>& x) {
       const AdamTensor& t = a.t[ti];
       const int64_t at = (c - a.first[ti]) * CHUNK;
-      if (t.n - at < CHUNK || !((a.wide[ti >> 5] >> (ti & 31)) & 1u)) return false;
+      const bool whole = t.n - at >= CHUNK && ((a.wide[ti >> 5] >> (ti & 31)) & 1u);
+      if (whole) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int b = warp + 8 * j;
-        const int64_t i = at + 128 * b + 4 * lane;
-        x.p[j] = load4_raw(static_cast<const P*>(t.p) + i);
-        x.g[j] = load4_raw(static_cast<const G*>(t.g) + i);
-        x.m[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
-        x.v[j] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
-        x.ms[j] = t.ms[at / 128 + b];
-        x.vs[j] = t.vs[at / 128 + b];
+        for (int j = 0; j < 2; ++j) {
+          const int b = warp + 8 * j;
+          const int64_t i = at + 128 * b + 4 * lane;
+          copy_async(&x.p[j][threadIdx.x], static_cast<const P*>(t.p) + i);
+          copy_async(&x.g[j][threadIdx.x], static_cast<const G*>(t.g) + i);
+          copy_async(&x.m[j][threadIdx.x], static_cast<const uint8_t*>(t.m) + i);
+          copy_async(&x.v[j][threadIdx.x], static_cast<const uint8_t*>(t.v) + i);
+          ms_next[j] = t.ms[at / 128 + b];
+          vs_next[j] = t.vs[at / 128 + b];
+        }
       }
-      return true;
+      return whole;
     };
-    Ahead<P, G> x, next;
-    int ti = 0;
+    const Packed k{both(a.minus_zero)};
+    int ti = 0, st = 0;
     bool whole = false;
     if (chunk < chunks) {
       ti = tensor_of(0, chunk);
-      whole = fetch(ti, chunk, x);
+      whole = fetch(ti, chunk, stage[0]);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     while (chunk < chunks) {
       const int64_t after = chunk + gridDim.x;
       int ti_next = ti;
       bool whole_next = false;
+      float scales[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) scales[j] = ms_next[j], scales[2 + j] = vs_next[j];
       if (after < chunks) {
         ti_next = tensor_of(ti, after);
-        whole_next = fetch(ti_next, after, next);
+        whole_next = fetch(ti_next, after, stage[st ^ 1]);
       }
+      asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;" ::: "memory");
       const AdamTensor& t = a.t[ti];
       const int64_t at = (chunk - a.first[ti]) * CHUNK;
       P* p = static_cast<P*>(t.p) + at;
@@ -280,22 +341,22 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 1) adamw(const __grid_co
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int b = warp + 8 * j, i = 128 * b + 4 * lane;
-          const float sm = x.ms[j], sv = x.vs[j];
-          float4 pp = Four_p::value(x.p[j]);
-          const float4 gg = Four_g::value(x.g[j]);
-          float4 mm = e4m3_values(x.m[j]), vv = e4m3_values(x.v[j]), r;
-          mm = make_float4(__fmul_rn(mm.x, sm), __fmul_rn(mm.y, sm), __fmul_rn(mm.z, sm), __fmul_rn(mm.w, sm));
-          vv = make_float4(__fmul_rn(vv.x, sv), __fmul_rn(vv.y, sv), __fmul_rn(vv.z, sv), __fmul_rn(vv.w, sv));
-          vv = make_float4(__fmul_rn(vv.x, vv.x), __fmul_rn(vv.y, vv.y), __fmul_rn(vv.z, vv.z), __fmul_rn(vv.w, vv.w));
-          r.x = move(pp.x, gg.x, mm.x, vv.x, a, f);
-          r.y = move(pp.y, gg.y, mm.y, vv.y, a, f);
-          r.z = move(pp.z, gg.z, mm.z, vv.z, a, f);
-          r.w = move(pp.w, gg.w, mm.w, vv.w, a, f);
-          const Scale s = state_scale(block_max(mm)), q = state_scale(block_max(r));
+          const float sm = scales[j], sv = scales[2 + j];
+          float4 pp = Four<P>::value(stage[st].p[j][threadIdx.x]);
+          const float4 gg = Four<G>::value(stage[st].g[j][threadIdx.x]);
+          float2 p0 = make_float2(pp.x, pp.y), p1 = make_float2(pp.z, pp.w), m0, m1, v0, v1;
+          e4m3_values(k, stage[st].m[j][threadIdx.x], sm, m0, m1);
+          e4m3_values(k, stage[st].v[j][threadIdx.x], sv, v0, v1);
+          v0 = k.mul(v0, v0);
+          v1 = k.mul(v1, v1);
+          const float2 r0 = move2(k, p0, make_float2(gg.x, gg.y), m0, v0, a, f);
+          const float2 r1 = move2(k, p1, make_float2(gg.z, gg.w), m1, v1, a, f);
+          pp = make_float4(p0.x, p0.y, p1.x, p1.y);
+          const Scale s = state_scale(block_max(m0, m1)), q = state_scale(block_max(r0, r1));
           store4(p + i, pp);
           if (copy) store4(copy + i, pp);
-          __stcs(reinterpret_cast<uint32_t*>(m + i), encode4<false>(mm.x, mm.y, mm.z, mm.w, s, BSMM_E4M3));
-          __stcs(reinterpret_cast<uint32_t*>(v + i), root_codes(r, q));
+          __stcs(reinterpret_cast<uint32_t*>(m + i), state_codes(m0, m1, s));
+          __stcs(reinterpret_cast<uint32_t*>(v + i), root_codes(k, r0, r1, q));
           if (lane == 0) ms[b] = s.s, vs[b] = q.s;
         }
       } else {
@@ -310,18 +371,18 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 1) adamw(const __grid_co
             mm[j] = rr[j] = 0.f;
             if (i < n) {
               float pp = load1(p + i);
-              float vv = __fmul_rn(e4m3_values(v[i]).x, sv);
+              float vv = e4m3_value(k, v[i], sv);
               vv = __fmul_rn(vv, vv);
-              mm[j] = __fmul_rn(e4m3_values(m[i]).x, sm);
+              mm[j] = e4m3_value(k, m[i], sm);
               rr[j] = move(pp, load1(g + i), mm[j], vv, a, f);
               store1(p + i, pp);
               if (copy) copy[i] = __float2bfloat16_rn(pp);
             }
           }
-          const Scale s = state_scale(block_max(make_float4(mm[0], mm[1], mm[2], mm[3])));
-          const Scale q = state_scale(block_max(make_float4(rr[0], rr[1], rr[2], rr[3])));
-          const uint32_t mc = encode4<false>(mm[0], mm[1], mm[2], mm[3], s, BSMM_E4M3);
-          const uint32_t vc = root_codes(make_float4(rr[0], rr[1], rr[2], rr[3]), q);
+          const float2 m0 = make_float2(mm[0], mm[1]), m1 = make_float2(mm[2], mm[3]);
+          const float2 r0 = make_float2(rr[0], rr[1]), r1 = make_float2(rr[2], rr[3]);
+          const Scale s = state_scale(block_max(m0, m1)), q = state_scale(block_max(r0, r1));
+          const uint32_t mc = state_codes(m0, m1, s), vc = root_codes(k, r0, r1, q);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int i = 128 * b + lane + 32 * j;
@@ -330,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 1) adamw(const __grid_co
           if (lane == 0) ms[b] = s.s, vs[b] = q.s;
         }
       }
-      x = next;
+      st ^= 1;
       chunk = after;
       ti = ti_next;
       whole = whole_next;
@@ -358,6 +419,7 @@ cudaError_t launch_adamw(const AdamwRequest& r, cudaStream_t s) {
   a.beta1 = r.beta1;
   a.beta2 = r.beta2;
   a.weight_decay = r.weight_decay;
+  a.minus_zero = -0.f;
   using Kernel = void (*)(AdamParams);
   const Kernel kernels[8] = {
       adamw<float, float, false>,          adamw<float, float, true>,
@@ -365,6 +427,11 @@ cudaError_t launch_adamw(const AdamwRequest& r, cudaStream_t s) {
       adamw<__nv_bfloat16, float, false>,  adamw<__nv_bfloat16, float, true>,
       adamw<__nv_bfloat16, __nv_bfloat16, false>, adamw<__nv_bfloat16, __nv_bfloat16, true>};
   const Kernel kern = kernels[(r.p_bf16 ? 4 : 0) + (r.g_bf16 ? 2 : 0) + (r.bits8 ? 1 : 0)];
+  const int smem = r.bits8 ? 2 * 2 * kThreads * ((r.p_bf16 ? 8 : 16) + (r.g_bf16 ? 8 : 16) + 8) : 0;  // two Stages
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   for (int64_t i = 0; i < r.count;) {
     a.count = 0;
     for (unsigned& w : a.wide) w = 0;
@@ -383,9 +450,9 @@ cudaError_t launch_adamw(const AdamwRequest& r, cudaStream_t s) {
       ++a.count;
     }
     if (a.count == 0) break;
-    const int64_t grid = std::min<int64_t>(a.first[a.count], (r.bits8 ? 3 : 8) * ctx->num_sms);
+    const int64_t grid = std::min<int64_t>(a.first[a.count], (r.bits8 ? kBlocks8 : 8) * ctx->num_sms);
     TraceScope tr(r.bits8 ? "adamw (8 bits)" : "adamw", s);
-    kern<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
+    kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

@@ -1,15 +1,23 @@
-// Addresses and sizes of a list of tensors in one call from Python.
+// What the binding asks of many tensors, in one call from Python: the addresses
+// and sizes of a list, and new tensors.
 //
 // An optimizer's step over hundreds of small tensors is over on the GPU before
 // an interpreter has asked each of them for its address, its size, its type,
 // its device and its layout (400 tensors: about 140 us); here that is a few
 // nanoseconds a tensor.  What does not pass is left to the caller to explain.
 #define PY_SSIZE_T_CLEAN
+#include <ATen/Functions.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/DynamicTypes.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
+#include <torch/csrc/utils/pybind.h>
 
 #include <cstdint>
 #include <cstring>
+#include <utility>
+#include <vector>
 
 namespace {
 
@@ -71,9 +79,39 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   Py_RETURN_NONE;
 }
 
+// empties(device, dtype, shape, dtype, shape, ...) -> a list of new tensors.
+PyObject* empties(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_TYPE(nargs % 2 == 1, "empties(device, dtype, shape, ...)");
+  const long device = PyLong_AsLong(args[0]);
+  if (PyErr_Occurred()) return nullptr;
+  THPObjectPtr out(PyList_New(nargs / 2));
+  if (!out) return nullptr;
+  for (Py_ssize_t i = 1; i < nargs; i += 2) {
+    TORCH_CHECK_TYPE(THPDtype_Check(args[i]) && PyTuple_Check(args[i + 1]), "empties(device, dtype, shape, ...)");
+    std::vector<int64_t> shape(static_cast<size_t>(PyTuple_GET_SIZE(args[i + 1])));
+    for (size_t d = 0; d < shape.size(); ++d)
+      shape[d] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[i + 1], static_cast<Py_ssize_t>(d)));
+    if (PyErr_Occurred()) return nullptr;
+    const auto options = at::TensorOptions()
+                             .dtype(reinterpret_cast<THPDtype*>(args[i])->scalar_type)
+                             .device(c10::kCUDA, static_cast<c10::DeviceIndex>(device));
+    at::Tensor t;
+    {
+      pybind11::gil_scoped_release unlocked;
+      t = at::empty(shape, options);
+    }
+    PyList_SET_ITEM(out.get(), i / 2, THPVariable_Wrap(std::move(t)));
+  }
+  return out.release();
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"addresses", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(addresses)), METH_FASTCALL,
      "Addresses, sizes and type of a list of contiguous CUDA tensors, or None."},
+    {"empties", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empties)), METH_FASTCALL,
+     "New CUDA tensors of given types and shapes."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
