@@ -938,7 +938,7 @@ bsmm_status combine_sizes(int64_t T, int64_t S, int k, int64_t N, bsmm_dtype typ
   if (type != BSMM_F32 && type != BSMM_BF16) return fail(BSMM_ERR_INVALID_ARG, "the token's rows must be F32 or BF16");
   if (k < 1 || N < 1) return fail(BSMM_ERR_SHAPE, "k and N must be at least 1");
   if (k > 32) return fail(BSMM_ERR_UNSUPPORTED, "up to 32 experts a token");
-  if (T > INT32_MAX / k || S > INT32_MAX || N > (1 << 24)) return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
+  if (T > INT32_MAX / k || S > INT32_MAX || N > (1 << 23)) return fail(BSMM_ERR_SHAPE, "size beyond the supported range");
   return BSMM_OK;
 }
 }  // namespace

@@ -696,7 +696,7 @@ bsmm_status bsmm_expert_backward(int64_t S, int64_t X_rows, int64_t E, int64_t N
 /* out[t] = sum over j of weights[t, j] y[slots[t, j]], in binary32, rounded once.
  *   y [S, N] bfloat16; slots [T, k]; a slot outside [0, S) has no part.
  *   weights binary32 [T, k], or NULL for 1.  out [T, N] F32 or BF16.
- *   k up to 32; any N >= 1; pointers aligned to their elements. */
+ *   k up to 32; N up to 2^23; pointers aligned to their elements. */
 bsmm_status bsmm_expert_combine(int64_t T, int64_t S, int k, int64_t N, const void* y, const int32_t* slots,
                                 const float* weights, void* out, bsmm_dtype out_type, bsmm_stream_t stream);
 

@@ -153,6 +153,61 @@ def test_more_tensors_than_a_launch_takes():
         assert same(d["params"][i], want[i][0]) and same(d["m"][i], want[i][1])
 
 
+@pytest.mark.parametrize("bits8", [False, True])
+def test_blocks_that_take_several_chunks(bits8):
+    """Large, small and ragged tensors in turn under the same blocks."""
+    sizes = [1500000, 5, 700001, 2048, 1000003, 4096, 300]
+    d = tensors(sizes, torch.float32, torch.bfloat16, bits8)
+    want = [expected(d, i, bits8, 9)[1] for i in range(len(sizes))]
+    _bsmm().adamw(d["params"], d["grads"], d["m"], d["v"], 9, m_scales=d.get("m_scales"), v_scales=d.get("v_scales"), **ARGS)
+    for i in range(len(sizes)):
+        wp, wm, wv = want[i]
+        assert same(d["params"][i], wp), sizes[i]
+        if bits8:
+            for name, x, root in (("m", wm, False), ("v", np.sqrt(wv), True)):
+                s = O.scales(x)[:(sizes[i] + 127) // 128]
+                assert same(d[name + "_scales"][i], s) and same(d[name][i], O.codes(x, s, root)), (sizes[i], name)
+        else:
+            assert same(d["m"][i], wm) and same(d["v"][i], wv), sizes[i]
+
+
+def test_lists_that_do_not_fit():
+    bsmm = _bsmm()
+    kw = dict(step=1, lr=0.1)
+
+    def z(*sizes):
+        return [torch.zeros(n, device="cuda") for n in sizes]
+
+    p = z(6, 200)
+    with pytest.raises(ValueError, match="CUDA tensors on the current device"):
+        bsmm.adamw(p, z(6) + [torch.zeros(200)], z(6, 200), z(6, 200), **kw)
+    with pytest.raises(ValueError, match="contiguous"):
+        bsmm.adamw(p, [torch.zeros(12, device="cuda")[::2], *z(200)], z(6, 200), z(6, 200), **kw)
+    with pytest.raises(ValueError, match=r"m\[1\] holds 199"):
+        bsmm.adamw(p, z(6, 200), z(6, 199), z(6, 200), **kw)
+    with pytest.raises(ValueError, match="v holds 3 tensors"):
+        bsmm.adamw(p, z(6, 200), z(6, 200), z(6, 200, 1), **kw)
+    with pytest.raises(ValueError, match="one type"):
+        bsmm.adamw(p, [p[0], p[1].bfloat16()], z(6, 200), z(6, 200), **kw)
+    with pytest.raises(ValueError, match="1-byte"):
+        bsmm.adamw(p, z(6, 200), z(6, 200), z(6, 200), m_scales=z(1, 2), v_scales=z(1, 2), **kw)
+    with pytest.raises(TypeError, match="Tensors"):
+        bsmm.adamw(p, [p[0], 1.0], z(6, 200), z(6, 200), **kw)
+    codes = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in (6, 200)]
+    with pytest.raises(ValueError, match=r"v_scales\[1\] holds 1 numbers, 2 needed"):
+        bsmm.adamw(p, z(6, 200), codes, codes, m_scales=z(1, 2), v_scales=z(1, 1), **kw)
+    assert not any(t.any() for t in p)
+
+
+def test_parameters_and_tuples():
+    """Parameters (which require gradients) and any sequence of tensors."""
+    a = [torch.nn.Parameter(torch.ones(300, device="cuda")), torch.nn.Parameter(torch.ones(20, 10, device="cuda"))]
+    g = tuple(torch.ones_like(t) for t in a)
+    _bsmm().adamw(iter(a), g, [torch.zeros_like(t) for t in g], [torch.zeros_like(t) for t in g], 1, lr=0.5, weight_decay=0.0)
+    for t in a:
+        assert torch.equal(t.detach(), torch.full_like(t, 0.5))
+
+
 def test_schedule_on_the_device_and_in_a_graph():
     """A captured step takes lr, step and grad_scale from `hyper` at each replay."""
     bsmm = _bsmm()

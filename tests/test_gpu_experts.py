@@ -152,6 +152,44 @@ def test_nan_reaches_its_row_and_feature_only(rows):
     assert (bad[~hit] == _f64(want)[~hit]).all()
 
 
+@pytest.mark.parametrize("counts", [[10, 0, 3, 40], [100, 0, 260, 90]])
+@pytest.mark.parametrize("K", [96, 640])
+def test_rows_by_number_or_copied(counts, K):
+    """Few rows an expert are fetched by number, many are copied ahead: both give
+    the bits of rows that lie in the slots' order."""
+    d = make(counts, 288, K, 77)
+    off = offsets_of(counts)
+    at = d["rows"].long()
+    e = dict(d, x=d["x"][at], x_scales=d["x_scales"][at], rows=None)
+    assert torch.equal(run(d, off), run(e, off))
+
+
+@pytest.mark.parametrize("off", [[0, 70, 20, 90, 60], [90, 0, 90, 0, 90], [-2 ** 31, 2 ** 31 - 1, -1, 50, 2]])
+def test_offsets_that_fall_stay_inside(off):
+    """Offsets that are none: unspecified sums, in their own arrays."""
+    bsmm = _bsmm()
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    d = make([30, 20, 20, 20], 96, 128, 40)
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        flat = torch.full((n + 8192,), 77, device="cuda").to(dtype)
+        return flat, flat[4096:4096 + n].view(shape)
+
+    fy, y = guarded((90, 96), torch.bfloat16)
+    run(d, o, y=y)
+    dY, W, X, r = backward_inputs([30, 20, 20, 20], 96, 128, 40)
+    fx, dX = guarded((90, 128), torch.bfloat16)
+    fw, dW = guarded((4, 96, 128), torch.bfloat16)
+    need = bsmm.expert_backward_workspace_size(90, 4, 96, 128)
+    fs, ws = guarded((need,), torch.uint8)
+    bsmm.expert_backward(dY, W, X, o, rows=r, dX=dX, dW=dW, workspace=ws)
+    torch.cuda.synchronize()
+    for f in (fy, fx, fw, fs):
+        assert bool((f[:4096] == f[0]).all()) and bool((f[-4096:] == f[0]).all())
+    assert bsmm.check_device_status()[0] == 0
+
+
 def test_gemm_past_32_bits():
     """An output of more than 2^32 bytes: its last rows."""
     bsmm = _bsmm()
@@ -211,6 +249,25 @@ def test_backward_slots_of_no_expert():
                                 X.float().cpu().numpy(), off.cpu().numpy(), r.cpu().numpy(), "e5m2")
     check(dX, rX, mX, 96, left=1.5)
     check(dW, rW, mW, 33)
+
+
+def test_backward_one_after_another():
+    """Calls that share a workspace, each overlapping the end of the one before."""
+    bsmm = _bsmm()
+    sets = [backward_inputs(c, 160, 288, 50, seed=i) + (offsets_of(c),)
+            for i, c in enumerate(([130, 0, 70, 33], [3, 200, 1, 29], [0, 0, 233, 0]))]
+    alone = []
+    for dY, W, X, r, off in sets:
+        alone.append([t.clone() for t in bsmm.expert_backward(dY, W, X, off, rows=r)])
+        torch.cuda.synchronize()
+    ws = torch.empty(bsmm.expert_backward_workspace_size(233, 4, 160, 288), dtype=torch.uint8, device="cuda")
+    got = []
+    for i in range(30):
+        dY, W, X, r, off = sets[i % 3]
+        dX, dW = bsmm.expert_backward(dY, W, X, off, rows=r, workspace=ws)
+        got.append((dX + 0, dW + 0))  # read by the next kernel of the stream
+    for i, (dX, dW) in enumerate(got):
+        assert torch.equal(dX, alone[i % 3][0]) and torch.equal(dW, alone[i % 3][1]), i
 
 
 def test_backward_without_slots():

@@ -67,6 +67,13 @@ def test_route(T, E, k, dtype, renormalize):
     check_route(logits_of(T, E, dtype), k, renormalize)
 
 
+@pytest.mark.parametrize("T,E,k", [(20011, 64, 4), (9000, 300, 10), (30007, 6, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens(T, E, k, dtype):
+    """Several tokens a warp, the last blocks and runs partial."""
+    check_route(logits_of(T, E, dtype, ties=dtype is torch.bfloat16), k, False)
+
+
 @pytest.mark.parametrize("T", [9, 777])
 @pytest.mark.parametrize("E,k", [(8, 3), (40, 8), (256, 16)])
 def test_ties_go_to_the_lowest_index(T, E, k):
@@ -179,6 +186,10 @@ def pairs(T, S, k, seed=0, dropped=True):
 
 COMBINES = [(1, 1, 8), (1, 4, 4096), (16, 4, 513), (33, 2, 1024), (5, 8, 2056), (300, 3, 96), (7, 32, 264), (64, 1, 1),
             (2, 17, 40)]
+
+
+# many tokens (smaller blocks), and rows of more columns than a block takes
+COMBINES += [(700, 4, 4104), (640, 2, 513), (1300, 1, 72), (2, 3, 9000), (650, 9, 40)]
 
 
 @pytest.mark.parametrize("T,k,N", COMBINES)
