@@ -254,6 +254,16 @@ def _lists():
 _LISTS = None
 
 
+def _match(pattern, *tensors):
+    """The tensors' addresses and sizes, where they fit the pattern
+    (tensor_lists.cpp) on the current device; else None, and the caller's own
+    checks say what is wrong.  A tenth of the time of those."""
+    first = tensors[0]
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        return None
+    return _lists().match(pattern, torch._C._cuda_getDevice(), *tensors)
+
+
 def _empties(dev, stream, *specs):
     """Several outputs, ``specs`` being type, shape, type, shape, ...: in one call
     where they come from the current stream's pool (see :func:`_empty`)."""
@@ -1055,8 +1065,8 @@ def route(logits, k, renormalize=True, weights=None, ids=None, offsets=None, row
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D float32 or bfloat16 tensor [T, E]")
     (T, E), k = logits.shape, int(k)
-    ld = _rows(logits, "logits", (T, E), _FLOATS)
     dev = logits.device
+    ld = E if _match("F:TE", logits) else _rows(logits, "logits", (T, E), _FLOATS)
     if not _current(logits):
         raise ValueError(f"logits is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
     if k < 0:
@@ -1091,6 +1101,11 @@ def route_backward(d_weights, logits, ids, weights, renormalize=True, d_logits=N
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D float32 or bfloat16 tensor [T, E]")
     T, E = logits.shape
+    fit = _match("F:TE i:Tk f:Tk f:Tk", logits, ids, weights, d_weights) if d_logits is None else None
+    if fit:
+        k, dev = fit[6], logits.device
+        d_logits = _empty((T, E), logits.dtype, dev, stream)
+        return _route_backward(T, E, k, logits, E, renormalize, fit[3], fit[1], fit[2], d_logits, dev, stream)
     ld = _rows(logits, "logits", (T, E), _FLOATS)
     _want(ids, "ids", dtypes=_I32)
     if ids.dim() != 2 or ids.shape[0] != T:
@@ -1104,9 +1119,14 @@ def route_backward(d_weights, logits, ids, weights, renormalize=True, d_logits=N
     _same_device(dev, logits=logits)
     if d_logits is None:
         d_logits = _empty((T, E), logits.dtype, dev, stream)
+    return _route_backward(T, E, k, logits, ld, renormalize, d_weights.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                           d_logits, dev, stream)
+
+
+def _route_backward(T, E, k, logits, ld, renormalize, d_weights, ids, weights, d_logits, dev, stream):
     _check(lib().bsmm_route_backward(T, E, k, logits.data_ptr(), BF16 if logits.dtype is torch.bfloat16 else F32, ld,
-                                     1 if renormalize else 0, d_weights.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                                     d_logits.data_ptr(), _raw_stream(stream, dev)), "bsmm_route_backward")
+                                     1 if renormalize else 0, d_weights, ids, weights, d_logits.data_ptr(),
+                                     _raw_stream(stream, dev)), "bsmm_route_backward")
     return d_logits
 
 
@@ -1124,22 +1144,33 @@ def expert_gemm(x, x_scales, w, w_atoms, offsets, rows=None, x_type="e4m3", w_ty
     E batches; ``offsets`` [E + 1] and ``rows`` [S] int32 (None: slot s is row
     s of x).  Slots of no expert are left as they are in ``y``."""
     xt, wt = _code(x_type), _code(w_type)
-    _want(x, "x", itemsize=1)
-    _want(w, "w", itemsize=1)
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError("x and w must be code tensors [X, K] and [E, N, K]")
-    (X, K), (E, N) = x.shape, w.shape[:2]
-    _want(w, "w", (E, N, K))
-    _want(x_scales, "x_scales", itemsize=1)
-    if K % 32 == 0:  # else the library says why
-        _want(x_scales, "x_scales", (X, K // 32))
-        _want(w_atoms, "w_atoms", min_bytes=scale_atoms_size(E, N, K, wt, SCALE_UE8M0))
-    S = _expert_slots(offsets, rows, E, X)
+    fit = _match("c:XK c:XB c:ENK .:# i:O i?:S", x, x_scales, w, w_atoms, offsets, rows)
+    if fit:
+        X, K, B, E, N, atoms, slots = fit[6:13]
+        S = X if rows is None else fit[13]
+        if K != 32 * B or slots != E + 1 or atoms < scale_atoms_size(E, N, K, wt, SCALE_UE8M0):
+            fit = None
+    if not fit:
+        _want(x, "x", itemsize=1)
+        _want(w, "w", itemsize=1)
+        if x.dim() != 2 or w.dim() != 3:
+            raise ValueError("x and w must be code tensors [X, K] and [E, N, K]")
+        (X, K), (E, N) = x.shape, w.shape[:2]
+        _want(w, "w", (E, N, K))
+        _want(x_scales, "x_scales", itemsize=1)
+        if K % 32 == 0:  # else the library says why
+            _want(x_scales, "x_scales", (X, K // 32))
+            _want(w_atoms, "w_atoms", min_bytes=scale_atoms_size(E, N, K, wt, SCALE_UE8M0))
+        S = _expert_slots(offsets, rows, E, X)
     if y is not None:
         _want(y, "y", (S, N), dtypes=_BF16)
     if workspace is not None:
         _want(workspace, "workspace")
-    dev = _on_device(x=x, x_scales=x_scales, w=w, w_atoms=w_atoms, offsets=offsets, rows=rows, y=y, workspace=workspace)
+    if fit and y is None and workspace is None:
+        dev = x.device
+    else:
+        dev = _on_device(x=x, x_scales=x_scales, w=w, w_atoms=w_atoms, offsets=offsets, rows=rows, y=y,
+                         workspace=workspace)
     if y is None:
         y = _empty((S, N), torch.bfloat16, dev, stream)
     if workspace is None and rows is not None:
@@ -1171,21 +1202,30 @@ def expert_backward(dY, W, X, offsets, rows=None, fp8="e5m2", dX=None, dW=None, 
     [E, N, K] and ``X`` [rows of x, K]: returns ``(dX, dW)``, ``dX`` [S, K] by
     slot (:func:`expert_combine` without weights sums it by token) and ``dW``
     [E, N, K], bfloat16."""
-    for t, n, dims in ((dY, "dY", 2), (W, "W", 3), (X, "X", 2)):
-        _want(t, n, dtypes=_BF16)
-        if t.dim() != dims:
-            raise ValueError("dY, W and X must be bfloat16 tensors [S, N], [E, N, K] and [rows, K]")
-    E, N, K = W.shape
-    _want(X, "X", (X.shape[0], K))
-    S = _expert_slots(offsets, rows, E, X.shape[0])
-    _want(dY, "dY", (S, N))
+    fit = _match("b:SN b:ENK b:RK i:O i?:S", dY, W, X, offsets, rows)
+    if fit:
+        S, N, E, K, R, slots = fit[5:11]
+        if slots != E + 1 or (rows is None and R != S):
+            fit = None
+    if not fit:
+        for t, n, dims in ((dY, "dY", 2), (W, "W", 3), (X, "X", 2)):
+            _want(t, n, dtypes=_BF16)
+            if t.dim() != dims:
+                raise ValueError("dY, W and X must be bfloat16 tensors [S, N], [E, N, K] and [rows, K]")
+        E, N, K = W.shape
+        _want(X, "X", (X.shape[0], K))
+        S = _expert_slots(offsets, rows, E, X.shape[0])
+        _want(dY, "dY", (S, N))
     if dX is not None:
         _want(dX, "dX", (S, K), dtypes=_BF16)
     if dW is not None:
         _want(dW, "dW", (E, N, K), dtypes=_BF16)
     if workspace is not None:
         _want(workspace, "workspace")
-    dev = _on_device(dY=dY, W=W, X=X, offsets=offsets, rows=rows, dX=dX, dW=dW, workspace=workspace)
+    if fit and dX is dW is workspace is None:
+        dev = dY.device
+    else:
+        dev = _on_device(dY=dY, W=W, X=X, offsets=offsets, rows=rows, dX=dX, dW=dW, workspace=workspace)
     if dX is None and dW is None:
         dX, dW = _empties(dev, stream, torch.bfloat16, (S, K), torch.bfloat16, (E, N, K))
     if dX is None:
@@ -1215,13 +1255,14 @@ def _combined(y, slots, weights):
 def expert_combine(y, slots, weights=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """``out[t] = sum over j of weights[t, j] * y[slots[t, j]]`` (weights None:
     1; a slot outside y has no part): ``out`` [T, N] float32 or bfloat16."""
-    S, N, T, k = _combined(y, slots, weights)
+    fit = _match("b:SN i:Tk f?:Tk", y, slots, weights)
+    S, N, T, k = fit[3:] if fit else _combined(y, slots, weights)
     dtype = out_dtype if out is None else out.dtype
     if dtype not in _FLOATS:
         raise ValueError(f"out must be torch.float32 or torch.bfloat16, got {dtype}")
     if out is not None:
         _want(out, "out", (T, N))
-    dev = _on_device(y=y, slots=slots, weights=weights, out=out)
+    dev = y.device if fit and out is None else _on_device(y=y, slots=slots, weights=weights, out=out)
     if out is None:
         out = _empty((T, N), dtype, dev, stream)
     _check(lib().bsmm_expert_combine(T, S, k, N, y.data_ptr(), slots.data_ptr(), _at(weights), out.data_ptr(),
@@ -1234,13 +1275,19 @@ def expert_combine_backward(d_out, y, slots, weights=None, dy=None, d_weights=No
     """Backward of :func:`expert_combine`: returns ``(dy, d_weights)``, ``dy``
     [S, N] bfloat16 (slots that do not occur are left as they are) and
     ``d_weights`` [T, k] float32 (None without weights)."""
-    S, N, T, k = _combined(y, slots, weights)
-    _want(d_out, "d_out", (T, N), dtypes=_FLOATS)
-    if dy is not None:
-        _want(dy, "dy", (S, N), dtypes=_BF16)
-    if d_weights is not None:
-        _want(d_weights, "d_weights", (T, k), dtypes=_F32)
-    dev = _on_device(y=y, slots=slots, weights=weights, d_out=d_out, dy=dy, d_weights=d_weights)
+    fit = _match("b:SN i:Tk f?:Tk F:TN b?:SN f?:Tk", y, slots, weights, d_out, dy, d_weights)
+    if fit:
+        (S, N, T, k), dev = fit[6:], y.device
+    else:
+        S, N, T, k = _combined(y, slots, weights)
+        _want(d_out, "d_out", (T, N), dtypes=_FLOATS)
+        if dy is not None:
+            _want(dy, "dy", (S, N), dtypes=_BF16)
+        if d_weights is not None:
+            _want(d_weights, "d_weights", (T, k), dtypes=_F32)
+        dev = _on_device(y=y, slots=slots, weights=weights, d_out=d_out, dy=dy, d_weights=d_weights)
+    if dy is d_weights is None and weights is not None:
+        dy, d_weights = _empties(dev, stream, torch.bfloat16, (S, N), torch.float32, (T, k))
     if dy is None:
         dy = _empty((S, N), torch.bfloat16, dev, stream)
     if d_weights is None and weights is not None:

@@ -1,5 +1,5 @@
 // What the binding asks of many tensors, in one call from Python: the addresses
-// and sizes of a list, and new tensors.
+// and sizes of a list, those of a call's arguments, and new tensors.
 //
 // An optimizer's step over hundreds of small tensors is over on the GPU before
 // an interpreter has asked each of them for its address, its size, its type,
@@ -107,9 +107,100 @@ PyObject* empties(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// match(pattern, device, tensor, ...) -> (address, ..., size, ...), or None.
+// The pattern has a word a tensor: its type, `?` where None may take its place
+// (address None), `:` and a letter a dimension.  Types: f binary32, b bfloat16,
+// F either, i int32, c one byte of any type, . any.  The same letter is the same
+// size everywhere; the sizes follow the addresses in the order of their letters'
+// first places.  `#` for the dimensions: any, and the tensor's bytes as a size.
+// All are contiguous CUDA tensors on the device.
+PyObject* match(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  TORCH_CHECK_TYPE(nargs >= 2 && PyUnicode_Check(args[0]), "match(pattern, device, tensor, ...)");
+  const char* at = PyUnicode_AsUTF8(args[0]);
+  const long device = PyLong_AsLong(args[1]);
+  if (!at || PyErr_Occurred()) return nullptr;
+  constexpr Py_ssize_t kMost = 16;
+  const Py_ssize_t n = nargs - 2;
+  TORCH_CHECK_TYPE(n <= kMost, "at most 16 tensors");
+  uint64_t address[kMost];
+  bool given[kMost];
+  char letters[2 * kMost];
+  int64_t sizes[2 * kMost];
+  int count = 0;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    while (*at == ' ') ++at;
+    const char type = *at;
+    TORCH_CHECK_TYPE(type, "a pattern for fewer tensors");
+    const bool optional = *++at == '?';
+    if (optional) ++at;
+    TORCH_CHECK_TYPE(*at == ':', "a pattern's word is type:dimensions");
+    ++at;
+    given[i] = args[i + 2] != Py_None;
+    if (!given[i]) {
+      if (!optional) Py_RETURN_NONE;
+      while (*at && *at != ' ') ++at;
+      continue;
+    }
+    if (!THPVariable_Check(args[i + 2])) Py_RETURN_NONE;
+    const at::Tensor& t = THPVariable_Unpack(args[i + 2]);
+    if (t.layout() != c10::kStrided || !t.is_cuda() || t.get_device() != device || !t.is_contiguous()) Py_RETURN_NONE;
+    const c10::ScalarType st = t.scalar_type();
+    const bool f32 = st == c10::ScalarType::Float, bf16 = st == c10::ScalarType::BFloat16;
+    const bool right = type == 'f' ? f32
+                       : type == 'b' ? bf16
+                       : type == 'F' ? f32 || bf16
+                       : type == 'i' ? st == c10::ScalarType::Int
+                       : type == 'c' ? t.element_size() == 1
+                                     : type == '.';
+    if (!right) Py_RETURN_NONE;
+    if (*at == '#') {
+      TORCH_CHECK_TYPE(count < 2 * kMost, "too many sizes");
+      letters[count] = '\0';  // no letter's
+      sizes[count++] = t.numel() * static_cast<int64_t>(t.element_size());
+      ++at;
+    } else {
+      int64_t d = 0;
+      for (; *at && *at != ' '; ++at, ++d) {
+        if (d >= t.dim()) Py_RETURN_NONE;
+        int j = 0;
+        while (j < count && letters[j] != *at) ++j;
+        if (j == count) {
+          TORCH_CHECK_TYPE(count < 2 * kMost, "too many sizes");
+          letters[count] = *at;
+          sizes[count++] = t.size(d);
+        } else if (sizes[j] != t.size(d)) {
+          Py_RETURN_NONE;
+        }
+      }
+      if (d != t.dim()) Py_RETURN_NONE;
+    }
+    address[i] = reinterpret_cast<uint64_t>(t.data_ptr());
+  }
+  THPObjectPtr out(PyTuple_New(n + count));
+  if (!out) return nullptr;
+  for (Py_ssize_t i = 0; i < n + count; ++i) {
+    PyObject* v;
+    if (i >= n) {
+      v = PyLong_FromLongLong(sizes[i - n]);
+    } else if (given[i]) {
+      v = PyLong_FromUnsignedLongLong(address[i]);
+    } else {
+      Py_INCREF(Py_None);
+      v = Py_None;
+    }
+    if (!v) return nullptr;
+    PyTuple_SET_ITEM(out.get(), i, v);
+  }
+  return out.release();
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"addresses", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(addresses)), METH_FASTCALL,
      "Addresses, sizes and type of a list of contiguous CUDA tensors, or None."},
+    {"match", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(match)), METH_FASTCALL,
+     "Addresses and sizes of a call's tensors that fit a pattern, or None."},
     {"empties", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empties)), METH_FASTCALL,
      "New CUDA tensors of given types and shapes."},
     {nullptr, nullptr, 0, nullptr}};
