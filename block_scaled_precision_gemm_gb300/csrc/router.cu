@@ -432,7 +432,7 @@ struct RouteBackwardParams {
 // w dw; over all experts' softmax p, dl = -p mean besides, and w_j dw_j at the
 // chosen.  The row passes through shared memory, where the chosen are added.
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(256) route_backward(const RouteBackwardParams p) {
+__global__ void __launch_bounds__(256, VPL <= 8 ? 6 : 1) route_backward(const RouteBackwardParams p) {
   using R = RowLoad<VPL, BF16>;
   extern __shared__ __align__(16) float rows_sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(256) route_backward(const RouteBackwardParams 
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        d[j] = expf(d[j] - largest);
+        d[j] = exp_term(d[j] - largest);
         sum += d[j];
       }
       sum = warp_sum(sum);
@@ -468,6 +468,12 @@ __global__ void __launch_bounds__(256) route_backward(const RouteBackwardParams 
 #pragma unroll
       for (int j = 0; j < VPL; ++j) d[j] = largest > -INFINITY ? d[j] * scale : 0.f;
     }
+    // whether an expert occurs twice: one of its lanes then finds another's number
+    // in its place (matching the lanes' values took as long as all the rest)
+    __syncwarp();
+    if (id >= 0) row[id] = __int_as_float(lane);
+    __syncwarp();
+    const bool distinct = __all_sync(kAll, id < 0 || __float_as_int(row[id]) == lane);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < VPL; j += R::V) {
@@ -485,8 +491,7 @@ __global__ void __launch_bounds__(256) route_backward(const RouteBackwardParams 
     const float at_chosen = p.renormalize ? w * (dw - mean) : wd;
     // at once where no expert occurs twice; else one after the other, so that
     // its parts add up in their order
-    const uint32_t same = __match_any_sync(kAll, id >= 0 ? id : ~lane);
-    if (__all_sync(kAll, same == 1u << lane)) {
+    if (distinct) {
       if (id >= 0) row[id] += at_chosen;
     } else {
       for (int j = 0; j < p.k; ++j) {
@@ -772,7 +777,7 @@ struct RunRouteBackward {
   static cudaError_t run(RouteBackwardParams& p, int sms, cudaStream_t s) {
     p.vec = whole_vectors<VPL, BF16>(p.logits, p.ld, p.E);
     const int smem = 8 * 32 * VPL * 4;
-    const int64_t blocks = std::min<int64_t>(ceil_div(p.T, 8), 8 * sms);
+    const int64_t blocks = std::min<int64_t>(ceil_div(p.T, 8), 16 * sms);
     TraceScope tr("route_backward", s);
     route_backward<VPL, BF16><<<static_cast<unsigned>(blocks), 256, smem, s>>>(p);
     return cudaGetLastError();
