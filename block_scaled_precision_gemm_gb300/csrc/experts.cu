@@ -32,6 +32,14 @@
 //               eight blocks' 4k cycles of MMAs
 //   warps 4-19  epilogue: accumulator -> registers -> bfloat16 rows
 // Sums are FP32 over the whole contraction and are rounded to bfloat16 once.
+//
+// What bounds it (2070 MHz): a 256-row block's MMAs take 512 cycles, and 65536
+// rows x 32 experts of 4096 x 4096 run 690 us, 3.2 PFLOP/s, under the power cap.
+// Few rows: a block takes 430 cycles to issue, less than its weights take to
+// arrive when all SMs load (64 experts, 8 rows each: 1.1 GB in 180 us, 6.2 TB/s).
+// Between the two, with little shared between tiles, L2 delivers about 38 bytes
+// a cycle and SM: a block of 256 rows then takes 850 cycles.  A launch takes
+// about 7 us beside its blocks.
 // Every wait is bounded; on expiry a CTA records the site and winds down.
 #include <cuda_bf16.h>
 
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the whole warp, one lane of it issuing (elect_one)
         const uint32_t issue = elect_one();
         int stage = 0, g = 0, narrow_half = 0;
-        uint32_t phase = 0, tph = 0, gph = 0;  // tph: a bit per half of the accumulator
+        uint32_t phase = 0, tph = 0, gph = 0, used = 0;  // tph, used: a bit per half of the accumulator
         bool ok = true, ready = false, scales_ready = false;
         const uint64_t a_d0 = smem_desc(smem_u32(sA), 16, 1024, 2), b_d0 = smem_desc(smem_u32(sB), 16, 1024, 2);
         const uint64_t sfa_d0 = smem_desc(smem_u32(sSFA), 0, 128, 0), sfb_d0 = smem_desc(smem_u32(sSFB), 0, 128, 0);
@@ -453,10 +461,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int h = 0; h < 2; ++h)
             if ((halves >> h) & 1u) tc_commit_pair_mc_if(issue, &tfull[h], 0x3);
           tph ^= halves;
+          used |= halves;
           if (halves != 3u) narrow_half ^= 1;
         }
         tc_commit_pair_mc_if(issue, done, 0x1);
         if (issue) mbar_wait(done, 0, p.timeout_ns, never_abort, p.status, kSiteDone);
+        // the epilogues' last arrivals, the follower's among them, have landed
+        // before this CTA may exit
+        if (issue && ok)
+          for (int h = 0; h < 2; ++h)
+            if ((used >> h) & 1u)
+              mbar_wait(&tempty[h], ((tph >> h) & 1u) ^ 1u, p.timeout_ns, abort_flag, p.status, kSiteDrain);
       }
       __syncwarp();
     } else {
@@ -625,8 +640,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncwarp();
   if (p.late_wait) pdl_wait();
   tc_fence_before();
-  cluster_arrive_relaxed();  // no signal may target a CTA that has exited; the
-  cluster_wait();            // stores need not have landed for that
+  // No signal may target a CTA that has exited: those to this CTA were waited for
+  // above.  The stores need not have landed for that, so the arrival is relaxed.
+  cluster_arrive_relaxed();
+  cluster_wait();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);

@@ -6,8 +6,13 @@
 //   combine           out[t] = sum over j of weights[t, j] y[slots[t, j]]
 //   combine_backward  dy and the weights' gradient
 //
-// All of it is bound by memory (the sums) or by latency (a decode step's few
-// tokens): one pass over each array, no atomic whose order could show.
+// One pass over each array, no atomic whose order could show.  The sums are
+// bound by memory: 16384 tokens x 4 rows of 4096, 0.67 GB forward in 98 us (6.8
+// TB/s), 1.21 GB backward in 189 us (6.4 TB/s).  The choice is bound by its
+// instructions, 368 a token of 256 experts (a warp a token; 65536 tokens, 8 of 256
+// experts, bfloat16: choose 34 us, place 10; binary32 60 in all), its backward
+// by the latency of a token's chain (21 us against 11 for its bytes), a decode
+// step's few tokens by one launch (16 tokens: 3.7 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
