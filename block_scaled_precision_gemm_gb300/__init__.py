@@ -1350,7 +1350,7 @@ def _explain_list(ts, name, sizes, per, dtypes, itemsize):
 
 def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, grad_scale=1.0, m_scales=None,
           v_scales=None, copies=None, hyper=None, stream=None):
-    """One AdamW step on lists of tensors, in place, in one launch per 96.
+    """One AdamW step on lists of tensors, in place, in one launch per 384.
 
     ``params`` and ``grads`` float32 or bfloat16.  ``m`` and ``v`` float32, or
     with ``m_scales`` and ``v_scales`` (float32, one per 128 numbers) E4M3 codes

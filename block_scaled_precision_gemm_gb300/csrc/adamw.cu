@@ -12,12 +12,13 @@
 // 6.8 TB/s.  With states in 8 bits, 10 to 16 bytes, the root, the division and the
 // two quantizations bind (issue 72% busy): 268M numbers with bfloat16 gradients and
 // copies, 4.3 GB, in 809 us, 5.4 TB/s.  The tensors' addresses are kernel parameters (up to
-// kTensors a launch), cut into chunks of 2048 or 4096 numbers that the blocks
+// 384 a launch), cut into chunks of 2048 or 4096 numbers that the blocks
 // take in turn: small tensors share a launch and large ones spread over all SMs.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "blockquant.cuh"
 #include "internal.h"
@@ -25,7 +26,8 @@
 namespace bsmm {
 namespace {
 
-constexpr int kTensors = 96;
+// Tensors of a launch: 7 KB of kernel parameters, or 28 KB for longer lists.
+constexpr int kFew = 96, kMany = 384;
 template <bool BITS8>
 constexpr int kChunk = BITS8 ? 2048 : 4096;
 constexpr int kThreads = 256;
@@ -41,24 +43,28 @@ struct AdamTensor {
   __nv_bfloat16* copy;
   int64_t n;
 };
-struct AdamParams {
-  AdamTensor t[kTensors];
-  int64_t first[kTensors + 1];  // chunks before each tensor
-  unsigned wide[kTensors / 32];  // bit: the tensor's arrays suit 4-number accesses
-  int count;
+struct AdamNumbers {
   float b1, b2, c1, c2, eps;       // c = 1 - b
   float decay, rate, root2, scale;  // 1 - lr wd, lr / bias1, 1 / sqrt(bias2), of the gradient
   const float* hyper;              // device: lr, step, grad_scale instead
   double beta1, beta2, weight_decay;
   float minus_zero;
 };
+template <int N>
+struct AdamParams : AdamNumbers {
+  int count;
+  unsigned wide[N / 32];  // bit: the tensor's arrays suit 4-number accesses
+  int64_t first[N + 1];   // chunks before each tensor
+  AdamTensor t[N];
+};
+static_assert(sizeof(AdamParams<kMany>) <= 32764, "kernel parameters");
 
 struct Factors {
   float decay, rate, root2, scale;
 };
 
 // Returns the root of the new v.
-__device__ __forceinline__ float move(float& p, float g, float& m, float& v, const AdamParams& a, const Factors& f) {
+__device__ __forceinline__ float move(float& p, float g, float& m, float& v, const AdamNumbers& a, const Factors& f) {
   g = __fmul_rn(g, f.scale);
   m = __fadd_rn(__fmul_rn(a.b1, m), __fmul_rn(a.c1, g));
   v = __fadd_rn(__fmul_rn(a.b2, v), __fmul_rn(__fmul_rn(a.c2, g), g));
@@ -77,7 +83,7 @@ struct Packed {
   __device__ __forceinline__ float2 add(float2 a, float2 b) const { return __fadd2_rn(a, b); }
 };
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 move2(const Packed& k, float2& p, float2 g, float2& m, float2& v, const AdamParams& a,
+__device__ __forceinline__ float2 move2(const Packed& k, float2& p, float2 g, float2& m, float2& v, const AdamNumbers& a,
                                         const Factors& f) {
   g = k.mul(g, both(f.scale));
   m = k.add(k.mul(both(a.b1), m), k.mul(both(a.c1), g));
@@ -209,8 +215,8 @@ __device__ __forceinline__ void copy_async(T* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(src), "n"(BYTES) : "memory");
 }
 
-template <typename P, typename G, bool BITS8>
-__global__ void __launch_bounds__(kThreads, BITS8 ? kBlocks8 : 1) adamw(const __grid_constant__ AdamParams a) {
+template <typename P, typename G, bool BITS8, int N>
+__global__ void __launch_bounds__(kThreads, BITS8 ? kBlocks8 : 1) adamw(const __grid_constant__ AdamParams<N> a) {
   constexpr int CHUNK = kChunk<BITS8>;
   __shared__ Factors shared;
   Factors f{a.decay, a.rate, a.root2, a.scale};
@@ -249,13 +255,17 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? kBlocks8 : 1) adamw(const __
       __nv_bfloat16* copy = t.copy ? t.copy + at : nullptr;
       float* m = static_cast<float*>(t.m) + at;
       float* v = static_cast<float*>(t.v) + at;
-      if (n == CHUNK && ((a.wide[ti >> 5] >> (ti & 31)) & 1u)) {
+      const bool wide = (a.wide[ti >> 5] >> (ti & 31)) & 1u;
+      const int fours = wide ? n & ~3 : 0;  // the rest one by one
+      auto by_fours = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float4 pp[2], gg[2], mm[2], vv[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int i = 4 * (threadIdx.x + kThreads * (2 * h + j));
+            if (!WHOLE && i >= fours) break;
             pp[j] = load4(p + i);
             gg[j] = load4(g + i);
             mm[j] = load4(m + i);
@@ -264,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? kBlocks8 : 1) adamw(const __
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int i = 4 * (threadIdx.x + kThreads * (2 * h + j));
+            if (!WHOLE && i >= fours) break;
             move(pp[j].x, gg[j].x, mm[j].x, vv[j].x, a, f);
             move(pp[j].y, gg[j].y, mm[j].y, vv[j].y, a, f);
             move(pp[j].z, gg[j].z, mm[j].z, vv[j].z, a, f);
@@ -274,15 +285,16 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? kBlocks8 : 1) adamw(const __
             if (copy) store4(copy + i, pp[j]);
           }
         }
-      } else {
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-          float pp = load1(p + i), mm = m[i], vv = v[i];
-          move(pp, load1(g + i), mm, vv, a, f);
-          store1(p + i, pp);
-          m[i] = mm;
-          v[i] = vv;
-          if (copy) copy[i] = __float2bfloat16_rn(pp);
-        }
+      };
+      if (fours == CHUNK) by_fours(std::true_type());
+      else if (fours) by_fours(std::false_type());
+      for (int i = fours + threadIdx.x; i < n; i += kThreads) {
+        float pp = load1(p + i), mm = m[i], vv = v[i];
+        move(pp, load1(g + i), mm, vv, a, f);
+        store1(p + i, pp);
+        m[i] = mm;
+        v[i] = vv;
+        if (copy) copy[i] = __float2bfloat16_rn(pp);
       }
     }
   } else {
@@ -401,12 +413,56 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? kBlocks8 : 1) adamw(const __
   }
 }
 
+template <int N>
+cudaError_t launch_lists(const AdamwRequest& r, const AdamNumbers& numbers, int sms, cudaStream_t s) {
+  using Kernel = void (*)(AdamParams<N>);
+  constexpr Kernel kernels[8] = {
+      adamw<float, float, false, N>,         adamw<float, float, true, N>,
+      adamw<float, __nv_bfloat16, false, N>, adamw<float, __nv_bfloat16, true, N>,
+      adamw<__nv_bfloat16, float, false, N>, adamw<__nv_bfloat16, float, true, N>,
+      adamw<__nv_bfloat16, __nv_bfloat16, false, N>, adamw<__nv_bfloat16, __nv_bfloat16, true, N>};
+  const Kernel kern = kernels[(r.p_bf16 ? 4 : 0) + (r.g_bf16 ? 2 : 0) + (r.bits8 ? 1 : 0)];
+  const int smem = r.bits8 ? 2 * 2 * kThreads * ((r.p_bf16 ? 8 : 16) + (r.g_bf16 ? 8 : 16) + 8) : 0;  // two Stages
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  AdamParams<N> a;
+  static_cast<AdamNumbers&>(a) = numbers;
+  a.first[0] = 0;
+  for (int64_t i = 0; i < r.count;) {
+    a.count = 0;
+    for (unsigned& w : a.wide) w = 0;
+    for (; i < r.count && a.count < N; ++i) {
+      if (r.n[i] == 0) continue;
+      AdamTensor& t = a.t[a.count];
+      t = AdamTensor{r.p[i], r.g[i], r.m[i], r.v[i], r.bits8 ? r.m_scales[i] : nullptr, r.bits8 ? r.v_scales[i] : nullptr,
+                     r.copies ? static_cast<__nv_bfloat16*>(r.copies[i]) : nullptr, r.n[i]};
+      const uintptr_t state = r.bits8 ? 4 : 16;
+      const bool wide = reinterpret_cast<uintptr_t>(t.p) % (r.p_bf16 ? 8 : 16) == 0 &&
+                        reinterpret_cast<uintptr_t>(t.g) % (r.g_bf16 ? 8 : 16) == 0 &&
+                        reinterpret_cast<uintptr_t>(t.m) % state == 0 && reinterpret_cast<uintptr_t>(t.v) % state == 0 &&
+                        reinterpret_cast<uintptr_t>(t.copy) % 8 == 0;
+      if (wide) a.wide[a.count >> 5] |= 1u << (a.count & 31);
+      a.first[a.count + 1] = a.first[a.count] + ceil_div(t.n, r.bits8 ? kChunk<true> : kChunk<false>);
+      ++a.count;
+    }
+    if (a.count == 0) break;
+    const int64_t grid = std::min<int64_t>(a.first[a.count], (r.bits8 ? kBlocks8 : 8) * sms);
+    TraceScope tr(r.bits8 ? "adamw (8 bits)" : "adamw", s);
+    kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_adamw(const AdamwRequest& r, cudaStream_t s) {
   const DeviceCtx* ctx = device_ctx();
   if (!ctx) return cudaErrorInitializationError;
-  AdamParams a{};
+  AdamNumbers a{};
   a.b1 = static_cast<float>(r.beta1);
   a.b2 = static_cast<float>(r.beta2);
   a.c1 = static_cast<float>(1.0 - r.beta1);
@@ -422,43 +478,7 @@ cudaError_t launch_adamw(const AdamwRequest& r, cudaStream_t s) {
   a.beta2 = r.beta2;
   a.weight_decay = r.weight_decay;
   a.minus_zero = -0.f;
-  using Kernel = void (*)(AdamParams);
-  const Kernel kernels[8] = {
-      adamw<float, float, false>,          adamw<float, float, true>,
-      adamw<float, __nv_bfloat16, false>,  adamw<float, __nv_bfloat16, true>,
-      adamw<__nv_bfloat16, float, false>,  adamw<__nv_bfloat16, float, true>,
-      adamw<__nv_bfloat16, __nv_bfloat16, false>, adamw<__nv_bfloat16, __nv_bfloat16, true>};
-  const Kernel kern = kernels[(r.p_bf16 ? 4 : 0) + (r.g_bf16 ? 2 : 0) + (r.bits8 ? 1 : 0)];
-  const int smem = r.bits8 ? 2 * 2 * kThreads * ((r.p_bf16 ? 8 : 16) + (r.g_bf16 ? 8 : 16) + 8) : 0;  // two Stages
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  for (int64_t i = 0; i < r.count;) {
-    a.count = 0;
-    for (unsigned& w : a.wide) w = 0;
-    for (; i < r.count && a.count < kTensors; ++i) {
-      if (r.n[i] == 0) continue;
-      AdamTensor& t = a.t[a.count];
-      t = AdamTensor{r.p[i], r.g[i], r.m[i], r.v[i], r.bits8 ? r.m_scales[i] : nullptr, r.bits8 ? r.v_scales[i] : nullptr,
-                     r.copies ? static_cast<__nv_bfloat16*>(r.copies[i]) : nullptr, r.n[i]};
-      const uintptr_t state = r.bits8 ? 4 : 16;
-      const bool wide = reinterpret_cast<uintptr_t>(t.p) % (r.p_bf16 ? 8 : 16) == 0 &&
-                        reinterpret_cast<uintptr_t>(t.g) % (r.g_bf16 ? 8 : 16) == 0 &&
-                        reinterpret_cast<uintptr_t>(t.m) % state == 0 && reinterpret_cast<uintptr_t>(t.v) % state == 0 &&
-                        reinterpret_cast<uintptr_t>(t.copy) % 8 == 0;
-      if (wide) a.wide[a.count >> 5] |= 1u << (a.count & 31);
-      a.first[a.count + 1] = a.first[a.count] + ceil_div(t.n, r.bits8 ? kChunk<true> : kChunk<false>);
-      ++a.count;
-    }
-    if (a.count == 0) break;
-    const int64_t grid = std::min<int64_t>(a.first[a.count], (r.bits8 ? kBlocks8 : 8) * ctx->num_sms);
-    TraceScope tr(r.bits8 ? "adamw (8 bits)" : "adamw", s);
-    kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return r.count <= kFew ? launch_lists<kFew>(r, a, ctx->num_sms, s) : launch_lists<kMany>(r, a, ctx->num_sms, s);
 }
 
 }  // namespace bsmm

@@ -713,7 +713,7 @@ bsmm_status bsmm_expert_combine_backward(int64_t T, int64_t S, int k, int64_t N,
 /* AdamW over many tensors                                                   */
 /* ------------------------------------------------------------------------ */
 
-/* One step of AdamW on `count` tensors, launched together (up to 96 a launch).
+/* One step of AdamW on `count` tensors, launched together (up to 384 a launch).
  * No counterpart on the pages.  In binary32, every operation rounded on its
  * own, with b1, b2 and c = 1 - b rounded from binary64:
  *

@@ -144,8 +144,9 @@ def test_tensors_that_are_not_aligned(bits8):
             assert torch.equal(a, b), k
 
 
-def test_more_tensors_than_a_launch_takes():
-    sizes = [1 + (i * 37) % 300 for i in range(250)]
+@pytest.mark.parametrize("count", [96, 97, 250, 900])
+def test_more_tensors_than_a_launch_takes(count):
+    sizes = [1 + (i * 37) % 300 for i in range(count)]
     d = tensors(sizes)
     want = [expected(d, i, False, 4)[1] for i in range(len(sizes))]
     _bsmm().adamw(d["params"], d["grads"], d["m"], d["v"], 4, **ARGS)
