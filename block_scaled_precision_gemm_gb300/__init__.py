@@ -32,6 +32,7 @@ Entry points (see ``include/bsmm.h`` for the full contract):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from array import array
 
@@ -1048,6 +1049,15 @@ def _same_device(dev, **named):
             raise ValueError(f"{n} is on {t.device}, the other arguments on {dev}")
 
 
+# The sizes below depend on their arguments alone, which a model repeats: asked
+# for once each, they cost a call 0.1 us instead of 0.6 to 0.9.
+
+@functools.lru_cache(maxsize=4096)
+def _atoms_size(E, N, K, code) -> int:
+    return scale_atoms_size(E, N, K, code, SCALE_UE8M0)
+
+
+@functools.lru_cache(maxsize=4096)
 def route_workspace_size(T, E) -> int:
     return lib().bsmm_route_workspace_size(T, E)
 
@@ -1130,6 +1140,7 @@ def _route_backward(T, E, k, logits, ld, renormalize, d_weights, ids, weights, d
     return d_logits
 
 
+@functools.lru_cache(maxsize=4096)
 def expert_gemm_workspace_size(S, E, K, by_rows=True) -> int:
     return lib().bsmm_expert_gemm_workspace_size(S, E, K, 1 if by_rows else 0)
 
@@ -1148,7 +1159,7 @@ def expert_gemm(x, x_scales, w, w_atoms, offsets, rows=None, x_type="e4m3", w_ty
     if fit:
         X, K, B, E, N, atoms, slots = fit[6:13]
         S = X if rows is None else fit[13]
-        if K != 32 * B or slots != E + 1 or atoms < scale_atoms_size(E, N, K, wt, SCALE_UE8M0):
+        if K != 32 * B or slots != E + 1 or atoms < _atoms_size(E, N, K, wt):
             fit = None
     if not fit:
         _want(x, "x", itemsize=1)
@@ -1160,7 +1171,7 @@ def expert_gemm(x, x_scales, w, w_atoms, offsets, rows=None, x_type="e4m3", w_ty
         _want(x_scales, "x_scales", itemsize=1)
         if K % 32 == 0:  # else the library says why
             _want(x_scales, "x_scales", (X, K // 32))
-            _want(w_atoms, "w_atoms", min_bytes=scale_atoms_size(E, N, K, wt, SCALE_UE8M0))
+            _want(w_atoms, "w_atoms", min_bytes=_atoms_size(E, N, K, wt))
         S = _expert_slots(offsets, rows, E, X)
     if y is not None:
         _want(y, "y", (S, N), dtypes=_BF16)
@@ -1193,6 +1204,7 @@ def _expert_slots(offsets, rows, E, X) -> int:
     return rows.shape[0]
 
 
+@functools.lru_cache(maxsize=4096)
 def expert_backward_workspace_size(S, E, N, K) -> int:
     return lib().bsmm_expert_backward_workspace_size(S, E, N, K)
 
