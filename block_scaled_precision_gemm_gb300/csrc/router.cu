@@ -183,31 +183,41 @@ struct RowLoad {
   }
 };
 
-// One token by one warp: lane j < k returns its j-th choice (-1: none) and weight.
-// Every lane sorts its logits (groups of 8 of them); then each choice is the
-// largest of the lanes' first ones, and the lane that held it moves on.
+// A token's logits in a lane: keys for the choice, sorted in groups of 8, and the
+// lane's part of the softmax's sum (over all experts only).
 template <int VPL, bool BF16>
-__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane, int& id, float& weight) {
+struct LaneKeys {
   using R = RowLoad<VPL, BF16>;
   using Q = Ranked<BF16>;
   using Key = typename Q::Key;
-  constexpr int G = VPL < 8 ? VPL : 8;
-  float l[VPL];
-  R::load(p.logits, t * p.ld, p.E, p.vec, lane, l);
+  static constexpr int G = VPL < 8 ? VPL : 8;
   Key key[VPL];
+  float part;
+
+  __device__ __forceinline__ void load(const RouteParams& p, int64_t t, int lane) {
+    float l[VPL];
+    R::load(p.logits, t * p.ld, p.E, p.vec, lane, l);
+    part = 0.f;
+    if (!p.renormalize) {
+      float largest = l[0];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) key[j] = Q::make(l[j], R::index(j, lane));
+      for (int j = 1; j < VPL; ++j) largest = fmaxf(largest, l[j]);
+      largest = ordered_value(__reduce_max_sync(kAll, ordered(largest)));
 #pragma unroll
-  for (int g = 0; g < VPL; g += G) sort_falling<G>(key + g);
-  Key got = 0, first = 0;
-  // `depth`: how many of a group's keys can still be asked for
-  auto round = [&](int n, int depth) {
+      for (int j = 0; j < VPL; ++j) part += exp_term(l[j] - largest);
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = Q::make(l[j], R::index(j, lane));
+#pragma unroll
+    for (int g = 0; g < VPL; g += G) sort_falling<G>(key + g);
+  }
+  // The largest key of the warp; the lane that holds it moves on.  `depth`: how
+  // many of a group's keys can still be asked for.
+  __device__ __forceinline__ Key next(int depth) {
     Key mine = key[0];
 #pragma unroll
     for (int g = G; g < VPL; g += G) mine = max(mine, key[g]);
     const Key best = Q::most(mine);
-    if (n == 0) first = best;
-    if (lane == n) got = best;
 #pragma unroll
     for (int g = 0; g < VPL; g += G) {
       const bool taken = key[g] == best;
@@ -216,6 +226,37 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane
         if (j < depth) key[g + j] = taken ? key[g + j + 1] : key[g + j];
       if (G - 1 < depth) key[g + G - 1] = taken ? Key(0) : key[g + G - 1];
     }
+    return best;
+  }
+};
+
+// A warp takes two tokens at once, one a half: a token's n-th choice is lane n's
+// of its half (up to 16), so that what follows the choice (id, weight, rank) is
+// done once for both.  Longer rows, and k above 16: one token, lane n < 32.
+template <int VPL, bool BF16>
+constexpr bool kPairs = VPL * (BF16 ? 1 : 2) <= 16;
+
+// ONE token or two (t, t + 1) by one warp: each lane's choice (-1: none) and weight.
+template <int VPL, bool BF16, bool ONE>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, bool second, int lane, int& id, float& weight) {
+  using L = LaneKeys<VPL, BF16>;
+  using Q = typename L::Q;
+  using Key = typename L::Key;
+  constexpr int HALF = ONE ? 32 : 16;
+  const bool upper = !ONE && lane >= 16;
+  const int place = lane & (HALF - 1);
+  L a, b;
+  a.load(p, t, lane);
+  if (!ONE) b.load(p, second ? t + 1 : t, lane);
+  Key got = 0, first = 0;
+  auto round = [&](int n, int depth) {
+    Key best = a.next(depth);
+    if (!ONE) {
+      const Key other = b.next(depth);
+      best = upper ? other : best;
+    }
+    if (n == 0) first = best;
+    if (place == n) got = best;
   };
   if (p.k <= 8) {
 #pragma unroll
@@ -224,18 +265,20 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane
       round(n, 7 - n);
     }
   } else {
-    for (int n = 0; n < p.k; ++n) round(n, G);
+    for (int n = 0; n < p.k; ++n) round(n, L::G);
   }
   id = Q::none(got) ? -1 : Q::place(got);
-  const float largest = Q::value(first);
-  const float e = id >= 0 ? expf(Q::value(got) - largest) : 0.f;
-  float part = e;
-  if (!p.renormalize) {
-    part = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) part += exp_term(l[j] - largest);
+  const float e = id >= 0 ? expf(Q::value(got) - Q::value(first)) : 0.f;
+  float sum;
+  if (ONE) {
+    sum = p.renormalize ? e : a.part;
+  } else if (p.renormalize) {
+    sum = e;
+  } else {  // the halves exchange their parts of each other's token
+    sum = (upper ? b.part : a.part) + __shfl_xor_sync(kAll, upper ? a.part : b.part, 16);
   }
-  const float sum = warp_sum(part);
+#pragma unroll
+  for (int o = HALF / 2; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
   weight = id >= 0 ? __fdiv_rn(e, sum) : 0.f;
 }
 
@@ -244,29 +287,44 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane
 // in earlier runs; slots as a pair's rank in its own run and total [E] as the
 // block's numbers of pairs.  A token's experts differ, so its lanes count
 // without conflict and in the tokens' order: the layout is stable.
-template <int VPL, bool BF16, int WARPS>
-__device__ __forceinline__ void choose_tokens(const RouteParams& p, int64_t t0, int64_t t1, int64_t run, int* counts,
-                                              int* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* mine = counts + warp * p.E;
-  const int64_t end = min(t1, t0 + run * (warp + 1));
-  for (int64_t t = t0 + run * warp; t < end; ++t) {
+template <int VPL, bool BF16, bool ONE>
+__device__ __forceinline__ void choose_run(const RouteParams& p, int64_t begin, int64_t end, int* mine) {
+  const int lane = threadIdx.x & 31;
+  const bool upper = !ONE && lane >= 16;
+  const int place = ONE ? lane : lane & 15;
+  for (int64_t t = begin; t < end; t += ONE ? 1 : 2) {
+    const bool second = !ONE && t + 1 < end;
     int id;
     float w;
-    choose<VPL, BF16>(p, t, lane, id, w);
-    if (lane < p.k) {
-      const int64_t at = t * p.k + lane;
-      p.ids[at] = id;
-      p.weights[at] = w;
-      int rank = -1;
-      if (id >= 0) {
+    choose<VPL, BF16, ONE>(p, t, second, lane, id, w);
+    const bool active = place < p.k && (!upper || second);
+    int rank = -1;
+#pragma unroll
+    for (int h = 0; h < (ONE ? 1 : 2); ++h) {
+      if (active && id >= 0 && upper == (h == 1)) {
         rank = mine[id];
         mine[id] = rank + 1;
       }
+      __syncwarp();
+    }
+    if (active) {
+      const int64_t at = (t + (upper ? 1 : 0)) * p.k + place;
+      p.ids[at] = id;
+      p.weights[at] = w;
       p.slots[at] = rank;
     }
-    __syncwarp();
   }
+}
+template <int VPL, bool BF16, int WARPS>
+__device__ __forceinline__ void choose_tokens(const RouteParams& p, int64_t t0, int64_t t1, int64_t run, int* counts,
+                                              int* total) {
+  const int warp = threadIdx.x >> 5;
+  int* mine = counts + warp * p.E;
+  const int64_t begin = t0 + run * warp, end = min(t1, begin + run);
+  if (kPairs<VPL, BF16> && p.k <= 16 && run > 1)
+    choose_run<VPL, BF16, !kPairs<VPL, BF16>>(p, begin, end, mine);
+  else
+    choose_run<VPL, BF16, true>(p, begin, end, mine);
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += 32 * WARPS) {
     int n[WARPS], sum = 0;
