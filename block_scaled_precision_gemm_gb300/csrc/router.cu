@@ -8,11 +8,11 @@
 //
 // One pass over each array, no atomic whose order could show.  The sums are
 // bound by memory: 16384 tokens x 4 rows of 4096, 0.67 GB forward in 98 us (6.8
-// TB/s), 1.21 GB backward in 189 us (6.4 TB/s).  The choice is bound by its
-// instructions, 368 a token of 256 experts (a warp a token; 65536 tokens, 8 of 256
-// experts, bfloat16: choose 34 us, place 10; binary32 60 in all), its backward
-// by the latency of a token's chain (21 us against 11 for its bytes), a decode
-// step's few tokens by one launch (16 tokens: 3.7 us).
+// TB/s), 1.21 GB backward in 189 us (6.4 TB/s).  The choice is bound by the latency
+// of a token's rounds and by its instructions (65536 tokens, 8 of 256 experts,
+// bfloat16: choose 31 us, place 10; binary32 57 in all), its backward by the
+// latency of a token's chain (21 us against 11 for its bytes), a decode step's few
+// tokens by one launch (16 tokens: 3.7 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -449,9 +449,11 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place(const RouteParams p
     p.rows[i] = -1;
 }
 
-// Few tokens: everything in one block and one launch.
+// Few tokens: everything in one block and one launch (us, one launch / two: 64
+// tokens of 64 experts 5.6 / 6.7, of 256 9.5 / 9.4; 128 tokens 8.1 / 7.1 and 16.1 /
+// 9.9; the second launch costs the host 6 more).
 constexpr int kFewWarps = 16;
-constexpr int64_t kFewTokens = 128;
+constexpr int64_t kFewTokens = 64;
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(32 * kFewWarps) route_few(const RouteParams p) {
   extern __shared__ int sm[];

@@ -57,7 +57,7 @@ def check_route(l, k, renormalize, **kw):
 
 ROUTES = [(1, 1, 1), (1, 2, 2), (3, 5, 5), (16, 64, 4), (7, 33, 8), (128, 64, 8), (129, 64, 8), (127, 256, 6),
           (300, 33, 7), (1000, 128, 2), (2000, 256, 8), (130, 1000, 32), (64, 1024, 32), (513, 1024, 4), (4097, 7, 2),
-          (260, 512, 1)]
+          (260, 512, 1), (65, 256, 8), (64, 256, 16), (66, 40, 17)]
 
 
 @pytest.mark.parametrize("T,E,k", ROUTES)
