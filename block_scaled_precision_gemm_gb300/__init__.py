@@ -1366,8 +1366,9 @@ def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
 
     ``params`` and ``grads`` float32 or bfloat16.  ``m`` and ``v`` float32, or
     with ``m_scales`` and ``v_scales`` (float32, one per 128 numbers) E4M3 codes
-    of ``m`` and of ``sqrt(v)``; zeros start a run.  ``copies`` receives the
-    updated parameters in bfloat16.  ``hyper``, a float32 tensor ``(lr, step,
+    of ``m`` and of ``sqrt(v)``, rounded to nearest for betas up to (0.944,
+    0.9558) and dithered by ``step`` above, where nearest would not follow; zeros
+    start a run.  ``copies`` receives the updated parameters in bfloat16.  ``hyper``, a float32 tensor ``(lr, step,
     grad_scale)`` on the device, takes the place of those arguments when the
     kernels run (a captured step's schedule)."""
     params = list(params)

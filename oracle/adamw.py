@@ -26,12 +26,55 @@ def scales(x):
     return np.where(top == 0, np.float32(1), s).astype(np.float32)
 
 
-def codes(x, s, root=False):
-    """E4M3 codes of x for the scales s; a root that is not zero keeps the smallest code."""
+def codes(x, s, root=False, step=None):
+    """E4M3 codes of x for the scales s; a root that is not zero keeps the
+    smallest code.  ``step``: None to round to nearest, or the step whose dither rounds."""
     x = np.asarray(x, np.float32)
-    q = np.clip(div32(x, np.repeat(s, 128)[:x.size]), -448, 448)
-    c = F.encode(q, "e4m3")
-    return np.where((x > 0) & (c == 0), 1, c).astype(np.uint8) if root else c
+    q = div32(x, np.repeat(s, 128)[:x.size])
+    if root:
+        q = np.where((x > 0) & (q < 2.0 ** -9), np.float32(2.0 ** -9), q)
+    if step is not None:
+        h = dither(x.size, step)
+        q = dithered(q, h >> np.uint32(12) if root else h & np.uint32(0xFFFFF))
+    return F.encode(np.clip(q, -448, 448), "e4m3")
+
+
+def dither(numbers, step):
+    """32 bits for each number of a tensor at a step."""
+    u = np.uint32
+    golden, root3 = u(0x9E3779B9), u(0xBB67AE85)
+
+    def word(x):
+        x = (x ^ (x >> u(16))) * golden
+        return x ^ (x >> u(15))
+
+    def bits(x, j):
+        x = x * root3 + j * golden
+        return x ^ (x >> u(16))
+
+    i = np.arange(numbers, dtype=u)
+    key = bits(word(np.full(1, step, u)), np.zeros(1, u))
+    return bits(word((i >> u(2)) ^ key), i & u(3))
+
+
+def dithered(q, r):
+    """q on E4M3's grid (as if that had no largest number): the number below its
+    magnitude, or where the part cut off plus r 2^-20 of a step passes one the number
+    above.  A zero has no sign."""
+    a = np.abs(np.asarray(q, np.float64))
+    step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(a, 2.0 ** -9))), -6) - 3)
+    # what the sum of a and 2^-6 keeps in binary32, below 2^-6
+    a = np.where(a < 2.0 ** -6, (a.astype(np.float32) + np.float32(2.0 ** -6)).astype(np.float64) - 2.0 ** -6, a)
+    low = np.floor(a / step)
+    cut = (a / step - low) * 2.0 ** 20
+    y = np.copysign((low + (cut + r >= 2.0 ** 20)) * step, q)
+    return np.where(y == 0, 0.0, y).astype(np.float32)
+
+
+def dithers(betas):
+    """Whether the library dithers 8-bit states: where a step moves them by less
+    than half steps of E4M3."""
+    return betas[0] > 17 / 18 or 1 - betas[1] < 2.0 ** -4.5
 
 
 def values(c, s):
