@@ -99,7 +99,6 @@ struct ExpertParams {
   int J, j_tiles;
   int row_tiles;
   int b_ks4;
-  int late_wait;      // the kernel before writes nothing that is read here
   __nv_bfloat16* y;   // [S][F], or [E][J][F]
   uint32_t idesc;     // without N
   int* status;
@@ -286,8 +285,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   if constexpr (!GRAD) tiles = starts[p.E];
   // Launched before the kernel ahead has ended.  The weights' gradient reads
   // nothing of the kernel ahead of it (dX), so it waits for it last: its blocks
-  // fill the SMs that dX's last tiles leave.
-  if (!p.late_wait) pdl_wait();
+  // fill the SMs that dX's last tiles leave.  What it reads is expert_quant's, the
+  // kernel ahead of dX (and the offsets, older still).  The only wait for that one is
+  // dX's, which it passes on: all of dX's blocks fence between their wait and the
+  // word that lets this kernel start, and this kernel's fence before its loads, for
+  // the copies by TMA too.
+  if constexpr (GRAD) {
+    __threadfence();
+    fence_proxy_async();
+  } else {
+    pdl_wait();
+    __threadfence();
+  }
   pdl_launch();
 
   // 640 threads with 96 registers each: the epilogue's 64 sums and the scale
@@ -500,19 +509,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         // the words of the group from block k0 on, as this lane stores them
+        // (plain loads: the kernel ahead may write them while this one is there)
         uint4 w[SG];
         auto load = [&](int k0) {
           if (k0 >= t.k_tiles) return;
           if constexpr (GRAD) {
 #pragma unroll
             for (int j = 0; j < SG; ++j)
-              if (k0 + j < t.k_tiles) w[j] = __ldg(reinterpret_cast<const uint4*>(src[0] + (k0 + j) * 512));
+              if (k0 + j < t.k_tiles) w[j] = *reinterpret_cast<const uint4*>(src[0] + (k0 + j) * 512);
           } else if (p.b_vec && k0 + SG <= t.k_tiles) {
 #pragma unroll
             for (int h = 0; h < SG; h += 4) {
               uint4 v[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + 4 * (k0 + h)));
+              for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(src[i] + 4 * (k0 + h));
               w[h] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
               w[h + 1] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
               w[h + 2] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
@@ -529,13 +539,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (p.b_word) {
-                  v[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i]) + k0 + j);
+                  v[i] = *(reinterpret_cast<const uint32_t*>(src[i]) + k0 + j);
                 } else {
                   v[i] = 0;
 #pragma unroll
                   for (int b = 0; b < 4; ++b) {
                     const int kb = 4 * (k0 + j) + b;
-                    v[i] |= (kb < blocks ? static_cast<uint32_t>(__ldg(src[i] + kb)) : 127u) << (8 * b);
+                    v[i] |= (kb < blocks ? static_cast<uint32_t>(src[i][kb]) : 127u) << (8 * b);
                   }
                 }
               }
@@ -638,7 +648,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 
   __syncwarp();
-  if (p.late_wait) pdl_wait();
+  if constexpr (GRAD) pdl_wait();
   tc_fence_before();
   // No signal may target a CTA that has exited: those to this CTA were waited for
   // above.  The stores need not have landed for that, so the arrival is relaxed.
@@ -1158,7 +1168,6 @@ cudaError_t launch_expert_backward(const ExpertBackwardRequest& r, cudaStream_t 
   p.J = static_cast<int>(r.N);
   p.j_tiles = static_cast<int>(ceil_div(r.N, PJ));
   p.row_tiles = row_tiles;
-  p.late_wait = 1;
   p.y = static_cast<__nv_bfloat16*>(r.dW);
   p.idesc = idesc;
   CUtensorMap ta, tsa, tb, tb16;
