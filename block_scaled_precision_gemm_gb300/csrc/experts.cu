@@ -613,7 +613,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       __nv_bfloat16* dst = p.y + static_cast<int64_t>(t.out0 + row + (odd ? 1 : 0)) * p.F + f;
       uint32_t v[32];  // bfloat16 pairs: this lane's feature in rows 2 c and 2 c + 1
       if (t.k_tiles > 0) {
-        if (!mbar_wait(&tfull[g >> 1], tph, p.timeout_ns, abort_flag, p.status, kSiteEpilogue)) break;
+        // agreed on by the warp: what follows takes all its lanes
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[g >> 1], tph, p.timeout_ns, abort_flag, p.status, kSiteEpilogue)))
+          break;
         tph ^= 1u;
         tc_fence_after();
         if (live > 0) {
