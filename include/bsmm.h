@@ -640,8 +640,9 @@ bsmm_status bsmm_route(int64_t T, int64_t E, int k, const void* logits, bsmm_dty
 /* Its backward pass, from d_weights [T, k] and the forward's ids and weights:
  * with mean = sum over j of weights d_weights,
  *   renormalize = 1  d_logits[id_j] = weights_j (d_weights_j - mean), else 0;
- *   renormalize = 0  d_logits[i] = -p_i mean, p the softmax of the logits, and
- *                    weights_j d_weights_j besides at id_j.
+ *   renormalize = 0  d_logits[i] = -p_i mean, p the softmax of the logits (a term
+ *                    e^(l_i - m) below 2^-126 counts as 0), and weights_j
+ *                    d_weights_j besides at id_j.
  * d_logits [T, E] of the logits' type, contiguous: overwritten.  An id outside
  * [0, E) has no part.  The logits are read for renormalize = 0 only. */
 bsmm_status bsmm_route_backward(int64_t T, int64_t E, int k, const void* logits, bsmm_dtype logits_type, int64_t ld,
