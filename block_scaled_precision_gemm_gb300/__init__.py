@@ -1368,10 +1368,15 @@ def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     with ``m_scales`` and ``v_scales`` (float32, one per 128 numbers) E4M3 codes
     of ``m`` and of ``sqrt(v)``, rounded to nearest for betas up to (0.944,
     0.9558) and dithered by ``step`` above, where nearest would not follow; zeros
-    start a run.  ``copies`` receives the updated parameters in bfloat16.  ``hyper``, a float32 tensor ``(lr, step,
-    grad_scale)`` on the device, takes the place of those arguments when the
-    kernels run (a captured step's schedule)."""
+    start a run.  ``copies`` receives the updated parameters in bfloat16.
+    ``hyper``, a float32 tensor ``(lr, step, grad_scale)`` on the device, takes the
+    place of those arguments when the kernels run (a captured step's schedule).
+
+    The versions of ``params`` and ``copies`` rise, so that a backward pass
+    through what autograd has saved of them raises, as after torch's own
+    in-place changes (a graph's replay changes them without that)."""
     params = list(params)
+    copies = None if copies is None else list(copies)
     if (m_scales is None) != (v_scales is None):
         raise ValueError("m_scales and v_scales go together")
     bits8 = m_scales is not None
@@ -1394,3 +1399,4 @@ def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
                             BF16 if gt is torch.bfloat16 else F32, mm, vv, E4M3 if bits8 else F32, ms, vs, cc,
                             lr, betas[0], betas[1], eps, weight_decay, int(step), grad_scale, _at(hyper),
                             _raw_stream(stream, params[0].device)), "bsmm_adamw")
+    _lists().changed(params, copies)

@@ -1,5 +1,5 @@
 // What the binding asks of many tensors, in one call from Python: the addresses
-// and sizes of a list, those of a call's arguments, and new tensors.
+// and sizes of a list, those of a call's arguments, new tensors, and their versions.
 //
 // An optimizer's step over hundreds of small tensors is over on the GPU before
 // an interpreter has asked each of them for its address, its size, its type,
@@ -77,6 +77,24 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   Py_XDECREF(sizes);
   if (r || PyErr_Occurred()) return r;
   Py_RETURN_NONE;
+}
+
+// changed(list or None, ...): the versions of the lists' tensors rise by one, as
+// after an in-place change by torch (those made in inference mode have none).
+PyObject* changed(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  for (Py_ssize_t a = 0; a < nargs; ++a) {
+    if (args[a] == Py_None) continue;
+    TORCH_CHECK_TYPE(PyList_CheckExact(args[a]), "changed(list or None, ...)");
+    for (Py_ssize_t i = 0; i < PyList_GET_SIZE(args[a]); ++i) {
+      PyObject* item = PyList_GET_ITEM(args[a], i);
+      TORCH_CHECK_TYPE(THPVariable_Check(item), "changed: a list of tensors");
+      const at::Tensor& t = THPVariable_Unpack(item);
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
+  }
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
 }
 
 // empties(device, dtype, shape, dtype, shape, ...) -> a list of new tensors.
@@ -203,6 +221,8 @@ PyMethodDef methods[] = {
      "Addresses and sizes of a call's tensors that fit a pattern, or None."},
     {"empties", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empties)), METH_FASTCALL,
      "New CUDA tensors of given types and shapes."},
+    {"changed", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(changed)), METH_FASTCALL,
+     "Raises the versions of lists of tensors."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
