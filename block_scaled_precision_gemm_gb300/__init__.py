@@ -1315,17 +1315,19 @@ def expert_combine_backward(d_out, y, slots, weights=None, dy=None, d_weights=No
 # AdamW                                                                       #
 # --------------------------------------------------------------------------- #
 
-def _tensor_list(ts, name, sizes, per=1, dtypes=None, itemsize=None):
+def _tensor_list(ts, name, sizes, per=1, dtypes=None, itemsize=None, gaps=False):
     """A list of contiguous CUDA tensors of one type, on the current device:
     their addresses and sizes (64-bit words) and that type.  ``sizes``: those of
-    another list, of which each tensor holds ceil(size / per) numbers."""
+    another list, of which each tensor holds ceil(size / per) numbers.  ``gaps``:
+    None may stand in a tensor's place (address 0)."""
     ts = list(ts)
-    dev = ts[0].get_device() if ts and isinstance(ts[0], torch.Tensor) else -1
+    first = next((t for t in ts if t is not None), None) if gaps else ts[0] if ts else None
+    dev = first.get_device() if isinstance(first, torch.Tensor) else -1
     found = None
-    if not ts or (dev >= 0 and dev == torch._C._cuda_getDevice()):
-        found = _lists().addresses(ts, dev, sizes, per)
-    if found is None or (ts and not _list_type(found[2], dtypes, itemsize)):
-        _explain_list(ts, name, sizes, per, dtypes, itemsize)
+    if not ts or (dev >= 0 and dev == torch._C._cuda_getDevice()) or (gaps and first is None):
+        found = _lists().addresses(ts, dev, sizes, per, gaps)
+    if found is None or (found[2] is not None and not _list_type(found[2], dtypes, itemsize)):
+        _explain_list(ts, name, sizes, per, dtypes, itemsize, gaps)
     return found
 
 
@@ -1333,12 +1335,13 @@ def _list_type(dtype, dtypes, itemsize) -> bool:
     return (dtypes is None or dtype in dtypes) and (itemsize is None or dtype.itemsize == itemsize)
 
 
-def _explain_list(ts, name, sizes, per, dtypes, itemsize):
+def _explain_list(ts, name, sizes, per, dtypes, itemsize, gaps):
     """Raises for what is wrong with a list of tensors."""
-    for t in ts:
+    given = [t for t in ts if t is not None] if gaps else ts
+    for t in given:
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must hold torch.Tensors")
-    kinds = {t.dtype for t in ts}
+    kinds = {t.dtype for t in given}
     if len(kinds) > 1:
         raise ValueError(f"{name} must be of one type, got {' and '.join(sorted(str(k) for k in kinds))}")
     for dtype in kinds:
@@ -1351,11 +1354,11 @@ def _explain_list(ts, name, sizes, per, dtypes, itemsize):
         if len(ts) != len(want):
             raise ValueError(f"{name} holds {len(ts)} tensors, {len(want)} needed")
         for i, (t, n) in enumerate(zip(ts, want)):
-            if t.numel() != n:
+            if t is not None and t.numel() != n:
                 raise ValueError(f"{name}[{i}] holds {t.numel()} numbers, {n} needed")
-    if not all(t.is_cuda and t.get_device() == torch._C._cuda_getDevice() for t in ts):
+    if not all(t.is_cuda and t.get_device() == torch._C._cuda_getDevice() for t in given):
         raise ValueError(f"{name} must be CUDA tensors on the current device")
-    if not all(t.layout is torch.strided and t.is_contiguous() for t in ts):
+    if not all(t.layout is torch.strided and t.is_contiguous() for t in given):
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} must be tensors with memory of their own")
 
@@ -1368,7 +1371,8 @@ def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     with ``m_scales`` and ``v_scales`` (float32, one per 128 numbers) E4M3 codes
     of ``m`` and of ``sqrt(v)``, rounded to nearest for betas up to (0.944,
     0.9558) and dithered by ``step`` above, where nearest would not follow; zeros
-    start a run.  ``copies`` receives the updated parameters in bfloat16.
+    start a run.  ``copies`` receives the updated parameters in bfloat16,
+    where its entry is not None.
     ``hyper``, a float32 tensor ``(lr, step, grad_scale)`` on the device, takes the
     place of those arguments when the kernels run (a captured step's schedule).
 
@@ -1389,7 +1393,7 @@ def adamw(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
         ms, _, _ = _tensor_list(m_scales, "m_scales", n, 128, dtypes=_F32)
         vs, _, _ = _tensor_list(v_scales, "v_scales", n, 128, dtypes=_F32)
     if copies is not None:
-        cc, _, _ = _tensor_list(copies, "copies", n, dtypes=_BF16)
+        cc, _, _ = _tensor_list(copies, "copies", n, dtypes=_BF16, gaps=True)
     if hyper is not None:
         _want(hyper, "hyper", (3,), dtypes=_F32)
         _on_device(hyper=hyper)

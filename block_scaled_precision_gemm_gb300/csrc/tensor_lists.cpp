@@ -21,15 +21,17 @@
 
 namespace {
 
-// addresses(list, device, sizes, per) -> (addresses, sizes, dtype), or None.
+// addresses(list, device, sizes, per, gaps) -> (addresses, sizes, dtype), or None.
 // All items have to be contiguous CUDA tensors of one type on that device and,
-// where sizes is not None, item i holds ceil(sizes[i] / per) numbers.  Both
-// results are bytes: 64-bit words in the list's order.
+// where sizes is not None, item i holds ceil(sizes[i] / per) numbers; with gaps
+// an item may be None (address and size 0).  Both results are bytes: 64-bit words
+// in the list's order.  The type is None where there is no tensor.
 PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 4 || !PyList_CheckExact(args[0])) {
-    PyErr_SetString(PyExc_TypeError, "addresses(list, device, sizes, per)");
+  if (nargs != 5 || !PyList_CheckExact(args[0])) {
+    PyErr_SetString(PyExc_TypeError, "addresses(list, device, sizes, per, gaps)");
     return nullptr;
   }
+  const bool gaps = args[4] == Py_True;
   const Py_ssize_t n = PyList_GET_SIZE(args[0]);
   const long device = PyLong_AsLong(args[1]), per = PyLong_AsLong(args[3]);
   if (PyErr_Occurred()) return nullptr;
@@ -44,14 +46,21 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   bool good = where && sizes;
   try {
     c10::ScalarType type = c10::ScalarType::Undefined;
+    bool any = false;
     for (Py_ssize_t i = 0; good && i < n; ++i) {
       PyObject* item = PyList_GET_ITEM(args[0], i);
+      if (gaps && item == Py_None) {
+        std::memset(PyBytes_AS_STRING(where) + 8 * i, 0, 8);
+        std::memset(PyBytes_AS_STRING(sizes) + 8 * i, 0, 8);
+        continue;
+      }
       if (!THPVariable_Check(item)) {
         good = false;
         break;
       }
       const at::Tensor& t = THPVariable_Unpack(item);
-      if (i == 0) type = t.scalar_type();
+      if (!any) type = t.scalar_type();
+      any = true;
       good = t.layout() == c10::kStrided && t.is_cuda() && t.get_device() == device && t.scalar_type() == type &&
              t.is_contiguous();
       if (!good) break;
@@ -68,7 +77,7 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       std::memcpy(PyBytes_AS_STRING(where) + 8 * i, &address, 8);
       std::memcpy(PyBytes_AS_STRING(sizes) + 8 * i, &count, 8);
     }
-    if (good && n) dtype = reinterpret_cast<PyObject*>(torch::getTHPDtype(type));
+    if (good && any) dtype = reinterpret_cast<PyObject*>(torch::getTHPDtype(type));
   } catch (...) {  // a tensor without memory of its own, for one
     good = false;
   }
@@ -80,7 +89,8 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 // changed(list or None, ...): the versions of the lists' tensors rise by one, as
-// after an in-place change by torch (those made in inference mode have none).
+// after an in-place change by torch (those made in inference mode have none; None
+// may stand in a tensor's place).
 PyObject* changed(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   for (Py_ssize_t a = 0; a < nargs; ++a) {
@@ -88,6 +98,7 @@ PyObject* changed(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     TORCH_CHECK_TYPE(PyList_CheckExact(args[a]), "changed(list or None, ...)");
     for (Py_ssize_t i = 0; i < PyList_GET_SIZE(args[a]); ++i) {
       PyObject* item = PyList_GET_ITEM(args[a], i);
+      if (item == Py_None) continue;
       TORCH_CHECK_TYPE(THPVariable_Check(item), "changed: a list of tensors");
       const at::Tensor& t = THPVariable_Unpack(item);
       if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
