@@ -4,7 +4,7 @@ part of the Python binding that is compiled against torch.
 Each translation unit is compiled in parallel into ``_build/`` at the repository
 root; the shared library is linked into this package directory.  A unit is
 recompiled when it, or any header under ``csrc/`` or ``include/``, is newer
-than its object.
+than its object, and the library linked when an object is newer than it.
 """
 
 from __future__ import annotations
@@ -75,7 +75,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if ptxas_info:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
-    units = len(jobs)
     src = os.path.join(CSRC, "tensor_lists.cpp")
     if force or not os.path.exists(LISTS) or os.path.getmtime(LISTS) < os.path.getmtime(src):
         jobs.append(_lists_command(src))
@@ -89,7 +88,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if r.returncode:
                 raise RuntimeError(f"{os.path.basename(cmd[0])} failed for "
                                    f"{next(a for a in cmd if a.endswith(('.cu', '.cpp')))}")
-    if units or not os.path.exists(LIB):
+    # also after a build that compiled units and then failed
+    if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(map(os.path.getmtime, objs)):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode:
