@@ -246,8 +246,8 @@ def _lists():
         try:
             from . import _tensor_lists
         except ImportError as e:
-            raise RuntimeError("_tensor_lists.so is missing: build it first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+            raise RuntimeError("_tensor_lists.so cannot be loaded: build it for this torch and Python first "
+                               f"(python -c 'import __graft_entry__ as g; g.build()'): {e}") from e
         _LISTS = _tensor_lists
     return _LISTS
 

@@ -5,6 +5,9 @@ Each translation unit is compiled in parallel into ``_build/`` at the repository
 root; the shared library is linked into this package directory.  A unit is
 recompiled when it, or any header under ``csrc/`` or ``include/``, is newer
 than its object, and the library linked when an object is newer than it.
+_tensor_lists.so fits one torch and one Python: it is compiled again when either
+is another than the one noted beside the objects.  What is built takes its place
+whole, when it is done.
 """
 
 from __future__ import annotations
@@ -45,6 +48,34 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _lists_abi() -> str:
+    """What _tensor_lists.so fits."""
+    import torch
+    return f"torch {torch.__version__}, C++ ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, Python {sysconfig.get_config_var('SOABI')}"
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def _run(cmd: list[str]) -> subprocess.CompletedProcess:
+    """Runs a compiler; the file after its -o appears when it has succeeded."""
+    at = cmd.index("-o") + 1
+    out, part = cmd[at], f"{cmd[at]}.{os.getpid()}.part"
+    try:
+        r = subprocess.run(cmd[:at] + [part] + cmd[at + 1:], capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(part, out)
+    finally:
+        if os.path.exists(part):
+            os.remove(part)
+    return r
+
+
 def _lists_command(src: str) -> list[str]:
     """Compiles and links _tensor_lists.so with the host compiler."""
     import torch
@@ -76,11 +107,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
     src = os.path.join(CSRC, "tensor_lists.cpp")
-    if force or not os.path.exists(LISTS) or os.path.getmtime(LISTS) < os.path.getmtime(src):
+    abi, noted = _lists_abi(), os.path.join(BUILD, "_tensor_lists.abi")
+    if force or not os.path.exists(LISTS) or os.path.getmtime(LISTS) < os.path.getmtime(src) or _read(noted) != abi:
         jobs.append(_lists_command(src))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-            results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
+            results = list(ex.map(_run, jobs))
         for cmd, r in zip(jobs, results):
             if verbose or ptxas_info or r.returncode:
                 print(" ".join(cmd))
@@ -88,10 +120,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if r.returncode:
                 raise RuntimeError(f"{os.path.basename(cmd[0])} failed for "
                                    f"{next(a for a in cmd if a.endswith(('.cu', '.cpp')))}")
+        if src in jobs[-1]:
+            with open(noted, "w") as f:
+                f.write(abi)
     # also after a build that compiled units and then failed
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(map(os.path.getmtime, objs)):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        r = _run(cmd)
         if r.returncode:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     return LIB

@@ -7,6 +7,7 @@ import time
 
 import pytest
 
+import block_scaled_precision_gemm_gb300 as bsmm
 from block_scaled_precision_gemm_gb300 import _build
 
 # writes its inputs' names and its own run's number to the file after -o, or fails as told
@@ -14,7 +15,8 @@ COMPILER = """#!{python}
 import os, sys
 here = os.path.dirname(os.path.abspath(__file__))
 name = os.path.basename(__file__)
-if os.path.exists(os.path.join(here, name + ".fails")):
+fails = os.path.join(here, name + ".fails")
+if os.path.exists(fails) and open(fails).read() in sys.argv:
     open(sys.argv[sys.argv.index("-o") + 1], "w").write("half")
     sys.exit(1)
 log = os.path.join(here, name + ".log")
@@ -74,7 +76,7 @@ def test_objects_of_a_build_that_failed_are_linked_by_the_next(tree, fails):
     newer(tree / "csrc" / "a.cu", tree / "_build" / "a.cu.o")
     newer(tree / "csrc" / "tensor_lists.cpp", tree / "lists.so")
     if fails == "g++":
-        (tree / "bin" / "g++.fails").write_text("")
+        (tree / "bin" / "g++.fails").write_text("-o")
         with pytest.raises(RuntimeError, match="failed for"):
             _build.build()
         (tree / "bin" / "g++.fails").unlink()
@@ -88,3 +90,43 @@ def test_objects_of_a_build_that_failed_are_linked_by_the_next(tree, fails):
             _build.subprocess.run = real
     _build.build()
     assert (tree / "lib.so").read_text() != old
+
+
+@pytest.mark.parametrize("word,tool,made", [("-c", "nvcc", "_build/a.cu.o"), ("-lcudart_static", "nvcc", "lib.so"),
+                                            ("-o", "g++", "lists.so")])
+def test_a_command_that_fails_leaves_what_was_there(tree, word, tool, made):
+    _build.build()
+    old = (tree / made).read_text()
+    for n in ("a.cu", "tensor_lists.cpp"):
+        newer(tree / "csrc" / n, tree / ("lists.so" if n.endswith("cpp") else "_build/a.cu.o"))
+    (tree / "bin" / (tool + ".fails")).write_text(word)
+    with pytest.raises(RuntimeError, match="failed"):
+        _build.build()
+    assert (tree / made).read_text() == old
+    (tree / "bin" / (tool + ".fails")).unlink()
+    _build.build()
+    assert (tree / made).read_text() != old
+    assert not [f for f in os.listdir(tree) + os.listdir(tree / "_build") if f.endswith(".part")]
+
+
+@pytest.mark.parametrize("what", ["torch", "python"])
+def test_another_torch_or_python_compiles_the_lists_again(tree, monkeypatch, what):
+    import torch
+    _build.build()
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    else:
+        real = _build.sysconfig.get_config_var
+        monkeypatch.setattr(_build.sysconfig, "get_config_var", lambda n: "cpython-0" if n == "SOABI" else real(n))
+    _build.build()
+    assert len(runs(tree, "g++")) == 2 and len(runs(tree, "nvcc")) == 3
+    _build.build()
+    assert len(runs(tree, "g++")) == 2
+
+
+def test_lists_that_cannot_be_loaded_say_why(monkeypatch):
+    monkeypatch.setattr(bsmm, "_LISTS", None)
+    monkeypatch.delattr(bsmm, "_tensor_lists", raising=False)
+    monkeypatch.setitem(sys.modules, "block_scaled_precision_gemm_gb300._tensor_lists", None)
+    with pytest.raises(RuntimeError, match="cannot be loaded.*: .*halted"):
+        bsmm._lists()
