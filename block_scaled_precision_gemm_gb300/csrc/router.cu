@@ -24,7 +24,9 @@ namespace bsmm {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kRouteBlocks = 152;  // most blocks of tokens: one per SM, as each reads the others' counts
+// Most blocks of tokens, as each reads the others' counts: one per SM of the GPU
+// this is written for.  (A constant, because the workspace's size does not ask a device.)
+constexpr int kRouteBlocks = 152;
 constexpr int kPlaceThreads = 1024;
 
 __device__ __forceinline__ float bf16_value(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
@@ -145,7 +147,6 @@ struct RouteParams {
   int64_t T;
   int E, k;
   const void* logits;
-  int bf16;
   int64_t ld;
   int vec;  // rows are 16-byte aligned and E fills the lanes' vectors
   int renormalize;
@@ -909,7 +910,6 @@ cudaError_t launch_route(const RouteRequest& r, cudaStream_t s) {
   p.E = static_cast<int>(r.E);
   p.k = r.k;
   p.logits = r.logits;
-  p.bf16 = r.bf16;
   p.ld = r.ld;
   p.renormalize = r.renormalize;
   p.ids = r.ids;
