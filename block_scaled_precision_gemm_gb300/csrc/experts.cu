@@ -37,9 +37,10 @@
 // rows x 32 experts of 4096 x 4096 run 690 us, 3.2 PFLOP/s, under the power cap.
 // Few rows: a block takes 430 cycles to issue, less than its weights take to
 // arrive when all SMs load (64 experts, 8 rows each: 1.1 GB in 180 us, 6.2 TB/s).
-// Between the two, with little shared between tiles, L2 delivers about 38 bytes
-// a cycle and SM: a block of 256 rows then takes 850 cycles.  A launch takes
-// about 7 us beside its blocks.
+// Between the two it is what the tiles make of the waves: 128 tiles of a ragged
+// prefill on 76 clusters run as two waves of which 1.7 are filled, and a launch takes
+// about 7 us beside its blocks (3002 rows x 8 experts of 2048 x 4096: 33 us, the
+// tensor pipe 45 % busy where 8192 rows x 8 of 4096 x 4096 reach 65 %).
 // Every wait is bounded; on expiry a CTA records the site and winds down.
 #include <cuda_bf16.h>
 
@@ -668,11 +669,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 // x's codes and scales by slot.  The TMA's gather of four rows at a time takes
 // about 70 cycles an instruction and a CTA, and is paid again for every tile of
 // features, so from 64 rows a tile on it outlasts the MMAs; a pass ahead costs
-// about 8 us and the copy's bytes.  Measured (us, gathered by the producer /
-// ahead; 32 experts of 4096 x 2048): 48 rows an expert 68 / 76, 64 78 / 76, 128
-// 105 / 78, 256 214 / 95; 8 experts of 2048 x 4096: 48 rows 29 / 35, 128 37 / 37,
-// 256 87 / 48.  Rows that crowd on few experts move the crossing down (32
-// experts, 48 rows: 80 / 74), so it is set at 48 rows an expert.
+// 1 to 2 us, its launch overlapped, and the copy's bytes (7 us by itself for 3002
+// rows of 4096).  Measured back to back on changing weights, us, gathered by the
+// producer / ahead, each expert alike | its load from 0.6 to 1.4 of that:
+//   rows an expert               32          49         64         96        128        256
+//   8 of 2048 x 4096    19/21 | 20/21  21/21|24/21  21/21|24/21  25/21|32/22  28/22|37/23  45/25|83/33
+//   32 of 512 x 1024    11/11 | 11/11  11/12|11/12  11/12|11/12  12/12|13/12  12/12|14/12  17/14|28/18
+//   32 of 4096 x 4096   97/99 |105/99 107/101|115/101 108/103|127/103 136/106|163/106 164/108|191/110 281/126|411/149
+// and so for 4, 8 and 32 experts of 512, 2048 and 4096 features, contractions of
+// 1024 and 4096: above 48 rows an expert the copy loses 1 us at most (9 %, of the
+// smallest products at 49 to 64 rows) and wins up to 2.7 times; below, the
+// producer loses where the loads are uneven (all rows on a quarter of 8 experts,
+// 32 rows an expert: 28/18), which the host does not know.
 __global__ void __launch_bounds__(256) expert_gather(const uint8_t* x, const uint8_t* scales, const int* rows, int S,
                                                      int X, int K, uint8_t* out, uint8_t* out_scales) {
   const int units = K / 16, blocks = K / 32;

@@ -7,12 +7,15 @@
 //   combine_backward  dy and the weights' gradient
 //
 // One pass over each array, no atomic whose order could show.  The sums are
-// bound by memory: 16384 tokens x 4 rows of 4096, 0.67 GB forward in 98 us (6.8
-// TB/s), 1.21 GB backward in 189 us (6.4 TB/s).  The choice is bound by the latency
-// of a token's rounds and by its instructions (65536 tokens, 8 of 256 experts,
-// bfloat16: choose 31 us, place 10; binary32 57 in all), its backward by the
-// latency of a token's chain (21 us against 11 for its bytes), a decode step's few
-// tokens by one launch (16 tokens: 3.7 us).
+// bound by memory: 16384 tokens x 4 rows of 4096, 0.67 GB forward in 101 us (6.65
+// TB/s), 1.21 GB backward in 188 us (6.4 TB/s); 2048 tokens x 32 rows 85 and 180 us
+// (6.5, 6.1).  Rows of 4101, with accesses of two bytes, are bound by their
+// instructions forward (87 % of issue: 215 us) and by latency backward (424; 290 from
+// binary32).  The choice is bound by the latency of a token's rounds and by its
+// instructions (65536 tokens, 8 of 256 experts, bfloat16: choose 31 us, place 10;
+// binary32 57 in all, 61 over all experts), its backward by the latency of a
+// token's chain (21 us against 11 for its bytes; renormalized 15), a decode step's
+// few tokens by one launch (16 tokens: 3.1 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>

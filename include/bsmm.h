@@ -730,17 +730,20 @@ bsmm_status bsmm_expert_combine_backward(int64_t T, int64_t S, int k, int64_t N,
  *   m, v     state_type F32: binary32.  E4M3: codes of m and of sqrt(v), each
  *            with a binary32 scale per 128 consecutive numbers (m_scales,
  *            v_scales: ceil(n / 128); the last block may be shorter), scale =
- *            max(absmax * binary32(1 / 448), 2^-126), 1 for a block of zeros; the codes are
- *            bsmm_quantize's for that scale (to nearest) where beta1 <= 17/18
- *            and beta2 <= 1 - 2^-4.5 (0.9558).  Above either, a step moves a state by less
- *            than half a step of its codes, which nearest would lose for ever:
+ *            max(absmax * binary32(1 / 448), 2^-126), 1 for a block of zeros
+ *            (bsmm_quantize divides by 448, which may differ in the last bit, and
+ *            stops at 1e-10).  The codes are bsmm_quantize's for that scale (to
+ *            nearest) where beta1 <= 17/18 and beta2 <= 1 - 2^-4.5 (0.9558).  Above
+ *            either, a step moves a state by less than half a step of its codes,
+ *            which nearest would lose for ever:
  *            there the quotient by the scale goes to one of the two codes around
  *            it, up where the part cut off, in 2^-20 of the codes' distance, plus
  *            r reaches 2^20 (below 2^-6 the quotient is rounded to a multiple of
  *            2^-29 first).  r is the high 20 bits of h for v and the low 20 for m:
- *            modulo 2^32, with G = 0x9E3779B9 and R = 0xBB67AE85, word(x) = y ^ y >> 15
- *            for y = (x ^ x >> 16) G, bits(x, j) = z ^ z >> 16 for z = x R + j G, and i the
- *            number's place in its tensor, h = bits(word(i / 4 ^ bits(word(step), 0)), i % 4).
+ *            modulo 2^32, with G = 0x9E3779B9 and R = 0xBB67AE85, word(x) = y ^
+ *            y >> 15 for y = (x ^ x >> 16) G, bits(x, j) = z ^ z >> 16 for z = x R +
+ *            j G, and i the number's place in its tensor,
+ *            h = bits(word(i / 4 ^ bits(word(step), 0)), i % 4).
  *            The mean is kept, and the same call gives the same bits.
  *            Either way a root that is not zero never rounds to zero (a second
  *            moment lost beside a first moment that is not would divide by eps).
