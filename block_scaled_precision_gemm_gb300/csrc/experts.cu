@@ -40,7 +40,7 @@
 // Between the two it is what the tiles make of the waves: 128 tiles of a ragged
 // prefill on 76 clusters run as two waves of which 1.7 are filled, and a launch takes
 // about 7 us beside its blocks (3002 rows x 8 experts of 2048 x 4096: 33 us, the
-// tensor pipe 45 % busy where 8192 rows x 8 of 4096 x 4096 reach 65 %).
+// tensor pipe 44 % busy where 8192 rows x 8 of 4096 x 4096 reach 65 %).
 // Every wait is bounded; on expiry a CTA records the site and winds down.
 #include <cuda_bf16.h>
 
